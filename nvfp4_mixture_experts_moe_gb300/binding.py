@@ -1,4 +1,5 @@
-"""Thin Python binding of the C ABI in ``include/moe_nvfp4.h``.
+"""Thin Python binding of the C ABI in ``include/moe_nvfp4.h`` and
+``include/moe_block.h``.
 
 Argument marshalling only: every function here takes torch tensors (or None
 for a NULL pointer) where the C call takes pointers, passes their device
@@ -55,6 +56,40 @@ class MoeGemmArgs(ctypes.Structure):
                 ("out", ctypes.c_void_p), ("out_amax", ctypes.c_void_p), ("rows", ctypes.c_int)]
 
 
+class MoeKv4Cache(ctypes.Structure):
+    _fields_ = [("num_pages", ctypes.c_int), ("page_tokens", ctypes.c_int), ("kv_heads", ctypes.c_int),
+                ("head_dim", ctypes.c_int), ("k_gs", ctypes.c_float), ("v_gs", ctypes.c_float),
+                ("pool", ctypes.c_void_p)]
+
+
+class MoeKv4AttnArgs(ctypes.Structure):
+    _fields_ = [("cache", MoeKv4Cache), ("batch", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("total_q", ctypes.c_int), ("max_q", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("cu_q", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("scale", ctypes.c_float),
+                ("causal", ctypes.c_int), ("window", ctypes.c_int), ("out", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)]
+
+
+class MoeKvStepArgs(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int), ("page_tokens", ctypes.c_int), ("max_pages", ctypes.c_int),
+                ("tokens", ctypes.c_int), ("free_capacity", ctypes.c_int),
+                ("ctx_len", ctypes.c_void_p), ("new_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p),
+                ("free_pages", ctypes.c_void_p), ("free_count", ctypes.c_void_p),
+                ("free_count_out", ctypes.c_void_p), ("kv_len", ctypes.c_void_p), ("cu_q", ctypes.c_void_p),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("device_status", ctypes.c_void_p)]
+
+
+class MoeBlockNormArgs(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int), ("H", ctypes.c_int),
+                ("x", ctypes.c_void_p), ("x_stride", ctypes.c_longlong),
+                ("gate", ctypes.c_void_p), ("gate_stride", ctypes.c_longlong),
+                ("residual", ctypes.c_void_p), ("residual_stride", ctypes.c_longlong),
+                ("residual_f32", ctypes.c_int), ("w_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+                ("residual_scale", ctypes.c_float), ("branch_scale", ctypes.c_float), ("eps", ctypes.c_float),
+                ("w_offset", ctypes.c_float), ("residual_out", ctypes.c_void_p), ("out", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
@@ -85,7 +120,17 @@ _SIGS = {
     "moe_kernel_launches": (ctypes.c_ulonglong, []),
     "moe_permute_noalloc": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "moe_debug_set": (_I, [_I, ctypes.c_longlong]),
+    "moe_kv4_pool_size": (_Z, [_I, _I, _I, _I]),
+    "moe_kv4_append": (_I, [ctypes.POINTER(MoeKv4Cache), _P, _P, ctypes.c_longlong, ctypes.c_longlong, _P, _I,
+                            _P, _P]),
+    "moe_kv4_read": (_I, [ctypes.POINTER(MoeKv4Cache), _P, _I, _P, _P, _P, _P]),
+    "moe_kv4_attention_workspace_size": (_Z, [ctypes.POINTER(MoeKv4AttnArgs)]),
+    "moe_kv4_attention": (_I, [ctypes.POINTER(MoeKv4AttnArgs), _P, _Z, _P]),
+    "moe_kv_step": (_I, [ctypes.POINTER(MoeKvStepArgs), _P]),
+    "moe_block_norm": (_I, [ctypes.POINTER(MoeBlockNormArgs), _P]),
 }
+
+MOE_KV4_WS_ZERO = 4096  # leading workspace bytes of moe_kv4_attention that start at zero
 
 MOE_STAGE_COUNT = 8
 STAGES = ["route", "permute", "quantize_x", "gemm1_gate_up_swiglu", "quantize_h", "gemm2_down",
@@ -266,3 +311,36 @@ def moe_permute_noalloc(topk_ids, T, k, E, counts, offsets, perm, inv_perm, devi
 def moe_debug_set(key, value):
     """Test hook (process-wide): see MOE_DEBUG_* in include/moe_nvfp4.h."""
     _check(lib().moe_debug_set(int(key), int(value)), "moe_debug_set")
+
+
+def moe_kv4_pool_size(num_pages, page_tokens, kv_heads, head_dim):
+    return lib().moe_kv4_pool_size(num_pages, page_tokens, kv_heads, head_dim)
+
+
+def moe_kv4_append(cache: MoeKv4Cache, k, v, k_stride, v_stride, slots, tokens, device_status=None, stream=None):
+    _check(lib().moe_kv4_append(ctypes.byref(cache), _ptr(k), _ptr(v), k_stride, v_stride, _ptr(slots), tokens,
+                                _ptr(device_status), _stream(stream)),
+           "moe_kv4_append")
+
+
+def moe_kv4_read(cache: MoeKv4Cache, slots, n, k_out, v_out, device_status=None, stream=None):
+    _check(lib().moe_kv4_read(ctypes.byref(cache), _ptr(slots), n, _ptr(k_out), _ptr(v_out), _ptr(device_status),
+                              _stream(stream)),
+           "moe_kv4_read")
+
+
+def moe_kv4_attention_workspace_size(args: MoeKv4AttnArgs):
+    return lib().moe_kv4_attention_workspace_size(ctypes.byref(args))
+
+
+def moe_kv4_attention(args: MoeKv4AttnArgs, ws, stream=None):
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().moe_kv4_attention(ctypes.byref(args), _ptr(ws), nbytes, _stream(stream)), "moe_kv4_attention")
+
+
+def moe_kv_step(args: MoeKvStepArgs, stream=None):
+    _check(lib().moe_kv_step(ctypes.byref(args), _stream(stream)), "moe_kv_step")
+
+
+def moe_block_norm(args: MoeBlockNormArgs, stream=None):
+    _check(lib().moe_block_norm(ctypes.byref(args), _stream(stream)), "moe_block_norm")

@@ -1,0 +1,231 @@
+"""What a decoder block runs around the MoE layer when it serves tokens.
+
+``KvStep`` places a step's new tokens in pages (``moe_kv_step``), ``Kv4Cache``
+keeps one layer's keys and values as NVFP4 pages, appends to them, reads rows
+back and attends over them (``moe_kv4_append``, ``moe_kv4_read``,
+``moe_kv4_attention``), ``block_norm`` fuses the norm after a block, its gate,
+the residual and the norm before the next block (``moe_block_norm``). The C
+calls and their contracts are in ``include/moe_block.h``; torch only
+allocates. Wrong shapes, types or devices raise ``ValueError``; what the C
+call refuses raises ``MoeError``.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import binding as B
+
+
+def _need(ok, what):
+    if not ok:
+        raise ValueError(what)
+
+
+def _ints(t, shape, what):
+    _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape,
+          f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
+    return t.data_ptr()
+
+
+def _rows(t, heads, dim, what):
+    """Address and row stride of a bf16 [n, heads, dim] tensor whose rows' heads are contiguous."""
+    _need(t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim,
+          f"{what}: a CUDA bf16 tensor [rows, {heads}, {dim}] is needed")
+    st = t.stride()
+    _need(t.shape[0] == 0 or ((st[2] == 1) and (heads == 1 or st[1] == dim)),
+          f"{what}: a row's heads have to be contiguous")
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * dim)
+
+
+def _on(stream, *made):
+    """Tensors allocated here for a call on another stream stay reserved until that stream is done with them."""
+    if isinstance(stream, torch.cuda.Stream):
+        for t in made:
+            if t is not None:
+                t.record_stream(stream)
+
+
+class Kv4Cache:
+    """Paged NVFP4 keys and values of one layer.
+
+    ``k_gs`` and ``v_gs`` are the calibrated global scales in the quant
+    convention (2688 / amax). ``pool`` may be given (uint8, layout in
+    ``include/moe_block.h``); otherwise it is allocated, uninitialised.
+    """
+
+    def __init__(self, num_pages, page_tokens, kv_heads, head_dim, k_gs, v_gs, device="cuda", pool=None):
+        nbytes = B.moe_kv4_pool_size(num_pages, page_tokens, kv_heads, head_dim)
+        _need(nbytes > 0, "cache sizes: page_tokens 16, 32, 64 or 128, head_dim 64 or 128, 1 to 1024 kv heads, "
+                          "num_pages * page_tokens < 2^31")
+        if pool is None:
+            pool = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        _need(pool.is_cuda and pool.dtype == torch.uint8 and pool.is_contiguous() and pool.numel() == nbytes,
+              f"pool: a contiguous CUDA uint8 tensor of {nbytes} bytes is needed")
+        self.num_pages, self.page_tokens = num_pages, page_tokens
+        self.kv_heads, self.head_dim = kv_heads, head_dim
+        self.pool = pool
+        self.desc = B.MoeKv4Cache(num_pages, page_tokens, kv_heads, head_dim, float(k_gs), float(v_gs),
+                                  pool.data_ptr())
+
+    def append(self, k, v, slots, device_status=None, stream=None):
+        """bf16 ``[tokens, kv_heads, head_dim]`` rows into the slots (int32; negative ones are skipped)."""
+        kp, ks = _rows(k, self.kv_heads, self.head_dim, "k")
+        vp, vs = _rows(v, self.kv_heads, self.head_dim, "v")
+        n = k.shape[0]
+        _need(v.shape[0] == n, "k and v have different lengths")
+        B.moe_kv4_append(self.desc, kp, vp, ks, vs, _ints(slots, (n,), "slots"), n, device_status, stream)
+
+    def read(self, slots, stream=None, device_status=None):
+        """The slots' rows as bf16 (k, v) ``[n, kv_heads, head_dim]``; negative slots give zeros."""
+        n = slots.numel()
+        k, v = (torch.empty(n, self.kv_heads, self.head_dim, dtype=torch.bfloat16, device=self.pool.device)
+                for _ in range(2))
+        B.moe_kv4_read(self.desc, _ints(slots, (n,), "slots"), n, k, v, device_status, stream)
+        _on(stream, k, v)
+        return k, v
+
+    def attention_workspace(self, total_q, batch, q_heads, max_q, max_pages=1):
+        """A workspace for calls of up to these sizes; its leading bytes start at zero."""
+        a = B.MoeKv4AttnArgs(cache=self.desc, batch=batch, q_heads=q_heads, total_q=total_q, max_q=max_q,
+                             max_pages=max_pages, scale=1.0, causal=1)
+        n = B.moe_kv4_attention_workspace_size(a)
+        _need(n > 0, "attention sizes outside the limits")
+        ws = torch.empty(n, dtype=torch.uint8, device=self.pool.device)
+        ws[:B.MOE_KV4_WS_ZERO].zero_()
+        return ws
+
+    def attention(self, q, cu_q, kv_len, block_table, max_q, scale=None, causal=True, window=0, want_lse=False,
+                  out=None, lse=None, ws=None, stream=None):
+        """Attention of ``q`` (bf16 ``[total_q, q_heads, head_dim]``) over the cached tokens.
+
+        ``cu_q`` int32 ``[batch + 1]``, ``kv_len`` int32 ``[batch]`` (new
+        tokens included, already appended), ``block_table`` int32 ``[batch,
+        max_pages]``, ``max_q`` a bound on every request's query rows.
+        Returns (out, lse); lse (fp32 ``[total_q, q_heads]``) is None unless
+        wanted or given.
+        """
+        total_q, heads, batch = q.shape[0], q.shape[1], kv_len.shape[0]
+        qp, qs = _rows(q, heads, self.head_dim, "q")
+        _need(block_table.dim() == 2, "block_table: [batch, max_pages] is needed")
+        max_pages = block_table.shape[1]
+        made = []
+        if out is None:
+            out = torch.empty(total_q, heads, self.head_dim, dtype=torch.bfloat16, device=q.device)
+            made.append(out)
+        _need(out.is_cuda and out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape,
+              "out: a contiguous CUDA bf16 tensor like q is needed")
+        if lse is None and want_lse:
+            lse = torch.empty(total_q, heads, dtype=torch.float32, device=q.device)
+            made.append(lse)
+        _need(lse is None or (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
+                              and tuple(lse.shape) == (total_q, heads)),
+              "lse: a contiguous CUDA fp32 tensor [total_q, q_heads] is needed")
+        if ws is None:
+            ws = self.attention_workspace(total_q, batch, heads, max_q, max_pages)
+            made.append(ws)
+        if scale is None:
+            scale = self.head_dim ** -0.5
+        a = B.MoeKv4AttnArgs(self.desc, batch, heads, total_q, max_q, max_pages, qp, qs,
+                             _ints(cu_q, (batch + 1,), "cu_q"), _ints(kv_len, (batch,), "kv_len"),
+                             _ints(block_table, (batch, max_pages), "block_table"), scale, 1 if causal else 0, window,
+                             out.data_ptr(), None if lse is None else lse.data_ptr())
+        if made:
+            _on(stream, *made)
+        B.moe_kv4_attention(a, ws, stream)
+        return out, lse
+
+
+class KvStep:
+    """One step's tables for up to ``batch`` requests and ``tokens`` new tokens.
+
+    Holds the outputs, rewritten by every ``run``: ``kv_len`` ``[batch]``,
+    ``cu_q`` ``[batch + 1]``, ``slots`` and ``positions`` ``[tokens]``,
+    ``free_count`` ``[1]``, and ``status`` ``[1]``, which ``run`` sets to
+    MOE_ERR_DEVICE when a request was refused or its lengths were bad (the
+    caller clears it).
+    """
+
+    def __init__(self, batch, tokens, page_tokens, max_pages, device="cuda"):
+        self.batch, self.tokens, self.page_tokens, self.max_pages = batch, tokens, page_tokens, max_pages
+        made = [torch.empty(n, dtype=torch.int32, device=device) for n in (batch, batch + 1, tokens, tokens, 1)]
+        self.kv_len, self.cu_q, self.slots, self.positions, self.free_count = made
+        self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._outs = [t.data_ptr() for t in (self.free_count, self.kv_len, self.cu_q, self.slots, self.positions,
+                                             self.status)]
+
+    def run(self, ctx_len, new_len, block_table, free_pages, free_count, stream=None):
+        """Extends ``block_table`` (int32 ``[batch, max_pages]``) in place and fills the outputs.
+
+        ``free_pages[:free_count]`` is the stack of free pages, taken from its
+        top; ``self.free_count`` says how many are left. The next step's
+        ``ctx_len`` and ``free_count`` are copies of ``kv_len`` and
+        ``self.free_count`` (they may not be these very tensors).
+        """
+        b = self.batch
+        _need(free_pages.dim() == 1, "free_pages: one dimension is needed")
+        cap = free_pages.shape[0]
+        a = B.MoeKvStepArgs(b, self.page_tokens, self.max_pages, self.tokens, cap, _ints(ctx_len, (b,), "ctx_len"),
+                            _ints(new_len, (b,), "new_len"), _ints(block_table, (b, self.max_pages), "block_table"),
+                            _ints(free_pages, (cap,), "free_pages"), _ints(free_count, (1,), "free_count"),
+                            *self._outs)
+        B.moe_kv_step(a, stream)
+        return self
+
+
+def _matrix(t, T, H, what):
+    _need(t.is_cuda and t.dtype == torch.bfloat16 and tuple(t.shape) == (T, H) and (t.stride(1) == 1 or H == 1),
+          f"{what}: a CUDA bf16 tensor [{T}, {H}] with contiguous rows is needed")
+    return t.data_ptr(), (t.stride(0) if T > 1 else H)
+
+
+def _vector(t, H, what):
+    if t is None:
+        return None
+    _need(t.is_cuda and t.dtype == torch.bfloat16 and tuple(t.shape) == (H,) and t.is_contiguous(),
+          f"{what}: a contiguous CUDA bf16 tensor [{H}] is needed")
+    return t.data_ptr()
+
+
+def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6,
+               w_offset=0.0, residual_out=None, out=None, stream=None):
+    """Norm after a block, gate, residual, norm before the next block, in one pass.
+
+    ``r = residual_scale * residual + branch_scale * gate * rms(x) * (w_post +
+    w_offset)``, ``out = rms(r) * (w_pre + w_offset)``; ``x`` bf16 ``[T, H]``
+    or None (only the norm before), ``residual`` bf16 or fp32 ``[T, H]``,
+    ``gate`` bf16 ``[T, H]`` or ``[H]``. Returns (r, out); out is None without
+    ``w_pre``. ``residual_out`` may be ``residual`` itself.
+    """
+    _need(residual.is_cuda and residual.dim() == 2 and residual.dtype in (torch.bfloat16, torch.float32),
+          "residual: a CUDA bf16 or fp32 tensor [T, H] is needed")
+    T, H = residual.shape
+    _need(H == 1 or residual.stride(1) == 1, "residual: contiguous rows are needed")
+    xp, xs = (None, 0) if x is None else _matrix(x, T, H, "x")
+    if gate is None:
+        gp, gst = None, 0
+    elif gate.dim() == 1:
+        gp, gst = _vector(gate, H, "gate"), 0
+    else:
+        gp, gst = _matrix(gate, T, H, "gate")
+    made = []
+    if residual_out is None:
+        residual_out = torch.empty(T, H, dtype=residual.dtype, device=residual.device)
+        made.append(residual_out)
+    _need(residual_out.is_cuda and residual_out.dtype == residual.dtype and residual_out.shape == residual.shape
+          and residual_out.is_contiguous(), "residual_out: a contiguous CUDA tensor like residual is needed")
+    if w_pre is None:
+        out = None
+    elif out is None:
+        out = torch.empty(T, H, dtype=torch.bfloat16, device=residual.device)
+        made.append(out)
+    if out is not None:
+        _need(out.is_cuda and out.dtype == torch.bfloat16 and tuple(out.shape) == (T, H) and out.is_contiguous(),
+              "out: a contiguous CUDA bf16 tensor [T, H] is needed")
+    a = B.MoeBlockNormArgs(T, H, xp, xs, gp, gst, residual.data_ptr(), residual.stride(0) if T > 1 else H,
+                           1 if residual.dtype == torch.float32 else 0, _vector(w_post, H, "w_post"),
+                           _vector(w_pre, H, "w_pre"), residual_scale, branch_scale, eps, w_offset,
+                           residual_out.data_ptr(), None if out is None else out.data_ptr())
+    if made:
+        _on(stream, *made)
+    B.moe_block_norm(a, stream)
+    return residual_out, out

@@ -54,7 +54,7 @@ moe_status cuda_ok(cudaError_t e) {
 }
 
 // sm_103 only. Checked once per device.
-static moe_status check_device() {
+moe_status check_device() {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_ok(e);

@@ -104,6 +104,30 @@ __device__ __forceinline__ uint32_t cvt_e4m3x2_f16x2(uint32_t two_bytes) {
   return r;
 }
 
+// e2m1 codes of two fp32 values with the hardware conversion: round to
+// nearest, ties to the even code, saturating at 6, the sign kept (also on a
+// zero result); `lo` lands in bits 0-3 of the byte, `hi` in bits 4-7.
+__device__ __forceinline__ uint32_t e2m1x2_rn(float lo, float hi) {
+  uint16_t r;
+  asm("{\n .reg .b8 b;\n cvt.rn.satfinite.e2m1x2.f32 b, %1, %2;\n cvt.u16.u8 %0, b;\n}"
+      : "=h"(r)
+      : "f"(hi), "f"(lo));
+  return r & 0xffu;
+}
+
+// E4M3 (fn) encoding of a non-negative fp32, nearest-even, saturating at 448.
+__device__ __forceinline__ uint32_t e4m3_encode_sat(float s) {
+  uint16_t r;
+  // both halves get s, so the byte order of the packed result does not matter
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(s), "f"(s));
+  return r & 0xffu;
+}
+
+__device__ __forceinline__ float e4m3_decode(uint32_t code) {
+  const uint32_t h2 = cvt_e4m3x2_f16x2((code & 0xffu) * 0x101u);  // same byte in both halves
+  return __half2float(__ushort_as_half((unsigned short)(h2 & 0xffffu)));
+}
+
 __device__ __forceinline__ uint32_t hmul2_u32(uint32_t a, uint32_t b) {
   __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
   return *reinterpret_cast<uint32_t*>(&r);

@@ -27,6 +27,9 @@ inline cudaError_t launch_ex(bool pdl, void (*kernel)(KArgs...), dim3 grid, dim3
 // Records the CUDA error string for moe_last_cuda_error() and maps it.
 moe_status cuda_ok(cudaError_t e);
 
+// MOE_OK on an sm_103 device, else MOE_ERR_UNSUPPORTED (or the CUDA error).
+moe_status check_device();
+
 // Adds n to the process-wide count of kernels this library launched.
 void count_launches(int n);
 

@@ -1,0 +1,40 @@
+// The NVFP4 key/value cache as the kernels see it (include/moe_block.h has
+// the layout) and the launchers of the block operators.
+#pragma once
+
+#include "common.cuh"
+#include "moe_block.h"
+
+namespace moe {
+
+constexpr int kKvBlock = 16;  // tokens of one contiguous block of a (page, head)
+
+// Byte offsets inside a block of 16 tokens.
+template <int D>
+struct Kv4Block {
+  static constexpr int kCodeRow = D / 2, kScaleRow = D / 16;
+  static constexpr int kKeyScales = kKvBlock * kCodeRow;
+  static constexpr int kValueCodes = kKeyScales + kKvBlock * kScaleRow;
+  static constexpr int kValueScales = kValueCodes + kKvBlock * kCodeRow;
+  static constexpr int kBytes = kValueScales + kKvBlock * kScaleRow;
+  static_assert(kBytes == 18 * D, "block bytes");
+};
+
+// Offset of the 16-token block that holds a slot, for one head. 64-bit: a
+// pool of 2^31 tokens is far larger than 2^32 bytes.
+__device__ __forceinline__ size_t kv4_block_offset(int64_t page, int head, int kv_heads, int blocks_per_page,
+                                                   int block, int block_bytes) {
+  return (((size_t)page * kv_heads + head) * blocks_per_page + block) * (size_t)block_bytes;
+}
+
+moe_status launch_kv4_append(const moe_kv4_cache& c, const uint16_t* k, const uint16_t* v, long long k_stride,
+                             long long v_stride, const int32_t* slots, int tokens, int32_t* status, cudaStream_t s);
+moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, uint16_t* k_out, uint16_t* v_out,
+                           int32_t* status, cudaStream_t s);
+moe_status launch_kv_step(const moe_kv_step_args& a, cudaStream_t s);
+moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
+
+size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a);
+moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream_t s);
+
+}  // namespace moe

@@ -31,4 +31,4 @@ operations, the precision the CUDA kernels use.
 
 Parity status of each function is stated in its docstring ("pinned by ...").
 """
-from . import nvfp4, moe, mxfp4  # noqa: F401
+from . import nvfp4, moe, mxfp4, block  # noqa: F401
