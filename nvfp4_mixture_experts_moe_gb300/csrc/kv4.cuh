@@ -34,6 +34,15 @@ moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, 
 moe_status launch_kv_step(const moe_kv_step_args& a, cudaStream_t s);
 moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
 
+// Attention of requests with up to max_rows (at most kKvDecodeRows) query rows
+// per key/value head; the others are skipped.
+constexpr int kKvDecodeRows = 16;
+constexpr int kKvMaxCtas = 160;      // CTAs of the attention kernels, one per SM
+constexpr int kKvTilesPerCta = 4;    // fewer 32-token tiles than this do not get a CTA of their own
+size_t kv4_decode_ws_floats(int head_dim, int rows);
+moe_status launch_kv4_decode(const moe_kv4_attn_args& a, int max_rows, int* status, int* counters, float* partials,
+                             cudaStream_t s);
+
 size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a);
 moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream_t s);
 

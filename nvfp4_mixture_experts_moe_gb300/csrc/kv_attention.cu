@@ -8,7 +8,7 @@ namespace {
 constexpr int kWarps = 4;
 
 template <int D>
-__global__ void __launch_bounds__(kWarps * 32) kv4_attention_simple_kernel(moe_kv4_attn_args a, int* status) {
+__global__ void __launch_bounds__(kWarps * 32) kv4_attention_simple_kernel(moe_kv4_attn_args a, int min_rows, int* status) {
   using L = Kv4Block<D>;
   __shared__ float qs[kWarps][D];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -24,6 +24,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_simple_kernel(moe_k
     else hi = mid - 1;
   }
   const int b = lo, n = a.cu_q[b + 1] - a.cu_q[b], i = row - a.cu_q[b];
+  if (n * group <= min_rows) return;
   if (n > a.max_q || a.cu_q[b + 1] > a.total_q) {
     if (lane == 0) set_status(status, MOE_ERR_DEVICE);
     return;
@@ -106,14 +107,27 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_attention_simple_kernel(moe_k
 
 }  // namespace
 
-size_t kv4_attention_ws_bytes(const moe_kv4_attn_args&) { return MOE_KV4_WS_ZERO; }
+// A request's query rows per key/value head (its tokens times the group's
+// query heads) decide its kernel; max_q bounds them, so calls of single or
+// few drafted tokens launch only the decode kernel.
+size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a) {
+  const long long rows = (long long)a.max_q * (a.q_heads / a.cache.kv_heads);
+  const int decode_rows = rows < kKvDecodeRows ? (int)rows : kKvDecodeRows;
+  return align_up(MOE_KV4_WS_ZERO + kv4_decode_ws_floats(a.cache.head_dim, decode_rows) * sizeof(float));
+}
 
 moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream_t s) {
+  int* status = &static_cast<WsHeader*>(ws)->status;
+  int* counters = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
+  static_assert(sizeof(WsHeader) + kKvMaxCtas * sizeof(int) <= MOE_KV4_WS_ZERO, "zero region");
+  float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_KV4_WS_ZERO);
+  const long long rows = (long long)a.max_q * (a.q_heads / a.cache.kv_heads);
+  moe_status st = launch_kv4_decode(a, rows < kKvDecodeRows ? (int)rows : kKvDecodeRows, status, counters, partials, s);
+  if (st != MOE_OK || rows <= kKvDecodeRows) return st;
   const long long ctas = ((long long)a.total_q * a.q_heads + kWarps - 1) / kWarps;
   if (ctas > 0x7fffffffll) return MOE_ERR_UNSUPPORTED;
   auto k = a.cache.head_dim == 64 ? kv4_attention_simple_kernel<64> : kv4_attention_simple_kernel<128>;
-  cudaError_t e = launch_ex(false, k, dim3((unsigned)ctas), dim3(kWarps * 32), 0, s, a,
-                            &static_cast<WsHeader*>(ws)->status);
+  cudaError_t e = launch_ex(false, k, dim3((unsigned)ctas), dim3(kWarps * 32), 0, s, a, kKvDecodeRows, status);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
   return MOE_OK;

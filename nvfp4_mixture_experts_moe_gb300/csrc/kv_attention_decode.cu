@@ -1,0 +1,731 @@
+// Attention over the NVFP4 cache for few query rows: single tokens and
+// drafted tokens of up to 16 rows per (request, key/value head), a row being
+// one (token, query head) pair of the head's group.
+//
+// Mathematics. For a row q and cached token j: s_j = scale (q . k_j), out =
+// sum_j p_j v_j / sum_j p_j with p_j = 2^(s_j log2 e - m), m a running
+// maximum. The row enters as f16 times a power of two that puts its largest
+// element in [2^14, 2^15) (exact for bf16 down to 2^-24 of that element), the
+// keys as e2m1 * e4m3 in f16 (exact: at most six significant bits), so the
+// products are exact and summed in fp32. p_j is rounded to f16 for the second
+// product (2^-11 of itself, the row's p_j taken from an m that is at most 8
+// below the running maximum, so p_j <= 256), and the values enter exactly
+// like the keys; sums and statistics are fp32.
+//
+// What bounds it: the cache's bytes, 1.125 D per token and head. The kernel
+// is a tile queue dealt out evenly: a tile is 32 tokens of one (request,
+// head); all tiles in order (request, head, token) are cut into one range per
+// CTA and that into one range per warp. Each warp streams its tiles through a
+// private ring of shared-memory stages (bulk copies, mbarriers), so there is
+// no synchronisation between warps until their ranges end, whatever the
+// lengths. Ranges that cut a (request, head) leave partial results (m, sum,
+// unnormalised output), joined first by the warps of a CTA, then by the last
+// CTA to finish one; every join adds in the order of the ranges, so results
+// do not depend on timing.
+//
+// mma.sync rather than tcgen05: at 1 to 16 rows the tensor work is a few
+// per cent of the time, and the dequantised operand never has to leave the
+// registers that converted it.
+#include "kernels.cuh"
+#include "kv4.cuh"
+#include "tc_ptx.cuh"
+
+namespace moe {
+namespace {
+
+using namespace tc;
+
+constexpr int kTile = 32;          // tokens of a tile: two blocks
+constexpr int kChunk = 1024;       // requests of one launch
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kSlack = 8.0f;     // how far above m a score may be before m follows (log2)
+constexpr unsigned kFull = 0xffffffffu;
+
+struct DecodeArgs {
+  moe_kv4_attn_args a;
+  int b0, nb;          // the requests of this launch
+  int max_rows;        // requests with more query rows belong to another kernel
+  int* status;
+  int* counters;       // [kKvMaxCtas] zero between launches
+  float* partials;     // see Slots
+  long long wait_limit;
+};
+
+// One partial result: rows x D fp32 output, then (m, l) of each row.
+template <int D, int NT>
+struct Slots {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kFloats = kRows * (D + 2);
+};
+
+template <int D, int NT>
+struct Shape {
+  static constexpr int kWarps = NT == 1 ? 16 : 12;
+  static constexpr int kStageBytes = kTile / kKvBlock * Kv4Block<D>::kBytes;
+  static constexpr int kStages = (128 / D) * (NT == 1 ? 3 : 4);
+  static constexpr int kThreads = kWarps * 32;
+};
+
+template <int D, int NT>
+struct Smem {
+  using Sh = Shape<D, NT>;
+  alignas(128) uint8_t ring[Sh::kWarps][Sh::kStages][Sh::kStageBytes];
+  uint64_t full[Sh::kWarps][Sh::kStages];
+  int pre[kChunk + 1];     // tiles (over all heads) before each request
+  int warp_sum[Sh::kWarps];
+  int abort;
+  int last[2];
+  static_assert(Sh::kStages * Sh::kStageBytes >= Slots<D, NT>::kFloats * 4, "a warp's ring holds its last partial");
+};
+
+// Lengths of one request, cut to what the tables can hold.
+struct Request {
+  int row0, n, kv;   // first query row, query rows, cached tokens
+  bool bad;
+};
+
+__device__ __forceinline__ Request load_request(const moe_kv4_attn_args& a, int b) {
+  Request r;
+  const int c0 = __ldg(a.cu_q + b), c1 = __ldg(a.cu_q + b + 1), kv = __ldg(a.kv_len + b);
+  const int cap = a.max_pages * a.cache.page_tokens;
+  r.row0 = c0;
+  r.n = c1 - c0;
+  r.kv = max(0, min(kv, cap));
+  r.bad = kv != r.kv;
+  if (c0 < 0 || r.n < 0 || c1 > a.total_q || r.n > a.max_q) {
+    r.n = 0;
+    r.bad = true;
+  }
+  return r;
+}
+
+// First token any of the request's rows sees.
+__device__ __forceinline__ int first_seen(const moe_kv4_attn_args& a, const Request& r) {
+  return a.window > 0 ? max(0, min(r.kv, r.kv - r.n + 1 - a.window)) : 0;
+}
+
+// Row of the MMA's token side <-> token of a 16-token block (the same map
+// within each half): with it the 16-byte key loads are free of bank conflicts
+// and the value loads have two-way ones (128 cycles of shared memory a tile
+// with the identity, 80 with this).
+__device__ __forceinline__ int token_of(int r) { return r ^ ((r >> 1) & 1); }
+
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// 2^k for any k a pair of bf16 exponents can differ by, as two factors.
+__device__ __forceinline__ float2 pow2_pair(int k) {
+  const int h = k >> 1;
+  return make_float2(__int_as_float((127 + h) << 23), __int_as_float((127 + k - h) << 23));
+}
+
+__device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
+  int lo = 0, hi = n;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (arr[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+struct Segment {
+  int b, h;      // request (within the launch), key/value head
+  int s0, s1;    // its tiles
+};
+
+__device__ __forceinline__ Segment segment_of(const int* pre, int nb, int heads, int tile) {
+  Segment s;
+  s.b = last_at_most(pre, nb - 1, tile);
+  const int per = (pre[s.b + 1] - pre[s.b]) / heads;
+  s.h = (tile - pre[s.b]) / per;
+  s.s0 = pre[s.b] + s.h * per;
+  s.s1 = s.s0 + per;
+  return s;
+}
+
+// Writes rows of a finished (request, head) from n partials: the join's
+// elements [e0, e1) step 32 lanes, four floats each. final: normalised bf16
+// (and lse) to the output, else a partial to dst.
+template <bool OTHER_CTAS, class T>
+__device__ __forceinline__ T load_partial(const T* p) {
+  if constexpr (OTHER_CTAS) return __ldcg(p);
+  else return *p;
+}
+
+template <int D, int NT, bool OTHER_CTAS, class Src>
+__device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src, int e0,
+                                     int e1, int step, float* dst) {
+  constexpr int kRows = 8 * NT;
+  const int group = a.q_heads / a.cache.kv_heads;
+  for (int e = e0; e < e1; e += step) {
+    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
+    if (row >= rq.n * group) continue;
+    float m = -INFINITY;
+    for (int i = 0; i < n; ++i) m = fmaxf(m, load_partial<OTHER_CTAS>(src(i) + kRows * D + 2 * row));
+    const float mu = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const float* s = src(i);
+      const float2 ml = load_partial<OTHER_CTAS>(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
+      const float4 v = load_partial<OTHER_CTAS>(reinterpret_cast<const float4*>(s + row * D + d));
+      const float w = ex2(ml.x - mu);
+      l += w * ml.y;
+      o.x += w * v.x;
+      o.y += w * v.y;
+      o.z += w * v.z;
+      o.w += w * v.w;
+    }
+    if (dst != nullptr) {
+      *reinterpret_cast<float4*>(dst + row * D + d) = o;
+      if (d == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(m, l);
+    } else {
+      const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+      const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
+      *reinterpret_cast<uint2*>(a.out + at * D + d) =
+          make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
+      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? mu * kLn2 + logf(l) : -INFINITY;
+    }
+  }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(DecodeArgs p) {
+  using Sh = Shape<D, NT>;
+  using L = Kv4Block<D>;
+  using Sm = Smem<D, NT>;
+  constexpr int W = Sh::kWarps, S = Sh::kStages, kRows = 8 * NT, MT = D / 16;
+  constexpr int kKeyWords = D / 32;     // 32-bit code words of one key row per lane
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  Sm* sm = reinterpret_cast<Sm*>(smem_raw);
+  const moe_kv4_attn_args& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g8 = lane >> 2, t4 = lane & 3;
+  const int P = a.cache.page_tokens, Hk = a.cache.kv_heads, group = a.q_heads / Hk;
+
+  // ------------------------------------------------ tiles before each request
+  if (tid == 0) {
+    sm->abort = 0;
+    sm->pre[0] = 0;
+  }
+  if (lane < S) mbar_init(&sm->full[warp][lane], 1);
+  fence_barrier_init();
+  int carry = 0;
+  bool bad = false;
+  for (int base = 0; base < p.nb; base += Sh::kThreads) {
+    const int b = base + tid;
+    int tiles = 0;
+    if (b < p.nb) {
+      const Request r = load_request(a, p.b0 + b);
+      bad |= r.bad;
+      const long long rows = (long long)r.n * group;
+      if (rows > 0 && rows <= p.max_rows) tiles = ((r.kv + kTile - 1) / kTile - first_seen(a, r) / kTile) * Hk;
+    }
+    int incl = tiles;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int v = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) sm->warp_sum[warp] = incl;
+    __syncthreads();
+    int before = carry;
+    for (int w = 0; w < W; ++w) {
+      const int v = sm->warp_sum[w];
+      if (w < warp) before += v;
+      carry += v;
+    }
+    if (b < p.nb) sm->pre[b + 1] = before + incl;
+    __syncthreads();
+  }
+  if (bad && blockIdx.x == 0) set_status(p.status, MOE_ERR_DEVICE);
+  const int total = sm->pre[p.nb];
+
+  // rows that see nothing at all: zeros
+  for (int b = blockIdx.x; b < p.nb; b += gridDim.x) {
+    if (sm->pre[b + 1] != sm->pre[b]) continue;
+    const Request r = load_request(a, p.b0 + b);
+    if (r.n == 0 || (long long)r.n * group > p.max_rows) continue;
+    const size_t at = (size_t)r.row0 * a.q_heads;
+    for (int i = tid; i < r.n * a.q_heads * D / 8; i += Sh::kThreads)
+      reinterpret_cast<uint4*>(a.out + at * D)[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (a.lse != nullptr)
+      for (int i = tid; i < r.n * a.q_heads; i += Sh::kThreads) a.lse[at + i] = -INFINITY;
+  }
+  if (total == 0) return;
+
+  // ------------------------------------------------------- this warp's range
+  const int G = min((int)gridDim.x, (total + kKvTilesPerCta - 1) / kKvTilesPerCta);
+  const int cta = blockIdx.x;
+  if (cta >= G) return;
+  const int C0 = (int)((long long)total * cta / G), C1 = (int)((long long)total * (cta + 1) / G);
+  const int wact = min(W, C1 - C0);
+  auto range = [&](int w) { return C0 + (int)((long long)(C1 - C0) * w / wact); };
+  const int r0 = warp < wact ? range(warp) : 0, r1 = warp < wact ? range(warp + 1) : 0;
+  volatile int* abort = &sm->abort;
+  float* const slots = p.partials;
+  auto head_slot = [&](int w) { return slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats; };
+  auto tail_slot = [&](int w) { return reinterpret_cast<float*>(&sm->ring[w][0][0]); };
+  auto cta_slot = [&](int c, int which) {
+    return slots + ((size_t)kKvMaxCtas * W + (size_t)c * 2 + which) * Slots<D, NT>::kFloats;
+  };
+
+  if (warp < wact) {
+    // Lane i holds where tile base + i comes from and issues its copies.
+    int d_b = 0, d_h = 0, d_tok = 0, d_valid = 0, d_seg_end = 0, base = r0;
+    const uint8_t *d_src0 = nullptr, *d_src1 = nullptr;
+    auto describe = [&](int from) {
+      base = from;
+      const int tile = from + lane;
+      d_valid = 0;
+      if (tile < r1) {
+        const Segment s = segment_of(sm->pre, p.nb, Hk, tile);
+        const Request r = load_request(a, p.b0 + s.b);
+        d_b = s.b;
+        d_h = s.h;
+        d_seg_end = s.s1;
+        d_tok = (first_seen(a, r) / kTile + (tile - s.s0)) * kTile;
+        const int32_t* table = a.block_table + (size_t)(p.b0 + s.b) * a.max_pages;
+        const uint8_t* pool = static_cast<const uint8_t*>(a.cache.pool);
+        const int page = __ldg(table + d_tok / P);
+        if (page >= 0 && page < a.cache.num_pages) {
+          d_valid = P >= kTile ? 3 : 1;
+          d_src0 = pool + kv4_block_offset(page, s.h, Hk, P / kKvBlock, d_tok % P / kKvBlock, L::kBytes);
+        } else {
+          set_status(p.status, MOE_ERR_DEVICE);
+        }
+        if (P < kTile && d_tok + kKvBlock < r.kv) {
+          const int page1 = __ldg(table + d_tok / P + 1);
+          if (page1 >= 0 && page1 < a.cache.num_pages) {
+            d_valid |= 2;
+            d_src1 = pool + kv4_block_offset(page1, s.h, Hk, 1, 0, L::kBytes);
+          } else {
+            set_status(p.status, MOE_ERR_DEVICE);
+          }
+        }
+      }
+    };
+    auto issue = [&](int tile) {   // the caller has described it
+      const int slot = (tile - r0) % S;
+      if (lane == tile - base) {
+        const uint32_t dst = smem_u32(&sm->ring[warp][slot][0]);
+        uint64_t* bar = &sm->full[warp][slot];
+        if (d_valid == 3 && P >= kTile) {
+          mbar_arrive_expect_tx(bar, 2 * L::kBytes);
+          bulk_g2s(dst, d_src0, 2 * L::kBytes, bar);
+        } else {
+          const uint32_t n = (uint32_t)((d_valid & 1) + (d_valid >> 1)) * L::kBytes;
+          mbar_arrive_expect_tx(bar, n);
+          if (d_valid & 1) bulk_g2s(dst, d_src0, L::kBytes, bar);
+          if (d_valid & 2) bulk_g2s(dst + L::kBytes, d_src1, L::kBytes, bar);
+        }
+      }
+    };
+
+    describe(r0);
+    __syncwarp();
+    for (int i = 0; i < S; ++i)
+      if (r0 + i < r1) issue(r0 + i);
+
+    uint32_t qf[NT][MT][2];        // the rows as B fragments
+    float o[NT][MT][4];            // out^T: rows d, columns query rows
+    float mult[NT][2], m[NT][2], l[NT][2];
+    int last[NT][2];               // position of the query of rows 2t, 2t + 1
+    Request rq = {0, 0, 0, false};
+    int h = 0, plain0 = 0, plain1 = 0;   // tiles with every token in [plain0, plain1) need no mask
+    int seg_end = r0, seg_begin = 0;
+    int next = r0 + min(S, r1 - r0);     // the next tile to issue
+
+    for (int tile = r0; tile < r1; ++tile) {
+      const int src = tile - base;       // < 32: described before it was issued
+      const int tok0 = __shfl_sync(kFull, d_tok, src), valid = __shfl_sync(kFull, d_valid, src);
+      if (tile == seg_end || tile == r0) {   // a new (request, head)
+        const int b = __shfl_sync(kFull, d_b, src);
+        h = __shfl_sync(kFull, d_h, src);
+        seg_end = __shfl_sync(kFull, d_seg_end, src);
+        seg_begin = tile;
+        rq = load_request(a, p.b0 + b);
+        const int low = a.causal ? rq.kv - rq.n : rq.kv - 1;   // the first row's last token
+        plain1 = low + 1;
+        plain0 = a.window > 0 ? rq.kv - a.window : 0;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int row = nt * 8 + g8;
+          uint4 raw[D / 32];
+          uint32_t mx = 0;
+          const bool real = row < rq.n * group;
+          if (real) {
+            const uint16_t* q = a.q + (size_t)(rq.row0 + row / group) * a.q_stride + (h * group + row % group) * D +
+                                t4 * (D / 4);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
+          }
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            if (!real) raw[i] = make_uint4(0u, 0u, 0u, 0u);
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              mx = max(mx, max(finite_mag(w[j] & 0x7fffu), finite_mag((w[j] >> 16) & 0x7fffu)));
+          }
+          mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
+          mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
+          const int ex = min(max((int)(mx >> 7), 1), 254);
+          const float2 up = pow2_pair(141 - ex);   // largest element to [2^14, 2^15)
+#pragma unroll
+          for (int i = 0; i < D / 32; ++i) {
+            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              qf[nt][2 * i + j / 2][j & 1] = pack_f16x2(__uint_as_float(w[j] << 16) * up.x * up.y,
+                                                        __uint_as_float(w[j] & 0xffff0000u) * up.x * up.y);
+          }
+          const float2 dn = pow2_pair(ex - 141);
+          const float mine = a.scale * kLog2e / a.cache.k_gs * dn.x * dn.y;   // row g8's, fetched as columns 2t, 2t + 1
+          mult[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
+          mult[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const int r = nt * 8 + 2 * t4 + c;
+            last[nt][c] = a.causal ? rq.kv - rq.n + r / group : rq.kv - 1;
+            m[nt][c] = -INFINITY;
+            l[nt][c] = 0.0f;
+          }
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.0f;
+        }
+      }
+
+      const int slot = (tile - r0) % S;
+      const bool ok = mbar_wait(&sm->full[warp][slot], ((tile - r0) / S) & 1, abort, p.wait_limit);
+      if (!__all_sync(kFull, ok)) break;
+      const uint8_t* stage = &sm->ring[warp][slot][0];
+      const bool masked = tok0 < plain0 || tok0 + kTile > plain1 || valid != 3;
+
+      // ---------------------------------------------------------- scores
+      float s[NT][2][4];
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const uint8_t* kb = stage + blk * L::kBytes;
+        uint32_t kw[2][kKeyWords];   // key codes of MMA rows g8 and g8 + 8
+        uint32_t ks[2][2];           // their scales, each doubled to f16x2
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          const int row = token_of(g8) + 8 * r;
+          const uint8_t* sf = kb + L::kKeyScales + row * L::kScaleRow;
+          if constexpr (D == 128) {
+            const uint4 v = *reinterpret_cast<const uint4*>(kb + row * L::kCodeRow + 16 * t4);
+            kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
+            const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(sf + 2 * t4));
+            ks[r][0] = __byte_perm(two, 0, 0x1010);
+            ks[r][1] = __byte_perm(two, 0, 0x3232);
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(kb + row * L::kCodeRow + 8 * t4);
+            kw[r][0] = v.x, kw[r][1] = v.y;
+            ks[r][0] = ks[r][1] = cvt_e4m3x2_f16x2((uint32_t)sf[t4] * 0x101u);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[nt][blk][i] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kKeyWords; ++w) {
+          uint32_t lo[4], hi[4];
+          cvt_e2m1x8_f16(kw[0][w], lo);
+          cvt_e2m1x8_f16(kw[1][w], hi);
+          const uint32_t s0 = ks[0][w * 2 / kKeyWords], s1 = ks[1][w * 2 / kKeyWords];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t af[4] = {hmul2_u32(lo[2 * i], s0), hmul2_u32(hi[2 * i], s1), hmul2_u32(lo[2 * i + 1], s0),
+                                    hmul2_u32(hi[2 * i + 1], s1)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][blk], af, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float v = s[nt][blk][i] * mult[nt][i & 1];
+            if (masked) {
+              const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
+              const int hi_tok = last[nt][i & 1], lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
+              if (tok > hi_tok || tok < lo_tok || !(valid >> blk & 1)) v = -INFINITY;
+            }
+            s[nt][blk][i] = v;
+          }
+      }
+
+      // ------------------------------------------- running maximum and p
+      bool grow = false;
+      float top[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          top[nt][c] = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
+          grow |= top[nt][c] > m[nt][c] + kSlack;
+        }
+      if (__any_sync(kFull, grow)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = top[nt][c];
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+            const float mn = fmaxf(m[nt][c], x);
+            const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][c] - mn);   // 0 from -inf
+            m[nt][c] = mn;
+            l[nt][c] *= f;
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              o[nt][mt][c] *= f;
+              o[nt][mt][c + 2] *= f;
+            }
+          }
+      }
+      uint32_t pf[NT][2][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+#pragma unroll
+        for (int blk = 0; blk < 2; ++blk) {
+          const float p0 = ex2(s[nt][blk][0] - m0), p1 = ex2(s[nt][blk][1] - m1);
+          const float p2 = ex2(s[nt][blk][2] - m0), p3 = ex2(s[nt][blk][3] - m1);
+          l[nt][0] += p0 + p2;
+          l[nt][1] += p1 + p3;
+          pf[nt][blk][0] = movmatrix_trans(pack_f16x2(p0, p1));
+          pf[nt][blk][1] = movmatrix_trans(pack_f16x2(p2, p3));
+        }
+      }
+
+      // ----------------------------------------------------------- values
+#pragma unroll
+      for (int blk = 0; blk < 2; ++blk) {
+        const uint8_t* vb = stage + blk * L::kBytes;
+        uint32_t vw[4][MT / 4];    // value codes of MMA columns 2t, 2t + 1, 2t + 8, 2t + 9
+        uint32_t sc[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int tok = token_of(2 * t4 + (k & 1)) + 8 * (k >> 1);
+          sc[k] = vb[L::kValueScales + tok * L::kScaleRow + (D == 128 ? g8 : g8 / 2)];
+          if constexpr (D == 128) {
+            const uint2 v = *reinterpret_cast<const uint2*>(vb + L::kValueCodes + tok * L::kCodeRow + 8 * g8);
+            vw[k][0] = v.x, vw[k][1] = v.y;
+          } else {
+            vw[k][0] = *reinterpret_cast<const uint32_t*>(vb + L::kValueCodes + tok * L::kCodeRow + 4 * g8);
+          }
+          // what was never appended may decode as NaN: 0 * p instead
+          if (masked && (tok0 + blk * kKvBlock + tok >= rq.kv || !(valid >> blk & 1))) sc[k] = 0;
+        }
+        const uint32_t s01 = cvt_e4m3x2_f16x2(sc[0] | sc[1] << 8), s23 = cvt_e4m3x2_f16x2(sc[2] | sc[3] << 8);
+#pragma unroll
+        for (int w = 0; w < MT / 4; ++w) {
+          // bytes (even d of token 2t, of 2t + 1) and (odd d ...): one conversion gives an MMA register
+          uint32_t e01[4], o01[4], e23[4], o23[4];
+          cvt_e2m1x8_f16((vw[0][w] & 0x0f0f0f0fu) | (vw[1][w] << 4 & 0xf0f0f0f0u), e01);
+          cvt_e2m1x8_f16((vw[0][w] >> 4 & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u), o01);
+          cvt_e2m1x8_f16((vw[2][w] & 0x0f0f0f0fu) | (vw[3][w] << 4 & 0xf0f0f0f0u), e23);
+          cvt_e2m1x8_f16((vw[2][w] >> 4 & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), o23);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t af[4] = {hmul2_u32(e01[i], s01), hmul2_u32(o01[i], s01), hmul2_u32(e23[i], s23),
+                                    hmul2_u32(o23[i], s23)};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], af, pf[nt][blk][0], pf[nt][blk][1]);
+          }
+        }
+      }
+
+      // The stage is free: every word read from it went through an MMA above
+      // (volatile, in order with the copy below), on every lane.
+      if (next < r1) {
+        __syncwarp();
+        if (next - base >= 32) {
+          // descriptors run out S tiles ahead of the tile being read: the
+          // ones still needed (tile + 1 .. next - 1) are kept by shifting
+          describe(tile + 1);
+          __syncwarp();
+        }
+        issue(next);
+        ++next;
+      }
+
+      // --------------------------------------- the end of a range or segment
+      if (tile + 1 == seg_end || tile + 1 == r1) {
+        const Segment sg = segment_of(sm->pre, p.nb, Hk, tile);
+        const bool whole = seg_begin == sg.s0 && tile + 1 == sg.s1;
+        float* dst = tile + 1 == r1 ? tail_slot(warp) : head_slot(warp);
+        if (tile + 1 == r1) __syncwarp();   // every lane is done with the ring
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float sum = l[nt][c];
+            sum += __shfl_xor_sync(kFull, sum, 4);
+            sum += __shfl_xor_sync(kFull, sum, 8);
+            sum += __shfl_xor_sync(kFull, sum, 16);
+            const int row = nt * 8 + 2 * t4 + c;
+            if (whole) {
+              if (row < rq.n * group) {
+                const float inv = sum > 0.0f ? 1.0f / (sum * a.cache.v_gs) : 0.0f;
+                const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
+                uint32_t w[MT];
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  w[mt] = float2_to_bf16x2_bits(o[nt][mt][c] * inv, o[nt][mt][c + 2] * inv);
+                uint4* out = reinterpret_cast<uint4*>(a.out + at * D + g8 * (D / 8));
+#pragma unroll
+                for (int i = 0; i < MT / 4; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                if (g8 == 0 && a.lse != nullptr)
+                  a.lse[at] = sum > 0.0f ? m[nt][c] * kLn2 + logf(sum) : -INFINITY;
+              }
+            } else {
+              float2* out = reinterpret_cast<float2*>(dst + row * D + g8 * (D / 8));
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) out[mt] = make_float2(o[nt][mt][c], o[nt][mt][c + 2]);
+              if (g8 == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(m[nt][c], sum);
+            }
+          }
+      }
+    }
+    if (*abort) {   // copies in flight land before the shared memory is given up
+      for (int t = max(r0, next - S); t < next; ++t) {
+        const long long t0 = clock64();
+        while (!mbar_try_wait(&sm->full[warp][(t - r0) % S], ((t - r0) / S) & 1) && clock64() - t0 < 4000000000ll) {
+        }
+      }
+    }
+  }
+  __syncthreads();
+  if (sm->abort) {
+    if (tid == 0) set_status(p.status, MOE_ERR_TIMEOUT);
+  }
+
+  // ------------------------------------ joins of what this CTA's warps cut
+  // A segment that spans several warps' ranges, or leaves the CTA's, is
+  // joined by those warps, each taking an equal share of its elements.
+  constexpr int kElems = kRows * D / 4;
+  auto warp_of = [&](int tile) { return (int)(((long long)(tile - C0 + 1) * wact - 1) / (C1 - C0)); };
+  if (warp < wact) {
+    for (int side = 0; side < 2; ++side) {   // the segment this range begins with, then the one it ends with
+      const Segment sg = segment_of(sm->pre, p.nb, Hk, side == 0 ? r0 : r1 - 1);
+      if (side == 1 && sg.s0 <= r0) break;    // the same segment
+      const int lo = max(sg.s0, C0), hi = min(sg.s1, C1);
+      const int w0 = warp_of(lo), w1 = warp_of(hi - 1);
+      const bool inside = sg.s0 >= C0 && sg.s1 <= C1;
+      if (inside && w0 == w1) continue;       // written when it ended
+      const Request rq = load_request(a, p.b0 + sg.b);
+      // warp w's piece is in its tail slot when it reaches the end of w's range
+      auto src = [&](int i) -> const float* {
+        const int w = w0 + i;
+        return range(w + 1) <= hi ? tail_slot(w) : head_slot(w);
+      };
+      const int n = w1 - w0 + 1, mine = warp - w0;
+      join<D, NT, false>(a, rq, sg.h, n, src, kElems * mine / n + lane, kElems * (mine + 1) / n, 32,
+                  inside ? nullptr : cta_slot(cta, sg.s0 < C0 ? 0 : 1));
+    }
+  }
+
+  // --------------------------- segments that several CTAs cut: the last joins
+  const Segment first = segment_of(sm->pre, p.nb, Hk, C0), end = segment_of(sm->pre, p.nb, Hk, C1 - 1);
+  const bool cut0 = first.s0 < C0, cut1 = end.s1 > C1 && end.s0 >= C0;
+  if (!cut0 && !cut1) return;
+  auto cta_of = [&](int tile) { return (int)(((long long)(tile + 1) * G - 1) / total); };
+  __threadfence();
+  __syncthreads();
+  if (tid < 2) {
+    const bool cut = tid == 0 ? cut0 : cut1;
+    int is_last = 0;
+    if (cut) {
+      const Segment& sg = tid == 0 ? first : end;
+      const int c0 = cta_of(sg.s0), c1 = cta_of(sg.s1 - 1);
+      if (atomicAdd(p.counters + c0, 1) == c1 - c0) {
+        p.counters[c0] = 0;   // everyone has arrived: ready for the next launch
+        is_last = 1;
+      }
+    }
+    sm->last[tid] = is_last;
+  }
+  __syncthreads();
+  for (int side = 0; side < 2; ++side) {
+    if (!sm->last[side]) continue;
+    __threadfence();
+    const Segment& sg = side == 0 ? first : end;
+    const int c0 = cta_of(sg.s0), n = cta_of(sg.s1 - 1) - c0 + 1;
+    const Request rq = load_request(a, p.b0 + sg.b);
+    // the CTA the segment begins in holds its tail, the others their head
+    auto src = [&](int i) -> const float* { return cta_slot(c0 + i, i == 0 ? 1 : 0); };
+    join<D, NT, true>(a, rq, sg.h, n, src, tid, kElems, Sh::kThreads, nullptr);
+  }
+}
+
+template <int D, int NT>
+size_t partial_floats() {
+  return (size_t)kKvMaxCtas * (Shape<D, NT>::kWarps + 2) * Slots<D, NT>::kFloats;
+}
+
+template <int D, int NT>
+cudaError_t launch(const DecodeArgs& p, int ctas, cudaStream_t s) {
+  auto k = kv4_decode_kernel<D, NT>;
+  const size_t smem = sizeof(Smem<D, NT>);
+  static_assert(sizeof(Smem<D, NT>) <= 227 * 1024, "shared memory");
+  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_ex(false, k, dim3(ctas), dim3(Shape<D, NT>::kThreads), smem, s, p);
+}
+
+}  // namespace
+
+size_t kv4_decode_ws_floats(int head_dim, int rows) {
+  if (head_dim == 64) return rows <= 8 ? partial_floats<64, 1>() : partial_floats<64, 2>();
+  return rows <= 8 ? partial_floats<128, 1>() : partial_floats<128, 2>();
+}
+
+moe_status launch_kv4_decode(const moe_kv4_attn_args& a, int max_rows, int* status, int* counters, float* partials,
+                             cudaStream_t s) {
+  int dev = 0, sms = 152;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  DecodeArgs p;
+  p.a = a;
+  p.max_rows = max_rows;
+  p.status = status;
+  p.counters = counters;
+  p.partials = partials;
+  p.wait_limit = debug_wait_limit();
+  const int ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
+  for (int b0 = 0; b0 < a.batch; b0 += kChunk) {
+    p.b0 = b0;
+    p.nb = a.batch - b0 < kChunk ? a.batch - b0 : kChunk;
+    cudaError_t e;
+    if (a.cache.head_dim == 64) e = max_rows <= 8 ? launch<64, 1>(p, ctas, s) : launch<64, 2>(p, ctas, s);
+    else e = max_rows <= 8 ? launch<128, 1>(p, ctas, s) : launch<128, 2>(p, ctas, s);
+    if (e != cudaSuccess) return cuda_ok(e);
+    count_launches(1);
+  }
+  return MOE_OK;
+}
+
+}  // namespace moe
