@@ -112,7 +112,7 @@ moe_status moe_kv4_read(const moe_kv4_cache* cache, const int32_t* slots, int n,
  * than max_q or total_q (those requests' rows are not written).
  * Errors: NULL pointers (lse may be), misaligned pool / q / out (16 bytes), a
  * q_stride that is not a multiple of 8 or smaller than a row, negative sizes,
- * a non-finite scale, a window without causal -> MOE_ERR_INVALID_ARG; q_heads % kv_heads != 0,
+ * max_q < 1, a non-finite scale, a window without causal -> MOE_ERR_INVALID_ARG; q_heads % kv_heads != 0,
  * head_dim or page_tokens outside the cache's limits, batch > 4096, or more
  * than 2^31 - 1 (request, head, 32-token) tiles -> MOE_ERR_UNSUPPORTED; a
  * missing, misaligned or short workspace -> MOE_ERR_WORKSPACE. batch = 0 or

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 import torch
 
@@ -121,14 +122,20 @@ _SIGS = {
     "moe_permute_noalloc": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P, _P]),
     "moe_debug_set": (_I, [_I, ctypes.c_longlong]),
     "moe_kv4_pool_size": (_Z, [_I, _I, _I, _I]),
-    "moe_kv4_append": (_I, [ctypes.POINTER(MoeKv4Cache), _P, _P, ctypes.c_longlong, ctypes.c_longlong, _P, _I,
-                            _P, _P]),
-    "moe_kv4_read": (_I, [ctypes.POINTER(MoeKv4Cache), _P, _I, _P, _P, _P, _P]),
-    "moe_kv4_attention_workspace_size": (_Z, [ctypes.POINTER(MoeKv4AttnArgs)]),
-    "moe_kv4_attention": (_I, [ctypes.POINTER(MoeKv4AttnArgs), _P, _Z, _P]),
-    "moe_kv_step": (_I, [ctypes.POINTER(MoeKvStepArgs), _P]),
-    "moe_block_norm": (_I, [ctypes.POINTER(MoeBlockNormArgs), _P]),
+    # argument structs: a byref() or the bytes of one (PACK_*)
+    "moe_kv4_append": (_I, [_P, _P, _P, ctypes.c_longlong, ctypes.c_longlong, _P, _I, _P, _P]),
+    "moe_kv4_read": (_I, [_P, _P, _I, _P, _P, _P, _P]),
+    "moe_kv4_attention_workspace_size": (_Z, [_P]),
+    "moe_kv4_attention": (_I, [_P, _P, _Z, _P]),
+    "moe_kv_step": (_I, [_P, _P]),
+    "moe_block_norm": (_I, [_P, _P]),
 }
+
+# The same structs as bytes: for a call per layer and token, filling a ctypes
+# struct field by field costs more than the launch.
+PACK_KV4_ATTN = struct.Struct("@4i2fP5iPqPPPfiiPP")
+PACK_KV_STEP = struct.Struct("@5i11P")
+PACK_BLOCK_NORM = struct.Struct("@iiPqPqPqiPPffffPP")
 
 MOE_KV4_WS_ZERO = 4096  # leading workspace bytes of moe_kv4_attention that start at zero
 
@@ -171,6 +178,8 @@ def _ptr(t):
 
 def _stream(stream):
     if stream is None:
+        if torch.cuda.is_initialized():  # the handle alone: building a Stream object takes longer than a launch
+            return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -317,30 +326,34 @@ def moe_kv4_pool_size(num_pages, page_tokens, kv_heads, head_dim):
     return lib().moe_kv4_pool_size(num_pages, page_tokens, kv_heads, head_dim)
 
 
-def moe_kv4_append(cache: MoeKv4Cache, k, v, k_stride, v_stride, slots, tokens, device_status=None, stream=None):
-    _check(lib().moe_kv4_append(ctypes.byref(cache), _ptr(k), _ptr(v), k_stride, v_stride, _ptr(slots), tokens,
-                                _ptr(device_status), _stream(stream)),
-           "moe_kv4_append")
+def _arg(a):
+    return a if isinstance(a, bytes) else ctypes.byref(a)
 
 
-def moe_kv4_read(cache: MoeKv4Cache, slots, n, k_out, v_out, device_status=None, stream=None):
-    _check(lib().moe_kv4_read(ctypes.byref(cache), _ptr(slots), n, _ptr(k_out), _ptr(v_out), _ptr(device_status),
-                              _stream(stream)),
-           "moe_kv4_read")
+def moe_kv4_append(cache, k, v, k_stride, v_stride, slots, tokens, device_status=None, stream=None):
+    st = lib().moe_kv4_append(_arg(cache), _ptr(k), _ptr(v), k_stride, v_stride, _ptr(slots), tokens,
+                              _ptr(device_status), _stream(stream))
+    _check(st, "moe_kv4_append")
 
 
-def moe_kv4_attention_workspace_size(args: MoeKv4AttnArgs):
-    return lib().moe_kv4_attention_workspace_size(ctypes.byref(args))
+def moe_kv4_read(cache, slots, n, k_out, v_out, device_status=None, stream=None):
+    st = lib().moe_kv4_read(_arg(cache), _ptr(slots), n, _ptr(k_out), _ptr(v_out), _ptr(device_status),
+                            _stream(stream))
+    _check(st, "moe_kv4_read")
 
 
-def moe_kv4_attention(args: MoeKv4AttnArgs, ws, stream=None):
+def moe_kv4_attention_workspace_size(args):
+    return lib().moe_kv4_attention_workspace_size(_arg(args))
+
+
+def moe_kv4_attention(args, ws, stream=None):
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().moe_kv4_attention(ctypes.byref(args), _ptr(ws), nbytes, _stream(stream)), "moe_kv4_attention")
+    _check(lib().moe_kv4_attention(_arg(args), _ptr(ws), nbytes, _stream(stream)), "moe_kv4_attention")
 
 
-def moe_kv_step(args: MoeKvStepArgs, stream=None):
-    _check(lib().moe_kv_step(ctypes.byref(args), _stream(stream)), "moe_kv_step")
+def moe_kv_step(args, stream=None):
+    _check(lib().moe_kv_step(_arg(args), _stream(stream)), "moe_kv_step")
 
 
-def moe_block_norm(args: MoeBlockNormArgs, stream=None):
-    _check(lib().moe_block_norm(ctypes.byref(args), _stream(stream)), "moe_block_norm")
+def moe_block_norm(args, stream=None):
+    _check(lib().moe_block_norm(_arg(args), _stream(stream)), "moe_block_norm")

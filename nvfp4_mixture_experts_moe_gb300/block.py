@@ -16,33 +16,42 @@ import torch
 from . import binding as B
 
 
+_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+
+
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
 
 
 def _ints(t, shape, what):
-    _need(t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and tuple(t.shape) == shape,
-          f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
+    if not (t.is_cuda and t.dtype is _I32 and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
     return t.data_ptr()
 
 
 def _rows(t, heads, dim, what):
     """Address and row stride of a bf16 [n, heads, dim] tensor whose rows' heads are contiguous."""
-    _need(t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1] == heads and t.shape[2] == dim,
-          f"{what}: a CUDA bf16 tensor [rows, {heads}, {dim}] is needed")
+    n = t.shape[0] if t.dim() == 3 else -1
+    if not (t.is_cuda and t.dtype is _BF16 and t.shape == (n, heads, dim)):
+        raise ValueError(f"{what}: a CUDA bf16 tensor [rows, {heads}, {dim}] is needed")
     st = t.stride()
-    _need(t.shape[0] == 0 or ((st[2] == 1) and (heads == 1 or st[1] == dim)),
-          f"{what}: a row's heads have to be contiguous")
-    return t.data_ptr(), (st[0] if t.shape[0] > 1 else heads * dim)
+    if n > 0 and not (st[2] == 1 and (heads == 1 or st[1] == dim)):
+        raise ValueError(f"{what}: a row's heads have to be contiguous")
+    return t.data_ptr(), (st[0] if n > 1 else heads * dim)
 
 
-def _on(stream, *made):
-    """Tensors allocated here for a call on another stream stay reserved until that stream is done with them."""
-    if isinstance(stream, torch.cuda.Stream):
-        for t in made:
-            if t is not None:
-                t.record_stream(stream)
+def _like(t, shape, dtype, what):
+    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous CUDA {dtype} tensor of shape {tuple(shape)} is needed")
+    return t.data_ptr()
+
+
+def _made(t, stream):
+    """A tensor allocated here for a call on another stream stays reserved until that stream is done with it."""
+    if stream is not None and isinstance(stream, torch.cuda.Stream):
+        t.record_stream(stream)
+    return t
 
 
 class Kv4Cache:
@@ -64,34 +73,37 @@ class Kv4Cache:
         self.num_pages, self.page_tokens = num_pages, page_tokens
         self.kv_heads, self.head_dim = kv_heads, head_dim
         self.pool = pool
-        self.desc = B.MoeKv4Cache(num_pages, page_tokens, kv_heads, head_dim, float(k_gs), float(v_gs),
-                                  pool.data_ptr())
+        self._fields = (num_pages, page_tokens, kv_heads, head_dim, float(k_gs), float(v_gs), pool.data_ptr())
+        self.desc = B.MoeKv4Cache(*self._fields)
 
     def append(self, k, v, slots, device_status=None, stream=None):
         """bf16 ``[tokens, kv_heads, head_dim]`` rows into the slots (int32; negative ones are skipped)."""
         kp, ks = _rows(k, self.kv_heads, self.head_dim, "k")
         vp, vs = _rows(v, self.kv_heads, self.head_dim, "v")
         n = k.shape[0]
-        _need(v.shape[0] == n, "k and v have different lengths")
+        if v.shape[0] != n:
+            raise ValueError("k and v have different lengths")
         B.moe_kv4_append(self.desc, kp, vp, ks, vs, _ints(slots, (n,), "slots"), n, device_status, stream)
 
     def read(self, slots, stream=None, device_status=None):
         """The slots' rows as bf16 (k, v) ``[n, kv_heads, head_dim]``; negative slots give zeros."""
-        n = slots.numel()
-        k, v = (torch.empty(n, self.kv_heads, self.head_dim, dtype=torch.bfloat16, device=self.pool.device)
-                for _ in range(2))
-        B.moe_kv4_read(self.desc, _ints(slots, (n,), "slots"), n, k, v, device_status, stream)
-        _on(stream, k, v)
+        n = slots.shape[0] if slots.dim() == 1 else -1
+        at = _ints(slots, (n,), "slots")
+        shape = (n, self.kv_heads, self.head_dim)
+        k = _made(torch.empty(shape, dtype=_BF16, device=self.pool.device), stream)
+        v = _made(torch.empty_like(k), stream)
+        B.moe_kv4_read(self.desc, at, n, k.data_ptr(), v.data_ptr(), device_status, stream)
         return k, v
 
-    def attention_workspace(self, total_q, batch, q_heads, max_q, max_pages=1):
+    def attention_workspace(self, total_q, batch, q_heads, max_q, max_pages=1, stream=None):
         """A workspace for calls of up to these sizes; its leading bytes start at zero."""
         a = B.MoeKv4AttnArgs(cache=self.desc, batch=batch, q_heads=q_heads, total_q=total_q, max_q=max_q,
                              max_pages=max_pages, scale=1.0, causal=1)
         n = B.moe_kv4_attention_workspace_size(a)
         _need(n > 0, "attention sizes outside the limits")
         ws = torch.empty(n, dtype=torch.uint8, device=self.pool.device)
-        ws[:B.MOE_KV4_WS_ZERO].zero_()
+        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
+            ws[:B.MOE_KV4_WS_ZERO].zero_()
         return ws
 
     def attention(self, q, cu_q, kv_len, block_table, max_q, scale=None, causal=True, window=0, want_lse=False,
@@ -104,33 +116,27 @@ class Kv4Cache:
         Returns (out, lse); lse (fp32 ``[total_q, q_heads]``) is None unless
         wanted or given.
         """
-        total_q, heads, batch = q.shape[0], q.shape[1], kv_len.shape[0]
+        total_q, heads = q.shape[0], q.shape[1]
+        batch = kv_len.shape[0]
         qp, qs = _rows(q, heads, self.head_dim, "q")
-        _need(block_table.dim() == 2, "block_table: [batch, max_pages] is needed")
+        if block_table.dim() != 2:
+            raise ValueError("block_table: [batch, max_pages] is needed")
         max_pages = block_table.shape[1]
-        made = []
+        shape = (total_q, heads, self.head_dim)
         if out is None:
-            out = torch.empty(total_q, heads, self.head_dim, dtype=torch.bfloat16, device=q.device)
-            made.append(out)
-        _need(out.is_cuda and out.dtype == torch.bfloat16 and out.is_contiguous() and out.shape == q.shape,
-              "out: a contiguous CUDA bf16 tensor like q is needed")
+            out = _made(torch.empty(shape, dtype=_BF16, device=q.device), stream)
+            op = out.data_ptr()
+        else:
+            op = _like(out, shape, _BF16, "out")
         if lse is None and want_lse:
-            lse = torch.empty(total_q, heads, dtype=torch.float32, device=q.device)
-            made.append(lse)
-        _need(lse is None or (lse.is_cuda and lse.dtype == torch.float32 and lse.is_contiguous()
-                              and tuple(lse.shape) == (total_q, heads)),
-              "lse: a contiguous CUDA fp32 tensor [total_q, q_heads] is needed")
+            lse = _made(torch.empty(total_q, heads, dtype=_F32, device=q.device), stream)
+        lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse")
         if ws is None:
-            ws = self.attention_workspace(total_q, batch, heads, max_q, max_pages)
-            made.append(ws)
-        if scale is None:
-            scale = self.head_dim ** -0.5
-        a = B.MoeKv4AttnArgs(self.desc, batch, heads, total_q, max_q, max_pages, qp, qs,
-                             _ints(cu_q, (batch + 1,), "cu_q"), _ints(kv_len, (batch,), "kv_len"),
-                             _ints(block_table, (batch, max_pages), "block_table"), scale, 1 if causal else 0, window,
-                             out.data_ptr(), None if lse is None else lse.data_ptr())
-        if made:
-            _on(stream, *made)
+            ws = _made(self.attention_workspace(total_q, batch, heads, max_q, max_pages, stream), stream)
+        a = B.PACK_KV4_ATTN.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
+                                 _ints(cu_q, (batch + 1,), "cu_q"), _ints(kv_len, (batch,), "kv_len"),
+                                 _ints(block_table, (batch, max_pages), "block_table"),
+                                 self.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, lp)
         B.moe_kv4_attention(a, ws, stream)
         return out, lse
 
@@ -162,28 +168,23 @@ class KvStep:
         ``self.free_count`` (they may not be these very tensors).
         """
         b = self.batch
-        _need(free_pages.dim() == 1, "free_pages: one dimension is needed")
-        cap = free_pages.shape[0]
-        a = B.MoeKvStepArgs(b, self.page_tokens, self.max_pages, self.tokens, cap, _ints(ctx_len, (b,), "ctx_len"),
-                            _ints(new_len, (b,), "new_len"), _ints(block_table, (b, self.max_pages), "block_table"),
-                            _ints(free_pages, (cap,), "free_pages"), _ints(free_count, (1,), "free_count"),
-                            *self._outs)
+        cap = free_pages.shape[0] if free_pages.dim() == 1 else -1
+        a = B.PACK_KV_STEP.pack(b, self.page_tokens, self.max_pages, self.tokens, cap, _ints(ctx_len, (b,), "ctx_len"),
+                                _ints(new_len, (b,), "new_len"),
+                                _ints(block_table, (b, self.max_pages), "block_table"),
+                                _ints(free_pages, (cap,), "free_pages"), _ints(free_count, (1,), "free_count"),
+                                *self._outs)
         B.moe_kv_step(a, stream)
         return self
 
 
 def _matrix(t, T, H, what):
-    _need(t.is_cuda and t.dtype == torch.bfloat16 and tuple(t.shape) == (T, H) and (t.stride(1) == 1 or H == 1),
-          f"{what}: a CUDA bf16 tensor [{T}, {H}] with contiguous rows is needed")
-    return t.data_ptr(), (t.stride(0) if T > 1 else H)
-
-
-def _vector(t, H, what):
-    if t is None:
-        return None
-    _need(t.is_cuda and t.dtype == torch.bfloat16 and tuple(t.shape) == (H,) and t.is_contiguous(),
-          f"{what}: a contiguous CUDA bf16 tensor [{H}] is needed")
-    return t.data_ptr()
+    if not (t.is_cuda and t.dtype is _BF16 and t.shape == (T, H)):
+        raise ValueError(f"{what}: a CUDA bf16 tensor [{T}, {H}] is needed")
+    st = t.stride()
+    if st[1] != 1 and H > 1:
+        raise ValueError(f"{what}: contiguous rows are needed")
+    return t.data_ptr(), (st[0] if T > 1 else H)
 
 
 def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1.0, branch_scale=1.0, eps=1e-6,
@@ -196,36 +197,36 @@ def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1
     ``gate`` bf16 ``[T, H]`` or ``[H]``. Returns (r, out); out is None without
     ``w_pre``. ``residual_out`` may be ``residual`` itself.
     """
-    _need(residual.is_cuda and residual.dim() == 2 and residual.dtype in (torch.bfloat16, torch.float32),
-          "residual: a CUDA bf16 or fp32 tensor [T, H] is needed")
-    T, H = residual.shape
-    _need(H == 1 or residual.stride(1) == 1, "residual: contiguous rows are needed")
-    xp, xs = (None, 0) if x is None else _matrix(x, T, H, "x")
+    dtype = residual.dtype
+    if not (residual.is_cuda and residual.dim() == 2 and (dtype is _BF16 or dtype is _F32)):
+        raise ValueError("residual: a CUDA bf16 or fp32 tensor [T, H] is needed")
+    T, H = shape = residual.shape
+    rs = residual.stride()
+    if rs[1] != 1 and H > 1:
+        raise ValueError("residual: contiguous rows are needed")
+    xp, xs = (0, 0) if x is None else _matrix(x, T, H, "x")
     if gate is None:
-        gp, gst = None, 0
+        gp, gst = 0, 0
     elif gate.dim() == 1:
-        gp, gst = _vector(gate, H, "gate"), 0
+        gp, gst = _like(gate, (H,), _BF16, "gate"), 0
     else:
         gp, gst = _matrix(gate, T, H, "gate")
-    made = []
     if residual_out is None:
-        residual_out = torch.empty(T, H, dtype=residual.dtype, device=residual.device)
-        made.append(residual_out)
-    _need(residual_out.is_cuda and residual_out.dtype == residual.dtype and residual_out.shape == residual.shape
-          and residual_out.is_contiguous(), "residual_out: a contiguous CUDA tensor like residual is needed")
+        residual_out = _made(torch.empty(shape, dtype=dtype, device=residual.device), stream)
+        rp = residual_out.data_ptr()
+    else:
+        rp = _like(residual_out, shape, dtype, "residual_out")
     if w_pre is None:
-        out = None
-    elif out is None:
-        out = torch.empty(T, H, dtype=torch.bfloat16, device=residual.device)
-        made.append(out)
-    if out is not None:
-        _need(out.is_cuda and out.dtype == torch.bfloat16 and tuple(out.shape) == (T, H) and out.is_contiguous(),
-              "out: a contiguous CUDA bf16 tensor [T, H] is needed")
-    a = B.MoeBlockNormArgs(T, H, xp, xs, gp, gst, residual.data_ptr(), residual.stride(0) if T > 1 else H,
-                           1 if residual.dtype == torch.float32 else 0, _vector(w_post, H, "w_post"),
-                           _vector(w_pre, H, "w_pre"), residual_scale, branch_scale, eps, w_offset,
-                           residual_out.data_ptr(), None if out is None else out.data_ptr())
-    if made:
-        _on(stream, *made)
+        out, op, wp = None, 0, 0
+    else:
+        wp = _like(w_pre, (H,), _BF16, "w_pre")
+        if out is None:
+            out = _made(torch.empty(shape, dtype=_BF16, device=residual.device), stream)
+            op = out.data_ptr()
+        else:
+            op = _like(out, shape, _BF16, "out")
+    a = B.PACK_BLOCK_NORM.pack(T, H, xp, xs, gp, gst, residual.data_ptr(), rs[0] if T > 1 else H,
+                               1 if dtype is _F32 else 0, 0 if w_post is None else _like(w_post, (H,), _BF16, "w_post"),
+                               wp, residual_scale, branch_scale, eps, w_offset, rp, op)
     B.moe_block_norm(a, stream)
     return residual_out, out

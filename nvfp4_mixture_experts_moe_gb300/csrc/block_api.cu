@@ -98,6 +98,7 @@ moe_status moe_kv4_attention(const moe_kv4_attn_args* args, void* ws, size_t ws_
   if (st != MOE_OK) return st;
   if (args->batch == 0 || args->total_q == 0) return MOE_OK;
   const long long row = (long long)args->q_heads * args->cache.head_dim;
+  if (args->max_q < 1) return MOE_ERR_INVALID_ARG;
   if (!args->q || !args->cu_q || !args->kv_len || !args->out) return MOE_ERR_INVALID_ARG;
   if (!args->block_table && args->max_pages > 0) return MOE_ERR_INVALID_ARG;
   if (!aligned(args->q, 16) || !aligned(args->out, 16) || args->q_stride % 8 || args->q_stride < row)

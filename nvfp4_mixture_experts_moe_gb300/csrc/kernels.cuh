@@ -1,6 +1,7 @@
 // Internal launchers shared between the translation units of the library.
 #pragma once
 
+#include <atomic>
 #include <utility>
 
 #include "common.cuh"
@@ -29,6 +30,22 @@ moe_status cuda_ok(cudaError_t e);
 
 // MOE_OK on an sm_103 device, else MOE_ERR_UNSUPPORTED (or the CUDA error).
 moe_status check_device();
+
+// SMs of the current device (looked up once per device).
+int sm_count();
+
+// Opts a kernel into its dynamic shared memory, once per kernel and device.
+template <class K>
+inline cudaError_t opt_in_smem(K kernel, size_t bytes, std::atomic<unsigned long long>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 // Adds n to the process-wide count of kernels this library launched.
 void count_launches(int n);

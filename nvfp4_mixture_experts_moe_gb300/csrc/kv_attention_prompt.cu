@@ -700,7 +700,8 @@ cudaError_t launch(const PromptArgs& p, int ctas, cudaStream_t s) {
   auto k = kv4_prompt_kernel<D>;
   constexpr size_t smem = sizeof(Smem<D>) + 1024;
   static_assert(smem <= 227 * 1024, "shared memory");
-  cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  static std::atomic<unsigned long long> done{0};
+  cudaError_t e = opt_in_smem(k, smem, done);
   if (e != cudaSuccess) return e;
   return launch_ex(false, k, dim3(ctas), dim3(kThreads), smem, s, p);
 }
@@ -713,9 +714,6 @@ size_t kv4_prompt_ws_floats(int head_dim) {
 
 moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, int* counters, float* partials,
                              cudaStream_t s) {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   PromptArgs p;
   p.a = a;
   p.min_rows = min_rows;
@@ -723,7 +721,7 @@ moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* stat
   p.counters = counters;
   p.partials = partials;
   p.wait_limit = debug_wait_limit();
-  const int ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
+  const int sms = sm_count(), ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
   for (int b0 = 0; b0 < a.batch; b0 += kChunk) {
     p.b0 = b0;
     p.nb = a.batch - b0 < kChunk ? a.batch - b0 : kChunk;

@@ -160,9 +160,7 @@ __global__ void __launch_bounds__(kThreads) kv_step_kernel(moe_kv_step_args a) {
 }  // namespace
 
 moe_status launch_kv_step(const moe_kv_step_args& a, cudaStream_t s) {
-  int dev = 0, sms = 152;
-  cudaGetDevice(&dev);
-  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  const int sms = sm_count();
   const int want = (int)(((long long)a.tokens + kThreads - 1) / kThreads);
   const int ctas = want < 1 ? 1 : (want < sms ? want : sms);
   cudaError_t e = launch_ex(false, kv_step_kernel, dim3(ctas), dim3(kThreads), 0, s, a);

@@ -218,6 +218,18 @@ def test_structs_match_the_header(tmp_path):
     out = subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout
     got = {tuple(line.split()[:2]): int(line.split()[2]) for line in out.splitlines()}
     assert got.pop(("zero", "bytes")) == B.MOE_KV4_WS_ZERO
+    # the packed forms are the structs' bytes
+    for pack, py in ((B.PACK_KV4_ATTN, B.MoeKv4AttnArgs), (B.PACK_KV_STEP, B.MoeKvStepArgs),
+                     (B.PACK_BLOCK_NORM, B.MoeBlockNormArgs)):
+        assert pack.size == ctypes.sizeof(py)
+        n = len(pack.unpack(bytes(pack.size)))
+        vals = list(range(1, n + 1))
+        a = py.from_buffer_copy(pack.pack(*vals))
+        flat = []
+        for name, _ in py._fields_:
+            v = getattr(a, name)
+            flat += [getattr(v, f) for f, _ in v._fields_] if isinstance(v, ctypes.Structure) else [v]
+        assert flat == vals, py
     for cname, py in structs.items():
         assert got.pop((cname, "size")) == ctypes.sizeof(py), cname
         for name, _ in py._fields_:
