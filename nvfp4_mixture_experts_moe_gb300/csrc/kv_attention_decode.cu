@@ -13,11 +13,11 @@
 // like the keys; sums and statistics are fp32.
 //
 // What bounds it: the cache's bytes, 1.125 D per token and head. The kernel
-// is a tile queue dealt out evenly: a tile is 32 tokens of one (request,
-// head); all tiles in order (request, head, token) are cut into one range per
+// is a tile queue dealt out evenly: a tile is 32 or 64 tokens of one
+// (request, head); all tiles in order (request, head, token) are cut into one range per
 // CTA and that into one range per warp. Each warp streams its tiles through a
-// private ring of shared-memory stages (bulk copies, mbarriers), so there is
-// no synchronisation between warps until their ranges end, whatever the
+// private ring of shared-memory stages (16-byte asynchronous copies), so there
+// is no synchronisation between warps until their ranges end, whatever the
 // lengths. Ranges that cut a (request, head) leave partial results (m, sum,
 // unnormalised output), joined first by the warps of a CTA, then by the last
 // CTA to finish one; every join adds in the order of the ranges, so results
@@ -26,6 +26,8 @@
 // mma.sync rather than tcgen05: at 1 to 16 rows the tensor work is a few
 // per cent of the time, and the dequantised operand never has to leave the
 // registers that converted it.
+#include <type_traits>
+
 #include "kernels.cuh"
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
@@ -35,7 +37,6 @@ namespace {
 
 using namespace tc;
 
-constexpr int kTile = 32;          // tokens of a tile: two blocks
 constexpr int kChunk = 1024;       // requests of one launch
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;     // how far above m a score may be before m follows (log2)
@@ -48,7 +49,6 @@ struct DecodeArgs {
   int* status;
   int* counters;       // [kKvMaxCtas] zero between launches
   float* partials;     // see Slots
-  long long wait_limit;
 };
 
 // One partial result: rows x D fp32 output, then (m, l) of each row.
@@ -58,11 +58,14 @@ struct Slots {
   static constexpr int kFloats = kRows * (D + 2);
 };
 
+// A tile is 4608 bytes of one (request, head): 32 tokens at D = 128, 64 at 64.
 template <int D, int NT>
 struct Shape {
   static constexpr int kWarps = NT == 1 ? 16 : 12;
-  static constexpr int kStageBytes = kTile / kKvBlock * Kv4Block<D>::kBytes;
-  static constexpr int kStages = (128 / D) * (NT == 1 ? 3 : 4);
+  static constexpr int kBlocks = 256 / D;              // 16-token blocks of a tile
+  static constexpr int kTile = kBlocks * kKvBlock;
+  static constexpr int kStageBytes = kBlocks * Kv4Block<D>::kBytes;
+  static constexpr int kStages = NT == 1 ? 3 : 4;
   static constexpr int kThreads = kWarps * 32;
 };
 
@@ -70,10 +73,8 @@ template <int D, int NT>
 struct Smem {
   using Sh = Shape<D, NT>;
   alignas(128) uint8_t ring[Sh::kWarps][Sh::kStages][Sh::kStageBytes];
-  uint64_t full[Sh::kWarps][Sh::kStages];
   int pre[kChunk + 1];     // tiles (over all heads) before each request
   int warp_sum[Sh::kWarps];
-  int abort;
   int last[2];
   static_assert(Sh::kStages * Sh::kStageBytes >= Slots<D, NT>::kFloats * 4, "a warp's ring holds its last partial");
 };
@@ -211,21 +212,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   using L = Kv4Block<D>;
   using Sm = Smem<D, NT>;
   constexpr int W = Sh::kWarps, S = Sh::kStages, kRows = 8 * NT, MT = D / 16;
+  constexpr int NB = Sh::kBlocks, kTile = Sh::kTile;
   constexpr int kKeyWords = D / 32;     // 32-bit code words of one key row per lane
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm* sm = reinterpret_cast<Sm*>(smem_raw);
   const moe_kv4_attn_args& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g8 = lane >> 2, t4 = lane & 3;
-  const int P = a.cache.page_tokens, Hk = a.cache.kv_heads, group = a.q_heads / Hk;
+  const int P = a.cache.page_tokens, p_log = __ffs(P) - 1, Hk = a.cache.kv_heads, group = a.q_heads / Hk;
 
   // ------------------------------------------------ tiles before each request
-  if (tid == 0) {
-    sm->abort = 0;
-    sm->pre[0] = 0;
-  }
-  if (lane < S) mbar_init(&sm->full[warp][lane], 1);
-  fence_barrier_init();
+  if (tid == 0) sm->pre[0] = 0;
   int carry = 0;
   bool bad = false;
   for (int base = 0; base < p.nb; base += Sh::kThreads) {
@@ -278,7 +275,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   const int wact = min(W, C1 - C0);
   auto range = [&](int w) { return C0 + (int)((long long)(C1 - C0) * w / wact); };
   const int r0 = warp < wact ? range(warp) : 0, r1 = warp < wact ? range(warp + 1) : 0;
-  volatile int* abort = &sm->abort;
   float* const slots = p.partials;
   auto head_slot = [&](int w) { return slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats; };
   auto tail_slot = [&](int w) { return reinterpret_cast<float*>(&sm->ring[w][0][0]); };
@@ -287,13 +283,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   };
 
   if (warp < wact) {
-    // Lane i holds where tile base + i comes from and issues its copies.
+    // Lane i holds where tile base + i comes from: one place per page, of
+    // min(P, kTile) tokens. Everything that needs a division or the tables is
+    // done here, once in 32 tiles.
+    const int run_log = min(p_log - 4, NB == 2 ? 1 : 2);   // log2 of the blocks of a copy
     int d_b = 0, d_h = 0, d_tok = 0, d_valid = 0, d_seg_end = 0, base = r0;
-    const uint8_t *d_src0 = nullptr, *d_src1 = nullptr;
+    const uint8_t* d_src[NB];
     auto describe = [&](int from) {
       base = from;
       const int tile = from + lane;
       d_valid = 0;
+#pragma unroll
+      for (int i = 0; i < NB; ++i) d_src[i] = nullptr;
       if (tile < r1) {
         const Segment s = segment_of(sm->pre, p.nb, Hk, tile);
         const Request r = load_request(a, p.b0 + s.b);
@@ -301,47 +302,59 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
         d_h = s.h;
         d_seg_end = s.s1;
         d_tok = (first_seen(a, r) / kTile + (tile - s.s0)) * kTile;
-        const int32_t* table = a.block_table + (size_t)(p.b0 + s.b) * a.max_pages;
-        const uint8_t* pool = static_cast<const uint8_t*>(a.cache.pool);
-        const int page = __ldg(table + d_tok / P);
-        if (page >= 0 && page < a.cache.num_pages) {
-          d_valid = P >= kTile ? 3 : 1;
-          d_src0 = pool + kv4_block_offset(page, s.h, Hk, P / kKvBlock, d_tok % P / kKvBlock, L::kBytes);
-        } else {
-          set_status(p.status, MOE_ERR_DEVICE);
-        }
-        if (P < kTile && d_tok + kKvBlock < r.kv) {
-          const int page1 = __ldg(table + d_tok / P + 1);
-          if (page1 >= 0 && page1 < a.cache.num_pages) {
-            d_valid |= 2;
-            d_src1 = pool + kv4_block_offset(page1, s.h, Hk, 1, 0, L::kBytes);
+        const int32_t* table = a.block_table + (size_t)(p.b0 + s.b) * a.max_pages + (d_tok >> p_log);
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int blk = i << run_log;
+          if (blk >= NB || d_tok + blk * kKvBlock >= r.kv) break;
+          const int page = __ldg(table + i);
+          if (page >= 0 && page < a.cache.num_pages) {
+            d_valid |= ((1 << (1 << run_log)) - 1) << blk;
+            d_src[i] = static_cast<const uint8_t*>(a.cache.pool) +
+                       kv4_block_offset(page, s.h, Hk, P / kKvBlock, (d_tok & (P - 1)) / kKvBlock, L::kBytes);
           } else {
             set_status(p.status, MOE_ERR_DEVICE);
           }
         }
       }
     };
-    auto issue = [&](int tile) {   // the caller has described it
-      const int slot = (tile - r0) % S;
-      if (lane == tile - base) {
-        const uint32_t dst = smem_u32(&sm->ring[warp][slot][0]);
-        uint64_t* bar = &sm->full[warp][slot];
-        if (d_valid == 3 && P >= kTile) {
-          mbar_arrive_expect_tx(bar, 2 * L::kBytes);
-          bulk_g2s(dst, d_src0, 2 * L::kBytes, bar);
-        } else {
-          const uint32_t n = (uint32_t)((d_valid & 1) + (d_valid >> 1)) * L::kBytes;
-          mbar_arrive_expect_tx(bar, n);
-          if (d_valid & 1) bulk_g2s(dst, d_src0, L::kBytes, bar);
-          if (d_valid & 2) bulk_g2s(dst + L::kBytes, d_src1, L::kBytes, bar);
+    // All lanes copy a described tile into a slot, one group per tile.
+    auto issue = [&](int tile, int slot) {
+      const int src = tile - base;
+      const int valid = __shfl_sync(kFull, d_valid, src);
+      const uint32_t dst = smem_u32(&sm->ring[warp][0][0]) + slot * Sh::kStageBytes + lane * 16;
+      const uint8_t* from[NB];
+#pragma unroll
+      for (int i = 0; i < NB; ++i) {
+        if (i > 0 && (i << run_log) >= NB) break;
+        from[i] = reinterpret_cast<const uint8_t*>(
+                      __shfl_sync(kFull, reinterpret_cast<unsigned long long>(d_src[i]), src)) + lane * 16;
+      }
+      if ((1 << run_log) == NB) {
+        if (valid) {
+#pragma unroll
+          for (int c = 0; c < Sh::kStageBytes; c += 512) cp_async_16(dst + c, from[0] + c, 16);
+        }
+      } else {
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          if (!(valid >> blk & 1)) continue;
+          // blocks 0, 1 (and 2, 3) share a page of 32 tokens
+          const uint8_t* f = run_log == 0 ? from[blk] : from[blk / 2] + (blk & 1) * L::kBytes;
+#pragma unroll
+          for (int c = 0; c < L::kBytes; c += 512)
+            if (c + 512 <= L::kBytes || lane * 16 < L::kBytes - c)
+              cp_async_16(dst + blk * L::kBytes + c, f + c, 16);
         }
       }
     };
 
     describe(r0);
     __syncwarp();
-    for (int i = 0; i < S; ++i)
-      if (r0 + i < r1) issue(r0 + i);
+    for (int i = 0; i < S; ++i) {
+      if (r0 + i < r1) issue(r0 + i, i);
+      cp_async_commit();
+    }
 
     uint32_t qf[NT][MT][2];        // the rows as B fragments
     float o[NT][MT][4];            // out^T: rows d, columns query rows
@@ -352,7 +365,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
     int seg_end = r0, seg_begin = 0;
     int next = r0 + min(S, r1 - r0);     // the next tile to issue
 
-    for (int tile = r0; tile < r1; ++tile) {
+    int slot = 0;
+    for (int tile = r0; tile < r1; ++tile, slot = slot + 1 == S ? 0 : slot + 1) {
       const int src = tile - base;       // < 32: described before it was issued
       const int tok0 = __shfl_sync(kFull, d_tok, src), valid = __shfl_sync(kFull, d_valid, src);
       if (tile == seg_end || tile == r0) {   // a new (request, head)
@@ -387,7 +401,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
           mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
           mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
           const int ex = min(max((int)(mx >> 7), 1), 254);
-          const float2 up = pow2_pair(141 - ex);   // largest element to [2^14, 2^15)
+          float2 up = pow2_pair(141 - ex);   // largest element to [2^14, 2^15)
+          if (a.scale < 0.0f) up.x = -up.x;  // so that a larger score is a larger product
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
@@ -397,7 +412,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
                                                         __uint_as_float(w[j] & 0xffff0000u) * up.x * up.y);
           }
           const float2 dn = pow2_pair(ex - 141);
-          const float mine = a.scale * kLog2e / a.cache.k_gs * dn.x * dn.y;   // row g8's, fetched as columns 2t, 2t + 1
+          // row g8's factor, fetched as columns 2t, 2t + 1; never 0, so that a hidden score stays -inf
+          const float mine = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * dn.x * dn.y, 1e-37f);
           mult[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
           mult[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
 #pragma unroll
@@ -414,163 +430,172 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
         }
       }
 
-      const int slot = (tile - r0) % S;
-      const bool ok = mbar_wait(&sm->full[warp][slot], ((tile - r0) / S) & 1, abort, p.wait_limit);
-      if (!__all_sync(kFull, ok)) break;
-      const uint8_t* stage = &sm->ring[warp][slot][0];
-      const bool masked = tok0 < plain0 || tok0 + kTile > plain1 || valid != 3;
+      cp_async_wait<S - 1>();   // this tile's group, on every lane
+      __syncwarp();
+      const uint8_t* stage = &sm->ring[warp][0][0] + slot * Sh::kStageBytes;
+      const bool masked = tok0 < plain0 || tok0 + kTile > plain1 || valid != (1 << NB) - 1;
 
-      // ---------------------------------------------------------- scores
-      float s[NT][2][4];
+      // Two copies of the tile's work, so that tiles every row sees whole (all
+      // but a request's last, for a single token) carry no mask.
+      auto work = [&](auto with_mask) {
+        constexpr bool kMask = decltype(with_mask)::value;
+        // ---------------------------------------------------------- scores
+        float s[NT][NB][4];
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const uint8_t* kb = stage + blk * L::kBytes;
-        uint32_t kw[2][kKeyWords];   // key codes of MMA rows g8 and g8 + 8
-        uint32_t ks[2][2];           // their scales, each doubled to f16x2
+        for (int blk = 0; blk < NB; ++blk) {
+          const uint8_t* kb = stage + blk * L::kBytes;
+          uint32_t kw[2][kKeyWords];   // key codes of MMA rows g8 and g8 + 8
+          uint32_t ks[2][2];           // their scales, each doubled to f16x2
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          const int row = token_of(g8) + 8 * r;
-          const uint8_t* sf = kb + L::kKeyScales + row * L::kScaleRow;
-          if constexpr (D == 128) {
-            const uint4 v = *reinterpret_cast<const uint4*>(kb + row * L::kCodeRow + 16 * t4);
-            kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
-            const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(sf + 2 * t4));
-            ks[r][0] = __byte_perm(two, 0, 0x1010);
-            ks[r][1] = __byte_perm(two, 0, 0x3232);
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(kb + row * L::kCodeRow + 8 * t4);
-            kw[r][0] = v.x, kw[r][1] = v.y;
-            ks[r][0] = ks[r][1] = cvt_e4m3x2_f16x2((uint32_t)sf[t4] * 0x101u);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[nt][blk][i] = 0.0f;
-#pragma unroll
-        for (int w = 0; w < kKeyWords; ++w) {
-          uint32_t lo[4], hi[4];
-          cvt_e2m1x8_f16(kw[0][w], lo);
-          cvt_e2m1x8_f16(kw[1][w], hi);
-          const uint32_t s0 = ks[0][w * 2 / kKeyWords], s1 = ks[1][w * 2 / kKeyWords];
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const uint32_t af[4] = {hmul2_u32(lo[2 * i], s0), hmul2_u32(hi[2 * i], s1), hmul2_u32(lo[2 * i + 1], s0),
-                                    hmul2_u32(hi[2 * i + 1], s1)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][blk], af, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
-          }
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            float v = s[nt][blk][i] * mult[nt][i & 1];
-            if (masked) {
-              const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
-              const int hi_tok = last[nt][i & 1], lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
-              if (tok > hi_tok || tok < lo_tok || !(valid >> blk & 1)) v = -INFINITY;
+          for (int r = 0; r < 2; ++r) {
+            const int row = token_of(g8) + 8 * r;
+            const uint8_t* sf = kb + L::kKeyScales + row * L::kScaleRow;
+            if constexpr (D == 128) {
+              const uint4 v = *reinterpret_cast<const uint4*>(kb + row * L::kCodeRow + 16 * t4);
+              kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
+              const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(sf + 2 * t4));
+              ks[r][0] = __byte_perm(two, 0, 0x1010);
+              ks[r][1] = __byte_perm(two, 0, 0x3232);
+            } else {
+              const uint2 v = *reinterpret_cast<const uint2*>(kb + row * L::kCodeRow + 8 * t4);
+              kw[r][0] = v.x, kw[r][1] = v.y;
+              ks[r][0] = ks[r][1] = cvt_e4m3x2_f16x2((uint32_t)sf[t4] * 0x101u);
             }
-            s[nt][blk][i] = v;
           }
-      }
-
-      // ------------------------------------------- running maximum and p
-      bool grow = false;
-      float top[NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          top[nt][c] = fmaxf(fmaxf(s[nt][0][c], s[nt][0][c + 2]), fmaxf(s[nt][1][c], s[nt][1][c + 2]));
-          grow |= top[nt][c] > m[nt][c] + kSlack;
+            for (int i = 0; i < 4; ++i) s[nt][blk][i] = 0.0f;
+#pragma unroll
+          for (int w = 0; w < kKeyWords; ++w) {
+            uint32_t lo[4], hi[4];
+            cvt_e2m1x8_f16(kw[0][w], lo);
+            cvt_e2m1x8_f16(kw[1][w], hi);
+            const uint32_t s0 = ks[0][w * 2 / kKeyWords], s1 = ks[1][w * 2 / kKeyWords];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t af[4] = {hmul2_u32(lo[2 * i], s0), hmul2_u32(hi[2 * i], s1),
+                                      hmul2_u32(lo[2 * i + 1], s0), hmul2_u32(hi[2 * i + 1], s1)};
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][blk], af, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
+            }
+          }
+          if constexpr (kMask) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
+                const int hi_tok = last[nt][i & 1], lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
+                if (tok > hi_tok || tok < lo_tok || !(valid >> blk & 1)) s[nt][blk][i] = -INFINITY;
+              }
+          }
         }
-      if (__any_sync(kFull, grow)) {
+
+        // ------------------------------------------- running maximum and p
+        bool grow = false;
+        float top[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float x = top[nt][c];
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-            const float mn = fmaxf(m[nt][c], x);
-            const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][c] - mn);   // 0 from -inf
-            m[nt][c] = mn;
-            l[nt][c] *= f;
+            float x = fmaxf(s[nt][0][c], s[nt][0][c + 2]);
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-              o[nt][mt][c] *= f;
-              o[nt][mt][c + 2] *= f;
+            for (int blk = 1; blk < NB; ++blk) x = fmaxf(x, fmaxf(s[nt][blk][c], s[nt][blk][c + 2]));
+            top[nt][c] = x * mult[nt][c];
+            grow |= top[nt][c] > m[nt][c] + kSlack;
+          }
+        if (__any_sync(kFull, grow)) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+              float x = top[nt][c];
+              x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
+              x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
+              x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
+              const float mn = fmaxf(m[nt][c], x);
+              const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][c] - mn);   // 0 from -inf
+              m[nt][c] = mn;
+              l[nt][c] *= f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) {
+                o[nt][mt][c] *= f;
+                o[nt][mt][c + 2] *= f;
+              }
+            }
+        }
+        uint32_t pf[NT][NB][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float m0 = m[nt][0], m1 = m[nt][1];
+          if constexpr (kMask) {   // a row that has seen nothing yet
+            if (m0 == -INFINITY) m0 = 0.0f;
+            if (m1 == -INFINITY) m1 = 0.0f;
+          }
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            const float p0 = ex2(fmaf(s[nt][blk][0], mult[nt][0], -m0)), p1 = ex2(fmaf(s[nt][blk][1], mult[nt][1], -m1));
+            const float p2 = ex2(fmaf(s[nt][blk][2], mult[nt][0], -m0)), p3 = ex2(fmaf(s[nt][blk][3], mult[nt][1], -m1));
+            l[nt][0] += p0 + p2;
+            l[nt][1] += p1 + p3;
+            pf[nt][blk][0] = movmatrix_trans(pack_f16x2(p0, p1));
+            pf[nt][blk][1] = movmatrix_trans(pack_f16x2(p2, p3));
+          }
+        }
+
+        // ----------------------------------------------------------- values
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          const uint8_t* vb = stage + blk * L::kBytes;
+          uint32_t vw[4][MT / 4];    // value codes of MMA columns 2t, 2t + 1, 2t + 8, 2t + 9
+          uint32_t sc[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int tok = token_of(2 * t4 + (k & 1)) + 8 * (k >> 1);
+            sc[k] = vb[L::kValueScales + tok * L::kScaleRow + (D == 128 ? g8 : g8 / 2)];
+            if constexpr (D == 128) {
+              const uint2 v = *reinterpret_cast<const uint2*>(vb + L::kValueCodes + tok * L::kCodeRow + 8 * g8);
+              vw[k][0] = v.x, vw[k][1] = v.y;
+            } else {
+              vw[k][0] = *reinterpret_cast<const uint32_t*>(vb + L::kValueCodes + tok * L::kCodeRow + 4 * g8);
+            }
+            // what was never appended may decode as NaN: 0 * p instead
+            if constexpr (kMask) {
+              if (tok0 + blk * kKvBlock + tok >= rq.kv || !(valid >> blk & 1)) sc[k] = 0;
             }
           }
-      }
-      uint32_t pf[NT][2][2];
+          const uint32_t s01 = cvt_e4m3x2_f16x2(sc[0] | sc[1] << 8), s23 = cvt_e4m3x2_f16x2(sc[2] | sc[3] << 8);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float m0 = m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m1 = m[nt][1] == -INFINITY ? 0.0f : m[nt][1];
+          for (int w = 0; w < MT / 4; ++w) {
+            // bytes (even d of token 2t, of 2t + 1) and (odd d ...): one conversion gives an MMA register
+            uint32_t e01[4], o01[4], e23[4], o23[4];
+            cvt_e2m1x8_f16((vw[0][w] & 0x0f0f0f0fu) | (vw[1][w] << 4 & 0xf0f0f0f0u), e01);
+            cvt_e2m1x8_f16((vw[0][w] >> 4 & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u), o01);
+            cvt_e2m1x8_f16((vw[2][w] & 0x0f0f0f0fu) | (vw[3][w] << 4 & 0xf0f0f0f0u), e23);
+            cvt_e2m1x8_f16((vw[2][w] >> 4 & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), o23);
 #pragma unroll
-        for (int blk = 0; blk < 2; ++blk) {
-          const float p0 = ex2(s[nt][blk][0] - m0), p1 = ex2(s[nt][blk][1] - m1);
-          const float p2 = ex2(s[nt][blk][2] - m0), p3 = ex2(s[nt][blk][3] - m1);
-          l[nt][0] += p0 + p2;
-          l[nt][1] += p1 + p3;
-          pf[nt][blk][0] = movmatrix_trans(pack_f16x2(p0, p1));
-          pf[nt][blk][1] = movmatrix_trans(pack_f16x2(p2, p3));
-        }
-      }
-
-      // ----------------------------------------------------------- values
+            for (int i = 0; i < 4; ++i) {
+              const uint32_t af[4] = {hmul2_u32(e01[i], s01), hmul2_u32(o01[i], s01), hmul2_u32(e23[i], s23),
+                                      hmul2_u32(o23[i], s23)};
 #pragma unroll
-      for (int blk = 0; blk < 2; ++blk) {
-        const uint8_t* vb = stage + blk * L::kBytes;
-        uint32_t vw[4][MT / 4];    // value codes of MMA columns 2t, 2t + 1, 2t + 8, 2t + 9
-        uint32_t sc[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const int tok = token_of(2 * t4 + (k & 1)) + 8 * (k >> 1);
-          sc[k] = vb[L::kValueScales + tok * L::kScaleRow + (D == 128 ? g8 : g8 / 2)];
-          if constexpr (D == 128) {
-            const uint2 v = *reinterpret_cast<const uint2*>(vb + L::kValueCodes + tok * L::kCodeRow + 8 * g8);
-            vw[k][0] = v.x, vw[k][1] = v.y;
-          } else {
-            vw[k][0] = *reinterpret_cast<const uint32_t*>(vb + L::kValueCodes + tok * L::kCodeRow + 4 * g8);
-          }
-          // what was never appended may decode as NaN: 0 * p instead
-          if (masked && (tok0 + blk * kKvBlock + tok >= rq.kv || !(valid >> blk & 1))) sc[k] = 0;
-        }
-        const uint32_t s01 = cvt_e4m3x2_f16x2(sc[0] | sc[1] << 8), s23 = cvt_e4m3x2_f16x2(sc[2] | sc[3] << 8);
-#pragma unroll
-        for (int w = 0; w < MT / 4; ++w) {
-          // bytes (even d of token 2t, of 2t + 1) and (odd d ...): one conversion gives an MMA register
-          uint32_t e01[4], o01[4], e23[4], o23[4];
-          cvt_e2m1x8_f16((vw[0][w] & 0x0f0f0f0fu) | (vw[1][w] << 4 & 0xf0f0f0f0u), e01);
-          cvt_e2m1x8_f16((vw[0][w] >> 4 & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u), o01);
-          cvt_e2m1x8_f16((vw[2][w] & 0x0f0f0f0fu) | (vw[3][w] << 4 & 0xf0f0f0f0u), e23);
-          cvt_e2m1x8_f16((vw[2][w] >> 4 & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), o23);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t af[4] = {hmul2_u32(e01[i], s01), hmul2_u32(o01[i], s01), hmul2_u32(e23[i], s23),
-                                    hmul2_u32(o23[i], s23)};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], af, pf[nt][blk][0], pf[nt][blk][1]);
+              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], af, pf[nt][blk][0], pf[nt][blk][1]);
+            }
           }
         }
-      }
+      };
+      if (masked) work(std::true_type{});
+      else work(std::false_type{});
 
-      // The stage is free: every word read from it went through an MMA above
-      // (volatile, in order with the copy below), on every lane.
+      __syncwarp();   // every lane has read the stage
       if (next < r1) {
+        // descriptors run out S tiles ahead of the tile being read
+        if (next - base >= 32) describe(tile + 1);
         __syncwarp();
-        if (next - base >= 32) {
-          // descriptors run out S tiles ahead of the tile being read: the
-          // ones still needed (tile + 1 .. next - 1) are kept by shifting
-          describe(tile + 1);
-          __syncwarp();
-        }
-        issue(next);
+        issue(next, slot);
         ++next;
       }
+      cp_async_commit();
 
       // --------------------------------------- the end of a range or segment
       if (tile + 1 == seg_end || tile + 1 == r1) {
@@ -610,18 +635,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
           }
       }
     }
-    if (*abort) {   // copies in flight land before the shared memory is given up
-      for (int t = max(r0, next - S); t < next; ++t) {
-        const long long t0 = clock64();
-        while (!mbar_try_wait(&sm->full[warp][(t - r0) % S], ((t - r0) / S) & 1) && clock64() - t0 < 4000000000ll) {
-        }
-      }
-    }
   }
   __syncthreads();
-  if (sm->abort) {
-    if (tid == 0) set_status(p.status, MOE_ERR_TIMEOUT);
-  }
 
   // ------------------------------------ joins of what this CTA's warps cut
   // A segment that spans several warps' ranges, or leaves the CTA's, is
@@ -712,7 +727,6 @@ moe_status launch_kv4_decode(const moe_kv4_attn_args& a, int max_rows, int* stat
   p.status = status;
   p.counters = counters;
   p.partials = partials;
-  p.wait_limit = debug_wait_limit();
   const int sms = sm_count(), ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
   for (int b0 = 0; b0 < a.batch; b0 += kChunk) {
     p.b0 = b0;
