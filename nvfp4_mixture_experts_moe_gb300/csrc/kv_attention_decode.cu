@@ -75,6 +75,7 @@ struct Smem {
   alignas(128) uint8_t ring[Sh::kWarps][Sh::kStages][Sh::kStageBytes];
   int pre[kChunk + 1];     // tiles (over all heads) before each request
   int warp_sum[Sh::kWarps];
+  int start[Sh::kWarps + 1];   // the warps' ranges
   int last[2];
   static_assert(Sh::kStages * Sh::kStageBytes >= Slots<D, NT>::kFloats * 4, "a warp's ring holds its last partial");
 };
@@ -172,26 +173,38 @@ template <int D, int NT, bool OTHER_CTAS, class Src>
 __device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src, int e0,
                                      int e1, int step, float* dst) {
   constexpr int kRows = 8 * NT;
-  const int group = a.q_heads / a.cache.kv_heads;
+  const int group = a.q_heads / a.cache.kv_heads, rows = rq.n * group;
   for (int e = e0; e < e1; e += step) {
     const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-    if (row >= rq.n * group) continue;
-    float m = -INFINITY;
-    for (int i = 0; i < n; ++i) m = fmaxf(m, load_partial<OTHER_CTAS>(src(i) + kRows * D + 2 * row));
-    const float mu = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f;
+    if (row >= rows) break;   // e only grows
+    // running maximum over the pieces, four loads in flight
+    float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-    for (int i = 0; i < n; ++i) {
-      const float* s = src(i);
-      const float2 ml = load_partial<OTHER_CTAS>(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
-      const float4 v = load_partial<OTHER_CTAS>(reinterpret_cast<const float4*>(s + row * D + d));
-      const float w = ex2(ml.x - mu);
-      l += w * ml.y;
-      o.x += w * v.x;
-      o.y += w * v.y;
-      o.z += w * v.z;
-      o.w += w * v.w;
+#pragma unroll 1
+    for (int i = 0; i < n; i += 4) {
+      float2 ml[4];
+      float4 v[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.0f);
+        v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i + j < n) {
+          const float* s = src(i + j);
+          ml[j] = load_partial<OTHER_CTAS>(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
+          v[j] = load_partial<OTHER_CTAS>(reinterpret_cast<const float4*>(s + row * D + d));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float mn = fmaxf(m, ml[j].x), mu = mn == -INFINITY ? 0.0f : mn;
+        const float w0 = ex2(m - mu), w1 = ex2(ml[j].x - mu);   // 0 from -inf
+        m = mn;
+        l = l * w0 + ml[j].y * w1;
+        o.x = o.x * w0 + v[j].x * w1;
+        o.y = o.y * w0 + v[j].y * w1;
+        o.z = o.z * w0 + v[j].z * w1;
+        o.w = o.w * w0 + v[j].w * w1;
+      }
     }
     if (dst != nullptr) {
       *reinterpret_cast<float4*>(dst + row * D + d) = o;
@@ -201,7 +214,7 @@ __device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& 
       const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
       *reinterpret_cast<uint2*>(a.out + at * D + d) =
           make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
-      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? mu * kLn2 + logf(l) : -INFINITY;
+      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
     }
   }
 }
@@ -272,9 +285,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   const int cta = blockIdx.x;
   if (cta >= G) return;
   const int C0 = (int)((long long)total * cta / G), C1 = (int)((long long)total * (cta + 1) / G);
-  const int wact = min(W, C1 - C0);
-  auto range = [&](int w) { return C0 + (int)((long long)(C1 - C0) * w / wact); };
-  const int r0 = warp < wact ? range(warp) : 0, r1 = warp < wact ? range(warp + 1) : 0;
+  const int wact = min(W, C1 - C0);   // (a CTA's range times W fits 32 bits: it is at most 2^31 / 152 tiles)
+  const int r0 = C0 + (int)((unsigned)(C1 - C0) * min(warp, wact) / (unsigned)wact);
+  const int r1 = C0 + (int)((unsigned)(C1 - C0) * min(warp + 1, wact) / (unsigned)wact);
+  if (lane == 0) sm->start[warp + 1] = r1;   // read after the barrier that follows the loop
+  if (tid == 0) sm->start[0] = C0;
   float* const slots = p.partials;
   auto head_slot = [&](int w) { return slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats; };
   auto tail_slot = [&](int w) { return reinterpret_cast<float*>(&sm->ring[w][0][0]); };
@@ -287,7 +302,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
     // min(P, kTile) tokens. Everything that needs a division or the tables is
     // done here, once in 32 tiles.
     const int run_log = min(p_log - 4, NB == 2 ? 1 : 2);   // log2 of the blocks of a copy
-    int d_b = 0, d_h = 0, d_tok = 0, d_valid = 0, d_seg_end = 0, base = r0;
+    int d_b = 0, d_h = 0, d_tok = 0, d_valid = 0, d_s0 = 0, d_seg_end = 0, base = r0;
     const uint8_t* d_src[NB];
     auto describe = [&](int from) {
       base = from;
@@ -300,6 +315,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
         const Request r = load_request(a, p.b0 + s.b);
         d_b = s.b;
         d_h = s.h;
+        d_s0 = s.s0;
         d_seg_end = s.s1;
         d_tok = (first_seen(a, r) / kTile + (tile - s.s0)) * kTile;
         const int32_t* table = a.block_table + (size_t)(p.b0 + s.b) * a.max_pages + (d_tok >> p_log);
@@ -362,7 +378,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
     int last[NT][2];               // position of the query of rows 2t, 2t + 1
     Request rq = {0, 0, 0, false};
     int h = 0, plain0 = 0, plain1 = 0;   // tiles with every token in [plain0, plain1) need no mask
-    int seg_end = r0, seg_begin = 0;
+    int seg_end = r0;
+    bool from_start = false;             // the segment's first tile is in this range
     int next = r0 + min(S, r1 - r0);     // the next tile to issue
 
     int slot = 0;
@@ -373,7 +390,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
         const int b = __shfl_sync(kFull, d_b, src);
         h = __shfl_sync(kFull, d_h, src);
         seg_end = __shfl_sync(kFull, d_seg_end, src);
-        seg_begin = tile;
+        from_start = __shfl_sync(kFull, d_s0, src) == tile;
         rq = load_request(a, p.b0 + b);
         const int low = a.causal ? rq.kv - rq.n : rq.kv - 1;   // the first row's last token
         plain1 = low + 1;
@@ -599,8 +616,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
 
       // --------------------------------------- the end of a range or segment
       if (tile + 1 == seg_end || tile + 1 == r1) {
-        const Segment sg = segment_of(sm->pre, p.nb, Hk, tile);
-        const bool whole = seg_begin == sg.s0 && tile + 1 == sg.s1;
+        const bool whole = from_start && tile + 1 == seg_end;
         float* dst = tile + 1 == r1 ? tail_slot(warp) : head_slot(warp);
         if (tile + 1 == r1) __syncwarp();   // every lane is done with the ring
 #pragma unroll
@@ -642,7 +658,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   // A segment that spans several warps' ranges, or leaves the CTA's, is
   // joined by those warps, each taking an equal share of its elements.
   constexpr int kElems = kRows * D / 4;
-  auto warp_of = [&](int tile) { return (int)(((long long)(tile - C0 + 1) * wact - 1) / (C1 - C0)); };
+  auto warp_of = [&](int tile) { return (int)(((unsigned)(tile - C0 + 1) * wact - 1) / (unsigned)(C1 - C0)); };
   if (warp < wact) {
     for (int side = 0; side < 2; ++side) {   // the segment this range begins with, then the one it ends with
       const Segment sg = segment_of(sm->pre, p.nb, Hk, side == 0 ? r0 : r1 - 1);
@@ -655,7 +671,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       // warp w's piece is in its tail slot when it reaches the end of w's range
       auto src = [&](int i) -> const float* {
         const int w = w0 + i;
-        return range(w + 1) <= hi ? tail_slot(w) : head_slot(w);
+        return sm->start[w + 1] <= hi ? tail_slot(w) : head_slot(w);
       };
       const int n = w1 - w0 + 1, mine = warp - w0;
       join<D, NT, false>(a, rq, sg.h, n, src, kElems * mine / n + lane, kElems * (mine + 1) / n, 32,
