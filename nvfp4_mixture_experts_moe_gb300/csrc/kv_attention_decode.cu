@@ -69,6 +69,11 @@ struct Shape {
   static constexpr int kThreads = kWarps * 32;
 };
 
+struct Ends {
+  int b, h, s0, s1;   // request, head, tiles
+  int row0, n;
+};
+
 template <int D, int NT>
 struct Smem {
   using Sh = Shape<D, NT>;
@@ -76,8 +81,14 @@ struct Smem {
   int pre[kChunk + 1];     // tiles (over all heads) before each request
   int warp_sum[Sh::kWarps];
   int start[Sh::kWarps + 1];   // the warps' ranges
+  int parked[Sh::kWarps];      // ring stage that holds a warp's first partial
+  Ends ends[Sh::kWarps][2];    // the segments a warp's range begins and ends with
   int last[2];
   static_assert(Sh::kStages * Sh::kStageBytes >= Slots<D, NT>::kFloats * 4, "a warp's ring holds its last partial");
+  // A range has at most one partial before its last: a piece of a segment
+  // that began earlier. It stays in the stage its last tile came from, the
+  // ring going on with one stage less; if it does not fit, it goes to memory.
+  static constexpr bool kPark = Sh::kStageBytes >= Slots<D, NT>::kFloats * 4;
 };
 
 // Lengths of one request, cut to what the tables can hold.
@@ -160,9 +171,9 @@ __device__ __forceinline__ Segment segment_of(const int* pre, int nb, int heads,
   return s;
 }
 
-// Writes rows of a finished (request, head) from n partials: the join's
-// elements [e0, e1) step 32 lanes, four floats each. final: normalised bf16
-// (and lse) to the output, else a partial to dst.
+// Joins n partials of a (request, head), in their order: warp `mine` of `warps`
+// takes its share of the columns, a lane one row. To the output (normalised
+// bf16, lse) or, dst given, to a partial.
 template <bool OTHER_CTAS, class T>
 __device__ __forceinline__ T load_partial(const T* p) {
   if constexpr (OTHER_CTAS) return __ldcg(p);
@@ -170,22 +181,23 @@ __device__ __forceinline__ T load_partial(const T* p) {
 }
 
 template <int D, int NT, bool OTHER_CTAS, class Src>
-__device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src, int e0,
-                                     int e1, int step, float* dst) {
-  constexpr int kRows = 8 * NT;
-  const int group = a.q_heads / a.cache.kv_heads, rows = rq.n * group;
-  for (int e = e0; e < e1; e += step) {
-    const int row = e / (D / 4), d = (e % (D / 4)) * 4;
-    if (row >= rows) break;   // e only grows
-    // running maximum over the pieces, four loads in flight
+__device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src, int mine,
+                                     int warps, float* dst) {
+  constexpr int kRows = 8 * NT, kLanes = 32 / kRows, kBatch = OTHER_CTAS ? 4 : 2;
+  const int group = a.q_heads / a.cache.kv_heads, lane = threadIdx.x & 31, row = lane / kLanes;
+  if (row >= rq.n * group) return;
+  const int c1 = D / 4 * (mine + 1) / warps;
+  for (int c = D / 4 * mine / warps + lane % kLanes; c < c1; c += kLanes) {
+    const int d = 4 * c;
     float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-    for (int i = 0; i < n; i += 4) {
-      float2 ml[4];
-      float4 v[4];
+    for (int i = 0; i < n; i += kBatch) {
+      float2 ml[kBatch];
+      float4 v[kBatch];
+      float mn = m;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < kBatch; ++j) {
         ml[j] = make_float2(-INFINITY, 0.0f);
         v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i + j < n) {
@@ -195,15 +207,22 @@ __device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& 
         }
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float mn = fmaxf(m, ml[j].x), mu = mn == -INFINITY ? 0.0f : mn;
-        const float w0 = ex2(m - mu), w1 = ex2(ml[j].x - mu);   // 0 from -inf
-        m = mn;
-        l = l * w0 + ml[j].y * w1;
-        o.x = o.x * w0 + v[j].x * w1;
-        o.y = o.y * w0 + v[j].y * w1;
-        o.z = o.z * w0 + v[j].z * w1;
-        o.w = o.w * w0 + v[j].w * w1;
+      for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);
+      const float mu = mn == -INFINITY ? 0.0f : mn, w0 = ex2(m - mu);   // 0 from -inf
+      m = mn;
+      l *= w0;
+      o.x *= w0;
+      o.y *= w0;
+      o.z *= w0;
+      o.w *= w0;
+#pragma unroll
+      for (int j = 0; j < kBatch; ++j) {
+        const float w = ex2(ml[j].x - mu);
+        l += w * ml[j].y;
+        o.x += w * v[j].x;
+        o.y += w * v[j].y;
+        o.z += w * v[j].z;
+        o.w += w * v[j].w;
       }
     }
     if (dst != nullptr) {
@@ -288,11 +307,21 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   const int wact = min(W, C1 - C0);   // (a CTA's range times W fits 32 bits: it is at most 2^31 / 152 tiles)
   const int r0 = C0 + (int)((unsigned)(C1 - C0) * min(warp, wact) / (unsigned)wact);
   const int r1 = C0 + (int)((unsigned)(C1 - C0) * min(warp + 1, wact) / (unsigned)wact);
-  if (lane == 0) sm->start[warp + 1] = r1;   // read after the barrier that follows the loop
+  if (lane == 0) {   // read after the barrier that follows the loop
+    sm->start[warp + 1] = r1;
+    sm->parked[warp] = -1;
+  }
+  __syncwarp();
   if (tid == 0) sm->start[0] = C0;
   float* const slots = p.partials;
-  auto head_slot = [&](int w) { return slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats; };
-  auto tail_slot = [&](int w) { return reinterpret_cast<float*>(&sm->ring[w][0][0]); };
+  auto head_slot = [&](int w) {
+    return Sm::kPark ? reinterpret_cast<float*>(&sm->ring[w][sm->parked[w]][0])
+                     : slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats;
+  };
+  // clear of the parked stage: a partial that can be parked is one stage long
+  auto tail_slot = [&](int w) {
+    return reinterpret_cast<float*>(&sm->ring[w][Sm::kPark && sm->parked[w] == 0 ? 1 : 0][0]);
+  };
   auto cta_slot = [&](int c, int which) {
     return slots + ((size_t)kKvMaxCtas * W + (size_t)c * 2 + which) * Slots<D, NT>::kFloats;
   };
@@ -382,16 +411,23 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
     bool from_start = false;             // the segment's first tile is in this range
     int next = r0 + min(S, r1 - r0);     // the next tile to issue
 
-    int slot = 0;
-    for (int tile = r0; tile < r1; ++tile, slot = slot + 1 == S ? 0 : slot + 1) {
+    int slot = 0, parked = -1;
+    auto advance = [&](int s) { return s + 1 == S ? 0 : s + 1; };
+    for (int tile = r0; tile < r1; ++tile) {
       const int src = tile - base;       // < 32: described before it was issued
       const int tok0 = __shfl_sync(kFull, d_tok, src), valid = __shfl_sync(kFull, d_valid, src);
       if (tile == seg_end || tile == r0) {   // a new (request, head)
         const int b = __shfl_sync(kFull, d_b, src);
         h = __shfl_sync(kFull, d_h, src);
         seg_end = __shfl_sync(kFull, d_seg_end, src);
-        from_start = __shfl_sync(kFull, d_s0, src) == tile;
+        const int s0 = __shfl_sync(kFull, d_s0, src);
+        from_start = s0 == tile;
         rq = load_request(a, p.b0 + b);
+        if (lane == 0) {
+          const Ends e = {b, h, s0, seg_end, rq.row0, rq.n};
+          if (tile == r0) sm->ends[warp][0] = e;
+          if (seg_end >= r1) sm->ends[warp][1] = e;
+        }
         const int low = a.causal ? rq.kv - rq.n : rq.kv - 1;   // the first row's last token
         plain1 = low + 1;
         plain0 = a.window > 0 ? rq.kv - a.window : 0;
@@ -447,7 +483,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
         }
       }
 
-      cp_async_wait<S - 1>();   // this tile's group, on every lane
+      if (parked < 0) cp_async_wait<S - 1>();   // this tile's group, on every lane
+      else cp_async_wait<S - 2>();
       __syncwarp();
       const uint8_t* stage = &sm->ring[warp][0][0] + slot * Sh::kStageBytes;
       const bool masked = tok0 < plain0 || tok0 + kTile > plain1 || valid != (1 << NB) - 1;
@@ -605,7 +642,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       else work(std::false_type{});
 
       __syncwarp();   // every lane has read the stage
-      if (next < r1) {
+      const bool seg_done = tile + 1 == seg_end, done = tile + 1 == r1;
+      const bool park = Sm::kPark && seg_done && !done && !from_start;
+      if (park) {
+        parked = slot;
+        if (lane == 0) sm->parked[warp] = slot;
+        __syncwarp();
+      } else if (next < r1) {
         // descriptors run out S tiles ahead of the tile being read
         if (next - base >= 32) describe(tile + 1);
         __syncwarp();
@@ -615,10 +658,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       cp_async_commit();
 
       // --------------------------------------- the end of a range or segment
-      if (tile + 1 == seg_end || tile + 1 == r1) {
-        const bool whole = from_start && tile + 1 == seg_end;
-        float* dst = tile + 1 == r1 ? tail_slot(warp) : head_slot(warp);
-        if (tile + 1 == r1) __syncwarp();   // every lane is done with the ring
+      if (seg_done || done) {
+        const bool whole = from_start && seg_done;
+        float* dst = done ? tail_slot(warp) : head_slot(warp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -650,6 +692,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
             }
           }
       }
+      slot = advance(slot);
+      if (slot == parked) slot = advance(slot);
     }
   }
   __syncthreads();
@@ -657,58 +701,56 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   // ------------------------------------ joins of what this CTA's warps cut
   // A segment that spans several warps' ranges, or leaves the CTA's, is
   // joined by those warps, each taking an equal share of its elements.
-  constexpr int kElems = kRows * D / 4;
   auto warp_of = [&](int tile) { return (int)(((unsigned)(tile - C0 + 1) * wact - 1) / (unsigned)(C1 - C0)); };
   if (warp < wact) {
     for (int side = 0; side < 2; ++side) {   // the segment this range begins with, then the one it ends with
-      const Segment sg = segment_of(sm->pre, p.nb, Hk, side == 0 ? r0 : r1 - 1);
+      const Ends sg = sm->ends[warp][side];
       if (side == 1 && sg.s0 <= r0) break;    // the same segment
       const int lo = max(sg.s0, C0), hi = min(sg.s1, C1);
       const int w0 = warp_of(lo), w1 = warp_of(hi - 1);
       const bool inside = sg.s0 >= C0 && sg.s1 <= C1;
       if (inside && w0 == w1) continue;       // written when it ended
-      const Request rq = load_request(a, p.b0 + sg.b);
+      const Request rq = {sg.row0, sg.n, 0, false};
       // warp w's piece is in its tail slot when it reaches the end of w's range
       auto src = [&](int i) -> const float* {
         const int w = w0 + i;
         return sm->start[w + 1] <= hi ? tail_slot(w) : head_slot(w);
       };
-      const int n = w1 - w0 + 1, mine = warp - w0;
-      join<D, NT, false>(a, rq, sg.h, n, src, kElems * mine / n + lane, kElems * (mine + 1) / n, 32,
-                  inside ? nullptr : cta_slot(cta, sg.s0 < C0 ? 0 : 1));
+      join<D, NT, false>(a, rq, sg.h, w1 - w0 + 1, src, warp - w0, w1 - w0 + 1,
+                         inside ? nullptr : cta_slot(cta, sg.s0 < C0 ? 0 : 1));
     }
   }
 
   // --------------------------- segments that several CTAs cut: the last joins
-  const Segment first = segment_of(sm->pre, p.nb, Hk, C0), end = segment_of(sm->pre, p.nb, Hk, C1 - 1);
+  const Ends first = sm->ends[0][0], end = sm->ends[wact - 1][1];
   const bool cut0 = first.s0 < C0, cut1 = end.s1 > C1 && end.s0 >= C0;
   if (!cut0 && !cut1) return;
   auto cta_of = [&](int tile) { return (int)(((long long)(tile + 1) * G - 1) / total); };
-  __threadfence();
   __syncthreads();
   if (tid < 2) {
     const bool cut = tid == 0 ? cut0 : cut1;
     int is_last = 0;
     if (cut) {
-      const Segment& sg = tid == 0 ? first : end;
+      const Ends& sg = tid == 0 ? first : end;
       const int c0 = cta_of(sg.s0), c1 = cta_of(sg.s1 - 1);
+      __threadfence();   // cumulative: the CTA's partials, ordered before by the barrier
       if (atomicAdd(p.counters + c0, 1) == c1 - c0) {
         p.counters[c0] = 0;   // everyone has arrived: ready for the next launch
         is_last = 1;
       }
+      __threadfence();
     }
     sm->last[tid] = is_last;
   }
   __syncthreads();
   for (int side = 0; side < 2; ++side) {
     if (!sm->last[side]) continue;
-    __threadfence();
-    const Segment& sg = side == 0 ? first : end;
+    const Ends& sg = side == 0 ? first : end;
     const int c0 = cta_of(sg.s0), n = cta_of(sg.s1 - 1) - c0 + 1;
-    const Request rq = load_request(a, p.b0 + sg.b);
+    const Request rq = {sg.row0, sg.n, 0, false};
     // the CTA the segment begins in holds its tail, the others their head
     auto src = [&](int i) -> const float* { return cta_slot(c0 + i, i == 0 ? 1 : 0); };
-    join<D, NT, true>(a, rq, sg.h, n, src, tid, kElems, Sh::kThreads, nullptr);
+    join<D, NT, true>(a, rq, sg.h, n, src, warp, W, nullptr);
   }
 }
 
