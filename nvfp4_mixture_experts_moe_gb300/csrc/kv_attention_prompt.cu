@@ -44,6 +44,8 @@ constexpr int kWarpBlocks = kTok / kKvBlock / kDeqWarps;
 static_assert(kWarpBlocks == 2, "blocks of a dequant warp");
 constexpr int kMmaWarp = kSoftWarps + kDeqWarps;
 constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kSetup = 2;              // what starting and ending a row tile costs, in KV tiles
+constexpr int kSplitRows = 64;         // row tiles of up to this many rows are split over their KV tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;
 constexpr unsigned kFull = 0xffffffffu;
@@ -61,23 +63,6 @@ struct PromptArgs {
 
 template <int D>
 constexpr int kSlotFloats = kRowTile * (D + 2);
-
-template <int D>
-struct Smem {
-  static constexpr int kHalves = D / 64;
-  static constexpr int kTile = kHalves * 128 * 128;   // 128 rows x D f16
-  alignas(1024) uint8_t q[2][kTile];
-  alignas(1024) uint8_t k[2][kTile];
-  alignas(1024) uint8_t v[2][kTile];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
-  uint64_t drain;
-  alignas(8) uint8_t hole[4][8];       // blocks of a tile whose page is bad
-  int pre[kChunk + 1];                 // KV tiles (over all heads and row tiles) before each request
-  uint32_t tmem_base;
-  int abort;
-  int last[2];
-};
 
 struct Request {
   int row0, n, kv;
@@ -110,81 +95,135 @@ __device__ __forceinline__ int row_tile_tiles(const moe_kv4_attn_args& a, const 
   return max(1, (hi + kTok - 1) / kTok - lo / kTok);
 }
 
-// The pieces of a CTA's range, one (request, head, row tile) after another.
-// Every warp role walks them for itself; all lanes call it together.
-struct Pieces {
-  const moe_kv4_attn_args& a;
-  const int* pre;
-  int b0, nb, group, c1;
-  // the current piece
-  Request rq;
-  int b, h, q;
-  int x;            // linear index of the piece's first tile
+// Where a warp stands in its CTA's range, one (request, head, row tile) after
+// another. The range counts units: a row tile's kSetup first units stand for
+// its set-up and its end, then one unit per KV tile; a piece that holds only
+// set-up units is passed over. Every warp walks the range for itself, in its
+// own copy in shared memory, through two functions that are not inlined: the
+// kernel's loops have to stay small, its warps run different code and share
+// one instruction cache.
+struct Walk {
+  int row0, n, kv;  // the request
+  int b, h, q;      // request (within the launch), head, row tile
+  int x;            // linear index of the row tile's first unit
   int first;        // first token of the row tile's first KV tile
   int tiles;        // KV tiles of the row tile
   int t0, t1;       // this piece's
-  int per_head;     // KV tiles of the request per head
+  int more;         // 0 past the last piece
+};
 
-  __device__ __forceinline__ Pieces(const moe_kv4_attn_args& a_, const int* pre_, int b0_, int nb_, int group_, int C0,
-                                    int C1)
-      : a(a_), pre(pre_), b0(b0_), nb(nb_), group(group_), c1(C1), x(C0) {
-    const int lane = threadIdx.x & 31;
-    int lo = 0, hi = nb - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (pre[mid] <= C0) lo = mid;
-      else hi = mid - 1;
+struct Range {
+  const PromptArgs* p;
+  const int* pre;   // units before each request
+  int C0, C1;       // the CTA's
+};
+
+__device__ __noinline__ void walk_next(const Range& rg, Walk* w) {
+  const moe_kv4_attn_args& a = rg.p->a;
+  const int group = a.q_heads / a.cache.kv_heads;
+  Request r = {w->row0, w->n, w->kv, false};
+  int x = w->x, tiles = w->tiles, q = w->q, first = 0, t1;
+  do {
+    x += tiles + kSetup;
+    if (x >= rg.C1) {
+      w->more = 0;
+      return;
     }
-    enter(lo);
-    int rem = C0 - pre[b];
-    h = rem / per_head;
-    rem -= h * per_head;
-    // 32 row tiles at a time until the one that holds the tile
-    for (q = 0;; q += 32) {
-      int f, v = (long long)(q + lane) * kRowTile < (long long)rq.n * group ? row_tile_tiles(a, rq, group, q + lane, f) : 0;
-      int incl = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += u;
-      }
-      const unsigned past = __ballot_sync(kFull, incl > rem);
-      if (past) {
-        const int at = __ffs(past) - 1;
-        rem -= __shfl_sync(kFull, incl - v, at);
-        q += at;
-        break;
-      }
-      rem -= __shfl_sync(kFull, incl, 31);
-    }
-    tiles = row_tile_tiles(a, rq, group, q, first);
-    t0 = rem;
-    t1 = min(tiles, rem + c1 - x);
-  }
-  __device__ __forceinline__ void enter(int b_) {
-    b = b_;
-    rq = load_request(a, b0 + b);
-    per_head = (pre[b + 1] - pre[b]) / a.cache.kv_heads;
-  }
-  __device__ __forceinline__ bool more() const { return x < c1; }
-  __device__ __forceinline__ void next() {
-    x += t1 - t0;
-    if (x >= c1) return;
-    if ((long long)(++q) * kRowTile >= (long long)rq.n * group) {
+    if ((long long)(++q) * kRowTile >= (long long)r.n * group) {
       q = 0;
-      if (++h == a.cache.kv_heads) {
-        h = 0;
-        int nx = b + 1;
-        while (pre[nx + 1] == pre[nx]) ++nx;
-        enter(nx);
+      if (++w->h == a.cache.kv_heads) {
+        w->h = 0;
+        do ++w->b;
+        while (rg.pre[w->b + 1] == rg.pre[w->b]);
+        r = load_request(a, rg.p->b0 + w->b);
+        w->row0 = r.row0;
+        w->n = r.n;
+        w->kv = r.kv;
       }
     }
-    tiles = row_tile_tiles(a, rq, group, q, first);
-    t0 = 0;
-    t1 = min(tiles, c1 - x);
+    tiles = row_tile_tiles(a, r, group, q, first);
+    t1 = min(tiles, rg.C1 - x - kSetup);
+  } while (t1 <= 0);
+  w->x = x;
+  w->q = q;
+  w->first = first;
+  w->tiles = tiles;
+  w->t0 = 0;
+  w->t1 = t1;
+}
+
+// All lanes together.
+__device__ __noinline__ void walk_begin(const Range& rg, Walk* w) {
+  const moe_kv4_attn_args& a = rg.p->a;
+  const int lane = threadIdx.x & 31, group = a.q_heads / a.cache.kv_heads;
+  int lo = 0, hi = rg.p->nb - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (rg.pre[mid] <= rg.C0) lo = mid;
+    else hi = mid - 1;
   }
-  __device__ __forceinline__ int rows() const { return min(kRowTile, rq.n * group - q * kRowTile); }
-  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == tiles; }
+  const Request r = load_request(a, rg.p->b0 + lo);
+  const int per_head = (rg.pre[lo + 1] - rg.pre[lo]) / a.cache.kv_heads;
+  int rem = rg.C0 - rg.pre[lo];
+  const int h = rem / per_head;
+  rem -= h * per_head;
+  int q = 0, f = 0, tiles;
+  for (;; q += 32) {   // 32 row tiles at a time until the one that holds the unit
+    const int v = (long long)(q + lane) * kRowTile < (long long)r.n * group
+                      ? row_tile_tiles(a, r, group, q + lane, f) + kSetup
+                      : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const unsigned past = __ballot_sync(kFull, incl > rem);
+    if (past) {
+      const int at = __ffs(past) - 1;
+      rem -= __shfl_sync(kFull, incl - v, at);
+      tiles = __shfl_sync(kFull, v, at) - kSetup;
+      f = __shfl_sync(kFull, f, at);
+      q += at;
+      break;
+    }
+    rem -= __shfl_sync(kFull, incl, 31);
+  }
+  if (lane == 0) {
+    const int x = rg.C0 - rem, t0 = max(0, rem - kSetup), t1 = min(tiles, rg.C1 - x - kSetup);
+    *w = {r.row0, r.n, r.kv, lo, h, q, x, f, tiles, t0, t1, 1};
+    if (t1 <= t0) walk_next(rg, w);
+  }
+  __syncwarp();
+}
+
+// A row tile at one end of a CTA's range.
+struct Ends {
+  int row0, rows, h, q;   // first query row of the request, rows of the tile, head, index
+  int lo, hi;             // the CTAs that hold its first and its last KV tile
+  int t0, t1, tiles;      // KV tiles done here, of all
+};
+
+template <int D>
+struct Smem {
+  static constexpr int kHalves = D / 64;
+  static constexpr int kTile = kHalves * 128 * 128;   // 128 rows x D f16
+  alignas(1024) uint8_t q[2][kTile];
+  alignas(1024) uint8_t kv[2][2][kTile];   // keys, values: two stages each
+  uint64_t q_full[2], s_full[2], o_full[2];
+  uint64_t p_full[2][2];               // the halves of P
+  uint64_t h_done[2];                  // the first half's product is in O
+  uint64_t kv_full[2][2], kv_empty[2][2];   // [keys or values][stage]
+  uint64_t x_full, x_empty;            // the second warpgroup's half of a split row tile
+  uint64_t drain;
+  float2 x_ml[kSplitRows];             // (m, l) of its rows; its output lies in q[1]
+  alignas(8) uint8_t hole[4][8];       // blocks of a tile whose page is bad
+  int pre[kChunk + 1];                 // units (over all heads and row tiles) before each request
+  Walk walk[kThreads / 32];
+  Ends ends[2];                        // the first and the last row tile of this CTA's range
+  uint32_t tmem_base;
+  int abort;
+  int last[2];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -198,9 +237,51 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-__device__ __forceinline__ float2 pow2_pair(int k) {
-  const int h = k >> 1;
-  return make_float2(__int_as_float((127 + h) << 23), __int_as_float((127 + k - h) << 23));
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ float2 unpack2(uint64_t v) {
+  float2 r;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
+// Waits for the tensor-memory loads in flight; the registers they fill are
+// operands, so no use of them moves ahead of the wait.
+__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+// 2^k for -126 <= k <= 127.
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 // Byte offset of 16-byte chunk c (of D/8) of row r in a 128-row f16 tile:
@@ -214,7 +295,7 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
+__global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_constant__ PromptArgs p) {
   using L = Kv4Block<D>;
   using Sm = Smem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -223,20 +304,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hk = a.cache.kv_heads, group = a.q_heads / Hk;
 
-  // ------------------------------------------------ tiles before each request
+  // ------------------------------------------------ units before each request
   if (tid == 0) {
     sm->abort = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->q_full[i], 4);
       mbar_init(&sm->s_full[i], 1);
-      mbar_init(&sm->p_full[i], 4);
+      mbar_init(&sm->p_full[i][0], 4);
+      mbar_init(&sm->p_full[i][1], 4);
+      mbar_init(&sm->h_done[i], 1);
       mbar_init(&sm->o_full[i], 1);
-      mbar_init(&sm->k_full[i], kDeqWarps);
-      mbar_init(&sm->k_empty[i], 1);
-      mbar_init(&sm->v_full[i], kDeqWarps);
-      mbar_init(&sm->v_empty[i], 1);
+      mbar_init(&sm->kv_full[0][i], kDeqWarps);
+      mbar_init(&sm->kv_full[1][i], kDeqWarps);
+      mbar_init(&sm->kv_empty[0][i], 1);
+      mbar_init(&sm->kv_empty[1][i], 1);
     }
+    mbar_init(&sm->x_full, 4);
+    mbar_init(&sm->x_empty, 4);
     mbar_init(&sm->drain, 1);
+    sm->ends[0].tiles = sm->ends[1].tiles = 0;
     fence_barrier_init();
   }
   for (int b = warp; b < p.nb; b += kThreads / 32) {   // a warp per request
@@ -246,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
     if (rows > p.min_rows)
       for (int q = lane; (long long)q * kRowTile < rows; q += 32) {
         int f;
-        sum += row_tile_tiles(a, r, group, q, f);
+        sum += row_tile_tiles(a, r, group, q, f) + kSetup;
       }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
@@ -275,8 +361,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
   const int total = sm->pre[p.nb];
   const int G = min((int)gridDim.x, total), cta = blockIdx.x;
   if (cta >= G) return;
-  const int C0 = (int)((long long)total * cta / G), C1 = (int)((long long)total * (cta + 1) / G);
+  const Range rg = {&p, sm->pre, (int)((long long)total * cta / G), (int)((long long)total * (cta + 1) / G)};
   if (warp == kMmaWarp) tmem_alloc(&sm->tmem_base, kTmemCols);
+  Walk* const w = &sm->walk[warp];
+  walk_begin(rg, w);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -286,181 +374,243 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
   auto wait = [&](uint64_t* bar, int phase) {   // all lanes: the warp's common answer
     return __all_sync(kFull, mbar_wait(bar, (uint32_t)(phase & 1), abort, p.wait_limit)) != 0;
   };
-  Pieces pc(a, sm->pre, p.b0, p.nb, group, C0, C1);
+  auto next = [&]() {                           // the warp's next piece
+    __syncwarp();
+    if (lane == 0) walk_next(rg, w);
+    __syncwarp();
+  };
+  auto cta_of = [&](int unit) { return (int)(((long long)(unit + 1) * G - 1) / total); };
+  auto record = [&](int which) {                // the warp's piece as one of the range's ends
+    if (lane == 0)
+      sm->ends[which] = {w->row0, min(kRowTile, w->n * group - w->q * kRowTile), w->h, w->q, cta_of(w->x + kSetup),
+                         cta_of(w->x + kSetup + w->tiles - 1), w->t0, w->t1, w->tiles};
+  };
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
     const int i = warp >> 2;                       // row tile of this warpgroup
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t s_t = tmem + lanes + 128 * i, o_t = tmem + lanes + 256 + 128 * i;
-    int js = 0, jo = 0;                            // S tiles and items this warpgroup has seen
-    int jt = 0;                                    // tiles of the CTA before the current piece
-    bool ok = true;
-    for (; pc.more() && ok; pc.next()) {
-      const int rows = pc.rows(), nt = pc.t1 - pc.t0;
+    int js = 0, jo = 0, jx = 0;                    // S tiles, items, split items this warpgroup has seen
+    int jt = 0;                                    // tiles of the CTA before the next piece
+    for (; w->more; next()) {
+      const int q0 = w->q * kRowTile, rows = min(kRowTile, w->n * group - q0);
+      const int t0 = w->t0, nt = w->t1 - t0, kv = w->kv, row0 = w->row0, h = w->h;
       const int jt0 = jt;
       jt += nt;
-      if (i * 128 >= rows) continue;
-      const int r = i * 128 + (warp & 3) * 32 + lane;   // row within the item
-      const bool real = r < rows, active = i * 128 + (warp & 3) * 32 < rows;
-      const int rr = pc.q * kRowTile + (real ? r : 0), token = rr / group;
-      const size_t at = (size_t)(pc.rq.row0 + token) * a.q_heads + pc.h * group + rr % group;
-      // the row as f16, largest element in [2^14, 2^15)
+      // A row tile of few rows: both warpgroups hold all its rows and take
+      // every other KV tile, joined at the end.
+      const bool split = rows <= kSplitRows;
+      if (!split && i * 128 >= rows) continue;
+      const int r = (split ? 0 : i * 128) + (warp & 3) * 32 + lane;   // row within the item
+      const bool real = r < rows, active = r - lane < rows;
+      const int rr = q0 + (real ? r : 0), token = rr / group, qh = h * group + rr - token * group;
+      const size_t at = (size_t)(row0 + token) * a.q_heads + qh;
+      // the row as f16, largest element in [2^14, 2^15) (smaller only below 2^-112)
       float c;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(pc.rq.row0 + token) * a.q_stride +
-                                                          (pc.h * group + rr % group) * D);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(row0 + token) * a.q_stride + qh * D);
+        const uint32_t dst = smem_u32(&sm->q[split ? 0 : i][0]);
+        const bool keep = !split || i == 0;
+        uint4 raw[D / 8];
+#pragma unroll
+        for (int v = 0; v < D / 8; ++v) raw[v] = __ldg(src + v);
         uint32_t mx = 0;
 #pragma unroll
         for (int v = 0; v < D / 8; ++v) {
-          const uint4 w = __ldg(src + v);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            mx = max(mx, max(finite_mag(ww[j] & 0x7fffu), finite_mag((ww[j] >> 16) & 0x7fffu)));
+          mx = max_u16x2(max_u16x2(mx, raw[v].x & 0x7fff7fffu), raw[v].y & 0x7fff7fffu);
+          mx = max_u16x2(max_u16x2(mx, raw[v].z & 0x7fff7fffu), raw[v].w & 0x7fff7fffu);
+          if (keep) sts16(dst + tile_chunk(r & 127, v), raw[v]);   // converted in place below
         }
-        const int ex = min(max((int)(mx >> 7), 1), 254);
-        float2 up = pow2_pair(141 - ex);
-        const float2 dn = pow2_pair(ex - 141);
+        const int ex = min(max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15), 254);
         // never 0, so that a hidden score stays -inf
-        c = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * dn.x * dn.y, 1e-37f);
-        if (a.scale < 0.0f) up.x = -up.x;          // so that larger scores stay larger products
-        const uint32_t dst = smem_u32(&sm->q[i][0]);
-#pragma unroll 4
-        for (int v = 0; v < D / 8; ++v) {
-          const uint4 w = __ldg(src + v);
-          const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-          uint32_t o[4];
+        c = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
+        const float up = a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);   // larger scores stay larger products
+        if (keep) {
+#pragma unroll 2
+          for (int v = 0; v < D / 8; ++v) {
+            uint4* chunk = reinterpret_cast<uint4*>(&sm->q[split ? 0 : i][tile_chunk(r & 127, v)]);
+            uint4 x = *chunk;
+            uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
-          for (int j = 0; j < 4; ++j)
-            o[j] = pack_f16x2(__uint_as_float(ww[j] << 16) * up.x * up.y,
-                              __uint_as_float(ww[j] & 0xffff0000u) * up.x * up.y);
-          sts16(dst + tile_chunk(r & 127, v), make_uint4(o[0], o[1], o[2], o[3]));
+            for (int j = 0; j < 4; ++j)
+              xw[j] = pack_f16x2(__uint_as_float(xw[j] << 16) * up, __uint_as_float(xw[j] & 0xffff0000u) * up);
+            *chunk = x;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->q_full[split ? 0 : i]);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->q_full[i]);
-      const int hi_tok = a.causal ? pc.rq.kv - pc.rq.n + token : pc.rq.kv - 1;
+      const int hi_tok = a.causal ? kv - w->n + token : kv - 1;
       const int lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
-      float m = -INFINITY, l0 = 0.0f, l1 = 0.0f;
-      for (int t = 0; t < nt; ++t, ++js) {
+      const int tok_first = w->first + t0 * kTok;
+      float m = -INFINITY;
+      uint64_t l2 = pack2(0.0f, 0.0f);
+      const uint64_t c2 = pack2(c, c);
+      const int step = split ? 2 : 1, begin = split ? i : 0;
+      bool ok = true;
+      for (int t = begin; t < nt && ok; t += step, ++js) {
         if (!(ok = wait(&sm->s_full[i], js))) break;
         tc_fence_after();
-        if (active) {
-          const int tok0 = pc.first + (pc.t0 + t) * kTok;
-          const uint64_t hole = *reinterpret_cast<const volatile uint64_t*>(sm->hole[(jt0 + t) & 3]);
-          const bool masked = __any_sync(kFull, tok0 + kTok - 1 > hi_tok || tok0 < lo_tok) || hole != 0;
+        const int tok0 = tok_first + t * kTok;
+        const uint64_t hole = *reinterpret_cast<const volatile uint64_t*>(sm->hole[(jt0 + t) & 3]);
+        const bool masked = __any_sync(kFull, tok0 + kTok - 1 > hi_tok || tok0 < lo_tok) || hole != 0;
+        // one 32-column piece of S, read while the piece before is worked on
+        auto work = [&](uint32_t (&sr)[32], int piece) {
+          if (masked) {   // bit e: column e is seen
+            const int hi = hi_tok - tok0 - 32 * piece, lo = lo_tok - tok0 - 32 * piece;
+            uint32_t see = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
+            see &= lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+            const uint32_t bad = (uint32_t)(hole >> (16 * piece));
+            if (bad & 0xffu) see &= 0xffff0000u;
+            if (bad & 0xff00u) see &= 0x0000ffffu;
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (!(see >> e & 1u)) sr[e] = 0xff800000u;
+          }
+          float u0 = __uint_as_float(sr[0]), u1 = __uint_as_float(sr[1]);
+#pragma unroll
+          for (int e = 2; e < 30; e += 4) {
+            u0 = max3(u0, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+            u1 = max3(u1, __uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
+          }
+          const float top = max3(u0, u1, fmaxf(__uint_as_float(sr[30]), __uint_as_float(sr[31]))) * c;
+          if (__any_sync(kFull, top > m + kSlack)) {
+            const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+            m = mn;
+            const float2 l = unpack2(l2);
+            l2 = pack2(l.x * f, l.y * f);
+            // From piece 2 on the first half of P is with the tensor core:
+            // O waits for it, and it needs no factor of its own.
+            const bool handed = piece >= 2;
+            if (handed && !wait(&sm->h_done[i], js)) return false;
+            if (handed) tc_fence_after();
+            if (t > begin || handed) {
 #pragma unroll 1
-          for (int piece = 0; piece < 4; ++piece) {
-            uint32_t sr[32];
-            tmem_ld32(s_t + 32 * piece, sr);
-            tmem_ld_wait();
-            float s[32];
-#pragma unroll
-            for (int e = 0; e < 32; ++e) s[e] = __uint_as_float(sr[e]);
-            if (masked) {
-              const int base = tok0 + 32 * piece;
-              const uint32_t bad = (uint32_t)(hole >> (16 * piece)) & 0xffffu;
-#pragma unroll
-              for (int e = 0; e < 32; ++e)
-                if (base + e > hi_tok || base + e < lo_tok || (bad >> (8 * (e / 16)) & 0xffu)) s[e] = -INFINITY;
-            }
-            float t0 = fmaxf(s[0], s[1]), t1 = fmaxf(s[2], s[3]);
-#pragma unroll
-            for (int e = 4; e < 32; e += 4) {
-              t0 = fmaxf(t0, fmaxf(s[e], s[e + 1]));
-              t1 = fmaxf(t1, fmaxf(s[e + 2], s[e + 3]));
-            }
-            const float top = fmaxf(t0, t1) * c;
-            if (__any_sync(kFull, top > m + kSlack)) {
-              const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
-              m = mn;
-              l0 *= f;
-              l1 *= f;
-              if (t > 0) {
-#pragma unroll 1
-                for (int cc = 0; cc < D; cc += 16) {
-                  uint32_t o[16];
-                  tmem_ld16(o_t + cc, o);
-                  tmem_ld_wait();
-#pragma unroll
-                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                  tmem_st16(o_t + cc, o);
-                }
-              }
-              const uint32_t f2 = pack_f16x2(f, f);   // pieces of P already stored: one more f16 rounding
-#pragma unroll 1
-              for (int pp = 0; pp < piece; ++pp) {
+              for (int cc = 0; cc < D; cc += 16) {
                 uint32_t o[16];
-                tmem_ld16(s_t + 16 * pp, o);
+                tmem_ld16(o_t + cc, o);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(o[e], f2);
-                tmem_st16(s_t + 16 * pp, o);
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                tmem_st16(o_t + cc, o);
               }
-              tmem_st_wait();
             }
-            const float mu = m == -INFINITY ? 0.0f : m;
-            uint32_t pk[16];
+            const uint32_t f2 = pack_f16x2(f, f);   // pieces of P already stored: one more f16 rounding
+#pragma unroll 1
+            for (int pp = handed ? 2 : 0; pp < piece; ++pp) {
+              uint32_t o[16];
+              tmem_ld16(s_t + 16 * pp, o);
+              tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-              const float p0 = ex2(fmaf(s[2 * e], c, -mu)), p1 = ex2(fmaf(s[2 * e + 1], c, -mu));
-              l0 += p0;
-              l1 += p1;
-              pk[e] = pack_f16x2(p0, p1);
+              for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(o[e], f2);
+              tmem_st16(s_t + 16 * pp, o);
             }
-            tmem_st16(s_t + 16 * piece, pk);
+            tmem_st_wait();
           }
-          tmem_st_wait();
-          tc_fence_before();
+          const float mu = m == -INFINITY ? 0.0f : m;
+          const uint64_t m2 = pack2(-mu, -mu);
+          uint32_t pk[16];
+          uint64_t sum = pack2(0.0f, 0.0f);
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 y = unpack2(fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), c2, m2));
+            const float p0 = ex2(y.x), p1 = ex2(y.y);
+            sum = add2(sum, pack2(p0, p1));
+            pk[e] = pack_f16x2(p0, p1);
+          }
+          l2 = add2(l2, sum);
+          tmem_st16(s_t + 16 * piece, pk);
+          return true;
+        };
+        // P's halves are handed over as they are done. A half lies in columns
+        // of S that have been read: pieces 0, 1 write [0, 32), 2, 3 [32, 64).
+        uint32_t s0[32], s1[32];
+        if (active) tmem_ld32(s_t, s0);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (active) {
+            ld_wait(s0);
+            tmem_ld32(s_t + 64 * half + 32, s1);
+            ok = work(s0, 2 * half) && ok;
+            ld_wait(s1);
+            if (half == 0) tmem_ld32(s_t + 64, s0);
+            ok = work(s1, 2 * half + 1) && ok;
+            tmem_st_wait();
+            tc_fence_before();
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->p_full[i][half]);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->p_full[i]);
       }
-      if (!ok || !(ok = wait(&sm->o_full[i], jo))) break;
-      ++jo;
+      if (!ok) break;
+      const bool any = begin < nt;                 // the second half of a split tile may be empty
+      if (any && !wait(&sm->o_full[i], jo++)) break;
       tc_fence_after();
-      if (!active) continue;
-      const float l = l0 + l1;
-      if (pc.whole()) {
-        const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
-        uint4* out = reinterpret_cast<uint4*>(a.out + at * D);
-#pragma unroll
-        for (int cc = 0; cc < D; cc += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_t + cc, o);
+      float l = unpack2(l2).x + unpack2(l2).y;
+      float* xo = reinterpret_cast<float*>(&sm->q[1][0]);   // a split tile's second half goes through here
+      float own = 1.0f, other = 0.0f;              // factors of this half and of the other
+      if (split && i == 0) {
+        if (!wait(&sm->x_full, jx++)) break;
+        if (active) {
+          const float2 x = sm->x_ml[r];
+          const float mn = fmaxf(m, x.x), mu = mn == -INFINITY ? 0.0f : mn;
+          own = ex2(m - mu);
+          other = ex2(x.x - mu);
+          l = l * own + x.y * other;
+          m = mn;
+        }
+      }
+      if (active) {
+        const bool give = split && i == 1, whole = t0 == 0 && nt == w->tiles;
+        if (!give && whole) own *= l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+        if (!give && whole) other *= l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+        const bool blank = give ? !any : whole && !(l > 0.0f);   // O holds nothing to read
+        float* dst = give ? xo + r * D : slot(cta, t0 > 0 ? 0 : 1) + (size_t)r * D;
+#pragma unroll 1
+        for (int cc = 0; cc < D; cc += 16) {
+          uint32_t o[16];
+          tmem_ld16(o_t + cc, o);
           tmem_ld_wait();
-          if (real) {
+          float f[16];
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              uint32_t w[4];
+          for (int e = 0; e < 16; ++e) f[e] = blank ? 0.0f : __uint_as_float(o[e]) * own;
+          if (split && i == 0) {
 #pragma unroll
-              for (int j = 0; j < 4; ++j)
-                w[j] = l > 0.0f ? float2_to_bf16x2_bits(__uint_as_float(o[e + 2 * j]) * inv,
-                                                        __uint_as_float(o[e + 2 * j + 1]) * inv)
-                                : 0u;
-              out[(cc + e) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int e = 0; e < 16; e += 4) {   // 16-byte chunks swizzled by the row
+              const float4 x = *reinterpret_cast<const float4*>(xo + r * D + (((cc + e) / 4) ^ (r & (D / 4 - 1))) * 4);
+              f[e] += x.x * other;
+              f[e + 1] += x.y * other;
+              f[e + 2] += x.z * other;
+              f[e + 3] += x.w * other;
             }
           }
-        }
-        if (real && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
-      } else {
-        float* dst = slot(cta, pc.t0 > 0 ? 0 : 1);
+          if (!give && !real) continue;
+          if (!give && whole) {
+            uint4* out = reinterpret_cast<uint4*>(a.out + at * D + cc);
+            out[0] = make_uint4(float2_to_bf16x2_bits(f[0], f[1]), float2_to_bf16x2_bits(f[2], f[3]),
+                                float2_to_bf16x2_bits(f[4], f[5]), float2_to_bf16x2_bits(f[6], f[7]));
+            out[1] = make_uint4(float2_to_bf16x2_bits(f[8], f[9]), float2_to_bf16x2_bits(f[10], f[11]),
+                                float2_to_bf16x2_bits(f[12], f[13]), float2_to_bf16x2_bits(f[14], f[15]));
+          } else {
 #pragma unroll
-        for (int cc = 0; cc < D; cc += 32) {
-          uint32_t o[32];
-          tmem_ld32(o_t + cc, o);
-          tmem_ld_wait();
-          if (real) {
-#pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(dst + r * D + cc + e) = make_uint4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+            for (int e = 0; e < 16; e += 4)
+              *reinterpret_cast<float4*>(dst + (give ? (((cc + e) / 4) ^ (r & (D / 4 - 1))) * 4 : cc + e)) =
+                  make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
           }
         }
-        if (real) *reinterpret_cast<float2*>(dst + kRowTile * D + 2 * r) = make_float2(m, l);
+        if (give) sm->x_ml[r] = make_float2(m, l);
+        else if (real && !whole)
+          *reinterpret_cast<float2*>(slot(cta, t0 > 0 ? 0 : 1) + kRowTile * D + 2 * r) = make_float2(m, l);
+        else if (real && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
       }
       tc_fence_before();
+      if (split) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(i == 1 ? &sm->x_full : &sm->x_empty);
+        if (i == 1 && !wait(&sm->x_empty, jx++)) break;
+      }
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------- dequant
@@ -469,102 +619,117 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
     constexpr int kChunks = D / 32;                // 16-byte code chunks of a row
     const int cl = lane % kChunks, tl = lane / kChunks;   // this lane's chunk, and its row within a load
     constexpr int kRowsPerLoad = 32 / kChunks;
-    const int P = a.cache.page_tokens;
+    const int P = a.cache.page_tokens, p_log = __ffs(P) - 1;
     struct Raw {
       uint4 codes[kWarpBlocks][kLoads];
       uint32_t sf[kWarpBlocks][kLoads];            // two scale bytes each
-    } rk, rv;
+    } cur, nxt;
+    // The walk runs two tiles ahead: a tile's page ids are read one tile before
+    // its data, and its data one tile before it is converted.
+    int n_page[kWarpBlocks], n_left[kWarpBlocks], n_at[kWarpBlocks], n_h = 0, lt = w->t0;
+    bool n_any = false;
     const uint8_t* src[kWarpBlocks];
     int left[kWarpBlocks];                         // tokens of the block that exist
-    bool hole[kWarpBlocks];
-    int lt = pc.t0;
-    auto locate = [&]() {                          // the walk's next tile
+    auto look_up = [&]() {                         // page ids of the walk's next tile
+      n_any = w->more != 0;
+#pragma unroll
+      for (int x = 0; x < kWarpBlocks; ++x) n_left[x] = n_page[x] = n_at[x] = 0;
+      if (!n_any) return;
+      n_h = w->h;
+      const int tok0 = w->first + lt * kTok + blk0 * kKvBlock, kv = w->kv;
+      const int32_t* table = a.block_table + (size_t)(p.b0 + w->b) * a.max_pages;
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x) {
-        left[x] = 0;
-        hole[x] = false;
+        const int tok = tok0 + x * kKvBlock;
+        n_left[x] = max(0, kv - tok);
+        n_at[x] = (tok & (P - 1)) / kKvBlock;
+        if (n_left[x] > 0) n_page[x] = __ldg(table + (tok >> p_log));
       }
-      if (!pc.more()) return;
-#pragma unroll
-      for (int x = 0; x < kWarpBlocks; ++x) {
-        const int tok = pc.first + lt * kTok + (blk0 + x) * kKvBlock;
-        if (tok < pc.rq.kv) {
-          const int page = __ldg(a.block_table + (size_t)(pc.b0 + pc.b) * a.max_pages + tok / P);
-          hole[x] = page < 0 || page >= a.cache.num_pages;
-          if (!hole[x]) {
-            left[x] = pc.rq.kv - tok;
-            src[x] = static_cast<const uint8_t*>(a.cache.pool) +
-                     kv4_block_offset(page, pc.h, Hk, P / kKvBlock, tok % P / kKvBlock, L::kBytes);
-          } else if (lane == 0) {
-            set_status(p.status, MOE_ERR_DEVICE);
-          }
-        }
-      }
-      if (++lt == pc.t1) {
-        pc.next();
+      if (++lt == w->t1) {
+        next();
         lt = 0;
       }
     };
-    auto load = [&](Raw& r, int codes, int scales) {
+    bool have = false;
+    uint32_t holes = 0;                            // of the located tile, bit x
+    auto locate = [&]() {                          // where the looked-up tile lies
+      have = n_any;
+      holes = 0;
+#pragma unroll
+      for (int x = 0; x < kWarpBlocks; ++x) {
+        left[x] = n_left[x];
+        if (left[x] > 0 && (n_page[x] < 0 || n_page[x] >= a.cache.num_pages)) {
+          holes |= 1u << x;
+          left[x] = 0;
+          if (lane == 0) set_status(p.status, MOE_ERR_DEVICE);
+        }
+        src[x] = static_cast<const uint8_t*>(a.cache.pool) + tl * L::kCodeRow + 16 * cl +
+                 kv4_block_offset(left[x] > 0 ? n_page[x] : 0, n_h, Hk, P / kKvBlock, n_at[x], L::kBytes);
+      }
+    };
+    auto load = [&](int which) {                   // keys (0) or values (1) of the located tile
+      const int at = which ? L::kValueCodes : 0;
+      const int sat = at + L::kKeyScales - (tl * L::kCodeRow + 16 * cl) + tl * L::kScaleRow + 2 * cl;
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x)
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
-          const int row = y * kRowsPerLoad + tl;
-          r.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what was not appended enters as zeros
-          r.sf[x][y] = 0u;
-          if (row < left[x]) {
-            r.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(src[x] + codes + row * L::kCodeRow + 16 * cl));
-            r.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(src[x] + scales + row * L::kScaleRow + 2 * cl));
+          nxt.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what was not appended enters as zeros
+          nxt.sf[x][y] = 0u;
+          if (y * kRowsPerLoad + tl < left[x]) {
+            nxt.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(src[x] + at + y * kRowsPerLoad * L::kCodeRow));
+            nxt.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(src[x] + sat + y * kRowsPerLoad * L::kScaleRow));
           }
         }
     };
-    auto store = [&](uint32_t tile, const Raw& r) {
+    auto store = [&](uint32_t tile) {
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x)
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
           const int row = (blk0 + x) * kKvBlock + y * kRowsPerLoad + tl;
-          const uint32_t two = cvt_e4m3x2_f16x2(r.sf[x][y]);
-          const uint32_t s0 = __byte_perm(two, 0, 0x1010), s1 = __byte_perm(two, 0, 0x3232);
-          const uint32_t w[4] = {r.codes[x][y].x, r.codes[x][y].y, r.codes[x][y].z, r.codes[x][y].w};
-          uint4 f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            uint32_t h[4];
-            cvt_e2m1x8_f16(w[j], h);
-            const uint32_t sc = j < 2 ? s0 : s1;
-            f[j] = make_uint4(hmul2_u32(h[0], sc), hmul2_u32(h[1], sc), hmul2_u32(h[2], sc), hmul2_u32(h[3], sc));
-          }
+          const uint32_t two = cvt_e4m3x2_f16x2(cur.sf[x][y]);
+          const uint32_t sc0 = __byte_perm(two, 0, 0x1010), sc1 = __byte_perm(two, 0, 0x3232);
+          const uint32_t wd[4] = {cur.codes[x][y].x, cur.codes[x][y].y, cur.codes[x][y].z, cur.codes[x][y].w};
           // the two 64-column halves share banks: their lanes store in different orders
+          const bool flip = D == 128 && cl >= 2;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const bool flip = D == 128 && cl >= 2;
-            const uint4 v = flip ? f[j ^ 2] : f[j];
-            sts16(tile + tile_chunk(row, 4 * cl + (flip ? j ^ 2 : j)), v);
+            uint32_t f[4];
+            cvt_e2m1x8_f16(flip ? wd[j ^ 2] : wd[j], f);
+            const uint32_t sc = (j < 2) != flip ? sc0 : sc1;
+            sts16(tile + tile_chunk(row, 4 * cl + (flip ? j ^ 2 : j)),
+                  make_uint4(hmul2_u32(f[0], sc), hmul2_u32(f[1], sc), hmul2_u32(f[2], sc), hmul2_u32(f[3], sc)));
           }
         }
     };
+    look_up();
     locate();
-    load(rk, 0, L::kKeyScales);
-    load(rv, L::kValueCodes, L::kValueScales);
-    const int n = C1 - C0;
-    for (int j = 0; j < n; ++j) {
-      const int s = j & 1, phase = (j >> 1) & 1;
-      if (!wait(&sm->k_empty[s], phase ^ 1)) break;
-      if (lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = (lane == 0 ? hole[0] : hole[kWarpBlocks - 1]) ? 0xff : 0;
-      store(smem_u32(&sm->k[s][0]), rk);
+    load(0);
+    cur = nxt;
+    load(1);
+    uint32_t holes_now = holes;
+    bool go = have;
+    look_up();
+    // keys and values of a tile in turn: convert one, start the loads of the same of the next tile
+    for (int u = 0; go; ++u) {
+      const int which = u & 1, j = u >> 1, s = j & 1;
+      if (!wait(&sm->kv_empty[which][s], (j >> 1) ^ 1)) break;
+      if (which == 0 && lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = holes_now >> lane & 1 ? 0xff : 0;
+      store(smem_u32(&sm->kv[which][s][0]));
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->k_full[s]);
-      locate();
-      load(rk, 0, L::kKeyScales);
-      if (!wait(&sm->v_empty[s], phase ^ 1)) break;
-      store(smem_u32(&sm->v[s][0]), rv);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->v_full[s]);
-      load(rv, L::kValueCodes, L::kValueScales);
+      if (lane == 0) mbar_arrive(&sm->kv_full[which][s]);
+      cur = nxt;
+      if (which == 0) {
+        locate();
+        load(0);
+        look_up();
+      } else {
+        load(1);
+        holes_now = holes;
+        go = have;
+      }
     }
   } else {
     // ------------------------------------------------------------------ MMA
@@ -572,59 +737,67 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
     const uint32_t id_o = idesc_f16(128, D, 0) | (1u << 16);   // values: N (d) contiguous
     constexpr int kHalf = 128 * 128;
     const uint64_t qd = smem_desc(smem_u32(&sm->q[0][0]), 16, 1024, kSwizzle128B);
-    const uint64_t kd = smem_desc(smem_u32(&sm->k[0][0]), 16, 1024, kSwizzle128B);
+    const uint64_t kd = smem_desc(smem_u32(&sm->kv[0][0][0]), 16, 1024, kSwizzle128B);
     // MN-major: leading offset between 64-column halves, stride between 8-token groups
-    const uint64_t vd = smem_desc(smem_u32(&sm->v[0][0]), kHalf, 1024, kSwizzle128B);
-    auto issue_s = [&](int i, int s) {
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-        mma_f16(tmem + 128 * i, qd + (uint64_t)((i * Sm::kTile) >> 4) + off,
-                kd + (uint64_t)((s * Sm::kTile) >> 4) + off, id_s, kk != 0);
-      }
-      tc_commit(&sm->s_full[i]);
-    };
-    auto issue_o = [&](int i, int s, bool first) {
-#pragma unroll
-      for (int kk = 0; kk < kTok / 16; ++kk)
-        mma_f16_tmem_a(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk,
-                       vd + (uint64_t)((s * Sm::kTile + kk * 2048) >> 4), id_o, !(first && kk == 0));
-    };
-    int j = 0, items0 = 0, items1 = 0, p0 = 0, p1 = 0;
+    const uint64_t vd = smem_desc(smem_u32(&sm->kv[1][0][0]), kHalf, 1024, kSwizzle128B);
+    int j0 = 0, n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0, pieces = 0;
     bool ok = true;
-    for (; pc.more() && ok; pc.next()) {
-      const int nt = pc.t1 - pc.t0, mine = pc.rows() > 128 ? 2 : 1;
-      ok = wait(&sm->q_full[0], items0++);
-      if (ok && mine == 2) ok = wait(&sm->q_full[1], items1++);
-      if (!ok || !(ok = wait(&sm->k_full[j & 1], j >> 1))) break;
-      tc_fence_after();
-      if (lane == 0) {
-        for (int i = 0; i < mine; ++i) issue_s(i, j & 1);
-        tc_commit(&sm->k_empty[j & 1]);
-      }
-      __syncwarp();
-      for (int t = 0; t < nt && ok; ++t, ++j) {
-        const int s = j & 1;
-        const bool next = t + 1 < nt;
-        if (!(ok = wait(&sm->v_full[s], j >> 1))) break;
-        for (int i = 0; i < mine; ++i) {
-          if (!(ok = wait(&sm->p_full[i], i == 0 ? p0++ : p1++))) break;
-          if (next && i == 0 && !(ok = wait(&sm->k_full[s ^ 1], (j + 1) >> 1))) break;
-          tc_fence_after();
-          if (lane == 0) {
-            issue_o(i, s, t == 0);
-            if (next) issue_s(i, s ^ 1);
-            else tc_commit(&sm->o_full[i]);
+    for (; w->more && ok; next()) {
+      const int nt = w->t1 - w->t0, rows = min(kRowTile, w->n * group - w->q * kRowTile);
+      record(pieces++ > 0);
+      // Two streams of (S, softmax, O): the row tiles, or a split tile's even
+      // and odd KV tiles. A visit multiplies P by V for one KV tile of one
+      // stream and starts the stream's next S.
+      const bool split = rows <= kSplitRows;
+      const int ns = split ? min(nt, 2) : rows > 128 ? 2 : 1, ahead = split ? 2 : 1;
+      if (!(ok = wait(&sm->q_full[0], n_q0++))) break;
+      if (!split && ns == 2 && !(ok = wait(&sm->q_full[1], n_q1++))) break;
+      for (int t = -ahead; t < nt && ok; ++t) {
+        for (int i = split ? t & 1 : 0; i < (split ? (t & 1) + 1 : ns) && ok; ++i) {
+          const bool opens = split || i == 0, closes = split || i == ns - 1;
+          if (t >= 0) {
+            const int j = j0 + t, s = j & 1;
+            if (opens && !(ok = wait(&sm->kv_full[1][s], j >> 1))) break;
+            for (int half = 0; half < 2 && ok; ++half) {   // half by half as P arrives
+              if (!(ok = wait(&sm->p_full[i][half], i ? n_p1 : n_p0))) break;
+              tc_fence_after();
+              if (lane == 0) {
+                uint64_t d = vd + (uint64_t)((s * Sm::kTile + half * 4 * 2048) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                  mma_f16_tmem_a(tmem + 256 + 128 * i, tmem + 128 * i + 32 * half + 8 * kk, d + kk * (2048 >> 4), id_o,
+                                 t >= ahead || half + kk > 0);
+                if (half == 0) tc_commit(&sm->h_done[i]);
+                else if (closes) tc_commit(&sm->kv_empty[1][s]);
+              }
+              __syncwarp();
+            }
+            if (!ok) break;
+            if (i) ++n_p1;
+            else ++n_p0;
+          }
+          if (t + ahead < nt) {
+            const int j = j0 + t + ahead, s = j & 1;
+            if (opens && !(ok = wait(&sm->kv_full[0][s], j >> 1))) break;
+            tc_fence_after();
+            if (lane == 0) {
+              const uint64_t qa = qd + (uint64_t)((split ? 0 : i * Sm::kTile) >> 4);
+              const uint64_t kb = kd + (uint64_t)((s * Sm::kTile) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                mma_f16(tmem + 128 * i, qa + off, kb + off, id_s, kk != 0);
+              }
+              tc_commit(&sm->s_full[i]);
+              if (closes) tc_commit(&sm->kv_empty[0][s]);
+            }
+          } else if (t >= 0 && lane == 0) {   // (a split piece of one tile has no second stream)
+            tc_commit(&sm->o_full[i]);
           }
           __syncwarp();
         }
-        if (!ok) break;
-        if (lane == 0) {
-          tc_commit(&sm->v_empty[s]);
-          if (next) tc_commit(&sm->k_empty[s ^ 1]);
-        }
-        __syncwarp();
       }
+      j0 += nt;
     }
     if (lane == 0) {
       tc_commit(&sm->drain);
@@ -638,59 +811,79 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(PromptArgs p) {
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-  if (tid == 0 && sm->abort) set_status(p.status, MOE_ERR_TIMEOUT);
+  if (sm->abort) {   // a walk stopped short: the range's ends, so that the counters below stay right
+    if (tid == 0) set_status(p.status, MOE_ERR_TIMEOUT);
+    if (warp == 0) {
+      int pieces = 0;
+      for (walk_begin(rg, w); w->more; next()) record(pieces++ > 0);
+    }
+    __syncthreads();
+  }
 
   // ----------------------------- row tiles that several CTAs cut: the last joins
-  Pieces first(a, sm->pre, p.b0, p.nb, group, C0, C1), end(a, sm->pre, p.b0, p.nb, group, C1 - 1, C1);
-  const int s0 = C0 - first.t0, s1 = s0 + first.tiles;            // tiles of the first row tile
-  const int e0 = C1 - 1 - end.t0, e1 = e0 + end.tiles;            // and of the last
-  const bool cut0 = s0 < C0, cut1 = e1 > C1 && e0 >= C0;
+  const bool cut0 = sm->ends[0].tiles > 0 && (sm->ends[0].t0 > 0 || sm->ends[0].t1 < sm->ends[0].tiles);
+  const bool cut1 = sm->ends[1].tiles > 0 && sm->ends[1].t1 < sm->ends[1].tiles;
   if (!cut0 && !cut1) return;
-  auto cta_of = [&](int tile) { return (int)(((long long)(tile + 1) * G - 1) / total); };
-  __threadfence();
-  __syncthreads();
   if (tid < 2) {
-    const bool cut = tid == 0 ? cut0 : cut1;
-    const int lo = cta_of(tid == 0 ? s0 : e0), hi = cta_of((tid == 0 ? s1 : e1) - 1);
     int is_last = 0;
-    if (cut && atomicAdd(p.counters + lo, 1) == hi - lo) {
-      p.counters[lo] = 0;   // everyone has arrived: ready for the next launch
-      is_last = 1;
+    if (tid == 0 ? cut0 : cut1) {
+      const Ends& e = sm->ends[tid];
+      __threadfence();   // cumulative: the CTA's partials, ordered before by the barrier
+      if (atomicAdd(p.counters + e.lo, 1) == e.hi - e.lo) {
+        p.counters[e.lo] = 0;   // everyone has arrived: ready for the next launch
+        is_last = 1;
+      }
+      __threadfence();
     }
     sm->last[tid] = is_last;
   }
   __syncthreads();
   for (int side = 0; side < 2; ++side) {
     if (!sm->last[side]) continue;
-    __threadfence();
-    const Pieces& pp = side == 0 ? first : end;
-    const int lo = cta_of(side == 0 ? s0 : e0), n = cta_of((side == 0 ? s1 : e1) - 1) - lo + 1;
-    for (int e = tid; e < pp.rows() * (D / 4); e += kThreads) {
-      const int row = e / (D / 4), d = e % (D / 4) * 4;
-      float m = -INFINITY;
-      for (int x = 0; x < n; ++x) m = fmaxf(m, __ldcg(slot(lo + x, x == 0 ? 1 : 0) + kRowTile * D + 2 * row));
-      const float mu = m == -INFINITY ? 0.0f : m;
-      float l = 0.0f;
+    const Ends e = sm->ends[side];
+    const int n = e.hi - e.lo + 1;
+    for (int x = tid; x < e.rows * (D / 4); x += kThreads) {
+      const int row = x / (D / 4), d = x % (D / 4) * 4;
+      float m = -INFINITY, l = 0.0f;
       float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
-      for (int x = 0; x < n; ++x) {
-        const float* src = slot(lo + x, x == 0 ? 1 : 0);
-        const float2 ml = __ldcg(reinterpret_cast<const float2*>(src + kRowTile * D + 2 * row));
-        const float4 v = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
-        const float w = ex2(ml.x - mu);
-        l += w * ml.y;
-        o.x += w * v.x;
-        o.y += w * v.y;
-        o.z += w * v.z;
-        o.w += w * v.w;
+#pragma unroll 1
+      for (int c = 0; c < n; c += 4) {
+        float2 ml[4];
+        float4 v[4];
+        float mn = m;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.0f);
+          v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (c + k < n) {   // the row tile's first CTA holds it at its end, the others at their start
+            const float* src = slot(e.lo + c + k, c + k == 0 ? 1 : 0);
+            ml[k] = __ldcg(reinterpret_cast<const float2*>(src + kRowTile * D + 2 * row));
+            v[k] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) mn = fmaxf(mn, ml[k].x);
+        const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m - mu);   // 0 from -inf
+        m = mn;
+        l *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float g = ex2(ml[k].x - mu);
+          l += g * ml[k].y;
+          o.x += g * v[k].x;
+          o.y += g * v[k].y;
+          o.z += g * v[k].z;
+          o.w += g * v[k].w;
+        }
       }
-      const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
-      const int rr = pp.q * kRowTile + row;
-      const size_t at = (size_t)(pp.rq.row0 + rr / group) * a.q_heads + pp.h * group + rr % group;
+      const float inv = 1.0f / (l * a.cache.v_gs);
+      const int rr = e.q * kRowTile + row, token = rr / group;
+      const size_t at = (size_t)(e.row0 + token) * a.q_heads + e.h * group + rr - token * group;
       *reinterpret_cast<uint2*>(a.out + at * D + d) =
           l > 0.0f ? make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv))
                    : make_uint2(0u, 0u);
-      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? mu * kLn2 + logf(l) : -INFINITY;
+      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
     }
   }
 }

@@ -222,8 +222,15 @@ class Scene:
 
     def run(self, q=None, **kw):
         kw = {"max_q": self.max_q, **kw}
-        return self.cache.attention(self.q.cuda() if q is None else q, _cuda(self.cu), _cuda([kv for kv, _ in self.lens]),
-                                    _cuda(self.table), **kw)
+        own = "ws" not in kw
+        if own:
+            kw["ws"] = self.cache.attention_workspace(self.total, len(self.lens), self.qheads, kw["max_q"], self.W)
+        got = self.cache.attention(self.q.cuda() if q is None else q, _cuda(self.cu),
+                                   _cuda([kv for kv, _ in self.lens]), _cuda(self.table), **kw)
+        if own:   # no wait gave up, no bad data, and the workspace is as it has to be for the next call
+            assert B().moe_get_device_status(kw["ws"]) == 0
+            assert not kw["ws"][:B().MOE_KV4_WS_ZERO].any()
+        return got
 
     def check(self, out, lse=None, scale=None, causal=True, window=0, rows=None):
         scale = self.D ** -0.5 if scale is None else scale
@@ -278,6 +285,18 @@ def test_prompts(qheads, heads, D, P, lens, window):
     s = Scene(lens, qheads, heads, D, P, seed=len(lens) + D)
     out, lse = s.run(want_lse=True, window=window)
     s.check(out, lse, window=window, rows=40)
+
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+@pytest.mark.parametrize("window", [0, 200])
+def test_row_tiles_of_every_kind_in_turn(D, P, window):
+    """Few-row and many-row requests of one or a few tiles in one call, so that a CTA's range has pieces of all
+    kinds one after another, single-tile ones among them."""
+    lens = [((17 * b) % 390 + n, n) for b in range(36) for n in ((3, 5, 9, 20, 40, 70)[b % 6],)]
+    s = Scene(lens, 8, 2, D, P, seed=D + window)
+    for _ in range(3):
+        out, lse = s.run(want_lse=True, window=window)
+    s.check(out, lse, window=window, rows=3)
 
 
 @pytest.mark.parametrize("D", [64, 128])
