@@ -12,8 +12,8 @@
 //   by plain loads a tile ahead (the packed cache is small and read by
 //   several row tiles: it comes from L2), converted into 128-byte-swizzled
 //   shared-memory tiles, keys K-major, values with d contiguous (MN-major);
-// * one thread issues S_i = Q_i K^T and O_i += P_i V for the two row tiles i in
-//   turn, so one tile's softmax runs under the other's MMAs; P_i (f16, read
+// * two threads issue S_i = Q_i K^T and O_i += P_i V, each for one of the two row
+//   tiles i, so one tile's softmax runs under the other's MMAs; P_i (f16, read
 //   from tensor memory) lies in S_i's columns;
 // * eight softmax warps, one row per thread: one pass over S in 32-column
 //   pieces with the running maximum of the tiles before; a piece that exceeds
@@ -42,8 +42,8 @@ constexpr int kChunk = 1024;           // requests of one launch
 constexpr int kSoftWarps = 8, kDeqWarps = 4;
 constexpr int kWarpBlocks = kTok / kKvBlock / kDeqWarps;
 static_assert(kWarpBlocks == 2, "blocks of a dequant warp");
-constexpr int kMmaWarp = kSoftWarps + kDeqWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kMmaWarp = kSoftWarps + kDeqWarps;   // and the one after it
+constexpr int kThreads = (kMmaWarp + 2) * 32;
 constexpr int kSetup = 2;              // what starting and ending a row tile costs, in KV tiles
 constexpr int kSplitRows = 64;         // row tiles of up to this many rows are split over their KV tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -211,8 +211,8 @@ struct Smem {
   alignas(1024) uint8_t q[2][kTile];
   alignas(1024) uint8_t kv[2][2][kTile];   // keys, values: two stages each
   uint64_t q_full[2], s_full[2], o_full[2];
-  uint64_t p_full[2][2];               // the halves of P
-  uint64_t h_done[2];                  // the first half's product is in O
+  uint64_t p_full[2];
+  uint64_t turn[2];                    // stream i may issue
   uint64_t kv_full[2][2], kv_empty[2][2];   // [keys or values][stage]
   uint64_t x_full, x_empty;            // the second warpgroup's half of a split row tile
   uint64_t drain;
@@ -310,18 +310,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->q_full[i], 4);
       mbar_init(&sm->s_full[i], 1);
-      mbar_init(&sm->p_full[i][0], 4);
-      mbar_init(&sm->p_full[i][1], 4);
-      mbar_init(&sm->h_done[i], 1);
+      mbar_init(&sm->p_full[i], 4);
+      mbar_init(&sm->turn[i], 1);
       mbar_init(&sm->o_full[i], 1);
       mbar_init(&sm->kv_full[0][i], kDeqWarps);
       mbar_init(&sm->kv_full[1][i], kDeqWarps);
-      mbar_init(&sm->kv_empty[0][i], 1);
-      mbar_init(&sm->kv_empty[1][i], 1);
+      mbar_init(&sm->kv_empty[0][i], 2);
+      mbar_init(&sm->kv_empty[1][i], 2);
     }
     mbar_init(&sm->x_full, 4);
     mbar_init(&sm->x_empty, 4);
-    mbar_init(&sm->drain, 1);
+    mbar_init(&sm->drain, 2);
     sm->ends[0].tiles = sm->ends[1].tiles = 0;
     fence_barrier_init();
   }
@@ -481,12 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
             m = mn;
             const float2 l = unpack2(l2);
             l2 = pack2(l.x * f, l.y * f);
-            // From piece 2 on the first half of P is with the tensor core:
-            // O waits for it, and it needs no factor of its own.
-            const bool handed = piece >= 2;
-            if (handed && !wait(&sm->h_done[i], js)) return false;
-            if (handed) tc_fence_after();
-            if (t > begin || handed) {
+            if (t > begin) {
 #pragma unroll 1
               for (int cc = 0; cc < D; cc += 16) {
                 uint32_t o[16];
@@ -499,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
             }
             const uint32_t f2 = pack_f16x2(f, f);   // pieces of P already stored: one more f16 rounding
 #pragma unroll 1
-            for (int pp = handed ? 2 : 0; pp < piece; ++pp) {
+            for (int pp = 0; pp < piece; ++pp) {
               uint32_t o[16];
               tmem_ld16(s_t + 16 * pp, o);
               tmem_ld_wait();
@@ -522,27 +516,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           }
           l2 = add2(l2, sum);
           tmem_st16(s_t + 16 * piece, pk);
-          return true;
         };
-        // P's halves are handed over as they are done. A half lies in columns
-        // of S that have been read: pieces 0, 1 write [0, 32), 2, 3 [32, 64).
-        uint32_t s0[32], s1[32];
-        if (active) tmem_ld32(s_t, s0);
+        // piece x of P goes to columns [16 x, 16 x + 16) of S, read by then
+        if (active) {
+          uint32_t s0[32], s1[32];
+          tmem_ld32(s_t, s0);
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half) {
-          if (active) {
+          for (int half = 0; half < 2; ++half) {
             ld_wait(s0);
             tmem_ld32(s_t + 64 * half + 32, s1);
-            ok = work(s0, 2 * half) && ok;
+            work(s0, 2 * half);
             ld_wait(s1);
             if (half == 0) tmem_ld32(s_t + 64, s0);
-            ok = work(s1, 2 * half + 1) && ok;
-            tmem_st_wait();
-            tc_fence_before();
+            work(s1, 2 * half + 1);
           }
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->p_full[i][half]);
+          tmem_st_wait();
+          tc_fence_before();
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->p_full[i]);
       }
       if (!ok) break;
       const bool any = begin < nt;                 // the second half of a split tile may be empty
@@ -623,7 +615,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     struct Raw {
       uint4 codes[kWarpBlocks][kLoads];
       uint32_t sf[kWarpBlocks][kLoads];            // two scale bytes each
-    } cur, nxt;
+    } rk, rv;
     // The walk runs two tiles ahead: a tile's page ids are read one tile before
     // its data, and its data one tile before it is converted.
     int n_page[kWarpBlocks], n_left[kWarpBlocks], n_at[kWarpBlocks], n_h = 0, lt = w->t0;
@@ -667,30 +659,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
                  kv4_block_offset(left[x] > 0 ? n_page[x] : 0, n_h, Hk, P / kKvBlock, n_at[x], L::kBytes);
       }
     };
-    auto load = [&](int which) {                   // keys (0) or values (1) of the located tile
-      const int at = which ? L::kValueCodes : 0;
+    auto load = [&](Raw& r, int at) {              // keys or values of the located tile
       const int sat = at + L::kKeyScales - (tl * L::kCodeRow + 16 * cl) + tl * L::kScaleRow + 2 * cl;
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x)
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
-          nxt.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what was not appended enters as zeros
-          nxt.sf[x][y] = 0u;
+          r.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what was not appended enters as zeros
+          r.sf[x][y] = 0u;
           if (y * kRowsPerLoad + tl < left[x]) {
-            nxt.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(src[x] + at + y * kRowsPerLoad * L::kCodeRow));
-            nxt.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(src[x] + sat + y * kRowsPerLoad * L::kScaleRow));
+            r.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(src[x] + at + y * kRowsPerLoad * L::kCodeRow));
+            r.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(src[x] + sat + y * kRowsPerLoad * L::kScaleRow));
           }
         }
     };
-    auto store = [&](uint32_t tile) {
+    auto store = [&](uint32_t tile, const Raw& r) {
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x)
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
           const int row = (blk0 + x) * kKvBlock + y * kRowsPerLoad + tl;
-          const uint32_t two = cvt_e4m3x2_f16x2(cur.sf[x][y]);
+          const uint32_t two = cvt_e4m3x2_f16x2(r.sf[x][y]);
           const uint32_t sc0 = __byte_perm(two, 0, 0x1010), sc1 = __byte_perm(two, 0, 0x3232);
-          const uint32_t wd[4] = {cur.codes[x][y].x, cur.codes[x][y].y, cur.codes[x][y].z, cur.codes[x][y].w};
+          const uint32_t wd[4] = {r.codes[x][y].x, r.codes[x][y].y, r.codes[x][y].z, r.codes[x][y].w};
           // the two 64-column halves share banks: their lanes store in different orders
           const bool flip = D == 128 && cl >= 2;
 #pragma unroll
@@ -705,31 +696,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     };
     look_up();
     locate();
-    load(0);
-    cur = nxt;
-    load(1);
-    uint32_t holes_now = holes;
-    bool go = have;
+    load(rk, 0);
+    load(rv, L::kValueCodes);
     look_up();
-    // keys and values of a tile in turn: convert one, start the loads of the same of the next tile
-    for (int u = 0; go; ++u) {
-      const int which = u & 1, j = u >> 1, s = j & 1;
-      if (!wait(&sm->kv_empty[which][s], (j >> 1) ^ 1)) break;
-      if (which == 0 && lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = holes_now >> lane & 1 ? 0xff : 0;
-      store(smem_u32(&sm->kv[which][s][0]));
+    for (int j = 0; have; ++j) {
+      const int s = j & 1, phase = (j >> 1) ^ 1;
+      if (!wait(&sm->kv_empty[0][s], phase)) break;
+      if (lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = holes >> lane & 1 ? 0xff : 0;
+      store(smem_u32(&sm->kv[0][s][0]), rk);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->kv_full[which][s]);
-      cur = nxt;
-      if (which == 0) {
-        locate();
-        load(0);
-        look_up();
-      } else {
-        load(1);
-        holes_now = holes;
-        go = have;
-      }
+      if (lane == 0) mbar_arrive(&sm->kv_full[0][s]);
+      locate();
+      load(rk, 0);
+      look_up();
+      if (!wait(&sm->kv_empty[1][s], phase)) break;
+      store(smem_u32(&sm->kv[1][s][0]), rv);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->kv_full[1][s]);
+      load(rv, L::kValueCodes);
     }
   } else {
     // ------------------------------------------------------------------ MMA
@@ -740,62 +726,65 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     const uint64_t kd = smem_desc(smem_u32(&sm->kv[0][0][0]), 16, 1024, kSwizzle128B);
     // MN-major: leading offset between 64-column halves, stride between 8-token groups
     const uint64_t vd = smem_desc(smem_u32(&sm->kv[1][0][0]), kHalf, 1024, kSwizzle128B);
-    int j0 = 0, n_q0 = 0, n_q1 = 0, n_p0 = 0, n_p1 = 0, pieces = 0;
+    // Two streams of (S, softmax, O), a warp each: the item's row tiles, or a
+    // split tile's even and odd KV tiles. Both walk every KV tile and give its
+    // shared memory back, used or not. With two row tiles the warps take turns
+    // with their batches (P V of a KV tile, then the next S): a stream's MMAs
+    // run while the other's softmax does (interleaved freely they fall into
+    // step, and the tensor core idles through both softmaxes at once), and a
+    // warp's waits hide behind the other's batch.
+    const int i = warp - kMmaWarp;
+    int j0 = 0, items = 0, n_q1 = 0, n_p = 0, n_turn = 0;
     bool ok = true;
-    for (; w->more && ok; next()) {
+    for (; w->more && ok; next(), ++items) {
       const int nt = w->t1 - w->t0, rows = min(kRowTile, w->n * group - w->q * kRowTile);
-      record(pieces++ > 0);
-      // Two streams of (S, softmax, O): the row tiles, or a split tile's even
-      // and odd KV tiles. A visit multiplies P by V for one KV tile of one
-      // stream and starts the stream's next S.
-      const bool split = rows <= kSplitRows;
-      const int ns = split ? min(nt, 2) : rows > 128 ? 2 : 1, ahead = split ? 2 : 1;
-      if (!(ok = wait(&sm->q_full[0], n_q0++))) break;
-      if (!split && ns == 2 && !(ok = wait(&sm->q_full[1], n_q1++))) break;
-      for (int t = -ahead; t < nt && ok; ++t) {
-        for (int i = split ? t & 1 : 0; i < (split ? (t & 1) + 1 : ns) && ok; ++i) {
-          const bool opens = split || i == 0, closes = split || i == ns - 1;
+      if (i == 0) record(items > 0);
+      const bool split = rows <= kSplitRows, two = rows > 128, idle = i == 1 && !split && !two;
+      const int ahead = split ? 2 : 1;
+      if (!(ok = wait(&sm->q_full[0], items))) break;
+      if (i == 1 && two && !(ok = wait(&sm->q_full[1], n_q1++))) break;
+      const uint64_t qa = qd + (uint64_t)((split ? 0 : i * Sm::kTile) >> 4);
+      for (int t = -ahead; t < nt; ++t) {
+        const bool mine = split ? (t & 1) == i : !idle, more = t + ahead < nt;
+        const int jv = j0 + t, sv = jv & 1, jk = jv + ahead, sk = jk & 1;
+        if (t >= 0 && !(ok = wait(&sm->kv_full[1][sv], jv >> 1))) break;
+        if (more && !(ok = wait(&sm->kv_full[0][sk], jk >> 1))) break;
+        if (t >= 0 && mine && !(ok = wait(&sm->p_full[i], n_p++))) break;
+        // stream 0 starts, so its first turn needs no hand-over
+        if (two && !(ok = wait(&sm->turn[i], i ? n_turn : n_turn - 1))) break;
+        n_turn += two;
+        tc_fence_after();
+        if (lane == 0) {
           if (t >= 0) {
-            const int j = j0 + t, s = j & 1;
-            if (opens && !(ok = wait(&sm->kv_full[1][s], j >> 1))) break;
-            for (int half = 0; half < 2 && ok; ++half) {   // half by half as P arrives
-              if (!(ok = wait(&sm->p_full[i][half], i ? n_p1 : n_p0))) break;
-              tc_fence_after();
-              if (lane == 0) {
-                uint64_t d = vd + (uint64_t)((s * Sm::kTile + half * 4 * 2048) >> 4);
+            if (mine) {
+              const uint64_t vb = vd + (uint64_t)((sv * Sm::kTile) >> 4);
 #pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                  mma_f16_tmem_a(tmem + 256 + 128 * i, tmem + 128 * i + 32 * half + 8 * kk, d + kk * (2048 >> 4), id_o,
-                                 t >= ahead || half + kk > 0);
-                if (half == 0) tc_commit(&sm->h_done[i]);
-                else if (closes) tc_commit(&sm->kv_empty[1][s]);
-              }
-              __syncwarp();
+              for (int kk = 0; kk < kTok / 16; ++kk)
+                mma_f16_tmem_a(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk, vb + kk * (2048 >> 4), id_o,
+                               t >= ahead || kk > 0);
+              tc_commit(&sm->kv_empty[1][sv]);
+              if (!more) tc_commit(&sm->o_full[i]);
+            } else {
+              mbar_arrive(&sm->kv_empty[1][sv]);
             }
-            if (!ok) break;
-            if (i) ++n_p1;
-            else ++n_p0;
           }
-          if (t + ahead < nt) {
-            const int j = j0 + t + ahead, s = j & 1;
-            if (opens && !(ok = wait(&sm->kv_full[0][s], j >> 1))) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint64_t qa = qd + (uint64_t)((split ? 0 : i * Sm::kTile) >> 4);
-              const uint64_t kb = kd + (uint64_t)((s * Sm::kTile) >> 4);
+          if (more) {
+            if (mine) {
+              const uint64_t kb = kd + (uint64_t)((sk * Sm::kTile) >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
                 const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
                 mma_f16(tmem + 128 * i, qa + off, kb + off, id_s, kk != 0);
               }
               tc_commit(&sm->s_full[i]);
-              if (closes) tc_commit(&sm->kv_empty[0][s]);
+              tc_commit(&sm->kv_empty[0][sk]);
+            } else {
+              mbar_arrive(&sm->kv_empty[0][sk]);
             }
-          } else if (t >= 0 && lane == 0) {   // (a split piece of one tile has no second stream)
-            tc_commit(&sm->o_full[i]);
           }
-          __syncwarp();
+          if (two) mbar_arrive(&sm->turn[i ^ 1]);
         }
+        __syncwarp();
       }
       j0 += nt;
     }
