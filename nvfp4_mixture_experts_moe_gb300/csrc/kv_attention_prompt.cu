@@ -210,7 +210,8 @@ struct Smem {
   static constexpr int kTile = kHalves * 128 * 128;   // 128 rows x D f16
   alignas(1024) uint8_t q[2][kTile];
   alignas(1024) uint8_t kv[2][2][kTile];   // keys, values: two stages each
-  uint64_t q_full[2], s_full[2], o_full[2];
+  uint64_t q_full[2], q_split;         // rows of the streams' row tiles, of a split one
+  uint64_t s_full[2], o_full[2];
   uint64_t p_full[2];
   uint64_t turn[2];                    // stream i may issue
   uint64_t kv_full[2][2], kv_empty[2][2];   // [keys or values][stage]
@@ -318,6 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       mbar_init(&sm->kv_empty[0][i], 2);
       mbar_init(&sm->kv_empty[1][i], 2);
     }
+    mbar_init(&sm->q_split, 4);
     mbar_init(&sm->x_full, 4);
     mbar_init(&sm->x_empty, 4);
     mbar_init(&sm->drain, 2);
@@ -392,25 +394,38 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     const uint32_t s_t = tmem + lanes + 128 * i, o_t = tmem + lanes + 256 + 128 * i;
     int js = 0, jo = 0, jx = 0;                    // S tiles, items, split items this warpgroup has seen
     int jt = 0;                                    // tiles of the CTA before the next piece
-    for (; w->more; next()) {
-      const int q0 = w->q * kRowTile, rows = min(kRowTile, w->n * group - q0);
-      const int t0 = w->t0, nt = w->t1 - t0, kv = w->kv, row0 = w->row0, h = w->h;
-      const int jt0 = jt;
-      jt += nt;
-      // A row tile of few rows: both warpgroups hold all its rows and take
-      // every other KV tile, joined at the end.
-      const bool split = rows <= kSplitRows;
-      if (!split && i * 128 >= rows) continue;
-      const int r = (split ? 0 : i * 128) + (warp & 3) * 32 + lane;   // row within the item
-      const bool real = r < rows, active = r - lane < rows;
-      const int rr = q0 + (real ? r : 0), token = rr / group, qh = h * group + rr - token * group;
-      const size_t at = (size_t)(row0 + token) * a.q_heads + qh;
-      // the row as f16, largest element in [2^14, 2^15) (smaller only below 2^-112)
-      float c;
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(row0 + token) * a.q_stride + qh * D);
-        const uint32_t dst = smem_u32(&sm->q[split ? 0 : i][0]);
-        const bool keep = !split || i == 0;
+    struct Item {
+      // A row tile of few rows is split: both warpgroups hold all its rows and
+      // take every other KV tile, joined at the end.
+      bool split, real, active, whole;             // real: this thread's row exists, active: one of the warp's does
+      int r, t0, nt, jt0, tok0, hi_tok, lo_tok;    // row within the tile; its KV tiles here; first token; what it sees
+      size_t at;                                   // (token, head) of the row
+      float c;                                     // from S to scores in powers of two
+    };
+    // The warpgroup's next row tile: its rows as f16 into shared memory, the
+    // largest element in [2^14, 2^15) (smaller only below 2^-112).
+    auto enter = [&](Item& it) {
+      for (; w->more; next()) {
+        const int q0 = w->q * kRowTile, rows = min(kRowTile, w->n * group - q0), h = w->h, kv = w->kv;
+        it.split = rows <= kSplitRows;
+        it.jt0 = jt;
+        it.t0 = w->t0;
+        it.nt = w->t1 - w->t0;
+        jt += it.nt;
+        if (!it.split && i * 128 >= rows) continue;
+        it.whole = it.nt == w->tiles;
+        it.r = (it.split ? 0 : i * 128) + (warp & 3) * 32 + lane;
+        it.real = it.r < rows;
+        it.active = it.r - lane < rows;
+        const int rr = q0 + (it.real ? it.r : 0), token = rr / group, qh = h * group + rr - token * group;
+        it.at = (size_t)(w->row0 + token) * a.q_heads + qh;
+        it.hi_tok = a.causal ? kv - w->n + token : kv - 1;
+        it.lo_tok = a.window > 0 ? it.hi_tok - a.window + 1 : 0;
+        it.tok0 = w->first + it.t0 * kTok;
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(w->row0 + token) * a.q_stride + qh * D);
+        const int qi = it.split ? 0 : i;
+        const uint32_t dst = smem_u32(&sm->q[qi][0]);
+        const bool keep = !it.split || i == 0;
         uint4 raw[D / 8];
 #pragma unroll
         for (int v = 0; v < D / 8; ++v) raw[v] = __ldg(src + v);
@@ -419,16 +434,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         for (int v = 0; v < D / 8; ++v) {
           mx = max_u16x2(max_u16x2(mx, raw[v].x & 0x7fff7fffu), raw[v].y & 0x7fff7fffu);
           mx = max_u16x2(max_u16x2(mx, raw[v].z & 0x7fff7fffu), raw[v].w & 0x7fff7fffu);
-          if (keep) sts16(dst + tile_chunk(r & 127, v), raw[v]);   // converted in place below
+          if (keep) sts16(dst + tile_chunk(it.r & 127, v), raw[v]);   // converted in place below
         }
         const int ex = min(max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15), 254);
         // never 0, so that a hidden score stays -inf
-        c = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
+        it.c = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
         const float up = a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);   // larger scores stay larger products
         if (keep) {
 #pragma unroll 2
           for (int v = 0; v < D / 8; ++v) {
-            uint4* chunk = reinterpret_cast<uint4*>(&sm->q[split ? 0 : i][tile_chunk(r & 127, v)]);
+            uint4* chunk = reinterpret_cast<uint4*>(&sm->q[qi][tile_chunk(it.r & 127, v)]);
             uint4 x = *chunk;
             uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -438,22 +453,115 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           }
           fence_proxy_async_smem();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&sm->q_full[split ? 0 : i]);
+          if (lane == 0) mbar_arrive(it.split ? &sm->q_split : &sm->q_full[i]);
+        }
+        next();
+        return true;
+      }
+      return false;
+    };
+    Item it, done;
+    done.split = false;
+    bool pending = false, have = false, ok = true;
+    float m = 0.0f, l = 0.0f;
+    for (;;) {
+      // Write out the row tile that is done and enter the next one: the next
+      // one first, so that its first S runs under the writing, unless the rows
+      // of the one that is done are still in use (a split one's by the other
+      // stream).
+#pragma unroll 1
+      for (int pass = 0; pass < 2 && ok; ++pass) {
+        if ((pass == 0) != done.split) {
+          have = enter(it);
+          continue;
+        }
+        if (!pending) continue;
+        const int begin = done.split ? i : 0;
+        const bool any = begin < done.nt;            // the second half of a split tile may be empty
+        if (any && !(ok = wait(&sm->o_full[i], jo++))) break;
+        tc_fence_after();
+        float* xo = reinterpret_cast<float*>(&sm->q[1][0]);   // a split tile's second half goes through here
+        float own = 1.0f, other = 0.0f;              // factors of this half and of the other
+        if (done.split && i == 0) {
+          if (!(ok = wait(&sm->x_full, jx++))) break;
+          if (done.active) {
+            const float2 x = sm->x_ml[done.r];
+            const float mn = fmaxf(m, x.x), mu = mn == -INFINITY ? 0.0f : mn;
+            own = ex2(m - mu);
+            other = ex2(x.x - mu);
+            l = l * own + x.y * other;
+            m = mn;
+          }
+        }
+        if (done.active) {
+          const bool give = done.split && i == 1, final = !give && done.whole;
+          if (final) {
+            const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+            own *= inv;
+            other *= inv;
+          }
+          const bool blank = give ? !any : final && !(l > 0.0f);   // O holds nothing to read
+          const int which = done.t0 > 0 ? 0 : 1, swz = give ? done.r & (D / 4 - 1) : 0;
+          float* dst = give ? xo + done.r * D : slot(cta, which) + (size_t)done.r * D;
+#pragma unroll 1
+          for (int cc = 0; cc < D; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(o_t + cc, o);
+            ld_wait(o);
+            float f[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) f[e] = blank ? 0.0f : __uint_as_float(o[e]) * own;
+            if (done.split && i == 0) {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {   // 16-byte chunks swizzled by the row
+                const float4 x = *reinterpret_cast<const float4*>(
+                    xo + done.r * D + (((cc + e) / 4) ^ (done.r & (D / 4 - 1))) * 4);
+                f[e] += x.x * other;
+                f[e + 1] += x.y * other;
+                f[e + 2] += x.z * other;
+                f[e + 3] += x.w * other;
+              }
+            }
+            if (!give && !done.real) continue;
+            if (final) {
+              uint4* out = reinterpret_cast<uint4*>(a.out + done.at * D + cc);
+#pragma unroll
+              for (int e = 0; e < 32; e += 8)
+                out[e / 8] = make_uint4(float2_to_bf16x2_bits(f[e], f[e + 1]), float2_to_bf16x2_bits(f[e + 2], f[e + 3]),
+                                        float2_to_bf16x2_bits(f[e + 4], f[e + 5]),
+                                        float2_to_bf16x2_bits(f[e + 6], f[e + 7]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4)
+                *reinterpret_cast<float4*>(dst + (((cc + e) / 4) ^ swz) * 4) =
+                    make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            }
+          }
+          if (give) sm->x_ml[done.r] = make_float2(m, l);
+          else if (done.real && !final)
+            *reinterpret_cast<float2*>(slot(cta, which) + kRowTile * D + 2 * done.r) = make_float2(m, l);
+          else if (done.real && a.lse != nullptr) a.lse[done.at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+        }
+        tc_fence_before();
+        if (done.split) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(i == 1 ? &sm->x_full : &sm->x_empty);
+          if (i == 1 && !(ok = wait(&sm->x_empty, jx++))) break;
         }
       }
-      const int hi_tok = a.causal ? kv - w->n + token : kv - 1;
-      const int lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
-      const int tok_first = w->first + t0 * kTok;
-      float m = -INFINITY;
+      if (!ok || !have) break;
+      const int nt = it.nt, hi_tok = it.hi_tok, lo_tok = it.lo_tok;
+      const float c = it.c;
+      const bool active = it.active;
+      m = -INFINITY;
       uint64_t l2 = pack2(0.0f, 0.0f);
       const uint64_t c2 = pack2(c, c);
-      const int step = split ? 2 : 1, begin = split ? i : 0;
-      bool ok = true;
-      for (int t = begin; t < nt && ok; t += step, ++js) {
+      const int step = it.split ? 2 : 1, begin = it.split ? i : 0;
+      for (int t = begin; t < nt; t += step, ++js) {
         if (!(ok = wait(&sm->s_full[i], js))) break;
         tc_fence_after();
-        const int tok0 = tok_first + t * kTok;
-        const uint64_t hole = *reinterpret_cast<const volatile uint64_t*>(sm->hole[(jt0 + t) & 3]);
+        const int tok0 = it.tok0 + t * kTok;
+        const uint64_t hole = *reinterpret_cast<const volatile uint64_t*>(sm->hole[(it.jt0 + t) & 3]);
         const bool masked = __any_sync(kFull, tok0 + kTok - 1 > hi_tok || tok0 < lo_tok) || hole != 0;
         // one 32-column piece of S, read while the piece before is worked on
         auto work = [&](uint32_t (&sr)[32], int piece) {
@@ -537,72 +645,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         if (lane == 0) mbar_arrive(&sm->p_full[i]);
       }
       if (!ok) break;
-      const bool any = begin < nt;                 // the second half of a split tile may be empty
-      if (any && !wait(&sm->o_full[i], jo++)) break;
-      tc_fence_after();
-      float l = unpack2(l2).x + unpack2(l2).y;
-      float* xo = reinterpret_cast<float*>(&sm->q[1][0]);   // a split tile's second half goes through here
-      float own = 1.0f, other = 0.0f;              // factors of this half and of the other
-      if (split && i == 0) {
-        if (!wait(&sm->x_full, jx++)) break;
-        if (active) {
-          const float2 x = sm->x_ml[r];
-          const float mn = fmaxf(m, x.x), mu = mn == -INFINITY ? 0.0f : mn;
-          own = ex2(m - mu);
-          other = ex2(x.x - mu);
-          l = l * own + x.y * other;
-          m = mn;
-        }
-      }
-      if (active) {
-        const bool give = split && i == 1, whole = t0 == 0 && nt == w->tiles;
-        if (!give && whole) own *= l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
-        if (!give && whole) other *= l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
-        const bool blank = give ? !any : whole && !(l > 0.0f);   // O holds nothing to read
-        float* dst = give ? xo + r * D : slot(cta, t0 > 0 ? 0 : 1) + (size_t)r * D;
-#pragma unroll 1
-        for (int cc = 0; cc < D; cc += 16) {
-          uint32_t o[16];
-          tmem_ld16(o_t + cc, o);
-          tmem_ld_wait();
-          float f[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) f[e] = blank ? 0.0f : __uint_as_float(o[e]) * own;
-          if (split && i == 0) {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4) {   // 16-byte chunks swizzled by the row
-              const float4 x = *reinterpret_cast<const float4*>(xo + r * D + (((cc + e) / 4) ^ (r & (D / 4 - 1))) * 4);
-              f[e] += x.x * other;
-              f[e + 1] += x.y * other;
-              f[e + 2] += x.z * other;
-              f[e + 3] += x.w * other;
-            }
-          }
-          if (!give && !real) continue;
-          if (!give && whole) {
-            uint4* out = reinterpret_cast<uint4*>(a.out + at * D + cc);
-            out[0] = make_uint4(float2_to_bf16x2_bits(f[0], f[1]), float2_to_bf16x2_bits(f[2], f[3]),
-                                float2_to_bf16x2_bits(f[4], f[5]), float2_to_bf16x2_bits(f[6], f[7]));
-            out[1] = make_uint4(float2_to_bf16x2_bits(f[8], f[9]), float2_to_bf16x2_bits(f[10], f[11]),
-                                float2_to_bf16x2_bits(f[12], f[13]), float2_to_bf16x2_bits(f[14], f[15]));
-          } else {
-#pragma unroll
-            for (int e = 0; e < 16; e += 4)
-              *reinterpret_cast<float4*>(dst + (give ? (((cc + e) / 4) ^ (r & (D / 4 - 1))) * 4 : cc + e)) =
-                  make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
-          }
-        }
-        if (give) sm->x_ml[r] = make_float2(m, l);
-        else if (real && !whole)
-          *reinterpret_cast<float2*>(slot(cta, t0 > 0 ? 0 : 1) + kRowTile * D + 2 * r) = make_float2(m, l);
-        else if (real && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
-      }
-      tc_fence_before();
-      if (split) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(i == 1 ? &sm->x_full : &sm->x_empty);
-        if (i == 1 && !wait(&sm->x_empty, jx++)) break;
-      }
+      l = unpack2(l2).x + unpack2(l2).y;
+      done = it;
+      pending = true;
     }
   } else if (warp < kMmaWarp) {
     // ------------------------------------------------------------- dequant
@@ -734,15 +779,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     // step, and the tensor core idles through both softmaxes at once), and a
     // warp's waits hide behind the other's batch.
     const int i = warp - kMmaWarp;
-    int j0 = 0, items = 0, n_q1 = 0, n_p = 0, n_turn = 0;
-    bool ok = true;
-    for (; w->more && ok; next(), ++items) {
+    int j0 = 0, n_q = 0, n_qs = 0, n_p = 0, n_turn = 0;
+    bool ok = true, first = true;
+    while (w->more && ok) {
       const int nt = w->t1 - w->t0, rows = min(kRowTile, w->n * group - w->q * kRowTile);
-      if (i == 0) record(items > 0);
+      if (i == 0) record(!first);
+      first = false;
       const bool split = rows <= kSplitRows, two = rows > 128, idle = i == 1 && !split && !two;
       const int ahead = split ? 2 : 1;
-      if (!(ok = wait(&sm->q_full[0], items))) break;
-      if (i == 1 && two && !(ok = wait(&sm->q_full[1], n_q1++))) break;
+      if (split) ok = wait(&sm->q_split, n_qs++);
+      else if (!idle) ok = wait(&sm->q_full[i], n_q++);
+      if (!ok) break;
       const uint64_t qa = qd + (uint64_t)((split ? 0 : i * Sm::kTile) >> 4);
       for (int t = -ahead; t < nt; ++t) {
         const bool mine = split ? (t & 1) == i : !idle, more = t + ahead < nt;
@@ -785,6 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           if (two) mbar_arrive(&sm->turn[i ^ 1]);
         }
         __syncwarp();
+        if (t == -ahead) next();   // the next piece, while there is time
       }
       j0 += nt;
     }
@@ -831,48 +879,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     if (!sm->last[side]) continue;
     const Ends e = sm->ends[side];
     const int n = e.hi - e.lo + 1;
-    for (int x = tid; x < e.rows * (D / 4); x += kThreads) {
-      const int row = x / (D / 4), d = x % (D / 4) * 4;
-      float m = -INFINITY, l = 0.0f;
-      float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 1
-      for (int c = 0; c < n; c += 4) {
-        float2 ml[4];
-        float4 v[4];
-        float mn = m;
+    constexpr int kX = 4, kB = 2;   // elements and partials in flight per thread
+    for (int x0 = tid; x0 < e.rows * (D / 4); x0 += kX * kThreads) {
+      float m[kX], l[kX];
+      float4 o[kX];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.0f);
-          v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (c + k < n) {   // the row tile's first CTA holds it at its end, the others at their start
-            const float* src = slot(e.lo + c + k, c + k == 0 ? 1 : 0);
-            ml[k] = __ldcg(reinterpret_cast<const float2*>(src + kRowTile * D + 2 * row));
-            v[k] = __ldcg(reinterpret_cast<const float4*>(src + row * D + d));
+      for (int y = 0; y < kX; ++y) {
+        m[y] = -INFINITY;
+        l[y] = 0.0f;
+        o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      }
+#pragma unroll 1
+      for (int c = 0; c < n; c += kB) {
+        float2 ml[kX][kB];
+        float4 v[kX][kB];
+#pragma unroll
+        for (int y = 0; y < kX; ++y)
+#pragma unroll
+          for (int k = 0; k < kB; ++k) {
+            const int x = x0 + y * kThreads;
+            ml[y][k] = make_float2(-INFINITY, 0.0f);
+            v[y][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (c + k < n && x < e.rows * (D / 4)) {   // the row tile's first CTA holds it at its end, the others at their start
+              const float* src = slot(e.lo + c + k, c + k == 0 ? 1 : 0);
+              ml[y][k] = __ldcg(reinterpret_cast<const float2*>(src + kRowTile * D + 2 * (x / (D / 4))));
+              v[y][k] = __ldcg(reinterpret_cast<const float4*>(src) + x);
+            }
+          }
+#pragma unroll
+        for (int y = 0; y < kX; ++y) {
+          float mn = m[y];
+#pragma unroll
+          for (int k = 0; k < kB; ++k) mn = fmaxf(mn, ml[y][k].x);
+          const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m[y] - mu);   // 0 from -inf
+          m[y] = mn;
+          l[y] *= f;
+          o[y] = make_float4(o[y].x * f, o[y].y * f, o[y].z * f, o[y].w * f);
+#pragma unroll
+          for (int k = 0; k < kB; ++k) {
+            const float g = ex2(ml[y][k].x - mu);
+            l[y] += g * ml[y][k].y;
+            o[y].x += g * v[y][k].x;
+            o[y].y += g * v[y][k].y;
+            o[y].z += g * v[y][k].z;
+            o[y].w += g * v[y][k].w;
           }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mn = fmaxf(mn, ml[k].x);
-        const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m - mu);   // 0 from -inf
-        m = mn;
-        l *= f;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float g = ex2(ml[k].x - mu);
-          l += g * ml[k].y;
-          o.x += g * v[k].x;
-          o.y += g * v[k].y;
-          o.z += g * v[k].z;
-          o.w += g * v[k].w;
-        }
       }
-      const float inv = 1.0f / (l * a.cache.v_gs);
-      const int rr = e.q * kRowTile + row, token = rr / group;
-      const size_t at = (size_t)(e.row0 + token) * a.q_heads + e.h * group + rr - token * group;
-      *reinterpret_cast<uint2*>(a.out + at * D + d) =
-          l > 0.0f ? make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv))
-                   : make_uint2(0u, 0u);
-      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+#pragma unroll
+      for (int y = 0; y < kX; ++y) {
+        const int x = x0 + y * kThreads;
+        if (x >= e.rows * (D / 4)) break;
+        const int row = x / (D / 4), d = x % (D / 4) * 4, rr = e.q * kRowTile + row, token = rr / group;
+        const float inv = 1.0f / (l[y] * a.cache.v_gs);
+        const size_t at = (size_t)(e.row0 + token) * a.q_heads + e.h * group + rr - token * group;
+        *reinterpret_cast<uint2*>(a.out + at * D + d) =
+            l[y] > 0.0f ? make_uint2(float2_to_bf16x2_bits(o[y].x * inv, o[y].y * inv),
+                                     float2_to_bf16x2_bits(o[y].z * inv, o[y].w * inv))
+                        : make_uint2(0u, 0u);
+        if (d == 0 && a.lse != nullptr) a.lse[at] = l[y] > 0.0f ? m[y] * kLn2 + logf(l[y]) : -INFINITY;
+      }
     }
   }
 }
