@@ -37,7 +37,7 @@ moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream
   const int few = decode_rows(a);
   moe_status st = MOE_OK;
   if (few > 0) st = launch_kv4_decode(a, few, status, counters, partials, s);
-  if (st == MOE_OK && any_prompt(a)) st = launch_kv4_prompt(a, few, status, counters, partials, s);
+  if (st == MOE_OK && any_prompt(a)) st = launch_kv4_prompt(a, few, status, partials, s);
   return st;
 }
 

@@ -25,8 +25,10 @@
 // are about as many as the schedulers issue in that time.
 //
 // Work is dealt out by KV tiles: all (request, head, row tile, KV tile) in
-// order, one equal range per CTA; a row tile that two or more CTAs cut leaves
-// fp32 partials that the last of them joins in order.
+// order, one equal range per CTA. A row tile that two or more CTAs cut leaves
+// fp32 partials and a note of them (at most one per CTA); a second, small
+// launch joins them in order. (The last CTA to arrive doing it alone took 5 us
+// per partial: 133 KB through one SM.)
 #include "kernels.cuh"
 #include "kv4.cuh"
 #include "tc_ptx.cuh"
@@ -51,18 +53,27 @@ constexpr float kSlack = 8.0f;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTmemCols = 512;
 
+// The row tile that begins in a CTA's range and goes on past it.
+struct Cut {
+  int row0, rows, h, q;   // first query row of the request, rows of the tile, head, index
+  int n;                  // CTAs that hold a piece of it; 0: there is none
+  int pad[3];
+};
+
 struct PromptArgs {
   moe_kv4_attn_args a;
   int b0, nb;
   int min_rows;        // requests with at most this many rows belong to another kernel
   int* status;
-  int* counters;       // [kKvMaxCtas] zero between launches
+  Cut* cuts;           // [kKvMaxCtas]
   float* partials;     // [kKvMaxCtas][2][kRowTile x D, then (m, l) per row]
   long long wait_limit;
 };
 
 template <int D>
 constexpr int kSlotFloats = kRowTile * (D + 2);
+constexpr size_t kCutFloats = (size_t)kKvMaxCtas * sizeof(Cut) / sizeof(float);
+static_assert(sizeof(Cut) == 32, "sectors");
 
 struct Request {
   int row0, n, kv;
@@ -197,13 +208,6 @@ __device__ __noinline__ void walk_begin(const Range& rg, Walk* w) {
   __syncwarp();
 }
 
-// A row tile at one end of a CTA's range.
-struct Ends {
-  int row0, rows, h, q;   // first query row of the request, rows of the tile, head, index
-  int lo, hi;             // the CTAs that hold its first and its last KV tile
-  int t0, t1, tiles;      // KV tiles done here, of all
-};
-
 template <int D>
 struct Smem {
   static constexpr int kHalves = D / 64;
@@ -221,10 +225,8 @@ struct Smem {
   alignas(8) uint8_t hole[4][8];       // blocks of a tile whose page is bad
   int pre[kChunk + 1];                 // units (over all heads and row tiles) before each request
   Walk walk[kThreads / 32];
-  Ends ends[2];                        // the first and the last row tile of this CTA's range
   uint32_t tmem_base;
   int abort;
-  int last[2];
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -323,7 +325,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     mbar_init(&sm->x_full, 4);
     mbar_init(&sm->x_empty, 4);
     mbar_init(&sm->drain, 2);
-    sm->ends[0].tiles = sm->ends[1].tiles = 0;
     fence_barrier_init();
   }
   for (int b = warp; b < p.nb; b += kThreads / 32) {   // a warp per request
@@ -361,7 +362,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
   __syncthreads();
   const int total = sm->pre[p.nb];
   const int G = min((int)gridDim.x, total), cta = blockIdx.x;
-  if (cta >= G) return;
+  if (cta >= G) {
+    if (tid == 0) p.cuts[cta].n = 0;
+    return;
+  }
   const Range rg = {&p, sm->pre, (int)((long long)total * cta / G), (int)((long long)total * (cta + 1) / G)};
   if (warp == kMmaWarp) tmem_alloc(&sm->tmem_base, kTmemCols);
   Walk* const w = &sm->walk[warp];
@@ -381,11 +385,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     __syncwarp();
   };
   auto cta_of = [&](int unit) { return (int)(((long long)(unit + 1) * G - 1) / total); };
-  auto record = [&](int which) {                // the warp's piece as one of the range's ends
-    if (lane == 0)
-      sm->ends[which] = {w->row0, min(kRowTile, w->n * group - w->q * kRowTile), w->h, w->q, cta_of(w->x + kSetup),
-                         cta_of(w->x + kSetup + w->tiles - 1), w->t0, w->t1, w->tiles};
-  };
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
@@ -501,6 +500,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
             other *= inv;
           }
           const bool blank = give ? !any : final && !(l > 0.0f);   // O holds nothing to read
+          const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
           const int which = done.t0 > 0 ? 0 : 1, swz = give ? done.r & (D / 4 - 1) : 0;
           float* dst = give ? xo + done.r * D : slot(cta, which) + (size_t)done.r * D;
 #pragma unroll 1
@@ -524,17 +524,32 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
             }
             if (!give && !done.real) continue;
             if (final) {
-              uint4* out = reinterpret_cast<uint4*>(a.out + done.at * D + cc);
+              uint16_t* out = a.out + done.at * D + cc;
 #pragma unroll
-              for (int e = 0; e < 32; e += 8)
-                out[e / 8] = make_uint4(float2_to_bf16x2_bits(f[e], f[e + 1]), float2_to_bf16x2_bits(f[e + 2], f[e + 3]),
-                                        float2_to_bf16x2_bits(f[e + 4], f[e + 5]),
-                                        float2_to_bf16x2_bits(f[e + 6], f[e + 7]));
-            } else {
+              for (int e = 0; e < 32; e += 16) {
+                uint32_t b[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) b[k] = float2_to_bf16x2_bits(f[e + 2 * k], f[e + 2 * k + 1]);
+                if (wide) {   // a whole sector per thread
+                  stg_v8(out + e, b);
+                } else {
+                  reinterpret_cast<uint4*>(out + e)[0] = make_uint4(b[0], b[1], b[2], b[3]);
+                  reinterpret_cast<uint4*>(out + e)[1] = make_uint4(b[4], b[5], b[6], b[7]);
+                }
+              }
+            } else if (give) {
 #pragma unroll
               for (int e = 0; e < 32; e += 4)
                 *reinterpret_cast<float4*>(dst + (((cc + e) / 4) ^ swz) * 4) =
                     make_float4(f[e], f[e + 1], f[e + 2], f[e + 3]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) {
+                uint32_t b[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) b[k] = __float_as_uint(f[e + k]);
+                stg_v8(dst + cc + e, b);
+              }
             }
           }
           if (give) sm->x_ml[done.r] = make_float2(m, l);
@@ -780,11 +795,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     // warp's waits hide behind the other's batch.
     const int i = warp - kMmaWarp;
     int j0 = 0, n_q = 0, n_qs = 0, n_p = 0, n_turn = 0;
-    bool ok = true, first = true;
+    bool ok = true;
+    Cut cut = {0, 0, 0, 0, 0, {0, 0, 0}};
     while (w->more && ok) {
       const int nt = w->t1 - w->t0, rows = min(kRowTile, w->n * group - w->q * kRowTile);
-      if (i == 0) record(!first);
-      first = false;
+      if (w->t0 == 0 && w->t1 < w->tiles) {   // only a range's last piece can be one
+        const int lo = cta_of(w->x + kSetup), hi = cta_of(w->x + kSetup + w->tiles - 1);
+        cut = {w->row0, rows, w->h, w->q, hi - lo + 1, {0, 0, 0}};
+      }
       const bool split = rows <= kSplitRows, two = rows > 128, idle = i == 1 && !split && !two;
       const int ahead = split ? 2 : 1;
       if (split) ok = wait(&sm->q_split, n_qs++);
@@ -836,6 +854,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       }
       j0 += nt;
     }
+    if (!ok) cut.n = 0;   // timed out: nothing to join
+    if (lane == 0 && i == 0) p.cuts[cta] = cut;
     if (lane == 0) {
       tc_commit(&sm->drain);
       const long long t0 = clock64();
@@ -848,98 +868,80 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
-  if (sm->abort) {   // a walk stopped short: the range's ends, so that the counters below stay right
-    if (tid == 0) set_status(p.status, MOE_ERR_TIMEOUT);
-    if (warp == 0) {
-      int pieces = 0;
-      for (walk_begin(rg, w); w->more; next()) record(pieces++ > 0);
-    }
-    __syncthreads();
-  }
+  if (tid == 0 && sm->abort) set_status(p.status, MOE_ERR_TIMEOUT);
+}
 
-  // ----------------------------- row tiles that several CTAs cut: the last joins
-  const bool cut0 = sm->ends[0].tiles > 0 && (sm->ends[0].t0 > 0 || sm->ends[0].t1 < sm->ends[0].tiles);
-  const bool cut1 = sm->ends[1].tiles > 0 && sm->ends[1].t1 < sm->ends[1].tiles;
-  if (!cut0 && !cut1) return;
-  if (tid < 2) {
-    int is_last = 0;
-    if (tid == 0 ? cut0 : cut1) {
-      const Ends& e = sm->ends[tid];
-      __threadfence();   // cumulative: the CTA's partials, ordered before by the barrier
-      if (atomicAdd(p.counters + e.lo, 1) == e.hi - e.lo) {
-        p.counters[e.lo] = 0;   // everyone has arrived: ready for the next launch
-        is_last = 1;
-      }
-      __threadfence();
-    }
-    sm->last[tid] = is_last;
+// Joins the partials of the row tiles that several CTAs cut: block (c, part)
+// takes kJoinRows rows of the tile that begins in CTA c. Four elements per
+// thread, all their loads in flight together: the partials lie in L2.
+constexpr int kJoinThreads = 256;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) kv4_prompt_join_kernel(const __grid_constant__ PromptArgs p) {
+  constexpr int kX = 4, kB = 2;   // elements and partials in flight per thread
+  constexpr int kRows = kX * kJoinThreads / (D / 4);
+  pdl_wait();
+  const Cut cut = p.cuts[blockIdx.x];
+  const int x0 = blockIdx.y * kRows * (D / 4) + threadIdx.x, end = cut.rows * (D / 4);
+  if (cut.n < 2 || x0 >= end) return;
+  const moe_kv4_attn_args& a = p.a;
+  const int group = a.q_heads / a.cache.kv_heads;
+  float m[kX], l[kX];
+  float4 o[kX];
+#pragma unroll
+  for (int y = 0; y < kX; ++y) {
+    m[y] = -INFINITY;
+    l[y] = 0.0f;
+    o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   }
-  __syncthreads();
-  for (int side = 0; side < 2; ++side) {
-    if (!sm->last[side]) continue;
-    const Ends e = sm->ends[side];
-    const int n = e.hi - e.lo + 1;
-    constexpr int kX = 4, kB = 2;   // elements and partials in flight per thread
-    for (int x0 = tid; x0 < e.rows * (D / 4); x0 += kX * kThreads) {
-      float m[kX], l[kX];
-      float4 o[kX];
-#pragma unroll
-      for (int y = 0; y < kX; ++y) {
-        m[y] = -INFINITY;
-        l[y] = 0.0f;
-        o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      }
 #pragma unroll 1
-      for (int c = 0; c < n; c += kB) {
-        float2 ml[kX][kB];
-        float4 v[kX][kB];
+  for (int c = 0; c < cut.n; c += kB) {
+    float2 ml[kX][kB];
+    float4 v[kX][kB];
 #pragma unroll
-        for (int y = 0; y < kX; ++y)
+    for (int y = 0; y < kX; ++y)
 #pragma unroll
-          for (int k = 0; k < kB; ++k) {
-            const int x = x0 + y * kThreads;
-            ml[y][k] = make_float2(-INFINITY, 0.0f);
-            v[y][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (c + k < n && x < e.rows * (D / 4)) {   // the row tile's first CTA holds it at its end, the others at their start
-              const float* src = slot(e.lo + c + k, c + k == 0 ? 1 : 0);
-              ml[y][k] = __ldcg(reinterpret_cast<const float2*>(src + kRowTile * D + 2 * (x / (D / 4))));
-              v[y][k] = __ldcg(reinterpret_cast<const float4*>(src) + x);
-            }
-          }
-#pragma unroll
-        for (int y = 0; y < kX; ++y) {
-          float mn = m[y];
-#pragma unroll
-          for (int k = 0; k < kB; ++k) mn = fmaxf(mn, ml[y][k].x);
-          const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m[y] - mu);   // 0 from -inf
-          m[y] = mn;
-          l[y] *= f;
-          o[y] = make_float4(o[y].x * f, o[y].y * f, o[y].z * f, o[y].w * f);
-#pragma unroll
-          for (int k = 0; k < kB; ++k) {
-            const float g = ex2(ml[y][k].x - mu);
-            l[y] += g * ml[y][k].y;
-            o[y].x += g * v[y][k].x;
-            o[y].y += g * v[y][k].y;
-            o[y].z += g * v[y][k].z;
-            o[y].w += g * v[y][k].w;
-          }
+      for (int k = 0; k < kB; ++k) {
+        const int x = x0 + y * kJoinThreads;
+        ml[y][k] = make_float2(-INFINITY, 0.0f);
+        v[y][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (c + k < cut.n && x < end) {   // the tile's first CTA holds it at its end, the others at their start
+          const float* src = p.partials + ((size_t)(blockIdx.x + c + k) * 2 + (c + k == 0 ? 1 : 0)) * kSlotFloats<D>;
+          ml[y][k] = *reinterpret_cast<const float2*>(src + kRowTile * D + 2 * (x / (D / 4)));
+          v[y][k] = reinterpret_cast<const float4*>(src)[x];
         }
       }
 #pragma unroll
-      for (int y = 0; y < kX; ++y) {
-        const int x = x0 + y * kThreads;
-        if (x >= e.rows * (D / 4)) break;
-        const int row = x / (D / 4), d = x % (D / 4) * 4, rr = e.q * kRowTile + row, token = rr / group;
-        const float inv = 1.0f / (l[y] * a.cache.v_gs);
-        const size_t at = (size_t)(e.row0 + token) * a.q_heads + e.h * group + rr - token * group;
-        *reinterpret_cast<uint2*>(a.out + at * D + d) =
-            l[y] > 0.0f ? make_uint2(float2_to_bf16x2_bits(o[y].x * inv, o[y].y * inv),
-                                     float2_to_bf16x2_bits(o[y].z * inv, o[y].w * inv))
-                        : make_uint2(0u, 0u);
-        if (d == 0 && a.lse != nullptr) a.lse[at] = l[y] > 0.0f ? m[y] * kLn2 + logf(l[y]) : -INFINITY;
+    for (int y = 0; y < kX; ++y) {
+      float mn = m[y];
+#pragma unroll
+      for (int k = 0; k < kB; ++k) mn = fmaxf(mn, ml[y][k].x);
+      const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m[y] - mu);   // 0 from -inf
+      m[y] = mn;
+      l[y] *= f;
+      o[y] = make_float4(o[y].x * f, o[y].y * f, o[y].z * f, o[y].w * f);
+#pragma unroll
+      for (int k = 0; k < kB; ++k) {
+        const float g = ex2(ml[y][k].x - mu);
+        l[y] += g * ml[y][k].y;
+        o[y].x += g * v[y][k].x;
+        o[y].y += g * v[y][k].y;
+        o[y].z += g * v[y][k].z;
+        o[y].w += g * v[y][k].w;
       }
     }
+  }
+#pragma unroll
+  for (int y = 0; y < kX; ++y) {
+    const int x = x0 + y * kJoinThreads;
+    if (x >= end) break;
+    const int row = x / (D / 4), d = x % (D / 4) * 4, rr = cut.q * kRowTile + row, token = rr / group;
+    const float inv = 1.0f / (l[y] * a.cache.v_gs);
+    const size_t at = (size_t)(cut.row0 + token) * a.q_heads + cut.h * group + rr - token * group;
+    *reinterpret_cast<uint2*>(a.out + at * D + d) =
+        l[y] > 0.0f ? make_uint2(float2_to_bf16x2_bits(o[y].x * inv, o[y].y * inv),
+                                 float2_to_bf16x2_bits(o[y].z * inv, o[y].w * inv))
+                    : make_uint2(0u, 0u);
+    if (d == 0 && a.lse != nullptr) a.lse[at] = l[y] > 0.0f ? m[y] * kLn2 + logf(l[y]) : -INFINITY;
   }
 }
 
@@ -951,23 +953,26 @@ cudaError_t launch(const PromptArgs& p, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = opt_in_smem(k, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, k, dim3(ctas), dim3(kThreads), smem, s, p);
+  e = launch_ex(false, k, dim3(ctas), dim3(kThreads), smem, s, p);
+  if (e != cudaSuccess) return e;
+  constexpr int rows = 4 * kJoinThreads / (D / 4);
+  return launch_ex(true, kv4_prompt_join_kernel<D>, dim3(ctas, kRowTile / rows), dim3(kJoinThreads), 0, s, p);
 }
 
 }  // namespace
 
 size_t kv4_prompt_ws_floats(int head_dim) {
-  return (size_t)kKvMaxCtas * 2 * (head_dim == 64 ? kSlotFloats<64> : kSlotFloats<128>);
+  return kCutFloats + (size_t)kKvMaxCtas * 2 * (head_dim == 64 ? kSlotFloats<64> : kSlotFloats<128>);
 }
 
-moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, int* counters, float* partials,
+moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials,
                              cudaStream_t s) {
   PromptArgs p;
   p.a = a;
   p.min_rows = min_rows;
   p.status = status;
-  p.counters = counters;
-  p.partials = partials;
+  p.cuts = reinterpret_cast<Cut*>(partials);
+  p.partials = partials + kCutFloats;
   p.wait_limit = debug_wait_limit();
   const int sms = sm_count(), ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
   for (int b0 = 0; b0 < a.batch; b0 += kChunk) {
@@ -975,7 +980,7 @@ moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* stat
     p.nb = a.batch - b0 < kChunk ? a.batch - b0 : kChunk;
     cudaError_t e = a.cache.head_dim == 64 ? launch<64>(p, ctas, s) : launch<128>(p, ctas, s);
     if (e != cudaSuccess) return cuda_ok(e);
-    count_launches(1);
+    count_launches(2);
   }
   return MOE_OK;
 }
