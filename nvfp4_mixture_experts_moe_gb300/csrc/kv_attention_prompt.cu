@@ -9,9 +9,9 @@
 //
 // Per CTA (one per SM):
 // * four dequant warps, each two 16-token blocks of the tile: codes and scales
-//   by plain loads a tile ahead (the packed cache is small and read by
-//   several row tiles: it comes from L2), converted into 128-byte-swizzled
-//   shared-memory tiles, keys K-major, values with d contiguous (MN-major);
+//   by plain loads a tile ahead, converted into 128-byte-swizzled shared-memory
+//   tiles, keys K-major, values with d contiguous (MN-major); a scout warp has
+//   looked up the pages and sent the blocks on their way into L2 before;
 // * two threads issue S_i = Q_i K^T and O_i += P_i V, each for one of the two row
 //   tiles i, so one tile's softmax runs under the other's MMAs; P_i (f16, read
 //   from tensor memory) lies in S_i's columns;
@@ -45,7 +45,8 @@ constexpr int kSoftWarps = 8, kDeqWarps = 4;
 constexpr int kWarpBlocks = kTok / kKvBlock / kDeqWarps;
 static_assert(kWarpBlocks == 2, "blocks of a dequant warp");
 constexpr int kMmaWarp = kSoftWarps + kDeqWarps;   // and the one after it
-constexpr int kThreads = (kMmaWarp + 2) * 32;
+constexpr int kScoutWarp = kMmaWarp + 2;
+constexpr int kThreads = (kScoutWarp + 1) * 32;
 constexpr int kSetup = 2;              // what starting and ending a row tile costs, in KV tiles
 constexpr int kSplitRows = 64;         // row tiles of up to this many rows are split over their KV tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -208,6 +209,14 @@ __device__ __noinline__ void walk_begin(const Range& rg, Walk* w) {
   __syncwarp();
 }
 
+// A 16-token block of a tile to come: where it lies, its tokens that exist.
+struct Place {
+  const uint8_t* src;
+  int left;
+  int hole;         // 0xff: its page is bad
+};
+constexpr int kPlaces = 8;             // tiles looked up ahead
+
 template <int D>
 struct Smem {
   static constexpr int kHalves = D / 64;
@@ -225,6 +234,9 @@ struct Smem {
   alignas(8) uint8_t hole[4][8];       // blocks of a tile whose page is bad
   int pre[kChunk + 1];                 // units (over all heads and row tiles) before each request
   Walk walk[kThreads / 32];
+  alignas(16) Place place[kPlaces][kTok / kKvBlock];
+  int place_more[kPlaces];             // 0: the range ends before this tile
+  uint64_t place_full[kPlaces], place_empty[kPlaces];
   uint32_t tmem_base;
   int abort;
 };
@@ -320,6 +332,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       mbar_init(&sm->kv_full[1][i], kDeqWarps);
       mbar_init(&sm->kv_empty[0][i], 2);
       mbar_init(&sm->kv_empty[1][i], 2);
+    }
+    for (int i = 0; i < kPlaces; ++i) {
+      mbar_init(&sm->place_full[i], 1);
+      mbar_init(&sm->place_empty[i], kDeqWarps);
     }
     mbar_init(&sm->q_split, 4);
     mbar_init(&sm->x_full, 4);
@@ -668,114 +684,114 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     // ------------------------------------------------------------- dequant
     const int blk0 = (warp - kSoftWarps) * kWarpBlocks;   // this warp's 16-token blocks of every tile
     constexpr int kLoads = D / 64;                 // 16-byte code loads per lane for a block's keys
-    constexpr int kChunks = D / 32;                // 16-byte code chunks of a row
-    const int cl = lane % kChunks, tl = lane / kChunks;   // this lane's chunk, and its row within a load
-    constexpr int kRowsPerLoad = 32 / kChunks;
-    const int P = a.cache.page_tokens, p_log = __ffs(P) - 1;
+    // This lane's 16-byte chunk of a row's codes (32 elements) and its row
+    // within a load. Eight neighbouring lanes take two neighbouring chunks of
+    // four rows: their 16-byte stores to the swizzled tile hit different banks.
+    const int cl = (lane & 1) + (D == 128 ? lane >> 4 << 1 : 0), tl = D == 128 ? lane >> 1 & 7 : lane >> 1;
+    constexpr int kRowsPerLoad = D == 128 ? 8 : 16;
+    uint32_t off[4];                               // of this lane's four 16-byte stores, in a tile
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off[j] = tile_chunk(tl, 4 * cl + j);
     struct Raw {
       uint4 codes[kWarpBlocks][kLoads];
       uint32_t sf[kWarpBlocks][kLoads];            // two scale bytes each
     } rk, rv;
-    // The walk runs two tiles ahead: a tile's page ids are read one tile before
-    // its data, and its data one tile before it is converted.
-    int n_page[kWarpBlocks], n_left[kWarpBlocks], n_at[kWarpBlocks], n_h = 0, lt = w->t0;
-    bool n_any = false;
-    const uint8_t* src[kWarpBlocks];
-    int left[kWarpBlocks];                         // tokens of the block that exist
-    auto look_up = [&]() {                         // page ids of the walk's next tile
-      n_any = w->more != 0;
-#pragma unroll
-      for (int x = 0; x < kWarpBlocks; ++x) n_left[x] = n_page[x] = n_at[x] = 0;
-      if (!n_any) return;
-      n_h = w->h;
-      const int tok0 = w->first + lt * kTok + blk0 * kKvBlock, kv = w->kv;
-      const int32_t* table = a.block_table + (size_t)(p.b0 + w->b) * a.max_pages;
+    auto load = [&](Raw& r, int j, int at) {       // keys or values of tile j
+      const int cat = at + tl * L::kCodeRow + 16 * cl, sat = at + L::kKeyScales + tl * L::kScaleRow + 2 * cl;
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x) {
-        const int tok = tok0 + x * kKvBlock;
-        n_left[x] = max(0, kv - tok);
-        n_at[x] = (tok & (P - 1)) / kKvBlock;
-        if (n_left[x] > 0) n_page[x] = __ldg(table + (tok >> p_log));
-      }
-      if (++lt == w->t1) {
-        next();
-        lt = 0;
-      }
-    };
-    bool have = false;
-    uint32_t holes = 0;                            // of the located tile, bit x
-    auto locate = [&]() {                          // where the looked-up tile lies
-      have = n_any;
-      holes = 0;
-#pragma unroll
-      for (int x = 0; x < kWarpBlocks; ++x) {
-        left[x] = n_left[x];
-        if (left[x] > 0 && (n_page[x] < 0 || n_page[x] >= a.cache.num_pages)) {
-          holes |= 1u << x;
-          left[x] = 0;
-          if (lane == 0) set_status(p.status, MOE_ERR_DEVICE);
-        }
-        src[x] = static_cast<const uint8_t*>(a.cache.pool) + tl * L::kCodeRow + 16 * cl +
-                 kv4_block_offset(left[x] > 0 ? n_page[x] : 0, n_h, Hk, P / kKvBlock, n_at[x], L::kBytes);
-      }
-    };
-    auto load = [&](Raw& r, int at) {              // keys or values of the located tile
-      const int sat = at + L::kKeyScales - (tl * L::kCodeRow + 16 * cl) + tl * L::kScaleRow + 2 * cl;
-#pragma unroll
-      for (int x = 0; x < kWarpBlocks; ++x)
+        const Place pl = sm->place[j & (kPlaces - 1)][blk0 + x];
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
           r.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what was not appended enters as zeros
           r.sf[x][y] = 0u;
-          if (y * kRowsPerLoad + tl < left[x]) {
-            r.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(src[x] + at + y * kRowsPerLoad * L::kCodeRow));
-            r.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(src[x] + sat + y * kRowsPerLoad * L::kScaleRow));
+          if (y * kRowsPerLoad + tl < pl.left) {
+            r.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(pl.src + cat + y * kRowsPerLoad * L::kCodeRow));
+            r.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(pl.src + sat + y * kRowsPerLoad * L::kScaleRow));
           }
         }
+      }
     };
     auto store = [&](uint32_t tile, const Raw& r) {
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x)
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
-          const int row = (blk0 + x) * kKvBlock + y * kRowsPerLoad + tl;
+          const uint32_t at = tile + ((blk0 + x) * kKvBlock + y * kRowsPerLoad) * 128;
           const uint32_t two = cvt_e4m3x2_f16x2(r.sf[x][y]);
           const uint32_t sc0 = __byte_perm(two, 0, 0x1010), sc1 = __byte_perm(two, 0, 0x3232);
           const uint32_t wd[4] = {r.codes[x][y].x, r.codes[x][y].y, r.codes[x][y].z, r.codes[x][y].w};
-          // the two 64-column halves share banks: their lanes store in different orders
-          const bool flip = D == 128 && cl >= 2;
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             uint32_t f[4];
-            cvt_e2m1x8_f16(flip ? wd[j ^ 2] : wd[j], f);
-            const uint32_t sc = (j < 2) != flip ? sc0 : sc1;
-            sts16(tile + tile_chunk(row, 4 * cl + (flip ? j ^ 2 : j)),
+            cvt_e2m1x8_f16(wd[j], f);
+            const uint32_t sc = j < 2 ? sc0 : sc1;
+            sts16(at + off[j],
                   make_uint4(hmul2_u32(f[0], sc), hmul2_u32(f[1], sc), hmul2_u32(f[2], sc), hmul2_u32(f[3], sc)));
           }
         }
     };
-    look_up();
-    locate();
-    load(rk, 0);
-    load(rv, L::kValueCodes);
-    look_up();
+    // a tile's data are read one tile before they are converted
+    bool have = wait(&sm->place_full[0], 0) && sm->place_more[0];
+    if (have) {
+      load(rk, 0, 0);
+      load(rv, 0, L::kValueCodes);
+    }
     for (int j = 0; have; ++j) {
-      const int s = j & 1, phase = (j >> 1) ^ 1;
+      const int s = j & 1, phase = (j >> 1) ^ 1, here = j & (kPlaces - 1), there = (j + 1) & (kPlaces - 1);
       if (!wait(&sm->kv_empty[0][s], phase)) break;
-      if (lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = holes >> lane & 1 ? 0xff : 0;
+      if (lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = (uint8_t)sm->place[here][blk0 + lane].hole;
       store(smem_u32(&sm->kv[0][s][0]), rk);
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->kv_full[0][s]);
-      locate();
-      load(rk, 0);
-      look_up();
+      if (lane == 0) {
+        mbar_arrive(&sm->kv_full[0][s]);
+        mbar_arrive(&sm->place_empty[here]);
+      }
+      if (!wait(&sm->place_full[there], (j + 1) / kPlaces)) break;
+      have = sm->place_more[there];
+      if (have) load(rk, j + 1, 0);
       if (!wait(&sm->kv_empty[1][s], phase)) break;
       store(smem_u32(&sm->kv[1][s][0]), rv);
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sm->kv_full[1][s]);
-      load(rv, L::kValueCodes);
+      if (have) load(rv, j + 1, L::kValueCodes);
+    }
+  } else if (warp == kScoutWarp) {
+    // --------------------------------------------------------------- scout
+    // Walks up to kPlaces tiles ahead of the conversion: a lane per block reads
+    // the page ids and starts the blocks' way into L2, so that the dequant
+    // warps' loads wait neither for the tables nor for memory.
+    const int P = a.cache.page_tokens, p_log = __ffs(P) - 1;
+    for (int j = 0, lt = w->t0;; ++j) {
+      const int here = j & (kPlaces - 1), more = w->more;
+      if (!wait(&sm->place_empty[here], (j / kPlaces) ^ 1)) break;
+      if (more && lane < kTok / kKvBlock) {
+        const int tok = w->first + lt * kTok + lane * kKvBlock;
+        Place pl = {nullptr, max(0, w->kv - tok), 0};
+        if (pl.left > 0) {
+          const int page = __ldg(a.block_table + (size_t)(p.b0 + w->b) * a.max_pages + (tok >> p_log));
+          if (page >= 0 && page < a.cache.num_pages) {
+            pl.src = static_cast<const uint8_t*>(a.cache.pool) +
+                     kv4_block_offset(page, w->h, Hk, P / kKvBlock, (tok & (P - 1)) / kKvBlock, L::kBytes);
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(pl.src), "r"((uint32_t)L::kBytes) : "memory");
+          } else {
+            pl.left = 0;
+            pl.hole = 0xff;
+            set_status(p.status, MOE_ERR_DEVICE);
+          }
+        }
+        sm->place[here][lane] = pl;
+      }
+      if (lane == 0) sm->place_more[here] = more;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->place_full[here]);
+      if (!more) break;
+      if (++lt == w->t1) {
+        next();
+        lt = 0;
+      }
     }
   } else {
     // ------------------------------------------------------------------ MMA
