@@ -731,32 +731,46 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           }
         }
     };
-    // a tile's data are read one tile before they are converted
-    bool have = wait(&sm->place_full[0], 0) && sm->place_more[0];
+    // A tile's data are read one tile before they are converted, and the keys
+    // go one tile ahead of the values: a stage of values is free only after
+    // the softmax of the tile two before, a stage of keys already before it.
+    auto place = [&](int j) {                      // whether there is a tile j
+      return wait(&sm->place_full[j & (kPlaces - 1)], j / kPlaces) && sm->place_more[j & (kPlaces - 1)] != 0;
+    };
+    auto keys = [&](int j) {
+      if (!wait(&sm->kv_empty[0][j & 1], (j >> 1) ^ 1)) return false;
+      if (lane < kWarpBlocks)
+        sm->hole[j & 3][blk0 + lane] = (uint8_t)sm->place[j & (kPlaces - 1)][blk0 + lane].hole;
+      store(smem_u32(&sm->kv[0][j & 1][0]), rk);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sm->kv_full[0][j & 1]);
+      return true;
+    };
+    bool have = place(0), ahead = false, ok = true;   // tiles j and j + 1 exist
     if (have) {
       load(rk, 0, 0);
       load(rv, 0, L::kValueCodes);
     }
-    for (int j = 0; have; ++j) {
-      const int s = j & 1, phase = (j >> 1) ^ 1, here = j & (kPlaces - 1), there = (j + 1) & (kPlaces - 1);
-      if (!wait(&sm->kv_empty[0][s], phase)) break;
-      if (lane < kWarpBlocks) sm->hole[j & 3][blk0 + lane] = (uint8_t)sm->place[here][blk0 + lane].hole;
-      store(smem_u32(&sm->kv[0][s][0]), rk);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sm->kv_full[0][s]);
-        mbar_arrive(&sm->place_empty[here]);
+    for (int j = -1; have && ok; ++j) {
+      if ((j < 0 || ahead) && !(ok = keys(j + 1))) break;
+      const bool more = (j < 0 || ahead) && place(j + 2);
+      if (more) load(rk, j + 2, 0);
+      if (j >= 0) {
+        const int s = j & 1;
+        if (!wait(&sm->kv_empty[1][s], (j >> 1) ^ 1)) break;
+        store(smem_u32(&sm->kv[1][s][0]), rv);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->kv_full[1][s]);
+        have = ahead;
+        if (have) load(rv, j + 1, L::kValueCodes);
       }
-      if (!wait(&sm->place_full[there], (j + 1) / kPlaces)) break;
-      have = sm->place_more[there];
-      if (have) load(rk, j + 1, 0);
-      if (!wait(&sm->kv_empty[1][s], phase)) break;
-      store(smem_u32(&sm->kv[1][s][0]), rv);
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sm->kv_full[1][s]);
-      if (have) load(rv, j + 1, L::kValueCodes);
+      if (have) {   // tile j + 1 is converted or in registers
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->place_empty[(j + 1) & (kPlaces - 1)]);
+      }
+      ahead = more;
     }
   } else if (warp == kScoutWarp) {
     // --------------------------------------------------------------- scout
