@@ -4,6 +4,7 @@
 // between the two reductions, so every array is read or written once.
 #include "kernels.cuh"
 #include "kv4.cuh"
+#include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
@@ -75,6 +76,8 @@ __device__ __forceinline__ float cta_sum(float v, float* red) {
 }
 
 constexpr int kMaxH = 16384;
+constexpr int kStages = 2;                      // rows a CTA of the stream kernel holds or fetches
+constexpr size_t kStreamSmem = 226 * 1024;      // of an SM's CTAs, 1 KiB each for the reductions
 constexpr int threads_max(int V, int N) { return kMaxH / (V * N) < 1024 ? kMaxH / (V * N) : 1024; }
 
 // V elements per vector, N vectors per thread (thread i takes vectors i, i + threads, ...).
@@ -142,6 +145,199 @@ __global__ void __launch_bounds__(threads_max(V, N)) block_norm_kernel(moe_block
   }
 }
 
+// Two fp32 at a time: bf16 pairs and the packed arithmetic of sm_100 on.
+struct Pair {
+  float x, y;
+};
+__device__ __forceinline__ unsigned long long bits(Pair p) {
+  unsigned long long v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(p.x), "f"(p.y));
+  return v;
+}
+__device__ __forceinline__ Pair pair(unsigned long long v) {
+  Pair p;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(p.x), "=f"(p.y) : "l"(v));
+  return p;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return pair(d);
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return pair(d);
+}
+__device__ __forceinline__ Pair bf16_pair(uint32_t w) { return {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)}; }
+
+struct Vec {   // eight bf16, or four fp32
+  uint32_t w[4];
+};
+__device__ __forceinline__ Vec vec16(const void* p, int at) {
+  const uint4 v = static_cast<const uint4*>(p)[at];
+  return {v.x, v.y, v.z, v.w};
+}
+
+// Many rows: persistent CTAs whose threads copy their own vectors of the rows
+// to come into shared memory (16-byte asynchronous copies, kStages rows deep),
+// so memory is busy through both reductions of a row. A thread reads only
+// what it copied: no barrier but the reductions'. The weights come from L1
+// for each row, asked for before the reduction in front of them: held in
+// registers they and the row do not fit 64.
+template <int N, bool F32>
+__global__ void __launch_bounds__(512, 2) block_norm_stream_kernel(moe_block_norm_args a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][32];
+  constexpr int kRes = F32 ? 2 : 1;                 // 16-byte pieces of a residual vector
+  const int vecs = a.H / 8, threads = blockDim.x, tid = threadIdx.x;
+  const bool has_x = a.x != nullptr, post = has_x && a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const bool gated = has_x && a.gate != nullptr, gate_rows = gated && a.gate_stride != 0;
+  const int piece = vecs * 16, stage = piece * (has_x + kRes + gate_rows);   // bytes
+  const int res_at = has_x ? piece : 0, gate_at = res_at + kRes * piece;
+  const float inv_h = 1.0f / (float)a.H;
+  const Pair offset{a.w_offset, a.w_offset}, keep{a.residual_scale, a.residual_scale};
+  const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+  auto fetch = [&](long long row, int slot) {
+    if (row < a.T) {
+      const uint32_t at = base + slot * stage;
+      const uint16_t* x = a.x + row * a.x_stride;
+      const uint16_t* g = a.gate + row * a.gate_stride;
+      const uint8_t* r = static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * (F32 ? 4 : 2);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = i * threads + tid;
+        if (c < vecs) {
+          if (has_x) tc::cp_async_16(at + c * 16, x + c * 8, 16);
+#pragma unroll
+          for (int k = 0; k < kRes; ++k) tc::cp_async_16(at + res_at + k * piece + c * 16, r + (c * kRes + k) * 16, 16);
+          if (gate_rows) tc::cp_async_16(at + gate_at + c * 16, g + c * 8, 16);
+        }
+      }
+    }
+    tc::cp_async_commit();
+  };
+  for (int s = 0; s < kStages; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+  int slot = 0;
+  for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
+    tc::cp_async_wait<kStages - 1>();
+    const uint8_t* at = ring + slot * stage;
+    Vec w[N];
+    Pair r[N][4];
+    float scale = a.branch_scale;
+    if (post) {
+      Pair s{0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = i * threads + tid;
+        if (c < vecs) {
+          w[i] = vec16(a.w_post, c);
+          const Vec x = vec16(at, c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s = fma2(bf16_pair(x.w[j]), bf16_pair(x.w[j]), s);
+        }
+      }
+      scale *= rsqrtf(cta_sum(s.x + s.y, red[0]) * inv_h + a.eps);
+    }
+    Pair s{0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = i * threads + tid;
+      if (c < vecs) {
+        Vec q = vec16(at + res_at, c);
+        if constexpr (F32) {
+          const Vec q1 = vec16(at + res_at, vecs + c);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            r[i][j] = mul2(keep, {__uint_as_float(q.w[2 * j]), __uint_as_float(q.w[2 * j + 1])});
+            r[i][2 + j] = mul2(keep, {__uint_as_float(q1.w[2 * j]), __uint_as_float(q1.w[2 * j + 1])});
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[i][j] = mul2(keep, bf16_pair(q.w[j]));
+        }
+        if (has_x) {
+          Pair n[4];
+          const Vec x = vec16(at, c);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) n[j] = mul2(bf16_pair(x.w[j]), {scale, scale});
+          if (post) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n[j] = mul2(n[j], add2(bf16_pair(w[i].w[j]), offset));
+          }
+          if (gated) {
+            const Vec g = gate_rows ? vec16(at + gate_at, c) : vec16(a.gate, c);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[i][j] = fma2(n[j], bf16_pair(g.w[j]), r[i][j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[i][j] = add2(n[j], r[i][j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s = fma2(r[i][j], r[i][j], s);
+        if (a.residual_out != nullptr) {
+          const float v[8] = {r[i][0].x, r[i][0].y, r[i][1].x, r[i][1].y, r[i][2].x, r[i][2].y, r[i][3].x, r[i][3].y};
+          store_res<8, F32>(a.residual_out, row * a.H + (size_t)c * 8, v);
+        }
+        if (pre) w[i] = vec16(a.w_pre, c);
+      }
+    }
+    fetch(row + (long long)kStages * gridDim.x, slot);   // this thread has read its part of the slot
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    if (pre) {
+      const float inv = rsqrtf(cta_sum(s.x + s.y, red[1]) * inv_h + a.eps);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = i * threads + tid;
+        if (c < vecs) {
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const Pair y = mul2(mul2(r[i][j], {inv, inv}), add2(bf16_pair(w[i].w[j]), offset));
+            v[2 * j] = y.x, v[2 * j + 1] = y.y;
+          }
+          store_bf16<8>(a.out + row * a.H + (size_t)c * 8, v);
+        }
+      }
+    }
+    if (!(post && pre)) __syncthreads();   // one reduction a row: its buffer is read by all before the next
+  }
+}
+
+// Some 1024 threads an SM, in CTAs of a row each: at 64 registers more would
+// not fit, and two rows a CTA keep 64 KiB or more in flight at every H.
+struct Stream {
+  int n, threads, per_sm;
+  size_t smem;
+  bool ok;
+};
+Stream plan_stream(const moe_block_norm_args& a) {
+  Stream p;
+  const int vecs = a.H / 8;
+  p.n = a.H <= 4096 ? 1 : 2;
+  p.threads = ((vecs + p.n - 1) / p.n + 31) / 32 * 32;
+  p.per_sm = 1024 / p.threads < 8 ? 1024 / p.threads : 8;
+  p.smem = (size_t)kStages * a.H * ((a.x ? 2 : 0) + (a.residual_f32 ? 4 : 2) + (a.gate && a.gate_stride ? 2 : 0));
+  // Every CTA has a row to fetch while it works on one.
+  p.ok = a.H <= 8192 && p.per_sm * (p.smem + 1024) <= kStreamSmem && a.T > 2 * p.per_sm * sm_count();
+  return p;
+}
+
+template <int N>
+cudaError_t launch_stream(const moe_block_norm_args& a, const Stream& p, cudaStream_t s) {
+  auto k = a.residual_f32 ? block_norm_stream_kernel<N, true> : block_norm_stream_kernel<N, false>;
+  static std::atomic<unsigned long long> done[2];
+  cudaError_t e = opt_in_smem(k, kStreamSmem / 2, done[a.residual_f32 ? 1 : 0]);
+  if (e != cudaSuccess) return e;
+  return launch_ex(false, k, dim3(p.per_sm * sm_count()), dim3(p.threads), p.smem, s, a);
+}
+
 template <int V, int N>
 cudaError_t launch(const moe_block_norm_args& a, cudaStream_t s) {
   const int vecs = (a.H + V - 1) / V;
@@ -164,6 +360,8 @@ moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s) {
   cudaError_t e;
   if (!vec) {
     e = a.H <= 4096 ? launch<1, 4>(a, s) : launch<1, 16>(a, s);
+  } else if (const Stream p = plan_stream(a); p.ok) {
+    e = p.n == 1 ? launch_stream<1>(a, p, s) : launch_stream<2>(a, p, s);
   } else if (a.H <= 8192 && a.T <= 304) {
     e = launch<8, 1>(a, s);   // few rows: as many threads per row as it has vectors
   } else {

@@ -475,6 +475,16 @@ def test_norm_matches_the_oracle(T, H, gate, f32, post, pre, has_x):
         assert (err <= 2.0 ** -18 * (size * gain + np.abs(ry)) + 2.0 ** -8 * np.abs(ry) + 1e-30).all(), err.max()
 
 
+# As many rows as make a CTA take several in turn, at widths that leave threads without a vector.
+@pytest.mark.parametrize("T,H,gate,f32,post,pre,has_x", [
+    (5000, 8, "token", True, True, True, True), (3001, 520, "channel", False, True, True, True),
+    (1000, 2880, None, True, True, False, True), (997, 4096, "token", True, False, True, True),
+    (913, 4104, "token", False, True, True, True), (640, 7168, "channel", False, True, True, True),
+    (2000, 1536, None, False, False, True, False), (700, 8192, None, True, True, True, True)])
+def test_norm_of_many_rows_matches_the_oracle(T, H, gate, f32, post, pre, has_x):
+    test_norm_matches_the_oracle(T, H, gate, f32, post, pre, has_x)
+
+
 def test_norm_strides_alignment_in_place_and_stream():
     from nvfp4_mixture_experts_moe_gb300 import block_norm
     T, H = 6, 256
