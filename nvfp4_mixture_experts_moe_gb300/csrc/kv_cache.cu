@@ -11,31 +11,35 @@
 namespace moe {
 namespace {
 
-constexpr int kThreads = 256;
-
-// One thread per block of 16 elements: 32 bytes of bf16 in, 8 bytes of codes
-// and a scale byte out. A warp takes D/16 blocks of 512/D consecutive tokens
-// of one head, so with consecutive slots its codes and scales are whole
-// 32-byte sectors.
+// One thread per block of 16 elements: 32 bytes of bf16 on one side, 8 bytes
+// of codes and a scale byte on the other. A warp takes D/16 blocks of 512/D
+// consecutive tokens of one head's keys or values, so with consecutive slots
+// its codes and scales are whole 32-byte sectors; the warps of a CTA take
+// the heads and sides of those tokens, which lie side by side in a row.
+constexpr int kMaxWarps = 16;
 template <int D>
 struct Place {
   static constexpr int kBlocks = D / 16;
   static constexpr int kTokens = 32 / kBlocks;
   int blk, h, kv, t;
-  __device__ __forceinline__ explicit Place(size_t i, int Hk) {
-    blk = (int)(i % kBlocks);
-    i /= kBlocks;
-    const int tl = (int)(i % kTokens);
-    i /= kTokens;
-    h = (int)(i % Hk);
-    i /= Hk;
-    kv = (int)(i & 1);
-    t = (int)(i >> 1) * kTokens + tl;
-  }
-  static size_t threads(int tokens, int Hk) {
-    return (size_t)((tokens + kTokens - 1) / kTokens) * 2 * Hk * 32;
+  __device__ __forceinline__ Place() {
+    const int pair = blockIdx.y * blockDim.y + threadIdx.y;
+    blk = threadIdx.x % kBlocks;
+    t = blockIdx.x * kTokens + threadIdx.x / kBlocks;
+    h = pair >> 1;
+    kv = pair & 1;
   }
 };
+
+template <class K, class... A>
+moe_status launch_cache(K kernel, int D, int Hk, int tokens, cudaStream_t s, A... args) {
+  const int warps = 2 * Hk < kMaxWarps ? 2 * Hk : kMaxWarps, per = 512 / D;
+  const dim3 grid((unsigned)(((long long)tokens + per - 1) / per), (2 * Hk + warps - 1) / warps);
+  const cudaError_t e = launch_ex(false, kernel, grid, dim3(32, warps), 0, s, args...);
+  if (e != cudaSuccess) return cuda_ok(e);
+  count_launches(1);
+  return MOE_OK;
+}
 
 // The block and the row within it of a slot; false for a slot outside the pool.
 template <int D>
@@ -46,35 +50,56 @@ __device__ __forceinline__ uint8_t* slot_row(const moe_kv4_cache& c, int slot, i
          kv4_block_offset(page, h, c.kv_heads, c.page_tokens / kKvBlock, pos / kKvBlock, Kv4Block<D>::kBytes);
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads)
+// 32 bytes of one thread: one load of a sector where the address allows it.
+template <bool kWide>
+__device__ __forceinline__ void load_32(const void* p, uint32_t (&w)[8]) {
+  if constexpr (kWide) {
+    asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = __ldg(static_cast<const uint4*>(p)), b = __ldg(static_cast<const uint4*>(p) + 1);
+    w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
+  }
+}
+
+// Largest magnitude of 16 bf16, as fp32; NaN if there is one.
+__device__ __forceinline__ float amax16(const uint32_t (&w)[8]) {
+  uint32_t m = w[0] & 0x7fff7fffu;
+#pragma unroll
+  for (int j = 1; j < 8; ++j) {
+    uint32_t x = w[j] & 0x7fff7fffu;
+    asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(x));
+  }
+  const float lo = __uint_as_float(m << 16), hi = __uint_as_float(m & 0xffff0000u);
+  return lo != lo ? lo : hi != hi ? hi : fmaxf(lo, hi);
+}
+
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kMaxWarps * 32)
     kv4_append_kernel(moe_kv4_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                       long long k_stride, long long v_stride, const int32_t* __restrict__ slots, int tokens,
                       int32_t* status) {
   using L = Kv4Block<D>;
-  const Place<D> p(blockIdx.x * (size_t)kThreads + threadIdx.x, c.kv_heads);
-  if (p.t >= tokens) return;
+  const Place<D> p;
+  if (p.t >= tokens || p.h >= c.kv_heads) return;
+  const uint16_t* src = p.kv ? v + (size_t)p.t * v_stride : k + (size_t)p.t * k_stride;
+  uint32_t w[8];
+  load_32<kWide>(src + (size_t)p.h * D + p.blk * 16, w);   // next to the slot's load, not behind it
   const int slot = slots[p.t];
   if (slot < 0) return;
   if (slot >= c.num_pages * c.page_tokens) {
     if (status != nullptr) *status = MOE_ERR_DEVICE;
     return;
   }
-  const uint16_t* src = p.kv ? v + (size_t)p.t * v_stride : k + (size_t)p.t * k_stride;
-  src += (size_t)p.h * D + p.blk * 16;
-  const uint4 v0 = ldg_stream(src), v1 = ldg_stream(src + 8);
-  const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
-  float f[16];
+  float amax = amax16(w);
+  if (amax != amax) {   // a NaN has no code: stored as 0
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    f[2 * j] = __uint_as_float(w[j] << 16);
-    f[2 * j + 1] = __uint_as_float(w[j] & 0xffff0000u);
-  }
-  float amax = 0.0f;
-#pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    if (!(f[j] == f[j])) f[j] = 0.0f;  // a NaN has no code: stored as 0
-    amax = fmaxf(amax, fabsf(f[j]));
+    for (int j = 0; j < 8; ++j) {
+      if ((w[j] & 0x7fffu) > 0x7f80u) w[j] &= 0xffff0000u;
+      if ((w[j] & 0x7fff0000u) > 0x7f800000u) w[j] &= 0xffffu;
+    }
+    amax = amax16(w);
   }
   const float gs = p.kv ? c.v_gs : c.k_gs;
   const uint32_t scale = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
@@ -84,7 +109,8 @@ __global__ void __launch_bounds__(kThreads)
     const float r = __fdiv_rn(gs, sval);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t b = e2m1x2_rn(__fmul_rn(f[2 * j], r), __fmul_rn(f[2 * j + 1], r));
+      const uint32_t b = e2m1x2_rn(__fmul_rn(__uint_as_float(w[j] << 16), r),
+                                   __fmul_rn(__uint_as_float(w[j] & 0xffff0000u), r));
       if (j < 4) lo |= b << (8 * j);
       else hi |= b << (8 * (j - 4));
     }
@@ -95,13 +121,13 @@ __global__ void __launch_bounds__(kThreads)
   blk[L::kKeyScales + row * L::kScaleRow + p.blk] = (uint8_t)scale;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThreads)
+template <int D, bool kWide>
+__global__ void __launch_bounds__(kMaxWarps * 32)
     kv4_read_kernel(moe_kv4_cache c, const int32_t* __restrict__ slots, int n, uint16_t* k_out, uint16_t* v_out,
                     int32_t* status) {
   using L = Kv4Block<D>;
-  const Place<D> p(blockIdx.x * (size_t)kThreads + threadIdx.x, c.kv_heads);
-  if (p.t >= n) return;
+  const Place<D> p;
+  if (p.t >= n || p.h >= c.kv_heads) return;
   uint16_t* out = p.kv ? v_out : k_out;
   if (out == nullptr) return;
   out += ((size_t)p.t * c.kv_heads + p.h) * D + p.blk * 16;
@@ -131,38 +157,31 @@ __global__ void __launch_bounds__(kThreads)
       o[j] = float2_to_bf16x2_bits(e.x * s * inv, e.y * s * inv);
     }
   }
-  reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
-  reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  if constexpr (kWide) {
+    stg_v8(out, o);
+  } else {
+    reinterpret_cast<uint4*>(out)[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    reinterpret_cast<uint4*>(out)[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
 }
 
 }  // namespace
 
 moe_status launch_kv4_append(const moe_kv4_cache& c, const uint16_t* k, const uint16_t* v, long long k_stride,
                              long long v_stride, const int32_t* slots, int tokens, int32_t* status, cudaStream_t s) {
-  const bool d64 = c.head_dim == 64;
-  const size_t n = d64 ? Place<64>::threads(tokens, c.kv_heads) : Place<128>::threads(tokens, c.kv_heads);
-  const size_t ctas = (n + kThreads - 1) / kThreads;
-  if (ctas > 0x7fffffffu) return MOE_ERR_UNSUPPORTED;
-  auto kern = d64 ? kv4_append_kernel<64> : kv4_append_kernel<128>;
-  cudaError_t e = launch_ex(false, kern, dim3((unsigned)ctas), dim3(kThreads), 0, s, c, k, v, k_stride, v_stride,
-                            slots, tokens, status);
-  if (e != cudaSuccess) return cuda_ok(e);
-  count_launches(1);
-  return MOE_OK;
+  const bool wide = reinterpret_cast<uintptr_t>(k) % 32 == 0 && reinterpret_cast<uintptr_t>(v) % 32 == 0 &&
+                    k_stride % 16 == 0 && v_stride % 16 == 0;
+  auto kern = c.head_dim == 64 ? (wide ? kv4_append_kernel<64, true> : kv4_append_kernel<64, false>)
+                               : (wide ? kv4_append_kernel<128, true> : kv4_append_kernel<128, false>);
+  return launch_cache(kern, c.head_dim, c.kv_heads, tokens, s, c, k, v, k_stride, v_stride, slots, tokens, status);
 }
 
 moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, uint16_t* k_out, uint16_t* v_out,
                            int32_t* status, cudaStream_t s) {
-  const bool d64 = c.head_dim == 64;
-  const size_t threads = d64 ? Place<64>::threads(n, c.kv_heads) : Place<128>::threads(n, c.kv_heads);
-  const size_t ctas = (threads + kThreads - 1) / kThreads;
-  if (ctas > 0x7fffffffu) return MOE_ERR_UNSUPPORTED;
-  auto kern = d64 ? kv4_read_kernel<64> : kv4_read_kernel<128>;
-  cudaError_t e =
-      launch_ex(false, kern, dim3((unsigned)ctas), dim3(kThreads), 0, s, c, slots, n, k_out, v_out, status);
-  if (e != cudaSuccess) return cuda_ok(e);
-  count_launches(1);
-  return MOE_OK;
+  const bool wide = reinterpret_cast<uintptr_t>(k_out) % 32 == 0 && reinterpret_cast<uintptr_t>(v_out) % 32 == 0;
+  auto kern = c.head_dim == 64 ? (wide ? kv4_read_kernel<64, true> : kv4_read_kernel<64, false>)
+                               : (wide ? kv4_read_kernel<128, true> : kv4_read_kernel<128, false>);
+  return launch_cache(kern, c.head_dim, c.kv_heads, n, s, c, slots, n, k_out, v_out, status);
 }
 
 }  // namespace moe

@@ -12,8 +12,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxBatch = 4096;
-constexpr int kThreads = 1024;
-constexpr int kPerThread = kMaxBatch / kThreads;
+constexpr int kMaxThreads = 1024;
 
 struct Req {
   int ctx, cnt;      // cleaned lengths
@@ -21,19 +20,37 @@ struct Req {
   bool fits, bad;
 };
 
+__device__ __forceinline__ unsigned ceil_div(unsigned a, unsigned b) { return (a + b - 1) / b; }
+
+// A row of the table holds at most INT_MAX tokens, so two cleaned lengths that
+// fit it, and their sum rounded up, are below 2^32.
 __device__ __forceinline__ Req load_req(const moe_kv_step_args& a, int b) {
   Req r;
   const int ctx = a.ctx_len[b], cnt = a.new_len[b];
   r.bad = ctx < 0 || cnt < 0;
   r.ctx = max(ctx, 0);
   r.cnt = max(cnt, 0);
-  const long long P = a.page_tokens, all = (long long)r.ctx + r.cnt;
-  r.fits = all <= P * a.max_pages;
-  r.need = r.fits ? (int)((all + P - 1) / P - (r.ctx + P - 1) / P) : 0;
+  const unsigned P = a.page_tokens, all = (unsigned)r.ctx + (unsigned)r.cnt;
+  r.fits = all <= P * (unsigned)a.max_pages;
+  r.need = r.fits ? (int)(ceil_div(all, P) - ceil_div(r.ctx, P)) : 0;
   return r;
 }
 
-__device__ __forceinline__ int saturated(long long x) { return (int)min(x, (long long)0x7fffffff); }
+// Sums are capped at 2^31: past every token and page there can be.
+constexpr unsigned kCap = 1u << 31;
+__device__ __forceinline__ unsigned add_capped(unsigned a, unsigned b) { return a + min(b, kCap - a); }
+__device__ __forceinline__ int saturated(unsigned x) { return (int)min(x, 0x7fffffffu); }
+
+__device__ __forceinline__ void warp_scan(unsigned& c, unsigned& n, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned x = __shfl_up_sync(0xffffffffu, c, o), y = __shfl_up_sync(0xffffffffu, n, o);
+    if (lane >= o) {
+      c = add_capped(c, x);
+      n = add_capped(n, y);
+    }
+  }
+}
 
 // Last index i in [0, n] with arr[i] <= x, for an ascending arr with arr[0] <= x.
 __device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
@@ -50,19 +67,21 @@ __device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
 // on another CTA; the pages and the tokens are then dealt out over the grid.
 // New pages are read from the free stack, never from table entries that
 // another CTA may be writing.
-__global__ void __launch_bounds__(kThreads) kv_step_kernel(moe_kv_step_args a) {
-  __shared__ long long warp_cnt[32], warp_need[32];
-  __shared__ int cu[kMaxBatch + 1];          // tokens before each request   (both
-  __shared__ int first[kMaxBatch + 1];       // pages wanted before each request   saturated)
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// kPer requests per thread.
+template <int kPer>
+__global__ void __launch_bounds__(kMaxThreads) kv_step_kernel(moe_kv_step_args a) {
+  __shared__ unsigned warp_cnt[32], warp_need[32];
+  __shared__ int cu[kMaxThreads * kPer + 1];      // tokens before each request   (both
+  __shared__ int first[kMaxThreads * kPer + 1];   // pages wanted before each request   saturated)
+  const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.batch, P = a.page_tokens;
-  const int avail = min(max(*a.free_count, 0), a.free_capacity);
-  bool bad = *a.free_count != avail;
+  const int count = *a.free_count;
 
-  long long cnt[kPerThread], need[kPerThread], sc = 0, sn = 0;
+  unsigned cnt[kPer], need[kPer], sc = 0, sn = 0;
+  bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * kPer + i;
     cnt[i] = need[i] = 0;
     if (b < B) {
       const Req r = load_req(a, b);
@@ -70,70 +89,70 @@ __global__ void __launch_bounds__(kThreads) kv_step_kernel(moe_kv_step_args a) {
       need[i] = r.need;
       bad |= r.bad || !r.fits;
     }
-    sc += cnt[i];
-    sn += need[i];
+    sc = add_capped(sc, cnt[i]);
+    sn = add_capped(sn, need[i]);
   }
-  long long ic = sc, in = sn;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, ic, o), y = __shfl_up_sync(0xffffffffu, in, o);
-    if (lane >= o) {
-      ic += x;
-      in += y;
-    }
-  }
+  unsigned ic = sc, in = sn;
+  warp_scan(ic, in, lane);
   if (lane == 31) {
     warp_cnt[warp] = ic;
     warp_need[warp] = in;
   }
   __syncthreads();
-  long long bc = ic - sc, bn = in - sn;
-  for (int w = 0; w < warp; ++w) {
-    bc += warp_cnt[w];
-    bn += warp_need[w];
-  }
+  unsigned tc = lane < (threads >> 5) ? warp_cnt[lane] : 0, tn = lane < (threads >> 5) ? warp_need[lane] : 0;
+  warp_scan(tc, tn, lane);
+  const unsigned all_cnt = __shfl_sync(0xffffffffu, tc, 31), all_need = __shfl_sync(0xffffffffu, tn, 31);
+  tc = __shfl_sync(0xffffffffu, tc, max(warp - 1, 0));
+  tn = __shfl_sync(0xffffffffu, tn, max(warp - 1, 0));
+  // tokens and pages before this thread's requests: the warps before and the lanes before
+  unsigned bc = __shfl_up_sync(0xffffffffu, ic, 1), bn = __shfl_up_sync(0xffffffffu, in, 1);
+  bc = add_capped(warp ? tc : 0, lane ? bc : 0);
+  bn = add_capped(warp ? tn : 0, lane ? bn : 0);
 #pragma unroll
-  for (int i = 0; i < kPerThread; ++i) {
-    const int b = tid * kPerThread + i;
-    if (b <= B) {
+  for (int i = 0; i < kPer; ++i) {
+    const int b = tid * kPer + i;
+    if (b < B) {
       cu[b] = saturated(bc);
       first[b] = saturated(bn);
     }
-    bc += cnt[i];
-    bn += need[i];
+    bc = add_capped(bc, cnt[i]);
+    bn = add_capped(bn, need[i]);
   }
-  if (tid == kThreads - 1 && B == kMaxBatch) {
-    cu[B] = saturated(bc);
-    first[B] = saturated(bn);
+  if (tid == 0) {
+    cu[B] = saturated(all_cnt);
+    first[B] = saturated(all_need);
   }
-  bad |= bc > a.tokens;
+  const int avail = min(max(count, 0), a.free_capacity);
+  bad |= count != avail || all_cnt > (unsigned)a.tokens;
   __syncthreads();
 
   // requests whose inclusive sum fits the stack get their pages: a prefix
   const int granted = last_at_most(first, B, avail);   // requests [0, granted) fit
   const int taken = first[granted];
-  const int gthread = blockIdx.x * kThreads + tid, gsize = gridDim.x * kThreads;
+  const int gthread = blockIdx.x * threads + tid, gsize = gridDim.x * threads;
 
   if (blockIdx.x == 0) {
 #pragma unroll
-    for (int i = 0; i < kPerThread; ++i) {
-      const int b = tid * kPerThread + i;
+    for (int i = 0; i < kPer; ++i) {
+      const int b = tid * kPer + i;
       if (b < B) {
         const Req r = load_req(a, b);
         const bool ok = r.fits && (r.need == 0 || b < granted);
         bad |= !ok;
         a.kv_len[b] = ok ? r.ctx + r.cnt : r.ctx;
       }
-      if (b <= B) a.cu_q[b] = cu[b];
+      if (b < B) a.cu_q[b] = cu[b];
     }
-    if (tid == kThreads - 1 && B == kMaxBatch) a.cu_q[B] = cu[B];
-    if (tid == 0) *a.free_count_out = avail - taken;
+    if (tid == 0) {
+      a.cu_q[B] = cu[B];
+      *a.free_count_out = avail - taken;
+    }
     if (bad && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
   }
 
   for (int i = gthread; i < taken; i += gsize) {
     const int b = last_at_most(first, B, i);  // the last request that starts at or before page i takes it
-    const int old = (int)(((long long)max(a.ctx_len[b], 0) + P - 1) / P);
+    const int old = (int)ceil_div(max(a.ctx_len[b], 0), P);
     a.block_table[(size_t)b * a.max_pages + old + (i - first[b])] = a.free_pages[avail - 1 - i];
   }
 
@@ -142,10 +161,9 @@ __global__ void __launch_bounds__(kThreads) kv_step_kernel(moe_kv_step_args a) {
     if (t < cu[B]) {
       const int b = last_at_most(cu, B, t);
       const Req r = load_req(a, b);
-      const long long at = (long long)r.ctx + (t - cu[b]);
-      pos = saturated(at);
+      pos = saturated((unsigned)r.ctx + (unsigned)(t - cu[b]));
       if (r.fits && (r.need == 0 || b < granted)) {
-        const int page = pos / P, old = (int)(((long long)r.ctx + P - 1) / P);
+        const int page = pos / P, old = (int)ceil_div(r.ctx, P);
         const int id = page < old ? a.block_table[(size_t)b * a.max_pages + page]
                                   : a.free_pages[avail - 1 - (first[b] + page - old)];
         const long long s = (long long)id * P + (pos - page * P);
@@ -160,10 +178,15 @@ __global__ void __launch_bounds__(kThreads) kv_step_kernel(moe_kv_step_args a) {
 }  // namespace
 
 moe_status launch_kv_step(const moe_kv_step_args& a, cudaStream_t s) {
-  const int sms = sm_count();
-  const int want = (int)(((long long)a.tokens + kThreads - 1) / kThreads);
-  const int ctas = want < 1 ? 1 : (want < sms ? want : sms);
-  cudaError_t e = launch_ex(false, kv_step_kernel, dim3(ctas), dim3(kThreads), 0, s, a);
+  // A thread per request and per token of an SM's share, as far as 1024 go;
+  // small CTAs start and synchronise sooner.
+  const long long sms = sm_count(), share = (a.tokens + sms - 1) / sms;
+  const long long want = share > a.batch ? share : a.batch;
+  const int threads = want > kMaxThreads ? kMaxThreads : want < 128 ? 128 : (int)(want + 31) / 32 * 32;
+  const long long need = ((long long)a.tokens + threads - 1) / threads;
+  const int ctas = (int)(need < 1 ? 1 : need < sms ? need : sms);
+  auto k = a.batch <= threads ? kv_step_kernel<1> : kv_step_kernel<kMaxBatch / kMaxThreads>;
+  cudaError_t e = launch_ex(false, k, dim3(ctas), dim3(threads), 0, s, a);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
   return MOE_OK;
