@@ -90,8 +90,8 @@ moe_status moe_kv4_read(const moe_kv4_cache* cache, const int32_t* slots, int n,
  *   s_j = scale * q . k_j;  p = softmax(s over the visible j);  out = sum p_j v_j
  *
  * causal = 1: j <= position; window > 0 (causal only): also j > position -
- * window. A query that sees nothing gets a
- * zero row and lse = -inf. lse is the natural logarithm of sum exp(s_j).
+ * window. A query that sees nothing gets a zero row and lse = -inf. lse is
+ * the natural logarithm of sum exp(s_j).
  * Products of q with the codes are exact, sums and softmax statistics are
  * fp32; the probabilities enter the second product as f16. Results do not
  * depend on timing: the same call gives the same bits.
@@ -112,11 +112,13 @@ moe_status moe_kv4_read(const moe_kv4_cache* cache, const int32_t* slots, int n,
  * than max_q or total_q (those requests' rows are not written).
  * Errors: NULL pointers (lse may be), misaligned pool / q / out (16 bytes), a
  * q_stride that is not a multiple of 8 or smaller than a row, negative sizes,
- * max_q < 1, a non-finite scale, a window without causal -> MOE_ERR_INVALID_ARG; q_heads % kv_heads != 0,
- * head_dim or page_tokens outside the cache's limits, batch > 4096, or more
- * than 2^31 - 1 (request, head, 32-token) tiles -> MOE_ERR_UNSUPPORTED; a
- * missing, misaligned or short workspace -> MOE_ERR_WORKSPACE. batch = 0 or
- * total_q = 0 -> MOE_OK with nothing enqueued.
+ * max_q < 1, a non-finite scale, a window without causal ->
+ * MOE_ERR_INVALID_ARG; q_heads % kv_heads != 0, head_dim or page_tokens
+ * outside the cache's limits, batch > 4096, or more than 2^31 - 1 (request,
+ * head, 32 cached tokens) or (256 rows, head, 128 cached tokens) tiles, the
+ * table taken as full -> MOE_ERR_UNSUPPORTED; a missing, misaligned or short
+ * workspace -> MOE_ERR_WORKSPACE. batch = 0 or total_q = 0 -> MOE_OK with
+ * nothing enqueued.
  */
 typedef struct {
   moe_kv4_cache cache;

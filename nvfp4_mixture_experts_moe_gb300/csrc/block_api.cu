@@ -45,6 +45,7 @@ moe_status check_attention(const moe_kv4_attn_args* a) {
   const long long tiles = (row_tokens + 31) / 32;
   if (a->batch > 0 && tiles > INT_MAX / ((long long)a->batch * a->cache.kv_heads)) return MOE_ERR_UNSUPPORTED;
   if ((long long)a->total_q * (a->q_heads / a->cache.kv_heads) > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  if (kv4_prompt_units(*a) > INT_MAX) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 

@@ -44,6 +44,7 @@ moe_status launch_kv4_decode(const moe_kv4_attn_args& a, int max_rows, int* stat
                              cudaStream_t s);
 // Attention of requests with more than min_rows rows.
 size_t kv4_prompt_ws_floats(int head_dim);
+long long kv4_prompt_units(const moe_kv4_attn_args& a);   // a bound on the units of work it counts in 32 bits
 moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials, cudaStream_t s);
 
 size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a);

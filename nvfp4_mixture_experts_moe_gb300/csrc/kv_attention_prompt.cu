@@ -361,19 +361,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
   }
   __syncthreads();
   if (warp == 0) {
-    int carry = 0;
+    long long carry = 0;
     for (int base = 0; base < p.nb; base += 32) {
       const int i = base + lane;
-      int v = i < p.nb ? sm->pre[i + 1] : 0;
+      long long v = i < p.nb ? sm->pre[i + 1] : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
-        const int u = __shfl_up_sync(kFull, v, o);
+        const long long u = __shfl_up_sync(kFull, v, o);
         if (lane >= o) v += u;
       }
-      if (i < p.nb) sm->pre[i + 1] = v + carry;
+      if (i < p.nb) sm->pre[i + 1] = (int)(v + carry);
       carry += __shfl_sync(kFull, v, 31);
     }
-    if (lane == 0) sm->pre[0] = 0;
+    if (lane == 0) {
+      sm->pre[0] = 0;
+      // Past what the host checked: requests that share rows. None is served.
+      if (carry > 0x7fffffff) {
+        sm->pre[p.nb] = 0;
+        set_status(p.status, MOE_ERR_DEVICE);
+      }
+    }
   }
   __syncthreads();
   const int total = sm->pre[p.nb];
@@ -993,6 +1000,12 @@ cudaError_t launch(const PromptArgs& p, int ctas, cudaStream_t s) {
 
 size_t kv4_prompt_ws_floats(int head_dim) {
   return kCutFloats + (size_t)kKvMaxCtas * 2 * (head_dim == 64 ? kSlotFloats<64> : kSlotFloats<128>);
+}
+
+long long kv4_prompt_units(const moe_kv4_attn_args& a) {
+  const long long rows = (long long)a.total_q * (a.q_heads / a.cache.kv_heads);
+  const long long tiles = (long long)a.max_pages * a.cache.page_tokens / kTok + 2 + kSetup;
+  return (rows / kRowTile + a.batch) * a.cache.kv_heads * tiles;
 }
 
 moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials,

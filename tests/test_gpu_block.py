@@ -300,6 +300,27 @@ def test_row_tiles_of_every_kind_in_turn(D, P, window):
 
 
 @pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[(700, 300), (130, 130)], [(3000, 9), (2000, 16)], [(400, 30), (5, 2), (999, 1)]])
+def test_timeout_is_reported_and_the_next_call_is_exact(D, lens):
+    """Every bounded wait gives up at once: the call records it, drains, frees its tensor memory and returns."""
+    s = Scene(lens, 8, 2, D, 64, seed=D)
+    ws = s.cache.attention_workspace(s.total, len(lens), 8, s.max_q, s.W)
+    good = s.run(want_lse=True, ws=ws)
+    assert B().moe_get_device_status(ws) == 0
+    B().moe_debug_set(B().MOE_DEBUG_WAIT_LIMIT, 1)
+    try:
+        s.run(want_lse=True, ws=ws)
+        torch.cuda.synchronize()
+    finally:
+        B().moe_debug_set(B().MOE_DEBUG_WAIT_LIMIT, 0)
+    assert B().moe_get_device_status(ws) == B().MOE_ERR_TIMEOUT
+    assert not ws[:B().MOE_KV4_WS_ZERO].any()
+    again = s.run(want_lse=True, ws=ws)
+    assert B().moe_get_device_status(ws) == 0
+    assert all(torch.equal(x, y) for x, y in zip(good, again))
+
+
+@pytest.mark.parametrize("D", [64, 128])
 def test_long_context_is_split_and_joined(D):
     lens = [(20000, 1), (3, 1), (9999, 2)]
     s = Scene(lens, 8, 2, D, 64, seed=D)
@@ -513,3 +534,65 @@ def test_norm_of_zero_rows_and_empty_batch():
     assert not r.any() and not y.any()
     r, y = block_norm(z[:0], z[:0], w_post=w, w_pre=w)
     assert r.shape == (0, 128) and y.shape == (0, 128)
+
+
+# ----------------------------------------------------------------- all together
+
+def _example():
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decoder_blocks.py")
+    spec = importlib.util.spec_from_file_location("decoder_blocks", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    return m
+
+
+def test_example_runs_and_repeats():
+    m = _example()
+    new = [70, 0, 130]
+    tokens = torch.randint(0, m.VOCAB, (200,), generator=torch.Generator().manual_seed(2)).cuda()
+    runs = []
+    for _ in range(2):
+        s = m.Server(3, 256)
+        t = s.step(tokens, new)
+        got = [t]
+        for _ in range(3):
+            t = s.step(t, [1, 1, 1])
+            got.append(t)
+        assert int(s.tables.status) == 0 and s.length.cpu().tolist() == [73, 3, 133]
+        assert all(B().moe_get_device_status(b.attn_ws) == 0 for b in s.blocks)
+        runs.append(torch.stack(got).cpu())
+    assert torch.equal(runs[0], runs[1])
+    assert m.main() == 0
+
+
+def test_prompt_in_pieces_gives_what_the_whole_prompt_gives():
+    """The cached rows are the same bytes either way; the outputs differ by the roundings of two attention kernels
+    (bf16 outputs, f16 probabilities, scores of at most some tens: 2^-6 of the largest value each element), carried
+    through the projection, and by the bf16 roundings of the projection and of the residual."""
+    m = _example()
+    n = 150
+    x = _bf16((n, m.HIDDEN), 5).cuda()
+    h = _bf16((n, m.HIDDEN), 6).cuda()
+    outs, rows = [], []
+    for pieces in ([150], [100, 1, 1, 3, 45]):
+        s = m.Server(1, 256)
+        block_, at, hs = s.blocks[0], 0, []
+        for c in pieces:
+            t = s.tables.run(s.length, torch.tensor([c], dtype=torch.int32, device="cuda"), s.block_table, s.free_pages,
+                             s.free_count)
+            hs.append(block_.attend(h[at:at + c], x[at:at + c], t, s.block_table, c)[0])
+            slots = t.slots[:c].clone()
+            rows.append(block_.cache.read(slots))
+            s.length.copy_(t.kv_len)
+            s.free_count.copy_(t.free_count)
+            at += c
+        outs.append(torch.cat(hs).double())
+    v = torch.cat([r[1] for r in rows[1:]])
+    # a matrix product of another height may round its bf16 rows differently: rows that differ before quantisation
+    same = [torch.equal(rows[0][i], torch.cat([r[i] for r in rows[1:]])) for i in (0, 1)]
+    vmax = float(v.abs().max())
+    da = block_.w_o.double().abs().sum(dim=1) * (2.0 ** -6 if all(same) else 2.0 ** -3) * vmax
+    bar = da + 2.0 ** -7 * (outs[0] - h.double()).abs() + 2.0 ** -7 * outs[0].abs()
+    assert ((outs[0] - outs[1]).abs() <= bar).all()

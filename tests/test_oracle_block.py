@@ -166,10 +166,11 @@ def test_attention_refuses_on_the_host(L):
     for bad in (dict(q=None), dict(cu_q=None), dict(kv_len=None), dict(out=None), dict(block_table=None),
                 dict(q=264), dict(out=264), dict(q_stride=1023), dict(q_stride=512), dict(scale=float("nan")),
                 dict(scale=float("inf")), dict(window=-1), dict(window=4, causal=0), dict(batch=-1), dict(total_q=-1),
-                dict(max_q=-1), dict(max_pages=-1), dict(q_heads=0), dict(cache=_cache(B, k_gs=-1.0))):
+                dict(max_q=-1), dict(max_q=0), dict(max_pages=-1), dict(q_heads=0), dict(cache=_cache(B, k_gs=-1.0))):
         assert call(_attn(B, **bad)) == B.MOE_ERR_INVALID_ARG, bad
     for bad in (dict(q_heads=7), dict(batch=5000), dict(cache=_cache(B, head_dim=80)), dict(max_pages=1 << 25),
-                dict(max_pages=1 << 24, batch=4096), dict(total_q=1 << 30)):
+                dict(max_pages=1 << 24, batch=4096), dict(total_q=1 << 30),
+                dict(batch=1, total_q=1 << 22, max_q=1 << 22, max_pages=1 << 18)):
         assert call(_attn(B, **bad)) == B.MOE_ERR_UNSUPPORTED, bad
         assert B.moe_kv4_attention_workspace_size(_attn(B, **bad)) == 0
 
