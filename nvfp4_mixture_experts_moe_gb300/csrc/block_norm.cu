@@ -84,6 +84,7 @@ constexpr int threads_max(int V, int N) { return kMaxH / (V * N) < 1024 ? kMaxH 
 template <int V, int N, bool F32>
 __global__ void __launch_bounds__(threads_max(V, N)) block_norm_kernel(moe_block_norm_args a) {
   __shared__ float red[2][32];
+  pdl_wait();
   const int vecs = a.H / V;
   const size_t row = blockIdx.x;
   const float inv_h = 1.0f / (float)a.H;
@@ -200,6 +201,7 @@ __global__ void __launch_bounds__(512, 2) block_norm_stream_kernel(moe_block_nor
   const bool gated = has_x && a.gate != nullptr, gate_rows = gated && a.gate_stride != 0;
   const int piece = vecs * 16, stage = piece * (has_x + kRes + gate_rows);   // bytes
   const int res_at = has_x ? piece : 0, gate_at = res_at + kRes * piece;
+  pdl_wait();
   const float inv_h = 1.0f / (float)a.H;
   const Pair offset{a.w_offset, a.w_offset}, keep{a.residual_scale, a.residual_scale};
   const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
@@ -335,7 +337,7 @@ cudaError_t launch_stream(const moe_block_norm_args& a, const Stream& p, cudaStr
   static std::atomic<unsigned long long> done[2];
   cudaError_t e = opt_in_smem(k, kStreamSmem / 2, done[a.residual_f32 ? 1 : 0]);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, k, dim3(p.per_sm * sm_count()), dim3(p.threads), p.smem, s, a);
+  return launch_ex(true, k, dim3(p.per_sm * sm_count()), dim3(p.threads), p.smem, s, a);
 }
 
 template <int V, int N>
@@ -343,7 +345,7 @@ cudaError_t launch(const moe_block_norm_args& a, cudaStream_t s) {
   const int vecs = (a.H + V - 1) / V;
   const int threads = ((vecs + N - 1) / N + 31) / 32 * 32;
   auto k = a.residual_f32 ? block_norm_kernel<V, N, true> : block_norm_kernel<V, N, false>;
-  return launch_ex(false, k, dim3(a.T), dim3(threads), 0, s, a);
+  return launch_ex(true, k, dim3(a.T), dim3(threads), 0, s, a);
 }
 
 bool vector_ok(const void* p, long long stride, size_t elem) {

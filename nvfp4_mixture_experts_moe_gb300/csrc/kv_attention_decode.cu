@@ -41,6 +41,7 @@ constexpr int kChunk = 1024;       // requests of one launch
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;     // how far above m a score may be before m follows (log2)
 constexpr unsigned kFull = 0xffffffffu;
+constexpr int kAlone = 24;         // tiles that a CTA works on in the time that a join across CTAs takes
 
 struct DecodeArgs {
   moe_kv4_attn_args a;
@@ -79,9 +80,9 @@ struct Smem {
   using Sh = Shape<D, NT>;
   alignas(128) uint8_t ring[Sh::kWarps][Sh::kStages][Sh::kStageBytes];
   int pre[kChunk + 1];     // tiles (over all heads) before each request
-  int warp_sum[Sh::kWarps];
+  int warp_sum[Sh::kWarps], warp_top[Sh::kWarps];
   int start[Sh::kWarps + 1];   // the warps' ranges
-  int parked[Sh::kWarps];      // ring stage that holds a warp's first partial
+  int piece[2][Sh::kWarps];    // where a warp's last and first partial lie in the ring, in floats
   Ends ends[Sh::kWarps][2];    // the segments a warp's range begins and ends with
   int last[2];
   static_assert(Sh::kStages * Sh::kStageBytes >= Slots<D, NT>::kFloats * 4, "a warp's ring holds its last partial");
@@ -140,10 +141,13 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
-// 2^k for any k a pair of bf16 exponents can differ by, as two factors.
-__device__ __forceinline__ float2 pow2_pair(int k) {
-  const int h = k >> 1;
-  return make_float2(__int_as_float((127 + h) << 23), __int_as_float((127 + k - h) << 23));
+// 2^k for -126 <= k <= 127.
+__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
 }
 
 __device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
@@ -154,6 +158,12 @@ __device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
     else hi = mid - 1;
   }
   return lo;
+}
+
+// x * y / z, where 32 bits hold it without a 64-bit division.
+__device__ __forceinline__ int mul_div(int x, int y, int z) {
+  const unsigned long long t = (unsigned long long)x * y;
+  return t >> 32 ? (int)(t / z) : (int)((unsigned)t / (unsigned)z);
 }
 
 struct Segment {
@@ -239,12 +249,12 @@ __device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& 
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(DecodeArgs p) {
+__global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(const __grid_constant__ DecodeArgs p) {
   using Sh = Shape<D, NT>;
   using L = Kv4Block<D>;
   using Sm = Smem<D, NT>;
   constexpr int W = Sh::kWarps, S = Sh::kStages, kRows = 8 * NT, MT = D / 16;
-  constexpr int NB = Sh::kBlocks, kTile = Sh::kTile;
+  constexpr int NB = Sh::kBlocks, kTile = Sh::kTile, kPart = NT == 1 ? NB : 2;
   constexpr int kKeyWords = D / 32;     // 32-bit code words of one key row per lane
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm* sm = reinterpret_cast<Sm*>(smem_raw);
@@ -254,8 +264,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   const int P = a.cache.page_tokens, p_log = __ffs(P) - 1, Hk = a.cache.kv_heads, group = a.q_heads / Hk;
 
   // ------------------------------------------------ tiles before each request
+  pdl_wait();
   if (tid == 0) sm->pre[0] = 0;
-  int carry = 0;
+  int carry = 0, longest = 0;   // tiles of all requests; of one (request, head)
   bool bad = false;
   for (int base = 0; base < p.nb; base += Sh::kThreads) {
     const int b = base + tid;
@@ -264,21 +275,28 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       const Request r = load_request(a, p.b0 + b);
       bad |= r.bad;
       const long long rows = (long long)r.n * group;
-      if (rows > 0 && rows <= p.max_rows) tiles = ((r.kv + kTile - 1) / kTile - first_seen(a, r) / kTile) * Hk;
+      if (rows > 0 && rows <= p.max_rows) tiles = (r.kv + kTile - 1) / kTile - first_seen(a, r) / kTile;
     }
+    const int top = __reduce_max_sync(kFull, tiles);
+    tiles *= Hk;
     int incl = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int v = __shfl_up_sync(kFull, incl, o);
       if (lane >= o) incl += v;
     }
-    if (lane == 31) sm->warp_sum[warp] = incl;
+    if (lane == 31) {
+      sm->warp_sum[warp] = incl;
+      sm->warp_top[warp] = top;
+    }
     __syncthreads();
     int before = carry;
+#pragma unroll
     for (int w = 0; w < W; ++w) {
       const int v = sm->warp_sum[w];
       if (w < warp) before += v;
       carry += v;
+      longest = max(longest, sm->warp_top[w]);
     }
     if (b < p.nb) sm->pre[b + 1] = before + incl;
     __syncthreads();
@@ -300,28 +318,29 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   if (total == 0) return;
 
   // ------------------------------------------------------- this warp's range
-  const int G = min((int)gridDim.x, (total + kKvTilesPerCta - 1) / kKvTilesPerCta);
-  const int cta = blockIdx.x;
+  // Equal ranges, or a (request, head) for each CTA where that takes little
+  // more of its time than the join across CTAs would.
+  const int cta = blockIdx.x, spread = min((int)gridDim.x, (total + kKvTilesPerCta - 1) / kKvTilesPerCta);
+  const int per_cta = (total + spread - 1) / spread;
+  const bool alone = p.nb * Hk <= (int)gridDim.x && longest <= per_cta + min(kAlone, 2 * per_cta + 8);
+  const int G = alone ? p.nb * Hk : spread;
   if (cta >= G) return;
-  const int C0 = (int)((long long)total * cta / G), C1 = (int)((long long)total * (cta + 1) / G);
+  int C0 = mul_div(total, cta, G), C1 = mul_div(total, cta + 1, G);
+  if (alone) {
+    const int b = cta / Hk, per = (sm->pre[b + 1] - sm->pre[b]) / Hk;
+    C0 = sm->pre[b] + (cta - b * Hk) * per;
+    C1 = C0 + per;
+    if (per == 0) return;
+  }
   const int wact = min(W, C1 - C0);   // (a CTA's range times W fits 32 bits: it is at most 2^31 / 152 tiles)
   const int r0 = C0 + (int)((unsigned)(C1 - C0) * min(warp, wact) / (unsigned)wact);
   const int r1 = C0 + (int)((unsigned)(C1 - C0) * min(warp + 1, wact) / (unsigned)wact);
   if (lane == 0) {   // read after the barrier that follows the loop
     sm->start[warp + 1] = r1;
-    sm->parked[warp] = -1;
   }
   __syncwarp();
   if (tid == 0) sm->start[0] = C0;
   float* const slots = p.partials;
-  auto head_slot = [&](int w) {
-    return Sm::kPark ? reinterpret_cast<float*>(&sm->ring[w][sm->parked[w]][0])
-                     : slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats;
-  };
-  // clear of the parked stage: a partial that can be parked is one stage long
-  auto tail_slot = [&](int w) {
-    return reinterpret_cast<float*>(&sm->ring[w][Sm::kPark && sm->parked[w] == 0 ? 1 : 0][0]);
-  };
   auto cta_slot = [&](int c, int which) {
     return slots + ((size_t)kKvMaxCtas * W + (size_t)c * 2 + which) * Slots<D, NT>::kFloats;
   };
@@ -331,7 +350,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
     // min(P, kTile) tokens. Everything that needs a division or the tables is
     // done here, once in 32 tiles.
     const int run_log = min(p_log - 4, NB == 2 ? 1 : 2);   // log2 of the blocks of a copy
-    int d_b = 0, d_h = 0, d_tok = 0, d_valid = 0, d_s0 = 0, d_seg_end = 0, base = r0;
+    int d_b = 0, d_h = 0, d_tok = 0, d_valid = 0, d_s0 = 0, d_seg_end = 0, d_row0 = 0, d_n = 0, base = r0;
     const uint8_t* d_src[NB];
     auto describe = [&](int from) {
       base = from;
@@ -344,6 +363,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
         const Request r = load_request(a, p.b0 + s.b);
         d_b = s.b;
         d_h = s.h;
+        d_row0 = r.row0;
+        d_n = r.n;
         d_s0 = s.s0;
         d_seg_end = s.s1;
         d_tok = (first_seen(a, r) / kTile + (tile - s.s0)) * kTile;
@@ -395,6 +416,14 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
     };
 
     describe(r0);
+    // The first segment's rows are asked for before any tile, or they would
+    // wait behind all the tiles in flight.
+    {
+      const char* q = reinterpret_cast<const char*>(
+          a.q + (size_t)__shfl_sync(kFull, d_row0, 0) * a.q_stride + (size_t)__shfl_sync(kFull, d_h, 0) * group * D);
+      for (int i = __shfl_sync(kFull, d_n, 0); i > 0; --i, q += a.q_stride * 2)
+        if (lane * 128 < group * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
+    }
     __syncwarp();
     for (int i = 0; i < S; ++i) {
       if (r0 + i < r1) issue(r0 + i, i);
@@ -434,39 +463,33 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int row = nt * 8 + g8;
+          const uint16_t* q = a.q + (size_t)(rq.row0 + row / group) * a.q_stride + (h * group + row % group) * D +
+                              t4 * (D / 4);
           uint4 raw[D / 32];
           uint32_t mx = 0;
-          const bool real = row < rq.n * group;
-          if (real) {
-            const uint16_t* q = a.q + (size_t)(rq.row0 + row / group) * a.q_stride + (h * group + row % group) * D +
-                                t4 * (D / 4);
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) raw[i] = __ldg(reinterpret_cast<const uint4*>(q) + i);
-          }
+          for (int i = 0; i < D / 32; ++i)
+            raw[i] = row < rq.n * group ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
-            if (!real) raw[i] = make_uint4(0u, 0u, 0u, 0u);
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              mx = max(mx, max(finite_mag(w[j] & 0x7fffu), finite_mag((w[j] >> 16) & 0x7fffu)));
+            mx = max_u16x2(max_u16x2(mx, raw[i].x & 0x7fff7fffu), raw[i].y & 0x7fff7fffu);
+            mx = max_u16x2(max_u16x2(mx, raw[i].z & 0x7fff7fffu), raw[i].w & 0x7fff7fffu);
           }
-          mx = max(mx, __shfl_xor_sync(kFull, mx, 1));
-          mx = max(mx, __shfl_xor_sync(kFull, mx, 2));
-          const int ex = min(max((int)(mx >> 7), 1), 254);
-          float2 up = pow2_pair(141 - ex);   // largest element to [2^14, 2^15)
-          if (a.scale < 0.0f) up.x = -up.x;  // so that a larger score is a larger product
+          mx = max_u16x2(mx, __shfl_xor_sync(kFull, mx, 1));
+          mx = max_u16x2(mx, __shfl_xor_sync(kFull, mx, 2));
+          // largest element to [2^14, 2^15) (smaller only below 2^-112)
+          const int ex = min(max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15), 254);
+          const float up = a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);   // a larger score is a larger product
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-              qf[nt][2 * i + j / 2][j & 1] = pack_f16x2(__uint_as_float(w[j] << 16) * up.x * up.y,
-                                                        __uint_as_float(w[j] & 0xffff0000u) * up.x * up.y);
+              qf[nt][2 * i + j / 2][j & 1] = pack_f16x2(__uint_as_float(w[j] << 16) * up,
+                                                        __uint_as_float(w[j] & 0xffff0000u) * up);
           }
-          const float2 dn = pow2_pair(ex - 141);
           // row g8's factor, fetched as columns 2t, 2t + 1; never 0, so that a hidden score stays -inf
-          const float mine = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * dn.x * dn.y, 1e-37f);
+          const float mine = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
           mult[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
           mult[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
 #pragma unroll
@@ -489,15 +512,16 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       const uint8_t* stage = &sm->ring[warp][0][0] + slot * Sh::kStageBytes;
       const bool masked = tok0 < plain0 || tok0 + kTile > plain1 || valid != (1 << NB) - 1;
 
-      // Two copies of the tile's work, so that tiles every row sees whole (all
-      // but a request's last, for a single token) carry no mask.
-      auto work = [&](auto with_mask) {
+      // Two copies of the work on a tile (on its halves for 16 rows at D = 64:
+      // registers), so that tiles every row sees whole (all but a request's
+      // last, for a single token) carry no mask.
+      auto work = [&](auto with_mask, const uint8_t* part, int tok0, int valid) {
         constexpr bool kMask = decltype(with_mask)::value;
         // ---------------------------------------------------------- scores
-        float s[NT][NB][4];
+        float s[NT][kPart][4];
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-          const uint8_t* kb = stage + blk * L::kBytes;
+        for (int blk = 0; blk < kPart; ++blk) {
+          const uint8_t* kb = part + blk * L::kBytes;
           uint32_t kw[2][kKeyWords];   // key codes of MMA rows g8 and g8 + 8
           uint32_t ks[2][2];           // their scales, each doubled to f16x2
 #pragma unroll
@@ -555,7 +579,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
           for (int c = 0; c < 2; ++c) {
             float x = fmaxf(s[nt][0][c], s[nt][0][c + 2]);
 #pragma unroll
-            for (int blk = 1; blk < NB; ++blk) x = fmaxf(x, fmaxf(s[nt][blk][c], s[nt][blk][c + 2]));
+            for (int blk = 1; blk < kPart; ++blk) x = fmaxf(x, fmaxf(s[nt][blk][c], s[nt][blk][c + 2]));
             top[nt][c] = x * mult[nt][c];
             grow |= top[nt][c] > m[nt][c] + kSlack;
           }
@@ -579,7 +603,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
               }
             }
         }
-        uint32_t pf[NT][NB][2];
+        uint32_t pf[NT][kPart][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float m0 = m[nt][0], m1 = m[nt][1];
@@ -588,7 +612,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
             if (m1 == -INFINITY) m1 = 0.0f;
           }
 #pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
+          for (int blk = 0; blk < kPart; ++blk) {
             const float p0 = ex2(fmaf(s[nt][blk][0], mult[nt][0], -m0)), p1 = ex2(fmaf(s[nt][blk][1], mult[nt][1], -m1));
             const float p2 = ex2(fmaf(s[nt][blk][2], mult[nt][0], -m0)), p3 = ex2(fmaf(s[nt][blk][3], mult[nt][1], -m1));
             l[nt][0] += p0 + p2;
@@ -600,8 +624,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
 
         // ----------------------------------------------------------- values
 #pragma unroll
-        for (int blk = 0; blk < NB; ++blk) {
-          const uint8_t* vb = stage + blk * L::kBytes;
+        for (int blk = 0; blk < kPart; ++blk) {
+          const uint8_t* vb = part + blk * L::kBytes;
           uint32_t vw[4][MT / 4];    // value codes of MMA columns 2t, 2t + 1, 2t + 8, 2t + 9
           uint32_t sc[4];
 #pragma unroll
@@ -638,16 +662,18 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
           }
         }
       };
-      if (masked) work(std::true_type{});
-      else work(std::false_type{});
+#pragma unroll 1
+      for (int blk = 0; blk < NB; blk += kPart) {
+        const uint8_t* part = stage + blk * L::kBytes;
+        if (masked) work(std::true_type{}, part, tok0 + blk * kKvBlock, valid >> blk);
+        else work(std::false_type{}, part, tok0 + blk * kKvBlock, valid >> blk);
+      }
 
       __syncwarp();   // every lane has read the stage
       const bool seg_done = tile + 1 == seg_end, done = tile + 1 == r1;
       const bool park = Sm::kPark && seg_done && !done && !from_start;
       if (park) {
         parked = slot;
-        if (lane == 0) sm->parked[warp] = slot;
-        __syncwarp();
       } else if (next < r1) {
         // descriptors run out S tiles ahead of the tile being read
         if (next - base >= 32) describe(tile + 1);
@@ -660,7 +686,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       // --------------------------------------- the end of a range or segment
       if (seg_done || done) {
         const bool whole = from_start && seg_done;
-        float* dst = done ? tail_slot(warp) : head_slot(warp);
+        // at the range's end clear of the parked stage: a partial that can be parked is one stage long
+        const int at = (warp * S + (done ? parked == 0 : slot)) * (Sh::kStageBytes / 4);
+        float* dst = Sm::kPark || done ? reinterpret_cast<float*>(smem_raw) + at
+                                       : slots + (size_t)(cta * W + warp) * Slots<D, NT>::kFloats;
+        if (lane == 0 && !whole) sm->piece[done ? 0 : 1][warp] = at;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -712,9 +742,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
       if (inside && w0 == w1) continue;       // written when it ended
       const Request rq = {sg.row0, sg.n, 0, false};
       // warp w's piece is in its tail slot when it reaches the end of w's range
+      const bool short_last = sm->start[w1 + 1] > hi;
       auto src = [&](int i) -> const float* {
         const int w = w0 + i;
-        return sm->start[w + 1] <= hi ? tail_slot(w) : head_slot(w);
+        if (!Sm::kPark && short_last && w == w1) return slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats;
+        return reinterpret_cast<const float*>(smem_raw) + sm->piece[short_last && w == w1][w];
       };
       join<D, NT, false>(a, rq, sg.h, w1 - w0 + 1, src, warp - w0, w1 - w0 + 1,
                          inside ? nullptr : cta_slot(cta, sg.s0 < C0 ? 0 : 1));
@@ -725,7 +757,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(D
   const Ends first = sm->ends[0][0], end = sm->ends[wact - 1][1];
   const bool cut0 = first.s0 < C0, cut1 = end.s1 > C1 && end.s0 >= C0;
   if (!cut0 && !cut1) return;
-  auto cta_of = [&](int tile) { return (int)(((long long)(tile + 1) * G - 1) / total); };
+  auto cta_of = [&](int tile) {   // the last c with total * c / G <= tile
+    const unsigned long long t = (unsigned long long)(tile + 1) * G - 1;
+    return t >> 32 ? (int)(t / total) : (int)((unsigned)t / (unsigned)total);
+  };
   __syncthreads();
   if (tid < 2) {
     const bool cut = tid == 0 ? cut0 : cut1;
@@ -767,7 +802,7 @@ cudaError_t launch(const DecodeArgs& p, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = opt_in_smem(k, smem, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(false, k, dim3(ctas), dim3(Shape<D, NT>::kThreads), smem, s, p);
+  return launch_ex(true, k, dim3(ctas), dim3(Shape<D, NT>::kThreads), smem, s, p);
 }
 
 }  // namespace

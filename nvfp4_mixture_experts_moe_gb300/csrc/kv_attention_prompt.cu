@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     mbar_init(&sm->drain, 2);
     fence_barrier_init();
   }
+  pdl_wait();
   for (int b = warp; b < p.nb; b += kThreads / 32) {   // a warp per request
     const Request r = load_request(a, p.b0 + b);
     const long long rows = (long long)r.n * group;
@@ -990,7 +991,7 @@ cudaError_t launch(const PromptArgs& p, int ctas, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   cudaError_t e = opt_in_smem(k, smem, done);
   if (e != cudaSuccess) return e;
-  e = launch_ex(false, k, dim3(ctas), dim3(kThreads), smem, s, p);
+  e = launch_ex(true, k, dim3(ctas), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess) return e;
   constexpr int rows = 4 * kJoinThreads / (D / 4);
   return launch_ex(true, kv4_prompt_join_kernel<D>, dim3(ctas, kRowTile / rows), dim3(kJoinThreads), 0, s, p);

@@ -35,7 +35,7 @@ template <class K, class... A>
 moe_status launch_cache(K kernel, int D, int Hk, int tokens, cudaStream_t s, A... args) {
   const int warps = 2 * Hk < kMaxWarps ? 2 * Hk : kMaxWarps, per = 512 / D;
   const dim3 grid((unsigned)(((long long)tokens + per - 1) / per), (2 * Hk + warps - 1) / warps);
-  const cudaError_t e = launch_ex(false, kernel, grid, dim3(32, warps), 0, s, args...);
+  const cudaError_t e = launch_ex(true, kernel, grid, dim3(32, warps), 0, s, args...);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
   return MOE_OK;
@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
                       long long k_stride, long long v_stride, const int32_t* __restrict__ slots, int tokens,
                       int32_t* status) {
   using L = Kv4Block<D>;
+  pdl_wait();
   const Place<D> p;
   if (p.t >= tokens || p.h >= c.kv_heads) return;
   const uint16_t* src = p.kv ? v + (size_t)p.t * v_stride : k + (size_t)p.t * k_stride;
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     kv4_read_kernel(moe_kv4_cache c, const int32_t* __restrict__ slots, int n, uint16_t* k_out, uint16_t* v_out,
                     int32_t* status) {
   using L = Kv4Block<D>;
+  pdl_wait();
   const Place<D> p;
   if (p.t >= n || p.h >= c.kv_heads) return;
   uint16_t* out = p.kv ? v_out : k_out;

@@ -75,6 +75,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv_step_kernel(moe_kv_step_args a
   __shared__ int first[kMaxThreads * kPer + 1];   // pages wanted before each request   saturated)
   const int tid = threadIdx.x, threads = blockDim.x, lane = tid & 31, warp = tid >> 5;
   const int B = a.batch, P = a.page_tokens;
+  pdl_wait();
   const int count = *a.free_count;
 
   unsigned cnt[kPer], need[kPer], sc = 0, sn = 0;
@@ -186,7 +187,7 @@ moe_status launch_kv_step(const moe_kv_step_args& a, cudaStream_t s) {
   const long long need = ((long long)a.tokens + threads - 1) / threads;
   const int ctas = (int)(need < 1 ? 1 : need < sms ? need : sms);
   auto k = a.batch <= threads ? kv_step_kernel<1> : kv_step_kernel<kMaxBatch / kMaxThreads>;
-  cudaError_t e = launch_ex(false, k, dim3(ctas), dim3(threads), 0, s, a);
+  cudaError_t e = launch_ex(true, k, dim3(ctas), dim3(threads), 0, s, a);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
   return MOE_OK;
