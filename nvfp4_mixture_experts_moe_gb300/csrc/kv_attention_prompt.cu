@@ -446,18 +446,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         it.lo_tok = a.window > 0 ? it.hi_tok - a.window + 1 : 0;
         it.tok0 = w->first + it.t0 * kTok;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(w->row0 + token) * a.q_stride + qh * D);
-        const int qi = it.split ? 0 : i;
-        const uint32_t dst = smem_u32(&sm->q[qi][0]);
+        // A row's 16-byte chunks come by neighbouring lanes (a row per thread
+        // would fetch every sector twice and took 5 us a tile), each thread
+        // then works on its own row in shared memory. The second warpgroup of
+        // a split tile needs its rows' factors only.
+        constexpr int kChunks = D / 8, kRows = 32 / kChunks;
+        uint8_t* tile = &sm->q[i][0];
+        const uint32_t dst = smem_u32(tile);
         const bool keep = !it.split || i == 0;
-        uint4 raw[D / 8];
+        uint4 raw[kChunks];
 #pragma unroll
-        for (int v = 0; v < D / 8; ++v) raw[v] = __ldg(src + v);
+        for (int v = 0; v < kChunks; ++v)
+          raw[v] = __ldg(reinterpret_cast<const uint4*>(__shfl_sync(
+                             kFull, reinterpret_cast<unsigned long long>(src), v * kRows + lane / kChunks)) + lane % kChunks);
+#pragma unroll
+        for (int v = 0; v < kChunks; ++v)
+          sts16(dst + tile_chunk((warp & 3) * 32 + v * kRows + lane / kChunks, lane % kChunks), raw[v]);
+        __syncwarp();
         uint32_t mx = 0;
 #pragma unroll
-        for (int v = 0; v < D / 8; ++v) {
-          mx = max_u16x2(max_u16x2(mx, raw[v].x & 0x7fff7fffu), raw[v].y & 0x7fff7fffu);
-          mx = max_u16x2(max_u16x2(mx, raw[v].z & 0x7fff7fffu), raw[v].w & 0x7fff7fffu);
-          if (keep) sts16(dst + tile_chunk(it.r & 127, v), raw[v]);   // converted in place below
+        for (int v = 0; v < kChunks; ++v) {
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + tile_chunk(it.r & 127, v));
+          mx = max_u16x2(max_u16x2(mx, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+          mx = max_u16x2(max_u16x2(mx, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
         }
         const int ex = min(max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15), 254);
         // never 0, so that a hidden score stays -inf
@@ -466,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         if (keep) {
 #pragma unroll 2
           for (int v = 0; v < D / 8; ++v) {
-            uint4* chunk = reinterpret_cast<uint4*>(&sm->q[qi][tile_chunk(it.r & 127, v)]);
+            uint4* chunk = reinterpret_cast<uint4*>(tile + tile_chunk(it.r & 127, v));
             uint4 x = *chunk;
             uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -813,6 +824,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       if (++lt == w->t1) {
         next();
         lt = 0;
+        if (w->more) {   // the next row tile's queries
+          const int r0 = w->q * kRowTile, r1 = min(r0 + kRowTile, w->n * group);
+          for (int token = r0 / group + lane; token * group < r1; token += 32)
+            asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                             a.q + (size_t)(w->row0 + token) * a.q_stride + (size_t)w->h * group * D),
+                         "r"((uint32_t)(group * D * 2))
+                         : "memory");
+        }
       }
     }
   } else {
