@@ -427,8 +427,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     };
     // The warpgroup's next row tile: its rows as f16 into shared memory, the
     // largest element in [2^14, 2^15) (smaller only below 2^-112).
+    bool passed = true;                            // the walk stands behind the row tile entered last
+    auto pass = [&]() {
+      if (!passed) next();
+      passed = true;
+    };
     auto enter = [&](Item& it) {
-      for (; w->more; next()) {
+      for (pass(); w->more; next()) {
         const int q0 = w->q * kRowTile, rows = min(kRowTile, w->n * group - q0), h = w->h, kv = w->kv;
         it.split = rows <= kSplitRows;
         it.jt0 = jt;
@@ -475,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         it.c = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
         const float up = a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);   // larger scores stay larger products
         if (keep) {
-#pragma unroll 2
+#pragma unroll 4
           for (int v = 0; v < D / 8; ++v) {
             uint4* chunk = reinterpret_cast<uint4*>(tile + tile_chunk(it.r & 127, v));
             uint4 x = *chunk;
@@ -489,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           __syncwarp();
           if (lane == 0) mbar_arrive(it.split ? &sm->q_split : &sm->q_full[i]);
         }
-        next();
+        passed = false;
         return true;
       }
       return false;
@@ -693,6 +698,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&sm->p_full[i]);
+        pass();                                    // while S is under way
       }
       if (!ok) break;
       l = unpack2(l2).x + unpack2(l2).y;
