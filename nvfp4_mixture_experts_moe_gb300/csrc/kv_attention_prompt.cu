@@ -13,16 +13,21 @@
 //   tiles, keys K-major, values with d contiguous (MN-major); a scout warp has
 //   looked up the pages and sent the blocks on their way into L2 before;
 // * two threads issue S_i = Q_i K^T and O_i += P_i V, each for one of the two row
-//   tiles i, so one tile's softmax runs under the other's MMAs; P_i (f16, read
-//   from tensor memory) lies in S_i's columns;
-// * eight softmax warps, one row per thread: one pass over S in 32-column
-//   pieces with the running maximum of the tiles before; a piece that exceeds
-//   it by more than 8 rescales O, the sum and the pieces of P already written
-//   (rare after the first tiles), so S is read from tensor memory once.
+//   tiles i, in halves of 64 tokens, so that the softmax of one half runs under
+//   the MMAs of the other; P_i (f16, read from tensor memory) lies in the
+//   columns of the half of S_i it came from;
+// * eight softmax warps, one row per thread: a half of S is read once; a half
+//   whose maximum exceeds the running one by more than 8 rescales O and the
+//   sum first, when the halves before have gone into O (rare after the first).
 //
 // What bounds it: per 128 tokens and 256 rows at D = 128 the MMAs take 2048
-// cycles and the exponentials 1024; the softmax and dequant warps' instructions
-// are about as many as the schedulers issue in that time.
+// cycles at their rate (2560 with S in halves: Q is read twice), the
+// exponentials 1024, and the softmax and dequant warps issue some 2000
+// instructions per scheduler. A KV tile takes 4300: the tensor pipe is given
+// work nearly all of that time and both softmax warps of a scheduler are
+// active in two thirds of it. A 16384-token prompt of 32 heads over 8 runs at
+// 1130 TFLOP/s (58 % of the measured matrix rate), one of 4096 tokens at 845:
+// there each CTA enters and leaves three to five row tiles, 4-5 us each.
 //
 // Work is dealt out by KV tiles: all (request, head, row tile, KV tile) in
 // order, one equal range per CTA. A row tile that two or more CTAs cut leaves
@@ -39,6 +44,7 @@ namespace {
 using namespace tc;
 
 constexpr int kTok = 128;              // cached tokens of a tile
+constexpr int kHalfTok = kTok / 2;     // and of a half: what softmax and MMA warps hand each other
 constexpr int kRowTile = 256;          // query rows of an item: two M = 128 tiles
 constexpr int kChunk = 1024;           // requests of one launch
 constexpr int kSoftWarps = 8, kDeqWarps = 4;
@@ -224,9 +230,8 @@ struct Smem {
   alignas(1024) uint8_t q[2][kTile];
   alignas(1024) uint8_t kv[2][2][kTile];   // keys, values: two stages each
   uint64_t q_full[2], q_split;         // rows of the streams' row tiles, of a split one
-  uint64_t s_full[2], o_full[2];
-  uint64_t p_full[2];
-  uint64_t turn[2];                    // stream i may issue
+  uint64_t s_full[2][2], p_full[2][2];   // [stream][half]
+  uint64_t pv_done[2], o_full[2];      // a half of a stream has gone into O, the last one of a row tile
   uint64_t kv_full[2][2], kv_empty[2][2];   // [keys or values][stage]
   uint64_t x_full, x_empty;            // the second warpgroup's half of a split row tile
   uint64_t drain;
@@ -324,9 +329,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     sm->abort = 0;
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->q_full[i], 4);
-      mbar_init(&sm->s_full[i], 1);
-      mbar_init(&sm->p_full[i], 4);
-      mbar_init(&sm->turn[i], 1);
+      for (int h = 0; h < 2; ++h) {
+        mbar_init(&sm->s_full[i][h], 1);
+        mbar_init(&sm->p_full[i][h], 4);
+      }
+      mbar_init(&sm->pv_done[i], 1);
       mbar_init(&sm->o_full[i], 1);
       mbar_init(&sm->kv_full[0][i], kDeqWarps);
       mbar_init(&sm->kv_full[1][i], kDeqWarps);
@@ -459,15 +466,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         uint8_t* tile = &sm->q[i][0];
         const uint32_t dst = smem_u32(tile);
         const bool keep = !it.split || i == 0;
-        uint4 raw[kChunks];
+        // (With no tile of its own it goes straight to its empty half, which it
+        // writes over these rows: nothing to fetch.)
+        if (keep || it.nt > 1) {
+          uint4 raw[kChunks];
 #pragma unroll
-        for (int v = 0; v < kChunks; ++v)
-          raw[v] = __ldg(reinterpret_cast<const uint4*>(__shfl_sync(
-                             kFull, reinterpret_cast<unsigned long long>(src), v * kRows + lane / kChunks)) + lane % kChunks);
+          for (int v = 0; v < kChunks; ++v)
+            raw[v] = __ldg(reinterpret_cast<const uint4*>(__shfl_sync(
+                               kFull, reinterpret_cast<unsigned long long>(src), v * kRows + lane / kChunks)) + lane % kChunks);
 #pragma unroll
-        for (int v = 0; v < kChunks; ++v)
-          sts16(dst + tile_chunk((warp & 3) * 32 + v * kRows + lane / kChunks, lane % kChunks), raw[v]);
-        __syncwarp();
+          for (int v = 0; v < kChunks; ++v)
+            sts16(dst + tile_chunk((warp & 3) * 32 + v * kRows + lane / kChunks, lane % kChunks), raw[v]);
+          __syncwarp();
+        }
         uint32_t mx = 0;
 #pragma unroll
         for (int v = 0; v < kChunks; ++v) {
@@ -612,93 +623,87 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       uint64_t l2 = pack2(0.0f, 0.0f);
       const uint64_t c2 = pack2(c, c);
       const int step = it.split ? 2 : 1, begin = it.split ? i : 0;
-      for (int t = begin; t < nt; t += step, ++js) {
-        if (!(ok = wait(&sm->s_full[i], js))) break;
-        tc_fence_after();
-        const int tok0 = it.tok0 + t * kTok;
-        const uint64_t hole = *reinterpret_cast<const volatile uint64_t*>(sm->hole[(it.jt0 + t) & 3]);
-        const bool masked = __any_sync(kFull, tok0 + kTok - 1 > hi_tok || tok0 < lo_tok) || hole != 0;
-        // one 32-column piece of S, read while the piece before is worked on
-        auto work = [&](uint32_t (&sr)[32], int piece) {
-          if (masked) {   // bit e: column e is seen
-            const int hi = hi_tok - tok0 - 32 * piece, lo = lo_tok - tok0 - 32 * piece;
-            uint32_t see = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
-            see &= lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
-            const uint32_t bad = (uint32_t)(hole >> (16 * piece));
-            if (bad & 0xffu) see &= 0xffff0000u;
-            if (bad & 0xff00u) see &= 0x0000ffffu;
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (!(see >> e & 1u)) sr[e] = 0xff800000u;
-          }
-          float u0 = __uint_as_float(sr[0]), u1 = __uint_as_float(sr[1]);
-#pragma unroll
-          for (int e = 2; e < 30; e += 4) {
-            u0 = max3(u0, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
-            u1 = max3(u1, __uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
-          }
-          const float top = max3(u0, u1, fmaxf(__uint_as_float(sr[30]), __uint_as_float(sr[31]))) * c;
-          if (__any_sync(kFull, top > m + kSlack)) {
-            const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
-            m = mn;
-            const float2 l = unpack2(l2);
-            l2 = pack2(l.x * f, l.y * f);
-            if (t > begin) {
+      for (int t = begin; t < nt && ok; t += step, ++js) {
 #pragma unroll 1
-              for (int cc = 0; cc < D; cc += 16) {
-                uint32_t o[16];
-                tmem_ld16(o_t + cc, o);
-                tmem_ld_wait();
+        for (int half = 0; half < 2; ++half) {
+          if (!(ok = wait(&sm->s_full[i][half], js))) break;
+          tc_fence_after();
+          const int tok0 = it.tok0 + t * kTok + half * kHalfTok;
+          const uint32_t hole = *reinterpret_cast<const volatile uint32_t*>(&sm->hole[(it.jt0 + t) & 3][4 * half]);
+          const bool masked = __any_sync(kFull, tok0 + kHalfTok - 1 > hi_tok || tok0 < lo_tok) || hole != 0;
+          if (active) {
+            const uint32_t s_h = s_t + kHalfTok * half;
+            uint32_t s0[32], s1[32];
+            tmem_ld32(s_h, s0);
+            tmem_ld32(s_h + 32, s1);
+            ld_wait(s0);
+            ld_wait(s1);
+            // 32 columns: those that are not seen go to -inf; the largest score
+            auto peak = [&](uint32_t (&sr)[32], int piece) {
+              if (masked) {   // bit e: column e is seen
+                const int hi = hi_tok - tok0 - 32 * piece, lo = lo_tok - tok0 - 32 * piece;
+                uint32_t see = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
+                see &= lo <= 0 ? ~0u : lo > 31 ? 0u : ~0u << lo;
+                const uint32_t bad = hole >> (16 * piece);
+                if (bad & 0xffu) see &= 0xffff0000u;
+                if (bad & 0xff00u) see &= 0x0000ffffu;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                tmem_st16(o_t + cc, o);
+                for (int e = 0; e < 32; ++e)
+                  if (!(see >> e & 1u)) sr[e] = 0xff800000u;
+              }
+              float u0 = __uint_as_float(sr[0]), u1 = __uint_as_float(sr[1]);
+#pragma unroll
+              for (int e = 2; e < 30; e += 4) {
+                u0 = max3(u0, __uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+                u1 = max3(u1, __uint_as_float(sr[e + 2]), __uint_as_float(sr[e + 3]));
+              }
+              return max3(u0, u1, fmaxf(__uint_as_float(sr[30]), __uint_as_float(sr[31])));
+            };
+            const float p0 = peak(s0, 0), p1 = peak(s1, 1), top = fmaxf(p0, p1) * c;
+            if (__any_sync(kFull, top > m + kSlack)) {
+              const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+              m = mn;
+              const float2 l = unpack2(l2);
+              l2 = pack2(l.x * f, l.y * f);
+              if (t > begin || half > 0) {   // O holds the halves before, once the last of them has gone in
+                if (!(ok = wait(&sm->pv_done[i], 2 * js + half - 1))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int cc = 0; cc < D; cc += 16) {
+                  uint32_t o[16];
+                  tmem_ld16(o_t + cc, o);
+                  tmem_ld_wait();
+#pragma unroll
+                  for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                  tmem_st16(o_t + cc, o);
+                }
               }
             }
-            const uint32_t f2 = pack_f16x2(f, f);   // pieces of P already stored: one more f16 rounding
-#pragma unroll 1
-            for (int pp = 0; pp < piece; ++pp) {
-              uint32_t o[16];
-              tmem_ld16(s_t + 16 * pp, o);
-              tmem_ld_wait();
+            const float mu = m == -INFINITY ? 0.0f : m;
+            const uint64_t m2 = pack2(-mu, -mu);
+            auto exps = [&](const uint32_t (&sr)[32], int piece) {
+              uint32_t pk[16];
+              uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
-              for (int e = 0; e < 16; ++e) o[e] = hmul2_u32(o[e], f2);
-              tmem_st16(s_t + 16 * pp, o);
-            }
+              for (int e = 0; e < 16; ++e) {
+                const float2 y = unpack2(fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), c2, m2));
+                const float p0 = ex2(y.x), p1 = ex2(y.y);
+                sum = add2(sum, pack2(p0, p1));
+                pk[e] = pack_f16x2(p0, p1);
+              }
+              l2 = add2(l2, sum);
+              tmem_st16(s_h + 16 * piece, pk);   // P takes the columns of S, read by then
+            };
+            exps(s0, 0);
+            exps(s1, 1);
             tmem_st_wait();
+            tc_fence_before();
           }
-          const float mu = m == -INFINITY ? 0.0f : m;
-          const uint64_t m2 = pack2(-mu, -mu);
-          uint32_t pk[16];
-          uint64_t sum = pack2(0.0f, 0.0f);
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 y = unpack2(fma2(pack2(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1])), c2, m2));
-            const float p0 = ex2(y.x), p1 = ex2(y.y);
-            sum = add2(sum, pack2(p0, p1));
-            pk[e] = pack_f16x2(p0, p1);
-          }
-          l2 = add2(l2, sum);
-          tmem_st16(s_t + 16 * piece, pk);
-        };
-        // piece x of P goes to columns [16 x, 16 x + 16) of S, read by then
-        if (active) {
-          uint32_t s0[32], s1[32];
-          tmem_ld32(s_t, s0);
-#pragma unroll 1
-          for (int half = 0; half < 2; ++half) {
-            ld_wait(s0);
-            tmem_ld32(s_t + 64 * half + 32, s1);
-            work(s0, 2 * half);
-            ld_wait(s1);
-            if (half == 0) tmem_ld32(s_t + 64, s0);
-            work(s1, 2 * half + 1);
-          }
-          tmem_st_wait();
-          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sm->p_full[i][half]);
+          pass();                                  // while S is under way
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->p_full[i]);
-        pass();                                    // while S is under way
+        if (!ok) break;
       }
       if (!ok) break;
       l = unpack2(l2).x + unpack2(l2).y;
@@ -842,7 +847,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     }
   } else {
     // ------------------------------------------------------------------ MMA
-    const uint32_t id_s = idesc_f16(128, 128, 0);
+    const uint32_t id_s = idesc_f16(128, kHalfTok, 0);
     const uint32_t id_o = idesc_f16(128, D, 0) | (1u << 16);   // values: N (d) contiguous
     constexpr int kHalf = 128 * 128;
     const uint64_t qd = smem_desc(smem_u32(&sm->q[0][0]), 16, 1024, kSwizzle128B);
@@ -851,13 +856,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     const uint64_t vd = smem_desc(smem_u32(&sm->kv[1][0][0]), kHalf, 1024, kSwizzle128B);
     // Two streams of (S, softmax, O), a warp each: the item's row tiles, or a
     // split tile's even and odd KV tiles. Both walk every KV tile and give its
-    // shared memory back, used or not. With two row tiles the warps take turns
-    // with their batches (P V of a KV tile, then the next S): a stream's MMAs
-    // run while the other's softmax does (interleaved freely they fall into
-    // step, and the tensor core idles through both softmaxes at once), and a
-    // warp's waits hide behind the other's batch.
+    // shared memory back, used or not. A stream's two halves of S take turns:
+    // while the softmax works on one, P V of the other and the S that follows
+    // in its columns are under way (whole tiles of S left either the softmax
+    // or the MMAs waiting: 8 % more time at D = 64, the same at 128, where
+    // S with N = 64 reads as much of Q as with N = 128).
     const int i = warp - kMmaWarp;
-    int j0 = 0, n_q = 0, n_qs = 0, n_p = 0, n_turn = 0;
+    int j0 = 0, n_q = 0, n_qs = 0, n_p = 0;
     bool ok = true;
     Cut cut = {0, 0, 0, 0, 0, {0, 0, 0}};
     while (w->more && ok) {
@@ -866,7 +871,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         const int lo = cta_of(w->x + kSetup), hi = cta_of(w->x + kSetup + w->tiles - 1);
         cut = {w->row0, rows, w->h, w->q, hi - lo + 1, {0, 0, 0}};
       }
-      const bool split = rows <= kSplitRows, two = rows > 128, idle = i == 1 && !split && !two;
+      const bool split = rows <= kSplitRows, idle = i == 1 && !split && rows <= 128;
       const int ahead = split ? 2 : 1;
       if (split) ok = wait(&sm->q_split, n_qs++);
       else if (!idle) ok = wait(&sm->q_full[i], n_q++);
@@ -877,42 +882,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         const int jv = j0 + t, sv = jv & 1, jk = jv + ahead, sk = jk & 1;
         if (t >= 0 && !(ok = wait(&sm->kv_full[1][sv], jv >> 1))) break;
         if (more && !(ok = wait(&sm->kv_full[0][sk], jk >> 1))) break;
-        if (t >= 0 && mine && !(ok = wait(&sm->p_full[i], n_p++))) break;
-        // stream 0 starts, so its first turn needs no hand-over
-        if (two && !(ok = wait(&sm->turn[i], i ? n_turn : n_turn - 1))) break;
-        n_turn += two;
-        tc_fence_after();
-        if (lane == 0) {
-          if (t >= 0) {
-            if (mine) {
-              const uint64_t vb = vd + (uint64_t)((sv * Sm::kTile) >> 4);
+#pragma unroll 1
+        for (int half = 0; half < 2; ++half) {
+          if (t >= 0 && mine && !(ok = wait(&sm->p_full[i][half], n_p))) break;
+          tc_fence_after();
+          if (lane == 0) {
+            const uint32_t s_h = tmem + 128 * i + kHalfTok * half;
+            if (t >= 0) {
+              if (mine) {
+                const uint64_t vb = vd + (uint64_t)((sv * Sm::kTile + half * (kHalfTok / 16) * 2048) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kTok / 16; ++kk)
-                mma_f16_tmem_a(tmem + 256 + 128 * i, tmem + 128 * i + 8 * kk, vb + kk * (2048 >> 4), id_o,
-                               t >= ahead || kk > 0);
-              tc_commit(&sm->kv_empty[1][sv]);
-              if (!more) tc_commit(&sm->o_full[i]);
-            } else {
-              mbar_arrive(&sm->kv_empty[1][sv]);
-            }
-          }
-          if (more) {
-            if (mine) {
-              const uint64_t kb = kd + (uint64_t)((sk * Sm::kTile) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
-                mma_f16(tmem + 128 * i, qa + off, kb + off, id_s, kk != 0);
+                for (int kk = 0; kk < kHalfTok / 16; ++kk)
+                  mma_f16_tmem_a(tmem + 256 + 128 * i, s_h + 8 * kk, vb + kk * (2048 >> 4), id_o,
+                                 t >= ahead || half > 0 || kk > 0);
+                tc_commit(&sm->pv_done[i]);
+                if (half) tc_commit(&sm->kv_empty[1][sv]);
+                if (half && !more) tc_commit(&sm->o_full[i]);
+              } else if (half) {
+                mbar_arrive(&sm->kv_empty[1][sv]);
               }
-              tc_commit(&sm->s_full[i]);
-              tc_commit(&sm->kv_empty[0][sk]);
-            } else {
-              mbar_arrive(&sm->kv_empty[0][sk]);
+            }
+            if (more) {
+              if (mine) {
+                const uint64_t kb = kd + (uint64_t)((sk * Sm::kTile + half * kHalfTok * 128) >> 4);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                  const uint64_t off = (uint64_t)(((kk >> 2) * kHalf + (kk & 3) * 32) >> 4);
+                  mma_f16(s_h, qa + off, kb + off, id_s, kk != 0);
+                }
+                tc_commit(&sm->s_full[i][half]);
+                if (half) tc_commit(&sm->kv_empty[0][sk]);
+              } else if (half) {
+                mbar_arrive(&sm->kv_empty[0][sk]);
+              }
             }
           }
-          if (two) mbar_arrive(&sm->turn[i ^ 1]);
+          __syncwarp();
         }
-        __syncwarp();
+        if (!ok) break;
+        n_p += t >= 0 && mine;
         if (t == -ahead) next();   // the next piece, while there is time
       }
       j0 += nt;
