@@ -1,7 +1,14 @@
 // Norm after a block, its gate, the residual and the norm before the next
 // block: n = x rsqrt(mean x^2 + eps) w_post, r = a residual + b gate n, out =
-// r rsqrt(mean r^2 + eps) w_pre, one CTA per row, the row in registers
-// between the two reductions, so every array is read or written once.
+// r rsqrt(mean r^2 + eps) w_pre, the row in registers between the two
+// reductions, so every array is read or written once.
+//
+// What bounds it: bytes. Few rows run one CTA each (8 x 4096: 2.5 us, launch
+// and one trip to memory), many rows the stream kernel: 16384 x 7168 with a
+// gate per row in 192 us, 6.1 TB/s or 90 % of the measured copy rate. One CTA
+// per row took 303 us there: its loads stop while its reductions run, and
+// with scalar arithmetic the instructions alone (370 per warp and 256
+// elements, now 150) took 240.
 #include "kernels.cuh"
 #include "kv4.cuh"
 #include "tc_ptx.cuh"

@@ -5,6 +5,11 @@
 // an inclusive scan S_b over the requests decides who gets pages (S_b <=
 // free_count), the i-th page taken is free[free_count - 1 - i], and a token
 // at position p of request b goes to table[b][p / P] * P + p % P.
+//
+// What bounds it: latency. Lengths, then a table entry, then the store are
+// three trips to memory of some 0.7 us; the scan between them is shuffles
+// and one exchange between warps. 64 decoding requests take 2.8 us, 500
+// requests with 31,000 new tokens 4.2 (replayed).
 #include "kernels.cuh"
 #include "kv4.cuh"
 
