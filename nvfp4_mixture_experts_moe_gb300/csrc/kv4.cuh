@@ -27,6 +27,13 @@ __device__ __forceinline__ size_t kv4_block_offset(int64_t page, int head, int k
   return (((size_t)page * kv_heads + head) * blocks_per_page + block) * (size_t)block_bytes;
 }
 
+// (x * y + z) / d of non-negative numbers; a 64-bit division (some 300
+// cycles) only where 32 bits do not hold the product.
+__device__ __forceinline__ int mul_div(int x, int y, int d, int z = 0) {
+  const unsigned long long t = (unsigned long long)x * y + z;
+  return t >> 32 ? (int)(t / d) : (int)((unsigned)t / (unsigned)d);
+}
+
 moe_status launch_kv4_append(const moe_kv4_cache& c, const uint16_t* k, const uint16_t* v, long long k_stride,
                              long long v_stride, const int32_t* slots, int tokens, int32_t* status, cudaStream_t s);
 moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, uint16_t* k_out, uint16_t* v_out,

@@ -173,12 +173,6 @@ __device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
   return lo;
 }
 
-// x * y / z, where 32 bits hold it without a 64-bit division.
-__device__ __forceinline__ int mul_div(int x, int y, int z) {
-  const unsigned long long t = (unsigned long long)x * y;
-  return t >> 32 ? (int)(t / z) : (int)((unsigned)t / (unsigned)z);
-}
-
 struct Segment {
   int b, h;      // request (within the launch), key/value head
   int s0, s1;    // its tiles
@@ -770,10 +764,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
   const Ends first = sm->ends[0][0], end = sm->ends[wact - 1][1];
   const bool cut0 = first.s0 < C0, cut1 = end.s1 > C1 && end.s0 >= C0;
   if (!cut0 && !cut1) return;
-  auto cta_of = [&](int tile) {   // the last c with total * c / G <= tile
-    const unsigned long long t = (unsigned long long)(tile + 1) * G - 1;
-    return t >> 32 ? (int)(t / total) : (int)((unsigned)t / (unsigned)total);
-  };
+  auto cta_of = [&](int tile) { return mul_div(tile + 1, G, total, -1); };   // the last c with total * c / G <= tile
   __syncthreads();
   if (tid < 2) {
     const bool cut = tid == 0 ? cut0 : cut1;

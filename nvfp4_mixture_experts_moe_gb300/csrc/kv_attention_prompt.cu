@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     if (tid == 0) p.cuts[cta].n = 0;
     return;
   }
-  const Range rg = {&p, sm->pre, (int)((long long)total * cta / G), (int)((long long)total * (cta + 1) / G)};
+  const Range rg = {&p, sm->pre, mul_div(total, cta, G), mul_div(total, cta + 1, G)};
   if (warp == kMmaWarp) tmem_alloc(&sm->tmem_base, kTmemCols);
   Walk* const w = &sm->walk[warp];
   walk_begin(rg, w);
@@ -415,7 +415,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     if (lane == 0) walk_next(rg, w);
     __syncwarp();
   };
-  auto cta_of = [&](int unit) { return (int)(((long long)(unit + 1) * G - 1) / total); };
+  auto cta_of = [&](int unit) { return mul_div(unit + 1, G, total, -1); };
 
   if (warp < kSoftWarps) {
     // ------------------------------------------------------------- softmax
@@ -434,13 +434,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     };
     // The warpgroup's next row tile: its rows as f16 into shared memory, the
     // largest element in [2^14, 2^15) (smaller only below 2^-112).
-    bool passed = true;                            // the walk stands behind the row tile entered last
-    auto pass = [&]() {
-      if (!passed) next();
-      passed = true;
+    bool moved = true;                             // the walk stands behind the row tile entered last
+    auto move_on = [&]() {
+      if (!moved) next();
+      moved = true;
     };
     auto enter = [&](Item& it) {
-      for (pass(); w->more; next()) {
+      for (move_on(); w->more; next()) {
         const int q0 = w->q * kRowTile, rows = min(kRowTile, w->n * group - q0), h = w->h, kv = w->kv;
         it.split = rows <= kSplitRows;
         it.jt0 = jt;
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           __syncwarp();
           if (lane == 0) mbar_arrive(it.split ? &sm->q_split : &sm->q_full[i]);
         }
-        passed = false;
+        moved = false;
         return true;
       }
       return false;
@@ -701,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(&sm->p_full[i][half]);
-          pass();                                  // while S is under way
+          move_on();                               // while S is under way
         }
         if (!ok) break;
       }

@@ -350,6 +350,20 @@ def test_rows_that_see_nothing(n):
     assert not out[:n - 2].any() and bool(torch.isneginf(lse[:n - 2]).all()) and not out[n:2 * n].any()
 
 
+@pytest.mark.parametrize("qheads,heads,D,n", [(8, 2, 64, 1), (8, 2, 128, 4), (8, 2, 64, 9), (8, 2, 128, 40)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_bad_query_spoils_its_own_row_only(qheads, heads, D, n, value):
+    s = Scene([(300, n), (90, n)], qheads, heads, D, 32, seed=n)
+    good, lse = s.run(want_lse=True)
+    q = s.q.clone().cuda()
+    row, head = n, 3                       # the second request's first token
+    q[row, head, 5] = value
+    out, lse2 = s.run(q=q, want_lse=True)
+    keep = torch.ones(s.total, qheads, dtype=torch.bool, device="cuda")
+    keep[row, head] = False
+    assert torch.equal(out[keep], good[keep]) and torch.equal(lse2[keep], lse[keep])
+
+
 @pytest.mark.parametrize("n,scale", [(1, 1.0), (1, 1e-3), (50, 2.0)])
 def test_extreme_scores(n, scale):
     """Scores of hundreds (one token takes all) and scores near zero (all tokens alike)."""
