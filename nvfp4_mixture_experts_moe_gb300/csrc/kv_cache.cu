@@ -47,13 +47,25 @@ moe_status launch_cache(K kernel, int D, int Hk, int tokens, cudaStream_t s, A..
   return MOE_OK;
 }
 
-// The block and the row within it of a slot; false for a slot outside the pool.
+// The cache with what every thread would work out again: page_tokens is a
+// power of two, and the division that decodes is one by a constant.
+struct Cache {
+  uint8_t* pool;
+  int slots, heads, page_log;
+  float gs[2], inv_gs[2];   // keys, values
+};
+
+Cache cache_of(const moe_kv4_cache& c) {
+  return {static_cast<uint8_t*>(c.pool), c.num_pages * c.page_tokens, c.kv_heads, __builtin_ctz(c.page_tokens),
+          {c.k_gs, c.v_gs}, {1.0f / c.k_gs, 1.0f / c.v_gs}};
+}
+
+// The block of a slot, and the row within it.
 template <int D>
-__device__ __forceinline__ uint8_t* slot_row(const moe_kv4_cache& c, int slot, int h, int& row) {
-  const int page = slot / c.page_tokens, pos = slot - page * c.page_tokens;
-  row = pos % kKvBlock;
-  return static_cast<uint8_t*>(c.pool) +
-         kv4_block_offset(page, h, c.kv_heads, c.page_tokens / kKvBlock, pos / kKvBlock, Kv4Block<D>::kBytes);
+__device__ __forceinline__ uint8_t* slot_row(const Cache& c, int slot, int h, int& row) {
+  const int page = slot >> c.page_log, block = (slot & ((1 << c.page_log) - 1)) / kKvBlock;
+  row = slot % kKvBlock;
+  return c.pool + kv4_block_offset(page, h, c.heads, (1 << c.page_log) / kKvBlock, block, Kv4Block<D>::kBytes);
 }
 
 // 32 bytes of one thread: one load of a sector where the address allows it.
@@ -83,19 +95,19 @@ __device__ __forceinline__ float amax16(const uint32_t (&w)[8]) {
 
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kMaxWarps * 32)
-    kv4_append_kernel(moe_kv4_cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
+    kv4_append_kernel(Cache c, const uint16_t* __restrict__ k, const uint16_t* __restrict__ v,
                       long long k_stride, long long v_stride, const int32_t* __restrict__ slots, int tokens,
                       int32_t* status) {
   using L = Kv4Block<D>;
   pdl_wait();
   const Place<D> p;
-  if (p.t >= tokens || p.h >= c.kv_heads) return;
+  if (p.t >= tokens || p.h >= c.heads) return;
   const uint16_t* src = p.kv ? v + (size_t)p.t * v_stride : k + (size_t)p.t * k_stride;
   uint32_t w[8];
   load_32<kWide>(src + (size_t)p.h * D + p.blk * 16, w);   // next to the slot's load, not behind it
   const int slot = slots[p.t];
   if (slot < 0) return;
-  if (slot >= c.num_pages * c.page_tokens) {
+  if (slot >= c.slots) {
     if (status != nullptr) *status = MOE_ERR_DEVICE;
     return;
   }
@@ -108,7 +120,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     }
     amax = amax16(w);
   }
-  const float gs = p.kv ? c.v_gs : c.k_gs;
+  const float gs = c.gs[p.kv];
   const uint32_t scale = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
   const float sval = e4m3_decode(scale);
   uint32_t lo = 0, hi = 0;
@@ -130,25 +142,25 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
 
 template <int D, bool kWide>
 __global__ void __launch_bounds__(kMaxWarps * 32)
-    kv4_read_kernel(moe_kv4_cache c, const int32_t* __restrict__ slots, int n, uint16_t* k_out, uint16_t* v_out,
+    kv4_read_kernel(Cache c, const int32_t* __restrict__ slots, int n, uint16_t* k_out, uint16_t* v_out,
                     int32_t* status) {
   using L = Kv4Block<D>;
   pdl_wait();
   const Place<D> p;
-  if (p.t >= n || p.h >= c.kv_heads) return;
+  if (p.t >= n || p.h >= c.heads) return;
   uint16_t* out = p.kv ? v_out : k_out;
   if (out == nullptr) return;
-  out += ((size_t)p.t * c.kv_heads + p.h) * D + p.blk * 16;
+  out += ((size_t)p.t * c.heads + p.h) * D + p.blk * 16;
   const int slot = slots[p.t];
   uint32_t o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-  if (slot >= c.num_pages * c.page_tokens) {
+  if (slot >= c.slots) {
     if (status != nullptr) *status = MOE_ERR_DEVICE;
   } else if (slot >= 0) {
     int row;
     const uint8_t* blk = slot_row<D>(c, slot, p.h, row) + (p.kv ? L::kValueCodes : 0);
     const uint2 codes = *reinterpret_cast<const uint2*>(blk + row * L::kCodeRow + p.blk * 8);
     const float s = e4m3_decode(blk[L::kKeyScales + row * L::kScaleRow + p.blk]);
-    const float inv = 1.0f / (p.kv ? c.v_gs : c.k_gs);
+    const float inv = c.inv_gs[p.kv];
     uint32_t h2[8];
     uint32_t a[4], b[4];
     cvt_e2m1x8_f16(codes.x, a);
@@ -181,7 +193,7 @@ moe_status launch_kv4_append(const moe_kv4_cache& c, const uint16_t* k, const ui
                     k_stride % 16 == 0 && v_stride % 16 == 0;
   auto kern = c.head_dim == 64 ? (wide ? kv4_append_kernel<64, true> : kv4_append_kernel<64, false>)
                                : (wide ? kv4_append_kernel<128, true> : kv4_append_kernel<128, false>);
-  return launch_cache(kern, c.head_dim, c.kv_heads, tokens, s, c, k, v, k_stride, v_stride, slots, tokens, status);
+  return launch_cache(kern, c.head_dim, c.kv_heads, tokens, s, cache_of(c), k, v, k_stride, v_stride, slots, tokens, status);
 }
 
 moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, uint16_t* k_out, uint16_t* v_out,
@@ -189,7 +201,7 @@ moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, 
   const bool wide = reinterpret_cast<uintptr_t>(k_out) % 32 == 0 && reinterpret_cast<uintptr_t>(v_out) % 32 == 0;
   auto kern = c.head_dim == 64 ? (wide ? kv4_read_kernel<64, true> : kv4_read_kernel<64, false>)
                                : (wide ? kv4_read_kernel<128, true> : kv4_read_kernel<128, false>);
-  return launch_cache(kern, c.head_dim, c.kv_heads, n, s, c, slots, n, k_out, v_out, status);
+  return launch_cache(kern, c.head_dim, c.kv_heads, n, s, cache_of(c), slots, n, k_out, v_out, status);
 }
 
 }  // namespace moe
