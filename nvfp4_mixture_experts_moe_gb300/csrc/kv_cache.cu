@@ -8,9 +8,10 @@
 //
 // What bounds them: bytes for prompts, latency for a decode step (1.8 us a
 // launch, replayed). 8191 tokens of 8 heads x 128 written and read back move
-// 86 MB in 20 us, 4.3 TB/s or 63 % of the measured copy rate; a third of the
-// rest is launches, and a thread's three dependent steps (slot, row, store)
-// leave the other two kernels of 10 us too short to fill their ends.
+// 86 MB in 19.2 us, 4.5 TB/s or 66 % of the measured copy rate; at 10 us
+// each the two kernels spend some 3 us on launch, first loads and last
+// stores, and issue instructions in two of three cycles (200 a warp and 512
+// elements: three correctly rounded divisions among them).
 #include "kernels.cuh"
 #include "kv4.cuh"
 
