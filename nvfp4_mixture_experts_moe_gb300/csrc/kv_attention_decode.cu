@@ -432,6 +432,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
         if (lane * 128 < group * D * 2) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + lane * 128));
     }
     __syncwarp();
+#pragma unroll 1
     for (int i = 0; i < S; ++i) {
       if (r0 + i < r1) issue(r0 + i, i);
       cp_async_commit();
