@@ -4,8 +4,8 @@
 // reductions, so every array is read or written once.
 //
 // What bounds it: bytes. Few rows run one CTA each (8 x 4096: 2.5 us, launch
-// and one trip to memory), many rows the stream kernel: 16384 x 7168 with a
-// gate per row in 192 us, 6.1 TB/s or 90 % of the measured copy rate. One CTA
+// and one trip to memory), more rows than CTAs the stream kernel: 16384 x 7168
+// with a gate per row in 192 us, 6.1 TB/s or 90 % of the measured copy rate. One CTA
 // per row took 303 us there: its loads stop while its reductions run, and
 // with scalar arithmetic the instructions alone (370 per warp and 256
 // elements, now 150) took 240.
@@ -319,32 +319,250 @@ __global__ void __launch_bounds__(512, 2) block_norm_stream_kernel(moe_block_nor
   }
 }
 
+// Rows that are not whole vectors at 16-byte addresses (odd H, offset or odd
+// strided views): the stream kernel with every array's aligned 16-byte
+// granules copied to shared memory as they lie, read there at any offset, and
+// the outputs packed there before they go out as granules. 16384 x 5003 with a
+// gate per row takes 252 us, 616 an element at a time (128 as whole vectors:
+// the rest is five barriers a row and twice the shared-memory reads).
+__device__ __forceinline__ Vec load_at(const uint8_t* smem, int off) {   // 16 bytes at an even offset
+  const uint4* p = reinterpret_cast<const uint4*>(smem) + (off >> 4);
+  const uint4 a = p[0], b = p[1];
+  uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  if (off & 8) {
+#pragma unroll
+    for (int j = 0; j < 6; ++j) w[j] = w[j + 2];
+  }
+  if (off & 4) {
+#pragma unroll
+    for (int j = 0; j < 5; ++j) w[j] = w[j + 1];
+  }
+  if (off & 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = __funnelshift_r(w[j], w[j + 1], 16);
+  }
+  return {w[0], w[1], w[2], w[3]};
+}
+
+__device__ __forceinline__ int lead_of(const void* p) { return (int)(reinterpret_cast<uintptr_t>(p) & 15); }
+
+// The granules that hold `bytes` bytes at src. One that reaches past an end of
+// the array (`first`: src is its start, `last`: src + bytes its end) is copied
+// element by element; elsewhere its other bytes lie between rows.
+__device__ __forceinline__ void fetch_bytes(uint8_t* dst, const uint8_t* src, int bytes, bool first, bool last) {
+  const int lead = lead_of(src), n = (lead + bytes + 15) >> 4;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    const int at = 16 * c - lead;   // in the row
+    if ((at >= 0 || !first) && (at + 16 <= bytes || !last)) {
+      tc::cp_async_16(static_cast<uint32_t>(__cvta_generic_to_shared(dst + 16 * c)), src + at, 16);
+    } else {
+      for (int e = 0; e < 16; e += 2)
+        if (at + e >= 0 && at + e < bytes)
+          *reinterpret_cast<uint16_t*>(dst + 16 * c + e) = *reinterpret_cast<const uint16_t*>(src + at + e);
+    }
+  }
+}
+
+// `bytes` bytes from packed + 16 on to dst, as granules but for the ends.
+__device__ __forceinline__ void store_bytes(uint8_t* dst, const uint8_t* packed, int bytes) {
+  const int lead = lead_of(dst), n = (lead + bytes + 15) >> 4;
+  for (int c = threadIdx.x; c < n; c += blockDim.x) {
+    const int at = 16 * c - lead;
+    const Vec v = load_at(packed, 16 + at);
+    if (at >= 0 && at + 16 <= bytes) {
+      *reinterpret_cast<uint4*>(dst + at) = make_uint4(v.w[0], v.w[1], v.w[2], v.w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 16; e += 2)
+        if (at + e >= 0 && at + e < bytes)
+          *reinterpret_cast<uint16_t*>(dst + at + e) = (uint16_t)(v.w[e / 4] >> (e % 4 * 8));
+    }
+  }
+}
+
+// Vector c of a weight of H elements, zeros past its end.
+__device__ __forceinline__ Vec weight_at(const uint16_t* p, int c, int H) {
+  if (8 * c + 8 <= H && lead_of(p) == 0) return vec16(p, c);
+  Vec v = {{0u, 0u, 0u, 0u}};
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    if (8 * c + e < H) v.w[e / 2] |= (uint32_t)p[8 * c + e] << (e % 2 * 16);
+  return v;
+}
+
+template <int N, bool F32>
+__global__ void __launch_bounds__(512, 2) block_norm_shift_kernel(moe_block_norm_args a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][32];
+  constexpr int kElem = F32 ? 4 : 2;
+  pdl_wait();
+  const int H = a.H, vecs = (H + 7) / 8, threads = blockDim.x, tid = threadIdx.x;
+  const bool has_x = a.x != nullptr, post = has_x && a.w_post != nullptr, pre = a.w_pre != nullptr;
+  const bool gated = has_x && a.gate != nullptr, gate_rows = gated && a.gate_stride != 0;
+  // a row's granules, one more for its offset and one that load_at() touches
+  const int piece = (vecs + 2) * 16, res_piece = (vecs * (F32 ? 2 : 1) + 2) * 16;
+  const int res_at = has_x ? piece : 0, gate_at = res_at + res_piece, stage = gate_at + (gate_rows ? piece : 0);
+  uint8_t* const packed = ring + kStages * stage;   // r on its way out, then y
+  const float inv_h = 1.0f / (float)H;
+  const Pair offset{a.w_offset, a.w_offset}, keep{a.residual_scale, a.residual_scale};
+  auto x_row = [&](long long row) { return reinterpret_cast<const uint8_t*>(a.x + row * a.x_stride); };
+  auto g_row = [&](long long row) { return reinterpret_cast<const uint8_t*>(a.gate + row * a.gate_stride); };
+  auto r_row = [&](long long row) { return static_cast<const uint8_t*>(a.residual) + row * a.residual_stride * kElem; };
+  auto fetch = [&](long long row, int slot) {
+    if (row < a.T) {
+      uint8_t* at = ring + slot * stage;
+      const bool first = row == 0, last = row == a.T - 1;
+      if (has_x) fetch_bytes(at, x_row(row), 2 * H, first, last);
+      fetch_bytes(at + res_at, r_row(row), kElem * H, first, last);
+      if (gate_rows) fetch_bytes(at + gate_at, g_row(row), 2 * H, first, last);
+    }
+    tc::cp_async_commit();
+  };
+  for (int s = 0; s < kStages; ++s) fetch(blockIdx.x + (long long)s * gridDim.x, s);
+  int slot = 0;
+  for (long long row = blockIdx.x; row < a.T; row += gridDim.x) {
+    tc::cp_async_wait<kStages - 1>();
+    __syncthreads();   // a vector's granules are copies of two threads
+    const uint8_t* at = ring + slot * stage;
+    const int x_lead = lead_of(x_row(row)), r_lead = lead_of(r_row(row)), g_lead = lead_of(g_row(row));
+    // the row's last vector may go on into what lies behind it
+    auto tail = [&](int c, int j, Pair v) {
+      return Pair{8 * c + 2 * j < H ? v.x : 0.0f, 8 * c + 2 * j + 1 < H ? v.y : 0.0f};
+    };
+    Pair r[N][4];
+    float scale = a.branch_scale;
+    if (post) {
+      Pair s{0.0f, 0.0f};
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = i * threads + tid;
+        if (c < vecs) {
+          const Vec x = load_at(at, 16 * c + x_lead);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const Pair v = tail(c, j, bf16_pair(x.w[j]));
+            s = fma2(v, v, s);
+          }
+        }
+      }
+      scale *= rsqrtf(cta_sum(s.x + s.y, red[0]) * inv_h + a.eps);
+    }
+    Pair s{0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int c = i * threads + tid;
+      if (c < vecs) {
+        if constexpr (F32) {
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const Vec q = load_at(at + res_at, 32 * c + 16 * k + r_lead);
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+              r[i][2 * k + j] = mul2(keep, {__uint_as_float(q.w[2 * j]), __uint_as_float(q.w[2 * j + 1])});
+          }
+        } else {
+          const Vec q = load_at(at + res_at, 16 * c + r_lead);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) r[i][j] = mul2(keep, bf16_pair(q.w[j]));
+        }
+        if (has_x) {
+          Pair n[4];
+          const Vec x = load_at(at, 16 * c + x_lead);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) n[j] = mul2(bf16_pair(x.w[j]), {scale, scale});
+          if (post) {
+            const Vec w = weight_at(a.w_post, c, H);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) n[j] = mul2(n[j], add2(bf16_pair(w.w[j]), offset));
+          }
+          if (gated) {
+            const Vec g = gate_rows ? load_at(at + gate_at, 16 * c + g_lead) : weight_at(a.gate, c, H);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[i][j] = fma2(n[j], bf16_pair(g.w[j]), r[i][j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r[i][j] = add2(n[j], r[i][j]);
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          r[i][j] = tail(c, j, r[i][j]);
+          s = fma2(r[i][j], r[i][j], s);
+        }
+        const float v[8] = {r[i][0].x, r[i][0].y, r[i][1].x, r[i][1].y, r[i][2].x, r[i][2].y, r[i][3].x, r[i][3].y};
+        store_res<8, F32>(packed + 16, (size_t)c * 8, v);
+      }
+    }
+    const float sum = cta_sum(s.x + s.y, red[1]);   // and all have read the slot and written their part of r
+    fetch(row + (long long)kStages * gridDim.x, slot);
+    slot = slot + 1 == kStages ? 0 : slot + 1;
+    if (a.residual_out != nullptr)
+      store_bytes(static_cast<uint8_t*>(a.residual_out) + row * H * kElem, packed, kElem * H);
+    if (pre) {
+      __syncthreads();
+      const float inv = rsqrtf(sum * inv_h + a.eps);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const int c = i * threads + tid;
+        if (c < vecs) {
+          const Vec w = weight_at(a.w_pre, c, H);
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const Pair y = mul2(mul2(r[i][j], {inv, inv}), add2(bf16_pair(w.w[j]), offset));
+            v[2 * j] = y.x, v[2 * j + 1] = y.y;
+          }
+          store_bf16<8>(reinterpret_cast<uint16_t*>(packed + 16) + c * 8, v);
+        }
+      }
+      __syncthreads();
+      store_bytes(reinterpret_cast<uint8_t*>(a.out + row * H), packed, 2 * H);
+    }
+  }
+}
+
 // Some 1024 threads an SM, in CTAs of a row each: at 64 registers more would
 // not fit, and two rows a CTA keep 64 KiB or more in flight at every H.
 struct Stream {
   int n, threads, per_sm;
   size_t smem;
-  bool ok;
 };
-Stream plan_stream(const moe_block_norm_args& a) {
+Stream plan_stream(const moe_block_norm_args& a, bool shift) {
   Stream p;
-  const int vecs = a.H / 8;
+  const size_t vecs = (a.H + 7) / 8, more = shift ? 2 : 0;   // granules of an array
+  const size_t x = a.x ? vecs + more : 0, res = vecs * (a.residual_f32 ? 2 : 1) + more,
+               gate = a.gate && a.gate_stride ? vecs + more : 0;
   p.n = a.H <= 4096 ? 1 : 2;
-  p.threads = ((vecs + p.n - 1) / p.n + 31) / 32 * 32;
+  p.threads = (int)((vecs + p.n - 1) / p.n + 31) / 32 * 32;
+  p.smem = 16 * (kStages * (x + res + gate) + (shift ? res : 0));
   p.per_sm = 1024 / p.threads < 8 ? 1024 / p.threads : 8;
-  p.smem = (size_t)kStages * a.H * ((a.x ? 2 : 0) + (a.residual_f32 ? 4 : 2) + (a.gate && a.gate_stride ? 2 : 0));
-  // Every CTA has a row to fetch while it works on one.
-  p.ok = a.H <= 8192 && p.per_sm * (p.smem + 1024) <= kStreamSmem && a.T > 2 * p.per_sm * sm_count();
+  const int fit = (int)(kStreamSmem / (p.smem + 1024));
+  if (shift && p.per_sm > fit) p.per_sm = fit;
+  if (a.H > 8192 || fit < p.per_sm) p.per_sm = 0;
   return p;
 }
 
-template <int N>
-cudaError_t launch_stream(const moe_block_norm_args& a, const Stream& p, cudaStream_t s) {
-  auto k = a.residual_f32 ? block_norm_stream_kernel<N, true> : block_norm_stream_kernel<N, false>;
-  static std::atomic<unsigned long long> done[2];
-  cudaError_t e = opt_in_smem(k, kStreamSmem / 2, done[a.residual_f32 ? 1 : 0]);
+template <class K>
+cudaError_t launch_stream(K k, const moe_block_norm_args& a, const Stream& p, std::atomic<unsigned long long>& done,
+                          cudaStream_t s) {
+  cudaError_t e = opt_in_smem(k, kStreamSmem, done);
   if (e != cudaSuccess) return e;
-  return launch_ex(true, k, dim3(p.per_sm * sm_count()), dim3(p.threads), p.smem, s, a);
+  const int ctas = p.per_sm * sm_count();
+  return launch_ex(true, k, dim3(a.T < ctas ? a.T : ctas), dim3(p.threads), p.smem, s, a);
+}
+
+template <int N>
+cudaError_t launch_vectors(const moe_block_norm_args& a, const Stream& p, cudaStream_t s) {
+  static std::atomic<unsigned long long> done[2];
+  return a.residual_f32 ? launch_stream(block_norm_stream_kernel<N, true>, a, p, done[1], s)
+                        : launch_stream(block_norm_stream_kernel<N, false>, a, p, done[0], s);
+}
+
+template <int N>
+cudaError_t launch_shift(const moe_block_norm_args& a, const Stream& p, cudaStream_t s) {
+  static std::atomic<unsigned long long> done[2];
+  return a.residual_f32 ? launch_stream(block_norm_shift_kernel<N, true>, a, p, done[1], s)
+                        : launch_stream(block_norm_shift_kernel<N, false>, a, p, done[0], s);
 }
 
 template <int V, int N>
@@ -366,11 +584,16 @@ moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s) {
   const bool vec = a.H % 8 == 0 && vector_ok(a.x, a.x_stride, 2) && vector_ok(a.gate, a.gate_stride, 2) &&
                    vector_ok(a.residual, a.residual_stride, re) && vector_ok(a.residual_out, a.H, re) &&
                    vector_ok(a.out, a.H, 2) && vector_ok(a.w_post, 0, 2) && vector_ok(a.w_pre, 0, 2);
+  const Stream p = plan_stream(a, !vec);
   cudaError_t e;
   if (!vec) {
-    e = a.H <= 4096 ? launch<1, 4>(a, s) : launch<1, 16>(a, s);
-  } else if (const Stream p = plan_stream(a); p.ok) {
-    e = p.n == 1 ? launch_stream<1>(a, p, s) : launch_stream<2>(a, p, s);
+    // Short rows an element at a time (16384 x 333: 24 us, 33 by granules;
+    // x 1001: 68 and 52).
+    if (a.H <= 512) e = launch<1, 4>(a, s);
+    else if (p.per_sm > 0) e = p.n == 1 ? launch_shift<1>(a, p, s) : launch_shift<2>(a, p, s);
+    else e = launch<1, 16>(a, s);
+  } else if (p.per_sm > 0 && a.T > p.per_sm * sm_count()) {   // more rows than CTAs
+    e = p.n == 1 ? launch_vectors<1>(a, p, s) : launch_vectors<2>(a, p, s);
   } else if (a.H <= 8192 && a.T <= 304) {
     e = launch<8, 1>(a, s);   // few rows: as many threads per row as it has vectors
   } else {

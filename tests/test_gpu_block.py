@@ -515,7 +515,11 @@ def test_norm_matches_the_oracle(T, H, gate, f32, post, pre, has_x):
     (5000, 8, "token", True, True, True, True), (3001, 520, "channel", False, True, True, True),
     (1000, 2880, None, True, True, False, True), (997, 4096, "token", True, False, True, True),
     (913, 4104, "token", False, True, True, True), (640, 7168, "channel", False, True, True, True),
-    (2000, 1536, None, False, False, True, False), (700, 8192, None, True, True, True, True)])
+    (2000, 1536, None, False, False, True, False), (700, 8192, None, True, True, True, True),
+    (3000, 77, "token", True, True, True, True), (1300, 2047, "token", False, True, True, True),
+    (700, 5003, None, True, True, True, True), (400, 7001, "channel", False, False, True, True),
+    (650, 4099, "token", True, True, False, True), (9, 8191, "token", True, True, True, True),
+    (2500, 9, None, False, True, True, False), (1000, 130, "channel", True, False, False, True)])
 def test_norm_of_many_rows_matches_the_oracle(T, H, gate, f32, post, pre, has_x):
     test_norm_matches_the_oracle(T, H, gate, f32, post, pre, has_x)
 
@@ -538,6 +542,37 @@ def test_norm_strides_alignment_in_place_and_stream():
     r, y = block_norm(x, inplace, w_post=w, w_pre=w, residual_out=inplace, stream=other)
     torch.cuda.synchronize()
     assert r is inplace and torch.equal(r, ref) and torch.equal(y, refy)
+
+
+@pytest.mark.parametrize("H,gap,at", [(130, 7, 1), (1001, 0, 0), (4095, 3, 5), (520, 1, 3), (64, 9, 2)])
+@pytest.mark.parametrize("f32", [False, True])
+def test_norm_of_rows_at_any_offset(H, gap, at, f32):
+    """Views into wider arrays, 2- or 4-byte aligned, the neighbours' bytes NaN; in place; against the copy's result."""
+    from nvfp4_mixture_experts_moe_gb300 import block_norm
+    T = 700
+    wide = torch.full((T * (H + gap) + at + 3,), float("nan"), dtype=torch.bfloat16, device="cuda")
+    view = lambda: wide.clone()[at:at + T * (H + gap)].view(T, H + gap)[:, :H]   # noqa: E731
+    x, g = view(), view()
+    x[:], g[:] = _bf16((T, H), 1).cuda(), _bf16((T, H), 2).cuda()
+    res = torch.randn(T, H, generator=torch.Generator().manual_seed(3)).cuda()
+    wr = torch.full((T * (H + gap) + at,), float("nan"), dtype=torch.float32 if f32 else torch.bfloat16, device="cuda")
+    r = wr[at:].view(T, H + gap)[:, :H]
+    r[:] = res
+    before = wr.clone()
+    w = _bf16((H + 1,), 4).cuda()[1:]
+    got, y = block_norm(x, r, gate=g, w_post=w, w_pre=w, eps=1e-5)
+    n = [t.double().cpu().numpy() for t in (x, r, g, w)]
+    rr, ry = block.block_norm(n[0], n[1], n[2], n[3], n[3], 1.0, 1.0, 1e-5, 0.0)
+    size = np.abs(n[1]) + np.abs(rr - n[1])
+    err = np.abs(got.double().cpu().numpy() - rr)
+    assert (err <= 2.0 ** -18 * size + (0 if f32 else 2.0 ** -8) * np.abs(rr)).all(), err.max()
+    gain = np.abs(ry) / np.maximum(np.abs(rr), 1e-30)
+    err = np.abs(y.double().cpu().numpy() - ry)
+    assert (err <= 2.0 ** -18 * (size * gain + np.abs(ry)) + 2.0 ** -8 * np.abs(ry) + 1e-30).all(), err.max()
+    assert torch.equal(wr.view(torch.int32 if f32 else torch.int16), before.view(torch.int32 if f32 else torch.int16))
+    if gap == 0 and at == 0:
+        r2, y2 = block_norm(x, r, gate=g, w_post=w, w_pre=w, eps=1e-5, residual_out=r)
+        assert r2 is r and torch.equal(r, got) and torch.equal(y2, y)
 
 
 def test_norm_of_zero_rows_and_empty_batch():
