@@ -943,77 +943,60 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
 }
 
 // Joins the partials of the row tiles that several CTAs cut: block (c, part)
-// takes kJoinRows rows of the tile that begins in CTA c. Four elements per
-// thread, all their loads in flight together: the partials lie in L2.
-constexpr int kJoinThreads = 256;
+// takes 1024 elements of the tile that begins in CTA c. Four elements per
+// thread, the loads of kJoinParts partials in flight together: a short tile
+// over a long context is in up to all CTAs' pieces, one trip to L2 after the
+// other (64 rows over 16000 tokens: 53 us the call with two partials and four
+// times the elements in flight, 36 so).
+constexpr int kJoinThreads = 256, kJoinParts = 4;
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) kv4_prompt_join_kernel(const __grid_constant__ PromptArgs p) {
-  constexpr int kX = 4, kB = 2;   // elements and partials in flight per thread
-  constexpr int kRows = kX * kJoinThreads / (D / 4);
   pdl_wait();
   const Cut cut = p.cuts[blockIdx.x];
-  const int x0 = blockIdx.y * kRows * (D / 4) + threadIdx.x, end = cut.rows * (D / 4);
-  if (cut.n < 2 || x0 >= end) return;
+  const int x = blockIdx.y * kJoinThreads + threadIdx.x;
+  if (cut.n < 2 || x >= cut.rows * (D / 4)) return;
   const moe_kv4_attn_args& a = p.a;
   const int group = a.q_heads / a.cache.kv_heads;
-  float m[kX], l[kX];
-  float4 o[kX];
-#pragma unroll
-  for (int y = 0; y < kX; ++y) {
-    m[y] = -INFINITY;
-    l[y] = 0.0f;
-    o[y] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  }
+  float m = -INFINITY, l = 0.0f;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll 1
-  for (int c = 0; c < cut.n; c += kB) {
-    float2 ml[kX][kB];
-    float4 v[kX][kB];
+  for (int c = 0; c < cut.n; c += kJoinParts) {
+    float2 ml[kJoinParts];
+    float4 v[kJoinParts];
+    float mn = m;
 #pragma unroll
-    for (int y = 0; y < kX; ++y)
-#pragma unroll
-      for (int k = 0; k < kB; ++k) {
-        const int x = x0 + y * kJoinThreads;
-        ml[y][k] = make_float2(-INFINITY, 0.0f);
-        v[y][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (c + k < cut.n && x < end) {   // the tile's first CTA holds it at its end, the others at their start
-          const float* src = p.partials + ((size_t)(blockIdx.x + c + k) * 2 + (c + k == 0 ? 1 : 0)) * kSlotFloats<D>;
-          ml[y][k] = *reinterpret_cast<const float2*>(src + kRowTile * D + 2 * (x / (D / 4)));
-          v[y][k] = reinterpret_cast<const float4*>(src)[x];
-        }
-      }
-#pragma unroll
-    for (int y = 0; y < kX; ++y) {
-      float mn = m[y];
-#pragma unroll
-      for (int k = 0; k < kB; ++k) mn = fmaxf(mn, ml[y][k].x);
-      const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m[y] - mu);   // 0 from -inf
-      m[y] = mn;
-      l[y] *= f;
-      o[y] = make_float4(o[y].x * f, o[y].y * f, o[y].z * f, o[y].w * f);
-#pragma unroll
-      for (int k = 0; k < kB; ++k) {
-        const float g = ex2(ml[y][k].x - mu);
-        l[y] += g * ml[y][k].y;
-        o[y].x += g * v[y][k].x;
-        o[y].y += g * v[y][k].y;
-        o[y].z += g * v[y][k].z;
-        o[y].w += g * v[y][k].w;
+    for (int k = 0; k < kJoinParts; ++k) {
+      ml[k] = make_float2(-INFINITY, 0.0f);
+      v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      if (c + k < cut.n) {   // the tile's first CTA holds it at its end, the others at their start
+        const float* src = p.partials + ((size_t)(blockIdx.x + c + k) * 2 + (c + k == 0 ? 1 : 0)) * kSlotFloats<D>;
+        ml[k] = *reinterpret_cast<const float2*>(src + kRowTile * D + 2 * (x / (D / 4)));
+        v[k] = reinterpret_cast<const float4*>(src)[x];
       }
     }
-  }
 #pragma unroll
-  for (int y = 0; y < kX; ++y) {
-    const int x = x0 + y * kJoinThreads;
-    if (x >= end) break;
-    const int row = x / (D / 4), d = x % (D / 4) * 4, rr = cut.q * kRowTile + row, token = rr / group;
-    const float inv = 1.0f / (l[y] * a.cache.v_gs);
-    const size_t at = (size_t)(cut.row0 + token) * a.q_heads + cut.h * group + rr - token * group;
-    *reinterpret_cast<uint2*>(a.out + at * D + d) =
-        l[y] > 0.0f ? make_uint2(float2_to_bf16x2_bits(o[y].x * inv, o[y].y * inv),
-                                 float2_to_bf16x2_bits(o[y].z * inv, o[y].w * inv))
-                    : make_uint2(0u, 0u);
-    if (d == 0 && a.lse != nullptr) a.lse[at] = l[y] > 0.0f ? m[y] * kLn2 + logf(l[y]) : -INFINITY;
+    for (int k = 0; k < kJoinParts; ++k) mn = fmaxf(mn, ml[k].x);
+    const float mu = mn == -INFINITY ? 0.0f : mn, f = ex2(m - mu);   // 0 from -inf
+    m = mn;
+    l *= f;
+    o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+    for (int k = 0; k < kJoinParts; ++k) {
+      const float g = ex2(ml[k].x - mu);
+      l += g * ml[k].y;
+      o.x += g * v[k].x;
+      o.y += g * v[k].y;
+      o.z += g * v[k].z;
+      o.w += g * v[k].w;
+    }
   }
+  const int row = x / (D / 4), d = x % (D / 4) * 4, rr = cut.q * kRowTile + row, token = rr / group;
+  const float inv = 1.0f / (l * a.cache.v_gs);
+  const size_t at = (size_t)(cut.row0 + token) * a.q_heads + cut.h * group + rr - token * group;
+  *reinterpret_cast<uint2*>(a.out + at * D + d) =
+      l > 0.0f ? make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv))
+               : make_uint2(0u, 0u);
+  if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
 }
 
 template <int D>
@@ -1026,7 +1009,7 @@ cudaError_t launch(const PromptArgs& p, int ctas, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   e = launch_ex(true, k, dim3(ctas), dim3(kThreads), smem, s, p);
   if (e != cudaSuccess) return e;
-  constexpr int rows = 4 * kJoinThreads / (D / 4);
+  constexpr int rows = kJoinThreads / (D / 4);
   return launch_ex(true, kv4_prompt_join_kernel<D>, dim3(ctas, kRowTile / rows), dim3(kJoinThreads), 0, s, p);
 }
 
