@@ -54,7 +54,10 @@ constexpr int kChunk = 1024;       // requests of one launch
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kSlack = 8.0f;     // how far above m a score may be before m follows (log2)
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kAlone = 24;         // tiles that a CTA works on in the time that a join across CTAs takes
+// Tiles that a CTA works on in the time that a join across CTAs takes, where
+// every SM has a range (which then begin and end anywhere); half where not.
+// 1 x 1000 tokens of 8 heads: 10.4 us cut, 11.7 whole; 8 x 1000: 12.4 and 11.7.
+constexpr int kAlone = 24;
 
 struct DecodeArgs {
   moe_kv4_attn_args a;
@@ -328,8 +331,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
   // Equal ranges, or a (request, head) for each CTA where that takes little
   // more of its time than the join across CTAs would.
   const int cta = blockIdx.x, spread = min((int)gridDim.x, (total + kKvTilesPerCta - 1) / kKvTilesPerCta);
-  const int per_cta = (total + spread - 1) / spread;
-  const bool alone = p.nb * Hk <= (int)gridDim.x && longest <= per_cta + min(kAlone, 2 * per_cta + 8);
+  const int per_cta = (total + spread - 1) / spread, more = spread == (int)gridDim.x ? kAlone : kAlone / 2;
+  const bool alone = p.nb * Hk <= (int)gridDim.x && longest <= per_cta + more;
   const int G = alone ? p.nb * Hk : spread;
   if (cta >= G) return;
   int C0 = mul_div(total, cta, G), C1 = mul_div(total, cta + 1, G);
