@@ -191,70 +191,133 @@ __device__ __forceinline__ Segment segment_of(const int* pre, int nb, int heads,
   return s;
 }
 
-// Joins n partials of a (request, head), in their order: warp `mine` of `warps`
-// takes its share of the columns, a lane one row. To the output (normalised
-// bf16, lse) or, dst given, to a partial.
-template <bool OTHER_CTAS, class T>
-__device__ __forceinline__ T load_partial(const T* p) {
-  if constexpr (OTHER_CTAS) return __ldcg(p);
-  else return *p;
-}
+// The running join of partials of one row's four neighbouring columns.
+struct Joined {
+  float m = -INFINITY, l = 0.0f;
+  float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+  template <int N>
+  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N]) {
+    float mn = m;
+#pragma unroll
+    for (int j = 0; j < N; ++j) mn = fmaxf(mn, ml[j].x);
+    const float mu = mn == -INFINITY ? 0.0f : mn, w0 = ex2(m - mu);   // 0 from -inf
+    m = mn;
+    l *= w0;
+    o.x *= w0;
+    o.y *= w0;
+    o.z *= w0;
+    o.w *= w0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const float w = ex2(ml[j].x - mu);
+      l += w * ml[j].y;
+      o.x += w * v[j].x;
+      o.y += w * v[j].y;
+      o.z += w * v[j].z;
+      o.w += w * v[j].w;
+    }
+  }
+  // normalised bf16 and lse
+  __device__ __forceinline__ void write(const moe_kv4_attn_args& a, const Request& rq, int h, int group, int row, int D,
+                                        int d) const {
+    const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+    const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
+    *reinterpret_cast<uint2*>(a.out + at * D + d) =
+        make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
+    if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+  }
+};
 
-template <int D, int NT, bool OTHER_CTAS, class Src>
-__device__ __forceinline__ void join(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src, int mine,
-                                     int warps, float* dst) {
-  constexpr int kRows = 8 * NT, kLanes = 32 / kRows, kBatch = OTHER_CTAS ? 4 : 2;
+// Joins n partials that a CTA's warps left in shared memory (one may lie in
+// global memory), in their order: warp `mine` of `warps` takes its share of the
+// columns, a lane part of one row. To the output or, dst given, to a partial.
+template <int D, int NT, class Src>
+__device__ __forceinline__ void join_warps(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src,
+                                           int mine, int warps, float* dst) {
+  constexpr int kRows = 8 * NT, kLanes = 32 / kRows, kBatch = 2;
   const int group = a.q_heads / a.cache.kv_heads, lane = threadIdx.x & 31, row = lane / kLanes;
   if (row >= rq.n * group) return;
   const int c1 = D / 4 * (mine + 1) / warps;
   for (int c = D / 4 * mine / warps + lane % kLanes; c < c1; c += kLanes) {
     const int d = 4 * c;
-    float m = -INFINITY, l = 0.0f;
-    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    Joined x;
 #pragma unroll 1
     for (int i = 0; i < n; i += kBatch) {
       float2 ml[kBatch];
       float4 v[kBatch];
-      float mn = m;
 #pragma unroll
       for (int j = 0; j < kBatch; ++j) {
         ml[j] = make_float2(-INFINITY, 0.0f);
         v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         if (i + j < n) {
           const float* s = src(i + j);
-          ml[j] = load_partial<OTHER_CTAS>(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
-          v[j] = load_partial<OTHER_CTAS>(reinterpret_cast<const float4*>(s + row * D + d));
+          ml[j] = *reinterpret_cast<const float2*>(s + kRows * D + 2 * row);
+          v[j] = *reinterpret_cast<const float4*>(s + row * D + d);
         }
       }
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) mn = fmaxf(mn, ml[j].x);
-      const float mu = mn == -INFINITY ? 0.0f : mn, w0 = ex2(m - mu);   // 0 from -inf
-      m = mn;
-      l *= w0;
-      o.x *= w0;
-      o.y *= w0;
-      o.z *= w0;
-      o.w *= w0;
-#pragma unroll
-      for (int j = 0; j < kBatch; ++j) {
-        const float w = ex2(ml[j].x - mu);
-        l += w * ml[j].y;
-        o.x += w * v[j].x;
-        o.y += w * v[j].y;
-        o.z += w * v[j].z;
-        o.w += w * v[j].w;
-      }
+      x.add(ml, v);
     }
     if (dst != nullptr) {
-      *reinterpret_cast<float4*>(dst + row * D + d) = o;
-      if (d == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(m, l);
+      *reinterpret_cast<float4*>(dst + row * D + d) = x.o;
+      if (d == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(x.m, x.l);
     } else {
-      const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
-      const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
-      *reinterpret_cast<uint2*>(a.out + at * D + d) =
-          make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
-      if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+      x.write(a, rq, h, group, row, D, d);
     }
+  }
+}
+
+// Joins n partials that CTAs left in global memory, up to one per CTA of the
+// grid, by a whole CTA: a warp reads whole rows (four neighbouring columns a
+// thread), and what threads there are beyond a row tile's columns take every
+// kParts-th partial, joined at the end through shared memory.
+template <int D, int NT, class Src>
+__device__ __forceinline__ void join_ctas(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src,
+                                          float* shared) {
+  constexpr int kRows = 8 * NT, kElems = kRows * D / 4, T = Shape<D, NT>::kThreads, kBatch = 4;
+  constexpr int kParts = T >= kElems ? T / kElems : 1, kStep = kParts > 1 ? kElems : T;
+  const int group = a.q_heads / a.cache.kv_heads, part = threadIdx.x / kStep;
+  for (int e = threadIdx.x - part * kStep; e < (kElems + kStep - 1) / kStep * kStep; e += kStep) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
+    const bool real = e < kElems && part < kParts && row < rq.n * group;
+    Joined x;
+    if (real)
+#pragma unroll 1
+      for (int i = part; i < n; i += kBatch * kParts) {
+        float2 ml[kBatch];
+        float4 v[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          ml[j] = make_float2(-INFINITY, 0.0f);
+          v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (i + j * kParts < n) {
+            const float* s = src(i + j * kParts);
+            ml[j] = __ldcg(reinterpret_cast<const float2*>(s + kRows * D + 2 * row));
+            v[j] = __ldcg(reinterpret_cast<const float4*>(s + row * D + d));
+          }
+        }
+        x.add(ml, v);
+      }
+    if constexpr (kParts > 1) {
+      float4* const os = reinterpret_cast<float4*>(shared);
+      float2* const mls = reinterpret_cast<float2*>(os + (kParts - 1) * kElems);
+      if (real && part > 0) {
+        os[(part - 1) * kElems + e] = x.o;
+        mls[(part - 1) * kElems + e] = make_float2(x.m, x.l);
+      }
+      __syncthreads();
+      if (real && part == 0) {
+        float2 ml[kParts - 1];
+        float4 v[kParts - 1];
+#pragma unroll
+        for (int j = 0; j < kParts - 1; ++j) {
+          ml[j] = mls[j * kElems + e];
+          v[j] = os[j * kElems + e];
+        }
+        x.add(ml, v);
+      }
+      __syncthreads();
+    }
+    if (real && part == 0) x.write(a, rq, h, group, row, D, d);
   }
 }
 
@@ -759,7 +822,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
         if (!Sm::kPark && short_last && w == w1) return slots + (size_t)(cta * W + w) * Slots<D, NT>::kFloats;
         return reinterpret_cast<const float*>(smem_raw) + sm->piece[short_last && w == w1][w];
       };
-      join<D, NT, false>(a, rq, sg.h, w1 - w0 + 1, src, warp - w0, w1 - w0 + 1,
+      join_warps<D, NT>(a, rq, sg.h, w1 - w0 + 1, src, warp - w0, w1 - w0 + 1,
                          inside ? nullptr : cta_slot(cta, sg.s0 < C0 ? 0 : 1));
     }
   }
@@ -793,7 +856,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
     const Request rq = {sg.row0, sg.n, 0, false};
     // the CTA the segment begins in holds its tail, the others their head
     auto src = [&](int i) -> const float* { return cta_slot(c0 + i, i == 0 ? 1 : 0); };
-    join<D, NT, true>(a, rq, sg.h, n, src, warp, W, nullptr);
+    join_ctas<D, NT>(a, rq, sg.h, n, src, reinterpret_cast<float*>(smem_raw));
   }
 }
 
