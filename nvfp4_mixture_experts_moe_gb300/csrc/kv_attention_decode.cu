@@ -229,17 +229,16 @@ struct Joined {
 };
 
 // Joins n partials that a CTA's warps left in shared memory (one may lie in
-// global memory), in their order: warp `mine` of `warps` takes its share of the
-// columns, a lane part of one row. To the output or, dst given, to a partial.
+// global memory), in their order: warp `mine` of `warps` takes every warps-th
+// run of 32 times four neighbouring columns (a row at D = 128), which its
+// lanes read without bank conflicts. To the output or, dst given, to a partial.
 template <int D, int NT, class Src>
 __device__ __forceinline__ void join_warps(const moe_kv4_attn_args& a, const Request& rq, int h, int n, Src src,
                                            int mine, int warps, float* dst) {
-  constexpr int kRows = 8 * NT, kLanes = 32 / kRows, kBatch = 2;
-  const int group = a.q_heads / a.cache.kv_heads, lane = threadIdx.x & 31, row = lane / kLanes;
-  if (row >= rq.n * group) return;
-  const int c1 = D / 4 * (mine + 1) / warps;
-  for (int c = D / 4 * mine / warps + lane % kLanes; c < c1; c += kLanes) {
-    const int d = 4 * c;
+  constexpr int kRows = 8 * NT, kBatch = 2;
+  const int group = a.q_heads / a.cache.kv_heads, lane = threadIdx.x & 31;
+  for (int e = 32 * mine + lane; e < rq.n * group * (D / 4); e += 32 * warps) {
+    const int row = e / (D / 4), d = e % (D / 4) * 4;
     Joined x;
 #pragma unroll 1
     for (int i = 0; i < n; i += kBatch) {
