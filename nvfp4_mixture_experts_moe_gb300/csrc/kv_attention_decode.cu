@@ -228,6 +228,11 @@ struct Joined {
   }
 };
 
+// Where a warp's partial holds four neighbouring columns of a row: the lanes
+// of a store have four pairs of rows and every fourth or second chunk, and
+// would otherwise meet in two banks' worth of addresses.
+__device__ __forceinline__ int warp_chunk(int row, int chunk) { return chunk ^ (row >> 1 & 3); }
+
 // Joins n partials that a CTA's warps left in shared memory (one may lie in
 // global memory), in their order: warp `mine` of `warps` takes every warps-th
 // run of 32 times four neighbouring columns (a row at D = 128), which its
@@ -251,7 +256,7 @@ __device__ __forceinline__ void join_warps(const moe_kv4_attn_args& a, const Req
         if (i + j < n) {
           const float* s = src(i + j);
           ml[j] = *reinterpret_cast<const float2*>(s + kRows * D + 2 * row);
-          v[j] = *reinterpret_cast<const float4*>(s + row * D + d);
+          v[j] = *reinterpret_cast<const float4*>(s + row * D + warp_chunk(row, d / 4) * 4);
         }
       }
       x.add(ml, v);
@@ -788,9 +793,10 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
                   a.lse[at] = sum > 0.0f ? m[nt][c] * kLn2 + logf(sum) : -INFINITY;
               }
             } else {
-              float2* out = reinterpret_cast<float2*>(dst + row * D + g8 * (D / 8));
 #pragma unroll
-              for (int mt = 0; mt < MT; ++mt) out[mt] = make_float2(o[nt][mt][c], o[nt][mt][c + 2]);
+              for (int mt = 0; mt < MT; ++mt)
+                *reinterpret_cast<float2*>(dst + row * D + warp_chunk(row, g8 * (D / 32) + mt / 2) * 4 + mt % 2 * 2) =
+                    make_float2(o[nt][mt][c], o[nt][mt][c + 2]);
               if (g8 == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(m[nt][c], sum);
             }
           }
