@@ -45,7 +45,7 @@ moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
 // per key/value head; the others are skipped.
 constexpr int kKvDecodeRows = 16;
 constexpr int kKvMaxCtas = 160;      // CTAs of the attention kernels, one per SM
-constexpr int kKvTilesPerCta = 8;    // fewer decode tiles than this do not get a CTA of their own
+constexpr int kKvTilesPerCta = 4;    // fewer decode tiles than this do not get a CTA of their own
 size_t kv4_decode_ws_floats(int head_dim, int rows);
 moe_status launch_kv4_decode(const moe_kv4_attn_args& a, int max_rows, int* status, int* counters, float* partials,
                              cudaStream_t s);

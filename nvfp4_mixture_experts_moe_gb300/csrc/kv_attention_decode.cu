@@ -36,9 +36,9 @@
 //
 // Measured (replayed): 4 requests of 131072 tokens, 8 heads x 128: 110 us,
 // 5.5 TB/s (81 % of the measured copy rate); 64 of up to 8192 in pages of 16:
-// 69 us, 4.5 TB/s (9 us until the first tiles are there, 9 after the last for
-// uneven ends and joins); 16 rows over 84,500 tokens at D = 64: 30.5 us; one
-// request of 1000 tokens: 10 us.
+// 69 us, 4.5 TB/s (9 us until the first tiles are there, 8 after the last for
+// uneven ends and joins); 16 rows over 84,500 tokens at D = 64: 29.5 us; one
+// request of 1000 tokens: 8.9 us.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -56,7 +56,8 @@ constexpr float kSlack = 8.0f;     // how far above m a score may be before m fo
 constexpr unsigned kFull = 0xffffffffu;
 // Tiles that a CTA works on in the time that a join across CTAs takes, where
 // every SM has a range (which then begin and end anywhere); half where not.
-// 1 x 1000 tokens of 8 heads: 10.4 us cut, 11.7 whole; 8 x 1000: 12.4 and 11.7.
+// (With the joins of then, 1 x 1000 tokens of 8 heads took 10.4 us cut and 11.7
+// whole, 8 x 1000 12.4 and 11.7.)
 constexpr int kAlone = 24;
 
 struct DecodeArgs {
@@ -397,7 +398,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
   // ------------------------------------------------------- this warp's range
   // Equal ranges, or a (request, head) for each CTA where that takes little
   // more of its time than the join across CTAs would.
-  const int cta = blockIdx.x, spread = min((int)gridDim.x, (total + kKvTilesPerCta - 1) / kKvTilesPerCta);
+  // Few tiles go to fewer CTAs, four to each or eight (1 x 1000 tokens of 8
+  // heads: 8.9 us with four, 9.4 with eight; 2 x 4066 of one: 11.1 and 10.3,
+  // the join of 32 partials).
+  const int least = longest > 16 * kKvTilesPerCta ? 2 * kKvTilesPerCta : kKvTilesPerCta;
+  const int cta = blockIdx.x, spread = min((int)gridDim.x, (total + least - 1) / least);
   const int per_cta = (total + spread - 1) / spread, more = spread == (int)gridDim.x ? kAlone : kAlone / 2;
   const bool alone = p.nb * Hk <= (int)gridDim.x && longest <= per_cta + more;
   const int G = alone ? p.nb * Hk : spread;
