@@ -58,6 +58,8 @@ constexpr int kFusedRoutePermuteMax = 2048;  // pairs routed and permuted by one
 // reads anything the predecessor writes. Without the attribute the wait
 // returns at once.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel in the stream, if it was launched so, start from now on.
+__device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Expert sharding (expert parallelism): the permutations group only the
 // pairs of experts [shard_lo, shard_lo + n) (n = the E they are given, the

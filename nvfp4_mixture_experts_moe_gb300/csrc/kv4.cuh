@@ -49,10 +49,12 @@ constexpr int kKvTilesPerCta = 4;    // fewer decode tiles than this do not get 
 size_t kv4_decode_ws_floats(int head_dim, int rows);
 moe_status launch_kv4_decode(const moe_kv4_attn_args& a, int max_rows, int* status, int* counters, float* partials,
                              cudaStream_t s);
-// Attention of requests with more than min_rows rows.
+// Attention of requests with more than min_rows rows; overlap: the launch
+// before in the stream is launch_kv4_decode's, with other partials.
 size_t kv4_prompt_ws_floats(int head_dim);
 long long kv4_prompt_units(const moe_kv4_attn_args& a);   // a bound on the units of work it counts in 32 bits
-moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials, cudaStream_t s);
+moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials, bool overlap,
+                             cudaStream_t s);
 
 size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a);
 moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream_t s);

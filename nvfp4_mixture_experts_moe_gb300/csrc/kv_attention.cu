@@ -1,6 +1,4 @@
 // Attention over the NVFP4 cache: which kernel takes which request.
-#include <algorithm>
-
 #include "kernels.cuh"
 #include "kv4.cuh"
 
@@ -22,22 +20,27 @@ static bool any_prompt(const moe_kv4_attn_args& a) {
   return (long long)a.max_q * (a.q_heads / a.cache.kv_heads) > kKvDecodeRows;
 }
 
-// The two kernels of a call run one after the other and share the workspace.
+// The two kernels of a call overlap: each has its own part of the workspace.
+static size_t decode_ws_bytes(const moe_kv4_attn_args& a) {
+  const int few = decode_rows(a);
+  return few > 0 ? align_up(kv4_decode_ws_floats(a.cache.head_dim, few) * sizeof(float)) : 0;
+}
+
 size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a) {
-  size_t floats = kv4_decode_ws_floats(a.cache.head_dim, decode_rows(a));
-  if (any_prompt(a)) floats = std::max(floats, kv4_prompt_ws_floats(a.cache.head_dim));
-  return align_up(MOE_KV4_WS_ZERO + floats * sizeof(float));
+  const size_t many = any_prompt(a) ? kv4_prompt_ws_floats(a.cache.head_dim) * sizeof(float) : 0;
+  return align_up(MOE_KV4_WS_ZERO + decode_ws_bytes(a) + many);
 }
 
 moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream_t s) {
   int* status = &static_cast<WsHeader*>(ws)->status;
   int* counters = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
   static_assert(sizeof(WsHeader) + kKvMaxCtas * sizeof(int) <= MOE_KV4_WS_ZERO, "zero region");
-  float* partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + MOE_KV4_WS_ZERO);
+  uint8_t* const partials = static_cast<uint8_t*>(ws) + MOE_KV4_WS_ZERO;
   const int few = decode_rows(a);
   moe_status st = MOE_OK;
-  if (few > 0) st = launch_kv4_decode(a, few, status, counters, partials, s);
-  if (st == MOE_OK && any_prompt(a)) st = launch_kv4_prompt(a, few, status, partials, s);
+  if (few > 0) st = launch_kv4_decode(a, few, status, counters, reinterpret_cast<float*>(partials), s);
+  if (st == MOE_OK && any_prompt(a))
+    st = launch_kv4_prompt(a, few, status, reinterpret_cast<float*>(partials + decode_ws_bytes(a)), few > 0, s);
   return st;
 }
 

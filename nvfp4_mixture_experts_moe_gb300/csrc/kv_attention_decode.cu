@@ -343,6 +343,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
 
   // ------------------------------------------------ tiles before each request
   pdl_wait();
+  pdl_trigger();   // after the wait: see the many-row kernel
   if (tid == 0) sm->pre[0] = 0;
   int carry = 0, longest = 0;   // tiles of all requests; of one (request, head)
   bool bad = false;

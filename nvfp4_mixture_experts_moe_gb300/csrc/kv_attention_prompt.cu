@@ -75,6 +75,12 @@ struct PromptArgs {
   Cut* cuts;           // [kKvMaxCtas]
   float* partials;     // [kKvMaxCtas][2][kRowTile x D, then (m, l) per row]
   long long wait_limit;
+  // Launched right behind the few-row kernel of the same call: that one lets
+  // this one start once everything before itself is done, and the two share
+  // no memory, so this one waits for it only at its own end (whoever waits
+  // for this kernel waits for both). A call of long and short requests then
+  // uses the SMs that the first leaves idle.
+  int overlap;
 };
 
 template <int D>
@@ -350,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     mbar_init(&sm->drain, 2);
     fence_barrier_init();
   }
-  pdl_wait();
+  if (!p.overlap) pdl_wait();
   for (int b = warp; b < p.nb; b += kThreads / 32) {   // a warp per request
     const Request r = load_request(a, p.b0 + b);
     const long long rows = (long long)r.n * group;
@@ -395,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
   const int G = min((int)gridDim.x, total), cta = blockIdx.x;
   if (cta >= G) {
     if (tid == 0) p.cuts[cta].n = 0;
+    if (p.overlap) pdl_wait();
     return;
   }
   const Range rg = {&p, sm->pre, mul_div(total, cta, G), mul_div(total, cta + 1, G)};
@@ -940,6 +947,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
   tc_fence_after();
   if (warp == kMmaWarp) tmem_dealloc(tmem, kTmemCols);
   if (tid == 0 && sm->abort) set_status(p.status, MOE_ERR_TIMEOUT);
+  if (p.overlap) pdl_wait();
 }
 
 // Joins the partials of the row tiles that several CTAs cut: block (c, part)
@@ -1025,7 +1033,7 @@ long long kv4_prompt_units(const moe_kv4_attn_args& a) {
   return (rows / kRowTile + a.batch) * a.cache.kv_heads * tiles;
 }
 
-moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials,
+moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* status, float* partials, bool overlap,
                              cudaStream_t s) {
   PromptArgs p;
   p.a = a;
@@ -1034,6 +1042,7 @@ moe_status launch_kv4_prompt(const moe_kv4_attn_args& a, int min_rows, int* stat
   p.cuts = reinterpret_cast<Cut*>(partials);
   p.partials = partials + kCutFloats;
   p.wait_limit = debug_wait_limit();
+  p.overlap = overlap && a.batch <= kChunk;   // one launch of each
   const int sms = sm_count(), ctas = sms < kKvMaxCtas ? sms : kKvMaxCtas;
   for (int b0 = 0; b0 < a.batch; b0 += kChunk) {
     p.b0 = b0;
