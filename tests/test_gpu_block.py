@@ -587,6 +587,50 @@ def test_norm_of_zero_rows_and_empty_batch():
 
 # ----------------------------------------------------------------- all together
 
+def test_calls_replay_from_a_graph():
+    """A step's tables, rows in and out, attention of short and long requests, a norm: replays on other lengths give
+    what direct calls give."""
+    from nvfp4_mixture_experts_moe_gb300 import Kv4Cache, KvStep, block_norm
+    Bn, heads, D, P, W, T = 4, 2, 64, 16, 40, 400
+    cache, plain = (Kv4Cache(Bn * W, P, heads, D, 400.0, 400.0) for _ in range(2))
+    q, kv = _bf16((T, 8, D), 1).cuda(), _bf16((T, 2 * heads, D), 2).cuda()
+    x, w = _bf16((T, 8 * D), 3).cuda(), _bf16((8 * D,), 4).cuda()
+    free = torch.arange(Bn * W, dtype=torch.int32, device="cuda")
+
+    def state():
+        return dict(ctx=torch.zeros(Bn, dtype=torch.int32, device="cuda"), new=torch.zeros(Bn, dtype=torch.int32, device="cuda"),
+                    table=torch.zeros(Bn, W, dtype=torch.int32, device="cuda"), step=KvStep(Bn, T, P, W),
+                    count=torch.full((1,), Bn * W, dtype=torch.int32, device="cuda"))
+
+    def call(c, s, ws):
+        t = s["step"].run(s["ctx"], s["new"], s["table"], free, s["count"])
+        c.append(kv[:, :heads], kv[:, heads:], t.slots)
+        o, _ = c.attention(q, t.cu_q, t.kv_len, s["table"], max_q=300, ws=ws)
+        r, y = block_norm(o.view(T, -1), x, w_post=w, w_pre=w)
+        s["ctx"].copy_(t.kv_len)
+        s["count"].copy_(t.free_count)
+        return o, r, y
+    got, ref = state(), state()
+    ws, ws2 = (c.attention_workspace(T, Bn, 8, 300, W) for c in (cache, plain))
+    call(cache, got, ws)   # once before the capture: kernels are loaded
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        outs = call(cache, got, ws)
+    for s in (got, ref):
+        s["ctx"].zero_()
+        s["count"].fill_(Bn * W)
+    for new in ([300, 3, 1, 90], [1, 1, 1, 1], [2, 130, 0, 4], [1, 0, 100, 1]):
+        for s in (got, ref):
+            s["new"].copy_(_cuda(new))
+        graph.replay()
+        want = call(plain, ref, ws2)
+        torch.cuda.synchronize()
+        n = sum(new)
+        assert all(torch.equal(a[:n], b[:n]) for a, b in zip(outs, want)), new
+    assert torch.equal(got["table"], ref["table"]) and B().moe_get_device_status(ws) == 0
+
+
 def _example():
     import importlib.util
     import os
