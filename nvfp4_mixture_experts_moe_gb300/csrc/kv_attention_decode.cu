@@ -34,9 +34,9 @@
 // rows (twice the matrix work per conversion) run further from the memory
 // rate than 8.
 //
-// Measured (replayed): 4 requests of 131072 tokens, 8 heads x 128: 110 us,
-// 5.5 TB/s (81 % of the measured copy rate); 64 of up to 8192 in pages of 16:
-// 69 us, 4.5 TB/s (9 us until the first tiles are there, 8 after the last for
+// Measured (replayed): 4 requests of 131072 tokens, 8 heads x 128: 108 us,
+// 5.6 TB/s (82 % of the measured copy rate); 64 of up to 8192 in pages of 16:
+// 68 us, 4.5 TB/s (9 us until the first tiles are there, 8 after the last for
 // uneven ends and joins); 16 rows over 84,500 tokens at D = 64: 29.5 us; one
 // request of 1000 tokens: 8.9 us.
 #include <type_traits>
@@ -517,7 +517,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
     uint32_t qf[NT][MT][2];        // the rows as B fragments
     float o[NT][MT][4];            // out^T: rows d, columns query rows
     float mult[NT][2], m[NT][2], l[NT][2];
-    int last[NT][2];               // position of the query of rows 2t, 2t + 1
     Request rq = {0, 0, 0, false};
     int h = 0, plain0 = 0, plain1 = 0;   // tiles with every token in [plain0, plain1) need no mask
     int seg_end = r0;
@@ -578,8 +577,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
           mult[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const int r = nt * 8 + 2 * t4 + c;
-            last[nt][c] = a.causal ? rq.kv - rq.n + r / group : rq.kv - 1;
             m[nt][c] = -INFINITY;
             l[nt][c] = 0.0f;
           }
@@ -601,6 +598,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
       // last, for a single token) carry no mask.
       auto work = [&](auto with_mask, const uint8_t* part, int tok0, int valid) {
         constexpr bool kMask = decltype(with_mask)::value;
+        const int recip = kMask ? (65535 + group) / group : 0;
         // ---------------------------------------------------------- scores
         float s[NT][kPart][4];
 #pragma unroll
@@ -648,7 +646,9 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
                 const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
-                const int hi_tok = last[nt][i & 1], lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
+                // the last token its query sees; row / group by the reciprocal (both at most 16)
+                const int token = (nt * 8 + 2 * t4 + (i & 1)) * recip >> 16;
+                const int hi_tok = a.causal ? rq.kv - rq.n + token : rq.kv - 1, lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
                 if (tok > hi_tok || tok < lo_tok || !(valid >> blk & 1)) s[nt][blk][i] = -INFINITY;
               }
           }
