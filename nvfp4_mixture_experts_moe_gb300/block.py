@@ -91,7 +91,7 @@ class Kv4Cache:
         at = _ints(slots, (n,), "slots")
         shape = (n, self.kv_heads, self.head_dim)
         k = _made(torch.empty(shape, dtype=_BF16, device=self.pool.device), stream)
-        v = _made(torch.empty_like(k), stream)
+        v = _made(torch.empty(shape, dtype=_BF16, device=self.pool.device), stream)
         B.moe_kv4_read(self.desc, at, n, k.data_ptr(), v.data_ptr(), device_status, stream)
         return k, v
 
