@@ -218,14 +218,15 @@ struct Joined {
       o.w += w * v[j].w;
     }
   }
-  // normalised bf16 and lse
+  // Normalised bf16 and lse. A row that has seen nothing has l = 0 and gets
+  // zeros and -inf; l is NaN where a score was, and so are the row and its lse.
   __device__ __forceinline__ void write(const moe_kv4_attn_args& a, const Request& rq, int h, int group, int row, int D,
                                         int d) const {
-    const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * a.cache.v_gs);
     const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
     *reinterpret_cast<uint2*>(a.out + at * D + d) =
         make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
-    if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+    if (d == 0 && a.lse != nullptr) a.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
   }
 };
 
@@ -786,7 +787,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
             const int row = nt * 8 + 2 * t4 + c;
             if (whole) {
               if (row < rq.n * group) {
-                const float inv = sum > 0.0f ? 1.0f / (sum * a.cache.v_gs) : 0.0f;
+                const float inv = sum == 0.0f ? 0.0f : 1.0f / (sum * a.cache.v_gs);   // NaN stays NaN
                 const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
                 uint32_t w[MT];
 #pragma unroll
@@ -796,7 +797,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
 #pragma unroll
                 for (int i = 0; i < MT / 4; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (g8 == 0 && a.lse != nullptr)
-                  a.lse[at] = sum > 0.0f ? m[nt][c] * kLn2 + logf(sum) : -INFINITY;
+                  a.lse[at] = sum == 0.0f ? -INFINITY : m[nt][c] * kLn2 + logf(sum);
               }
             } else {
 #pragma unroll

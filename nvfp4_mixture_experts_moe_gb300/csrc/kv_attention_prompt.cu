@@ -557,11 +557,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         if (done.active) {
           const bool give = done.split && i == 1, final = !give && done.whole;
           if (final) {
-            const float inv = l > 0.0f ? 1.0f / (l * a.cache.v_gs) : 0.0f;
+            // 0: a row that sees nothing; NaN: a bad query's row, which stays NaN
+            const float inv = l == 0.0f ? 0.0f : 1.0f / (l * a.cache.v_gs);
             own *= inv;
             other *= inv;
           }
-          const bool blank = give ? !any : final && !(l > 0.0f);   // O holds nothing to read
+          const bool blank = give ? !any : final && l == 0.0f;   // O holds nothing to read
           const bool wide = (reinterpret_cast<uintptr_t>(a.out) & 31) == 0;
           const int which = done.t0 > 0 ? 0 : 1, swz = give ? done.r & (D / 4 - 1) : 0;
           float* dst = give ? xo + done.r * D : slot(cta, which) + (size_t)done.r * D;
@@ -617,7 +618,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
           if (give) sm->x_ml[done.r] = make_float2(m, l);
           else if (done.real && !final)
             *reinterpret_cast<float2*>(slot(cta, which) + kRowTile * D + 2 * done.r) = make_float2(m, l);
-          else if (done.real && a.lse != nullptr) a.lse[done.at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+          else if (done.real && a.lse != nullptr) a.lse[done.at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
         }
         tc_fence_before();
         if (done.split) {
@@ -1006,9 +1007,9 @@ __global__ void __launch_bounds__(kJoinThreads) kv4_prompt_join_kernel(const __g
   const float inv = 1.0f / (l * a.cache.v_gs);
   const size_t at = (size_t)(cut.row0 + token) * a.q_heads + cut.h * group + rr - token * group;
   *reinterpret_cast<uint2*>(a.out + at * D + d) =
-      l > 0.0f ? make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv))
-               : make_uint2(0u, 0u);
-  if (d == 0 && a.lse != nullptr) a.lse[at] = l > 0.0f ? m * kLn2 + logf(l) : -INFINITY;
+      l == 0.0f ? make_uint2(0u, 0u)   // not what a NaN gives
+                : make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
+  if (d == 0 && a.lse != nullptr) a.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
 }
 
 template <int D>
