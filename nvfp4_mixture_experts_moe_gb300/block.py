@@ -6,7 +6,9 @@ back and attends over them (``moe_kv4_append``, ``moe_kv4_read``,
 ``moe_kv4_attention``), ``block_norm`` fuses the norm after a block, its gate,
 the residual and the norm before the next block (``moe_block_norm``). The C
 calls and their contracts are in ``include/moe_block.h``; torch only
-allocates. Wrong shapes, types or devices raise ``ValueError``; what the C
+allocates. A call runs on the current stream, or on ``stream=`` (a Stream or
+a raw handle), on which its outputs and its own workspace are then made; what
+the caller passes in has to be ready there. Wrong shapes, types or devices raise ``ValueError``; what the C
 call refuses raises ``MoeError``.
 """
 from __future__ import annotations
@@ -47,10 +49,24 @@ def _like(t, shape, dtype, what):
     return t.data_ptr()
 
 
-def _made(t, stream):
-    """A tensor allocated here for a call on another stream stays reserved until that stream is done with it."""
-    if stream is not None and isinstance(stream, torch.cuda.Stream):
-        t.record_stream(stream)
+def _empty(shape, dtype, device, stream, zeros=0):
+    """An output or workspace (its first ``zeros`` elements zero) of a call on ``stream``.
+
+    It is made on that stream: memory of the current one may still be used by work queued there, which the call does
+    not wait for. It stays reserved for what the current stream has queued when the caller gives it back.
+    """
+    if stream is None:
+        t = torch.empty(shape, dtype=dtype, device=device)
+        if zeros:
+            t[:zeros].zero_()
+        return t
+    here = torch.cuda.current_stream()
+    if not isinstance(stream, torch.cuda.Stream):   # a handle
+        stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = _empty(shape, dtype, device, None, zeros)
+    if stream.cuda_stream != here.cuda_stream:
+        t.record_stream(here)
     return t
 
 
@@ -90,21 +106,18 @@ class Kv4Cache:
         n = slots.shape[0] if slots.dim() == 1 else -1
         at = _ints(slots, (n,), "slots")
         shape = (n, self.kv_heads, self.head_dim)
-        k = _made(torch.empty(shape, dtype=_BF16, device=self.pool.device), stream)
-        v = _made(torch.empty(shape, dtype=_BF16, device=self.pool.device), stream)
+        k = _empty(shape, _BF16, self.pool.device, stream)
+        v = _empty(shape, _BF16, self.pool.device, stream)
         B.moe_kv4_read(self.desc, at, n, k.data_ptr(), v.data_ptr(), device_status, stream)
         return k, v
 
     def attention_workspace(self, total_q, batch, q_heads, max_q, max_pages=1, stream=None):
-        """A workspace for calls of up to these sizes; its leading bytes start at zero."""
+        """A workspace for calls of up to these sizes on ``stream``; its leading bytes start at zero."""
         a = B.MoeKv4AttnArgs(cache=self.desc, batch=batch, q_heads=q_heads, total_q=total_q, max_q=max_q,
                              max_pages=max_pages, scale=1.0, causal=1)
         n = B.moe_kv4_attention_workspace_size(a)
         _need(n > 0, "attention sizes outside the limits")
-        ws = torch.empty(n, dtype=torch.uint8, device=self.pool.device)
-        with torch.cuda.stream(stream if isinstance(stream, torch.cuda.Stream) else None):
-            ws[:B.MOE_KV4_WS_ZERO].zero_()
-        return ws
+        return _empty(n, torch.uint8, self.pool.device, stream, B.MOE_KV4_WS_ZERO)
 
     def attention(self, q, cu_q, kv_len, block_table, max_q, scale=None, causal=True, window=0, want_lse=False,
                   out=None, lse=None, ws=None, stream=None):
@@ -124,15 +137,15 @@ class Kv4Cache:
         max_pages = block_table.shape[1]
         shape = (total_q, heads, self.head_dim)
         if out is None:
-            out = _made(torch.empty(shape, dtype=_BF16, device=q.device), stream)
+            out = _empty(shape, _BF16, q.device, stream)
             op = out.data_ptr()
         else:
             op = _like(out, shape, _BF16, "out")
         if lse is None and want_lse:
-            lse = _made(torch.empty(total_q, heads, dtype=_F32, device=q.device), stream)
+            lse = _empty((total_q, heads), _F32, q.device, stream)
         lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse")
         if ws is None:
-            ws = _made(self.attention_workspace(total_q, batch, heads, max_q, max_pages, stream), stream)
+            ws = self.attention_workspace(total_q, batch, heads, max_q, max_pages, stream)
         a = B.PACK_KV4_ATTN.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
                                  _ints(cu_q, (batch + 1,), "cu_q"), _ints(kv_len, (batch,), "kv_len"),
                                  _ints(block_table, (batch, max_pages), "block_table"),
@@ -212,7 +225,7 @@ def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1
     else:
         gp, gst = _matrix(gate, T, H, "gate")
     if residual_out is None:
-        residual_out = _made(torch.empty(shape, dtype=dtype, device=residual.device), stream)
+        residual_out = _empty(shape, dtype, residual.device, stream)
         rp = residual_out.data_ptr()
     else:
         rp = _like(residual_out, shape, dtype, "residual_out")
@@ -221,7 +234,7 @@ def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1
     else:
         wp = _like(w_pre, (H,), _BF16, "w_pre")
         if out is None:
-            out = _made(torch.empty(shape, dtype=_BF16, device=residual.device), stream)
+            out = _empty(shape, _BF16, residual.device, stream)
             op = out.data_ptr()
         else:
             op = _like(out, shape, _BF16, "out")

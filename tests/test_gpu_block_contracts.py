@@ -3,7 +3,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_block import Scene, built  # noqa: F401
+from test_gpu_block import B, Scene, _bf16, _cuda, built  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +30,99 @@ def test_bad_query_gives_nan_rows(qheads, heads, D, lens, value):
     keep = torch.ones(s.total, qheads, dtype=torch.bool, device="cuda")
     keep[row, head] = False
     assert torch.equal(out[keep], good[keep]) and torch.equal(lse2[keep], lse[keep])
+
+
+# ------------------------------------------------- tensors made for a stream
+
+def _stream_of(other, handle):
+    return other.cuda_stream if handle else other
+
+
+def _queue_writes(*like):
+    """Queues, behind some 50 ms of work on the current stream, writes over memory that is then given back to the
+    allocator: tensors of these sizes made on this stream may take it, being ordered behind the writes."""
+    torch.cuda.synchronize()
+    made = [torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in like for _ in range(8)]
+    torch.cuda._sleep(100_000_000)
+    for t in made:
+        t.view(torch.uint8).fill_(0xFF)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+@pytest.mark.parametrize("what", ["read", "attention", "block_norm"])
+def test_outputs_on_another_stream_are_not_written_by_queued_work(what, handle):
+    from nvfp4_mixture_experts_moe_gb300 import block_norm
+    s = Scene([(100, 1), (300, 40)], 8, 2, 128, 64, seed=5)
+    q, cu, kv, tb = s.q.cuda(), _cuda(s.cu), _cuda([k for k, _ in s.lens]), _cuda(s.table)
+    ws = s.cache.attention_workspace(s.total, 2, 8, s.max_q, s.W)
+    slots = _cuda(s.table[1, 0] * 64 + np.arange(50))
+    x, w = _bf16((50, 1024), 1).cuda(), _bf16((1024,), 2).cuda()
+    call = {"read": lambda st: s.cache.read(slots, stream=st),
+            "attention": lambda st: s.cache.attention(q, cu, kv, tb, max_q=s.max_q, want_lse=True, ws=ws, stream=st),
+            "block_norm": lambda st: block_norm(x, x, w_post=w, w_pre=w, stream=st)}[what]
+    want = [t.clone() for t in call(None)]
+    other = torch.cuda.Stream()
+    _queue_writes(*want)
+    got = call(_stream_of(other, handle))
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_workspace_for_another_stream_is_not_written_by_queued_work(handle):
+    s = Scene([(20000, 1), (300, 1)], 8, 2, 128, 64, seed=5)
+    size = s.cache.attention_workspace(s.total, 2, 8, 1, s.W)
+    other = torch.cuda.Stream()
+    _queue_writes(size)
+    ws = s.cache.attention_workspace(s.total, 2, 8, 1, s.W, stream=_stream_of(other, handle))
+    torch.cuda.synchronize()
+    assert not ws[:B().MOE_KV4_WS_ZERO].any()
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_own_workspace_is_zeroed_on_the_calls_stream(handle):
+    """Joins across CTAs count arrivals in the workspace: zeroed late, they never run."""
+    s = Scene([(20000, 1), (300, 1)], 8, 2, 128, 64, seed=5)
+    want, _ = s.run()
+    args = (s.q.cuda(), _cuda(s.cu), _cuda([k for k, _ in s.lens]), _cuda(s.table))
+    out = torch.zeros_like(want)
+    used = [s.cache.attention_workspace(s.total, 2, 8, 1, s.W) for _ in range(8)]
+    for t in used:
+        t.fill_(0xFF)
+    del used, t
+    other = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(100_000_000)
+    s.cache.attention(*args, max_q=1, out=out, stream=_stream_of(other, handle))
+    torch.cuda.synchronize()
+    assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_outputs_given_back_on_the_current_stream_are_not_reused_early(handle):
+    """The caller waits for the other stream, queues a use and drops the tensors; the next call must not write them."""
+    s = Scene([(300, 1)], 1, 1, 64, 64, seed=2)
+    a, b = _cuda(s.table[0, 0] * 64 + np.arange(64)), _cuda(s.table[0, 1] * 64 + np.arange(64))
+    other = torch.cuda.Stream()
+    st = _stream_of(other, handle)
+    want = [t.clone() for t in s.cache.read(a)]
+    torch.cuda.synchronize()
+    got = s.cache.read(a, stream=st)
+    torch.cuda.current_stream().wait_stream(other)
+    torch.cuda._sleep(100_000_000)
+    use = [t.clone() for t in got]
+    del got
+    for _ in range(4):
+        s.cache.read(b, stream=st)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(use, want))
+
+
+def test_default_stream_by_its_handle():
+    s = Scene([(300, 1)], 1, 1, 64, 64, seed=2)
+    want, _ = s.run()
+    args = (s.q.cuda(), _cuda(s.cu), _cuda([300]), _cuda(s.table))
+    torch.cuda.synchronize()
+    got, _ = s.cache.attention(*args, max_q=1, stream=0)
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
