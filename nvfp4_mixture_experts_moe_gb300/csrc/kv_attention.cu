@@ -31,7 +31,12 @@ size_t kv4_attention_ws_bytes(const moe_kv4_attn_args& a) {
   return align_up(MOE_KV4_WS_ZERO + decode_ws_bytes(a) + many);
 }
 
-moe_status launch_kv4_attention(const moe_kv4_attn_args& a, void* ws, cudaStream_t s) {
+moe_status launch_kv4_attention(const moe_kv4_attn_args& args, void* ws, cudaStream_t s) {
+  moe_kv4_attn_args a = args;
+  // A window of all the tokens a table holds hides none. Below that the
+  // kernels' position - window stays within 32 bits, also for queries that
+  // stand before token 0.
+  if (a.window >= a.max_pages * a.cache.page_tokens) a.window = 0;
   int* status = &static_cast<WsHeader*>(ws)->status;
   int* counters = reinterpret_cast<int*>(static_cast<uint8_t*>(ws) + sizeof(WsHeader));
   static_assert(sizeof(WsHeader) + kKvMaxCtas * sizeof(int) <= MOE_KV4_WS_ZERO, "zero region");

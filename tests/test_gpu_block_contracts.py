@@ -126,3 +126,16 @@ def test_default_stream_by_its_handle():
     got, _ = s.cache.attention(*args, max_q=1, stream=0)
     torch.cuda.synchronize()
     assert torch.equal(got, want)
+
+
+# ---------------------------------------------------------------- windows
+
+@pytest.mark.parametrize("n", [4, 100, 300])
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 60, 2 ** 31 - 200])
+def test_windows_near_the_largest_integer(n, window):
+    """More query rows than cached tokens (a refused append) and a window that hides nothing."""
+    s = Scene([(2, n), (0, n), (10, n), (150, n)], 8, 2, 64, 16, seed=n)
+    ref, l0 = s.run(want_lse=True)
+    out, lse = s.run(want_lse=True, window=window)
+    s.check(out, lse, rows=20)
+    assert torch.equal(out, ref) and torch.equal(lse, l0)
