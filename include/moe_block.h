@@ -110,7 +110,9 @@ moe_status moe_kv4_read(const moe_kv4_cache* cache, const int32_t* slots, int n,
  * Bad device data is reported as MOE_ERR_DEVICE in the workspace status word
  * (moe_get_device_status): a page id outside the pool (its tokens count as
  * hidden), kv_len above max_pages * page_tokens (cut there), more query rows
- * than max_q or total_q (those requests' rows are not written).
+ * than max_q or total_q (those requests' rows are not written). What lies
+ * before every query's window is not used: those tokens need not have been
+ * appended, and entries of pages that hold no others may be anything.
  * Errors: NULL pointers (lse may be), misaligned pool / q / out (16 bytes), a
  * q_stride that is not a multiple of 8 or smaller than a row, negative sizes,
  * max_q < 1, a non-finite scale, a window without causal ->

@@ -451,12 +451,15 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
         d_n = r.n;
         d_s0 = s.s0;
         d_seg_end = s.s1;
-        d_tok = (first_seen(a, r) / kTile + (tile - s.s0)) * kTile;
+        const int seen = first_seen(a, r);
+        d_tok = (seen / kTile + (tile - s.s0)) * kTile;
+        const int unseen = (seen - d_tok) >> p_log;
         const int32_t* table = a.block_table + (size_t)(p.b0 + s.b) * a.max_pages + (d_tok >> p_log);
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const int blk = i << run_log;
           if (blk >= NB || d_tok + blk * kKvBlock >= r.kv) break;
+          if (i < unseen) continue;   // a page before every row's window may have been given back
           const int page = __ldg(table + i);
           if (page >= 0 && page < a.cache.num_pages) {
             d_valid |= ((1 << (1 << run_log)) - 1) << blk;
@@ -723,9 +726,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
             } else {
               vw[k][0] = *reinterpret_cast<const uint32_t*>(vb + L::kValueCodes + tok * L::kCodeRow + 4 * g8);
             }
-            // what was never appended may decode as NaN: 0 * p instead
+            // What was never appended, lies before every row's window or has a
+            // bad page is hidden (p = 0), but its scale may decode as NaN, which
+            // no appended row's does: 0 instead.
             if constexpr (kMask) {
-              if (tok0 + blk * kKvBlock + tok >= rq.kv || !(valid >> blk & 1)) sc[k] = 0;
+              if ((sc[k] & 0x7fu) == 0x7fu) sc[k] = 0;
             }
           }
           const uint32_t s01 = cvt_e4m3x2_f16x2(sc[0] | sc[1] << 8), s23 = cvt_e4m3x2_f16x2(sc[2] | sc[3] << 8);

@@ -110,16 +110,16 @@ __device__ __forceinline__ Request load_request(const moe_kv4_attn_args& a, int 
   return r;
 }
 
-// First token and number of KV tiles of a request's row tile; at least one
-// tile, so that rows that see nothing are written (as zeros) like any other.
+// First token that a request's row tile sees and number of its KV tiles (the
+// first holds that token); at least one tile, so that rows that see nothing are
+// written (as zeros) like any other.
 __device__ __forceinline__ int row_tile_tiles(const moe_kv4_attn_args& a, const Request& r, int group, int q,
-                                              int& first) {
+                                              int& seen) {
   const int rows = r.n * group;
   const int i0 = q * kRowTile / group, i1 = (min(rows, (q + 1) * kRowTile) - 1) / group;
   const int hi = a.causal ? max(0, r.kv - r.n + i1 + 1) : r.kv;
-  const int lo = a.window > 0 ? max(0, r.kv - r.n + i0 - a.window + 1) : 0;
-  first = lo / kTok * kTok;
-  return max(1, (hi + kTok - 1) / kTok - lo / kTok);
+  seen = a.window > 0 ? max(0, r.kv - r.n + i0 - a.window + 1) : 0;
+  return max(1, (hi + kTok - 1) / kTok - seen / kTok);
 }
 
 // Where a warp stands in its CTA's range, one (request, head, row tile) after
@@ -133,7 +133,7 @@ struct Walk {
   int row0, n, kv;  // the request
   int b, h, q;      // request (within the launch), head, row tile
   int x;            // linear index of the row tile's first unit
-  int first;        // first token of the row tile's first KV tile
+  int seen;         // first token that the row tile sees
   int tiles;        // KV tiles of the row tile
   int t0, t1;       // this piece's
   int more;         // 0 past the last piece
@@ -149,7 +149,7 @@ __device__ __noinline__ void walk_next(const Range& rg, Walk* w) {
   const moe_kv4_attn_args& a = rg.p->a;
   const int group = a.q_heads / a.cache.kv_heads;
   Request r = {w->row0, w->n, w->kv, false};
-  int x = w->x, tiles = w->tiles, q = w->q, first = 0, t1;
+  int x = w->x, tiles = w->tiles, q = w->q, seen = 0, t1;
   do {
     x += tiles + kSetup;
     if (x >= rg.C1) {
@@ -168,12 +168,12 @@ __device__ __noinline__ void walk_next(const Range& rg, Walk* w) {
         w->kv = r.kv;
       }
     }
-    tiles = row_tile_tiles(a, r, group, q, first);
+    tiles = row_tile_tiles(a, r, group, q, seen);
     t1 = min(tiles, rg.C1 - x - kSetup);
   } while (t1 <= 0);
   w->x = x;
   w->q = q;
-  w->first = first;
+  w->seen = seen;
   w->tiles = tiles;
   w->t0 = 0;
   w->t1 = t1;
@@ -224,11 +224,12 @@ __device__ __noinline__ void walk_begin(const Range& rg, Walk* w) {
   __syncwarp();
 }
 
-// A 16-token block of a tile to come: where it lies, its tokens that exist.
+// A 16-token block of a tile to come: where it lies, its tokens that may be
+// used. The others enter as zeros; a key before `from` enters as it is, its
+// score is not used.
 struct Place {
   const uint8_t* src;
-  int left;
-  int hole;         // 0xff: its page is bad
+  int from, to;     // to < 0: the block's page is bad
 };
 constexpr int kPlaces = 8;             // tiles looked up ahead
 
@@ -467,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         it.at = (size_t)(w->row0 + token) * a.q_heads + qh;
         it.hi_tok = a.causal ? kv - w->n + token : kv - 1;
         it.lo_tok = a.window > 0 ? it.hi_tok - a.window + 1 : 0;
-        it.tok0 = w->first + it.t0 * kTok;
+        it.tok0 = w->seen / kTok * kTok + it.t0 * kTok;
         const uint4* src = reinterpret_cast<const uint4*>(a.q + (size_t)(w->row0 + token) * a.q_stride + qh * D);
         // A row's 16-byte chunks come by neighbouring lanes (a row per thread
         // would fetch every sector twice and took 5 us a tile), each thread
@@ -738,16 +739,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       uint4 codes[kWarpBlocks][kLoads];
       uint32_t sf[kWarpBlocks][kLoads];            // two scale bytes each
     } rk, rv;
-    auto load = [&](Raw& r, int j, int at) {       // keys or values of tile j
+    auto load = [&](Raw& r, int j, int at) {       // keys (at 0) or values of tile j
       const int cat = at + tl * L::kCodeRow + 16 * cl, sat = at + L::kKeyScales + tl * L::kScaleRow + 2 * cl;
 #pragma unroll
       for (int x = 0; x < kWarpBlocks; ++x) {
         const Place pl = sm->place[j & (kPlaces - 1)][blk0 + x];
 #pragma unroll
         for (int y = 0; y < kLoads; ++y) {
-          r.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what was not appended enters as zeros
+          r.codes[x][y] = make_uint4(0u, 0u, 0u, 0u);   // what may not have been appended enters as zeros
           r.sf[x][y] = 0u;
-          if (y * kRowsPerLoad + tl < pl.left) {
+          if (y * kRowsPerLoad + tl < pl.to && (at == 0 || y * kRowsPerLoad + tl >= pl.from)) {
             r.codes[x][y] = __ldg(reinterpret_cast<const uint4*>(pl.src + cat + y * kRowsPerLoad * L::kCodeRow));
             r.sf[x][y] = __ldg(reinterpret_cast<const uint16_t*>(pl.src + sat + y * kRowsPerLoad * L::kScaleRow));
           }
@@ -782,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     auto keys = [&](int j) {
       if (!wait(&sm->kv_empty[0][j & 1], (j >> 1) ^ 1)) return false;
       if (lane < kWarpBlocks)
-        sm->hole[j & 3][blk0 + lane] = (uint8_t)sm->place[j & (kPlaces - 1)][blk0 + lane].hole;
+        sm->hole[j & 3][blk0 + lane] = sm->place[j & (kPlaces - 1)][blk0 + lane].to < 0 ? 0xff : 0;
       store(smem_u32(&sm->kv[0][j & 1][0]), rk);
       fence_proxy_async_smem();
       __syncwarp();
@@ -824,17 +825,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
       const int here = j & (kPlaces - 1), more = w->more;
       if (!wait(&sm->place_empty[here], (j / kPlaces) ^ 1)) break;
       if (more && lane < kTok / kKvBlock) {
-        const int tok = w->first + lt * kTok + lane * kKvBlock;
-        Place pl = {nullptr, max(0, w->kv - tok), 0};
-        if (pl.left > 0) {
+        const int tok = w->seen / kTok * kTok + lt * kTok + lane * kKvBlock;
+        // not past the end, nor before every row's window: pages there may have been given back
+        Place pl = {nullptr, w->seen - tok, w->kv - tok};
+        if (pl.from >= kKvBlock || pl.to < 0) pl.to = 0;
+        if (pl.to > 0) {
           const int page = __ldg(a.block_table + (size_t)(p.b0 + w->b) * a.max_pages + (tok >> p_log));
           if (page >= 0 && page < a.cache.num_pages) {
             pl.src = static_cast<const uint8_t*>(a.cache.pool) +
                      kv4_block_offset(page, w->h, Hk, P / kKvBlock, (tok & (P - 1)) / kKvBlock, L::kBytes);
             asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(pl.src), "r"((uint32_t)L::kBytes) : "memory");
           } else {
-            pl.left = 0;
-            pl.hole = 0xff;
+            pl.to = -1;
             set_status(p.status, MOE_ERR_DEVICE);
           }
         }

@@ -139,3 +139,38 @@ def test_windows_near_the_largest_integer(n, window):
     out, lse = s.run(want_lse=True, window=window)
     s.check(out, lse, rows=20)
     assert torch.equal(out, ref) and torch.equal(lse, l0)
+
+
+class Windowed(Scene):
+    """Only what some query sees was ever appended: NaN lies before it in its page, and the pages before are given
+    back: entry -1, or a page that nothing was appended to."""
+
+    def __init__(self, lens, window, blank, *a, **kw):
+        super().__init__(lens, *a, **kw)
+        pool = self.cache.pool.view(-1, self.heads, self.P // 16, 18 * self.D)
+        blank_page = sorted(set(range(pool.shape[0])) - set(self.table[self.table < pool.shape[0]].tolist()))[0]
+        self.shown = 0
+        for b, (kv, n) in enumerate(lens):
+            first = max(0, kv - n + 1 - window)
+            self.shown += first
+            for j in range(first // self.P + 1):
+                if (j + 1) * self.P <= first:
+                    self.table[b, j] = blank_page if blank else -1
+                    continue
+                page = self.table[b, j]
+                for t in range(j * self.P, first):
+                    blk, r = t % self.P // 16, t % 16
+                    for base, row in ((0, self.D // 2), (8 * self.D, self.D // 16), (9 * self.D, self.D // 2),
+                                      (17 * self.D, self.D // 16)):
+                        pool[page, :, blk, base + r * row:base + (r + 1) * row] = 0xFF
+
+
+@pytest.mark.parametrize("qheads,heads,D,P", [(8, 2, 128, 16), (8, 2, 64, 16), (4, 4, 64, 32), (16, 2, 128, 32),
+                                              (5, 1, 128, 64), (32, 2, 64, 64), (4, 1, 128, 128)])
+@pytest.mark.parametrize("n,window", [(1, 1), (1, 100), (2, 37), (9, 100), (100, 100), (300, 333)])
+@pytest.mark.parametrize("blank", [False, True])
+def test_nothing_before_the_window_is_used(qheads, heads, D, P, n, window, blank):
+    s = Windowed([(1000, n), (n + 3, n), (n + 555, n), (n + 129, n)], window, blank, qheads, heads, D, P, seed=n)
+    assert s.shown
+    out, lse = s.run(want_lse=True, window=window)   # and the status word stays clear
+    s.check(out, lse, window=window, rows=5)
