@@ -117,11 +117,11 @@ moe_status moe_kv4_read(const moe_kv4_cache* cache, const int32_t* slots, int n,
  * q_stride that is not a multiple of 8 or smaller than a row, negative sizes,
  * max_q < 1, a non-finite scale, a window without causal ->
  * MOE_ERR_INVALID_ARG; q_heads % kv_heads != 0, head_dim or page_tokens
- * outside the cache's limits, batch > 4096, or more than 2^31 - 1 (request,
- * head, 32 cached tokens) or (256 rows, head, 128 cached tokens) tiles, the
- * table taken as full -> MOE_ERR_UNSUPPORTED; a missing, misaligned or short
- * workspace -> MOE_ERR_WORKSPACE. batch = 0 or total_q = 0 -> MOE_OK with
- * nothing enqueued.
+ * outside the cache's limits, batch > 4096, max_pages * page_tokens > 2^31 -
+ * 129, or more than 2^31 - 1 (request, head, 32 cached tokens) or (256 rows,
+ * head, 128 cached tokens) tiles, the table taken as full ->
+ * MOE_ERR_UNSUPPORTED; a missing, misaligned or short workspace ->
+ * MOE_ERR_WORKSPACE. batch = 0 or total_q = 0 -> MOE_OK with nothing enqueued.
  */
 typedef struct {
   moe_kv4_cache cache;

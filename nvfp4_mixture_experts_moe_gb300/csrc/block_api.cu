@@ -41,7 +41,7 @@ moe_status check_attention(const moe_kv4_attn_args* a) {
   if (!std::isfinite(a->scale)) return MOE_ERR_INVALID_ARG;
   if (a->q_heads % a->cache.kv_heads || a->batch > 4096 || a->q_heads > 65536) return MOE_ERR_UNSUPPORTED;
   const long long row_tokens = (long long)a->max_pages * a->cache.page_tokens;
-  if (row_tokens > INT_MAX) return MOE_ERR_UNSUPPORTED;
+  if (row_tokens > INT_MAX - 128) return MOE_ERR_UNSUPPORTED;   // lengths are rounded up to tiles in 32 bits
   const long long tiles = (row_tokens + 31) / 32;
   if (a->batch > 0 && tiles > INT_MAX / ((long long)a->batch * a->cache.kv_heads)) return MOE_ERR_UNSUPPORTED;
   if ((long long)a->total_q * (a->q_heads / a->cache.kv_heads) > INT_MAX) return MOE_ERR_UNSUPPORTED;
