@@ -156,13 +156,16 @@ __global__ void __launch_bounds__(kMaxThreads) kv_step_kernel(moe_kv_step_args a
     if (bad && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
   }
 
-  for (int i = gthread; i < taken; i += gsize) {
+  // (unsigned: a step past the last of 2^31 - 1 stays an integer past it)
+  for (unsigned next = gthread; next < (unsigned)taken; next += gsize) {
+    const int i = (int)next;
     const int b = last_at_most(first, B, i);  // the last request that starts at or before page i takes it
     const int old = (int)ceil_div(max(a.ctx_len[b], 0), P);
     a.block_table[(size_t)b * a.max_pages + old + (i - first[b])] = a.free_pages[avail - 1 - i];
   }
 
-  for (int t = gthread; t < a.tokens; t += gsize) {
+  for (unsigned next = gthread; next < (unsigned)a.tokens; next += gsize) {
+    const int t = (int)next;
     int slot = -1, pos = 0;
     if (t < cu[B]) {
       const int b = last_at_most(cu, B, t);

@@ -174,3 +174,17 @@ def test_nothing_before_the_window_is_used(qheads, heads, D, P, n, window, blank
     assert s.shown
     out, lse = s.run(want_lse=True, window=window)   # and the status word stays clear
     s.check(out, lse, window=window, rows=5)
+
+
+# ------------------------------------------------------------------- tables
+
+def test_step_with_the_largest_bound_on_tokens():
+    from nvfp4_mixture_experts_moe_gb300 import KvStep
+    n = 2 ** 31 - 1
+    s = KvStep(1, n, 16, 2)
+    s.slots.fill_(7)
+    s.positions.fill_(7)
+    s.run(_cuda([5]), _cuda([3]), _cuda([[4, 0]]), _cuda([1]), _cuda([1]))
+    assert s.slots[:4].tolist() == [69, 70, 71, -1] and s.positions[:4].tolist() == [5, 6, 7, 0]
+    assert int(s.slots[3:].max()) == -1 and int(s.slots[3:].min()) == -1
+    assert int(s.positions[3:].max()) == 0 and int(s.positions[3:].min()) == 0 and int(s.status) == 0
