@@ -152,7 +152,9 @@ moe_status moe_kv4_attention(const moe_kv4_attn_args* args, void* ws, size_t ws_
  * it, or when its tokens would not fit max_pages pages (such a request takes
  * nothing from the ones after it). A request that needs no new page is never
  * refused for lack of pages. A refused request keeps its pages and length;
- * its new tokens get slot -1 and device_status becomes MOE_ERR_DEVICE.
+ * its new tokens get slot -1 and device_status becomes MOE_ERR_DEVICE. A
+ * token whose page id (from the table or the stack) is negative, or gives a
+ * slot past 2^31 - 1, gets slot -1 and is reported too.
  *
  * ctx_len, new_len int32 [batch] (a negative value counts as 0 and is reported)
  * block_table      int32 [batch, max_pages], in place: only the new entries are written

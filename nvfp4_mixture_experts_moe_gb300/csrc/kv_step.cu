@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kMaxThreads) kv_step_kernel(moe_kv_step_args a
                                   : a.free_pages[avail - 1 - (first[b] + page - old)];
         const long long s = (long long)id * P + (pos - page * P);
         slot = id < 0 || s > 0x7fffffff ? -1 : (int)s;
+        if (slot < 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
       }
     }
     a.slots[t] = slot;

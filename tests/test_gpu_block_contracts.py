@@ -188,3 +188,17 @@ def test_step_with_the_largest_bound_on_tokens():
     assert s.slots[:4].tolist() == [69, 70, 71, -1] and s.positions[:4].tolist() == [5, 6, 7, 0]
     assert int(s.slots[3:].max()) == -1 and int(s.slots[3:].min()) == -1
     assert int(s.positions[3:].max()) == 0 and int(s.positions[3:].min()) == 0 and int(s.status) == 0
+
+
+def test_step_reports_a_page_id_that_gives_no_slot():
+    """A request whose last page has room, but whose entry is no page: its token has nowhere to go."""
+    from nvfp4_mixture_experts_moe_gb300 import KvStep
+    for entry in (-1, 2 ** 31 - 1):
+        s = KvStep(2, 3, 16, 2)
+        tb = _cuda([[entry, 0], [4, 0]])
+        s.run(_cuda([5, 15]), _cuda([1, 2]), tb, _cuda([7]), _cuda([1]))
+        assert s.slots.cpu().tolist() == [-1, 4 * 16 + 15, 7 * 16] and s.kv_len.cpu().tolist() == [6, 17]
+        assert int(s.status) == B().MOE_ERR_DEVICE
+    s = KvStep(1, 1, 16, 2)     # and one from the stack
+    s.run(_cuda([16]), _cuda([1]), _cuda([[3, 0]]), _cuda([-2]), _cuda([1]))
+    assert s.slots.cpu().tolist() == [-1] and int(s.status) == B().MOE_ERR_DEVICE
