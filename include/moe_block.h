@@ -159,17 +159,17 @@ moe_status moe_kv4_attention(const moe_kv4_attn_args* args, void* ws, size_t ws_
  * ctx_len, new_len int32 [batch] (a negative value counts as 0 and is reported)
  * block_table      int32 [batch, max_pages], in place: only the new entries are written
  * free_pages       int32 [free_capacity]
- * free_count       int32 [1]; free_count_out int32 [1], another address
- * kv_len           int32 [batch] out, another array than ctx_len: ctx_len +
- *                  new_len, or ctx_len when refused
+ * free_count       int32 [1]; free_count_out int32 [1] out
+ * kv_len           int32 [batch] out: ctx_len + new_len, or ctx_len when refused
  * cu_q             int32 [batch + 1] out: prefix sums of new_len
  * slots, positions int32 [tokens] out: slot and position of each new token, in
  *                  request order; entries past the step's tokens get -1 and 0
  * tokens           host bound on the step's tokens (new tokens past it are
  *                  reported and not written; cu_q stays at the true sums)
  * Errors: batch outside 0..4096 -> MOE_ERR_UNSUPPORTED; page_tokens < 1,
- * max_pages < 1, negative sizes, max_pages * page_tokens > 2^31 - 1, NULL or
- * aliased pointers -> MOE_ERR_INVALID_ARG.
+ * max_pages < 1, negative sizes, max_pages * page_tokens > 2^31 - 1, NULL
+ * pointers, an output that overlaps an input or another output ->
+ * MOE_ERR_INVALID_ARG.
  */
 typedef struct {
   int batch, page_tokens, max_pages, tokens, free_capacity;

@@ -49,6 +49,28 @@ moe_status check_attention(const moe_kv4_attn_args* a) {
   return MOE_OK;
 }
 
+// Whether one of a step's outputs shares memory with an input or another
+// output: CTA 0 writes some of them while other CTAs still read lengths, and
+// the stack and the table are read and written without an order.
+bool step_arrays_overlap(const moe_kv_step_args& a) {
+  struct Array {
+    const int32_t* at;
+    long long n;
+  };
+  const Array arrays[] = {
+      {a.kv_len, a.batch}, {a.cu_q, a.batch + 1ll}, {a.slots, a.tokens}, {a.positions, a.tokens},
+      {a.free_count_out, 1}, {a.block_table, (long long)a.batch * a.max_pages}, {a.device_status, a.device_status ? 1 : 0},
+      // inputs
+      {a.ctx_len, a.batch}, {a.new_len, a.batch}, {a.free_pages, a.free_capacity}, {a.free_count, 1}};
+  constexpr int kOutputs = 7, kArrays = sizeof(arrays) / sizeof(arrays[0]);
+  for (int i = 0; i < kOutputs; ++i)
+    for (int j = i + 1; j < kArrays; ++j) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[i].at), y = reinterpret_cast<uintptr_t>(arrays[j].at);
+      if (arrays[i].n > 0 && arrays[j].n > 0 && x < y + 4 * arrays[j].n && y < x + 4 * arrays[i].n) return true;
+    }
+  return false;
+}
+
 }  // namespace
 }  // namespace moe
 
@@ -120,8 +142,7 @@ moe_status moe_kv_step(const moe_kv_step_args* a, moe_stream_t stream) {
   if (a->batch > 0 && (!a->ctx_len || !a->new_len || !a->block_table || !a->kv_len)) return MOE_ERR_INVALID_ARG;
   if (a->free_capacity > 0 && !a->free_pages) return MOE_ERR_INVALID_ARG;
   if (a->tokens > 0 && (!a->slots || !a->positions)) return MOE_ERR_INVALID_ARG;
-  // read by every CTA while CTA 0 writes the others
-  if (a->free_count == a->free_count_out || (a->batch > 0 && a->ctx_len == a->kv_len)) return MOE_ERR_INVALID_ARG;
+  if (step_arrays_overlap(*a)) return MOE_ERR_INVALID_ARG;
   const moe_status st = check_device();
   if (st != MOE_OK) return st;
   return launch_kv_step(*a, (cudaStream_t)stream);
