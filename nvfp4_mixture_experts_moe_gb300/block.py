@@ -49,6 +49,13 @@ def _like(t, shape, dtype, what):
     return t.data_ptr()
 
 
+def _on(stream):
+    """A context in which torch works on the stream of a call (None: the current one; a Stream; a raw handle)."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
 def _empty(shape, dtype, device, stream, zeros=0):
     """An output or workspace (its first ``zeros`` elements zero) of a call on ``stream``.
 
@@ -61,12 +68,10 @@ def _empty(shape, dtype, device, stream, zeros=0):
             t[:zeros].zero_()
         return t
     here = torch.cuda.current_stream()
-    if not isinstance(stream, torch.cuda.Stream):   # a handle
-        stream = torch.cuda.ExternalStream(int(stream)) if stream else torch.cuda.default_stream()
-    with torch.cuda.stream(stream):
+    with _on(stream):
         t = _empty(shape, dtype, device, None, zeros)
-    if stream.cuda_stream != here.cuda_stream:
-        t.record_stream(here)
+        if torch.cuda.current_stream().cuda_stream != here.cuda_stream:
+            t.record_stream(here)
     return t
 
 
@@ -76,6 +81,10 @@ class Kv4Cache:
     ``k_gs`` and ``v_gs`` are the calibrated global scales in the quant
     convention (2688 / amax). ``pool`` may be given (uint8, layout in
     ``include/moe_block.h``); otherwise it is allocated, uninitialised.
+
+    ``status`` (int32 ``[1]``) keeps what calls without a ``device_status`` or
+    workspace of their own report (MOE_ERR_DEVICE: a slot or page id outside
+    the pool, lengths past a bound; MOE_ERR_TIMEOUT); the caller clears it.
     """
 
     def __init__(self, num_pages, page_tokens, kv_heads, head_dim, k_gs, v_gs, device="cuda", pool=None):
@@ -89,6 +98,7 @@ class Kv4Cache:
         self.num_pages, self.page_tokens = num_pages, page_tokens
         self.kv_heads, self.head_dim = kv_heads, head_dim
         self.pool = pool
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._fields = (num_pages, page_tokens, kv_heads, head_dim, float(k_gs), float(v_gs), pool.data_ptr())
         self.desc = B.MoeKv4Cache(*self._fields)
 
@@ -99,7 +109,8 @@ class Kv4Cache:
         n = k.shape[0]
         if v.shape[0] != n:
             raise ValueError("k and v have different lengths")
-        B.moe_kv4_append(self.desc, kp, vp, ks, vs, _ints(slots, (n,), "slots"), n, device_status, stream)
+        B.moe_kv4_append(self.desc, kp, vp, ks, vs, _ints(slots, (n,), "slots"), n,
+                         self.status if device_status is None else device_status, stream)
 
     def read(self, slots, stream=None, device_status=None):
         """The slots' rows as bf16 (k, v) ``[n, kv_heads, head_dim]``; negative slots give zeros."""
@@ -108,7 +119,8 @@ class Kv4Cache:
         shape = (n, self.kv_heads, self.head_dim)
         k = _empty(shape, _BF16, self.pool.device, stream)
         v = _empty(shape, _BF16, self.pool.device, stream)
-        B.moe_kv4_read(self.desc, at, n, k.data_ptr(), v.data_ptr(), device_status, stream)
+        B.moe_kv4_read(self.desc, at, n, k.data_ptr(), v.data_ptr(),
+                       self.status if device_status is None else device_status, stream)
         return k, v
 
     def attention_workspace(self, total_q, batch, q_heads, max_q, max_pages=1, stream=None):
@@ -127,7 +139,8 @@ class Kv4Cache:
         tokens included, already appended), ``block_table`` int32 ``[batch,
         max_pages]``, ``max_q`` a bound on every request's query rows.
         Returns (out, lse); lse (fp32 ``[total_q, q_heads]``) is None unless
-        wanted or given.
+        wanted or given. Bad device data and waits that gave up are reported
+        in ``ws`` (``moe_get_device_status``), or without one in ``status``.
         """
         total_q, heads = q.shape[0], q.shape[1]
         batch = kv_len.shape[0]
@@ -144,13 +157,17 @@ class Kv4Cache:
         if lse is None and want_lse:
             lse = _empty((total_q, heads), _F32, q.device, stream)
         lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse")
-        if ws is None:
+        own = ws is None
+        if own:
             ws = self.attention_workspace(total_q, batch, heads, max_q, max_pages, stream)
         a = B.PACK_KV4_ATTN.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
                                  _ints(cu_q, (batch + 1,), "cu_q"), _ints(kv_len, (batch,), "kv_len"),
                                  _ints(block_table, (batch, max_pages), "block_table"),
                                  self.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, lp)
         B.moe_kv4_attention(a, ws, stream)
+        if own:
+            with _on(stream):
+                torch.maximum(self.status, ws[:4].view(_I32), out=self.status)
         return out, lse
 
 

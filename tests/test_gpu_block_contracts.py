@@ -202,3 +202,28 @@ def test_step_reports_a_page_id_that_gives_no_slot():
     s = KvStep(1, 1, 16, 2)     # and one from the stack
     s.run(_cuda([16]), _cuda([1]), _cuda([[3, 0]]), _cuda([-2]), _cuda([1]))
     assert s.slots.cpu().tolist() == [-1] and int(s.status) == B().MOE_ERR_DEVICE
+
+
+# ------------------------------------------------------------------ status
+
+def test_cache_keeps_the_status_of_calls_that_were_given_no_place_for_it():
+    s = Scene([(100, 1), (50, 1)], 8, 2, 128, 16, seed=6)
+    c, k = s.cache, _bf16((2, 2, 128), 1).cuda()
+    args = (s.q.cuda(), _cuda(s.cu), _cuda([100, 50]))
+    c.attention(*args, _cuda(s.table), max_q=1)
+    assert c.status.tolist() == [0]
+    c.append(k, k, _cuda([-1, c.num_pages * 16]))
+    assert c.status.tolist() == [B().MOE_ERR_DEVICE]
+    c.attention(*args, _cuda(s.table), max_q=1)       # kept until the caller clears it
+    assert c.status.tolist() == [B().MOE_ERR_DEVICE]
+    c.status.zero_()
+    c.read(_cuda([c.num_pages * 16]))
+    assert c.status.tolist() == [B().MOE_ERR_DEVICE]
+    c.status.zero_()
+    s.table[1, 2] = 10 ** 6
+    c.attention(*args, _cuda(s.table), max_q=1)
+    assert c.status.tolist() == [B().MOE_ERR_DEVICE]
+    c.status.zero_()
+    own = torch.zeros(1, dtype=torch.int32, device="cuda")
+    c.append(k, k, _cuda([-1, c.num_pages * 16]), device_status=own)
+    assert own.tolist() == [B().MOE_ERR_DEVICE] and c.status.tolist() == [0]
