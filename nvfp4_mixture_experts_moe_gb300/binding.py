@@ -177,6 +177,8 @@ def _ptr(t):
 
 
 def _stream(stream):
+    if type(stream) is int:
+        return stream
     if stream is None:
         if torch.cuda.is_initialized():  # the handle alone: building a Stream object takes longer than a launch
             return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())

@@ -19,6 +19,7 @@ from . import binding as B
 
 
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_C = torch._C
 
 
 def _need(ok, what):
@@ -26,27 +27,50 @@ def _need(ok, what):
         raise ValueError(what)
 
 
-def _ints(t, shape, what):
-    if not (t.is_cuda and t.dtype is _I32 and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{what}: a contiguous CUDA int32 tensor of shape {shape} is needed")
+def _where(stream):
+    """The current GPU, where kernels are launched, and the call's stream there as a handle (looked up once a call:
+    each of these takes a good part of a launch's time). Every tensor of the call has to lie on that GPU."""
+    try:
+        dev = _C._cuda_getDevice()
+    except (RuntimeError, AttributeError):   # no driver, or torch without CUDA: no tensor passes (the CPU's are -1)
+        return -2, 0
+    if stream is None:
+        return dev, _C._cuda_getCurrentRawStream(dev)
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != dev:
+            raise ValueError(f"stream: one of GPU {stream.device_index}, the current one is {dev}")
+        return dev, stream.cuda_stream
+    return dev, int(stream)
+
+
+def _ints(t, shape, what, dev):
+    if not (t.get_device() == dev and t.dtype is _I32 and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous int32 tensor of shape {tuple(shape)} on the current GPU is needed")
     return t.data_ptr()
 
 
-def _rows(t, heads, dim, what):
+def _rows(t, heads, dim, what, dev):
     """Address and row stride of a bf16 [n, heads, dim] tensor whose rows' heads are contiguous."""
     n = t.shape[0] if t.dim() == 3 else -1
-    if not (t.is_cuda and t.dtype is _BF16 and t.shape == (n, heads, dim)):
-        raise ValueError(f"{what}: a CUDA bf16 tensor [rows, {heads}, {dim}] is needed")
+    if not (t.get_device() == dev and t.dtype is _BF16 and t.shape == (n, heads, dim)):
+        raise ValueError(f"{what}: a bf16 tensor [rows, {heads}, {dim}] on the current GPU is needed")
     st = t.stride()
     if n > 0 and not (st[2] == 1 and (heads == 1 or st[1] == dim)):
         raise ValueError(f"{what}: a row's heads have to be contiguous")
     return t.data_ptr(), (st[0] if n > 1 else heads * dim)
 
 
-def _like(t, shape, dtype, what):
-    if not (t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
-        raise ValueError(f"{what}: a contiguous CUDA {dtype} tensor of shape {tuple(shape)} is needed")
+def _like(t, shape, dtype, what, dev):
+    if not (t.get_device() == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous()):
+        raise ValueError(f"{what}: a contiguous {dtype} tensor of shape {tuple(shape)} on the current GPU is needed")
     return t.data_ptr()
+
+
+def _status(t, dev):
+    """A ``device_status``: one int32 (or its address)."""
+    if not isinstance(t, int) and not (t.get_device() == dev and t.dtype is _I32 and t.numel() == 1):
+        raise ValueError("device_status: one int32 on the current GPU is needed")
+    return t
 
 
 def _on(stream):
@@ -99,28 +123,35 @@ class Kv4Cache:
         self.kv_heads, self.head_dim = kv_heads, head_dim
         self.pool = pool
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._dev = pool.get_device()
         self._fields = (num_pages, page_tokens, kv_heads, head_dim, float(k_gs), float(v_gs), pool.data_ptr())
         self.desc = B.MoeKv4Cache(*self._fields)
 
     def append(self, k, v, slots, device_status=None, stream=None):
         """bf16 ``[tokens, kv_heads, head_dim]`` rows into the slots (int32; negative ones are skipped)."""
-        kp, ks = _rows(k, self.kv_heads, self.head_dim, "k")
-        vp, vs = _rows(v, self.kv_heads, self.head_dim, "v")
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the cache lies on GPU {self._dev}, the current one is {dev}")
+        kp, ks = _rows(k, self.kv_heads, self.head_dim, "k", dev)
+        vp, vs = _rows(v, self.kv_heads, self.head_dim, "v", dev)
         n = k.shape[0]
         if v.shape[0] != n:
             raise ValueError("k and v have different lengths")
-        B.moe_kv4_append(self.desc, kp, vp, ks, vs, _ints(slots, (n,), "slots"), n,
-                         self.status if device_status is None else device_status, stream)
+        B.moe_kv4_append(self.desc, kp, vp, ks, vs, _ints(slots, (n,), "slots", dev), n,
+                         self.status if device_status is None else _status(device_status, dev), handle)
 
     def read(self, slots, stream=None, device_status=None):
         """The slots' rows as bf16 (k, v) ``[n, kv_heads, head_dim]``; negative slots give zeros."""
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the cache lies on GPU {self._dev}, the current one is {dev}")
         n = slots.shape[0] if slots.dim() == 1 else -1
-        at = _ints(slots, (n,), "slots")
+        at = _ints(slots, (n,), "slots", dev)
         shape = (n, self.kv_heads, self.head_dim)
         k = _empty(shape, _BF16, self.pool.device, stream)
         v = _empty(shape, _BF16, self.pool.device, stream)
         B.moe_kv4_read(self.desc, at, n, k.data_ptr(), v.data_ptr(),
-                       self.status if device_status is None else device_status, stream)
+                       self.status if device_status is None else _status(device_status, dev), handle)
         return k, v
 
     def attention_workspace(self, total_q, batch, q_heads, max_q, max_pages=1, stream=None):
@@ -142,9 +173,12 @@ class Kv4Cache:
         wanted or given. Bad device data and waits that gave up are reported
         in ``ws`` (``moe_get_device_status``), or without one in ``status``.
         """
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the cache lies on GPU {self._dev}, the current one is {dev}")
         total_q, heads = q.shape[0], q.shape[1]
         batch = kv_len.shape[0]
-        qp, qs = _rows(q, heads, self.head_dim, "q")
+        qp, qs = _rows(q, heads, self.head_dim, "q", dev)
         if block_table.dim() != 2:
             raise ValueError("block_table: [batch, max_pages] is needed")
         max_pages = block_table.shape[1]
@@ -153,18 +187,20 @@ class Kv4Cache:
             out = _empty(shape, _BF16, q.device, stream)
             op = out.data_ptr()
         else:
-            op = _like(out, shape, _BF16, "out")
+            op = _like(out, shape, _BF16, "out", dev)
         if lse is None and want_lse:
             lse = _empty((total_q, heads), _F32, q.device, stream)
-        lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse")
+        lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse", dev)
         own = ws is None
         if own:
             ws = self.attention_workspace(total_q, batch, heads, max_q, max_pages, stream)
+        elif ws.get_device() != dev or not ws.is_contiguous():
+            raise ValueError("ws: a contiguous tensor on the current GPU is needed")
         a = B.PACK_KV4_ATTN.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
-                                 _ints(cu_q, (batch + 1,), "cu_q"), _ints(kv_len, (batch,), "kv_len"),
-                                 _ints(block_table, (batch, max_pages), "block_table"),
+                                 _ints(cu_q, (batch + 1,), "cu_q", dev), _ints(kv_len, (batch,), "kv_len", dev),
+                                 _ints(block_table, (batch, max_pages), "block_table", dev),
                                  self.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, lp)
-        B.moe_kv4_attention(a, ws, stream)
+        B.moe_kv4_attention(a, ws, handle)
         if own:
             with _on(stream):
                 torch.maximum(self.status, ws[:4].view(_I32), out=self.status)
@@ -186,6 +222,7 @@ class KvStep:
         made = [torch.empty(n, dtype=torch.int32, device=device) for n in (batch, batch + 1, tokens, tokens, 1)]
         self.kv_len, self.cu_q, self.slots, self.positions, self.free_count = made
         self.status = torch.zeros(1, dtype=torch.int32, device=device)
+        self._dev = self.status.get_device()
         self._outs = [t.data_ptr() for t in (self.free_count, self.kv_len, self.cu_q, self.slots, self.positions,
                                              self.status)]
 
@@ -197,20 +234,23 @@ class KvStep:
         ``ctx_len`` and ``free_count`` are copies of ``kv_len`` and
         ``self.free_count`` (they may not be these very tensors).
         """
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the step's outputs lie on GPU {self._dev}, the current one is {dev}")
         b = self.batch
         cap = free_pages.shape[0] if free_pages.dim() == 1 else -1
-        a = B.PACK_KV_STEP.pack(b, self.page_tokens, self.max_pages, self.tokens, cap, _ints(ctx_len, (b,), "ctx_len"),
-                                _ints(new_len, (b,), "new_len"),
-                                _ints(block_table, (b, self.max_pages), "block_table"),
-                                _ints(free_pages, (cap,), "free_pages"), _ints(free_count, (1,), "free_count"),
-                                *self._outs)
-        B.moe_kv_step(a, stream)
+        a = B.PACK_KV_STEP.pack(b, self.page_tokens, self.max_pages, self.tokens, cap,
+                                _ints(ctx_len, (b,), "ctx_len", dev), _ints(new_len, (b,), "new_len", dev),
+                                _ints(block_table, (b, self.max_pages), "block_table", dev),
+                                _ints(free_pages, (cap,), "free_pages", dev),
+                                _ints(free_count, (1,), "free_count", dev), *self._outs)
+        B.moe_kv_step(a, handle)
         return self
 
 
-def _matrix(t, T, H, what):
-    if not (t.is_cuda and t.dtype is _BF16 and t.shape == (T, H)):
-        raise ValueError(f"{what}: a CUDA bf16 tensor [{T}, {H}] is needed")
+def _matrix(t, T, H, what, dev):
+    if not (t.get_device() == dev and t.dtype is _BF16 and t.shape == (T, H)):
+        raise ValueError(f"{what}: a bf16 tensor [{T}, {H}] on the current GPU is needed")
     st = t.stride()
     if st[1] != 1 and H > 1:
         raise ValueError(f"{what}: contiguous rows are needed")
@@ -227,36 +267,37 @@ def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1
     ``gate`` bf16 ``[T, H]`` or ``[H]``. Returns (r, out); out is None without
     ``w_pre``. ``residual_out`` may be ``residual`` itself.
     """
-    dtype = residual.dtype
-    if not (residual.is_cuda and residual.dim() == 2 and (dtype is _BF16 or dtype is _F32)):
-        raise ValueError("residual: a CUDA bf16 or fp32 tensor [T, H] is needed")
+    (dev, handle), dtype = _where(stream), residual.dtype
+    if not (residual.get_device() == dev and residual.dim() == 2 and (dtype is _BF16 or dtype is _F32)):
+        raise ValueError("residual: a bf16 or fp32 tensor [T, H] on the current GPU is needed")
     T, H = shape = residual.shape
     rs = residual.stride()
     if rs[1] != 1 and H > 1:
         raise ValueError("residual: contiguous rows are needed")
-    xp, xs = (0, 0) if x is None else _matrix(x, T, H, "x")
+    xp, xs = (0, 0) if x is None else _matrix(x, T, H, "x", dev)
     if gate is None:
         gp, gst = 0, 0
     elif gate.dim() == 1:
-        gp, gst = _like(gate, (H,), _BF16, "gate"), 0
+        gp, gst = _like(gate, (H,), _BF16, "gate", dev), 0
     else:
-        gp, gst = _matrix(gate, T, H, "gate")
+        gp, gst = _matrix(gate, T, H, "gate", dev)
     if residual_out is None:
         residual_out = _empty(shape, dtype, residual.device, stream)
         rp = residual_out.data_ptr()
     else:
-        rp = _like(residual_out, shape, dtype, "residual_out")
+        rp = _like(residual_out, shape, dtype, "residual_out", dev)
     if w_pre is None:
         out, op, wp = None, 0, 0
     else:
-        wp = _like(w_pre, (H,), _BF16, "w_pre")
+        wp = _like(w_pre, (H,), _BF16, "w_pre", dev)
         if out is None:
             out = _empty(shape, _BF16, residual.device, stream)
             op = out.data_ptr()
         else:
-            op = _like(out, shape, _BF16, "out")
+            op = _like(out, shape, _BF16, "out", dev)
     a = B.PACK_BLOCK_NORM.pack(T, H, xp, xs, gp, gst, residual.data_ptr(), rs[0] if T > 1 else H,
-                               1 if dtype is _F32 else 0, 0 if w_post is None else _like(w_post, (H,), _BF16, "w_post"),
-                               wp, residual_scale, branch_scale, eps, w_offset, rp, op)
-    B.moe_block_norm(a, stream)
+                               1 if dtype is _F32 else 0,
+                               0 if w_post is None else _like(w_post, (H,), _BF16, "w_post", dev), wp, residual_scale,
+                               branch_scale, eps, w_offset, rp, op)
+    B.moe_block_norm(a, handle)
     return residual_out, out

@@ -63,3 +63,105 @@ def test_step_arrays_of_no_length_overlap_nothing(L):  # noqa: F811
     d, _ = _step()
     _, a = _step(tokens=0, slots=d["ctx_len"], positions=d["ctx_len"], device_status=None)
     assert L.moe_kv_step(ctypes.byref(a), None) not in (B.MOE_OK, B.MOE_ERR_INVALID_ARG)
+
+
+# ------------------------------------------------------------------- devices
+
+class Fake:
+    """Answers as a contiguous tensor on a GPU would."""
+    is_cuda, device = True, torch.device("cpu")
+
+    def __init__(self, gpu, dtype, *shape):
+        self.gpu, self.dtype, self.shape = gpu, dtype, torch.Size(shape)
+
+    def get_device(self):
+        return self.gpu
+
+    def dim(self):
+        return len(self.shape)
+
+    def numel(self):
+        return self.shape.numel()
+
+    def element_size(self):
+        return self.dtype.itemsize
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return torch.empty(self.shape, device="meta").stride()
+
+    def data_ptr(self):
+        return 256
+
+
+BF, I32, U8 = torch.bfloat16, torch.int32, torch.uint8
+
+
+def _calls(block, gpu=0, cache_gpu=0, **where):
+    """Every call of block.py with the named arguments on another GPU."""
+    def f(name, dtype, *shape):
+        return Fake(where.get(name, gpu), dtype, *shape)
+    cache = block.Kv4Cache(4, 16, 2, 64, 1.0, 1.0, pool=Fake(cache_gpu, U8, 4 * 16 * 2 * 72))
+    cache.status = Fake(cache_gpu, I32, 1)
+    step = block.KvStep(2, 5, 16, 4, device="cpu")
+    step._dev = cache_gpu
+    return {
+        "append": lambda: cache.append(f("k", BF, 5, 2, 64), f("v", BF, 5, 2, 64), f("slots", I32, 5),
+                                       device_status=f("device_status", I32, 1)),
+        "read": lambda: cache.read(f("slots", I32, 5), device_status=f("device_status", I32, 1)),
+        "attention": lambda: cache.attention(
+            f("q", BF, 5, 4, 64), f("cu_q", I32, 3), f("kv_len", I32, 2), f("block_table", I32, 2, 4), max_q=3,
+            out=f("out", BF, 5, 4, 64), lse=f("lse", torch.float32, 5, 4), ws=f("ws", U8, 1 << 30)),
+        "step": lambda: step.run(f("ctx_len", I32, 2), f("new_len", I32, 2), f("block_table", I32, 2, 4),
+                                 f("free_pages", I32, 9), f("free_count", I32, 1)),
+        "norm": lambda: block.block_norm(f("x", BF, 3, 8), f("residual", BF, 3, 8), gate=f("gate", BF, 3, 8),
+                                         w_post=f("w", BF, 8), w_pre=f("w_pre", BF, 8), out=f("out", BF, 3, 8),
+                                         residual_out=f("residual_out", BF, 3, 8)),
+        "norm, gate per channel": lambda: block.block_norm(f("x", BF, 3, 8), f("residual", BF, 3, 8), gate=f("gate", BF, 8),
+                                                           w_pre=f("w_pre", BF, 8))}
+
+
+@pytest.fixture
+def block(monkeypatch, L):  # noqa: F811
+    """The module, with GPU 0 the current one and the C calls replaced by a record of them."""
+    from nvfp4_mixture_experts_moe_gb300 import block as module
+    reached = []
+    for name in ("moe_kv4_append", "moe_kv4_read", "moe_kv4_attention", "moe_kv_step", "moe_block_norm"):
+        monkeypatch.setattr(module.B, name, lambda *a, name=name: reached.append(name))
+    monkeypatch.setattr(module, "_where", lambda stream: (0, 0), raising=False)
+    module.reached = reached
+    yield module
+    del module.reached
+
+
+@pytest.mark.parametrize("call,names", [
+    ("append", ("k", "v", "slots", "device_status")), ("read", ("slots", "device_status")),
+    ("attention", ("q", "cu_q", "kv_len", "block_table", "out", "lse", "ws")),
+    ("step", ("ctx_len", "new_len", "block_table", "free_pages", "free_count")),
+    ("norm", ("x", "residual", "gate", "w", "w_pre", "out", "residual_out")), ("norm, gate per channel", ("gate",))])
+@pytest.mark.parametrize("gpu", [1, -1])
+def test_tensors_elsewhere_are_refused(block, call, names, gpu):
+    """On another GPU, or on the CPU."""
+    _calls(block)[call]()
+    for name in names:
+        with pytest.raises(ValueError):
+            _calls(block, **{name: gpu})[call]()
+    assert len(block.reached) == 1      # the one above
+
+
+@pytest.mark.parametrize("call", ["append", "read", "attention", "step"])
+def test_a_cache_or_step_of_another_gpu_is_refused(block, call):
+    with pytest.raises(ValueError):
+        _calls(block, cache_gpu=1)[call]()
+    assert not block.reached
+
+
+def test_cpu_tensors_are_refused(L):  # noqa: F811
+    from nvfp4_mixture_experts_moe_gb300 import Kv4Cache, KvStep, block_norm
+    x, i = torch.zeros(3, 64, dtype=BF), torch.zeros(3, dtype=I32)
+    for bad in (lambda: block_norm(x, x), lambda: KvStep(3, 3, 16, 1, device="cpu").run(i, i, i[:, None], i, i[:1]),
+                lambda: Kv4Cache(2, 16, 2, 64, 1.0, 1.0, device="cpu")):
+        with pytest.raises(ValueError):
+            bad()
