@@ -8,16 +8,19 @@ the residual and the norm before the next block (``moe_block_norm``). The C
 calls and their contracts are in ``include/moe_block.h``; torch only
 allocates. A call runs on the current stream, or on ``stream=`` (a Stream or
 a raw handle), on which its outputs and its own workspace are then made; what
-the caller passes in has to be ready there. Wrong shapes, types or devices raise ``ValueError``; what the C
-call refuses raises ``MoeError``.
+the caller passes in has to be ready there. Wrong shapes, types or devices
+raise ``ValueError``; what the C call refuses raises ``MoeError``.
 """
 from __future__ import annotations
+
+import struct
 
 import torch
 
 from . import binding as B
 
 
+_UNPACKABLE = (struct.error, OverflowError)   # a number of the caller's that is none, or does not fit its field
 _BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
 _C = torch._C
 
@@ -51,8 +54,9 @@ def _ints(t, shape, what, dev):
 
 def _rows(t, heads, dim, what, dev):
     """Address and row stride of a bf16 [n, heads, dim] tensor whose rows' heads are contiguous."""
-    n = t.shape[0] if t.dim() == 3 else -1
-    if not (t.get_device() == dev and t.dtype is _BF16 and t.shape == (n, heads, dim)):
+    shape = t.shape
+    n = shape[0] if len(shape) == 3 else -1
+    if not (t.get_device() == dev and t.dtype is _BF16 and shape == (n, heads, dim)):
         raise ValueError(f"{what}: a bf16 tensor [rows, {heads}, {dim}] on the current GPU is needed")
     st = t.stride()
     if n > 0 and not (st[2] == 1 and (heads == 1 or st[1] == dim)):
@@ -123,7 +127,7 @@ class Kv4Cache:
         self.kv_heads, self.head_dim = kv_heads, head_dim
         self.pool = pool
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        self._dev = pool.get_device()
+        self._dev, self._scale = pool.get_device(), head_dim ** -0.5
         self._fields = (num_pages, page_tokens, kv_heads, head_dim, float(k_gs), float(v_gs), pool.data_ptr())
         self.desc = B.MoeKv4Cache(*self._fields)
 
@@ -176,12 +180,13 @@ class Kv4Cache:
         dev, handle = _where(stream)
         if dev != self._dev:
             raise ValueError(f"the cache lies on GPU {self._dev}, the current one is {dev}")
-        total_q, heads = q.shape[0], q.shape[1]
-        batch = kv_len.shape[0]
+        try:
+            total_q, heads, _ = q.shape
+            batch, = kv_len.shape
+            _, max_pages = block_table.shape
+        except ValueError:
+            raise ValueError("q [rows, heads, dim], kv_len [batch] and block_table [batch, max_pages] are needed") from None
         qp, qs = _rows(q, heads, self.head_dim, "q", dev)
-        if block_table.dim() != 2:
-            raise ValueError("block_table: [batch, max_pages] is needed")
-        max_pages = block_table.shape[1]
         shape = (total_q, heads, self.head_dim)
         if out is None:
             out = _empty(shape, _BF16, q.device, stream)
@@ -194,12 +199,15 @@ class Kv4Cache:
         own = ws is None
         if own:
             ws = self.attention_workspace(total_q, batch, heads, max_q, max_pages, stream)
-        elif ws.get_device() != dev or not ws.is_contiguous():
-            raise ValueError("ws: a contiguous tensor on the current GPU is needed")
-        a = B.PACK_KV4_ATTN.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
-                                 _ints(cu_q, (batch + 1,), "cu_q", dev), _ints(kv_len, (batch,), "kv_len", dev),
-                                 _ints(block_table, (batch, max_pages), "block_table", dev),
-                                 self.head_dim ** -0.5 if scale is None else scale, 1 if causal else 0, window, op, lp)
+        elif ws.get_device() != dev:
+            raise ValueError("ws: a tensor on the current GPU is needed")
+        try:
+            a = B.PACK_KV4_ATTN.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
+                                     _ints(cu_q, (batch + 1,), "cu_q", dev), _ints(kv_len, (batch,), "kv_len", dev),
+                                     _ints(block_table, (batch, max_pages), "block_table", dev),
+                                     self._scale if scale is None else scale, 1 if causal else 0, window, op, lp)
+        except _UNPACKABLE as e:
+            raise ValueError(f"max_q, scale or window: {e}") from None
         B.moe_kv4_attention(a, ws, handle)
         if own:
             with _on(stream):
@@ -295,9 +303,12 @@ def block_norm(x, residual, gate=None, w_post=None, w_pre=None, residual_scale=1
             op = out.data_ptr()
         else:
             op = _like(out, shape, _BF16, "out", dev)
-    a = B.PACK_BLOCK_NORM.pack(T, H, xp, xs, gp, gst, residual.data_ptr(), rs[0] if T > 1 else H,
-                               1 if dtype is _F32 else 0,
-                               0 if w_post is None else _like(w_post, (H,), _BF16, "w_post", dev), wp, residual_scale,
-                               branch_scale, eps, w_offset, rp, op)
+    try:
+        a = B.PACK_BLOCK_NORM.pack(T, H, xp, xs, gp, gst, residual.data_ptr(), rs[0] if T > 1 else H,
+                                   1 if dtype is _F32 else 0,
+                                   0 if w_post is None else _like(w_post, (H,), _BF16, "w_post", dev), wp,
+                                   residual_scale, branch_scale, eps, w_offset, rp, op)
+    except _UNPACKABLE as e:
+        raise ValueError(f"scales, eps or w_offset: {e}") from None
     B.moe_block_norm(a, handle)
     return residual_out, out

@@ -165,3 +165,39 @@ def test_cpu_tensors_are_refused(L):  # noqa: F811
                 lambda: Kv4Cache(2, 16, 2, 64, 1.0, 1.0, device="cpu")):
         with pytest.raises(ValueError):
             bad()
+
+
+# -------------------------------------------------------------------- shapes
+
+def _attention(block, **kw):
+    cache = block.Kv4Cache(4, 16, 2, 64, 1.0, 1.0, pool=Fake(0, U8, 4 * 16 * 2 * 72))
+    cache.status = Fake(0, I32, 1)
+    a = dict(q=Fake(0, BF, 5, 4, 64), cu_q=Fake(0, I32, 3), kv_len=Fake(0, I32, 2), block_table=Fake(0, I32, 2, 4), max_q=3,
+             ws=Fake(0, U8, 1 << 30))
+    return cache.attention(**{**a, **kw})
+
+
+def test_wrong_shapes_and_numbers_are_value_errors(block):
+    _attention(block)
+    for bad in (dict(q=Fake(0, BF, 5)), dict(q=Fake(0, BF, 5, 256)), dict(q=Fake(0, BF)), dict(q=Fake(0, BF, 5, 4, 64, 1)),
+                dict(kv_len=Fake(0, I32)), dict(kv_len=Fake(0, I32, 2, 1)), dict(kv_len=Fake(0, I32, 3)),
+                dict(cu_q=Fake(0, I32)), dict(cu_q=Fake(0, I32, 2)), dict(block_table=Fake(0, I32, 2)),
+                dict(block_table=Fake(0, I32, 1, 4)), dict(max_q=2 ** 31), dict(max_q=1.5), dict(window=2 ** 31),
+                dict(window=-2 ** 32), dict(scale="1")):
+        with pytest.raises(ValueError):
+            _attention(block, **bad)
+    f = Fake(0, BF, 3, 8)
+    for bad in (dict(eps="1"), dict(branch_scale=None), dict(gate=Fake(0, BF)),
+                dict(gate=Fake(0, BF, 3, 8, 1)), dict(x=Fake(0, BF, 8))):
+        with pytest.raises(ValueError):
+            block.block_norm(**{**dict(x=f, residual=f), **bad})
+    for bad in (Fake(0, BF), Fake(0, BF, 8)):
+        with pytest.raises(ValueError):
+            block.block_norm(f, bad)
+    assert block.reached == ["moe_kv4_attention"]
+    with pytest.raises(ValueError):
+        block.Kv4Cache(4, 16, 2, 64, 1.0, 1.0, pool=Fake(0, U8, 4 * 16 * 2 * 72)).append(
+            Fake(0, BF, 5, 2, 64), Fake(0, BF, 5, 2, 64), Fake(0, I32))
+    for shape in ((), (3, 1)):
+        with pytest.raises(ValueError):
+            block.Kv4Cache(4, 16, 2, 64, 1.0, 1.0, pool=Fake(0, U8, 4 * 16 * 2 * 72)).read(Fake(0, I32, *shape))
