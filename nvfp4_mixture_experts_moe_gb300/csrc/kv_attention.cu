@@ -9,11 +9,13 @@ namespace moe {
 // which streams the cache at its rate with rows padded to 8 or 16, above that
 // the tcgen05 kernel, whose tiles hold 128 rows. Lengths live on the device,
 // so a call whose max_q allows both kinds launches both and each skips the
-// other's requests; a call of one request needs only the kernel for max_q.
+// other's requests; a call of one request needs only the kernel for max_q, and
+// a group of more query heads than the first takes rows only the second.
 static int decode_rows(const moe_kv4_attn_args& a) {
-  const long long rows = (long long)a.max_q * (a.q_heads / a.cache.kv_heads);
+  const int group = a.q_heads / a.cache.kv_heads;
+  const long long rows = (long long)a.max_q * group;
   if (rows <= kKvDecodeRows) return (int)rows;
-  return a.batch == 1 ? 0 : kKvDecodeRows;
+  return a.batch == 1 || group > kKvDecodeRows ? 0 : kKvDecodeRows;
 }
 
 static bool any_prompt(const moe_kv4_attn_args& a) {
@@ -21,8 +23,10 @@ static bool any_prompt(const moe_kv4_attn_args& a) {
 }
 
 // The two kernels of a call overlap: each has its own part of the workspace.
+// A workspace serves calls of any smaller size, fewer query heads among them,
+// so a group too wide for the first kernel leaves its part in.
 static size_t decode_ws_bytes(const moe_kv4_attn_args& a) {
-  const int few = decode_rows(a);
+  const int few = any_prompt(a) ? (a.batch == 1 ? 0 : kKvDecodeRows) : decode_rows(a);
   return few > 0 ? align_up(kv4_decode_ws_floats(a.cache.head_dim, few) * sizeof(float)) : 0;
 }
 

@@ -201,3 +201,18 @@ def test_wrong_shapes_and_numbers_are_value_errors(block):
     for shape in ((), (3, 1)):
         with pytest.raises(ValueError):
             block.Kv4Cache(4, 16, 2, 64, 1.0, 1.0, pool=Fake(0, U8, 4 * 16 * 2 * 72)).read(Fake(0, I32, *shape))
+
+
+def test_a_workspace_serves_every_smaller_call(L):  # noqa: F811
+    from nvfp4_mixture_experts_moe_gb300 import binding as B
+
+    def size(batch, heads, max_q, dim):
+        return B.moe_kv4_attention_workspace_size(
+            _attn(B, cache=_cache(B, kv_heads=1, head_dim=dim), batch=batch, q_heads=heads, max_q=max_q, total_q=batch * max_q))
+    for dim in (64, 128):
+        for batch in (1, 2, 9):
+            for heads in (1, 8, 12, 16, 17, 32, 64):
+                for max_q in (1, 2, 3, 16, 17, 100):
+                    most = size(batch, heads, max_q, dim)
+                    assert all(0 < size(b, h, m, dim) <= most for b in (1, 2, 9) if b <= batch
+                               for h in (1, 4, 8, 16, 17, 24, 32) if h <= heads for m in (1, 2, 5, 16, 40) if m <= max_q)

@@ -227,3 +227,15 @@ def test_cache_keeps_the_status_of_calls_that_were_given_no_place_for_it():
     own = torch.zeros(1, dtype=torch.int32, device="cuda")
     c.append(k, k, _cuda([-1, c.num_pages * 16]), device_status=own)
     assert own.tolist() == [B().MOE_ERR_DEVICE] and c.status.tolist() == [0]
+
+
+@pytest.mark.parametrize("group,n,launches", [(24, 1, 2), (17, 3, 2), (16, 1, 1), (16, 2, 3), (8, 2, 1), (8, 3, 3)])
+def test_only_kernels_that_can_have_work_are_launched(group, n, launches):
+    """One launch for at most 16 rows per key/value head, two for more, all three where a request may have either."""
+    s = Scene([(100, n), (50, n)], group, 1, 64, 16, seed=6)
+    args = (s.q.cuda(), _cuda(s.cu), _cuda([100, 50]), _cuda(s.table))
+    ws = s.cache.attention_workspace(s.total, 2, group, n, s.W)
+    before = B().lib().moe_kernel_launches()
+    out, lse = s.cache.attention(*args, max_q=n, want_lse=True, ws=ws)
+    assert B().lib().moe_kernel_launches() - before == launches
+    s.check(out, lse)
