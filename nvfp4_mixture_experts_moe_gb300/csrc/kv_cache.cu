@@ -12,6 +12,8 @@
 // each the two kernels spend some 3 us on launch, first loads and last
 // stores, and issue instructions in two of three cycles (200 a warp and 512
 // elements: three correctly rounded divisions among them).
+#include <cmath>
+
 #include "kernels.cuh"
 #include "kv4.cuh"
 
@@ -49,16 +51,45 @@ moe_status launch_cache(K kernel, int D, int Hk, int tokens, cudaStream_t s, A..
 }
 
 // The cache with what every thread would work out again: page_tokens is a
-// power of two, and the division that decodes is one by a constant.
+// power of two. Keys' and values' global scales: gs itself for append, for
+// read, which divides by it, its reciprocal as the sum of two floats.
 struct Cache {
   uint8_t* pool;
   int slots, heads, page_log;
-  float gs[2], inv_gs[2];   // keys, values
+  float2 gs[2];
 };
 
-Cache cache_of(const moe_kv4_cache& c) {
+float2 reciprocal(float gs) {
+  const double inv = 1.0 / gs;
+  const float x = (float)inv;
+  return {x, std::isfinite(x) ? (float)(inv - x) : 0.0f};
+}
+
+Cache cache_of(const moe_kv4_cache& c, float2 k_gs, float2 v_gs) {
   return {static_cast<uint8_t*>(c.pool), c.num_pages * c.page_tokens, c.kv_heads, __builtin_ctz(c.page_tokens),
-          {c.k_gs, c.v_gs}, {1.0f / c.k_gs, 1.0f / c.v_gs}};
+          {k_gs, v_gs}};
+}
+
+// e * scale / gs of a pair of codes, rounded once to bf16: e * (t + rest) is
+// truncated to fp32 and its last bit set (round to odd) before it is rounded.
+// e * scale has at most six significant bits, so the quotient is either a bf16
+// value, which the last bit does not move, or not half way between two, and
+// what was cut off no longer counts. (e * scale times the rounded reciprocal
+// in fp32 is off in one of some 50,000 values.)
+__device__ __forceinline__ uint32_t quotients(uint32_t e_f16x2, uint64_t t, uint64_t rest) {
+  const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&e_f16x2));
+  uint32_t x, y;
+  asm("{\n .reg .b64 e, r;\n mov.b64 e, {%2, %3};\n mul.rn.f32x2 r, e, %5;\n fma.rz.f32x2 r, e, %4, r;\n"
+      " mov.b64 {%0, %1}, r;\n}"
+      : "=r"(x), "=r"(y)
+      : "f"(e.x), "f"(e.y), "l"(t), "l"(rest));
+  return float2_to_bf16x2_bits(__uint_as_float(x | 1u), __uint_as_float(y | 1u));
+}
+
+__device__ __forceinline__ uint64_t twice(float x) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(x));
+  return r;
 }
 
 // The block of a slot, and the row within it.
@@ -121,7 +152,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     }
     amax = amax16(w);
   }
-  const float gs = c.gs[p.kv];
+  const float gs = c.gs[p.kv].x;
   const uint32_t scale = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
   const float sval = e4m3_decode(scale);
   uint32_t lo = 0, hi = 0;
@@ -161,21 +192,16 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     const uint8_t* blk = slot_row<D>(c, slot, p.h, row) + (p.kv ? L::kValueCodes : 0);
     const uint2 codes = *reinterpret_cast<const uint2*>(blk + row * L::kCodeRow + p.blk * 8);
     const float s = e4m3_decode(blk[L::kKeyScales + row * L::kScaleRow + p.blk]);
-    const float inv = c.inv_gs[p.kv];
-    uint32_t h2[8];
+    const float2 inv = c.gs[p.kv];
+    const float t = s * inv.x;
+    const uint64_t t2 = twice(t), rest2 = twice(fmaf(s, inv.x, -t) + s * inv.y);
     uint32_t a[4], b[4];
     cvt_e2m1x8_f16(codes.x, a);
     cvt_e2m1x8_f16(codes.y, b);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      h2[j] = a[j];
-      h2[4 + j] = b[j];
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float2 e = __half22float2(*reinterpret_cast<const __half2*>(&h2[j]));
-      // code * scale is exact in fp32
-      o[j] = float2_to_bf16x2_bits(e.x * s * inv, e.y * s * inv);
+      o[j] = quotients(a[j], t2, rest2);
+      o[4 + j] = quotients(b[j], t2, rest2);
     }
   }
   if constexpr (kWide) {
@@ -194,7 +220,8 @@ moe_status launch_kv4_append(const moe_kv4_cache& c, const uint16_t* k, const ui
                     k_stride % 16 == 0 && v_stride % 16 == 0;
   auto kern = c.head_dim == 64 ? (wide ? kv4_append_kernel<64, true> : kv4_append_kernel<64, false>)
                                : (wide ? kv4_append_kernel<128, true> : kv4_append_kernel<128, false>);
-  return launch_cache(kern, c.head_dim, c.kv_heads, tokens, s, cache_of(c), k, v, k_stride, v_stride, slots, tokens, status);
+  return launch_cache(kern, c.head_dim, c.kv_heads, tokens, s, cache_of(c, {c.k_gs, 0.0f}, {c.v_gs, 0.0f}), k, v, k_stride,
+                      v_stride, slots, tokens, status);
 }
 
 moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, uint16_t* k_out, uint16_t* v_out,
@@ -202,7 +229,8 @@ moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, 
   const bool wide = reinterpret_cast<uintptr_t>(k_out) % 32 == 0 && reinterpret_cast<uintptr_t>(v_out) % 32 == 0;
   auto kern = c.head_dim == 64 ? (wide ? kv4_read_kernel<64, true> : kv4_read_kernel<64, false>)
                                : (wide ? kv4_read_kernel<128, true> : kv4_read_kernel<128, false>);
-  return launch_cache(kern, c.head_dim, c.kv_heads, n, s, cache_of(c), slots, n, k_out, v_out, status);
+  return launch_cache(kern, c.head_dim, c.kv_heads, n, s, cache_of(c, reciprocal(c.k_gs), reciprocal(c.v_gs)), slots, n,
+                      k_out, v_out, status);
 }
 
 }  // namespace moe

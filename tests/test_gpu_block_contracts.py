@@ -1,4 +1,6 @@
 """Corners of the block operators' contracts (include/moe_block.h) on the GPU."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -239,3 +241,32 @@ def test_only_kernels_that_can_have_work_are_launched(group, n, launches):
     out, lse = s.cache.attention(*args, max_q=n, want_lse=True, ws=ws)
     assert B().lib().moe_kernel_launches() - before == launches
     s.check(out, lse)
+
+
+def _to_bf16(x):
+    """A Fraction to the nearest bf16 (normal range), ties to even."""
+    if x == 0:
+        return 0.0
+    e = Fraction(2) ** (np.frexp(float(abs(x)))[1] - 8)
+    return float(round(x / e) * e)      # round() of a Fraction is to even
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("gs", [6.7855424880981445, 448.0, 333.25, 112.0])
+def test_read_rounds_once(D, gs):
+    """Every code with every scale: e2m1 * e4m3 / gs, exactly, to the nearest bf16."""
+    from nvfp4_mixture_experts_moe_gb300 import Kv4Cache
+    from oracle import nvfp4
+    gs = float(np.float32(gs))
+    c = Kv4Cache(8, 16, 1, D, gs, gs)
+    scale = (np.arange(128 * D // 16) % 127).astype(np.uint8).reshape(8, 16, D // 16)
+    codes = np.tile(np.arange(16, dtype=np.uint8), (8, 16, D // 16))
+    half = np.concatenate([nvfp4.pack(codes.reshape(-1, D)).reshape(8, -1), scale.reshape(8, -1)], axis=1)
+    c.pool.copy_(torch.from_numpy(np.concatenate([half, half], axis=1).reshape(-1)))
+    k, v = c.read(_cuda(np.arange(128)))
+    mag = [0, 0.5, 1, 1.5, 2, 3, 4, 6]
+    val = [Fraction(m) for m in mag] + [-Fraction(m) for m in mag]
+    e4m3 = nvfp4.e4m3_decode(np.arange(127, dtype=np.uint8))
+    want = {(s, i): _to_bf16(val[i] * Fraction(float(e4m3[s])) / Fraction(gs)) for s in range(127) for i in range(16)}
+    ref = np.array([[want[int(s), i] for s in row for i in range(16)] for row in scale.reshape(128, -1)])
+    assert (k[:, 0].double().cpu().numpy() == ref).all() and (v[:, 0].double().cpu().numpy() == ref).all()
