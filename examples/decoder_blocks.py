@@ -84,7 +84,8 @@ class Server:
         self.length = torch.zeros(batch, dtype=torch.int32, device="cuda")
 
     def step(self, tokens, new):
-        """Feeds ``new[b]`` tokens of each request (``tokens``: all of them in order); the next token of each."""
+        """Feeds ``new[b]`` tokens of each request (``tokens``: all of them in order); the next token of each, -1 for one
+        that was fed nothing."""
         counts = torch.tensor(new, dtype=torch.int32, device="cuda")
         s = self.tables.run(self.length, counts, self.block_table, self.free_pages, self.free_count)
         h, x = block_norm(None, self.embedding[tokens], w_pre=self.norm, eps=EPS)
@@ -93,7 +94,14 @@ class Server:
         self.length.copy_(s.kv_len)
         self.free_count.copy_(s.free_count)
         last = s.cu_q[1:].long() - 1
-        return (x[last] @ self.head.t()).argmax(dim=-1)
+        return torch.where(counts > 0, (x[last] @ self.head.t()).argmax(dim=-1), -1)
+
+    def finish(self, request):
+        """Puts a request's pages back on the stack; its slot is empty then."""
+        pages, count = -(-int(self.length[request]) // PAGE), int(self.free_count)
+        self.free_pages[count:count + pages] = self.block_table[request, :pages]
+        self.free_count += pages
+        self.length[request] = 0
 
 
 def main():
@@ -108,7 +116,10 @@ def main():
     refused = int(server.tables.status)
     for b, row in enumerate(torch.stack(text, dim=1).tolist()):
         print(f"request {b}: {prompts[b]} prompt tokens, then {row}")
-    print(f"{int(server.free_count)} of {NUM_PAGES} pages free, status {refused}")
+    held = NUM_PAGES - int(server.free_count)
+    for b in range(len(prompts)):
+        server.finish(b)
+    print(f"{held} pages held, {int(server.free_count)} of {NUM_PAGES} free at the end, status {refused}")
     return refused
 
 

@@ -5,7 +5,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_block import B, Scene, _bf16, _cuda, built  # noqa: F401
+from test_gpu_block import B, Scene, _bf16, _cuda, _example, built  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -270,3 +270,27 @@ def test_read_rounds_once(D, gs):
     want = {(s, i): _to_bf16(val[i] * Fraction(float(e4m3[s])) / Fraction(gs)) for s in range(127) for i in range(16)}
     ref = np.array([[want[int(s), i] for s in row for i in range(16)] for row in scale.reshape(128, -1)])
     assert (k[:, 0].double().cpu().numpy() == ref).all() and (v[:, 0].double().cpu().numpy() == ref).all()
+
+
+# ------------------------------------------------------------------ example
+
+def test_example_gives_idle_requests_no_token_and_takes_pages_back():
+    m = _example()
+    s = m.Server(3, 256)
+    tokens = torch.randint(0, m.VOCAB, (200,), generator=torch.Generator().manual_seed(2)).cuda()
+    first = s.step(tokens, [70, 0, 130])
+    assert first[1].item() == -1 and (first[[0, 2]] >= 0).all()
+    used = {0: set(s.block_table[0, :5].tolist()), 2: set(s.block_table[2, :9].tolist())}
+    assert int(s.free_count) == m.NUM_PAGES - 5 - 9
+    s.finish(2)
+    assert s.length.cpu().tolist() == [70, 0, 0] and int(s.free_count) == m.NUM_PAGES - 5
+    assert set(s.free_pages[:int(s.free_count)].tolist()) == set(range(m.NUM_PAGES)) - used[0]
+    # the freed pages serve another request, whose tokens are those of a server that never held the first one
+    again = s.step(tokens[:130], [0, 130, 0])
+    assert again[0].item() == -1 and again[2].item() == -1 and int(s.free_count) == m.NUM_PAGES - 5 - 9
+    alone = m.Server(3, 256).step(tokens[:130], [0, 130, 0])
+    assert torch.equal(again, alone)
+    s.finish(0)
+    s.finish(1)
+    assert int(s.free_count) == m.NUM_PAGES and sorted(s.free_pages.tolist()) == list(range(m.NUM_PAGES))
+    assert int(s.tables.status) == 0
