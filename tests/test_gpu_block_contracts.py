@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+from oracle import block
 from test_gpu_block import B, Scene, _bf16, _cuda, _example, built  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -294,3 +295,78 @@ def test_example_gives_idle_requests_no_token_and_takes_pages_back():
     s.finish(1)
     assert int(s.free_count) == m.NUM_PAGES and sorted(s.free_pages.tolist()) == list(range(m.NUM_PAGES))
     assert int(s.tables.status) == 0
+
+
+# --------------------------------------------------------- long contexts
+
+@pytest.mark.parametrize("qheads,heads,D,n", [(16, 1, 128, 1), (12, 1, 128, 1), (8, 1, 128, 2), (16, 2, 128, 2),
+                                              (16, 1, 64, 1), (24, 1, 128, 1), (32, 1, 64, 1), (32, 2, 128, 1)])
+def test_long_contexts_of_wide_groups(qheads, heads, D, n):
+    """Nine to sixteen rows (partials that do not fit a stage go to memory), and groups of more than sixteen heads:
+    cut across warps and CTAs, whole beside them, twice the same."""
+    lens = [(20000, n), (n, n), (7001, n), (333, n)]
+    s = Scene(lens, qheads, heads, D, 64, seed=qheads + D)
+    out, lse = s.run(want_lse=True)
+    s.check(out, lse)
+    again, lse2 = s.run(want_lse=True)
+    assert torch.equal(out, again) and torch.equal(lse, lse2)
+    out, lse = s.run(want_lse=True, window=5000)
+    s.check(out, lse, window=5000)
+
+
+# ------------------------------------------------------- prompts in pieces
+
+def test_attention_of_a_prompt_in_pieces_row_by_row():
+    """A prompt fed whole, and fed in pieces through a block's tables and cache: the cached bytes are equal, and every
+    output element is within its own row's bar of the exact value. A piece that attended to itself alone, or to
+    nothing, would be outside the same bars."""
+    m = _example()
+    n, P = 150, m.PAGE
+    qkv = _bf16((n, m.Q_HEADS + 2 * m.KV_HEADS, m.DIM), 5).cuda()       # one projection for both
+    ranges = lambda cuts: list(zip(np.cumsum([0] + cuts[:-1]), np.cumsum(cuts)))   # noqa: E731
+    pieces = ranges([100, 1, 1, 3, 45])
+    got, rows = [], []
+    for cut in ([(0, n)], pieces):
+        s = m.Server(1, 256)
+        cache = s.blocks[0].cache
+        outs, slots = [], []
+        for a, b in cut:
+            t = s.tables.run(s.length, _cuda([b - a]), s.block_table, s.free_pages, s.free_count)
+            pos = t.positions[:b - a]
+            assert pos.cpu().tolist() == list(range(a, b))
+            k = m.rotate(qkv[a:b, m.Q_HEADS:m.Q_HEADS + m.KV_HEADS], pos)
+            cache.append(k, qkv[a:b, m.Q_HEADS + m.KV_HEADS:], t.slots[:b - a])
+            o, _ = cache.attention(m.rotate(qkv[a:b, :m.Q_HEADS], pos), t.cu_q, t.kv_len, s.block_table, max_q=int(b - a),
+                                   ws=s.blocks[0].attn_ws)
+            outs.append(o)
+            slots.append(t.slots[:b - a].clone())
+            s.length.copy_(t.kv_len)
+            s.free_count.copy_(t.free_count)
+        got.append(torch.cat(outs).double().cpu().numpy())
+        rows.append([x.cpu() for x in cache.read(torch.cat(slots))])
+        assert B().moe_get_device_status(s.blocks[0].attn_ws) == 0
+    assert torch.equal(rows[0][0], rows[1][0]) and torch.equal(rows[0][1], rows[1][1])
+
+    pos = torch.arange(n, device="cuda")
+    ref = block.KvCache(-(-n // P), P, m.KV_HEADS, m.DIM, 2688 / 6, 2688 / 6)
+    k = m.rotate(qkv[:, m.Q_HEADS:m.Q_HEADS + m.KV_HEADS], pos)
+    ref.append(k.float().cpu().numpy(), qkv[:, m.Q_HEADS + m.KV_HEADS:].float().cpu().numpy(), np.arange(n))
+    keys, vals = (ref.values(w, np.arange(n)) for w in (0, 1))
+    q = m.rotate(qkv[:, :m.Q_HEADS], pos).double().cpu().numpy()
+    start = np.zeros(n, int)
+    for a, b in pieces:
+        start[a:b] = a
+    alone = 0                                  # later rows whose piece alone gives something else
+    for i in range(n):
+        for h in range(m.Q_HEADS):
+            kv, v = keys[:, h * m.KV_HEADS // m.Q_HEADS], vals[:, h * m.KV_HEADS // m.Q_HEADS]
+            o, _, pv, sabs = block.attention(q[i, h], kv, v, m.DIM ** -0.5, i)
+            ds = sabs * ((m.DIM + 8) * 2.0 ** -22 + 2.0 ** -24) + 2.0 ** -20
+            bar = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * ds) * pv + n * 2.0 ** -25 * np.abs(v).max()
+            for g in got:
+                assert (np.abs(g[i, h] - o) <= bar).all(), (i, h)
+            if start[i]:
+                own, *_ = block.attention(q[i, h], kv[start[i]:], v[start[i]:], m.DIM ** -0.5, i - start[i])
+                assert (np.abs(o) > bar).any()          # nothing at all would be seen
+                alone += (np.abs(own - o) > bar).any()
+    assert alone == (n - 100) * m.Q_HEADS
