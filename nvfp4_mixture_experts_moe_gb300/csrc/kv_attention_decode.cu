@@ -8,8 +8,10 @@
 // element in [2^14, 2^15) (exact for bf16 down to 2^-24 of that element), the
 // keys as e2m1 * e4m3 in f16 (exact: at most six significant bits), so the
 // products are exact and summed in fp32. p_j is rounded to f16 for the second
-// product (2^-11 of itself, the row's p_j taken from an m that is at most 8
-// below the running maximum, so p_j <= 256), and the values enter exactly
+// product, from an m that lies 7 to 15 below the running maximum: the largest
+// p_j is 2^7 to 2^15, so one down to 2^-21 of it keeps 2^-11 of itself, and one
+// down to 2^-32 is not lost (many of those next to one token that takes nearly
+// all, whose value may be small, are the output). The values enter exactly
 // like the keys; sums and statistics are fp32.
 //
 // What bounds it: the cache's bytes, 1.125 D per token and head, where
@@ -52,7 +54,9 @@ using namespace tc;
 
 constexpr int kChunk = 1024;       // requests of one launch
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;     // how far above m a score may be before m follows (log2)
+// log2: m is set this far below the running maximum, and again when a score is
+// further above it than the slack.
+constexpr float kLead = 7.0f, kSlack = 15.0f;
 constexpr unsigned kFull = 0xffffffffu;
 // Tiles that a CTA works on in the time that a join across CTAs takes, where
 // every SM has a range (which then begin and end anywhere); half where not.
@@ -680,7 +684,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
               x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
               x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
               x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-              const float mn = fmaxf(m[nt][c], x);
+              const float mn = fmaxf(m[nt][c], x - kLead);
               const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][c] - mn);   // 0 from -inf
               m[nt][c] = mn;
               l[nt][c] *= f;

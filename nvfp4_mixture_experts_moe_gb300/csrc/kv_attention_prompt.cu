@@ -5,7 +5,7 @@
 // heads of a group share every dequantised key and value. Mathematics as in
 // kv_attention_decode.cu: rows as f16 times a power of two (exact), keys and
 // values as e2m1 * e4m3 in f16 (exact), fp32 scores, p = 2^(s - m) rounded to
-// f16, m at most 8 below the running maximum (log2), fp32 sums and output.
+// f16, m 7 to 15 below the running maximum (log2), fp32 sums and output.
 //
 // Per CTA (one per SM):
 // * four dequant warps, each two 16-token blocks of the tile: codes and scales
@@ -17,8 +17,8 @@
 //   the MMAs of the other; P_i (f16, read from tensor memory) lies in the
 //   columns of the half of S_i it came from;
 // * eight softmax warps, one row per thread: a half of S is read once; a half
-//   whose maximum exceeds the running one by more than 8 rescales O and the
-//   sum first, when the halves before have gone into O (rare after the first).
+//   whose maximum is more than 15 above m rescales O and the sum first, when
+//   the halves before have gone into O (rare after the first).
 //
 // What bounds it: per 128 tokens and 256 rows at D = 128 the MMAs take 2048
 // cycles at their rate (2560 with S in halves: Q is read twice), the
@@ -59,7 +59,7 @@ constexpr int kThreads = (kScoutWarp + 1) * 32;
 constexpr int kSetup = 2;              // what starting and ending a row tile costs, in KV tiles
 constexpr int kSplitRows = 64;         // row tiles of up to this many rows are split over their KV tiles
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kSlack = 8.0f;
+constexpr float kLead = 7.0f, kSlack = 15.0f;   // log2: m is set the first below the maximum, again past the second
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTmemCols = 512;
 
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
             };
             const float p0 = peak(s0, 0), p1 = peak(s1, 1), top = fmaxf(p0, p1) * c;
             if (__any_sync(kFull, top > m + kSlack)) {
-              const float mn = fmaxf(m, top), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+              const float mn = fmaxf(m, top - kLead), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
               m = mn;
               const float2 l = unpack2(l2);
               l2 = pack2(l.x * f, l.y * f);

@@ -370,3 +370,38 @@ def test_attention_of_a_prompt_in_pieces_row_by_row():
                 assert (np.abs(o) > bar).any()          # nothing at all would be seen
                 alone += (np.abs(own - o) > bar).any()
     assert alone == (n - 100) * m.Q_HEADS
+
+
+@pytest.mark.parametrize("D,group,n,batch", [(64, 1, 1, 320), (128, 1, 1, 320), (128, 4, 4, 320), (64, 4, 40, 30), (128, 4, 40, 30)])
+@pytest.mark.parametrize("gap", [14.3, 20.6, 24.6, 27.6])
+def test_small_probabilities_are_kept(D, group, n, batch, gap):
+    """One token 2^gap above 3000 others that are alike, with a value of zero: the output is the others' share. Enough
+    requests (on the same pages) that a warp, or a CTA, goes through a context alone. A probability enters the second
+    product as f16, the running maximum's as 2^7 or more: 2^-11 relative, at most 2^-25 / 2^7 absolute."""
+    from nvfp4_mixture_experts_moe_gb300 import Kv4Cache
+    heads, kv, P = 8, 3000, 64
+    W = -(-kv // P)
+    k, v = torch.zeros(kv, heads, D), torch.full((kv, heads, D), 0.75)
+    k[0], v[0] = 1.0, 0.0
+    v[1:, :, 1::2] = _bf16((kv - 1, heads, D // 2), 3).float()
+    k, v = k.to(torch.bfloat16), v.to(torch.bfloat16)
+    c = Kv4Cache(W, P, heads, D, 448.0, 448.0)
+    c.append(k.cuda(), v.cuda(), _cuda(np.arange(kv)))
+    ref = block.KvCache(W, P, heads, D, 448.0, 448.0)
+    ref.append(k.float().numpy(), v.float().numpy(), np.arange(kv))
+    keys, vals = (ref.values(w, np.arange(kv)) for w in (0, 1))
+    q = torch.ones(batch * n, heads * group, D, dtype=torch.bfloat16)
+    scale = float(np.float32(gap * np.log(2) / keys[0, 0].sum()))
+    table = _cuda(np.tile(np.arange(W), (batch, 1)))
+    out, lse = c.attention(q.cuda(), _cuda(np.arange(batch + 1) * n), _cuda([kv] * batch), table, max_q=n, want_lse=True,
+                           scale=scale)
+    assert c.status.tolist() == [0]
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for i in {0, n // 2, n - 1}:
+        for h in range(heads):
+            o, l, pv, sabs = block.attention(q[i, 0].double().numpy(), keys[:, h], vals[:, h], scale, kv - n + i)
+            ds = sabs * ((D + 8) * 2.0 ** -22 + 2.0 ** -24) + 2.0 ** -20
+            bar = 2.0 ** -8 * np.abs(o) + (2.0 ** -10 + 2 * ds) * pv + kv * 2.0 ** -32 * np.abs(vals).max()
+            rows = slice(i, batch * n, n), slice(h * group, (h + 1) * group)
+            assert (np.abs(out[rows] - o) <= bar).all(), (i, h, np.abs(out[rows] - o).max(), bar.max(), np.abs(o).max())
+            assert (np.abs(lse[rows] - l) <= ds + 2.0 ** -22 * abs(l) + kv * 2.0 ** -30).all()
