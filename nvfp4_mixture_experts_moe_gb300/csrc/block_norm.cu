@@ -585,6 +585,16 @@ moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s) {
                    vector_ok(a.residual, a.residual_stride, re) && vector_ok(a.residual_out, a.H, re) &&
                    vector_ok(a.out, a.H, 2) && vector_ok(a.w_post, 0, 2) && vector_ok(a.w_pre, 0, 2);
   const Stream p = plan_stream(a, !vec);
+  // Whole vectors: a CTA per row and a thread per vector as long as all rows
+  // run at once, which is one row an SM from H = 5120 on, and as many as the
+  // stream kernel has CTAs below; with more rows the stream kernel. (us, row by
+  // row / streamed: 152 x 8192 3.1 / 3.1, 160 x 8192 5.0 / 4.1, 304 x 7168 5.0 /
+  // 4.0, 304 x 5120 3.2 / 3.3, 304 x 4096 2.9 / 3.2, 1200 x 4096 8.8 / 7.9, 600 x
+  // 2048 2.8 / 3.1, 2400 x 2048 7.9 / 7.6.) Four vectors a thread are slower
+  // than one up to there (8 x 4096 3.4 and 2.2, 400 x 2048 3.6 and 2.5, 1200 x
+  // 1024 3.8 and 2.8) and are left for more rows than run at once where the
+  // stream kernel does not fit.
+  const int at_once = (a.H > 5120 ? 1 : p.per_sm > 0 ? p.per_sm : 2) * sm_count();
   cudaError_t e;
   if (!vec) {
     // Short rows an element at a time (16384 x 333: 24 us, 33 by granules;
@@ -592,10 +602,10 @@ moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s) {
     if (a.H <= 512) e = launch<1, 4>(a, s);
     else if (p.per_sm > 0) e = p.n == 1 ? launch_shift<1>(a, p, s) : launch_shift<2>(a, p, s);
     else e = launch<1, 16>(a, s);
-  } else if (p.per_sm > 0 && a.T > p.per_sm * sm_count()) {   // more rows than CTAs
+  } else if (p.per_sm > 0 && a.T > at_once) {
     e = p.n == 1 ? launch_vectors<1>(a, p, s) : launch_vectors<2>(a, p, s);
-  } else if (a.H <= 8192 && a.T <= 304) {
-    e = launch<8, 1>(a, s);   // few rows: as many threads per row as it has vectors
+  } else if (a.H <= 8192 && a.T <= at_once) {
+    e = launch<8, 1>(a, s);   // as many threads per row as it has vectors
   } else {
     e = launch<8, 4>(a, s);
   }

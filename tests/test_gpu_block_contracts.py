@@ -405,3 +405,14 @@ def test_small_probabilities_are_kept(D, group, n, batch, gap):
             rows = slice(i, batch * n, n), slice(h * group, (h + 1) * group)
             assert (np.abs(out[rows] - o) <= bar).all(), (i, h, np.abs(out[rows] - o).max(), bar.max(), np.abs(o).max())
             assert (np.abs(lse[rows] - l) <= ds + 2.0 ** -22 * abs(l) + kv * 2.0 ** -30).all()
+
+
+# -------------------------------------------------------------------- norms
+
+@pytest.mark.parametrize("T,H,gate,f32", [
+    (152, 8192, "channel", False), (153, 8192, "token", False), (160, 5128, "token", True), (304, 5120, "token", True),
+    (305, 5120, "token", True), (170, 6144, None, False), (400, 1024, "token", False), (1217, 1024, "channel", True),
+    (600, 2048, "token", True), (153, 7688, "token", True), (170, 7688, "channel", True), (170, 8200, "token", False)])
+def test_norm_on_either_side_of_each_variants_sizes(T, H, gate, f32):
+    from test_gpu_block import test_norm_matches_the_oracle as check
+    check(T, H, gate, f32, True, True, True)
