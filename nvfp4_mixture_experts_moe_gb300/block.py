@@ -71,9 +71,9 @@ def _like(t, shape, dtype, what, dev):
 
 
 def _status(t, dev):
-    """A ``device_status``: one int32 (or its address)."""
-    if not isinstance(t, int) and not (t.get_device() == dev and t.dtype is _I32 and t.numel() == 1):
-        raise ValueError("device_status: one int32 on the current GPU is needed")
+    """A ``device_status``: an int32 tensor (its first element is set) or an address."""
+    if not isinstance(t, int) and not (t.get_device() == dev and t.dtype is _I32 and t.numel() > 0):
+        raise ValueError("device_status: an int32 tensor on the current GPU is needed")
     return t
 
 

@@ -3,7 +3,7 @@
 // r rsqrt(mean r^2 + eps) w_pre, the row in registers between the two
 // reductions, so every array is read or written once.
 //
-// What bounds it: bytes. Few rows run one CTA each (8 x 4096: 2.5 us, launch
+// What bounds it: bytes. Few rows run one CTA each (8 x 4096: 2.3 us, launch
 // and one trip to memory), more rows than CTAs the stream kernel: 16384 x 7168
 // with a gate per row in 192 us, 6.1 TB/s or 90 % of the measured copy rate. One CTA
 // per row took 303 us there: its loads stop while its reductions run, and

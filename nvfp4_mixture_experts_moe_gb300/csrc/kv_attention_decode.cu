@@ -27,20 +27,23 @@
 // CTA to finish one; every join adds in the order of the ranges, so results
 // do not depend on timing. Where every (request, head) is short and there are
 // no more of them than SMs, a CTA takes one whole: the join across CTAs costs
-// 2 to 5 us (16 requests of 1024 tokens: 17.5 us cut, 12.2 whole).
+// 2 to 4 us (16 requests of 1024 tokens: 15.0 us cut, 11.1 whole).
 //
 // mma.sync rather than tcgen05: at 1 to 16 rows the tensor work is a few
 // per cent of the time, and the dequantised operand never has to leave the
 // registers that converted it. A tile of 32 tokens at D = 128 costs a warp
-// some 460 instructions, half of them conversions and scales, which is why 16
-// rows (twice the matrix work per conversion) run further from the memory
-// rate than 8.
+// 590 instructions for 8 rows and 670 for 16 (250 on the ALU pipe, half of them
+// conversions, 200 to 220 on the FMA pipe, most of them scales, 32 and 64
+// matrix, 48 and 65 of shared memory). With 16 rows the registers leave 12
+// warps instead of 16, which issue in 0.48 of the cycles instead of 0.63: these
+// run further from the memory rate.
 //
 // Measured (replayed): 4 requests of 131072 tokens, 8 heads x 128: 108 us,
-// 5.6 TB/s (82 % of the measured copy rate); 64 of up to 8192 in pages of 16:
-// 68 us, 4.5 TB/s (9 us until the first tiles are there, 8 after the last for
-// uneven ends and joins); 16 rows over 84,500 tokens at D = 64: 29.5 us; one
-// request of 1000 tokens: 8.9 us.
+// 5.6 TB/s (82 % of the measured copy rate), with 12 or 16 query heads to each
+// 161 and 163 us; 64 of up to 8192 in pages of 16: 69 us, 4.5 TB/s (9 us until
+// the first tiles are there, 8 after the last for uneven ends and joins), with
+// 16 query heads to each 118; 16 rows over 84,500 tokens at D = 64: 29.7 us
+// (26.3 from L2); one request of 1000 tokens: 9.2 us.
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -59,9 +62,11 @@ constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLead = 7.0f, kSlack = 15.0f;
 constexpr unsigned kFull = 0xffffffffu;
 // Tiles that a CTA works on in the time that a join across CTAs takes, where
-// every SM has a range (which then begin and end anywhere); half where not.
-// (With the joins of then, 1 x 1000 tokens of 8 heads took 10.4 us cut and 11.7
-// whole, 8 x 1000 12.4 and 11.7.)
+// every SM has a range (which then begin and end anywhere); half where not. (us
+// with 0, 12, 24, 48 and 96 here: 16 x 1024 tokens of 8 heads 15.0, 11.1, 11.1,
+// 11.1, 11.1; 16 x 4096 24.5, 24.4, 22.0, 22.0, 22.0; 8 x 1000 for 16 rows 23.8,
+// 23.7, 15.9, 15.9, 15.9; 1 x 1000 8.9, 8.9, 8.9, 8.9, 10.5; 16 of 256 to 2048
+// 15.5, 15.6, 15.5, 14.7, 14.7.)
 constexpr int kAlone = 24;
 
 struct DecodeArgs {
@@ -404,9 +409,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
   // ------------------------------------------------------- this warp's range
   // Equal ranges, or a (request, head) for each CTA where that takes little
   // more of its time than the join across CTAs would.
-  // Few tiles go to fewer CTAs, four to each or eight (1 x 1000 tokens of 8
-  // heads: 8.9 us with four, 9.4 with eight; 2 x 4066 of one: 11.1 and 10.3,
-  // the join of 32 partials).
+  // Few tiles go to fewer CTAs, four to each, or eight where a (request, head)
+  // has more than 64 and the join of its partials is what takes long. (us with
+  // four and eight: 1 x 1000 tokens of one head 7.9 and 8.6, 1 x 4096 at D = 64
+  // 8.9 and 9.2; 2 x 4066 of one 10.2 and 9.8, 1 x 4096 of 8 10.1 and 9.9, 1 x
+  // 16384 of one 15.5 and 12.2; with sixteen 2 x 4066 takes 11.2.)
   const int least = longest > 16 * kKvTilesPerCta ? 2 * kKvTilesPerCta : kKvTilesPerCta;
   const int cta = blockIdx.x, spread = min((int)gridDim.x, (total + least - 1) / least);
   const int per_cta = (total + spread - 1) / spread, more = spread == (int)gridDim.x ? kAlone : kAlone / 2;

@@ -23,11 +23,15 @@
 // What bounds it: per 128 tokens and 256 rows at D = 128 the MMAs take 2048
 // cycles at their rate (2560 with S in halves: Q is read twice), the
 // exponentials 1024, and the softmax and dequant warps issue some 2000
-// instructions per scheduler. A KV tile takes 4300: the tensor pipe is given
-// work nearly all of that time and both softmax warps of a scheduler are
-// active in two thirds of it. A 16384-token prompt of 32 heads over 8 runs at
-// 1130 TFLOP/s (58 % of the measured matrix rate), one of 4096 tokens at 845:
-// there each CTA enters and leaves three to five row tiles, 4-5 us each.
+// instructions per scheduler. A KV tile takes 4300: the tensor pipe is active in
+// 62 % of the cycles (45 % at D = 64, where the MMAs are half) and instructions
+// issue in 50 %, so neither is the limit but the chain between them: the two
+// softmax warps of a scheduler each go through wait, load from tensor memory,
+// maximum, vote, exponentials, store and arrive for a half of S, and what they
+// leave uncovered the MMAs, which wait for P, do not fill. A 16384-token prompt
+// of 32 heads over 8 runs at 1127 TFLOP/s (58 % of the measured matrix rate),
+// one of 4096 tokens at 838: there each CTA enters and leaves three to five row
+// tiles, 4-5 us each.
 //
 // Work is dealt out by KV tiles: all (request, head, row tile, KV tile) in
 // order, one equal range per CTA. A row tile that two or more CTAs cut leaves
@@ -56,8 +60,15 @@ static_assert(kWarpBlocks == 2, "blocks of a dequant warp");
 constexpr int kMmaWarp = kSoftWarps + kDeqWarps;   // and the one after it
 constexpr int kScoutWarp = kMmaWarp + 2;
 constexpr int kThreads = (kScoutWarp + 1) * 32;
-constexpr int kSetup = 2;              // what starting and ending a row tile costs, in KV tiles
-constexpr int kSplitRows = 64;         // row tiles of up to this many rows are split over their KV tiles
+// What starting and ending a row tile costs, in KV tiles. (us with 0, 1, 2, 3
+// and 5, 32 heads over 8: a 4096-token prompt 211, 184, 163, 161, 165; four of
+// 512 50, 41, 41, 39, 41; 16 requests of 1 to 181 new tokens on 3000 141, 139,
+// 139, 140, 141.)
+constexpr int kSetup = 2;
+// Row tiles of up to this many rows are split over their KV tiles. (us split
+// and not: 8 x 8 tokens over 16384, 32 rows, 103 and 117; 16 tokens over 16000,
+// 64 rows, 26.6 and 28.7.)
+constexpr int kSplitRows = 64;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLead = 7.0f, kSlack = 15.0f;   // log2: m is set the first below the maximum, again past the second
 constexpr unsigned kFull = 0xffffffffu;

@@ -8,10 +8,11 @@
 //
 // What bounds them: bytes for prompts, latency for a decode step (1.8 us a
 // launch, replayed). 8191 tokens of 8 heads x 128 written and read back move
-// 86 MB in 19.2 us, 4.5 TB/s or 66 % of the measured copy rate; at 10 us
-// each the two kernels spend some 3 us on launch, first loads and last
-// stores, and issue instructions in two of three cycles (200 a warp and 512
-// elements: three correctly rounded divisions among them).
+// 86 MB, 12.7 us at the measured copy rate; replayed, the two take 7.9 and 7.3
+// us (L2 holds what was just written), from and to memory 10 each, some 3 of
+// them launch, first loads and last stores. Instructions issue in 0.61 and 0.65
+// of the cycles (206 and 178 a warp and 512 elements; append's have three
+// correctly rounded divisions among them).
 #include <cmath>
 
 #include "kernels.cuh"

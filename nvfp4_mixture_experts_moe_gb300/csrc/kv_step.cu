@@ -8,8 +8,8 @@
 //
 // What bounds it: latency. Lengths, then a table entry, then the store are
 // three trips to memory of some 0.7 us; the scan between them is shuffles
-// and one exchange between warps. 64 decoding requests take 2.8 us, 500
-// requests with 31,000 new tokens 4.2 (replayed).
+// and one exchange between warps. 64 decoding requests take 2.9 us, 500
+// requests with 31,000 new tokens 4.4 (replayed).
 #include "kernels.cuh"
 #include "kv4.cuh"
 
