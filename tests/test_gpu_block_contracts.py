@@ -416,3 +416,43 @@ def test_small_probabilities_are_kept(D, group, n, batch, gap):
 def test_norm_on_either_side_of_each_variants_sizes(T, H, gate, f32):
     from test_gpu_block import test_norm_matches_the_oracle as check
     check(T, H, gate, f32, True, True, True)
+
+
+# ------------------------------------------------------------- back to back
+
+@pytest.mark.parametrize("D,P", [(64, 16), (128, 64)])
+def test_steps_back_to_back_read_what_was_just_appended(D, P):
+    """Tokens appended into blocks that the attention before has just read, with long and short requests in each call
+    (two kernels that overlap): queued without a wait, and with one after each call."""
+    from nvfp4_mixture_experts_moe_gb300 import Kv4Cache, KvStep
+    Bn, heads, W, steps = 6, 2, 64, 40
+    new = np.random.default_rng(D).choice([1, 2, 3, 9, 17], (steps, Bn))
+    new[:, 0], new[:, 1] = 1, 17                    # both kinds in every call
+    total = new.sum(1)
+    q, kv = _bf16((int(total.sum()), 8, D), 1).cuda(), _bf16((int(total.sum()), 2 * heads, D), 2).cuda()
+    counts = _cuda(new)
+    runs = []
+    for wait in (False, True):
+        c = Kv4Cache(Bn * W * 128 // P, P, heads, D, 400.0, 400.0)
+        s = KvStep(Bn, int(total.max()), P, W * 128 // P)
+        table = torch.zeros(Bn, W * 128 // P, dtype=torch.int32, device="cuda")
+        free = torch.arange(c.num_pages, dtype=torch.int32, device="cuda")
+        left, length = _cuda([c.num_pages]), _cuda([0] * Bn)
+        ws = c.attention_workspace(int(total.max()), Bn, 8, 17, table.shape[1])
+        at, outs = 0, []
+        for i in range(steps):
+            n = int(total[i])
+            s.run(length, counts[i], table, free, left)
+            c.append(kv[at:at + n, :heads], kv[at:at + n, heads:], s.slots[:n])
+            if wait:
+                torch.cuda.synchronize()
+            outs.append(c.attention(q[at:at + n], s.cu_q, s.kv_len, table, max_q=17, ws=ws)[0])
+            length.copy_(s.kv_len)
+            left.copy_(s.free_count)
+            at += n
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        assert int(s.status) == 0 and B().moe_get_device_status(ws) == 0
+        runs.append(torch.cat(outs))
+    assert torch.equal(*runs)
