@@ -108,7 +108,9 @@ class Kv4Cache:
 
     ``k_gs`` and ``v_gs`` are the calibrated global scales in the quant
     convention (2688 / amax). ``pool`` may be given (uint8, layout in
-    ``include/moe_block.h``); otherwise it is allocated, uninitialised.
+    ``include/moe_block.h``); otherwise it is allocated, uninitialised. What
+    the constructor makes is made on the current stream: a call on another one
+    comes after it (``stream.wait_stream``).
 
     ``status`` (int32 ``[1]``) keeps what calls without a ``device_status`` or
     workspace of their own report (MOE_ERR_DEVICE: a slot or page id outside
@@ -221,8 +223,9 @@ class KvStep:
     Holds the outputs, rewritten by every ``run``: ``kv_len`` ``[batch]``,
     ``cu_q`` ``[batch + 1]``, ``slots`` and ``positions`` ``[tokens]``,
     ``free_count`` ``[1]``, and ``status`` ``[1]``, which ``run`` sets to
-    MOE_ERR_DEVICE when a request was refused or its lengths were bad (the
-    caller clears it).
+    MOE_ERR_DEVICE when a request was refused, or its lengths or a page id were
+    bad (the caller clears it). They are made on the current stream: a run on
+    another one comes after it (``stream.wait_stream``).
     """
 
     def __init__(self, batch, tokens, page_tokens, max_pages, device="cuda"):
