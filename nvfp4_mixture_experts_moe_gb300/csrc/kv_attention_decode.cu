@@ -48,19 +48,16 @@
 
 #include "kernels.cuh"
 #include "kv4.cuh"
+#include "kv_rows.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
+using namespace rows;
 using namespace tc;
 
 constexpr int kChunk = 1024;       // requests of one launch
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-// log2: m is set this far below the running maximum, and again when a score is
-// further above it than the slack.
-constexpr float kLead = 7.0f, kSlack = 15.0f;
-constexpr unsigned kFull = 0xffffffffu;
 // Tiles that a CTA works on in the time that a join across CTAs takes, where
 // every SM has a range (which then begin and end anywhere); half where not. (us
 // with 0, 12, 24, 48 and 96 here: 16 x 1024 tokens of 8 heads 15.0, 11.1, 11.1,
@@ -76,13 +73,6 @@ struct DecodeArgs {
   int* status;
   int* counters;       // [kKvMaxCtas] zero between launches
   float* partials;     // see Slots
-};
-
-// One partial result: rows x D fp32 output, then (m, l) of each row.
-template <int D, int NT>
-struct Slots {
-  static constexpr int kRows = 8 * NT;
-  static constexpr int kFloats = kRows * (D + 2);
 };
 
 // A tile is 4608 bytes of one (request, head): 32 tokens at D = 128, 64 at 64.
@@ -144,38 +134,6 @@ __device__ __forceinline__ int first_seen(const moe_kv4_attn_args& a, const Requ
   return a.window > 0 ? max(0, min(r.kv, r.kv - r.n + 1 - a.window)) : 0;
 }
 
-// Row of the MMA's token side <-> token of a 16-token block (the same map
-// within each half): with it the 16-byte key loads are free of bank conflicts
-// and the value loads have two-way ones (128 cycles of shared memory a tile
-// with the identity, 80 with this).
-__device__ __forceinline__ int token_of(int r) { return r ^ ((r >> 1) & 1); }
-
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
-  uint32_t r;
-  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-// 2^k for -126 <= k <= 127.
-__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
 __device__ __forceinline__ int last_at_most(const int* arr, int n, int x) {
   int lo = 0, hi = n;
   while (lo < hi) {
@@ -201,48 +159,17 @@ __device__ __forceinline__ Segment segment_of(const int* pre, int nb, int heads,
   return s;
 }
 
-// The running join of partials of one row's four neighbouring columns.
-struct Joined {
-  float m = -INFINITY, l = 0.0f;
-  float4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  template <int N>
-  __device__ __forceinline__ void add(const float2 (&ml)[N], const float4 (&v)[N]) {
-    float mn = m;
-#pragma unroll
-    for (int j = 0; j < N; ++j) mn = fmaxf(mn, ml[j].x);
-    const float mu = mn == -INFINITY ? 0.0f : mn, w0 = ex2(m - mu);   // 0 from -inf
-    m = mn;
-    l *= w0;
-    o.x *= w0;
-    o.y *= w0;
-    o.z *= w0;
-    o.w *= w0;
-#pragma unroll
-    for (int j = 0; j < N; ++j) {
-      const float w = ex2(ml[j].x - mu);
-      l += w * ml[j].y;
-      o.x += w * v[j].x;
-      o.y += w * v[j].y;
-      o.z += w * v[j].z;
-      o.w += w * v[j].w;
-    }
-  }
-  // Normalised bf16 and lse. A row that has seen nothing has l = 0 and gets
-  // zeros and -inf; l is NaN where a score was, and so are the row and its lse.
-  __device__ __forceinline__ void write(const moe_kv4_attn_args& a, const Request& rq, int h, int group, int row, int D,
-                                        int d) const {
-    const float inv = l == 0.0f ? 0.0f : 1.0f / (l * a.cache.v_gs);
-    const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
-    *reinterpret_cast<uint2*>(a.out + at * D + d) =
-        make_uint2(float2_to_bf16x2_bits(o.x * inv, o.y * inv), float2_to_bf16x2_bits(o.z * inv, o.w * inv));
-    if (d == 0 && a.lse != nullptr) a.lse[at] = l == 0.0f ? -INFINITY : m * kLn2 + logf(l);
-  }
-};
-
-// Where a warp's partial holds four neighbouring columns of a row: the lanes
-// of a store have four pairs of rows and every fourth or second chunk, and
-// would otherwise meet in two banks' worth of addresses.
-__device__ __forceinline__ int warp_chunk(int row, int chunk) { return chunk ^ (row >> 1 & 3); }
+// Normalised bf16 and lse of a joined row. One that has seen nothing has l = 0
+// and gets zeros and -inf; l is NaN where a score was, and so are the row and
+// its lse.
+__device__ __forceinline__ void write_joined(const Joined& x, const moe_kv4_attn_args& a, const Request& rq, int h, int group,
+                                             int row, int D, int d) {
+  const float inv = x.l == 0.0f ? 0.0f : 1.0f / (x.l * a.cache.v_gs);
+  const size_t at = (size_t)(rq.row0 + row / group) * a.q_heads + h * group + row % group;
+  *reinterpret_cast<uint2*>(a.out + at * D + d) =
+      make_uint2(float2_to_bf16x2_bits(x.o.x * inv, x.o.y * inv), float2_to_bf16x2_bits(x.o.z * inv, x.o.w * inv));
+  if (d == 0 && a.lse != nullptr) a.lse[at] = x.l == 0.0f ? -INFINITY : x.m * kLn2 + logf(x.l);
+}
 
 // Joins n partials that a CTA's warps left in shared memory (one may lie in
 // global memory), in their order: warp `mine` of `warps` takes every warps-th
@@ -276,7 +203,7 @@ __device__ __forceinline__ void join_warps(const moe_kv4_attn_args& a, const Req
       *reinterpret_cast<float4*>(dst + row * D + d) = x.o;
       if (d == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(x.m, x.l);
     } else {
-      x.write(a, rq, h, group, row, D, d);
+      write_joined(x, a, rq, h, group, row, D, d);
     }
   }
 }
@@ -332,7 +259,7 @@ __device__ __forceinline__ void join_ctas(const moe_kv4_attn_args& a, const Requ
       }
       __syncthreads();
     }
-    if (real && part == 0) x.write(a, rq, h, group, row, D, d);
+    if (real && part == 0) write_joined(x, a, rq, h, group, row, D, d);
   }
 }
 
@@ -343,7 +270,6 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
   using Sm = Smem<D, NT>;
   constexpr int W = Sh::kWarps, S = Sh::kStages, kRows = 8 * NT, MT = D / 16;
   constexpr int NB = Sh::kBlocks, kTile = Sh::kTile, kPart = NT == 1 ? NB : 2;
-  constexpr int kKeyWords = D / 32;     // 32-bit code words of one key row per lane
   extern __shared__ __align__(128) uint8_t smem_raw[];
   Sm* sm = reinterpret_cast<Sm*>(smem_raw);
   const moe_kv4_attn_args& a = p.a;
@@ -529,9 +455,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
       cp_async_commit();
     }
 
-    uint32_t qf[NT][MT][2];        // the rows as B fragments
-    float o[NT][MT][4];            // out^T: rows d, columns query rows
-    float mult[NT][2], m[NT][2], l[NT][2];
+    RowState<D, NT> st;
     Request rq = {0, 0, 0, false};
     int h = 0, plain0 = 0, plain1 = 0;   // tiles with every token in [plain0, plain1) need no mask
     int seg_end = r0;
@@ -558,48 +482,11 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
         const int low = a.causal ? rq.kv - rq.n : rq.kv - 1;   // the first row's last token
         plain1 = low + 1;
         plain0 = a.window > 0 ? rq.kv - a.window : 0;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const int row = nt * 8 + g8;
-          const uint16_t* q = a.q + (size_t)(rq.row0 + row / group) * a.q_stride + (h * group + row % group) * D +
-                              t4 * (D / 4);
-          uint4 raw[D / 32];
-          uint32_t mx = 0;
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i)
-            raw[i] = row < rq.n * group ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            mx = max_u16x2(max_u16x2(mx, raw[i].x & 0x7fff7fffu), raw[i].y & 0x7fff7fffu);
-            mx = max_u16x2(max_u16x2(mx, raw[i].z & 0x7fff7fffu), raw[i].w & 0x7fff7fffu);
-          }
-          mx = max_u16x2(mx, __shfl_xor_sync(kFull, mx, 1));
-          mx = max_u16x2(mx, __shfl_xor_sync(kFull, mx, 2));
-          // largest element to [2^14, 2^15) (smaller only below 2^-112)
-          const int ex = min(max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15), 254);
-          const float up = a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);   // a larger score is a larger product
-#pragma unroll
-          for (int i = 0; i < D / 32; ++i) {
-            const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              qf[nt][2 * i + j / 2][j & 1] = pack_f16x2(__uint_as_float(w[j] << 16) * up,
-                                                        __uint_as_float(w[j] & 0xffff0000u) * up);
-          }
-          // row g8's factor, fetched as columns 2t, 2t + 1; never 0, so that a hidden score stays -inf
-          const float mine = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
-          mult[nt][0] = __shfl_sync(kFull, mine, 8 * t4);
-          mult[nt][1] = __shfl_sync(kFull, mine, 8 * t4 + 4);
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            m[nt][c] = -INFINITY;
-            l[nt][c] = 0.0f;
-          }
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[nt][mt][i] = 0.0f;
-        }
+        start_rows<D, NT>(st, a.scale, a.cache.k_gs, [&](int row) {
+          return row < rq.n * group
+                     ? a.q + (size_t)(rq.row0 + row / group) * a.q_stride + (h * group + row % group) * D
+                     : nullptr;
+        });
       }
 
       if (parked < 0) cp_async_wait<S - 1>();   // this tile's group, on every lane
@@ -614,154 +501,13 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
       auto work = [&](auto with_mask, const uint8_t* part, int tok0, int valid) {
         constexpr bool kMask = decltype(with_mask)::value;
         const int recip = kMask ? (65535 + group) / group : 0;
-        // ---------------------------------------------------------- scores
-        float s[NT][kPart][4];
-#pragma unroll
-        for (int blk = 0; blk < kPart; ++blk) {
-          const uint8_t* kb = part + blk * L::kBytes;
-          uint32_t kw[2][kKeyWords];   // key codes of MMA rows g8 and g8 + 8
-          uint32_t ks[2][2];           // their scales, each doubled to f16x2
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int row = token_of(g8) + 8 * r;
-            const uint8_t* sf = kb + L::kKeyScales + row * L::kScaleRow;
-            if constexpr (D == 128) {
-              const uint4 v = *reinterpret_cast<const uint4*>(kb + row * L::kCodeRow + 16 * t4);
-              kw[r][0] = v.x, kw[r][1] = v.y, kw[r][2] = v.z, kw[r][3] = v.w;
-              const uint32_t two = cvt_e4m3x2_f16x2(*reinterpret_cast<const uint16_t*>(sf + 2 * t4));
-              ks[r][0] = __byte_perm(two, 0, 0x1010);
-              ks[r][1] = __byte_perm(two, 0, 0x3232);
-            } else {
-              const uint2 v = *reinterpret_cast<const uint2*>(kb + row * L::kCodeRow + 8 * t4);
-              kw[r][0] = v.x, kw[r][1] = v.y;
-              ks[r][0] = ks[r][1] = cvt_e4m3x2_f16x2((uint32_t)sf[t4] * 0x101u);
-            }
-          }
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[nt][blk][i] = 0.0f;
-#pragma unroll
-          for (int w = 0; w < kKeyWords; ++w) {
-            uint32_t lo[4], hi[4];
-            cvt_e2m1x8_f16(kw[0][w], lo);
-            cvt_e2m1x8_f16(kw[1][w], hi);
-            const uint32_t s0 = ks[0][w * 2 / kKeyWords], s1 = ks[1][w * 2 / kKeyWords];
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t af[4] = {hmul2_u32(lo[2 * i], s0), hmul2_u32(hi[2 * i], s1),
-                                      hmul2_u32(lo[2 * i + 1], s0), hmul2_u32(hi[2 * i + 1], s1)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(s[nt][blk], af, qf[nt][2 * w + i][0], qf[nt][2 * w + i][1]);
-            }
-          }
-          if constexpr (kMask) {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
-                // the last token its query sees; row / group by the reciprocal (both at most 16)
-                const int token = (nt * 8 + 2 * t4 + (i & 1)) * recip >> 16;
-                const int hi_tok = a.causal ? rq.kv - rq.n + token : rq.kv - 1, lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
-                if (tok > hi_tok || tok < lo_tok || !(valid >> blk & 1)) s[nt][blk][i] = -INFINITY;
-              }
-          }
-        }
-
-        // ------------------------------------------- running maximum and p
-        bool grow = false;
-        float top[NT][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float x = fmaxf(s[nt][0][c], s[nt][0][c + 2]);
-#pragma unroll
-            for (int blk = 1; blk < kPart; ++blk) x = fmaxf(x, fmaxf(s[nt][blk][c], s[nt][blk][c + 2]));
-            top[nt][c] = x * mult[nt][c];
-            grow |= top[nt][c] > m[nt][c] + kSlack;
-          }
-        if (__any_sync(kFull, grow)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              float x = top[nt][c];
-              x = fmaxf(x, __shfl_xor_sync(kFull, x, 4));
-              x = fmaxf(x, __shfl_xor_sync(kFull, x, 8));
-              x = fmaxf(x, __shfl_xor_sync(kFull, x, 16));
-              const float mn = fmaxf(m[nt][c], x - kLead);
-              const float f = mn == -INFINITY ? 1.0f : ex2(m[nt][c] - mn);   // 0 from -inf
-              m[nt][c] = mn;
-              l[nt][c] *= f;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) {
-                o[nt][mt][c] *= f;
-                o[nt][mt][c + 2] *= f;
-              }
-            }
-        }
-        uint32_t pf[NT][kPart][2];
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float m0 = m[nt][0], m1 = m[nt][1];
-          if constexpr (kMask) {   // a row that has seen nothing yet
-            if (m0 == -INFINITY) m0 = 0.0f;
-            if (m1 == -INFINITY) m1 = 0.0f;
-          }
-#pragma unroll
-          for (int blk = 0; blk < kPart; ++blk) {
-            const float p0 = ex2(fmaf(s[nt][blk][0], mult[nt][0], -m0)), p1 = ex2(fmaf(s[nt][blk][1], mult[nt][1], -m1));
-            const float p2 = ex2(fmaf(s[nt][blk][2], mult[nt][0], -m0)), p3 = ex2(fmaf(s[nt][blk][3], mult[nt][1], -m1));
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            pf[nt][blk][0] = movmatrix_trans(pack_f16x2(p0, p1));
-            pf[nt][blk][1] = movmatrix_trans(pack_f16x2(p2, p3));
-          }
-        }
-
-        // ----------------------------------------------------------- values
-#pragma unroll
-        for (int blk = 0; blk < kPart; ++blk) {
-          const uint8_t* vb = part + blk * L::kBytes;
-          uint32_t vw[4][MT / 4];    // value codes of MMA columns 2t, 2t + 1, 2t + 8, 2t + 9
-          uint32_t sc[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int tok = token_of(2 * t4 + (k & 1)) + 8 * (k >> 1);
-            sc[k] = vb[L::kValueScales + tok * L::kScaleRow + (D == 128 ? g8 : g8 / 2)];
-            if constexpr (D == 128) {
-              const uint2 v = *reinterpret_cast<const uint2*>(vb + L::kValueCodes + tok * L::kCodeRow + 8 * g8);
-              vw[k][0] = v.x, vw[k][1] = v.y;
-            } else {
-              vw[k][0] = *reinterpret_cast<const uint32_t*>(vb + L::kValueCodes + tok * L::kCodeRow + 4 * g8);
-            }
-            // What was never appended, lies before every row's window or has a
-            // bad page is hidden (p = 0), but its scale may decode as NaN, which
-            // no appended row's does: 0 instead.
-            if constexpr (kMask) {
-              if ((sc[k] & 0x7fu) == 0x7fu) sc[k] = 0;
-            }
-          }
-          const uint32_t s01 = cvt_e4m3x2_f16x2(sc[0] | sc[1] << 8), s23 = cvt_e4m3x2_f16x2(sc[2] | sc[3] << 8);
-#pragma unroll
-          for (int w = 0; w < MT / 4; ++w) {
-            // bytes (even d of token 2t, of 2t + 1) and (odd d ...): one conversion gives an MMA register
-            uint32_t e01[4], o01[4], e23[4], o23[4];
-            cvt_e2m1x8_f16((vw[0][w] & 0x0f0f0f0fu) | (vw[1][w] << 4 & 0xf0f0f0f0u), e01);
-            cvt_e2m1x8_f16((vw[0][w] >> 4 & 0x0f0f0f0fu) | (vw[1][w] & 0xf0f0f0f0u), o01);
-            cvt_e2m1x8_f16((vw[2][w] & 0x0f0f0f0fu) | (vw[3][w] << 4 & 0xf0f0f0f0u), e23);
-            cvt_e2m1x8_f16((vw[2][w] >> 4 & 0x0f0f0f0fu) | (vw[3][w] & 0xf0f0f0f0u), o23);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint32_t af[4] = {hmul2_u32(e01[i], s01), hmul2_u32(o01[i], s01), hmul2_u32(e23[i], s23),
-                                      hmul2_u32(o23[i], s23)};
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) mma_f16_16816(o[nt][4 * w + i], af, pf[nt][blk][0], pf[nt][blk][1]);
-            }
-          }
-        }
+        attend_blocks<D, NT, kPart, kMask>(st, part, [&](int blk, int nt, int i) {
+          const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
+          // the last token its query sees; row / group by the reciprocal (both at most 16)
+          const int token = (nt * 8 + 2 * t4 + (i & 1)) * recip >> 16;
+          const int hi_tok = a.causal ? rq.kv - rq.n + token : rq.kv - 1, lo_tok = a.window > 0 ? hi_tok - a.window + 1 : 0;
+          return tok > hi_tok || tok < lo_tok || !(valid >> blk & 1);
+        });
       };
 #pragma unroll 1
       for (int blk = 0; blk < NB; blk += kPart) {
@@ -796,7 +542,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float sum = l[nt][c];
+            float sum = st.l[nt][c];
             sum += __shfl_xor_sync(kFull, sum, 4);
             sum += __shfl_xor_sync(kFull, sum, 8);
             sum += __shfl_xor_sync(kFull, sum, 16);
@@ -808,19 +554,19 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
                 uint32_t w[MT];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
-                  w[mt] = float2_to_bf16x2_bits(o[nt][mt][c] * inv, o[nt][mt][c + 2] * inv);
+                  w[mt] = float2_to_bf16x2_bits(st.o[nt][mt][c] * inv, st.o[nt][mt][c + 2] * inv);
                 uint4* out = reinterpret_cast<uint4*>(a.out + at * D + g8 * (D / 8));
 #pragma unroll
                 for (int i = 0; i < MT / 4; ++i) out[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 if (g8 == 0 && a.lse != nullptr)
-                  a.lse[at] = sum == 0.0f ? -INFINITY : m[nt][c] * kLn2 + logf(sum);
+                  a.lse[at] = sum == 0.0f ? -INFINITY : st.m[nt][c] * kLn2 + logf(sum);
               }
             } else {
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
                 *reinterpret_cast<float2*>(dst + row * D + warp_chunk(row, g8 * (D / 32) + mt / 2) * 4 + mt % 2 * 2) =
-                    make_float2(o[nt][mt][c], o[nt][mt][c + 2]);
-              if (g8 == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(m[nt][c], sum);
+                    make_float2(st.o[nt][mt][c], st.o[nt][mt][c + 2]);
+              if (g8 == 0) *reinterpret_cast<float2*>(dst + kRows * D + 2 * row) = make_float2(st.m[nt][c], sum);
             }
           }
       }
