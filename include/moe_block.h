@@ -7,6 +7,11 @@
  *   moe_kv4_read       cached rows back to bf16
  *   moe_kv4_attention  attention over that cache (single tokens, drafted tokens, prompts)
  *   moe_block_norm     norm after a block, gate, residual, norm before the next block
+ *   moe_rope           rotary positions (one or several axes) of queries and keys
+ *   moe_kv4_append_rope  the same on the way into the cache
+ *   moe_kv4_index_update, moe_kv4_select, moe_kv4_sparse_attention
+ *                      block means of the cached keys, the blocks that each
+ *                      query picks by them, attention over the picked blocks
  *
  * The conventions of moe_nvfp4.h hold: device pointers unless a comment says
  * "host", caller-owned buffers, asynchronous on `stream`, argument errors
@@ -227,6 +232,199 @@ typedef struct {
 } moe_block_norm_args;
 
 moe_status moe_block_norm(const moe_block_norm_args* args, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions. Of each head the first rotary_dim elements are turned in
+ * pairs: element i with i + rotary_dim / 2, or (adjacent) 2i with 2i + 1. Pair
+ * p of a token at positions pos[axis] turns by the angle
+ *   phi = pos[axis_p] * inv_freq_p
+ *   (a, b) -> scale * (a cos phi - b sin phi, a sin phi + b cos phi)
+ * (inverse: by -phi, which is also the backward pass). Text has one axis;
+ * images and video have time, height and width, each with pairs of its own.
+ *
+ * Angles of far positions lose nothing: moe_rope_turns (host) turns the
+ * frequencies into turns per position, inv_freq / (2 pi), as 64-bit fixed
+ * point fractions, and the kernels multiply them with the position modulo one
+ * turn. The lowest two bits of an entry are its axis (2^-62 turns per
+ * position). Sine and cosine are fp32.
+ *
+ * inv_freq double [n], finite, |inv_freq| <= 1024; axis int32 [n], 0..3 (NULL:
+ * all 0); turns uint64 [n]: all on the host. The caller copies turns to the device.
+ */
+#define MOE_ROPE_MAX_AXES 4
+moe_status moe_rope_turns(const double* inv_freq, const int32_t* axis, int n, uint64_t* turns);
+
+typedef struct {
+  int rotary_dim;         /* even, >= 2 */
+  int axes;               /* 1..4 rows of positions; every pair's axis is below it */
+  int adjacent;
+  float scale;            /* multiplies sine and cosine (1, or a long-context attention factor) */
+  const uint64_t* turns;  /* [rotary_dim / 2] */
+} moe_rope_plan;
+
+/* Queries and, with k_heads > 0, keys. Elements past rotary_dim are copied.
+ *
+ * q, k         bf16 [tokens, q_heads or k_heads, head_dim], row strides in elements, a row's heads contiguous
+ * q_out, k_out the same; may be the input itself (same address and stride), else share no element with an input or
+ *              with one another
+ * positions    int32 [axes, tokens]
+ * All in fp32 from the inputs on, each output rounded once.
+ * Limits: head_dim <= 512, any alignment of the element type; rows of 16-byte
+ * alignment and rotary_dim a multiple of 16 are moved in vectors.
+ * Errors: NULL pointers (k may be with k_heads = 0), an odd or too small or too
+ * large rotary_dim, axes outside 1..4, a non-finite scale, strides smaller
+ * than a row, outputs that overlap -> MOE_ERR_INVALID_ARG; head_dim > 512 or
+ * more than 65536 heads -> MOE_ERR_UNSUPPORTED. tokens = 0 -> MOE_OK. A pair
+ * whose axis is not below `axes` goes by the last one.
+ */
+typedef struct {
+  moe_rope_plan plan;
+  int tokens, head_dim, q_heads, k_heads, inverse;
+  const uint16_t* q;
+  long long q_stride;
+  const uint16_t* k;
+  long long k_stride;
+  const int32_t* positions;
+  uint16_t* q_out;
+  long long q_out_stride;
+  uint16_t* k_out;
+  long long k_out_stride;
+} moe_rope_args;
+
+moe_status moe_rope(const moe_rope_args* args, moe_stream_t stream);
+
+/* moe_kv4_append of keys that are turned on the way, and the turned queries:
+ * q_out like moe_rope's; keys are turned in fp32 and quantised from there (not
+ * rounded to bf16 in between), values as moe_kv4_append has them. A pair with
+ * a NaN, or one that turns infinities into a NaN, is stored as 0. A token with
+ * a negative slot (or one past the pool, which is reported) is not stored; its
+ * query is turned all the same.
+ * Limits: the cache's; rotary_dim a multiple of 32 (adjacent: of 16) and at
+ * most head_dim, else MOE_ERR_UNSUPPORTED. q_heads may be 0 (q, q_out NULL).
+ * Errors: moe_kv4_append's and moe_rope's; q, q_out 16-byte aligned with
+ * strides that are multiples of 8.
+ */
+typedef struct {
+  moe_kv4_cache cache;
+  moe_rope_plan plan;
+  int tokens, q_heads;
+  const uint16_t* q;
+  long long q_stride;
+  const uint16_t* k;
+  long long k_stride;
+  const uint16_t* v;
+  long long v_stride;
+  const int32_t* slots;
+  const int32_t* positions;
+  uint16_t* q_out;
+  long long q_out_stride;
+  int32_t* device_status;
+} moe_kv4_append_rope_args;
+
+moe_status moe_kv4_append_rope(const moe_kv4_append_rope_args* args, moe_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Sparse attention: each query attends to some blocks of block_tokens tokens
+ * of its request (block j holds the tokens j * block_tokens and on), the same
+ * ones for the query heads of a key/value head, picked by a score against the
+ * block's mean key.
+ *
+ * The index has a row of means for each (block that starts in a page, head):
+ * f16 [num_pages * max(1, page_tokens / block_tokens)][kv_heads][head_dim].
+ * Block j of a request has the rows of entry
+ *   block_table[b][j * block_tokens / page_tokens] * max(1, page_tokens / block_tokens)
+ *     + (j * block_tokens % page_tokens) / block_tokens
+ * so requests that share pages share means, and pages given back need no care.
+ * A mean is that of code * scale (the key times k_gs) over the block's tokens,
+ * rounded to a multiple of 2^(E - 6), E the exponent of the row's largest
+ * magnitude: whole numbers of 8 bits times a power of two.
+ *
+ * Limits: block_tokens 32, 64 or 128; means 16-byte aligned, moe_kv4_index_size
+ * bytes; it needs no initialisation (only means of complete blocks are used).
+ */
+typedef struct {
+  moe_kv4_cache cache;
+  int block_tokens;
+  uint16_t* means;
+} moe_kv4_index;
+
+size_t moe_kv4_index_size(int num_pages, int page_tokens, int kv_heads, int head_dim, int block_tokens);
+
+/* The means of the blocks that a step's new tokens made complete: request b
+ * brought cu_q[b+1] - cu_q[b] tokens, already appended, and now holds kv_len[b].
+ * A block with a page id outside the pool is left out and reported.
+ *
+ * cu_q int32 [batch + 1], kv_len int32 [batch], block_table int32 [batch, max_pages], max_q as in moe_kv4_attention
+ * (a request with more than max_q new tokens, or a kv_len past its table, is reported and left out).
+ * Errors: NULL pointers, misaligned means, negative sizes, max_q < 1 ->
+ * MOE_ERR_INVALID_ARG; another block_tokens, batch > 4096, max_pages *
+ * page_tokens > 2^31 - 129, the cache's limits -> MOE_ERR_UNSUPPORTED. batch =
+ * 0 -> MOE_OK.
+ */
+moe_status moe_kv4_index_update(const moe_kv4_index* index, int batch, int max_q, int max_pages, const int32_t* cu_q,
+                                const int32_t* kv_len, const int32_t* block_table, int32_t* device_status,
+                                moe_stream_t stream);
+
+/* The blocks that each query picks, for each key/value head. A query at
+ * position p sees the blocks 0 .. p / block_tokens. It takes the first `sink`
+ * and the last `local` of them (its own block is the last) and, up to `top` in
+ * all, those of the largest score in between; the lower block of equal ones.
+ *   u = sum over the group's heads of round(q 2^(5 - E)), E the exponent of the largest magnitude of the group's
+ *   queries (at least -100); score_j = u . mean_j
+ * All of that is exact (whole numbers below 2^24 times powers of two), so
+ * picks do not depend on the order of sums. Elements of q that are NaN or
+ * infinite count as 0.
+ *
+ * blocks  int32 [total_q, kv_heads, top], ascending, -1 in the places that are left; rows no request owns are left alone
+ * Others as in moe_kv4_attention (which has the contract of bad device data: a
+ * page id outside the pool scores like -infinity).
+ * Limits: 1 <= top <= 64, sink + local <= top, local >= 1, groups of up to 16
+ * query heads, a context of up to 2^28 tokens.
+ * Errors: as moe_kv4_attention and moe_kv4_index_update; sink, local or top
+ * outside the limits -> MOE_ERR_INVALID_ARG (top > 64: MOE_ERR_UNSUPPORTED).
+ */
+typedef struct {
+  moe_kv4_index index;
+  int batch, q_heads, total_q, max_q, max_pages;
+  const uint16_t* q;
+  long long q_stride;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* block_table;
+  int top, sink, local;
+  int32_t* blocks;
+  int32_t* device_status;
+} moe_kv4_select_args;
+
+moe_status moe_kv4_select(const moe_kv4_select_args* args, moe_stream_t stream);
+
+/* Attention as moe_kv4_attention's, causal, over the tokens of the listed
+ * blocks up to the query's position. The entries of a list may come in any
+ * order; one that is negative or past the query's position is skipped, one
+ * listed twice counts once. A query whose list has nothing gets zeros and lse =
+ * -inf. No workspace; the same call gives the same bits. The lists of
+ * neighbouring queries are worked on together, so lists that share blocks cost
+ * less than lists that do not.
+ *
+ * blocks int32 [total_q, kv_heads, top]
+ * Limits: those of moe_kv4_select. Errors: as there.
+ */
+typedef struct {
+  moe_kv4_cache cache;
+  int block_tokens, batch, q_heads, total_q, max_q, max_pages, top;
+  const uint16_t* q;
+  long long q_stride;
+  const int32_t* cu_q;
+  const int32_t* kv_len;
+  const int32_t* block_table;
+  const int32_t* blocks;
+  float scale;
+  uint16_t* out;
+  float* lse;
+  int32_t* device_status;
+} moe_kv4_sparse_args;
+
+moe_status moe_kv4_sparse_attention(const moe_kv4_sparse_args* args, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -91,6 +91,48 @@ class MoeBlockNormArgs(ctypes.Structure):
                 ("w_offset", ctypes.c_float), ("residual_out", ctypes.c_void_p), ("out", ctypes.c_void_p)]
 
 
+class MoeRopePlan(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int), ("axes", ctypes.c_int), ("adjacent", ctypes.c_int),
+                ("scale", ctypes.c_float), ("turns", ctypes.c_void_p)]
+
+
+class MoeRopeArgs(ctypes.Structure):
+    _fields_ = [("plan", MoeRopePlan), ("tokens", ctypes.c_int), ("head_dim", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("k_heads", ctypes.c_int), ("inverse", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("k", ctypes.c_void_p),
+                ("k_stride", ctypes.c_longlong), ("positions", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_longlong), ("k_out", ctypes.c_void_p), ("k_out_stride", ctypes.c_longlong)]
+
+
+class MoeKv4AppendRopeArgs(ctypes.Structure):
+    _fields_ = [("cache", MoeKv4Cache), ("plan", MoeRopePlan), ("tokens", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("k", ctypes.c_void_p),
+                ("k_stride", ctypes.c_longlong), ("v", ctypes.c_void_p), ("v_stride", ctypes.c_longlong),
+                ("slots", ctypes.c_void_p), ("positions", ctypes.c_void_p), ("q_out", ctypes.c_void_p),
+                ("q_out_stride", ctypes.c_longlong), ("device_status", ctypes.c_void_p)]
+
+
+class MoeKv4Index(ctypes.Structure):
+    _fields_ = [("cache", MoeKv4Cache), ("block_tokens", ctypes.c_int), ("means", ctypes.c_void_p)]
+
+
+class MoeKv4SelectArgs(ctypes.Structure):
+    _fields_ = [("index", MoeKv4Index), ("batch", ctypes.c_int), ("q_heads", ctypes.c_int), ("total_q", ctypes.c_int),
+                ("max_q", ctypes.c_int), ("max_pages", ctypes.c_int), ("q", ctypes.c_void_p),
+                ("q_stride", ctypes.c_longlong), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("block_table", ctypes.c_void_p), ("top", ctypes.c_int), ("sink", ctypes.c_int), ("local", ctypes.c_int),
+                ("blocks", ctypes.c_void_p), ("device_status", ctypes.c_void_p)]
+
+
+class MoeKv4SparseArgs(ctypes.Structure):
+    _fields_ = [("cache", MoeKv4Cache), ("block_tokens", ctypes.c_int), ("batch", ctypes.c_int), ("q_heads", ctypes.c_int),
+                ("total_q", ctypes.c_int), ("max_q", ctypes.c_int), ("max_pages", ctypes.c_int), ("top", ctypes.c_int),
+                ("q", ctypes.c_void_p), ("q_stride", ctypes.c_longlong), ("cu_q", ctypes.c_void_p),
+                ("kv_len", ctypes.c_void_p), ("block_table", ctypes.c_void_p), ("blocks", ctypes.c_void_p),
+                ("scale", ctypes.c_float), ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+                ("device_status", ctypes.c_void_p)]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _Z = ctypes.c_size_t
@@ -129,6 +171,13 @@ _SIGS = {
     "moe_kv4_attention": (_I, [_P, _P, _Z, _P]),
     "moe_kv_step": (_I, [_P, _P]),
     "moe_block_norm": (_I, [_P, _P]),
+    "moe_rope_turns": (_I, [_P, _P, _I, _P]),
+    "moe_rope": (_I, [_P, _P]),
+    "moe_kv4_append_rope": (_I, [_P, _P]),
+    "moe_kv4_index_size": (_Z, [_I, _I, _I, _I, _I]),
+    "moe_kv4_index_update": (_I, [_P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "moe_kv4_select": (_I, [_P, _P]),
+    "moe_kv4_sparse_attention": (_I, [_P, _P]),
 }
 
 # The same structs as bytes: for a call per layer and token, filling a ctypes
@@ -136,6 +185,10 @@ _SIGS = {
 PACK_KV4_ATTN = struct.Struct("@4i2fP5iPqPPPfiiPP")
 PACK_KV_STEP = struct.Struct("@5i11P")
 PACK_BLOCK_NORM = struct.Struct("@iiPqPqPqiPPffffPP")
+PACK_ROPE = struct.Struct("@3ifP5iPqPqPPqPq")
+PACK_KV4_APPEND_ROPE = struct.Struct("@4i2fP3ifP2iPqPqPqPPPqP")
+PACK_KV4_SELECT = struct.Struct("@4i2fPiP5iPqPPP3iPP")
+PACK_KV4_SPARSE = struct.Struct("@4i2fP7iPqPPPPfPPP")
 
 MOE_KV4_WS_ZERO = 4096  # leading workspace bytes of moe_kv4_attention that start at zero
 
@@ -359,3 +412,36 @@ def moe_kv_step(args, stream=None):
 
 def moe_block_norm(args, stream=None):
     _check(lib().moe_block_norm(_arg(args), _stream(stream)), "moe_block_norm")
+
+
+def moe_rope_turns(inv_freq, axis):
+    """The entries of a rotation's table (host only): whole numbers of 64 bits."""
+    n = len(inv_freq)
+    out = (ctypes.c_uint64 * n)()
+    _check(lib().moe_rope_turns((ctypes.c_double * n)(*inv_freq), (ctypes.c_int32 * n)(*axis), n, out), "moe_rope_turns")
+    return list(out)
+
+
+def moe_rope(args, stream=None):
+    _check(lib().moe_rope(_arg(args), _stream(stream)), "moe_rope")
+
+
+def moe_kv4_append_rope(args, stream=None):
+    _check(lib().moe_kv4_append_rope(_arg(args), _stream(stream)), "moe_kv4_append_rope")
+
+
+def moe_kv4_index_size(num_pages, page_tokens, kv_heads, head_dim, block_tokens):
+    return lib().moe_kv4_index_size(num_pages, page_tokens, kv_heads, head_dim, block_tokens)
+
+
+def moe_kv4_index_update(index, batch, max_q, max_pages, cu_q, kv_len, block_table, device_status=None, stream=None):
+    _check(lib().moe_kv4_index_update(_arg(index), batch, max_q, max_pages, _ptr(cu_q), _ptr(kv_len), _ptr(block_table),
+                                      _ptr(device_status), _stream(stream)), "moe_kv4_index_update")
+
+
+def moe_kv4_select(args, stream=None):
+    _check(lib().moe_kv4_select(_arg(args), _stream(stream)), "moe_kv4_select")
+
+
+def moe_kv4_sparse_attention(args, stream=None):
+    _check(lib().moe_kv4_sparse_attention(_arg(args), _stream(stream)), "moe_kv4_sparse_attention")

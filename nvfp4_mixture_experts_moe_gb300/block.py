@@ -4,8 +4,12 @@
 keeps one layer's keys and values as NVFP4 pages, appends to them, reads rows
 back and attends over them (``moe_kv4_append``, ``moe_kv4_read``,
 ``moe_kv4_attention``), ``block_norm`` fuses the norm after a block, its gate,
-the residual and the norm before the next block (``moe_block_norm``). The C
-calls and their contracts are in ``include/moe_block.h``; torch only
+the residual and the norm before the next block (``moe_block_norm``). ``Rope``
+rotates queries and keys by their positions (``moe_rope``), or the cache does so
+on the way in (``moe_kv4_append_rope``); ``Kv4BlockIndex`` keeps the mean keys of
+blocks of cached tokens and picks blocks for each query by them
+(``moe_kv4_index_update``, ``moe_kv4_select``), over which the cache attends
+(``moe_kv4_sparse_attention``). The C calls and their contracts are in ``include/moe_block.h``; torch only
 allocates. A call runs on the current stream, or on ``stream=`` (a Stream or
 a raw handle), on which its outputs and its own workspace are then made; what
 the caller passes in has to be ready there. Wrong shapes, types or devices
@@ -44,6 +48,13 @@ def _where(stream):
             raise ValueError(f"stream: one of GPU {stream.device_index}, the current one is {dev}")
         return dev, stream.cuda_stream
     return dev, int(stream)
+
+
+def _stamp(device_status, status, dev):
+    """The address a call reports to: its own ``device_status``, or its object's."""
+    if device_status is None:
+        return status.data_ptr()
+    return device_status if isinstance(device_status, int) else _status(device_status, dev).data_ptr()
 
 
 def _ints(t, shape, what, dev):
@@ -215,6 +226,239 @@ class Kv4Cache:
             with _on(stream):
                 torch.maximum(self.status, ws[:4].view(_I32), out=self.status)
         return out, lse
+
+
+    def append_rotated(self, q, k, v, slots, positions, rope, q_out=None, device_status=None, stream=None):
+        """``append`` of keys that ``rope`` turns on the way; returns the turned queries.
+
+        ``q`` bf16 ``[tokens, q_heads, head_dim]`` (None: keys and values
+        only), ``positions`` int32 ``[tokens]``, or ``[axes, tokens]`` for a
+        rotation of several axes. ``q_out`` may be ``q`` itself. The keys are
+        quantised from fp32, not rounded to bf16 in between.
+        """
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the cache lies on GPU {self._dev}, the current one is {dev}")
+        D = self.head_dim
+        kp, ks = _rows(k, self.kv_heads, D, "k", dev)
+        vp, vs = _rows(v, self.kv_heads, D, "v", dev)
+        n = k.shape[0]
+        if v.shape[0] != n:
+            raise ValueError("k and v have different lengths")
+        if q is None:
+            heads, qp, qs, op, os_ = 0, 0, 0, 0, 0
+        else:
+            heads = q.shape[1] if q.dim() == 3 and q.shape[0] == n else -1
+            qp, qs = _rows(q, heads, D, "q", dev)
+            if q_out is None:
+                q_out = _empty((n, heads, D), _BF16, q.device, stream)
+                op, os_ = q_out.data_ptr(), heads * D
+            else:
+                op, os_ = _rows(q_out, heads, D, "q_out", dev)
+                if q_out.shape[0] != n:
+                    raise ValueError("q and q_out have different lengths")
+        a = B.PACK_KV4_APPEND_ROPE.pack(*self._fields, *rope._plan(dev), n, heads, qp, qs, kp, ks, vp, vs,
+                                        _ints(slots, (n,), "slots", dev), rope._positions(positions, n, dev), op, os_,
+                                        _stamp(device_status, self.status, dev))
+        B.moe_kv4_append_rope(a, handle)
+        return q_out
+
+    def sparse_attention(self, q, cu_q, kv_len, block_table, blocks, block_tokens, max_q, scale=None, want_lse=False,
+                         out=None, lse=None, device_status=None, stream=None):
+        """Causal attention of ``q`` over the blocks of ``block_tokens`` tokens that ``blocks`` lists.
+
+        ``blocks`` int32 ``[total_q, kv_heads, top]`` (``Kv4BlockIndex.select``,
+        or a caller's own: any order, negative ones are skipped); the others and
+        the result (out, lse) as in ``attention``.
+        """
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the cache lies on GPU {self._dev}, the current one is {dev}")
+        try:
+            total_q, heads, _ = q.shape
+            batch, = kv_len.shape
+            _, max_pages = block_table.shape
+            _, _, top = blocks.shape
+        except ValueError:
+            raise ValueError("q [rows, heads, dim], kv_len [batch], block_table [batch, max_pages] and blocks [rows, "
+                             "kv_heads, top] are needed") from None
+        qp, qs = _rows(q, heads, self.head_dim, "q", dev)
+        shape = (total_q, heads, self.head_dim)
+        if out is None:
+            out = _empty(shape, _BF16, q.device, stream)
+            op = out.data_ptr()
+        else:
+            op = _like(out, shape, _BF16, "out", dev)
+        if lse is None and want_lse:
+            lse = _empty((total_q, heads), _F32, q.device, stream)
+        lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse", dev)
+        try:
+            a = B.PACK_KV4_SPARSE.pack(*self._fields, block_tokens, batch, heads, total_q, max_q, max_pages, top, qp, qs,
+                                       _ints(cu_q, (batch + 1,), "cu_q", dev), _ints(kv_len, (batch,), "kv_len", dev),
+                                       _ints(block_table, (batch, max_pages), "block_table", dev),
+                                       _ints(blocks, (total_q, self.kv_heads, top), "blocks", dev),
+                                       self._scale if scale is None else scale, op, lp,
+                                       _stamp(device_status, self.status, dev))
+        except _UNPACKABLE as e:
+            raise ValueError(f"block_tokens, max_q or scale: {e}") from None
+        B.moe_kv4_sparse_attention(a, handle)
+        return out, lse
+
+
+class Rope:
+    """Rotary positions of one or several axes.
+
+    Of each head the first ``rotary_dim`` elements are turned in pairs, element
+    i with ``i + rotary_dim / 2`` (``pairs="half"``) or 2i with 2i + 1
+    (``"adjacent"``), pair p by ``positions[axis of p] * inv_freq[p]``.
+    ``inv_freq`` (``rotary_dim / 2`` numbers) is ``theta ** (-2p / rotary_dim)``
+    unless given; ``sections`` (pairs of each axis, in order) or ``axes`` (the
+    axis of every pair, 0 to 3) say which position a pair goes by; ``scale``
+    multiplies sine and cosine. The table is made on the current stream.
+    """
+
+    def __init__(self, rotary_dim, theta=10000.0, inv_freq=None, sections=None, axes=None, pairs="half", scale=1.0,
+                 device="cuda"):
+        _need(isinstance(rotary_dim, int) and rotary_dim >= 2 and rotary_dim % 2 == 0, "rotary_dim: an even number is needed")
+        half = rotary_dim // 2
+        _need(pairs in ("half", "adjacent"), "pairs: half or adjacent")
+        _need(sections is None or axes is None, "sections or axes, not both")
+        freq = [theta ** (-2.0 * p / rotary_dim) for p in range(half)] if inv_freq is None else [float(f) for f in inv_freq]
+        if sections is not None:
+            axes = [i for i, n in enumerate(sections) for _ in range(n)]
+        axes = [0] * half if axes is None else [int(i) for i in axes]
+        _need(len(freq) == half and len(axes) == half, f"{half} frequencies and axes are needed")
+        _need(all(0 <= i < 4 for i in axes), "axes: 0 to 3")
+        self.rotary_dim, self.pairs, self.scale = rotary_dim, pairs, float(scale)
+        self.axes = len(sections) if sections is not None else max(axes) + 1
+        _need(1 <= self.axes <= 4, "sections: of 1 to 4 axes")
+        turns = B.moe_rope_turns(freq, axes)
+        self.turns = torch.tensor([t - 2 ** 64 if t >= 2 ** 63 else t for t in turns], dtype=torch.int64, device=device)
+        self._dev = self.turns.get_device()
+        self._fields = (rotary_dim, self.axes, int(pairs == "adjacent"), self.scale, self.turns.data_ptr())
+
+    def _plan(self, dev):
+        if dev != self._dev:
+            raise ValueError(f"the rotation's table lies on GPU {self._dev}, the current one is {dev}")
+        return self._fields
+
+    def _positions(self, positions, n, dev):
+        if self.axes == 1 and positions.dim() == 1:
+            return _ints(positions, (n,), "positions", dev)
+        return _ints(positions, (self.axes, n), "positions", dev)
+
+    def __call__(self, q, positions, k=None, inverse=False, out=None, k_out=None, stream=None):
+        """``q`` (bf16 ``[tokens, heads, head_dim]``) and ``k`` turned: q_out, or (q_out, k_out) with ``k``.
+
+        ``positions`` int32 ``[tokens]`` or ``[axes, tokens]``; ``inverse``
+        turns back (the backward pass). ``out`` and ``k_out`` may be ``q`` and
+        ``k`` themselves.
+        """
+        dev, handle = _where(stream)
+        plan = self._plan(dev)
+        try:
+            n, heads, D = q.shape
+            k_heads = 0 if k is None else k.shape[1]
+        except (ValueError, IndexError):
+            raise ValueError("q and k: [tokens, heads, head_dim] are needed") from None
+        qp, qs = _rows(q, heads, D, "q", dev)
+        kp, ks, kop, kos = 0, 0, 0, 0
+        if out is None:
+            out = _empty((n, heads, D), _BF16, q.device, stream)
+            op, os_ = out.data_ptr(), heads * D
+        else:
+            op, os_ = _rows(out, heads, D, "out", dev)
+        if k is not None:
+            kp, ks = _rows(k, k_heads, D, "k", dev)
+            if k_out is None:
+                k_out = _empty((n, k_heads, D), _BF16, k.device, stream)
+                kop, kos = k_out.data_ptr(), k_heads * D
+            else:
+                kop, kos = _rows(k_out, k_heads, D, "k_out", dev)
+        if out.shape[0] != n or (k is not None and not k.shape[0] == k_out.shape[0] == n):
+            raise ValueError("q, k and their outputs have different lengths")
+        B.moe_rope(B.PACK_ROPE.pack(*plan, n, D, heads, k_heads, 1 if inverse else 0, qp, qs, kp, ks,
+                                    self._positions(positions, n, dev), op, os_, kop, kos), handle)
+        return out if k is None else (out, k_out)
+
+
+class Kv4BlockIndex:
+    """Mean keys of a cache's blocks of ``block_tokens`` tokens (32, 64 or 128).
+
+    ``means`` f16 ``[entries, kv_heads, head_dim]`` (layout in
+    ``include/moe_block.h``) may be given; otherwise it is allocated,
+    uninitialised, on the current stream. Bad device data is reported in the
+    cache's ``status`` where a call has no ``device_status``.
+    """
+
+    def __init__(self, cache, block_tokens, means=None):
+        _need(block_tokens in (32, 64, 128), "block_tokens: 32, 64 or 128")
+        shape = (cache.num_pages * max(1, cache.page_tokens // block_tokens), cache.kv_heads, cache.head_dim)
+        if means is None:
+            means = torch.empty(shape, dtype=torch.float16, device=cache.pool.device)
+        _need(means.is_cuda and means.get_device() == cache._dev and means.dtype == torch.float16 and
+              means.is_contiguous() and means.shape == shape, f"means: a contiguous f16 tensor {shape} on the cache's GPU")
+        self.cache, self.block_tokens, self.means = cache, block_tokens, means
+        self._dev = cache._dev
+        self._fields = (*cache._fields, block_tokens, means.data_ptr())
+        self.desc = B.MoeKv4Index(cache.desc, block_tokens, means.data_ptr())
+
+    def _here(self, stream):
+        dev, handle = _where(stream)
+        if dev != self._dev:
+            raise ValueError(f"the index lies on GPU {self._dev}, the current one is {dev}")
+        return dev, handle
+
+    def update(self, cu_q, kv_len, block_table, max_q, device_status=None, stream=None):
+        """The means of the blocks that a step's new tokens, already appended, made complete.
+
+        ``cu_q``, ``kv_len``, ``block_table`` and ``max_q`` as for the cache's ``attention``.
+        """
+        dev, handle = self._here(stream)
+        try:
+            batch, = kv_len.shape
+            _, max_pages = block_table.shape
+        except ValueError:
+            raise ValueError("kv_len [batch] and block_table [batch, max_pages] are needed") from None
+        _need(isinstance(max_q, int) and max_q < 2 ** 31, "max_q: a whole number of 32 bits is needed")
+        B.moe_kv4_index_update(self.desc, batch, max_q, max_pages, _ints(cu_q, (batch + 1,), "cu_q", dev),
+                               _ints(kv_len, (batch,), "kv_len", dev),
+                               _ints(block_table, (batch, max_pages), "block_table", dev),
+                               _stamp(device_status, self.cache.status, dev), handle)
+
+    def select(self, q, cu_q, kv_len, block_table, max_q, top, sink=1, local=1, blocks=None, device_status=None,
+               stream=None):
+        """The blocks each query picks: int32 ``[total_q, kv_heads, top]``, ascending, padded with -1.
+
+        The first ``sink`` and last ``local`` blocks that a query sees, and the
+        best of those in between by the score of its group's queries against
+        the blocks' means, up to ``top`` (at most 64) in all.
+        """
+        dev, handle = self._here(stream)
+        c = self.cache
+        try:
+            total_q, heads, _ = q.shape
+            batch, = kv_len.shape
+            _, max_pages = block_table.shape
+        except ValueError:
+            raise ValueError("q [rows, heads, dim], kv_len [batch] and block_table [batch, max_pages] are needed") from None
+        qp, qs = _rows(q, heads, c.head_dim, "q", dev)
+        shape = (total_q, c.kv_heads, top)
+        if blocks is None:
+            _need(isinstance(top, int) and top >= 0, "top: a whole number is needed")
+            blocks = _empty(shape, _I32, q.device, stream)
+            bp = blocks.data_ptr()
+        else:
+            bp = _ints(blocks, shape, "blocks", dev)
+        try:
+            a = B.PACK_KV4_SELECT.pack(*self._fields, batch, heads, total_q, max_q, max_pages, qp, qs,
+                                       _ints(cu_q, (batch + 1,), "cu_q", dev), _ints(kv_len, (batch,), "kv_len", dev),
+                                       _ints(block_table, (batch, max_pages), "block_table", dev), top, sink, local, bp,
+                                       _stamp(device_status, c.status, dev))
+        except _UNPACKABLE as e:
+            raise ValueError(f"max_q, top, sink or local: {e}") from None
+        B.moe_kv4_select(a, handle)
+        return blocks
 
 
 class KvStep:

@@ -40,6 +40,13 @@ moe_status launch_kv4_read(const moe_kv4_cache& c, const int32_t* slots, int n, 
                            int32_t* status, cudaStream_t s);
 moe_status launch_kv_step(const moe_kv_step_args& a, cudaStream_t s);
 moe_status launch_block_norm(const moe_block_norm_args& a, cudaStream_t s);
+moe_status launch_rope(const moe_rope_args& a, cudaStream_t s);
+moe_status launch_kv4_append_rope(const moe_kv4_append_rope_args& a, cudaStream_t s);
+moe_status launch_kv4_index_update(const moe_kv4_index& x, int batch, int max_q, int max_pages, const int32_t* cu_q,
+                                   const int32_t* kv_len, const int32_t* table, int32_t* status, cudaStream_t s);
+moe_status launch_kv4_select(const moe_kv4_select_args& a, cudaStream_t s);
+moe_status launch_kv4_sparse(const moe_kv4_sparse_args& a, cudaStream_t s);
+constexpr int kSparseTop = 64, kSparseGroup = 16;   // blocks of a query, query heads of a key/value head
 
 // Attention of requests with up to max_rows (at most kKvDecodeRows) query rows
 // per key/value head; the others are skipped.

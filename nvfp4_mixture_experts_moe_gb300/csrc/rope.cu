@@ -1,0 +1,361 @@
+// Rotary positions of queries and keys, in place or on the way into the cache.
+//
+// Mathematics. Pair p of a token turns by pos * inv_freq_p. In turns the angle
+// is the fraction of pos * (inv_freq_p / 2 pi), so with the factor as a 64-bit
+// fixed-point fraction a product modulo 2^64 is that fraction to 2^-62 turns
+// per position, whatever the position. It is reduced to the nearest quarter
+// turn exactly, and sine and cosine of the rest (at most pi / 4) are Taylor
+// polynomials in fp32, whose terms end below 2^-28.
+//
+// A thread has eight pairs of a token for as many heads as it is given: their
+// sines and cosines (some 30 instructions a pair) are worked out once.
+#include "kernels.cuh"
+#include "kv4.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kThreads = 256;
+
+// (cos, sin) of a pair's angle, times the plan's scale.
+__device__ __forceinline__ float2 rotation(uint64_t turns, int pos, float scale) {
+  const uint64_t frac = (turns & ~3ull) * (uint64_t)(int64_t)pos;
+  const uint64_t quarter = (frac + (1ull << 61)) >> 62;
+  const int rest = (int)((int64_t)(frac - (quarter << 62)) >> 30);        // in 2^-34 turns, [-2^31, 2^31)
+  const float r = (float)rest * 3.6572952e-10f, x = r * r;               // 2 pi / 2^34
+  const float s = fmaf(r * x, fmaf(x, fmaf(x, fmaf(x, 1.0f / 362880.0f, -1.0f / 5040.0f), 1.0f / 120.0f), -1.0f / 6.0f), r);
+  const float c = fmaf(x, fmaf(x, fmaf(x, fmaf(x, fmaf(x, -1.0f / 3628800.0f, 1.0f / 40320.0f), -1.0f / 720.0f),
+                                       1.0f / 24.0f), -0.5f), 1.0f);
+  const bool swap = quarter & 1, neg_c = (quarter + 1) & 2, neg_s = quarter & 2;
+  const float cq = swap ? s : c, sq = swap ? c : s;
+  return make_float2(scale * (neg_c ? -cq : cq), scale * (neg_s ? -sq : sq));
+}
+
+__device__ __forceinline__ float2 rotation_of(const moe_rope_plan& plan, int pair, const int32_t* positions, int tokens, int t) {
+  const uint64_t turns = __ldg(reinterpret_cast<const unsigned long long*>(plan.turns) + pair);
+  const int axis = min((int)(turns & 3), plan.axes - 1);
+  return rotation(turns, __ldg(positions + (size_t)axis * tokens + t), plan.scale);
+}
+
+__device__ __forceinline__ void unpack8(const uint4& w, float (&x)[8]) {
+  const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(v[i] << 16);
+    x[2 * i + 1] = __uint_as_float(v[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(float2_to_bf16x2_bits(x[0], x[1]), float2_to_bf16x2_bits(x[2], x[3]),
+                    float2_to_bf16x2_bits(x[4], x[5]), float2_to_bf16x2_bits(x[6], x[7]));
+}
+
+__device__ __forceinline__ void turn(float2 cs, float& a, float& b) {
+  const float x = a;
+  a = fmaf(x, cs.x, -b * cs.y);
+  b = fmaf(x, cs.y, b * cs.x);
+}
+
+// Eight pairs: x and y are the first and second elements (halves), or sixteen
+// neighbouring elements (adjacent).
+__device__ __forceinline__ void turn8(const float2 (&cs)[8], bool adjacent, float (&x)[8], float (&y)[8]) {
+  if (adjacent) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      turn(cs[i], x[2 * i], x[2 * i + 1]);
+      turn(cs[4 + i], y[2 * i], y[2 * i + 1]);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(cs[i], x[i], y[i]);
+  }
+}
+
+struct RopeRows {
+  moe_rope_args a;
+  int splits, units, turning;   // threads of a token and unit; units of a head, the first `turning` of them with pairs
+};
+
+// Rows of 16-byte alignment, rotary_dim a multiple of 16: a unit is eight pairs
+// or sixteen elements to copy, two 16-byte loads and stores a head.
+__global__ void __launch_bounds__(kThreads) rope_vector_kernel(const __grid_constant__ RopeRows p) {
+  const moe_rope_args& a = p.a;
+  pdl_wait();
+  const unsigned idx = blockIdx.x * kThreads + threadIdx.x;
+  const int u = idx % p.units;
+  const unsigned rest = idx / p.units;
+  const int first = rest % p.splits, t = rest / p.splits;
+  if (t >= a.tokens) return;
+  const int R = a.plan.rotary_dim, heads = a.q_heads + a.k_heads;
+  const bool turns = u < p.turning;
+  int lo, hi;   // the unit's two runs of eight elements
+  float2 cs[8];
+  if (turns) {
+    lo = a.plan.adjacent ? 16 * u : 8 * u;
+    hi = a.plan.adjacent ? lo + 8 : lo + R / 2;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      cs[i] = rotation_of(a.plan, 8 * u + i, a.positions, a.tokens, t);
+      if (a.inverse) cs[i].y = -cs[i].y;
+    }
+  } else {
+    lo = R + 16 * (u - p.turning);
+    hi = lo + 8;
+  }
+  const bool second = hi < a.head_dim;
+  const uint16_t* const q = a.q + (size_t)t * a.q_stride;
+  const uint16_t* const k = a.k + (size_t)t * a.k_stride;
+  uint16_t* const qo = a.q_out + (size_t)t * a.q_out_stride;
+  uint16_t* const ko = a.k_out + (size_t)t * a.k_out_stride;
+  constexpr int kAhead = 4;
+  for (int h0 = first; h0 < heads; h0 += kAhead * p.splits) {
+    uint4 w[kAhead][2];
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int h = h0 + j * p.splits;
+      if (h >= heads) break;
+      const uint16_t* src = h < a.q_heads ? q + (size_t)h * a.head_dim : k + (size_t)(h - a.q_heads) * a.head_dim;
+      w[j][0] = *reinterpret_cast<const uint4*>(src + lo);
+      if (second) w[j][1] = *reinterpret_cast<const uint4*>(src + hi);
+    }
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j) {
+      const int h = h0 + j * p.splits;
+      if (h >= heads) break;
+      uint16_t* dst = h < a.q_heads ? qo + (size_t)h * a.head_dim : ko + (size_t)(h - a.q_heads) * a.head_dim;
+      if (turns) {
+        float x[8], y[8];
+        unpack8(w[j][0], x);
+        unpack8(w[j][1], y);
+        turn8(cs, a.plan.adjacent, x, y);
+        w[j][0] = pack8(x);
+        w[j][1] = pack8(y);
+      }
+      *reinterpret_cast<uint4*>(dst + lo) = w[j][0];
+      if (second) *reinterpret_cast<uint4*>(dst + hi) = w[j][1];
+    }
+  }
+}
+
+// Any alignment and even rotary_dim: a unit is one pair or two elements to copy.
+__global__ void __launch_bounds__(kThreads) rope_pair_kernel(const __grid_constant__ RopeRows p) {
+  const moe_rope_args& a = p.a;
+  pdl_wait();
+  const unsigned idx = blockIdx.x * kThreads + threadIdx.x;
+  const int u = idx % p.units;
+  const unsigned rest = idx / p.units;
+  const int first = rest % p.splits, t = rest / p.splits;
+  if (t >= a.tokens) return;
+  const int R = a.plan.rotary_dim, heads = a.q_heads + a.k_heads;
+  const bool turns = u < p.turning;
+  const int lo = !turns ? R + 2 * (u - p.turning) : a.plan.adjacent ? 2 * u : u;
+  const int hi = turns && !a.plan.adjacent ? u + R / 2 : lo + 1;
+  const bool second = hi < a.head_dim;
+  float2 cs = make_float2(1.0f, 0.0f);
+  if (turns) {
+    cs = rotation_of(a.plan, u, a.positions, a.tokens, t);
+    if (a.inverse) cs.y = -cs.y;
+  }
+  for (int h = first; h < heads; h += p.splits) {
+    const bool is_q = h < a.q_heads;
+    const uint16_t* src = is_q ? a.q + (size_t)t * a.q_stride + (size_t)h * a.head_dim
+                               : a.k + (size_t)t * a.k_stride + (size_t)(h - a.q_heads) * a.head_dim;
+    uint16_t* dst = is_q ? a.q_out + (size_t)t * a.q_out_stride + (size_t)h * a.head_dim
+                         : a.k_out + (size_t)t * a.k_out_stride + (size_t)(h - a.q_heads) * a.head_dim;
+    uint16_t x = src[lo], y = second ? src[hi] : (uint16_t)0;
+    if (turns) {
+      float fx = bf16_bits_to_float(x), fy = bf16_bits_to_float(y);
+      turn(cs, fx, fy);
+      x = float_to_bf16_bits(fx);
+      y = float_to_bf16_bits(fy);
+    }
+    dst[lo] = x;
+    if (second) dst[hi] = y;
+  }
+}
+
+// ------------------------------------------------ on the way into the cache
+
+struct AppendRope {
+  moe_kv4_append_rope_args a;
+  int splits;     // warps of a run of tokens
+  int page_log;
+};
+
+// Codes and scale of sixteen values of which a thread (kWhole) or a pair of
+// neighbouring threads has all. NaNs are gone, infinities saturate.
+__device__ __forceinline__ float amax8(const float (&x)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+  return m;
+}
+
+__device__ __forceinline__ uint32_t codes8(const float (&x)[8], float r) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w |= e2m1x2_rn(__fmul_rn(x[2 * i], r), __fmul_rn(x[2 * i + 1], r)) << (8 * i);
+  return w;
+}
+
+struct Scale {
+  uint32_t code;
+  float r;     // gs / scale; 0 with a scale of 0, whose codes are 0
+};
+
+__device__ __forceinline__ Scale scale_of(float amax, float gs) {
+  Scale s;
+  s.code = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
+  const float v = e4m3_decode(s.code);
+  s.r = v > 0.0f ? __fdiv_rn(gs, v) : 0.0f;
+  return s;
+}
+
+__device__ __forceinline__ void no_nan(float (&x)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (x[i] != x[i]) x[i] = 0.0f;
+}
+
+// A warp takes 512 / D consecutive tokens (a lane: sixteen elements of one) and
+// every splits-th of their rows: query heads, key heads, value heads.
+template <int D>
+__global__ void __launch_bounds__(kThreads) kv4_append_rope_kernel(const __grid_constant__ AppendRope p) {
+  using L = Kv4Block<D>;
+  constexpr int kUnits = D / 16, kTokens = 32 / kUnits, kWarps = kThreads / 32;
+  const moe_kv4_append_rope_args& a = p.a;
+  pdl_wait();
+  const int lane = threadIdx.x & 31, u = lane % kUnits;
+  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
+  const int first = w % p.splits;
+  const long long t0 = (long long)(w / p.splits) * kTokens;
+  if (t0 >= a.tokens) return;                        // the same for a whole warp
+  const bool real = t0 + lane / kUnits < a.tokens;
+  const int t = real ? (int)t0 + lane / kUnits : a.tokens - 1;   // lanes past the end follow, and store nothing
+  const int R = a.plan.rotary_dim, Hq = a.q_heads, Hk = a.cache.kv_heads;
+  const bool turns = u < R / 16;
+  const int lo = turns && !a.plan.adjacent ? 8 * u : 16 * u, hi = turns && !a.plan.adjacent ? lo + R / 2 : lo + 8;
+  const int slot = real ? __ldg(a.slots + t) : -1;
+  const long long limit = (long long)a.cache.num_pages << p.page_log;
+  const bool keep = slot >= 0 && slot < limit;
+  if (slot >= limit && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+  float2 cs[8];
+  if (turns)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) cs[i] = rotation_of(a.plan, 8 * u + i, a.positions, a.tokens, t);
+  const int row = slot % kKvBlock;
+  uint8_t* const pool = static_cast<uint8_t*>(a.cache.pool);
+  auto block_of = [&](int h) {
+    return pool + kv4_block_offset(slot >> p.page_log, h, Hk, (1 << p.page_log) / kKvBlock,
+                                   (slot & ((1 << p.page_log) - 1)) / kKvBlock, L::kBytes);
+  };
+  for (int r = first; r < Hq + 2 * Hk; r += p.splits) {
+    float x[8], y[8];
+    if (r < Hq) {
+      const uint16_t* src = a.q + (size_t)t * a.q_stride + r * D;
+      uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src + lo)), v1 = __ldg(reinterpret_cast<const uint4*>(src + hi));
+      if (turns) {
+        unpack8(v0, x);
+        unpack8(v1, y);
+        turn8(cs, a.plan.adjacent, x, y);
+        v0 = pack8(x);
+        v1 = pack8(y);
+      }
+      if (real) {
+        uint16_t* dst = a.q_out + (size_t)t * a.q_out_stride + r * D;
+        *reinterpret_cast<uint4*>(dst + lo) = v0;
+        *reinterpret_cast<uint4*>(dst + hi) = v1;
+      }
+      continue;
+    }
+    const bool key = r < Hq + Hk;
+    const int h = r - Hq - (key ? 0 : Hk);
+    const uint16_t* src = (key ? a.k + (size_t)t * a.k_stride : a.v + (size_t)t * a.v_stride) + h * D;
+    const int at0 = key ? lo : 16 * u, at1 = key ? hi : 16 * u + 8;
+    unpack8(__ldg(reinterpret_cast<const uint4*>(src + at0)), x);
+    unpack8(__ldg(reinterpret_cast<const uint4*>(src + at1)), y);
+    if (key && turns) turn8(cs, a.plan.adjacent, x, y);
+    no_nan(x);
+    no_nan(y);
+    const float gs = key ? a.cache.k_gs : a.cache.v_gs;
+    float mx = amax8(x), my = amax8(y);
+    // Halves: two neighbouring lanes have the two runs of a group of sixteen.
+    const float ox = __shfl_xor_sync(0xffffffffu, mx, 1), oy = __shfl_xor_sync(0xffffffffu, my, 1);
+    const bool split = key && turns && !a.plan.adjacent;
+    if (split) {
+      mx = fmaxf(mx, ox);
+      my = fmaxf(my, oy);
+    } else {
+      mx = my = fmaxf(mx, my);
+    }
+    if (!keep) continue;
+    const Scale sx = scale_of(mx, gs), sy = split ? scale_of(my, gs) : sx;
+    uint8_t* const blk = block_of(h) + (key ? 0 : L::kValueCodes);
+    *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at0 / 2) = codes8(x, sx.r);
+    *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at1 / 2) = codes8(y, sy.r);
+    uint8_t* const scales = blk + L::kKeyScales + row * L::kScaleRow;
+    if (!split) {
+      scales[u] = (uint8_t)sx.code;
+    } else if (u % 2 == 0) {
+      scales[at0 / 16] = (uint8_t)sx.code;
+      scales[at1 / 16] = (uint8_t)sy.code;
+    }
+  }
+}
+
+}  // namespace
+
+// How many threads share a token's heads: as many as keep the GPU busy, one
+// for every eight heads at least.
+static int head_splits(long long tokens_units, int heads) {
+  const long long want = (long long)sm_count() * 2048 / (tokens_units > 0 ? tokens_units : 1) + 1;
+  const long long least = (heads + 7) / 8;
+  return (int)(want < least ? least : want > heads ? heads : want);
+}
+
+moe_status launch_rope(const moe_rope_args& args, cudaStream_t s) {
+  moe_rope_args a = args;
+  const bool in_place = a.q_out == a.q && (a.k_heads == 0 || a.k_out == a.k);
+  if (a.k_heads == 0) {   // never used
+    a.k = a.q;
+    a.k_stride = a.q_stride;
+    a.k_out = a.q_out;
+    a.k_out_stride = a.q_out_stride;
+  }
+  auto wide = [](const void* x, long long stride) { return reinterpret_cast<uintptr_t>(x) % 16 == 0 && stride % 8 == 0; };
+  const bool vectors = a.head_dim % 8 == 0 && a.plan.rotary_dim % 16 == 0 && wide(a.q, a.q_stride) &&
+                       wide(a.k, a.k_stride) && wide(a.q_out, a.q_out_stride) && wide(a.k_out, a.k_out_stride);
+  const int per = vectors ? 16 : 2, rest = a.head_dim - a.plan.rotary_dim;
+  RopeRows p;
+  p.a = a;
+  p.turning = a.plan.rotary_dim / per;
+  p.units = p.turning + (in_place ? 0 : (rest + per - 1) / per);
+  const int heads = a.q_heads + a.k_heads;
+  p.splits = head_splits((long long)a.tokens * p.units, heads);
+  const long long per_token = (long long)p.splits * p.units;
+  if (a.tokens > (1ll << 31) / per_token) return MOE_ERR_UNSUPPORTED;   // threads are counted in 32 bits
+  const unsigned grid = (unsigned)((a.tokens * per_token + kThreads - 1) / kThreads);
+  const cudaError_t e = launch_ex(true, vectors ? rope_vector_kernel : rope_pair_kernel, dim3(grid), dim3(kThreads), 0, s, p);
+  if (e != cudaSuccess) return cuda_ok(e);
+  count_launches(1);
+  return MOE_OK;
+}
+
+moe_status launch_kv4_append_rope(const moe_kv4_append_rope_args& a, cudaStream_t s) {
+  AppendRope p;
+  p.a = a;
+  p.page_log = __builtin_ctz(a.cache.page_tokens);
+  const int D = a.cache.head_dim, rows = a.q_heads + 2 * a.cache.kv_heads, tokens = 512 / D;
+  const long long runs = ((long long)a.tokens + tokens - 1) / tokens;
+  p.splits = head_splits(runs * 32, rows);
+  const long long grid = (runs * p.splits + kThreads / 32 - 1) / (kThreads / 32);
+  if (grid > 0x7fffffffll / 8) return MOE_ERR_UNSUPPORTED;   // warps are counted in 32 bits
+  const cudaError_t e = launch_ex(true, D == 64 ? kv4_append_rope_kernel<64> : kv4_append_rope_kernel<128>,
+                                  dim3((unsigned)grid), dim3(kThreads), 0, s, p);
+  if (e != cudaSuccess) return cuda_ok(e);
+  count_launches(1);
+  return MOE_OK;
+}
+
+}  // namespace moe

@@ -6,15 +6,23 @@ Test infrastructure only (see the package docstring for who may import it).
 * ``KvCache``: NVFP4 rows by slot (``nvfp4.quantize`` with a static global
   scale) and the byte layout of a pool's 16-token blocks;
 * ``attention``: one query row at a time over cached values;
-* ``block_norm``: norm, gate, residual, norm.
+* ``block_norm``: norm, gate, residual, norm;
+* ``rope``: pairs as complex numbers, angles of exact fractions of a turn;
+* ``grid``, ``block_mean``, ``picks``: a block's mean key on its grid, and the
+  blocks that one query picks.
 
 Each is pinned by tests/test_oracle_block.py.
 """
 from __future__ import annotations
 
+from fractions import Fraction
+
 import numpy as np
 
 from . import nvfp4
+
+# 2 pi to 60 decimal places
+TWO_PI = Fraction(6283185307179586476925286766559005768394338798750211641949889, 10 ** 60)
 
 
 def step(ctx, new, table, free, count, P, tokens):
@@ -123,3 +131,51 @@ def block_norm(x, residual, gate=None, w_post=None, w_pre=None, a=1.0, b=1.0, ep
         n = x if w_post is None else rms(x, w_post)
         r = r + b * (n if gate is None else gate * n)
     return r, None if w_pre is None else rms(r, w_pre)
+
+
+def turns(inv_freq, position):
+    """The fraction of a turn, in [0, 1), by which a pair of this frequency turns at a position: exact up to the
+    60 places of pi."""
+    return Fraction(float(inv_freq)) * int(position) / TWO_PI % 1
+
+
+def rope(x, positions, inv_freq, axis, pairs, scale=1.0, inverse=False):
+    """``x`` [T, heads, D] turned; ``positions`` [axes, T]. Returns (y, sum |a| + |b| of each element's pair, scaled)."""
+    T, _, D = x.shape
+    half = len(inv_freq)
+    lo, hi = ((np.arange(half), half + np.arange(half)) if pairs == "half" else (2 * np.arange(half), 2 * np.arange(half) + 1))
+    angle = np.array([[float(turns(f, positions[a][t])) for f, a in zip(inv_freq, axis)] for t in range(T)])
+    z = np.exp((-2j if inverse else 2j) * np.pi * angle.reshape(T, half))[:, None]
+    y, size = x.copy(), np.abs(x)
+    w = (x[..., lo] + 1j * x[..., hi]) * z * scale
+    y[..., lo], y[..., hi] = w.real, w.imag
+    size[..., lo] = size[..., hi] = (np.abs(x[..., lo]) + np.abs(x[..., hi])) * abs(scale)
+    return y, size
+
+
+def grid(x, bits):
+    """``x`` rounded, ties to even, to multiples of 2^(E - bits), E the exponent of its largest magnitude (at least
+    -100). Returns (the multiples, the step)."""
+    top = max(np.abs(x).max(), 2.0 ** -100)
+    step = 2.0 ** (np.frexp(top)[1] - 1 - bits)
+    return np.rint(x / step), step
+
+
+def block_mean(rows):
+    """Mean of a block's rows [tokens, D] (code * scale, not divided by gs), on its grid of 8 bits."""
+    n, step = grid(np.asarray(rows, np.float64).sum(0) / len(rows), 6)
+    return n * step
+
+
+def picks(q, means, position, block_tokens, top, sink, local):
+    """One query's blocks for one head: ``q`` [group, D], ``means`` [blocks, D] (None where the page is bad)."""
+    if position < 0:
+        return []
+    seen = position // block_tokens + 1
+    if seen <= top:
+        return list(range(seen))
+    u = grid(np.where(np.isfinite(q), q, 0.0), 5)[0].sum(0)
+    ranked = range(sink, seen - local)
+    score = {j: -np.inf if means[j] is None else float(u @ means[j]) for j in ranked}
+    best = sorted(ranked, key=lambda j: (-score[j], j))[:top - sink - local]
+    return sorted(list(range(sink)) + best + list(range(seen - local, seen)))
