@@ -13,6 +13,20 @@ struct RowOwner {
   bool bad;
 };
 
+// Request b, its lengths cut to what the tables hold; n is set, b is -1 and bad
+// true for one whose rows cannot be.
+__device__ __forceinline__ RowOwner request_of(const int32_t* cu_q, const int32_t* kv_len, int total_q, int max_q, int cap,
+                                               int b) {
+  const int c0 = __ldg(cu_q + b), c1 = __ldg(cu_q + b + 1), kv = __ldg(kv_len + b);
+  RowOwner r = {b, c0, c1 - c0, max(0, min(kv, cap)), false};
+  r.bad = kv != r.kv;
+  if (c0 < 0 || r.n < 0 || c1 > total_q || r.n > max_q) {
+    r.b = -1;
+    r.bad = true;
+  }
+  return r;
+}
+
 // The request of row t, by a whole warp: cu_q ascends from 0. One load decides
 // where every request before t has one row (a decode step); otherwise 32
 // places at a time.
@@ -33,19 +47,22 @@ __device__ __forceinline__ RowOwner row_owner(const int32_t* cu_q, const int32_t
       width = min(step, end - lo);
     }
   }
-  const int c0 = __ldg(cu_q + lo), c1 = __ldg(cu_q + lo + 1);
-  if (c0 > t || c1 <= t) return r;   // past the last request
-  const int kv = __ldg(kv_len + lo);
-  r.n = c1 - c0;
-  r.c0 = c0;
-  r.kv = max(0, min(kv, cap));
-  r.bad = kv != r.kv;
-  if (c0 < 0 || c1 > total_q || r.n > max_q) {
-    r.bad = true;
-    return r;
+  if (__ldg(cu_q + lo) > t || __ldg(cu_q + lo + 1) <= t) return r;   // past the last request
+  return request_of(cu_q, kv_len, total_q, max_q, cap, lo);
+}
+
+// The same by a thread on its own.
+__device__ __forceinline__ RowOwner row_owner_thread(const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q,
+                                                     int max_q, int cap, int t) {
+  int lo = 0, hi = batch - 1;   // the last b with cu_q[b] <= t
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(cu_q + mid) <= t) lo = mid;
+    else hi = mid - 1;
   }
-  r.b = lo;
-  return r;
+  const RowOwner none = {-1, 0, 0, 0, false};
+  if (__ldg(cu_q + lo) > t || __ldg(cu_q + lo + 1) <= t) return none;
+  return request_of(cu_q, kv_len, total_q, max_q, cap, lo);
 }
 
 }  // namespace moe
