@@ -93,26 +93,95 @@ __device__ __forceinline__ float on_grid(uint32_t x, float scale) {
   return finite_bits(x) == 0 ? 0.0f : rintf(__uint_as_float(x << 16) * scale);
 }
 
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+  uint32_t r;
+  asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+  return r;
+}
+
 // ---------------------------------------------------------- few queries
 // D / 16 lanes score a block, kAhead blocks at a time (the trips to memory for
-// the table and the means are what takes long); then the CTA's threads find
-// the key of rank `need`, the CTAs of a cluster sending theirs to the first.
-constexpr int kThreads = 512, kWarps = kThreads / 32, kKeys = 8192, kPer = kKeys / kThreads + 1, kAhead = 4;
+// the table and the means are what takes long); the CTAs of a cluster send
+// their keys to the first. There a warp cuts each run of keys to its best, and
+// one warp cuts what is left of all runs: halving within a warp needs no
+// barriers, with them a step took 860 cycles.
+constexpr int kThreads = 512, kWarps = kThreads / 32, kKeys = 4096, kAhead = 4;
+constexpr int kPer = (kKeys + kSparseTop + kThreads - 1) / kThreads;      // keys a lane of the first cut
+constexpr int kPer2 = kWarps * kSparseTop / 32;                           // and of the second
 
 struct FewSmem {
-  uint32_t keys[kKeys + kSparseTop];
-  float u[128];
+  uint32_t keys[kPer * kThreads];
+  alignas(16) float u[128];
   int best[2][kSparseTop];               // blocks that earlier chunks left
   uint32_t best_key[2][kSparseTop];
-  int counts[3], above[kWarps], equal[kWarps];
-  uint32_t lowest, highest, group_top;
+  uint32_t run_key[kWarps * kSparseTop];
+  int run_blk[kWarps * kSparseTop];
+  uint32_t group_top;
 };
+
+// The `need` largest of `total` keys (reg[i]: key 32 i + lane, 0 past the end), the first of equal ones, to put(where,
+// i) in order; all where there are no more. By a whole warp.
+template <int N, class Put>
+__device__ __forceinline__ void warp_cut(const uint32_t (&reg)[N], int total, int need, Put put) {
+  const int lane = threadIdx.x & 31, groups = (total + 31) / 32;
+  uint32_t lo = 0xffffffffu, hi = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i)
+    if (32 * i + lane < total) {
+      lo = min(lo, reg[i]);
+      hi = max(hi, reg[i]);
+    }
+  lo = __reduce_min_sync(kFull, lo);
+  hi = __reduce_max_sync(kFull, hi) + 1;
+  int at_least = total, above = 0;   // keys >= lo, >= hi
+  for (int step = 0; at_least > need && hi - lo > 1; ++step) {
+    // three keys in between at once
+    const uint32_t m1 = middle(lo, hi, step), m0 = m1 - lo > 1 ? middle(lo, m1, step) : lo,
+                   m2 = hi - m1 > 1 ? middle(m1, hi, step) : hi;
+    int c0 = 0, c1 = 0, c2 = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (i >= groups) break;
+      c0 += reg[i] >= m0;
+      c1 += reg[i] >= m1;
+      c2 += reg[i] >= m2;
+    }
+    // at most 32 * 32 keys: two counts a word
+    const unsigned two = __reduce_add_sync(kFull, (unsigned)(c0 | c1 << 16));
+    c2 = m2 == hi ? above : __reduce_add_sync(kFull, c2);
+    c0 = m0 == lo ? at_least : (int)(two & 0xffffu);
+    c1 = (int)(two >> 16);
+    if (c2 >= need && m2 != hi) lo = m2, at_least = c2;
+    else if (c1 >= need) lo = m1, at_least = c1, hi = m2, above = c2;
+    else if (c0 >= need) lo = m0, at_least = c0, hi = m1, above = c1;
+    else hi = m0, above = c0;
+  }
+  int equals = at_least > need ? need - above : total;   // too many of one key: the first of them
+  int w = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (i >= groups) break;
+    const bool in = 32 * i + lane < total;
+    const unsigned below = (1u << lane) - 1, e = __ballot_sync(kFull, in && reg[i] == lo);
+    const bool take = in && (reg[i] > lo || (reg[i] == lo && __popc(e & below) < equals));
+    const unsigned t = __ballot_sync(kFull, take);
+    if (take) put(w + __popc(t & below), i);
+    w += __popc(t);
+    equals -= __popc(e);
+  }
+}
 
 // One query and head, by a whole cluster.
 template <int D>
 __device__ __forceinline__ void select_row(const SelectArgs& p, const RowOwner& own, int t, int h, FewSmem& sm, int rank,
                                            int ranks) {
   constexpr int kLanes = D / 16, kRows = 32 / kLanes;
+  constexpr int kStep = kWarps * kRows;   // blocks that a CTA's warps take at once
   const moe_kv4_select_args& a = p.a;
   const moe_kv4_cache& c = a.index.cache;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -129,157 +198,122 @@ __device__ __forceinline__ void select_row(const SelectArgs& p, const RowOwner& 
   }
   if (v.need == 0) return;
 
+  const int32_t* const table = a.block_table + (size_t)own.b * a.max_pages;
+  int entry[kAhead];
+  uint4 w[kAhead][2];
+  // The means of this thread's blocks of a round, asked for before what multiplies them is there.
+  auto load = [&](int from, int n, int j0) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int j = j0 + i * kStep + lane / kLanes;
+      entry[i] = j < n ? entry_of(a.index, page_log, p.block_log, table, from + j) : -2;
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
+      if (entry[i] >= 0) {
+        const uint4* m = reinterpret_cast<const uint4*>(a.index.means + ((size_t)entry[i] * Hk + h) * D) + lane % kLanes * 2;
+        w[i][0] = __ldg(m);
+        w[i][1] = __ldg(m + 1);
+      }
+    }
+  };
+  const int first = rank * kStep * kAhead + warp * kRows;
   if (tid == 0) sm.group_top = 0;
+  uint32_t x[kSparseGroup];   // element tid of the group's queries
+  if (tid < D) {
+    const uint16_t* const q = a.q + (size_t)t * a.q_stride + (size_t)h * heads * D + tid;
+#pragma unroll
+    for (int i = 0; i < kSparseGroup; ++i) x[i] = i < heads ? q[i * D] : 0u;
+  }
+  load(v.c0, min(kKeys, v.c1 - v.c0), first);
   __syncthreads();
-  const uint16_t* const q = a.q + (size_t)t * a.q_stride + (size_t)h * heads * D;
-  uint32_t top = 0;
-  for (int i = tid; i < heads * D; i += kThreads) top = max(top, finite_bits(q[i]));
-  top = __reduce_max_sync(kFull, top);
-  if (lane == 0) atomicMax(&sm.group_top, top);
+  if (tid < D) {
+    uint32_t top = 0;
+#pragma unroll
+    for (int i = 0; i < kSparseGroup; ++i) top = max(top, finite_bits(x[i]));
+    top = __reduce_max_sync(kFull, top);
+    if (lane == 0) atomicMax(&sm.group_top, top);
+  }
   __syncthreads();
   if (tid < D) {
     const float scale = grid_scale(sm.group_top);
     float s = 0.0f;
-    for (int i = 0; i < heads; ++i) s += on_grid(q[i * D + tid], scale);
+#pragma unroll
+    for (int i = 0; i < kSparseGroup; ++i) s += on_grid(x[i], scale);
     sm.u[tid] = s;
   }
   __syncthreads();
-  float mine[16];   // this lane's elements of u
-#pragma unroll
-  for (int i = 0; i < 16; ++i) mine[i] = sm.u[(lane % kLanes) * 16 + i];
 
-  const int32_t* const table = a.block_table + (size_t)own.b * a.max_pages;
   uint32_t* const keys = ranks > 1 ? cg::this_cluster().map_shared_rank(sm.keys, 0) : sm.keys;
   int carried = 0, side = 0;
   for (int from = v.c0; from < v.c1; from += kKeys) {
     const int n = min(kKeys, v.c1 - from);
     const bool last = from + n == v.c1;
-    constexpr int kStep = kWarps * kRows;   // blocks that a CTA's warps take at once
-    for (int j0 = rank * kStep * kAhead + warp * kRows; j0 < n; j0 += ranks * kStep * kAhead) {
-      int entry[kAhead];
+    for (int j0 = first; j0 < n; j0 += ranks * kStep * kAhead) {
+      if (from > v.c0 || j0 > first) load(from, n, j0);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
         const int j = j0 + i * kStep + lane / kLanes;
-        entry[i] = j < n ? entry_of(a.index, page_log, p.block_log, table, from + j) : -2;
-      }
-      uint4 w[kAhead][2];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (entry[i] >= 0) {
-          const uint4* m = reinterpret_cast<const uint4*>(a.index.means + ((size_t)entry[i] * Hk + h) * D) + lane % kLanes * 2;
-          w[i][0] = __ldg(m);
-          w[i][1] = __ldg(m + 1);
-        }
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
+        if (j - lane / kLanes >= n) break;   // the same for a whole warp
+        const float4* const u4 = reinterpret_cast<const float4*>(sm.u + lane % kLanes * 16);
         float s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const uint32_t x[4] = {w[i][k].x, w[i][k].y, w[i][k].z, w[i][k].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&x[e]));
-            s = fmaf(f.x, mine[8 * k + 2 * e], s);
-            s = fmaf(f.y, mine[8 * k + 2 * e + 1], s);
-          }
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t m0 = k % 2 ? w[i][k / 2].z : w[i][k / 2].x, m1 = k % 2 ? w[i][k / 2].w : w[i][k / 2].y;
+          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&m0));
+          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&m1));
+          const float4 uk = u4[k];
+          s = fmaf(f0.x, uk.x, s);
+          s = fmaf(f0.y, uk.y, s);
+          s = fmaf(f1.x, uk.z, s);
+          s = fmaf(f1.y, uk.w, s);
         }
 #pragma unroll
         for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(kFull, s, o);
-        const int j = j0 + i * kStep + lane / kLanes;
         if (lane % kLanes == 0 && j < n) {
           keys[carried + j] = order_key(entry[i] >= 0 ? fmaxf(s, kBadScore) : kBadScore);
           if (entry[i] < 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
         }
       }
     }
-    if (rank == 0) {
-      if (tid < carried) sm.keys[tid] = sm.best_key[side][tid];
-      if (tid < 3) sm.counts[tid] = 0;
-      if (tid == 0) sm.lowest = 0xffffffffu, sm.highest = 0;
-    }
+    if (rank == 0 && tid < carried) sm.keys[tid] = sm.best_key[side][tid];
     if (ranks > 1) cg::this_cluster().sync();
     else __syncthreads();
 
     if (rank == 0) {
-      // lo and hi: at least `need` keys are >= lo, fewer >= hi.
-      const int total = carried + n, seg = (total + kThreads - 1) / kThreads * 32;   // keys of a warp, neighbours
-      const int at = warp * seg + lane;
-      uint32_t reg[kPer], lowest = 0xffffffffu, highest = 0;
+      // A warp's run of neighbouring keys; what the runs before it keep is known beforehand.
+      const int total = carried + n, seg = (total + kThreads - 1) / kThreads * 32, at = warp * seg;
+      {
+        const int mine = max(0, min(seg, total - at));
+        int before = 0;
+        for (int k = 0; k < warp; ++k) before += min(max(0, min(seg, total - k * seg)), v.need);
+        uint32_t reg[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        reg[i] = 0;
-        if (i * 32 < seg && at + i * 32 < total) {
-          reg[i] = sm.keys[at + i * 32];
-          lowest = min(lowest, reg[i]);
-          highest = max(highest, reg[i]);
-        }
-      }
-      lowest = __reduce_min_sync(kFull, lowest);
-      highest = __reduce_max_sync(kFull, highest);
-      if (lane == 0) {
-        atomicMin(&sm.lowest, lowest);
-        atomicMax(&sm.highest, highest);
+        for (int i = 0; i < kPer; ++i) reg[i] = 32 * i + lane < mine ? sm.keys[at + 32 * i + lane] : 0u;
+        if (mine > 0)
+          warp_cut(reg, mine, v.need, [&](int where, int i) {
+            const int key = at + 32 * i + lane;
+            sm.run_key[before + where] = reg[i];
+            sm.run_blk[before + where] = key < carried ? sm.best[side][key] : from + key - carried;
+          });
       }
       __syncthreads();
-      uint32_t lo = sm.lowest, hi = sm.highest + 1;
-      int at_least = total;   // keys >= lo
-      for (int step = 0; at_least > v.need && hi - lo > 1; ++step) {
-        const uint32_t mid = middle(lo, hi, step);
-        int cnt = 0;
+      if (warp == 0) {
+        int left = 0;
+        for (int k = 0; k < kWarps; ++k) left += min(max(0, min(seg, total - k * seg)), v.need);
+        uint32_t reg[kPer2];
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-          if (i * 32 >= seg) break;
-          cnt += reg[i] >= mid;
-        }
-        cnt = __reduce_add_sync(kFull, cnt);
-        if (lane == 0 && cnt) atomicAdd(&sm.counts[step % 3], cnt);
-        if (tid == 0) sm.counts[(step + 1) % 3] = 0;   // read two steps ago
-        __syncthreads();
-        cnt = sm.counts[step % 3];
-        if (cnt >= v.need) lo = mid, at_least = cnt;
-        else hi = mid;
-      }
-      // Those above lo, and the first of its equals, in order.
-      int gt = 0, eq = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i * 32 >= seg) break;
-        const bool in = at + i * 32 < total;
-        gt += in && reg[i] > lo;
-        eq += in && reg[i] == lo;
-      }
-      gt = __reduce_add_sync(kFull, gt);
-      eq = __reduce_add_sync(kFull, eq);
-      if (lane == 0) sm.above[warp] = gt, sm.equal[warp] = eq;
-      __syncthreads();
-      int all_gt = 0, gt0 = 0, eq0 = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) gt0 += sm.above[w], eq0 += sm.equal[w];
-        all_gt += sm.above[w];
-      }
-      const int eq_max = min(total, v.need) - all_gt;    // equals that are taken
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (i * 32 >= seg) break;
-        const bool in = at + i * 32 < total;
-        const unsigned g = __ballot_sync(kFull, in && reg[i] > lo), e = __ballot_sync(kFull, in && reg[i] == lo);
-        const unsigned below = (1u << lane) - 1;
-        const int my_eq = eq0 + __popc(e & below);
-        if (in && (reg[i] > lo || (reg[i] == lo && my_eq < eq_max))) {
-          const int where = gt0 + __popc(g & below) + min(my_eq, eq_max), key = at + i * 32;
-          const int blk = key < carried ? sm.best[side][key] : from + key - carried;
+        for (int i = 0; i < kPer2; ++i) reg[i] = 32 * i + lane < left ? sm.run_key[32 * i + lane] : 0u;
+        warp_cut(reg, left, v.need, [&](int where, int i) {
+          const int blk = sm.run_blk[32 * i + lane];
           if (last) {
             out[a.sink + where] = blk;
           } else {
             sm.best[side ^ 1][where] = blk;
             sm.best_key[side ^ 1][where] = reg[i];
           }
-        }
-        gt0 += __popc(g);
-        eq0 += __popc(e);
+        });
       }
     }
     carried = min(carried + n, v.need);
@@ -296,19 +330,20 @@ __global__ void __launch_bounds__(kThreads) kv4_select_few_kernel(const __grid_c
   const int Hk = a.index.cache.kv_heads, cap = a.max_pages * a.index.cache.page_tokens;
   const int ranks = (int)cg::this_cluster().num_blocks(), rank = (int)cg::this_cluster().block_rank();
   const int item = blockIdx.x / ranks, h = item % Hk;
-  if (ranks > 1) cg::this_cluster().sync();     // all of them run before one writes to another
+  // All CTAs of a cluster run before one writes to another: they meet while the lengths come.
+  if (ranks > 1) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
   pdl_wait();
+  const RowOwner own = p.rows == 0 ? row_owner(a.cu_q, a.kv_len, a.batch, a.total_q, a.max_q, cap, item / Hk)
+                                   : request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, cap, item / Hk / p.rows);
+  if (ranks > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  if (own.bad && threadIdx.x == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+  if (own.b < 0) return;
   if (p.rows == 0) {
-    const int t = item / Hk;
-    const RowOwner own = row_owner(a.cu_q, a.kv_len, a.batch, a.total_q, a.max_q, cap, t);
-    if (own.bad && threadIdx.x == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-    if (own.b >= 0) select_row<D>(p, own, t, h, sm, rank, ranks);
+    select_row<D>(p, own, item / Hk, h, sm, rank, ranks);
     return;
   }
   // A request's rows, dealt out to `rows` CTAs.
-  const RowOwner own = request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, cap, item / Hk / p.rows);
-  if (own.bad && threadIdx.x == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-  if (own.b < 0 || own.n > kFewRows) return;
+  if (own.n > kFewRows) return;
   for (int i = item / Hk % p.rows; i < own.n; i += p.rows) select_row<D>(p, own, own.c0 + i, h, sm, rank, ranks);
 }
 
@@ -347,48 +382,52 @@ struct List {
   float bound;         // at least `need` entries reach it: what comes later and is not above cannot win
   __device__ __forceinline__ uint32_t key(int i) const { return sm.key[i][row]; }
 
-  // Cuts the list to at least `need` and at most `most` (>= need) entries, if it has more. Whole warps.
+  // Cuts the list to at least `need` and at most `most` (>= need) entries, if it has more. Whole warps, in step up to
+  // the longest list: what a thread has past its own is read and not counted.
   __device__ __forceinline__ void cut(int need, int most) {
+    const bool wanted = cnt > most && need > 0;
+    const int longest = __reduce_max_sync(kFull, wanted ? cnt : 0);
     uint32_t lo = 0xffffffffu, hi = 0;
-    for (int i = 0; i < cnt; ++i) {
+#pragma unroll 8
+    for (int i = 0; i < longest; ++i) {
       const uint32_t k = key(i);
-      lo = min(lo, k);
-      hi = max(hi, k);
+      if (i < cnt) {
+        lo = min(lo, k);
+        hi = max(hi, k);
+      }
     }
     hi += 1;
     int at_least = cnt, above = 0;     // entries >= lo, >= hi
-    const bool wanted = cnt > most && need > 0;
     for (int step = 0;; ++step) {
       const bool go = wanted && at_least > most && hi - lo > 1;
       if (!__any_sync(kFull, go)) break;
       const uint32_t mid = go ? middle(lo, hi, step) : 0xffffffffu;
       int c = 0;
 #pragma unroll 8
-      for (int i = 0; i < cnt; ++i) c += key(i) >= mid;
+      for (int i = 0; i < longest; ++i) c += key(i) >= mid && i < cnt;
       if (go) {
         if (c >= need) lo = mid, at_least = c;
         else hi = mid, above = c;
       }
     }
-    if (wanted) {
-      int equals = at_least > most ? need - above : cnt;   // too many of one key: the first of them
-      int w = 0;
-      for (int i = 0; i < cnt; ++i) {
-        const uint32_t k = key(i);
-        if (k > lo || (k == lo && equals-- > 0)) {
-          sm.key[w][row] = k;
-          sm.blk[w][row] = sm.blk[i][row];
-          ++w;
-        }
+    int equals = at_least > most ? need - above : cnt;   // too many of one key: the first of them
+    int w = wanted ? 0 : cnt;
+#pragma unroll 4
+    for (int i = 0; i < longest; ++i) {
+      const uint32_t k = key(i);
+      if (wanted && i < cnt && (k > lo || (k == lo && equals-- > 0))) {
+        sm.key[w][row] = k;
+        sm.blk[w][row] = sm.blk[i][row];
+        ++w;
       }
-      cnt = w;
-      bound = key_value(lo);
     }
+    cnt = w;
+    if (wanted) bound = key_value(lo);
   }
 };
 
 template <int D>
-__global__ void __launch_bounds__(kManyThreads) kv4_select_many_kernel(const __grid_constant__ SelectArgs p) {
+__global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const __grid_constant__ SelectArgs p) {
   using Sm = ManySmem<D>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   Sm& sm = *reinterpret_cast<Sm*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -456,20 +495,27 @@ __global__ void __launch_bounds__(kManyThreads) kv4_select_many_kernel(const __g
     {
       const uint16_t* const q = a.q + (size_t)min(t, a.total_q - 1) * a.q_stride + (size_t)h * heads * D;
       const bool real = v.need > 0;
-      uint32_t top = 0;
+      uint32_t pair = 0;
       if (real)
         for (int i = 0; i < heads * D / 8; ++i) {
           const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + i);
-          const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j) top = max(top, max(finite_bits(w[j]), finite_bits(w[j] >> 16)));
+          pair = max_u16x2(max_u16x2(pair, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
+          pair = max_u16x2(max_u16x2(pair, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
         }
+      uint32_t top = max(pair & 0xffffu, pair >> 16);
+      const bool finite = top < 0x7f80u;
+      if (!finite) {   // again without what counts as 0
+        top = 0;
+        for (int i = 0; i < heads * D; ++i) top = max(top, finite_bits(q[i]));
+      }
       const float scale = grid_scale(top);
+      const uint32_t scale2 = __float_as_uint(scale) >> 16 | (__float_as_uint(scale) & 0xffff0000u);
 #pragma unroll 1
       for (int d0 = 0; d0 < D; d0 += 32) {
-        float s[32];
+        // x scale + 192 in bf16 is 192 and the rounded product (at most 64), whose bits are 0x4300 + 64 + that
+        uint32_t r[16];
 #pragma unroll
-        for (int i = 0; i < 32; ++i) s[i] = 0.0f;
+        for (int i = 0; i < 16; ++i) r[i] = 0;
         if (real)
           for (int g = 0; g < heads; ++g)
 #pragma unroll
@@ -478,14 +524,15 @@ __global__ void __launch_bounds__(kManyThreads) kv4_select_many_kernel(const __g
               const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
-                s[8 * i + 2 * j] += on_grid(w[j] & 0xffffu, scale);
-                s[8 * i + 2 * j + 1] += on_grid(w[j] >> 16, scale);
+                uint32_t y = w[j];
+                if (!finite) y = (finite_bits(y) ? y & 0xffffu : 0u) | (finite_bits(y >> 16) ? y & 0xffff0000u : 0u);
+                r[4 * i + j] += fma_bf16x2(y, scale2, 0x43404340u) - 0x43004300u;
               }
             }
-        uint32_t r[16];
+        const float zero = real ? 64.0f * heads : 0.0f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const __half2 x = __floats2half2_rn(s[2 * i], s[2 * i + 1]);
+          const __half2 x = __floats2half2_rn((float)(r[i] & 0xffffu) - zero, (float)(r[i] >> 16) - zero);
           r[i] = *reinterpret_cast<const uint32_t*>(&x);
         }
         tmem_st16(tmem + lanes + 128 + d0 / 2, r);
@@ -524,7 +571,8 @@ __global__ void __launch_bounds__(kManyThreads) kv4_select_many_kernel(const __g
               ++list.cnt;
             }
           }
-          if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, list.cnt > kKeep ? min(kKeep, v.need + 7) : kList);
+          // One list too long: every list is cut that is much longer than it has to be.
+          if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, min(kKeep, v.need + 7));
         }
       }
     }
@@ -619,11 +667,11 @@ __global__ void __launch_bounds__(kManyThreads) kv4_select_many_kernel(const __g
 
 template <int D>
 cudaError_t launch_few(const SelectArgs& p, long long items, cudaStream_t s) {
-  // CTAs for a query: as many as leave each a round of its warps' blocks at the longest, and the GPU not twice full.
+  // CTAs for a query: as many as fit the GPU at once and have a round of blocks each where the table is full.
   const long long most = (long long)p.a.max_pages * p.a.index.cache.page_tokens >> p.block_log;
   const int step = kWarps * (512 / D) * kAhead;
   int ranks = 1;
-  while (ranks < 8 && items * ranks * 2 <= 2ll * sm_count() && most > (long long)step * ranks) ranks *= 2;
+  while (ranks < 8 && items * ranks * 2 <= sm_count() && most > (long long)step * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * ranks));
   cfg.blockDim = dim3(kThreads);
