@@ -18,6 +18,7 @@
 #include <cooperative_groups.h>
 
 #include <cfloat>
+#include <type_traits>
 
 #include "kernels.cuh"
 #include "kv4.cuh"
@@ -49,6 +50,7 @@ __device__ __forceinline__ uint32_t middle(uint32_t lo, uint32_t hi, int step) {
 
 // What a block whose page is not in the pool scores (one whose mean is NaN too): below every sum.
 constexpr float kBadScore = -FLT_MAX;
+__device__ __forceinline__ float finite_score(float s) { return fminf(fmaxf(s, kBadScore), FLT_MAX); }
 
 struct SelectArgs {
   moe_kv4_select_args a;
@@ -105,74 +107,161 @@ __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t 
 }
 
 // ---------------------------------------------------------- few queries
-// D / 16 lanes score a block, kAhead blocks at a time (the trips to memory for
-// the table and the means are what takes long); the CTAs of a cluster send
-// their keys to the first. There a warp cuts each run of keys to its best, and
-// one warp cuts what is left of all runs: halving within a warp needs no
-// barriers, with them a step took 860 cycles.
-constexpr int kThreads = 512, kWarps = kThreads / 32, kKeys = 4096, kAhead = 4;
-constexpr int kPer = (kKeys + kSparseTop + kThreads - 1) / kThreads;      // keys a lane of the first cut
-constexpr int kPer2 = kWarps * kSparseTop / 32;                           // and of the second
+// A warp scores 16 blocks with one chain of matrix products, the means coming
+// straight from memory as A fragments and u being the only column of B; the
+// CTAs of a cluster send their scores to the first. There a histogram of the
+// scores' range finds how far down the best go, its few candidates are ranked
+// by counting who is above them. All of it is short code: what is run once
+// waits for its instructions as much as for its data.
+constexpr int kThreads = 512, kWarps = kThreads / 32, kScores = 4096, kAhead = 1, kBins = 256, kCandidates = 256;
 
 struct FewSmem {
-  uint32_t keys[kPer * kThreads];
-  alignas(16) float u[128];
-  int best[2][kSparseTop];               // blocks that earlier chunks left
-  uint32_t best_key[2][kSparseTop];
-  uint32_t run_key[kWarps * kSparseTop];
-  int run_blk[kWarps * kSparseTop];
-  uint32_t group_top;
+  alignas(16) float score[kScores + kSparseTop];
+  alignas(16) __half u[128];
+  alignas(16) float cand[kCandidates];
+  int cand_blk[kCandidates];
+  int hist[kBins];
+  int best[kSparseTop];                  // blocks that earlier chunks left, and their scores
+  float best_score[kSparseTop];
+  int count[kWarps + 1];                 // of the warps
+  int bin, above;                        // the histogram's answer
+  unsigned lowest, highest, group_top;
 };
 
-// The `need` largest of `total` keys (reg[i]: key 32 i + lane, 0 past the end), the first of equal ones, to put(where,
-// i) in order; all where there are no more. By a whole warp.
-template <int N, class Put>
-__device__ __forceinline__ void warp_cut(const uint32_t (&reg)[N], int total, int need, Put put) {
-  const int lane = threadIdx.x & 31, groups = (total + 31) / 32;
-  uint32_t lo = 0xffffffffu, hi = 0;
+// The `need` largest of sm.score[0 .. total) to put(where, i) in order, the
+// first of equal ones; all where there are no more. By a whole CTA.
+template <class BlockOf, class Put>
+__device__ __forceinline__ void best_scores(FewSmem& sm, int total, int need, BlockOf block_of, Put put) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // What counts: scores in [lo, hi], `above` more lie over hi and are in.
+  float lo = -INFINITY, hi = INFINITY, from = 0.0f, scale = 0.0f;
+  int above = 0, bin = 0;
+  if (total > need) {
+#pragma unroll 1
+    while (true) {
+      // the range of what counts: of the whole, then of one bin of it
+      unsigned low = 0xffffffffu, high = 0;
+      for (int i = tid; i < total; i += kThreads) {
+        const float x = sm.score[i];
+        if (x >= lo && x <= hi && (scale == 0.0f || min((int)((0.5f * x - from) * scale), kBins - 1) == bin)) {
+          low = min(low, order_key(x));
+          high = max(high, order_key(x));
+        }
+      }
+      low = __reduce_min_sync(kFull, low);
+      high = __reduce_max_sync(kFull, high);
+      if (lane == 0) {
+        atomicMin(&sm.lowest, low);
+        atomicMax(&sm.highest, high);
+      }
+      if (tid < kBins) sm.hist[tid] = 0;
+      __syncthreads();
+      lo = key_value(sm.lowest);
+      hi = key_value(sm.highest);
+      if (lo == hi) break;   // all equal: the first of them
+      from = 0.5f * lo;
+      scale = (kBins - 1) / (0.5f * hi - from);
+      for (int i = tid; i < total; i += kThreads) {
+        const float x = sm.score[i];
+        if (x >= lo && x <= hi) atomicAdd(&sm.hist[min((int)((0.5f * x - from) * scale), kBins - 1)], 1);
+      }
+      __syncthreads();
+      if (tid == 0) sm.lowest = 0xffffffffu, sm.highest = 0;
+      if (warp == 0) {
+        // the highest bin with at least `need` scores in it and over it; a lane has eight bins, from the top
+        int mine[kBins / 32], sum = 0;
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (32 * i + lane < total) {
-      lo = min(lo, reg[i]);
-      hi = max(hi, reg[i]);
-    }
-  lo = __reduce_min_sync(kFull, lo);
-  hi = __reduce_max_sync(kFull, hi) + 1;
-  int at_least = total, above = 0;   // keys >= lo, >= hi
-  for (int step = 0; at_least > need && hi - lo > 1; ++step) {
-    // three keys in between at once
-    const uint32_t m1 = middle(lo, hi, step), m0 = m1 - lo > 1 ? middle(lo, m1, step) : lo,
-                   m2 = hi - m1 > 1 ? middle(m1, hi, step) : hi;
-    int c0 = 0, c1 = 0, c2 = 0;
+        for (int i = 0; i < kBins / 32; ++i) {
+          mine[i] = sm.hist[kBins - 1 - lane * (kBins / 32) - i];
+          sum += mine[i];
+        }
+        int incl = sum;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      if (i >= groups) break;
-      c0 += reg[i] >= m0;
-      c1 += reg[i] >= m1;
-      c2 += reg[i] >= m2;
+        for (int o = 1; o < 32; o <<= 1) {
+          const int v = __shfl_up_sync(kFull, incl, o);
+          if (lane >= o) incl += v;
+        }
+        int over = above + incl - sum;
+        const unsigned reached = __ballot_sync(kFull, above + incl >= need);
+        if (lane == __ffs(reached) - 1) {
+          int i = 0;
+#pragma unroll
+          for (int k = 0; k < kBins / 32 - 1; ++k)
+            if (i == k && over + mine[k] < need) over += mine[k], ++i;
+          sm.bin = kBins - 1 - lane * (kBins / 32) - i;
+          sm.above = over;
+        }
+      }
+      __syncthreads();
+      bin = sm.bin;
+      above = sm.above;
+      if (above + sm.hist[bin] <= kCandidates) break;
+      __syncthreads();
     }
-    // at most 32 * 32 keys: two counts a word
-    const unsigned two = __reduce_add_sync(kFull, (unsigned)(c0 | c1 << 16));
-    c2 = m2 == hi ? above : __reduce_add_sync(kFull, c2);
-    c0 = m0 == lo ? at_least : (int)(two & 0xffffu);
-    c1 = (int)(two >> 16);
-    if (c2 >= need && m2 != hi) lo = m2, at_least = c2;
-    else if (c1 >= need) lo = m1, at_least = c1, hi = m2, above = c2;
-    else if (c0 >= need) lo = m0, at_least = c0, hi = m1, above = c1;
-    else hi = m0, above = c0;
   }
-  int equals = at_least > need ? need - above : total;   // too many of one key: the first of them
-  int w = 0;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    if (i >= groups) break;
-    const bool in = 32 * i + lane < total;
-    const unsigned below = (1u << lane) - 1, e = __ballot_sync(kFull, in && reg[i] == lo);
-    const bool take = in && (reg[i] > lo || (reg[i] == lo && __popc(e & below) < equals));
+  // The candidates in order, a warp a run of neighbours.
+  auto level = [&](float x) {   // 2: in, 1: perhaps
+    if (total <= need || x > hi) return 2;
+    if (x < lo) return 0;
+    if (lo == hi) return 1;
+    const int b = min((int)((0.5f * x - from) * scale), kBins - 1);
+    return b > bin ? 2 : b == bin ? 1 : 0;
+  };
+  const bool ties = total > need && lo == hi;
+  const int seg = (total + kThreads - 1) / kThreads * 32, at = warp * seg, end = min(total, at + seg);
+  int mine = 0, equal = 0;
+  for (int i0 = at; i0 < end; i0 += 32) {
+    const int l = i0 + lane < end ? level(sm.score[i0 + lane]) : 0;
+    mine += __popc(__ballot_sync(kFull, l > (ties ? 1 : 0)));
+    equal += __popc(__ballot_sync(kFull, ties && l == 1));
+  }
+  if (lane == 0) sm.count[warp] = mine | equal << 16;   // at most 4159 of either
+  __syncthreads();
+  int w = 0, e0 = 0, n = 0;
+  for (int k = 0; k < kWarps; ++k) {
+    const int c = sm.count[k];
+    if (k < warp) w += c & 0xffff, e0 += c >> 16;
+    n += c & 0xffff;
+  }
+  // Of many equal ones only the first that are needed are taken, so that no more than kCandidates are left.
+  const int quota = need - above;
+  if (ties) {
+    w += min(e0, quota);
+    n += quota;
+  }
+  const unsigned before = (1u << lane) - 1;
+  for (int i0 = at; i0 < end; i0 += 32) {
+    const float x = i0 + lane < end ? sm.score[i0 + lane] : -INFINITY;
+    const int l = i0 + lane < end ? level(x) : 0;
+    const unsigned eq = __ballot_sync(kFull, ties && l == 1);
+    const bool take = ties ? l == 2 || (l == 1 && e0 + __popc(eq & before) < quota) : l > 0;
     const unsigned t = __ballot_sync(kFull, take);
-    if (take) put(w + __popc(t & below), i);
+    if (take) {
+      sm.cand[w + __popc(t & before)] = x;
+      sm.cand_blk[w + __popc(t & before)] = block_of(i0 + lane);
+    }
     w += __popc(t);
-    equals -= __popc(e);
+    e0 += __popc(eq);
+  }
+  __syncthreads();
+  // Who is among the best, and how many of those come first.
+  bool in = false;
+  if (tid < kCandidates) {
+    const float x = tid < n ? sm.cand[tid] : 0.0f;
+    int over = 0;
+    for (int j = 0; j < n; ++j) {
+      const float y = sm.cand[j];
+      over += y > x || (y == x && j < tid);
+    }
+    in = tid < n && over < need;
+    const unsigned t = __ballot_sync(kFull, in);
+    if (lane == 0) sm.count[warp] = __popc(t);
+    w = __popc(t & before);
+  }
+  __syncthreads();
+  if (in) {
+    for (int k = 0; k < warp; ++k) w += sm.count[k];
+    put(w, tid);
   }
 }
 
@@ -180,11 +269,11 @@ __device__ __forceinline__ void warp_cut(const uint32_t (&reg)[N], int total, in
 template <int D>
 __device__ __forceinline__ void select_row(const SelectArgs& p, const RowOwner& own, int t, int h, FewSmem& sm, int rank,
                                            int ranks) {
-  constexpr int kLanes = D / 16, kRows = 32 / kLanes;
-  constexpr int kStep = kWarps * kRows;   // blocks that a CTA's warps take at once
+  constexpr int kStep = kWarps * 16 * kAhead;   // blocks that a CTA's warps take at once
+  constexpr int kLoads = D / 32;                // 16-byte pieces of a lane's part of a row
   const moe_kv4_select_args& a = p.a;
   const moe_kv4_cache& c = a.index.cache;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g8 = lane >> 2, t4 = lane & 3;
   const int Hk = c.kv_heads, heads = a.q_heads / Hk, page_log = __ffs(c.page_tokens) - 1;
   const Visible v = visible(a, p.block_log, own.kv - own.n + t - own.c0);
   int32_t* const out = a.blocks + ((size_t)t * Hk + h) * a.top;
@@ -199,39 +288,42 @@ __device__ __forceinline__ void select_row(const SelectArgs& p, const RowOwner& 
   if (v.need == 0) return;
 
   const int32_t* const table = a.block_table + (size_t)own.b * a.max_pages;
-  int entry[kAhead];
-  uint4 w[kAhead][2];
-  // The means of this thread's blocks of a round, asked for before what multiplies them is there.
+  int entry[kAhead][2];
+  uint4 w[kAhead][2][kLoads];
+  // The means of the warp's blocks of a round, asked for before what multiplies them is there: rows g8 and g8 + 8 of each
+  // 16 blocks, elements D / 4 t4 and on.
   auto load = [&](int from, int n, int j0) {
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      const int j = j0 + i * kStep + lane / kLanes;
-      entry[i] = j < n ? entry_of(a.index, page_log, p.block_log, table, from + j) : -2;
-    }
+    for (int i = 0; i < kAhead; ++i)
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) {
-      w[i][0] = w[i][1] = make_uint4(0u, 0u, 0u, 0u);
-      if (entry[i] >= 0) {
-        const uint4* m = reinterpret_cast<const uint4*>(a.index.means + ((size_t)entry[i] * Hk + h) * D) + lane % kLanes * 2;
-        w[i][0] = __ldg(m);
-        w[i][1] = __ldg(m + 1);
+      for (int r = 0; r < 2; ++r) {
+        const int j = j0 + i * kWarps * 16 + r * 8 + g8;
+        entry[i][r] = j < n ? entry_of(a.index, page_log, p.block_log, table, from + j) : -2;
       }
-    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const uint4* m = reinterpret_cast<const uint4*>(a.index.means + ((size_t)max(entry[i][r], 0) * Hk + h) * D) + t4 * kLoads;
+#pragma unroll
+        for (int k = 0; k < kLoads; ++k) w[i][r][k] = entry[i][r] >= 0 ? __ldg(m + k) : make_uint4(0u, 0u, 0u, 0u);
+      }
   };
-  const int first = rank * kStep * kAhead + warp * kRows;
-  if (tid == 0) sm.group_top = 0;
-  uint32_t x[kSparseGroup];   // element tid of the group's queries
+  const int first = rank * kStep + warp * 16;
+  uint32_t x[kSparseGroup / 2];   // element tid of the group's queries, two a word
   if (tid < D) {
     const uint16_t* const q = a.q + (size_t)t * a.q_stride + (size_t)h * heads * D + tid;
 #pragma unroll
-    for (int i = 0; i < kSparseGroup; ++i) x[i] = i < heads ? q[i * D] : 0u;
+    for (int i = 0; i < kSparseGroup / 2; ++i)
+      x[i] = (2 * i < heads ? (uint32_t)q[2 * i * D] : 0u) | (2 * i + 1 < heads ? (uint32_t)q[(2 * i + 1) * D] << 16 : 0u);
   }
-  load(v.c0, min(kKeys, v.c1 - v.c0), first);
+  load(v.c0, min(kScores, v.c1 - v.c0), first);
+  if (tid == 0) sm.group_top = 0, sm.lowest = 0xffffffffu, sm.highest = 0;
   __syncthreads();
   if (tid < D) {
     uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < kSparseGroup; ++i) top = max(top, finite_bits(x[i]));
+    for (int i = 0; i < kSparseGroup / 2; ++i) top = max(top, max(finite_bits(x[i]), finite_bits(x[i] >> 16)));
     top = __reduce_max_sync(kFull, top);
     if (lane == 0) atomicMax(&sm.group_top, top);
   }
@@ -240,91 +332,65 @@ __device__ __forceinline__ void select_row(const SelectArgs& p, const RowOwner& 
     const float scale = grid_scale(sm.group_top);
     float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kSparseGroup; ++i) s += on_grid(x[i], scale);
-    sm.u[tid] = s;
+    for (int i = 0; i < kSparseGroup / 2; ++i) s += on_grid(x[i] & 0xffffu, scale) + on_grid(x[i] >> 16, scale);
+    sm.u[tid] = __float2half_rn(s);
   }
   __syncthreads();
-
-  uint32_t* const keys = ranks > 1 ? cg::this_cluster().map_shared_rank(sm.keys, 0) : sm.keys;
-  int carried = 0, side = 0;
-  for (int from = v.c0; from < v.c1; from += kKeys) {
-    const int n = min(kKeys, v.c1 - from);
+  int carried = 0;
+  for (int from = v.c0; from < v.c1; from += kScores) {
+    const int n = min(kScores, v.c1 - from);
     const bool last = from + n == v.c1;
-    for (int j0 = first; j0 < n; j0 += ranks * kStep * kAhead) {
+#pragma unroll 1
+    for (int j0 = first; j0 < n; j0 += ranks * kStep) {
       if (from > v.c0 || j0 > first) load(from, n, j0);
 #pragma unroll
       for (int i = 0; i < kAhead; ++i) {
-        const int j = j0 + i * kStep + lane / kLanes;
-        if (j - lane / kLanes >= n) break;   // the same for a whole warp
-        const float4* const u4 = reinterpret_cast<const float4*>(sm.u + lane % kLanes * 16);
-        float s = 0.0f;
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const uint32_t m0 = k % 2 ? w[i][k / 2].z : w[i][k / 2].x, m1 = k % 2 ? w[i][k / 2].w : w[i][k / 2].y;
-          const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&m0));
-          const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&m1));
-          const float4 uk = u4[k];
-          s = fmaf(f0.x, uk.x, s);
-          s = fmaf(f0.y, uk.y, s);
-          s = fmaf(f1.x, uk.z, s);
-          s = fmaf(f1.y, uk.w, s);
+        for (int k = 0; k < kLoads; ++k) {
+          const uint4 &x0 = w[i][0][k], &x1 = w[i][1][k];
+          // u as the first column of B, the others 0; elements in the order the A fragments have them
+          uint4 u = *reinterpret_cast<const uint4*>(sm.u + t4 * (D / 4) + k * 8);
+          if (g8 > 0) u = make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t lo[4] = {x0.x, x1.x, x0.y, x1.y}, hi[4] = {x0.z, x1.z, x0.w, x1.w};
+          mma_f16_16816(s, lo, u.x, u.y);
+          mma_f16_16816(s, hi, u.z, u.w);
         }
+        if (t4 == 0)
 #pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) s += __shfl_xor_sync(kFull, s, o);
-        if (lane % kLanes == 0 && j < n) {
-          keys[carried + j] = order_key(entry[i] >= 0 ? fmaxf(s, kBadScore) : kBadScore);
-          if (entry[i] < 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-        }
-      }
-    }
-    if (rank == 0 && tid < carried) sm.keys[tid] = sm.best_key[side][tid];
-    if (ranks > 1) cg::this_cluster().sync();
-    else __syncthreads();
-
-    if (rank == 0) {
-      // A warp's run of neighbouring keys; what the runs before it keep is known beforehand.
-      const int total = carried + n, seg = (total + kThreads - 1) / kThreads * 32, at = warp * seg;
-      {
-        const int mine = max(0, min(seg, total - at));
-        int before = 0;
-        for (int k = 0; k < warp; ++k) before += min(max(0, min(seg, total - k * seg)), v.need);
-        uint32_t reg[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) reg[i] = 32 * i + lane < mine ? sm.keys[at + 32 * i + lane] : 0u;
-        if (mine > 0)
-          warp_cut(reg, mine, v.need, [&](int where, int i) {
-            const int key = at + 32 * i + lane;
-            sm.run_key[before + where] = reg[i];
-            sm.run_blk[before + where] = key < carried ? sm.best[side][key] : from + key - carried;
-          });
-      }
-      __syncthreads();
-      if (warp == 0) {
-        int left = 0;
-        for (int k = 0; k < kWarps; ++k) left += min(max(0, min(seg, total - k * seg)), v.need);
-        uint32_t reg[kPer2];
-#pragma unroll
-        for (int i = 0; i < kPer2; ++i) reg[i] = 32 * i + lane < left ? sm.run_key[32 * i + lane] : 0u;
-        warp_cut(reg, left, v.need, [&](int where, int i) {
-          const int blk = sm.run_blk[32 * i + lane];
-          if (last) {
-            out[a.sink + where] = blk;
-          } else {
-            sm.best[side ^ 1][where] = blk;
-            sm.best_key[side ^ 1][where] = reg[i];
+          for (int r = 0; r < 2; ++r) {
+            const int j = j0 + i * kWarps * 16 + r * 8 + g8;
+            if (j < n) sm.score[carried + j] = entry[i][r] >= 0 ? finite_score(s[2 * r]) : kBadScore;
+            if (entry[i][r] == -1 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
           }
-        });
       }
     }
+    if (rank == 0 && tid < carried) sm.score[tid] = sm.best_score[tid];
+    __syncthreads();
+    if (ranks > 1) {
+      if (rank > 0) {   // whole lines to the first CTA
+        float* const to = cg::this_cluster().map_shared_rank(sm.score, 0) + carried;
+        for (int j0 = rank * kStep; j0 < n; j0 += ranks * kStep)
+          for (int j = j0 + tid; j < min(n, j0 + kStep); j += kThreads) to[j] = sm.score[carried + j];
+      }
+      cg::this_cluster().sync();
+    }
+    if (rank == 0)
+      best_scores(sm, carried + n, v.need,
+                  [&](int i) { return i < carried ? sm.best[i] : from + i - carried; },
+                  [&](int where, int i) {
+                    if (last) out[a.sink + where] = sm.cand_blk[i];
+                    else sm.best[where] = sm.cand_blk[i], sm.best_score[where] = sm.cand[i];
+                  });
     carried = min(carried + n, v.need);
-    side ^= 1;
+    if (tid == 0) sm.lowest = 0xffffffffu, sm.highest = 0;
     if (ranks > 1) cg::this_cluster().sync();   // the first has read what the others wrote
     else __syncthreads();
   }
 }
 
 template <int D>
-__global__ void __launch_bounds__(kThreads) kv4_select_few_kernel(const __grid_constant__ SelectArgs p) {
+__global__ void __launch_bounds__(kThreads, 2) kv4_select_few_kernel(const __grid_constant__ SelectArgs p) {
   __shared__ FewSmem sm;
   const moe_kv4_select_args& a = p.a;
   const int Hk = a.index.cache.kv_heads, cap = a.max_pages * a.index.cache.page_tokens;
@@ -348,13 +414,16 @@ __global__ void __launch_bounds__(kThreads) kv4_select_few_kernel(const __grid_c
 }
 
 // --------------------------------------------------------- many queries
-// Warps 0 to 3: a thread a query. It puts u into tensor memory (the A operand),
-// then reads its row of each score tile and appends what lies above its bound
-// to its list; a list of more than kKeep is cut at a key that leaves at least
-// `need`. Warps 4 to 7 bring the means of 64 blocks a stage (cp.async into
-// 128-byte-swizzled rows); one thread of warp 8 issues the products.
-constexpr int kTile = 128, kCols = 64, kStages = 2, kGroup = 32, kKeep = 64, kList = kKeep + kGroup;
+// Warps 0 to 3: a thread a query. Once u is in tensor memory (the A operand;
+// warps 0 to 7 work it out, a row a warp, and hand it over in the lists'
+// memory) the thread reads its row of each score tile and appends what lies
+// above its bound to its list; a list of more than kKeep is cut at a value that
+// leaves at least `need`. Warps 4 to 7 bring the means of 64 blocks a stage
+// (cp.async into 128-byte-swizzled rows); one thread of warp 8 issues the
+// products.
+constexpr int kTile = 128, kCols = 64, kStages = 2, kGroup = 32, kKeep = 64, kList = kKeep + kGroup;   // a list's places: one more
 constexpr int kManyThreads = 288, kTmem = 256;
+static_assert(kList % 16 == 0, "lists are read 16 entries at a time");
 constexpr int kMostBlocks = 65536;   // list entries name blocks in 16 bits
 constexpr long long kWaitLimit = 2ll * 1000 * 1000 * 1000;   // cycles (about 1 s)
 
@@ -365,8 +434,8 @@ struct Segment {
 template <int D>
 struct ManySmem {
   alignas(1024) uint8_t ring[kStages][kCols * D * 2];
-  uint32_t key[kList][kTile];
-  uint16_t blk[kList][kTile];
+  float score[kList + 1][kTile];
+  uint16_t blk[kList + 1][kTile];
   Segment seg[kTile];
   int owner[kTile + 2];          // of rows -1 .. kTile
   int segments, abort;
@@ -374,55 +443,73 @@ struct ManySmem {
   uint64_t full[kStages], empty[kStages], scored[2], read[2], rows_in, drained;
 };
 
-// A thread's list: cnt entries in the order of their blocks.
+// A thread's list: cnt entries in the order of their blocks; what is past them
+// is not above the bound.
 template <class Sm>
 struct List {
   Sm& sm;
   int row, cnt;
-  float bound;         // at least `need` entries reach it: what comes later and is not above cannot win
-  __device__ __forceinline__ uint32_t key(int i) const { return sm.key[i][row]; }
+  float bound;     // at least `need` entries reach it: what comes later and is not above cannot win
+  float top;       // no entry is above
 
-  // Cuts the list to at least `need` and at most `most` (>= need) entries, if it has more. Whole warps, in step up to
-  // the longest list: what a thread has past its own is read and not counted.
+  // Cuts a list of more than `most` entries to at least `need` and at most `most` (>= need). Whole warps, in step up to
+  // the longest list.
   __device__ __forceinline__ void cut(int need, int most) {
     const bool wanted = cnt > most && need > 0;
-    const int longest = __reduce_max_sync(kFull, wanted ? cnt : 0);
-    uint32_t lo = 0xffffffffu, hi = 0;
-#pragma unroll 8
-    for (int i = 0; i < longest; ++i) {
-      const uint32_t k = key(i);
-      if (i < cnt) {
-        lo = min(lo, k);
-        hi = max(hi, k);
-      }
-    }
-    hi += 1;
+    const int longest = (__reduce_max_sync(kFull, wanted ? cnt : 0) + 15) & ~15;
+    uint32_t lo = order_key(fmaxf(bound, kBadScore)), hi = order_key(top) + 1;
     int at_least = cnt, above = 0;     // entries >= lo, >= hi
+#pragma unroll 1
     for (int step = 0;; ++step) {
       const bool go = wanted && at_least > most && hi - lo > 1;
       if (!__any_sync(kFull, go)) break;
-      const uint32_t mid = go ? middle(lo, hi, step) : 0xffffffffu;
-      int c = 0;
-#pragma unroll 8
-      for (int i = 0; i < longest; ++i) c += key(i) >= mid && i < cnt;
+      const uint32_t key = go ? middle(lo, hi, step) : hi;
+      const float mid = key_value(key);
+      int c[2] = {0, 0};
+#pragma unroll 1
+      for (int i = 0; i < longest; i += 16) {
+        float x[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) x[j] = sm.score[i + j][row];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) c[j & 1] += x[j] >= mid;
+      }
       if (go) {
-        if (c >= need) lo = mid, at_least = c;
-        else hi = mid, above = c;
+        if (c[0] + c[1] >= need) lo = key, at_least = c[0] + c[1];
+        else hi = key, above = c[0] + c[1];
       }
     }
-    int equals = at_least > most ? need - above : cnt;   // too many of one key: the first of them
-    int w = wanted ? 0 : cnt;
-#pragma unroll 4
-    for (int i = 0; i < longest; ++i) {
-      const uint32_t k = key(i);
-      if (wanted && i < cnt && (k > lo || (k == lo && equals-- > 0))) {
-        sm.key[w][row] = k;
-        sm.blk[w][row] = sm.blk[i][row];
-        ++w;
+    const float from = key_value(lo);
+    int equals = at_least > most ? need - above : kList;   // too many of one score: the first of them
+    int w = 0;
+#pragma unroll 1
+    for (int i = 0; i < longest; i += 16) {   // read ahead of what is written: w <= i
+      float x[16];
+      uint16_t blk[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        x[j] = sm.score[i + j][row];
+        blk[j] = sm.blk[i + j][row];
+      }
+      if (wanted) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) sm.score[i + j][row] = -INFINITY;   // what is moved down is written again
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const bool equal = x[j] == from && i + j < cnt;
+          if (x[j] > from || (equal && equals > 0)) {
+            sm.score[w][row] = x[j];
+            sm.blk[w][row] = blk[j];
+            ++w;
+          }
+          equals -= equal;
+        }
       }
     }
-    cnt = w;
-    if (wanted) bound = key_value(lo);
+    if (wanted) {
+      cnt = w;
+      bound = from;
+    }
   }
 };
 
@@ -489,59 +576,101 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
   volatile int* const abort = &sm.abort;
   const int segments = sm.segments;
 
+  // ----------------------------------------------- the rows of u, a row a warp
+  constexpr int kRowLanes = D / 8, kPasses = 32 / kRowLanes;   // lanes of a head's row, heads at once
+  constexpr int kPad = D * 2 + 16;                              // bytes of a row of u on its way to tensor memory
+  static_assert(kPad * kTile <= (int)sizeof(sm.score), "u passes through the lists");
+  uint8_t* const rows_of_u = reinterpret_cast<uint8_t*>(sm.score);
+  if (segments > 0 && warp < 8) {
+    // kHeads of a lane at most, kRowsAtOnce rows asked for together
+    auto rows = [&](auto heads_of_lane, auto rows_at_once) {
+      constexpr int kHeads = decltype(heads_of_lane)::value, kAtOnce = decltype(rows_at_once)::value;
+      const int part = lane % kRowLanes, g0 = lane / kRowLanes;
+#pragma unroll 1
+      for (int r0 = warp * (kTile / 8); r0 < (warp + 1) * (kTile / 8); r0 += kAtOnce) {
+        uint4 x[kAtOnce][kHeads];
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b)
+#pragma unroll
+          for (int i = 0; i < kHeads; ++i) {
+            const int g = g0 + i * kPasses;
+            x[b][i] = g < heads && sm.owner[r0 + b + 1] >= 0
+                          ? __ldg(reinterpret_cast<const uint4*>(a.q + (size_t)(t0 + r0 + b) * a.q_stride +
+                                                                 (size_t)(h * heads + g) * D + part * 8))
+                          : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+        for (int b = 0; b < kAtOnce; ++b) {
+          uint32_t pair = 0;
+#pragma unroll
+          for (int i = 0; i < kHeads; ++i) {
+            pair = max_u16x2(max_u16x2(pair, x[b][i].x & 0x7fff7fffu), x[b][i].y & 0x7fff7fffu);
+            pair = max_u16x2(max_u16x2(pair, x[b][i].z & 0x7fff7fffu), x[b][i].w & 0x7fff7fffu);
+          }
+          uint32_t top = __reduce_max_sync(kFull, max(pair & 0xffffu, pair >> 16));
+          if (top >= 0x7f80u) {   // something counts as 0: the same for a whole warp
+            pair = 0;
+#pragma unroll
+            for (int i = 0; i < kHeads; ++i) {
+              uint32_t* const w = &x[b][i].x;
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                w[j] = (finite_bits(w[j]) ? w[j] & 0xffffu : 0u) | (finite_bits(w[j] >> 16) ? w[j] & 0xffff0000u : 0u);
+                pair = max_u16x2(pair, w[j] & 0x7fff7fffu);
+              }
+            }
+            top = __reduce_max_sync(kFull, max(pair & 0xffffu, pair >> 16));
+          }
+          const uint32_t scale = __float_as_uint(grid_scale(top)) >> 16, scale2 = scale | scale << 16;
+          // x scale + 192 in bf16 is 192 and the rounded product (at most 64), whose bits are 0x4300 + 64 + that; a
+          // lane's missing heads add 64 as well
+          uint32_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+          for (int i = 0; i < kHeads; ++i) {
+            sum[0] += fma_bf16x2(x[b][i].x, scale2, 0x43404340u) - 0x43004300u;
+            sum[1] += fma_bf16x2(x[b][i].y, scale2, 0x43404340u) - 0x43004300u;
+            sum[2] += fma_bf16x2(x[b][i].z, scale2, 0x43404340u) - 0x43004300u;
+            sum[3] += fma_bf16x2(x[b][i].w, scale2, 0x43404340u) - 0x43004300u;
+          }
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+#pragma unroll
+            for (int o = kRowLanes; o < 32; o <<= 1) sum[j] += __shfl_xor_sync(kFull, sum[j], o);
+            constexpr float kZero = 64.0f * kHeads * kPasses;
+            const __half2 y = __floats2half2_rn((float)(sum[j] & 0xffffu) - kZero, (float)(sum[j] >> 16) - kZero);
+            sum[j] = *reinterpret_cast<const uint32_t*>(&y);
+          }
+          if (g0 == 0)
+            *reinterpret_cast<uint4*>(rows_of_u + (r0 + b) * kPad + part * 16) = make_uint4(sum[0], sum[1], sum[2], sum[3]);
+        }
+      }
+    };
+    // as many rows as 32 registers hold
+    if (heads <= 2 * kPasses) rows(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+    else rows(std::integral_constant<int, kSparseGroup / kPasses>{}, std::integral_constant<int, kPasses / 2>{});
+  }
+  __syncthreads();
+
   if (segments > 0 && warp < 4) {
     // ------------------------------------------------------------- queries
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
-    {
-      const uint16_t* const q = a.q + (size_t)min(t, a.total_q - 1) * a.q_stride + (size_t)h * heads * D;
-      const bool real = v.need > 0;
-      uint32_t pair = 0;
-      if (real)
-        for (int i = 0; i < heads * D / 8; ++i) {
-          const uint4 x = __ldg(reinterpret_cast<const uint4*>(q) + i);
-          pair = max_u16x2(max_u16x2(pair, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
-          pair = max_u16x2(max_u16x2(pair, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
-        }
-      uint32_t top = max(pair & 0xffffu, pair >> 16);
-      const bool finite = top < 0x7f80u;
-      if (!finite) {   // again without what counts as 0
-        top = 0;
-        for (int i = 0; i < heads * D; ++i) top = max(top, finite_bits(q[i]));
+#pragma unroll
+    for (int d0 = 0; d0 < D; d0 += 32) {
+      uint32_t r[16];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint4 x = *reinterpret_cast<const uint4*>(rows_of_u + tid * kPad + d0 * 2 + i * 16);
+        r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
       }
-      const float scale = grid_scale(top);
-      const uint32_t scale2 = __float_as_uint(scale) >> 16 | (__float_as_uint(scale) & 0xffff0000u);
-#pragma unroll 1
-      for (int d0 = 0; d0 < D; d0 += 32) {
-        // x scale + 192 in bf16 is 192 and the rounded product (at most 64), whose bits are 0x4300 + 64 + that
-        uint32_t r[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) r[i] = 0;
-        if (real)
-          for (int g = 0; g < heads; ++g)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const uint4 x = __ldg(reinterpret_cast<const uint4*>(q + g * D + d0) + i);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint32_t y = w[j];
-                if (!finite) y = (finite_bits(y) ? y & 0xffffu : 0u) | (finite_bits(y >> 16) ? y & 0xffff0000u : 0u);
-                r[4 * i + j] += fma_bf16x2(y, scale2, 0x43404340u) - 0x43004300u;
-              }
-            }
-        const float zero = real ? 64.0f * heads : 0.0f;
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const __half2 x = __floats2half2_rn((float)(r[i] & 0xffffu) - zero, (float)(r[i] >> 16) - zero);
-          r[i] = *reinterpret_cast<const uint32_t*>(&x);
-        }
-        tmem_st16(tmem + lanes + 128 + d0 / 2, r);
-      }
-      tmem_st_wait();
-      tc_fence_before();
-      mbar_arrive(&sm.rows_in);
+      tmem_st16(tmem + lanes + 128 + d0 / 2, r);
     }
-    List<Sm> list = {sm, tid, 0, -INFINITY};
+    tmem_st_wait();
+    tc_fence_before();
+    mbar_arrive(&sm.rows_in);
+    // the lists' memory is the lists' once every query has its row
+    asm volatile("bar.sync 1, 128;" ::: "memory");
+    for (int i = 0; i < kList; ++i) sm.score[i][tid] = -INFINITY;
+    List<Sm> list = {sm, tid, 0, -INFINITY, -INFINITY};
     int tile = 0;
     bool ok = true;
     for (int sg = 0; sg < segments && ok; ++sg) {
@@ -562,17 +691,23 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
             mbar_arrive(&sm.read[buf]);
           }
           const int j = j0 + g * kGroup, n = min(kGroup, c1 - j);   // this row's blocks of the group
+          // Every score is written behind the list, and stays if it is above: a branch for each column costs six times
+          // as much.
+          const bool whole = __all_sync(kFull, n >= kGroup);
+          if (!whole)
+#pragma unroll
+            for (int i = 0; i < kGroup; ++i)
+              if (i >= n) r[i] = 0xff800000u;   // below every bound
 #pragma unroll
           for (int i = 0; i < kGroup; ++i) {
-            const float s = fmaxf(__uint_as_float(r[i]), kBadScore);   // which a NaN gives
-            if (s > list.bound && i < n) {
-              sm.key[list.cnt][tid] = order_key(s);
-              sm.blk[list.cnt][tid] = (uint16_t)(j + i);
-              ++list.cnt;
-            }
+            const float s = finite_score(__uint_as_float(r[i]));
+            sm.score[list.cnt][tid] = s;
+            sm.blk[list.cnt][tid] = (uint16_t)(j + i);
+            list.cnt += s > list.bound && (whole || i < n);
+            list.top = fmaxf(list.top, s);
           }
           // One list too long: every list is cut that is much longer than it has to be.
-          if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, min(kKeep, v.need + 7));
+          if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, min(kKeep, v.need + v.need / 2 + 8));
         }
       }
     }
@@ -669,9 +804,9 @@ template <int D>
 cudaError_t launch_few(const SelectArgs& p, long long items, cudaStream_t s) {
   // CTAs for a query: as many as fit the GPU at once and have a round of blocks each where the table is full.
   const long long most = (long long)p.a.max_pages * p.a.index.cache.page_tokens >> p.block_log;
-  const int step = kWarps * (512 / D) * kAhead;
+  constexpr int step = kWarps * 16 * kAhead;
   int ranks = 1;
-  while (ranks < 8 && items * ranks * 2 <= sm_count() && most > (long long)step * ranks) ranks *= 2;
+  while (ranks < 8 && items * ranks * 2 <= 2ll * sm_count() && most > (long long)step * ranks) ranks *= 2;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(items * ranks));
   cfg.blockDim = dim3(kThreads);
