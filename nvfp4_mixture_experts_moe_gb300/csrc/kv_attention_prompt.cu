@@ -43,12 +43,14 @@
 // join are one trip to memory after the other, 13 to 15 us in all.
 #include "kernels.cuh"
 #include "kv4.cuh"
+#include "kv_tiles.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
 using namespace tc;
+using namespace tiles;
 
 constexpr int kTok = 128;              // cached tokens of a tile
 constexpr int kHalfTok = kTok / 2;     // and of a half: what softmax and MMA warps hand each other
@@ -69,9 +71,6 @@ constexpr int kSetup = 2;
 // and not: 8 x 8 tokens over 16384, 32 rows, 103 and 117; 16 tokens over 16000,
 // 64 rows, 26.6 and 28.7.)
 constexpr int kSplitRows = 64;
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLead = 7.0f, kSlack = 15.0f;   // log2: m is set the first below the maximum, again past the second
-constexpr unsigned kFull = 0xffffffffu;
 constexpr int kTmemCols = 512;
 
 // The row tile that begins in a CTA's range and goes on past it.
@@ -267,74 +266,6 @@ struct Smem {
   int abort;
 };
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Two fp32 operations in one instruction.
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ float2 unpack2(uint64_t v) {
-  float2 r;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
-  return r;
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float r;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
-// Waits for the tensor-memory loads in flight; the registers they fill are
-// operands, so no use of them moves ahead of the wait.
-__device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])::"memory");
-}
-
-// 2^k for -126 <= k <= 127.
-__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
-
-// Byte offset of 16-byte chunk c (of D/8) of row r in a 128-row f16 tile:
-// 64-column halves of 128-byte rows, chunks swizzled by the row.
-__device__ __forceinline__ uint32_t tile_chunk(int r, int c) {
-  return (uint32_t)((c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4));
-}
-
-__device__ __forceinline__ void sts16(uint32_t addr, uint4 v) {
-  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_constant__ PromptArgs p) {
   using L = Kv4Block<D>;
@@ -499,13 +430,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
                                kFull, reinterpret_cast<unsigned long long>(src), v * kRows + lane / kChunks)) + lane % kChunks);
 #pragma unroll
           for (int v = 0; v < kChunks; ++v)
-            sts16(dst + tile_chunk((warp & 3) * 32 + v * kRows + lane / kChunks, lane % kChunks), raw[v]);
+            sts16(dst + tile_chunk<>((warp & 3) * 32 + v * kRows + lane / kChunks, lane % kChunks), raw[v]);
           __syncwarp();
         }
         uint32_t mx = 0;
 #pragma unroll
         for (int v = 0; v < kChunks; ++v) {
-          const uint4 x = *reinterpret_cast<const uint4*>(tile + tile_chunk(it.r & 127, v));
+          const uint4 x = *reinterpret_cast<const uint4*>(tile + tile_chunk<>(it.r & 127, v));
           mx = max_u16x2(max_u16x2(mx, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
           mx = max_u16x2(max_u16x2(mx, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
         }
@@ -516,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
         if (keep) {
 #pragma unroll 4
           for (int v = 0; v < D / 8; ++v) {
-            uint4* chunk = reinterpret_cast<uint4*>(tile + tile_chunk(it.r & 127, v));
+            uint4* chunk = reinterpret_cast<uint4*>(tile + tile_chunk<>(it.r & 127, v));
             uint4 x = *chunk;
             uint32_t* xw = reinterpret_cast<uint32_t*>(&x);
 #pragma unroll
@@ -745,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prompt_kernel(const __grid_co
     constexpr int kRowsPerLoad = D == 128 ? 8 : 16;
     uint32_t off[4];                               // of this lane's four 16-byte stores, in a tile
 #pragma unroll
-    for (int j = 0; j < 4; ++j) off[j] = tile_chunk(tl, 4 * cl + j);
+    for (int j = 0; j < 4; ++j) off[j] = tile_chunk<>(tl, 4 * cl + j);
     struct Raw {
       uint4 codes[kWarpBlocks][kLoads];
       uint32_t sf[kWarpBlocks][kLoads];            // two scale bytes each

@@ -34,6 +34,8 @@ struct SparseArgs {
   int cluster;    // CTAs that share one (split is then a whole CTA)
   int units;
   int block_log;  // log2 of block_tokens
+  int per;        // units of a request and head, of up to kSparseFewTokens rows (longer ones are another kernel's); 0: units
+                  // are runs of all rows
 };
 
 // A tile is 4608 bytes of one head: 2 blocks of 16 tokens at D = 128, 4 at 64.
@@ -109,10 +111,17 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
 
   for (int unit = (int)(blockIdx.x / p.cluster) * groups + group; unit < p.units;
        unit += (int)(gridDim.x / p.cluster) * groups) {
-    const int h = unit % Hk, t_end = min((unit / Hk + 1) * p.tile, a.total_q);
+    const int h = unit % Hk;
+    int t0 = unit / Hk * p.tile, t_end = min(t0 + p.tile, a.total_q);
+    RowOwner own;
+    if (p.per > 0) {
+      own = request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, a.max_pages * P, unit / Hk / p.per);
+      t0 = own.c0 + unit / Hk % p.per * p.tile;
+      t_end = own.b >= 0 && own.n <= kSparseFewTokens ? min(t0 + p.tile, own.c0 + own.n) : t0;
+    }
     // The rows of the unit that belong to one request, then those of the next.
-    for (int t = unit / Hk * p.tile, nrow; t < t_end; t += nrow) {
-      const RowOwner own = row_owner(a.cu_q, a.kv_len, a.batch, a.total_q, a.max_q, a.max_pages * P, t);
+    for (int t = t0, nrow; t < t_end; t += nrow) {
+      if (p.per == 0) own = row_owner(a.cu_q, a.kv_len, a.batch, a.total_q, a.max_q, a.max_pages * P, t);
       if (own.bad && lane == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
       nrow = own.n > 0 ? min(t_end, own.c0 + own.n) - t : t_end - t;
       if (own.b < 0) continue;
@@ -331,7 +340,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
 }
 
 template <int D, int NT>
-cudaError_t launch(SparseArgs& p, cudaStream_t s) {
+cudaError_t launch(SparseArgs& p, bool by_request, cudaStream_t s) {
   using Sh = Shape<D, NT>;
   auto k = kv4_sparse_kernel<D, NT>;
   constexpr size_t smem = sizeof(Smem<D, NT>);
@@ -344,7 +353,9 @@ cudaError_t launch(SparseArgs& p, cudaStream_t s) {
   p.tile = p.a.max_q == 1 ? 1 : 8 * NT / heads;
   if (p.tile > 8) p.tile = 8;                                   // a row has a bit of a byte
   if (p.tile > kListMax / p.a.top) p.tile = kListMax / p.a.top;
-  const long long units = ((long long)p.a.total_q + p.tile - 1) / p.tile * p.a.cache.kv_heads;
+  p.per = by_request ? (kSparseFewTokens + p.tile - 1) / p.tile : 0;
+  const long long units =
+      (by_request ? (long long)p.a.batch * p.per : ((long long)p.a.total_q + p.tile - 1) / p.tile) * p.a.cache.kv_heads;
   p.units = (int)units;
   // Enough warps a unit to fill the GPU once, as long as each has a tile.
   const int tiles = (p.tile * p.a.top * (p.a.block_tokens / kKvBlock) + Sh::kBlocks - 1) / Sh::kBlocks;
@@ -379,12 +390,15 @@ moe_status launch_kv4_sparse(const moe_kv4_sparse_args& a, cudaStream_t s) {
   p.a = a;
   p.block_log = __builtin_ctz(a.block_tokens);
   const bool wide = a.q_heads / a.cache.kv_heads > 8;
+  // Lengths are on the device: a call that allows longer requests launches both
+  // kernels, each skipping the other's.
+  const bool many = a.max_q > kSparseFewTokens;
   cudaError_t e;
-  if (a.cache.head_dim == 64) e = wide ? launch<64, 2>(p, s) : launch<64, 1>(p, s);
-  else e = wide ? launch<128, 2>(p, s) : launch<128, 1>(p, s);
+  if (a.cache.head_dim == 64) e = wide ? launch<64, 2>(p, many, s) : launch<64, 1>(p, many, s);
+  else e = wide ? launch<128, 2>(p, many, s) : launch<128, 1>(p, many, s);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
-  return MOE_OK;
+  return many ? launch_kv4_sparse_prompt(a, kSparseFewTokens, s) : MOE_OK;
 }
 
 }  // namespace moe
