@@ -246,12 +246,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               const bool partial = __any_sync(kFull, real && ((take0 && tok0 + kStep / 2 - 1 > pos) ||
                                                               (take1 && tok1 + kStep / 2 - 1 > pos))) || hole != 0;
               const bool some = !__all_sync(kFull, !real || (take0 && take1));   // rows that do not take it all
-              uint32_t s0[32], s1[32];
-              tmem_ld32(s_t, s0);
-              tmem_ld32(s_t + 32, s1);
-              ld_wait(s0);
-              ld_wait(s1);
-              auto peak = [&](uint32_t (&sr)[32], int piece) {
+              // A half of S at a time: 96 registers a thread are what two CTAs an SM leave, so the second half is read
+              // once more for its exponentials.
+              uint32_t sr[32];
+              auto read = [&](int piece) {
+                tmem_ld32(s_t + 32 * piece, sr);
+                ld_wait(sr);
                 if (partial) {   // bit e: column e is seen
                   const int hi = pos - (piece ? tok1 : tok0);
                   uint32_t see = hi >= 31 ? ~0u : hi < 0 ? 0u : (2u << hi) - 1u;
@@ -262,6 +262,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
                   for (int e = 0; e < 32; ++e)
                     if (!(see >> e & 1u)) sr[e] = 0xff800000u;
                 }
+              };
+              auto peak = [&]() {
                 float u0 = __uint_as_float(sr[0]), u1 = __uint_as_float(sr[1]);
 #pragma unroll
                 for (int e = 2; e < 30; e += 4) {
@@ -270,8 +272,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
                 }
                 return max3(u0, u1, fmaxf(__uint_as_float(sr[30]), __uint_as_float(sr[31])));
               };
-              const float p0 = peak(s0, 0), p1 = peak(s1, 1);
-              const float top = fmaxf(take0 ? p0 : -INFINITY, take1 ? p1 : -INFINITY) * c;
+              read(1);
+              const float p1 = peak();
+              read(0);
+              const float top = fmaxf(take0 ? peak() : -INFINITY, take1 ? p1 : -INFINITY) * c;
               if (__any_sync(kFull, top > m + kSlack)) {
                 const float mn = fmaxf(m, top - kLead), f = mn == -INFINITY ? 1.0f : ex2(m - mn);
                 m = mn;
@@ -293,8 +297,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               }
               const float mu = m == -INFINITY ? 0.0f : m;
               const uint64_t m2 = pack2(-mu, -mu), c2 = pack2(c, c);
-              auto exps = [&](const uint32_t (&sr)[32], int piece, bool take) {
-                uint32_t pk[16];
+              auto exps = [&](uint32_t (&pk)[16], bool take) {
                 uint64_t sum = pack2(0.0f, 0.0f);
 #pragma unroll
                 for (int e = 0; e < 16; ++e) {
@@ -310,10 +313,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
                   if (!take) sum = pack2(0.0f, 0.0f);
                 }
                 l2 = add2(l2, sum);
-                tmem_st16(s_t + 16 * piece, pk);   // P takes the columns of S, read by then
               };
-              exps(s0, 0, take0);
-              exps(s1, 1, take1);
+              uint32_t pk0[16], pk1[16];
+              exps(pk0, take0);
+              read(1);
+              exps(pk1, take1);
+              tmem_st16(s_t, pk0);   // P takes the columns of S, read by then
+              tmem_st16(s_t + 16, pk1);
             }
             tmem_st_wait();
             tc_fence_before();
@@ -331,25 +337,25 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
           struct Raw {
             uint4 codes[kLoads];
             uint32_t sf[kLoads];                       // two scale bytes each
-          } rk, rv;
-          // Where the block of a step lies and its tokens that are there; -1: its page is bad.
-          auto place = [&](int s, const uint8_t*& src) {
-            const int e = entry(s, x);
-            if (e >= count) return 0;
-            const int tok = ((base + sm->id[e]) << p.block_log) + ((s * kDeqWarps + x) & ((1 << sub_log) - 1)) * kKvBlock;
-            if (tok >= own.kv) return 0;
-            const int page = __ldg(table + (tok >> p_log));
-            if (page < 0 || page >= a.cache.num_pages) {
-              if (lane == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-              return -1;
-            }
-            src = static_cast<const uint8_t*>(a.cache.pool) +
-                  kv4_block_offset(page, h, Hk, P / kKvBlock, (tok & (P - 1)) / kKvBlock, L::kBytes);
-            return own.kv - tok;
           };
-          auto load = [&](Raw& r, const uint8_t* src, int to, int part) {   // keys (part 0) or values
-            const uint8_t *codes = src + part + tl * L::kCodeRow + 16 * cl,
-                          *scales = src + part + L::kKeyScales + tl * L::kScaleRow + 2 * cl;
+          // A step's block goes through three stages, a step apart: its page id is asked for, its codes are, it is
+          // converted (keys and values each behind one more step's).
+          struct Block {
+            int page, tok;                             // tok < 0: there is none
+            int to;                                    // its tokens that are there; -1: the page is bad
+            Raw k, v;
+          } b0, b1;
+          auto look_up = [&](Block& b, int s) {
+            const int e = s < steps ? entry(s, x) : count;
+            b.tok = -1;
+            if (e >= count) return;
+            const int tok = ((base + sm->id[e]) << p.block_log) + ((s * kDeqWarps + x) & ((1 << sub_log) - 1)) * kKvBlock;
+            if (tok >= own.kv) return;
+            b.tok = tok;
+            b.page = __ldg(table + (tok >> p_log));
+          };
+          auto load = [&](Raw& r, const uint8_t* src, int to) {
+            const uint8_t *codes = src + tl * L::kCodeRow + 16 * cl, *scales = src + L::kKeyScales + tl * L::kScaleRow + 2 * cl;
 #pragma unroll
             for (int y = 0; y < kLoads; ++y) {
               r.codes[y] = make_uint4(0u, 0u, 0u, 0u);   // what may not have been appended enters as zeros
@@ -360,6 +366,25 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               }
             }
           };
+          auto fetch = [&](Block& b) {
+            const uint8_t* src = nullptr;
+            b.to = 0;
+            if (b.tok >= 0) {
+              if (b.page >= 0 && b.page < a.cache.num_pages) {
+                src = static_cast<const uint8_t*>(a.cache.pool) +
+                      kv4_block_offset(b.page, h, Hk, P / kKvBlock, (b.tok & (P - 1)) / kKvBlock, L::kBytes);
+                b.to = own.kv - b.tok;
+              } else {
+                b.to = -1;
+                if (lane == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+              }
+            }
+            load(b.k, src, b.to);
+            load(b.v, src + L::kValueCodes, b.to);
+          };
+          uint32_t off[4];                             // of this lane's four 16-byte stores, in a tile
+#pragma unroll
+          for (int i = 0; i < 4; ++i) off[i] = tile_chunk<kStep>(x * kKvBlock + tl, 4 * cl + i);
           auto store = [&](uint32_t tile, const Raw& r) {
 #pragma unroll
             for (int y = 0; y < kLoads; ++y) {
@@ -371,32 +396,39 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
                 uint32_t f[4];
                 cvt_e2m1x8_f16(wd[i], f);
                 const uint32_t sc = i < 2 ? sc0 : sc1;
-                sts16(tile + tile_chunk<kStep>(x * kKvBlock + y * kRowsPerLoad + tl, 4 * cl + i),
+                sts16(tile + off[i] + y * kRowsPerLoad * 128,
                       make_uint4(hmul2_u32(f[0], sc), hmul2_u32(f[1], sc), hmul2_u32(f[2], sc), hmul2_u32(f[3], sc)));
               }
             }
           };
-          const uint8_t *src = nullptr, *next_src = nullptr;
-          int to = place(0, src);
-          load(rk, src, to, 0);
-          load(rv, src, to, L::kValueCodes);
-          for (int s = 0; s < steps; ++s) {
+          auto convert = [&](Block& b, int s) {
             const int j = js + s, st = j & 1;
-            const int next_to = s + 1 < steps ? place(s + 1, next_src) : 0;
-            if (!wait(&sm->k_empty[st], (j >> 1) ^ 1)) break;
-            if (lane == 0) sm->hole[j & 3][x] = to < 0 ? 0xff : 0;
-            store(smem_u32(sm->k[st]), rk);
+            if (!wait(&sm->k_empty[st], (j >> 1) ^ 1)) return false;
+            if (lane == 0) sm->hole[j & 3][x] = b.to < 0 ? 0xff : 0;
+            store(smem_u32(sm->k[st]), b.k);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->k_full[st]);
-            load(rk, next_src, next_to, 0);
-            if (!wait(&sm->v_empty[st], (j >> 1) ^ 1)) break;
-            store(smem_u32(sm->v[st]), rv);
+            if (!wait(&sm->v_empty[st], (j >> 1) ^ 1)) return false;
+            store(smem_u32(sm->v[st]), b.v);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->v_full[st]);
-            load(rv, next_src, next_to, L::kValueCodes);
-            to = next_to;
+            return true;
+          };
+          look_up(b0, 0);
+          look_up(b1, 1);
+          fetch(b0);
+          fetch(b1);
+          look_up(b0, 2);
+          look_up(b1, 3);
+          for (int s = 0; s < steps; s += 2) {
+            if (!convert(b0, s)) break;
+            fetch(b0);
+            look_up(b0, s + 4);
+            if (s + 1 == steps || !convert(b1, s + 1)) break;
+            fetch(b1);
+            look_up(b1, s + 5);
           }
         } else {
           // --------------------------------------------------------------- MMA
