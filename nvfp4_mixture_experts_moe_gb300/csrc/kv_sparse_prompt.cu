@@ -12,7 +12,9 @@
 // of the union. Then, in a CTA of which two share an SM:
 // * four dequant warps convert a 16-token block each of every step, keys
 //   K-major, values with d contiguous, from codes asked for a step ahead;
-// * one thread issues S = Q K^T of the step ahead and O += P V;
+// * a thread issues S = Q K^T, another O += P V (an issue takes its thread 45
+//   cycles and more: one thread for both took 2080 cycles a step without any
+//   softmax);
 // * four softmax warps have a row a thread. A warp none of whose tokens takes
 //   the step's blocks leaves zeros as P without looking at S; a row whose token
 //   does not has its P cleared; only where a block is not seen whole (the
@@ -36,7 +38,7 @@ constexpr int kTokens = 32;             // query tokens of a unit: a bit each of
 constexpr int kUnion = kTokens * kSparseTop;
 constexpr int kWindow = 8192;           // blocks whose union is built at once: longer contexts take several
 constexpr int kSoftWarps = 4, kDeqWarps = 4, kMmaWarp = kSoftWarps + kDeqWarps;
-constexpr int kThreads = (kMmaWarp + 1) * 32;
+constexpr int kThreads = (kMmaWarp + 2) * 32;
 constexpr int kTmemCols = 256;          // S of two steps, O
 static_assert(kStep / kKvBlock == kDeqWarps, "a 16-token block a dequant warp");
 
@@ -59,7 +61,7 @@ struct Smem {
   uint32_t bits[kWindow / 32];          // blocks of the window that are in it
   uint16_t before[kWindow / 32];        // how many come before a word's
   uint16_t id[kUnion];                  // its blocks, within the window
-  uint64_t q_full, s_full[2], p_full[2], pv_done, o_full;
+  uint64_t q_full, s_full[2], p_full[2], pv_done[2], o_full;
   uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], drain;
   alignas(4) uint8_t hole[4][4];        // 16-token blocks of a step whose page is bad
   int warp_sum[kThreads / 32 + 1];
@@ -80,11 +82,11 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
   if (tid == 0) {
     sm->abort = 0;
     mbar_init(&sm->q_full, kSoftWarps);
-    mbar_init(&sm->pv_done, 1);
     mbar_init(&sm->o_full, 1);
-    mbar_init(&sm->drain, 1);
+    mbar_init(&sm->drain, 2);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm->s_full[i], 1);
+      mbar_init(&sm->pv_done[i], 1);
       mbar_init(&sm->p_full[i], kSoftWarps);
       mbar_init(&sm->k_full[i], kDeqWarps);
       mbar_init(&sm->v_full[i], kDeqWarps);
@@ -282,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
                 const float2 l = unpack2(l2);
                 l2 = pack2(l.x * f, l.y * f);
                 if (!first || s > 0) {   // O holds the steps before, once the last of them has gone in
-                  if (!(ok = wait(&sm->pv_done, j - 1))) break;
+                  if (!(ok = wait(&sm->pv_done[(j - 1) & 1], (j - 1) >> 1))) break;
                   tc_fence_after();
 #pragma unroll 1
                   for (int cc = 0; cc < D; cc += 16) {
@@ -339,12 +341,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
             uint32_t sf[kLoads];                       // two scale bytes each
           };
           // A step's block goes through three stages, a step apart: its page id is asked for, its codes are, it is
-          // converted (keys and values each behind one more step's).
+          // converted (the keys behind one more step's).
           struct Block {
             int page, tok;                             // tok < 0: there is none
             int to;                                    // its tokens that are there; -1: the page is bad
             Raw k, v;
-          } b0, b1;
+          } blk;
           auto look_up = [&](Block& b, int s) {
             const int e = s < steps ? entry(s, x) : count;
             b.tok = -1;
@@ -401,49 +403,37 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               }
             }
           };
-          auto convert = [&](Block& b, int s) {
+          look_up(blk, 0);
+          fetch(blk);
+          look_up(blk, 1);
+          for (int s = 0; s < steps; ++s) {
             const int j = js + s, st = j & 1;
-            if (!wait(&sm->k_empty[st], (j >> 1) ^ 1)) return false;
-            if (lane == 0) sm->hole[j & 3][x] = b.to < 0 ? 0xff : 0;
-            store(smem_u32(sm->k[st]), b.k);
+            if (!wait(&sm->k_empty[st], (j >> 1) ^ 1)) break;
+            if (lane == 0) sm->hole[j & 3][x] = blk.to < 0 ? 0xff : 0;
+            store(smem_u32(sm->k[st]), blk.k);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->k_full[st]);
-            if (!wait(&sm->v_empty[st], (j >> 1) ^ 1)) return false;
-            store(smem_u32(sm->v[st]), b.v);
+            if (!wait(&sm->v_empty[st], (j >> 1) ^ 1)) break;
+            store(smem_u32(sm->v[st]), blk.v);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&sm->v_full[st]);
-            return true;
-          };
-          look_up(b0, 0);
-          look_up(b1, 1);
-          fetch(b0);
-          fetch(b1);
-          look_up(b0, 2);
-          look_up(b1, 3);
-          for (int s = 0; s < steps; s += 2) {
-            if (!convert(b0, s)) break;
-            fetch(b0);
-            look_up(b0, s + 4);
-            if (s + 1 == steps || !convert(b1, s + 1)) break;
-            fetch(b1);
-            look_up(b1, s + 5);
+            fetch(blk);
+            look_up(blk, s + 2);
           }
         } else {
           // --------------------------------------------------------------- MMA
-          constexpr uint32_t id_s = idesc_f16(128, kStep, 0);
-          constexpr uint32_t id_o = idesc_f16(128, D, 0) | (1u << 16);   // values: N (d) contiguous
-          const uint64_t qd = smem_desc(smem_u32(sm->q), 16, 1024, kSwizzle128B);
-          const uint64_t kd = smem_desc(smem_u32(sm->k[0]), 16, 1024, kSwizzle128B);
-          // MN-major: leading offset between 64-column halves, stride between 8-token groups
-          const uint64_t vd = smem_desc(smem_u32(sm->v[0]), kStep * 128, 1024, kSwizzle128B);
           bool ok = true;
-          if (!entered) ok = wait(&sm->q_full, jq);
-          for (int s = -1; s < steps && ok; ++s) {
-            const int j = js + s, buf = j & 1, ahead = j + 1, st = ahead & 1;
-            if (s + 1 < steps) {
-              if (!(ok = wait(&sm->k_full[st], ahead >> 1))) break;
+          if (warp == kMmaWarp) {
+            constexpr uint32_t id_s = idesc_f16(128, kStep, 0);
+            const uint64_t qd = smem_desc(smem_u32(sm->q), 16, 1024, kSwizzle128B);
+            const uint64_t kd = smem_desc(smem_u32(sm->k[0]), 16, 1024, kSwizzle128B);
+            if (!entered) ok = wait(&sm->q_full, jq);
+            for (int s = 0; s < steps && ok; ++s) {
+              const int j = js + s, st = j & 1;
+              // the columns' last P has gone into O
+              if (!(ok = wait(&sm->k_full[st], j >> 1) && wait(&sm->pv_done[st], (j >> 1) ^ 1))) break;
               tc_fence_after();
               if (lane == 0) {
                 const uint64_t kb = kd + (uint64_t)((st * Sm::kTile) >> 4);
@@ -456,18 +446,24 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               }
               __syncwarp();
             }
-            if (s < 0) continue;
-            if (!(ok = wait(&sm->v_full[buf], j >> 1) && wait(&sm->p_full[buf], j >> 1))) break;
-            tc_fence_after();
-            if (lane == 0) {
-              const uint64_t vb = vd + (uint64_t)((buf * Sm::kTile) >> 4);
+          } else {
+            constexpr uint32_t id_o = idesc_f16(128, D, 0) | (1u << 16);   // values: N (d) contiguous
+            // MN-major: leading offset between 64-column halves, stride between 8-token groups
+            const uint64_t vd = smem_desc(smem_u32(sm->v[0]), kStep * 128, 1024, kSwizzle128B);
+            for (int s = 0; s < steps && ok; ++s) {
+              const int j = js + s, st = j & 1;
+              if (!(ok = wait(&sm->v_full[st], j >> 1) && wait(&sm->p_full[st], j >> 1))) break;
+              tc_fence_after();
+              if (lane == 0) {
+                const uint64_t vb = vd + (uint64_t)((st * Sm::kTile) >> 4);
 #pragma unroll
-              for (int kk = 0; kk < kStep / 16; ++kk)
-                mma_f16_tmem_a(o_tmem, tmem + kStep * buf + 8 * kk, vb + kk * (2048 >> 4), id_o, !first || s > 0 || kk > 0);
-              tc_commit(&sm->pv_done);
-              tc_commit(&sm->v_empty[buf]);
+                for (int kk = 0; kk < kStep / 16; ++kk)
+                  mma_f16_tmem_a(o_tmem, tmem + kStep * st + 8 * kk, vb + kk * (2048 >> 4), id_o, !first || s > 0 || kk > 0);
+                tc_commit(&sm->pv_done[st]);
+                tc_commit(&sm->v_empty[st]);
+              }
+              __syncwarp();
             }
-            __syncwarp();
           }
         }
         entered = true;
@@ -476,7 +472,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
 
       // --------------------------------------------------------- the results
       if (steps_so_far > 0) {
-        if (warp == kMmaWarp && lane == 0) tc_commit(&sm->o_full);
+        if (warp == kMmaWarp + 1 && lane == 0) tc_commit(&sm->o_full);
         if (warp < kSoftWarps && wait(&sm->o_full, jq)) {
           tc_fence_after();
           const float2 two = unpack2(l2);
@@ -515,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
       }
     }
   }
-  if (warp == kMmaWarp && lane == 0) {   // what was issued is complete before tensor memory is given back
+  if (warp >= kMmaWarp && lane == 0) {   // what was issued is complete before tensor memory is given back
     tc_commit(&sm->drain);
     const long long t0 = clock64();
     while (!mbar_try_wait(&sm->drain, 0) && clock64() - t0 < 4000000000ll) {
