@@ -17,7 +17,7 @@
 namespace moe {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kWarps = 4, kAtOnce = 4;   // 16-token blocks asked for together
 constexpr unsigned kFull = 0xffffffffu;
 
 struct IndexArgs {
@@ -49,48 +49,64 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_index_kernel(const __grid_con
   const int32_t* const table = p.table + (size_t)b * p.max_pages;
   const int tok0 = blk * B, row0 = lane / kLanes, part = lane % kLanes;
 
+  // Page ids first, all at once, then the rows of kAtOnce 16-token blocks.
+  const int subs = B / kKvBlock;
+  const int my_page = lane < subs ? __ldg(table + (tok0 + lane * kKvBlock) / P) : 0;
+  if (__any_sync(kFull, my_page < 0 || my_page >= c.num_pages)) {
+    if (lane == 0 && p.status != nullptr) *p.status = MOE_ERR_DEVICE;
+    return;
+  }
   int sum[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) sum[i] = 0;
-  bool bad = false;
-  for (int s = 0; s < B / kKvBlock; ++s) {
-    const int tok = tok0 + s * kKvBlock, page = __ldg(table + tok / P);
-    if (page < 0 || page >= c.num_pages) {
-      bad = true;
-      break;
-    }
-    const uint8_t* const src = static_cast<const uint8_t*>(c.pool) +
-                               kv4_block_offset(page, h, c.kv_heads, P / kKvBlock, tok % P / kKvBlock, L::kBytes);
-    float part_sum[32];   // of at most two tokens: exact
+#pragma unroll 1
+  for (int s0 = 0; s0 < subs; s0 += kAtOnce) {
+    uint4 codes[kAtOnce][kRounds];
+    uint32_t two[kAtOnce][kRounds];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) part_sum[i] = 0.0f;
+    for (int s = 0; s < kAtOnce; ++s) {
+      const int tok = tok0 + (s0 + s) * kKvBlock, page = __shfl_sync(kFull, my_page, s0 + s);
+      const uint8_t* const src = static_cast<const uint8_t*>(c.pool) +
+                                 kv4_block_offset(page, h, c.kv_heads, P / kKvBlock, tok % P / kKvBlock, L::kBytes);
 #pragma unroll
-    for (int r = 0; r < kRounds; ++r) {
-      const int row = r * kRows + row0;
-      const uint4 codes = __ldg(reinterpret_cast<const uint4*>(src + row * L::kCodeRow) + part);
-      const uint32_t two = __ldg(reinterpret_cast<const uint16_t*>(src + L::kKeyScales + row * L::kScaleRow) + part);
-      const uint32_t sc = cvt_e4m3x2_f16x2(two);
-      const uint32_t w[4] = {codes.x, codes.y, codes.z, codes.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t v[4];
-        cvt_e2m1x8_f16(w[i], v);
-        const uint32_t s2 = __byte_perm(sc, 0, i < 2 ? 0x1010 : 0x3232);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const uint32_t prod = hmul2_u32(v[j], s2);   // exact
-          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&prod));
-          part_sum[8 * i + 2 * j] += f.x;
-          part_sum[8 * i + 2 * j + 1] += f.y;
+      for (int r = 0; r < kRounds; ++r) {
+        const int row = r * kRows + row0;
+        codes[s][r] = make_uint4(0u, 0u, 0u, 0u);
+        two[s][r] = 0u;
+        if (s0 + s < subs) {
+          codes[s][r] = __ldg(reinterpret_cast<const uint4*>(src + row * L::kCodeRow) + part);
+          two[s][r] = __ldg(reinterpret_cast<const uint16_t*>(src + L::kKeyScales + row * L::kScaleRow) + part);
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum[i] += __float2int_rn(part_sum[i] * 1024.0f);
-  }
-  if (bad) {   // the same for a whole warp
-    if (lane == 0 && p.status != nullptr) *p.status = MOE_ERR_DEVICE;
-    return;
+    for (int pair = 0; pair < kAtOnce; pair += 2) {
+      float part_sum[32];   // of at most four tokens, below 2^14: exact
+#pragma unroll
+      for (int i = 0; i < 32; ++i) part_sum[i] = 0.0f;
+#pragma unroll
+      for (int s = pair; s < pair + 2; ++s)
+#pragma unroll
+        for (int r = 0; r < kRounds; ++r) {
+          const uint32_t sc = cvt_e4m3x2_f16x2(two[s][r]);
+          const uint32_t w[4] = {codes[s][r].x, codes[s][r].y, codes[s][r].z, codes[s][r].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t v[4];
+            cvt_e2m1x8_f16(w[i], v);
+            const uint32_t s2 = __byte_perm(sc, 0, i < 2 ? 0x1010 : 0x3232);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t prod = hmul2_u32(v[j], s2);   // exact
+              const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&prod));
+              part_sum[8 * i + 2 * j] += f.x;
+              part_sum[8 * i + 2 * j + 1] += f.y;
+            }
+          }
+        }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sum[i] += __float2int_rn(part_sum[i] * 1024.0f);
+    }
   }
   unsigned top = 0;
 #pragma unroll

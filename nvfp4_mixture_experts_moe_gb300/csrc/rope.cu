@@ -16,6 +16,8 @@ namespace moe {
 namespace {
 
 constexpr int kThreads = 256;
+// Heads whose rows a thread has asked for, of a rotation and of an append.
+constexpr int kAhead = 4, kAppendAhead = 2;
 
 // (cos, sin) of a pair's angle, times the plan's scale.
 __device__ __forceinline__ float2 rotation(uint64_t turns, int pos, float scale) {
@@ -72,13 +74,39 @@ __device__ __forceinline__ void turn8(const float2 (&cs)[8], bool adjacent, floa
   }
 }
 
+// A thread's two runs of eight elements. One sector (kWide: 32-byte aligned,
+// the second run behind the first) in one load or store: halves of it in two
+// are two trips for the same bytes.
+__device__ __forceinline__ void load_runs(const uint16_t* p, int lo, int hi, bool wide, uint4 (&w)[2]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0].x), "=r"(w[0].y), "=r"(w[0].z), "=r"(w[0].w), "=r"(w[1].x), "=r"(w[1].y), "=r"(w[1].z),
+                   "=r"(w[1].w)
+                 : "l"(p + lo));
+  } else {
+    w[0] = *reinterpret_cast<const uint4*>(p + lo);
+    w[1] = *reinterpret_cast<const uint4*>(p + hi);
+  }
+}
+
+__device__ __forceinline__ void store_runs(uint16_t* p, int lo, int hi, bool wide, const uint4 (&w)[2]) {
+  if (wide) {
+    const uint32_t v[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+    stg_v8(p + lo, v);
+  } else {
+    *reinterpret_cast<uint4*>(p + lo) = w[0];
+    *reinterpret_cast<uint4*>(p + hi) = w[1];
+  }
+}
+
 struct RopeRows {
   moe_rope_args a;
   int splits, units, turning;   // threads of a token and unit; units of a head, the first `turning` of them with pairs
 };
 
 // Rows of 16-byte alignment, rotary_dim a multiple of 16: a unit is eight pairs
-// or sixteen elements to copy, two 16-byte loads and stores a head.
+// or sixteen elements to copy, two 16-byte loads and stores a head (kWide: one of 32).
+template <bool kWide>
 __global__ void __launch_bounds__(kThreads) rope_vector_kernel(const __grid_constant__ RopeRows p) {
   const moe_rope_args& a = p.a;
   pdl_wait();
@@ -108,7 +136,6 @@ __global__ void __launch_bounds__(kThreads) rope_vector_kernel(const __grid_cons
   const uint16_t* const k = a.k + (size_t)t * a.k_stride;
   uint16_t* const qo = a.q_out + (size_t)t * a.q_out_stride;
   uint16_t* const ko = a.k_out + (size_t)t * a.k_out_stride;
-  constexpr int kAhead = 4;
   for (int h0 = first; h0 < heads; h0 += kAhead * p.splits) {
     uint4 w[kAhead][2];
 #pragma unroll
@@ -116,8 +143,8 @@ __global__ void __launch_bounds__(kThreads) rope_vector_kernel(const __grid_cons
       const int h = h0 + j * p.splits;
       if (h >= heads) break;
       const uint16_t* src = h < a.q_heads ? q + (size_t)h * a.head_dim : k + (size_t)(h - a.q_heads) * a.head_dim;
-      w[j][0] = *reinterpret_cast<const uint4*>(src + lo);
-      if (second) w[j][1] = *reinterpret_cast<const uint4*>(src + hi);
+      if (second) load_runs(src, lo, hi, kWide, w[j]);
+      else w[j][0] = *reinterpret_cast<const uint4*>(src + lo);
     }
 #pragma unroll
     for (int j = 0; j < kAhead; ++j) {
@@ -132,8 +159,8 @@ __global__ void __launch_bounds__(kThreads) rope_vector_kernel(const __grid_cons
         w[j][0] = pack8(x);
         w[j][1] = pack8(y);
       }
-      *reinterpret_cast<uint4*>(dst + lo) = w[j][0];
-      if (second) *reinterpret_cast<uint4*>(dst + hi) = w[j][1];
+      if (second) store_runs(dst, lo, hi, kWide, w[j]);
+      else *reinterpret_cast<uint4*>(dst + lo) = w[j][0];
     }
   }
 }
@@ -181,14 +208,14 @@ struct AppendRope {
   moe_kv4_append_rope_args a;
   int splits;     // warps of a run of tokens
   int page_log;
+  bool wide_in, wide_out;   // rows are 32-byte aligned; and queries' runs neighbours
 };
 
-// Codes and scale of sixteen values of which a thread (kWhole) or a pair of
-// neighbouring threads has all. NaNs are gone, infinities saturate.
+// Largest magnitude of eight values; NaN if there is one.
 __device__ __forceinline__ float amax8(const float (&x)[8]) {
-  float m = 0.0f;
+  float m = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));
+  for (int i = 1; i < 8; ++i) asm("max.NaN.f32 %0, %0, %1;" : "+f"(m) : "f"(fabsf(x[i])));
   return m;
 }
 
@@ -218,88 +245,111 @@ __device__ __forceinline__ void no_nan(float (&x)[8]) {
     if (x[i] != x[i]) x[i] = 0.0f;
 }
 
-// A warp takes 512 / D consecutive tokens (a lane: sixteen elements of one) and
-// every splits-th of their rows: query heads, key heads, value heads.
+// A CTA has 512 / D consecutive tokens, whose sines and cosines it works out
+// once; a warp (a lane: sixteen elements of a token) takes every splits-th of
+// their rows: query heads, key heads, value heads.
 template <int D>
 __global__ void __launch_bounds__(kThreads) kv4_append_rope_kernel(const __grid_constant__ AppendRope p) {
   using L = Kv4Block<D>;
-  constexpr int kUnits = D / 16, kTokens = 32 / kUnits, kWarps = kThreads / 32;
+  constexpr int kUnits = D / 16, kTokens = 32 / kUnits;
+  __shared__ alignas(16) float2 table[kTokens][D / 2];
   const moe_kv4_append_rope_args& a = p.a;
   pdl_wait();
-  const int lane = threadIdx.x & 31, u = lane % kUnits;
-  const unsigned w = blockIdx.x * kWarps + (threadIdx.x >> 5);
-  const int first = w % p.splits;
-  const long long t0 = (long long)(w / p.splits) * kTokens;
-  if (t0 >= a.tokens) return;                        // the same for a whole warp
+  const int lane = threadIdx.x & 31, u = lane % kUnits, first = blockIdx.y * (blockDim.x / 32) + (threadIdx.x >> 5);
+  const int t0 = blockIdx.x * kTokens, R = a.plan.rotary_dim, Hq = a.q_heads, Hk = a.cache.kv_heads;
+  for (int i = threadIdx.x; i < kTokens * (R / 2); i += blockDim.x) {
+    const int token = i / (R / 2), pair = i - token * (R / 2);
+    table[token][pair] = rotation_of(a.plan, pair, a.positions, a.tokens, min(t0 + token, a.tokens - 1));
+  }
   const bool real = t0 + lane / kUnits < a.tokens;
-  const int t = real ? (int)t0 + lane / kUnits : a.tokens - 1;   // lanes past the end follow, and store nothing
-  const int R = a.plan.rotary_dim, Hq = a.q_heads, Hk = a.cache.kv_heads;
+  const int t = real ? t0 + lane / kUnits : a.tokens - 1;   // lanes past the end follow, and store nothing
   const bool turns = u < R / 16;
   const int lo = turns && !a.plan.adjacent ? 8 * u : 16 * u, hi = turns && !a.plan.adjacent ? lo + R / 2 : lo + 8;
   const int slot = real ? __ldg(a.slots + t) : -1;
   const long long limit = (long long)a.cache.num_pages << p.page_log;
   const bool keep = slot >= 0 && slot < limit;
   if (slot >= limit && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+  __syncthreads();
   float2 cs[8];
   if (turns)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) cs[i] = rotation_of(a.plan, 8 * u + i, a.positions, a.tokens, t);
+    for (int i = 0; i < 8; i += 2) {
+      const float4 two = *reinterpret_cast<const float4*>(&table[lane / kUnits][8 * u + i]);
+      cs[i] = make_float2(two.x, two.y);
+      cs[i + 1] = make_float2(two.z, two.w);
+    }
   const int row = slot % kKvBlock;
   uint8_t* const pool = static_cast<uint8_t*>(a.cache.pool);
   auto block_of = [&](int h) {
     return pool + kv4_block_offset(slot >> p.page_log, h, Hk, (1 << p.page_log) / kKvBlock,
                                    (slot & ((1 << p.page_log) - 1)) / kKvBlock, L::kBytes);
   };
-  for (int r = first; r < Hq + 2 * Hk; r += p.splits) {
-    float x[8], y[8];
-    if (r < Hq) {
-      const uint16_t* src = a.q + (size_t)t * a.q_stride + r * D;
-      uint4 v0 = __ldg(reinterpret_cast<const uint4*>(src + lo)), v1 = __ldg(reinterpret_cast<const uint4*>(src + hi));
-      if (turns) {
-        unpack8(v0, x);
-        unpack8(v1, y);
-        turn8(cs, a.plan.adjacent, x, y);
-        v0 = pack8(x);
-        v1 = pack8(y);
-      }
-      if (real) {
-        uint16_t* dst = a.q_out + (size_t)t * a.q_out_stride + r * D;
-        *reinterpret_cast<uint4*>(dst + lo) = v0;
-        *reinterpret_cast<uint4*>(dst + hi) = v1;
-      }
-      continue;
+  const int rows = Hq + 2 * Hk;
+  const uint16_t *const q = a.q + (size_t)t * a.q_stride, *const k = a.k + (size_t)t * a.k_stride,
+                 *const v = a.v + (size_t)t * a.v_stride;
+  for (int r0 = first; r0 < rows; r0 += kAppendAhead * p.splits) {
+    uint4 w[kAppendAhead][2];
+#pragma unroll
+    for (int i = 0; i < kAppendAhead; ++i) {
+      const int r = r0 + i * p.splits;
+      if (r >= rows) break;
+      const uint16_t* src = r < Hq ? q + r * D : r < Hq + Hk ? k + (r - Hq) * D : v + (r - Hq - Hk) * D;
+      const bool value = r >= Hq + Hk;
+      load_runs(src, value ? 16 * u : lo, value ? 16 * u + 8 : hi, p.wide_in && (value || a.plan.adjacent), w[i]);
     }
-    const bool key = r < Hq + Hk;
-    const int h = r - Hq - (key ? 0 : Hk);
-    const uint16_t* src = (key ? a.k + (size_t)t * a.k_stride : a.v + (size_t)t * a.v_stride) + h * D;
-    const int at0 = key ? lo : 16 * u, at1 = key ? hi : 16 * u + 8;
-    unpack8(__ldg(reinterpret_cast<const uint4*>(src + at0)), x);
-    unpack8(__ldg(reinterpret_cast<const uint4*>(src + at1)), y);
-    if (key && turns) turn8(cs, a.plan.adjacent, x, y);
-    no_nan(x);
-    no_nan(y);
-    const float gs = key ? a.cache.k_gs : a.cache.v_gs;
-    float mx = amax8(x), my = amax8(y);
-    // Halves: two neighbouring lanes have the two runs of a group of sixteen.
-    const float ox = __shfl_xor_sync(0xffffffffu, mx, 1), oy = __shfl_xor_sync(0xffffffffu, my, 1);
-    const bool split = key && turns && !a.plan.adjacent;
-    if (split) {
-      mx = fmaxf(mx, ox);
-      my = fmaxf(my, oy);
-    } else {
-      mx = my = fmaxf(mx, my);
-    }
-    if (!keep) continue;
-    const Scale sx = scale_of(mx, gs), sy = split ? scale_of(my, gs) : sx;
-    uint8_t* const blk = block_of(h) + (key ? 0 : L::kValueCodes);
-    *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at0 / 2) = codes8(x, sx.r);
-    *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at1 / 2) = codes8(y, sy.r);
-    uint8_t* const scales = blk + L::kKeyScales + row * L::kScaleRow;
-    if (!split) {
-      scales[u] = (uint8_t)sx.code;
-    } else if (u % 2 == 0) {
-      scales[at0 / 16] = (uint8_t)sx.code;
-      scales[at1 / 16] = (uint8_t)sy.code;
+#pragma unroll
+    for (int i = 0; i < kAppendAhead; ++i) {
+      const int r = r0 + i * p.splits;
+      if (r >= rows) break;
+      float x[8], y[8];
+      if (r < Hq) {
+        if (turns) {
+          unpack8(w[i][0], x);
+          unpack8(w[i][1], y);
+          turn8(cs, a.plan.adjacent, x, y);
+          w[i][0] = pack8(x);
+          w[i][1] = pack8(y);
+        }
+        if (real) {
+          uint16_t* dst = a.q_out + (size_t)t * a.q_out_stride + r * D;
+          store_runs(dst, lo, hi, p.wide_out, w[i]);
+        }
+        continue;
+      }
+      const bool key = r < Hq + Hk;
+      const int h = r - Hq - (key ? 0 : Hk), at0 = key ? lo : 16 * u, at1 = key ? hi : 16 * u + 8;
+      unpack8(w[i][0], x);
+      unpack8(w[i][1], y);
+      if (key && turns) turn8(cs, a.plan.adjacent, x, y);
+      const float gs = key ? a.cache.k_gs : a.cache.v_gs;
+      float mx = amax8(x), my = amax8(y);
+      if (mx != mx || my != my) {   // a NaN has no code: stored as 0
+        no_nan(x);
+        no_nan(y);
+        mx = amax8(x);
+        my = amax8(y);
+      }
+      // Halves: two neighbouring lanes have the two runs of a group of sixteen.
+      const float ox = __shfl_xor_sync(0xffffffffu, mx, 1), oy = __shfl_xor_sync(0xffffffffu, my, 1);
+      const bool split = key && turns && !a.plan.adjacent;
+      if (split) {
+        mx = fmaxf(mx, ox);
+        my = fmaxf(my, oy);
+      } else {
+        mx = my = fmaxf(mx, my);
+      }
+      if (!keep) continue;
+      const Scale sx = scale_of(mx, gs), sy = split ? scale_of(my, gs) : sx;
+      uint8_t* const blk = block_of(h) + (key ? 0 : L::kValueCodes);
+      *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at0 / 2) = codes8(x, sx.r);
+      *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at1 / 2) = codes8(y, sy.r);
+      uint8_t* const scales = blk + L::kKeyScales + row * L::kScaleRow;
+      if (!split) {
+        scales[u] = (uint8_t)sx.code;
+      } else if (u % 2 == 0) {
+        scales[at0 / 16] = (uint8_t)sx.code;
+        scales[at1 / 16] = (uint8_t)sy.code;
+      }
     }
   }
 }
@@ -331,12 +381,15 @@ moe_status launch_rope(const moe_rope_args& args, cudaStream_t s) {
   p.a = a;
   p.turning = a.plan.rotary_dim / per;
   p.units = p.turning + (in_place ? 0 : (rest + per - 1) / per);
+  auto sectors = [](const void* x, long long stride) { return reinterpret_cast<uintptr_t>(x) % 32 == 0 && stride % 16 == 0; };
+  const bool wide_units = vectors && a.plan.adjacent && a.head_dim % 16 == 0 && sectors(a.q, a.q_stride) && sectors(a.k, a.k_stride) &&
+           sectors(a.q_out, a.q_out_stride) && sectors(a.k_out, a.k_out_stride);
   const int heads = a.q_heads + a.k_heads;
   p.splits = head_splits((long long)a.tokens * p.units, heads);
   const long long per_token = (long long)p.splits * p.units;
   if (a.tokens > (1ll << 31) / per_token) return MOE_ERR_UNSUPPORTED;   // threads are counted in 32 bits
   const unsigned grid = (unsigned)((a.tokens * per_token + kThreads - 1) / kThreads);
-  const cudaError_t e = launch_ex(true, vectors ? rope_vector_kernel : rope_pair_kernel, dim3(grid), dim3(kThreads), 0, s, p);
+  const cudaError_t e = launch_ex(true, !vectors ? rope_pair_kernel : wide_units ? rope_vector_kernel<true> : rope_vector_kernel<false>, dim3(grid), dim3(kThreads), 0, s, p);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
   return MOE_OK;
@@ -348,11 +401,17 @@ moe_status launch_kv4_append_rope(const moe_kv4_append_rope_args& a, cudaStream_
   p.page_log = __builtin_ctz(a.cache.page_tokens);
   const int D = a.cache.head_dim, rows = a.q_heads + 2 * a.cache.kv_heads, tokens = 512 / D;
   const long long runs = ((long long)a.tokens + tokens - 1) / tokens;
-  p.splits = head_splits(runs * 32, rows);
-  const long long grid = (runs * p.splits + kThreads / 32 - 1) / (kThreads / 32);
-  if (grid > 0x7fffffffll / 8) return MOE_ERR_UNSUPPORTED;   // warps are counted in 32 bits
+  // A warp for each few rows, at least a CTA's eight where there are that many rows.
+  constexpr int kWarps = kThreads / 32;
+  const int least = rows < kWarps ? rows : kWarps, want = head_splits(runs * 32, rows);
+  p.splits = want < least ? least : want;
+  const int warps = p.splits < kWarps ? p.splits : kWarps, ctas = (p.splits + warps - 1) / warps;
+  p.splits = warps * ctas;
+  auto sectors = [](const void* x, long long stride) { return reinterpret_cast<uintptr_t>(x) % 32 == 0 && stride % 16 == 0; };
+  p.wide_in = sectors(a.q, a.q_stride) && sectors(a.k, a.k_stride) && sectors(a.v, a.v_stride);
+  p.wide_out = a.plan.adjacent && sectors(a.q_out, a.q_out_stride);
   const cudaError_t e = launch_ex(true, D == 64 ? kv4_append_rope_kernel<64> : kv4_append_rope_kernel<128>,
-                                  dim3((unsigned)grid), dim3(kThreads), 0, s, p);
+                                  dim3((unsigned)runs, ctas), dim3(warps * 32), 0, s, p);
   if (e != cudaSuccess) return cuda_ok(e);
   count_launches(1);
   return MOE_OK;
