@@ -482,7 +482,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
         const int low = a.causal ? rq.kv - rq.n : rq.kv - 1;   // the first row's last token
         plain1 = low + 1;
         plain0 = a.window > 0 ? rq.kv - a.window : 0;
-        start_rows<D, NT>(st, a.scale, a.cache.k_gs, [&](int row) {
+        start_rows<D, NT>(st, g8, t4, a.scale, a.cache.k_gs, [&](int row) {
           return row < rq.n * group
                      ? a.q + (size_t)(rq.row0 + row / group) * a.q_stride + (h * group + row % group) * D
                      : nullptr;
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_decode_kernel(c
       auto work = [&](auto with_mask, const uint8_t* part, int tok0, int valid) {
         constexpr bool kMask = decltype(with_mask)::value;
         const int recip = kMask ? (65535 + group) / group : 0;
-        attend_blocks<D, NT, kPart, kMask>(st, part, [&](int blk, int nt, int i) {
+        attend_blocks<D, NT, kPart, kMask>(st, g8, t4, part, [&](int blk, int nt, int i) {
           const int tok = tok0 + blk * kKvBlock + token_of(g8) + 8 * (i >> 1);
           // the last token its query sees; row / group by the reciprocal (both at most 16)
           const int token = (nt * 8 + 2 * t4 + (i & 1)) * recip >> 16;

@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
           if (r0 + i < r1) issue(r0 + i, i);
           cp_async_commit();
         }
-        start_rows<D, NT>(st, a.scale, a.cache.k_gs, [&](int row) {
+        start_rows<D, NT>(st, g8, t4, a.scale, a.cache.k_gs, [&](int row) {
           return row < used ? a.q + (size_t)(t + row / heads) * a.q_stride + (h * heads + row % heads) * D : nullptr;
         });
         int next = r0 + min(S, r1 - r0), slot = 0;
@@ -238,7 +238,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
           auto work = [&](auto with_mask, int blk0) {
             constexpr bool kMask = decltype(with_mask)::value;
             const int recip = kMask ? (65535 + heads) / heads : 0;
-            attend_blocks<D, NT, kPart, kMask>(st, stage + blk0 * L::kBytes, [&](int b, int nt, int i) {
+            attend_blocks<D, NT, kPart, kMask>(st, g8, t4, stage + blk0 * L::kBytes, [&](int b, int nt, int i) {
               const int blk = blk0 + b, half = blk / (NB / 2);
               const int tok = (half ? tok1 : tok0) + blk % (NB / 2) * kKvBlock + token_of(g8) + 8 * (i >> 1);
               const int row = (nt * 8 + 2 * t4 + (i & 1)) * recip >> 16;   // row / heads (both at most 16)
