@@ -26,6 +26,7 @@ using namespace rows;
 using namespace tc;
 
 constexpr int kListMax = 256;   // entries of a unit's lists: tile * top
+constexpr int kRawMax = kListMax + 3 * 8;   // with places of whole 16 bytes each, of up to 8 tokens
 
 struct SparseArgs {
   moe_kv4_sparse_args a;
@@ -53,7 +54,7 @@ struct Smem {
   using Sh = Shape<D, NT>;
   alignas(128) uint8_t ring[Sh::kWarps][Sh::kStages][Sh::kStageBytes];
   uint16_t list[Sh::kWarps][kListMax];   // the union: place in the lists, and rows (high byte)
-  static_assert(Sh::kStageBytes >= kListMax * 4, "the lists fit a stage");
+  static_assert(Sh::kStageBytes >= kRawMax * 4, "the lists fit a stage");
   static_assert(Sh::kStages * Sh::kStageBytes >= 2 * Slots<D, NT>::kFloats * 4, "a ring holds two partials");
 };
 
@@ -131,27 +132,41 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
       const size_t row_stride = (size_t)Hk * a.top;              // of blocks
 
       // ------------------------------------------- the union of the lists
+      // The rows are asked for now: they would wait behind all the tiles in flight.
+      for (int i = 0; i < nrow; ++i)
+        if (lane * 128 < heads * D * 2)
+          asm volatile("prefetch.global.L1 [%0];" ::"l"(
+              reinterpret_cast<const char*>(a.q + (size_t)(t + i) * a.q_stride + (size_t)h * heads * D) + lane * 128));
+      // A list has places of whole 16 bytes; -1: nothing. An entry is in the union where its list has it first.
       int* const raw = reinterpret_cast<int*>(ring);
-      const int entries = nrow * a.top;
+      const int places = (a.top + 3) & ~3, entries = nrow * places;
       for (int e = lane; e < entries; e += 32) {
-        const int i = e / a.top, x = __ldg(blocks + i * row_stride + e - i * a.top), pos = pos0 + i;
+        const int i = e / places, k = e - i * places, x = k < a.top ? __ldg(blocks + i * row_stride + k) : -1, pos = pos0 + i;
         raw[e] = x >= 0 && pos >= 0 && x <= pos >> p.block_log ? x : -1;
       }
       __syncwarp();
       int count = 0;
+#pragma unroll 1
       for (int e0 = 0; e0 < entries; e0 += 32) {
         const int e = e0 + lane, x = e < entries ? raw[e] : -1;
         unsigned mask = 0;
-        bool first = x >= 0;
+        int first = e;
+#pragma unroll 1
         for (int i = 0, j = 0; i < nrow; ++i)
-          for (int k = 0; k < a.top; ++k, ++j)
-            if (raw[j] == x) {
+#pragma unroll 2
+          for (int k = 0; k < places; k += 4, j += 4) {
+            const int4 y = *reinterpret_cast<const int4*>(raw + j);
+            const unsigned same = (y.x == x) | (y.y == x) << 1 | (y.z == x) << 2 | (y.w == x) << 3;
+            if (same) {
               mask |= 1u << i;
-              first &= j >= e;
+              first = min(first, j + __ffs(same) - 1);
             }
-        const unsigned keep = __ballot_sync(kFull, first);
-        if (first) list[count + __popc(keep & ((1u << lane) - 1))] = (uint16_t)(e | mask << 8);
-        count += __popc(keep);
+          }
+        const bool keep = x >= 0 && first == e;
+        const unsigned kept = __ballot_sync(kFull, keep);
+        // its token, its place in the list, the tokens that take it
+        if (keep) list[count + __popc(kept & ((1u << lane) - 1))] = (uint16_t)(e / places * a.top + e % places | mask << 8);
+        count += __popc(kept);
       }
       __syncwarp();
 
@@ -169,7 +184,8 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
         // tokens and rows, and a place for each 16-token block.
         int d_tok[2] = {0, 0}, d_rows = 0, d_valid = 0, base = r0;
         const uint8_t* d_src[NB];
-        auto describe = [&](int from) {
+        // (fresh: the lists are still where the union was built)
+        auto describe = [&](int from, bool fresh) {
           base = from;
           d_valid = d_rows = 0;
           d_tok[0] = d_tok[1] = 0;
@@ -182,7 +198,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
             const int sub = tile * NB + half * (NB / 2), at = sub >> sub_log;
             if (at >= count) break;
             const int code = list[at], e = code & 0xff, i = e / a.top;
-            const int blk = __ldg(blocks + i * row_stride + e - i * a.top);
+            const int blk = fresh ? raw[i * places + e - i * a.top] : __ldg(blocks + i * row_stride + e - i * a.top);
             d_tok[half] = (blk << p.block_log) + (sub - (at << sub_log)) * kKvBlock;
             d_rows |= code >> 8 << (8 * half);
 #pragma unroll
@@ -215,7 +231,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
           }
         };
 
-        describe(r0);
+        describe(r0, true);
         __syncwarp();
 #pragma unroll 1
         for (int i = 0; i < S; ++i) {
@@ -252,7 +268,7 @@ __global__ void __launch_bounds__(Shape<D, NT>::kThreads, 1) kv4_sparse_kernel(c
           }
           __syncwarp();   // every lane has read the stage
           if (next < r1) {
-            if (next - base >= 32) describe(tile + 1);
+            if (next - base >= 32) describe(tile + 1, false);
             __syncwarp();
             issue(next, slot);
             ++next;
