@@ -48,7 +48,7 @@ moe_status launch_kv4_select(const moe_kv4_select_args& a, cudaStream_t s);
 moe_status launch_kv4_sparse(const moe_kv4_sparse_args& a, cudaStream_t s);
 // Sparse attention of requests with more than min_tokens query rows.
 moe_status launch_kv4_sparse_prompt(const moe_kv4_sparse_args& a, int min_tokens, cudaStream_t s);
-constexpr int kSparseFewTokens = 16;
+constexpr int kSparseFewTokens = 24, kSparseManyUnits = 96;
 constexpr int kSparseTop = 64, kSparseGroup = 16;   // blocks of a query, query heads of a key/value head
 
 // Attention of requests with up to max_rows (at most kKvDecodeRows) query rows

@@ -32,7 +32,7 @@ using namespace tc;
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kFewRows = 8;
+constexpr int kFewRows = 8, kManyRows = 640;
 
 // A float's bits in the order of its value (0 is below every key of a number).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -427,18 +427,14 @@ static_assert(kList % 16 == 0, "lists are read 16 entries at a time");
 constexpr int kMostBlocks = 65536;   // list entries name blocks in 16 bits
 constexpr long long kWaitLimit = 2ll * 1000 * 1000 * 1000;   // cycles (about 1 s)
 
-struct Segment {
-  int b, end;     // request; the last row's c1
-};
-
 template <int D>
 struct ManySmem {
   alignas(1024) uint8_t ring[kStages][kCols * D * 2];
   float score[kList + 1][kTile];
   uint16_t blk[kList + 1][kTile];
-  Segment seg[kTile];
-  int owner[kTile + 2];          // of rows -1 .. kTile
-  int segments, abort;
+  int warp_sum[kManyThreads / 32];
+  int request, tile;             // what this CTA has: request, run of kTile of its rows
+  int abort;
   uint32_t tmem;
   uint64_t full[kStages], empty[kStages], scored[2], read[2], rows_in, drained;
 };
@@ -522,7 +518,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
   const moe_kv4_cache& c = a.index.cache;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int Hk = c.kv_heads, heads = a.q_heads / Hk, page_log = __ffs(c.page_tokens) - 1;
-  const int t0 = blockIdx.x / Hk * kTile, h = blockIdx.x % Hk;
+  const int h = blockIdx.x % Hk, cap = a.max_pages * c.page_tokens;
   pdl_wait();
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -535,55 +531,79 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     }
     mbar_init(&sm.rows_in, kTile);
     mbar_init(&sm.drained, 1);
-    sm.segments = 0;
+    sm.request = -1;
     sm.abort = 0;
     fence_barrier_init();
   }
   // ------------------------------------------------- whose rows these are
-  RowOwner own = {-1, 0, 0, 0, false};
+  // The CTA's place among the runs of all requests that are this kernel's, by a scan over the lengths.
+  int carry = blockIdx.x / Hk;   // runs before the CTA's, of this request and the ones after it
+  for (int b0 = 0; b0 < a.batch && carry >= 0; b0 += kManyThreads) {
+    int runs = 0;
+    if (b0 + tid < a.batch) {
+      const RowOwner r = request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, cap, b0 + tid);
+      if (r.bad && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+      if (r.b >= 0 && r.n > kFewRows) runs = (r.n + kTile - 1) / kTile;
+    }
+    int incl = runs;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += x;
+    }
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    int all = 0;
+#pragma unroll
+    for (int w = 0; w < kManyThreads / 32; ++w) {
+      const int x = sm.warp_sum[w];
+      if (w < warp) incl += x;
+      all += x;
+    }
+    if (incl > carry && incl - runs <= carry) {
+      sm.request = b0 + tid;
+      sm.tile = carry - (incl - runs);
+    }
+    carry -= all;
+    __syncthreads();
+  }
+  if (sm.request < 0) return;
+  const RowOwner own = request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, cap, sm.request);
+  const int t0 = own.c0 + sm.tile * kTile, rows = min(kTile, own.c0 + own.n - t0);
+  const int pos0 = own.kv - own.n + t0 - own.c0;       // the first row's position
+  const int32_t* const table = a.block_table + (size_t)own.b * a.max_pages;
+  // The last row ranks most blocks; where it ranks none, no row does.
+  const Visible last = visible(a, p.block_log, pos0 + rows - 1);
+  const int end = last.need > 0 ? last.c1 : 0;
+  auto ranks = [&](int r) { return r < rows && visible(a, p.block_log, pos0 + r).need > 0; };
   Visible v = {0, 0, 0, 0};
   const int t = t0 + tid;
-  if (tid < kTile) {
-    if (t < a.total_q) own = row_owner_thread(a.cu_q, a.kv_len, a.batch, a.total_q, a.max_q, a.max_pages * c.page_tokens, t);
-    if (own.bad && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-    if (own.b >= 0 && own.n <= kFewRows) own.b = -1;   // the other kernel's
+  if (tid < rows) {
     int32_t* const out = a.blocks + ((size_t)t * Hk + h) * a.top;
-    if (own.b >= 0) {
-      v = visible(a, p.block_log, own.kv - own.n + t - own.c0);
-      if (v.seen <= a.top) {
-        for (int i = 0; i < a.top; ++i) out[i] = i < v.seen ? i : -1;
-      } else {
-        for (int i = 0; i < a.sink; ++i) out[i] = i;
-        for (int i = 0; i < a.local; ++i) out[a.top - a.local + i] = v.c1 + i;
-      }
+    v = visible(a, p.block_log, pos0 + tid);
+    if (v.seen <= a.top) {
+      for (int i = 0; i < a.top; ++i) out[i] = i < v.seen ? i : -1;
+    } else {
+      for (int i = 0; i < a.sink; ++i) out[i] = i;
+      for (int i = 0; i < a.local; ++i) out[a.top - a.local + i] = v.c1 + i;
     }
-    sm.owner[tid + 1] = v.need > 0 ? own.b : -1;
-    if (tid == 0) sm.owner[0] = -1, sm.owner[kTile + 1] = -1;
   }
-  __syncthreads();
-  // Rows that rank blocks, as runs of one request; a later row of a run ends later.
-  if (tid < kTile && v.need > 0 && sm.owner[tid + 2] != own.b) {
-    int k = 0;   // runs that end before this one
-    for (int i = 0; i < tid; ++i) k += sm.owner[i + 1] >= 0 && sm.owner[i + 2] != sm.owner[i + 1];
-    sm.seg[k] = {own.b, v.c1};
-    atomicAdd(&sm.segments, 1);
-  }
+  if (last.need == 0) return;
   if (warp == 8) tmem_alloc(&sm.tmem, kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm.tmem;               // scores in columns 0..127 (two tiles), u in the D / 2 after 128
   volatile int* const abort = &sm.abort;
-  const int segments = sm.segments;
 
   // ----------------------------------------------- the rows of u, a row a warp
   constexpr int kRowLanes = D / 8, kPasses = 32 / kRowLanes;   // lanes of a head's row, heads at once
   constexpr int kPad = D * 2 + 16;                              // bytes of a row of u on its way to tensor memory
   static_assert(kPad * kTile <= (int)sizeof(sm.score), "u passes through the lists");
   uint8_t* const rows_of_u = reinterpret_cast<uint8_t*>(sm.score);
-  if (segments > 0 && warp < 8) {
+  if (warp < 8) {
     // kHeads of a lane at most, kRowsAtOnce rows asked for together
-    auto rows = [&](auto heads_of_lane, auto rows_at_once) {
+    auto work_out = [&](auto heads_of_lane, auto rows_at_once) {
       constexpr int kHeads = decltype(heads_of_lane)::value, kAtOnce = decltype(rows_at_once)::value;
       const int part = lane % kRowLanes, g0 = lane / kRowLanes;
 #pragma unroll 1
@@ -594,7 +614,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
 #pragma unroll
           for (int i = 0; i < kHeads; ++i) {
             const int g = g0 + i * kPasses;
-            x[b][i] = g < heads && sm.owner[r0 + b + 1] >= 0
+            x[b][i] = g < heads && ranks(r0 + b)
                           ? __ldg(reinterpret_cast<const uint4*>(a.q + (size_t)(t0 + r0 + b) * a.q_stride +
                                                                  (size_t)(h * heads + g) * D + part * 8))
                           : make_uint4(0u, 0u, 0u, 0u);
@@ -646,12 +666,12 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
       }
     };
     // as many rows as 32 registers hold
-    if (heads <= 2 * kPasses) rows(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
-    else rows(std::integral_constant<int, kSparseGroup / kPasses>{}, std::integral_constant<int, kPasses / 2>{});
+    if (heads <= 2 * kPasses) work_out(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{});
+    else work_out(std::integral_constant<int, kSparseGroup / kPasses>{}, std::integral_constant<int, kPasses / 2>{});
   }
   __syncthreads();
 
-  if (segments > 0 && warp < 4) {
+  if (warp < 4) {
     // ------------------------------------------------------------- queries
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
 #pragma unroll
@@ -673,42 +693,39 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     List<Sm> list = {sm, tid, 0, -INFINITY, -INFINITY};
     int tile = 0;
     bool ok = true;
-    for (int sg = 0; sg < segments && ok; ++sg) {
-      const Segment seg = sm.seg[sg];
-      const int c1 = v.need > 0 && own.b == seg.b ? v.c1 : 0;
-      for (int j0 = a.sink; j0 < seg.end; j0 += kCols, ++tile) {
-        const int buf = tile & 1;
-        ok = __all_sync(kFull, mbar_wait(&sm.scored[buf], tile >> 1 & 1, abort, kWaitLimit));
-        if (!ok) break;
-        tc_fence_after();
+    const int c1 = v.need > 0 ? v.c1 : 0;
+    for (int j0 = a.sink; j0 < end; j0 += kCols, ++tile) {
+      const int buf = tile & 1;
+      ok = __all_sync(kFull, mbar_wait(&sm.scored[buf], tile >> 1 & 1, abort, kWaitLimit));
+      if (!ok) break;
+      tc_fence_after();
 #pragma unroll 1
-        for (int g = 0; g < kCols / kGroup; ++g) {
-          uint32_t r[kGroup];
-          tmem_ld32(tmem + lanes + buf * kCols + g * kGroup, r);
-          tmem_ld_wait();
-          if (g == kCols / kGroup - 1) {
-            tc_fence_before();
-            mbar_arrive(&sm.read[buf]);
-          }
-          const int j = j0 + g * kGroup, n = min(kGroup, c1 - j);   // this row's blocks of the group
-          // Every score is written behind the list, and stays if it is above: a branch for each column costs six times
-          // as much.
-          const bool whole = __all_sync(kFull, n >= kGroup);
-          if (!whole)
-#pragma unroll
-            for (int i = 0; i < kGroup; ++i)
-              if (i >= n) r[i] = 0xff800000u;   // below every bound
-#pragma unroll
-          for (int i = 0; i < kGroup; ++i) {
-            const float s = finite_score(__uint_as_float(r[i]));
-            sm.score[list.cnt][tid] = s;
-            sm.blk[list.cnt][tid] = (uint16_t)(j + i);
-            list.cnt += s > list.bound && (whole || i < n);
-            list.top = fmaxf(list.top, s);
-          }
-          // One list too long: every list is cut that is much longer than it has to be.
-          if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, min(kKeep, v.need + v.need / 2 + 8));
+      for (int g = 0; g < kCols / kGroup; ++g) {
+        uint32_t r[kGroup];
+        tmem_ld32(tmem + lanes + buf * kCols + g * kGroup, r);
+        tmem_ld_wait();
+        if (g == kCols / kGroup - 1) {
+          tc_fence_before();
+          mbar_arrive(&sm.read[buf]);
         }
+        const int j = j0 + g * kGroup, n = min(kGroup, c1 - j);   // this row's blocks of the group
+        // Every score is written behind the list, and stays if it is above: a branch for each column costs six times
+        // as much.
+        const bool whole = __all_sync(kFull, n >= kGroup);
+        if (!whole)
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i)
+            if (i >= n) r[i] = 0xff800000u;   // below every bound
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          const float s = finite_score(__uint_as_float(r[i]));
+          sm.score[list.cnt][tid] = s;
+          sm.blk[list.cnt][tid] = (uint16_t)(j + i);
+          list.cnt += s > list.bound && (whole || i < n);
+          list.top = fmaxf(list.top, s);
+        }
+        // One list too long: every list is cut that is much longer than it has to be.
+        if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, min(kKeep, v.need + v.need / 2 + 8));
       }
     }
     // ------------------------------------------------- the best, in order
@@ -717,46 +734,42 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
       int32_t* const out = a.blocks + ((size_t)t * Hk + h) * a.top + a.sink;
       for (int i = 0; i < v.need; ++i) out[i] = ok && i < list.cnt ? sm.blk[i][tid] : -1;
     }
-  } else if (segments > 0 && warp < 8) {
+  } else if (warp < 8) {
     // --------------------------------------------------------------- means
     constexpr int kChunks = D / 8, kPerThread = kCols * kChunks / 128;   // 16-byte pieces of a row, of a thread
     int tile = 0, done = 0;
     bool ok = true;
-    for (int sg = 0; sg < segments && ok; ++sg) {
-      const Segment seg = sm.seg[sg];
-      const int32_t* const table = a.block_table + (size_t)seg.b * a.max_pages;
-      for (int j0 = a.sink; j0 < seg.end; j0 += kCols, ++tile) {
-        const int stage = tile % kStages;
-        // the table's entries first: they do not wait for the stage
-        int entry[kPerThread];
+    for (int j0 = a.sink; j0 < end; j0 += kCols, ++tile) {
+      const int stage = tile % kStages;
+      // the table's entries first: they do not wait for the stage
+      int entry[kPerThread];
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-          const int j = j0 + ((tid - 128) + 128 * i) / kChunks;
-          entry[i] = j < seg.end ? entry_of(a.index, page_log, p.block_log, table, j) : -2;
-        }
-        ok = __all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, kWaitLimit));
-        if (!ok) break;
-        const uint32_t dst = smem_u32(sm.ring[stage]);
+      for (int i = 0; i < kPerThread; ++i) {
+        const int j = j0 + ((tid - 128) + 128 * i) / kChunks;
+        entry[i] = j < end ? entry_of(a.index, page_log, p.block_log, table, j) : -2;
+      }
+      ok = __all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, kWaitLimit));
+      if (!ok) break;
+      const uint32_t dst = smem_u32(sm.ring[stage]);
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) {
-          const int idx = tid - 128 + 128 * i, row = idx / kChunks, ch = idx % kChunks;
-          // K halves of 64 elements one after the other, rows of 128 bytes
-          const uint32_t at = (uint32_t)(ch / 8 * (kCols * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-          if (entry[i] == -1) {   // a page that is not in the pool: a row of NaN, which no mean is
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at), "r"(0x7e007e00u) : "memory");
-            if (a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-          } else {
-            const uint16_t* src = a.index.means + ((size_t)max(entry[i], 0) * Hk + h) * D + ch * 8;
-            cp_async_16(dst + at, src, entry[i] >= 0 ? 16u : 0u);
-          }
+      for (int i = 0; i < kPerThread; ++i) {
+        const int idx = tid - 128 + 128 * i, row = idx / kChunks, ch = idx % kChunks;
+        // K halves of 64 elements one after the other, rows of 128 bytes
+        const uint32_t at = (uint32_t)(ch / 8 * (kCols * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
+        if (entry[i] == -1) {   // a page that is not in the pool: a row of NaN, which no mean is
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at), "r"(0x7e007e00u) : "memory");
+          if (a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+        } else {
+          const uint16_t* src = a.index.means + ((size_t)max(entry[i], 0) * Hk + h) * D + ch * 8;
+          cp_async_16(dst + at, src, entry[i] >= 0 ? 16u : 0u);
         }
-        cp_async_commit();
-        if (tile > done) {     // the stage before this one is in
-          cp_async_wait<1>();
-          fence_proxy_async_smem();
-          mbar_arrive(&sm.full[done % kStages]);
-          ++done;
-        }
+      }
+      cp_async_commit();
+      if (tile > done) {     // the stage before this one is in
+        cp_async_wait<1>();
+        fence_proxy_async_smem();
+        mbar_arrive(&sm.full[done % kStages]);
+        ++done;
       }
     }
     cp_async_wait_all();
@@ -764,28 +777,25 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
       fence_proxy_async_smem();
       mbar_arrive(&sm.full[done % kStages]);
     }
-  } else if (segments > 0 && lane == 0) {
+  } else if (lane == 0) {
     // ------------------------------------------------------------ products
     constexpr uint32_t idesc = idesc_f16(kTile, kCols, 0);
     int tile = 0;
     bool ok = mbar_wait(&sm.rows_in, 0, abort, kWaitLimit);
     tc_fence_after();
-    for (int sg = 0; sg < segments && ok; ++sg) {
-      const Segment seg = sm.seg[sg];
-      for (int j0 = a.sink; j0 < seg.end; j0 += kCols, ++tile) {
-        const int buf = tile & 1, stage = tile % kStages;
-        ok = mbar_wait(&sm.full[stage], tile / kStages & 1, abort, kWaitLimit) &&
-             mbar_wait(&sm.read[buf], (tile >> 1 & 1) ^ 1, abort, kWaitLimit);
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t src = smem_u32(sm.ring[stage]);
+    for (int j0 = a.sink; j0 < end && ok; j0 += kCols, ++tile) {
+      const int buf = tile & 1, stage = tile % kStages;
+      ok = mbar_wait(&sm.full[stage], tile / kStages & 1, abort, kWaitLimit) &&
+           mbar_wait(&sm.read[buf], (tile >> 1 & 1) ^ 1, abort, kWaitLimit);
+      if (!ok) break;
+      tc_fence_after();
+      const uint32_t src = smem_u32(sm.ring[stage]);
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k)
-          mma_f16_tmem_a(tmem + buf * kCols, tmem + 128 + k * 8,
-                         smem_desc(src + k / 4 * (kCols * 128) + k % 4 * 32, 16, 1024, kSwizzle128B), idesc, k != 0);
-        tc_commit(&sm.empty[stage]);
-        tc_commit(&sm.scored[buf]);
-      }
+      for (int k = 0; k < D / 16; ++k)
+        mma_f16_tmem_a(tmem + buf * kCols, tmem + 128 + k * 8,
+                       smem_desc(src + k / 4 * (kCols * 128) + k % 4 * 32, 16, 1024, kSwizzle128B), idesc, k != 0);
+      tc_commit(&sm.empty[stage]);
+      tc_commit(&sm.scored[buf]);
     }
     // What was issued is complete before tensor memory is given back (also after a wait that gave up).
     tc_commit(&sm.drained);
@@ -827,7 +837,9 @@ cudaError_t launch_many(const SelectArgs& p, cudaStream_t s) {
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = opt_in_smem(kv4_select_many_kernel<D>, smem, done);
   if (e != cudaSuccess) return e;
-  const unsigned tiles = (unsigned)(((long long)p.a.total_q + kTile - 1) / kTile);
+  // as many runs of kTile rows as the requests can have: each but its last is full, and holds more than kFewRows
+  const long long full = p.a.total_q / kTile, part = p.a.total_q / (kFewRows + 1);
+  const unsigned tiles = (unsigned)(full + (part < p.a.batch ? part : p.a.batch));
   return launch_ex(true, kv4_select_many_kernel<D>, dim3(tiles * p.a.index.cache.kv_heads), dim3(kManyThreads), smem, s, p);
 }
 
@@ -842,8 +854,10 @@ moe_status launch_kv4_select(const moe_kv4_select_args& a, cudaStream_t s) {
   // kFewRows rows launches both kernels, each skipping the other's. A CTA of
   // the first then has all rows of a request, as most requests will have one.
   const bool long_lists = ((long long)a.max_pages * a.index.cache.page_tokens >> p.block_log) > kMostBlocks;
-  const bool many = a.max_q > kFewRows && !long_lists;
-  p.rows = long_lists && a.max_q > kFewRows ? 0 : many ? 1 : a.max_q;
+  // A few rows go faster without it (us for 64 and 128 rows of 8 heads over 1024 blocks: 41 and 77 by the first, 57 and
+  // 60 by the second; over 128 blocks 19 and 32, 29 and 30).
+  const bool many = a.max_q > kFewRows && (long long)a.total_q * Hk > kManyRows && !long_lists;
+  p.rows = many ? 1 : a.max_q > kFewRows ? 0 : a.max_q;
   const long long items = (p.rows == 0 ? (long long)a.total_q : (long long)a.batch * p.rows) * Hk;
   cudaError_t e = D == 64 ? launch_few<64>(p, items, s) : launch_few<128>(p, items, s);
   if (e == cudaSuccess && many) e = D == 64 ? launch_many<64>(p, s) : launch_many<128>(p, s);

@@ -406,9 +406,16 @@ moe_status launch_kv4_sparse(const moe_kv4_sparse_args& a, cudaStream_t s) {
   p.a = a;
   p.block_log = __builtin_ctz(a.block_tokens);
   const bool wide = a.q_heads / a.cache.kv_heads > 8;
-  // Lengths are on the device: a call that allows longer requests launches both
-  // kernels, each skipping the other's.
-  const bool many = a.max_q > kSparseFewTokens;
+  // Which kernel. Requests of up to kSparseFewTokens rows are this one's (16
+  // requests of 24 new tokens over 16 blocks of 64, 32/8 heads x 128: 98 us here,
+  // 114 there; of 32: 99 and 81), and all are where the other one would not
+  // have a unit for most of the SMs (one of 64: 20 and 59 us; 16 of 64 190 and
+  // 94) or a group has one head (its 32 tokens fill a quarter of the tile's rows:
+  // 16 of 32 57 and 76). Lengths are on the device: a call that allows longer
+  // requests launches both kernels, each skipping the other's.
+  const int group = a.q_heads / a.cache.kv_heads;
+  const bool many = a.max_q > kSparseFewTokens && group > 1 &&
+                    (long long)a.total_q * a.cache.kv_heads >= kSparseManyUnits * (long long)(group < 4 ? 32 : 128 / group);
   cudaError_t e;
   if (a.cache.head_dim == 64) e = wide ? launch<64, 2>(p, many, s) : launch<64, 1>(p, many, s);
   else e = wide ? launch<128, 2>(p, many, s) : launch<128, 1>(p, many, s);
