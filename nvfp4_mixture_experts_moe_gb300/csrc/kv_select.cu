@@ -123,13 +123,14 @@ struct FewSmem {
   int hist[kBins];
   int best[kSparseTop];                  // blocks that earlier chunks left, and their scores
   float best_score[kSparseTop];
-  int count[kWarps + 1];                 // of the warps
+  int taken[kCandidates], found;
   int bin, above;                        // the histogram's answer
   unsigned lowest, highest, group_top;
 };
 
-// The `need` largest of sm.score[0 .. total) to put(where, i) in order, the
-// first of equal ones; all where there are no more. By a whole CTA.
+// The `need` largest of sm.score[0 .. total) to put(where, block, score), in the
+// order of the blocks, the first of equal ones; all where there are no more. By
+// a whole CTA.
 template <class BlockOf, class Put>
 __device__ __forceinline__ void best_scores(FewSmem& sm, int total, int need, BlockOf block_of, Put put) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -199,69 +200,62 @@ __device__ __forceinline__ void best_scores(FewSmem& sm, int total, int need, Bl
       __syncthreads();
     }
   }
-  // The candidates in order, a warp a run of neighbours.
-  auto level = [&](float x) {   // 2: in, 1: perhaps
-    if (total <= need || x > hi) return 2;
-    if (x < lo) return 0;
-    if (lo == hi) return 1;
-    const int b = min((int)((0.5f * x - from) * scale), kBins - 1);
-    return b > bin ? 2 : b == bin ? 1 : 0;
-  };
+  // The candidates, in any order: what is over the bin or in it; of many equal scores the first that are needed.
   const bool ties = total > need && lo == hi;
-  const int seg = (total + kThreads - 1) / kThreads * 32, at = warp * seg, end = min(total, at + seg);
-  int mine = 0, equal = 0;
-  for (int i0 = at; i0 < end; i0 += 32) {
-    const int l = i0 + lane < end ? level(sm.score[i0 + lane]) : 0;
-    mine += __popc(__ballot_sync(kFull, l > (ties ? 1 : 0)));
-    equal += __popc(__ballot_sync(kFull, ties && l == 1));
-  }
-  if (lane == 0) sm.count[warp] = mine | equal << 16;   // at most 4159 of either
+  if (tid == 0) sm.found = 0;
   __syncthreads();
-  int w = 0, e0 = 0, n = 0;
-  for (int k = 0; k < kWarps; ++k) {
-    const int c = sm.count[k];
-    if (k < warp) w += c & 0xffff, e0 += c >> 16;
-    n += c & 0xffff;
-  }
-  // Of many equal ones only the first that are needed are taken, so that no more than kCandidates are left.
-  const int quota = need - above;
-  if (ties) {
-    w += min(e0, quota);
-    n += quota;
-  }
-  const unsigned before = (1u << lane) - 1;
-  for (int i0 = at; i0 < end; i0 += 32) {
-    const float x = i0 + lane < end ? sm.score[i0 + lane] : -INFINITY;
-    const int l = i0 + lane < end ? level(x) : 0;
-    const unsigned eq = __ballot_sync(kFull, ties && l == 1);
-    const bool take = ties ? l == 2 || (l == 1 && e0 + __popc(eq & before) < quota) : l > 0;
-    const unsigned t = __ballot_sync(kFull, take);
-    if (take) {
-      sm.cand[w + __popc(t & before)] = x;
-      sm.cand_blk[w + __popc(t & before)] = block_of(i0 + lane);
+  for (int i = tid; i < total; i += kThreads) {
+    const float x = sm.score[i];
+    bool in = total <= need || x > hi;
+    if (!in && !ties && x >= lo) in = min((int)((0.5f * x - from) * scale), kBins - 1) >= bin;
+    if (in) {
+      const int at = atomicAdd(&sm.found, 1);
+      sm.cand[at] = x;
+      sm.cand_blk[at] = block_of(i);
     }
-    w += __popc(t);
-    e0 += __popc(eq);
+  }
+  if (ties) {
+    __syncthreads();
+    if (warp == 0) {
+      int at = sm.found;
+#pragma unroll 1
+      for (int i0 = 0; i0 < total && at < need; i0 += 32) {
+        const bool equal = i0 + lane < total && sm.score[i0 + lane] == lo;
+        const unsigned e = __ballot_sync(kFull, equal);
+        const int mine = at + __popc(e & ((1u << lane) - 1));
+        if (equal && mine < need) {
+          sm.cand[mine] = lo;
+          sm.cand_blk[mine] = block_of(i0 + lane);
+        }
+        at += __popc(e);
+      }
+      __syncwarp();
+      if (lane == 0) sm.found = min(at, need);
+    }
   }
   __syncthreads();
-  // Who is among the best, and how many of those come first.
+  // Who is among the best, and then how many of those are blocks before one's own.
+  const int n = sm.found;
   bool in = false;
-  if (tid < kCandidates) {
-    const float x = tid < n ? sm.cand[tid] : 0.0f;
+  int blk = 0;
+  if (tid < n) {
+    const float x = sm.cand[tid];
+    blk = sm.cand_blk[tid];
     int over = 0;
+#pragma unroll 4
     for (int j = 0; j < n; ++j) {
       const float y = sm.cand[j];
-      over += y > x || (y == x && j < tid);
+      over += y > x || (y == x && sm.cand_blk[j] < blk);
     }
-    in = tid < n && over < need;
-    const unsigned t = __ballot_sync(kFull, in);
-    if (lane == 0) sm.count[warp] = __popc(t);
-    w = __popc(t & before);
+    in = over < need;
+    sm.taken[tid] = in ? blk : 0x7fffffff;
   }
   __syncthreads();
   if (in) {
-    for (int k = 0; k < warp; ++k) w += sm.count[k];
-    put(w, tid);
+    int where = 0;
+#pragma unroll 4
+    for (int j = 0; j < n; ++j) where += sm.taken[j] < blk;
+    put(where, blk, sm.cand[tid]);
   }
 }
 
@@ -378,9 +372,9 @@ __device__ __forceinline__ void select_row(const SelectArgs& p, const RowOwner& 
     if (rank == 0)
       best_scores(sm, carried + n, v.need,
                   [&](int i) { return i < carried ? sm.best[i] : from + i - carried; },
-                  [&](int where, int i) {
-                    if (last) out[a.sink + where] = sm.cand_blk[i];
-                    else sm.best[where] = sm.cand_blk[i], sm.best_score[where] = sm.cand[i];
+                  [&](int where, int blk, float score) {
+                    if (last) out[a.sink + where] = blk;
+                    else sm.best[where] = blk, sm.best_score[where] = score;
                   });
     carried = min(carried + n, v.need);
     if (tid == 0) sm.lowest = 0xffffffffu, sm.highest = 0;
