@@ -273,9 +273,9 @@ typedef struct {
  * alignment and rotary_dim a multiple of 16 are moved in vectors.
  * Errors: NULL pointers (k may be with k_heads = 0), an odd or too small or too
  * large rotary_dim, axes outside 1..4, a non-finite scale, strides smaller
- * than a row, outputs that overlap -> MOE_ERR_INVALID_ARG; head_dim > 512 or
- * more than 65536 heads -> MOE_ERR_UNSUPPORTED. tokens = 0 -> MOE_OK. A pair
- * whose axis is not below `axes` goes by the last one.
+ * than a row, outputs that overlap -> MOE_ERR_INVALID_ARG; head_dim > 512, more
+ * than 65536 heads or 2^32 elements -> MOE_ERR_UNSUPPORTED. tokens = 0 ->
+ * MOE_OK. A pair whose axis is not below `axes` goes by the last one.
  */
 typedef struct {
   moe_rope_plan plan;
@@ -299,8 +299,8 @@ moe_status moe_rope(const moe_rope_args* args, moe_stream_t stream);
  * a NaN, or one that turns infinities into a NaN, is stored as 0. A token with
  * a negative slot (or one past the pool, which is reported) is not stored; its
  * query is turned all the same.
- * Limits: the cache's; rotary_dim a multiple of 32 (adjacent: of 16) and at
- * most head_dim, else MOE_ERR_UNSUPPORTED. q_heads may be 0 (q, q_out NULL).
+ * Limits: the cache's; rotary_dim a multiple of 32 (adjacent: of 16), at most
+ * 2^30 tokens, else MOE_ERR_UNSUPPORTED. q_heads may be 0 (q, q_out NULL).
  * Errors: moe_kv4_append's and moe_rope's; q, q_out 16-byte aligned with
  * strides that are multiples of 8.
  */
@@ -377,7 +377,7 @@ moe_status moe_kv4_index_update(const moe_kv4_index* index, int batch, int max_q
  *
  * blocks  int32 [total_q, kv_heads, top], ascending, -1 in the places that are left; rows no request owns are left alone
  * Others as in moe_kv4_attention (which has the contract of bad device data: a
- * page id outside the pool scores like -infinity).
+ * page id outside the pool scores lowest, as does a mean that is NaN).
  * Limits: 1 <= top <= 64, sink + local <= top, local >= 1, groups of up to 16
  * query heads, a context of up to 2^28 tokens.
  * Errors: as moe_kv4_attention and moe_kv4_index_update; sink, local or top
@@ -398,7 +398,11 @@ typedef struct {
 
 moe_status moe_kv4_select(const moe_kv4_select_args* args, moe_stream_t stream);
 
-/* Attention as moe_kv4_attention's, causal, over the tokens of the listed
+/* (In selection and sparse attention of requests with many rows, waits are
+ * bounded: one that gave up is reported as MOE_ERR_TIMEOUT in device_status, the
+ * rows are then not valid.)
+ *
+ * Attention as moe_kv4_attention's, causal, over the tokens of the listed
  * blocks up to the query's position. The entries of a list may come in any
  * order; one that is negative or past the query's position is skipped, one
  * listed twice counts once. A query whose list has nothing gets zeros and lse =

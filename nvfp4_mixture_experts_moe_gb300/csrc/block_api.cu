@@ -265,6 +265,7 @@ moe_status moe_rope(const moe_rope_args* a, moe_stream_t stream) {
   moe_status st = check_plan(a->plan, a->head_dim);
   if (st != MOE_OK) return st;
   if (a->tokens == 0) return MOE_OK;
+  if ((long long)a->tokens * (a->q_heads + a->k_heads) > (1ll << 32) / a->head_dim) return MOE_ERR_UNSUPPORTED;
   const bool k = a->k_heads > 0;
   if (!a->q || !a->q_out || !a->positions || (k && (!a->k || !a->k_out))) return MOE_ERR_INVALID_ARG;
   if (!aligned(a->q, 2) || !aligned(a->q_out, 2) || (k && (!aligned(a->k, 2) || !aligned(a->k_out, 2))))
@@ -291,7 +292,8 @@ moe_status moe_kv4_append_rope(const moe_kv4_append_rope_args* a, moe_stream_t s
   if (st != MOE_OK) return st;
   st = check_plan(a->plan, a->cache.head_dim);
   if (st != MOE_OK) return st;
-  if (a->plan.rotary_dim % (a->plan.adjacent ? 16 : 32) || a->q_heads > 65536) return MOE_ERR_UNSUPPORTED;
+  if (a->plan.rotary_dim % (a->plan.adjacent ? 16 : 32) || a->q_heads > 65536 || a->tokens > 1 << 30)
+    return MOE_ERR_UNSUPPORTED;
   if (a->tokens == 0) return MOE_OK;
   const long long row = (long long)a->cache.kv_heads * a->cache.head_dim, qw = (long long)a->q_heads * a->cache.head_dim;
   if (!a->k || !a->v || !a->slots || !a->positions || !aligned(a->k, 16) || !aligned(a->v, 16)) return MOE_ERR_INVALID_ARG;

@@ -56,6 +56,7 @@ struct SelectArgs {
   moe_kv4_select_args a;
   int block_log;
   int rows;      // CTAs of a request (few queries); 0: of any row
+  long long wait_limit;
 };
 
 // Which blocks a query at `pos` takes without asking and which it ranks.
@@ -419,7 +420,6 @@ constexpr int kTile = 128, kCols = 64, kStages = 2, kGroup = 32, kKeep = 64, kLi
 constexpr int kManyThreads = 288, kTmem = 256;
 static_assert(kList % 16 == 0, "lists are read 16 entries at a time");
 constexpr int kMostBlocks = 65536;   // list entries name blocks in 16 bits
-constexpr long long kWaitLimit = 2ll * 1000 * 1000 * 1000;   // cycles (about 1 s)
 
 template <int D>
 struct ManySmem {
@@ -690,7 +690,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     const int c1 = v.need > 0 ? v.c1 : 0;
     for (int j0 = a.sink; j0 < end; j0 += kCols, ++tile) {
       const int buf = tile & 1;
-      ok = __all_sync(kFull, mbar_wait(&sm.scored[buf], tile >> 1 & 1, abort, kWaitLimit));
+      ok = __all_sync(kFull, mbar_wait(&sm.scored[buf], tile >> 1 & 1, abort, p.wait_limit));
       if (!ok) break;
       tc_fence_after();
 #pragma unroll 1
@@ -742,7 +742,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
         const int j = j0 + ((tid - 128) + 128 * i) / kChunks;
         entry[i] = j < end ? entry_of(a.index, page_log, p.block_log, table, j) : -2;
       }
-      ok = __all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, kWaitLimit));
+      ok = __all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, p.wait_limit));
       if (!ok) break;
       const uint32_t dst = smem_u32(sm.ring[stage]);
 #pragma unroll
@@ -775,12 +775,12 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     // ------------------------------------------------------------ products
     constexpr uint32_t idesc = idesc_f16(kTile, kCols, 0);
     int tile = 0;
-    bool ok = mbar_wait(&sm.rows_in, 0, abort, kWaitLimit);
+    bool ok = mbar_wait(&sm.rows_in, 0, abort, p.wait_limit);
     tc_fence_after();
     for (int j0 = a.sink; j0 < end && ok; j0 += kCols, ++tile) {
       const int buf = tile & 1, stage = tile % kStages;
-      ok = mbar_wait(&sm.full[stage], tile / kStages & 1, abort, kWaitLimit) &&
-           mbar_wait(&sm.read[buf], (tile >> 1 & 1) ^ 1, abort, kWaitLimit);
+      ok = mbar_wait(&sm.full[stage], tile / kStages & 1, abort, p.wait_limit) &&
+           mbar_wait(&sm.read[buf], (tile >> 1 & 1) ^ 1, abort, p.wait_limit);
       if (!ok) break;
       tc_fence_after();
       const uint32_t src = smem_u32(sm.ring[stage]);
@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     // What was issued is complete before tensor memory is given back (also after a wait that gave up).
     tc_commit(&sm.drained);
     const long long c0 = clock64();
-    while (!mbar_try_wait(&sm.drained, 0) && clock64() - c0 < kWaitLimit) {
+    while (!mbar_try_wait(&sm.drained, 0) && clock64() - c0 < 4000000000ll) {
     }
   }
   tc_fence_before();
@@ -843,6 +843,7 @@ moe_status launch_kv4_select(const moe_kv4_select_args& a, cudaStream_t s) {
   SelectArgs p;
   p.a = a;
   p.block_log = __builtin_ctz(a.index.block_tokens);
+  p.wait_limit = debug_wait_limit();
   const int D = a.index.cache.head_dim, Hk = a.index.cache.kv_heads;
   // Lengths are on the device: a call that allows requests of more than
   // kFewRows rows launches both kernels, each skipping the other's. A CTA of
