@@ -1,12 +1,16 @@
 """Serving with the library's operators: two decoder blocks, prompts and decode steps in one loop.
 
 Each step places the new tokens in pages (``KvStep``); each block then projects
-q, k and v (a plain matrix product), appends k and v to its NVFP4 cache,
-attends over it (``Kv4Cache``), adds the residual and norms for the MoE layer
-(``block_norm``), runs it (``Nvfp4MoeLayer``) and adds and norms again.
-Weights are random: the text is noise, the data flow is a server's.
+q, k and v (a plain matrix product), turns q and k (``Rope``) while it appends
+k and v to its NVFP4 cache, attends over it (``Kv4Cache``), adds the residual
+and norms for the MoE layer (``block_norm``), runs it (``Nvfp4MoeLayer``) and
+adds and norms again. Weights are random: the text is noise, the data flow is a
+server's.
 
-    python examples/decoder_blocks.py
+    python examples/decoder_blocks.py [top]
+
+With ``top`` every token attends to that many blocks of 32 tokens: the first,
+its own and the best of the rest (``Kv4BlockIndex``).
 """
 import os
 import sys
@@ -14,7 +18,8 @@ import sys
 import torch
 
 sys.path.insert(0, os.path.join(os.path.dirname(os.path.abspath(__file__)), ".."))
-from nvfp4_mixture_experts_moe_gb300 import Kv4Cache, KvStep, Nvfp4MoeLayer, block_norm  # noqa: E402
+from nvfp4_mixture_experts_moe_gb300 import (Kv4BlockIndex, Kv4Cache, KvStep, Nvfp4MoeLayer, Rope,  # noqa: E402
+                                            block_norm)
 
 HIDDEN, INTER, EXPERTS, TOP_K, VOCAB, LAYERS = 512, 256, 16, 4, 1000, 2
 Q_HEADS, KV_HEADS, DIM = 8, 2, 64
@@ -22,19 +27,10 @@ PAGE, MAX_PAGES, NUM_PAGES = 16, 20, 64
 EPS = 1e-6
 
 
-def rotate(x, positions):
-    """Rotary position embedding of ``[tokens, heads, DIM]``, halves paired."""
-    freq = 10000.0 ** (-torch.arange(0, DIM // 2, device=x.device) / (DIM // 2))
-    angle = positions[:, None].float() * freq
-    cos, sin = angle.cos()[:, None], angle.sin()[:, None]
-    a, b = x.float().chunk(2, dim=-1)
-    return torch.cat((a * cos - b * sin, a * sin + b * cos), dim=-1).to(x.dtype)
-
-
 class Block:
     """One decoder block and its cache."""
 
-    def __init__(self, seed, max_tokens, batch):
+    def __init__(self, seed, max_tokens, batch, rope, top=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
 
         def weight(rows, cols):
@@ -44,6 +40,8 @@ class Block:
         self.norm_moe = torch.ones(HIDDEN, dtype=torch.bfloat16, device="cuda")
         # keys and values of normed rows stay within about 6
         self.cache = Kv4Cache(NUM_PAGES, PAGE, KV_HEADS, DIM, k_gs=2688 / 6, v_gs=2688 / 6)
+        self.rope, self.top = rope, top
+        self.index = Kv4BlockIndex(self.cache, 32) if top else None
         self.attn_ws = self.cache.attention_workspace(max_tokens, batch, Q_HEADS, max_tokens, MAX_PAGES)
         self.moe = Nvfp4MoeLayer(T=max_tokens, H=HIDDEN, I=INTER, E=EXPERTS, k=TOP_K)
         for e in range(EXPERTS + 1):
@@ -55,11 +53,16 @@ class Block:
         """Attention half: residual stream ``h`` and its normed rows ``x`` to the same for the MoE layer."""
         n = x.shape[0]
         qkv = (x @ self.w_qkv.t()).view(n, Q_HEADS + 2 * KV_HEADS, DIM)
-        positions = step.positions[:n]
-        q = rotate(qkv[:, :Q_HEADS], positions)
-        k = rotate(qkv[:, Q_HEADS:Q_HEADS + KV_HEADS], positions)
-        self.cache.append(k, qkv[:, Q_HEADS + KV_HEADS:], step.slots[:n])
-        o, _ = self.cache.attention(q, step.cu_q, step.kv_len, table, max_q=max_q, ws=self.attn_ws)
+        keys = Q_HEADS + KV_HEADS
+        q = self.cache.append_rotated(qkv[:, :Q_HEADS], qkv[:, Q_HEADS:keys], qkv[:, keys:], step.slots[:n],
+                                      step.positions[:n], self.rope)
+        if self.top:
+            where = dict(cu_q=step.cu_q, kv_len=step.kv_len, block_table=table, max_q=max_q)
+            self.index.update(**where)
+            blocks = self.index.select(q, **where, top=self.top)
+            o, _ = self.cache.sparse_attention(q, **where, blocks=blocks, block_tokens=32)
+        else:
+            o, _ = self.cache.attention(q, step.cu_q, step.kv_len, table, max_q=max_q, ws=self.attn_ws)
         return block_norm(o.view(n, -1) @ self.w_o.t(), h, w_pre=self.norm_moe, eps=EPS)
 
     def __call__(self, h, x, step, table, max_q, next_norm):
@@ -68,15 +71,16 @@ class Block:
 
 
 class Server:
-    """``batch`` request slots over shared pages."""
+    """``batch`` request slots over shared pages; ``top`` blocks for each token to attend to (0: every token)."""
 
-    def __init__(self, batch, max_tokens, seed=0):
+    def __init__(self, batch, max_tokens, seed=0, top=0):
         g = torch.Generator(device="cuda").manual_seed(seed)
         self.batch, self.max_tokens = batch, max_tokens
         self.embedding = torch.randn(VOCAB, HIDDEN, generator=g, device="cuda").to(torch.bfloat16)
         self.head = torch.randn(VOCAB, HIDDEN, generator=g, device="cuda").to(torch.bfloat16)
         self.norm = torch.ones(HIDDEN, dtype=torch.bfloat16, device="cuda")
-        self.blocks = [Block(seed + 1 + i, max_tokens, batch) for i in range(LAYERS)]
+        rope = Rope(DIM)
+        self.blocks = [Block(seed + 1 + i, max_tokens, batch, rope, top) for i in range(LAYERS)]
         self.tables = KvStep(batch, max_tokens, PAGE, MAX_PAGES)
         self.block_table = torch.zeros(batch, MAX_PAGES, dtype=torch.int32, device="cuda")
         self.free_pages = torch.arange(NUM_PAGES, dtype=torch.int32, device="cuda")
@@ -104,16 +108,16 @@ class Server:
         self.length[request] = 0
 
 
-def main():
+def main(top=0):
     prompts = [70, 9, 130]
-    server = Server(len(prompts), max_tokens=256)
+    server = Server(len(prompts), max_tokens=256, top=top)
     tokens = torch.randint(0, VOCAB, (sum(prompts),), generator=torch.Generator().manual_seed(1)).cuda()
     token = server.step(tokens, prompts)                       # the prompts in one step
     text = [token]
     for _ in range(12):                                        # then one token of each request at a time
         token = server.step(token, [1] * len(prompts))
         text.append(token)
-    refused = int(server.tables.status)
+    refused = int(server.tables.status) or max(int(b.cache.status) for b in server.blocks)
     for b, row in enumerate(torch.stack(text, dim=1).tolist()):
         print(f"request {b}: {prompts[b]} prompt tokens, then {row}")
     held = NUM_PAGES - int(server.free_count)
@@ -124,4 +128,4 @@ def main():
 
 
 if __name__ == "__main__":
-    sys.exit(main())
+    sys.exit(main(int(sys.argv[1]) if len(sys.argv) > 1 else 0))

@@ -25,7 +25,7 @@ from . import binding as B
 
 
 _UNPACKABLE = (struct.error, OverflowError)   # a number of the caller's that is none, or does not fit its field
-_BF16, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_BF16, _F32, _I32, _DENSE = torch.bfloat16, torch.float32, torch.int32, torch.contiguous_format
 _C = torch._C
 
 
@@ -112,6 +112,11 @@ def _empty(shape, dtype, device, stream, zeros=0):
         if torch.cuda.current_stream().cuda_stream != here.cuda_stream:
             t.record_stream(here)
     return t
+
+
+def _rows_like(t, stream):
+    """A contiguous output of the shape and type of rows (``_rows``) of a call on ``stream``."""
+    return torch.empty_like(t, memory_format=_DENSE) if stream is None else _empty(t.shape, t.dtype, t.device, stream)
 
 
 class Kv4Cache:
@@ -245,20 +250,20 @@ class Kv4Cache:
         n = k.shape[0]
         if v.shape[0] != n:
             raise ValueError("k and v have different lengths")
+        sp, pp = _ints(slots, (n,), "slots", dev), rope._positions(positions, n, dev)
         if q is None:
             heads, qp, qs, op, os_ = 0, 0, 0, 0, 0
         else:
             heads = q.shape[1] if q.dim() == 3 and q.shape[0] == n else -1
             qp, qs = _rows(q, heads, D, "q", dev)
             if q_out is None:
-                q_out = _empty((n, heads, D), _BF16, q.device, stream)
+                q_out = _rows_like(q, stream)
                 op, os_ = q_out.data_ptr(), heads * D
             else:
                 op, os_ = _rows(q_out, heads, D, "q_out", dev)
                 if q_out.shape[0] != n:
                     raise ValueError("q and q_out have different lengths")
-        a = B.PACK_KV4_APPEND_ROPE.pack(*self._fields, *rope._plan(dev), n, heads, qp, qs, kp, ks, vp, vs,
-                                        _ints(slots, (n,), "slots", dev), rope._positions(positions, n, dev), op, os_,
+        a = B.PACK_KV4_APPEND_ROPE.pack(*self._fields, *rope._plan(dev), n, heads, qp, qs, kp, ks, vp, vs, sp, pp, op, os_,
                                         _stamp(device_status, self.status, dev))
         B.moe_kv4_append_rope(a, handle)
         return q_out
@@ -283,12 +288,11 @@ class Kv4Cache:
             raise ValueError("q [rows, heads, dim], kv_len [batch], block_table [batch, max_pages] and blocks [rows, "
                              "kv_heads, top] are needed") from None
         qp, qs = _rows(q, heads, self.head_dim, "q", dev)
-        shape = (total_q, heads, self.head_dim)
         if out is None:
-            out = _empty(shape, _BF16, q.device, stream)
+            out = _rows_like(q, stream)
             op = out.data_ptr()
         else:
-            op = _like(out, shape, _BF16, "out", dev)
+            op = _like(out, q.shape, _BF16, "out", dev)
         if lse is None and want_lse:
             lse = _empty((total_q, heads), _F32, q.device, stream)
         lp = 0 if lse is None else _like(lse, (total_q, heads), _F32, "lse", dev)
@@ -363,22 +367,27 @@ class Rope:
             raise ValueError("q and k: [tokens, heads, head_dim] are needed") from None
         qp, qs = _rows(q, heads, D, "q", dev)
         kp, ks, kop, kos = 0, 0, 0, 0
-        if out is None:
-            out = _empty((n, heads, D), _BF16, q.device, stream)
-            op, os_ = out.data_ptr(), heads * D
-        else:
-            op, os_ = _rows(out, heads, D, "out", dev)
+        pp = self._positions(positions, n, dev)
         if k is not None:
             kp, ks = _rows(k, k_heads, D, "k", dev)
+            if k.shape[0] != n:
+                raise ValueError("q and k have different lengths")
             if k_out is None:
-                k_out = _empty((n, k_heads, D), _BF16, k.device, stream)
+                k_out = _rows_like(k, stream)
                 kop, kos = k_out.data_ptr(), k_heads * D
             else:
                 kop, kos = _rows(k_out, k_heads, D, "k_out", dev)
-        if out.shape[0] != n or (k is not None and not k.shape[0] == k_out.shape[0] == n):
-            raise ValueError("q, k and their outputs have different lengths")
-        B.moe_rope(B.PACK_ROPE.pack(*plan, n, D, heads, k_heads, 1 if inverse else 0, qp, qs, kp, ks,
-                                    self._positions(positions, n, dev), op, os_, kop, kos), handle)
+                if k_out.shape[0] != n:
+                    raise ValueError("k and k_out have different lengths")
+        if out is None:
+            out = _rows_like(q, stream)
+            op, os_ = out.data_ptr(), heads * D
+        else:
+            op, os_ = _rows(out, heads, D, "out", dev)
+            if out.shape[0] != n:
+                raise ValueError("q and out have different lengths")
+        B.moe_rope(B.PACK_ROPE.pack(*plan, n, D, heads, k_heads, 1 if inverse else 0, qp, qs, kp, ks, pp, op, os_, kop, kos),
+                   handle)
         return out if k is None else (out, k_out)
 
 

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from oracle import block
-from test_gpu_block import B, Scene, _bf16, _cuda
+from test_gpu_block import B, Scene, _bf16, _cuda, _example
 from test_gpu_sparse import Picker, _attend, _check_sparse, _index_of, _lists, _step_args
 
 pytestmark = pytest.mark.gpu
@@ -348,3 +348,43 @@ def test_calls_with_nothing_to_do():
     out, lse = c.sparse_attention(e(2, 4, 64).zero_(), cu, i(2), i(2, 0), i(2, 2, 4), block_tokens=32, max_q=1, want_lse=True)
     assert not out.any() and bool((lse == -float("inf")).all())     # queries of requests that hold nothing: reported below
     assert int(c.status) == 0
+
+
+# ---------------------------------------------------------------- the example
+
+def test_example_with_chosen_blocks_runs_and_repeats():
+    m = _example()
+    tokens = torch.randint(0, m.VOCAB, (200,), generator=torch.Generator().manual_seed(2)).cuda()
+    runs = []
+    for _ in range(2):
+        s = m.Server(3, 256, top=3)
+        t = s.step(tokens, [70, 0, 130])
+        got = [t]
+        for _ in range(3):
+            t = s.step(t, [1, 1, 1])
+            got.append(t)
+        assert int(s.tables.status) == 0 and s.length.cpu().tolist() == [73, 3, 133]
+        assert all(int(b.cache.status) == 0 for b in s.blocks)
+        runs.append(torch.stack(got).cpu())
+    assert torch.equal(runs[0], runs[1])
+    assert m.main(top=3) == 0
+
+
+def test_example_with_every_block_attends_as_without_blocks():
+    """The cached rows are the same bytes; the outputs differ by the roundings of two attention kernels (bf16 outputs, f16
+    probabilities, scores of at most some tens: 2^-6 of the largest value each element), carried through the projection, and
+    by the bf16 roundings of the projection and of the residual."""
+    m = _example()
+    n = 200
+    x, h = _bf16((n, m.HIDDEN), 5).cuda(), _bf16((n, m.HIDDEN), 6).cuda()
+    outs, rows = [], []
+    for top in (0, 64):
+        s = m.Server(2, 256, top=top)
+        b = s.blocks[0]
+        t = s.tables.run(s.length, _cuda([150, 50]), s.block_table, s.free_pages, s.free_count)
+        outs.append(b.attend(h, x, t, s.block_table, 150)[0].double())
+        rows.append(b.cache.read(t.slots[:n]))
+    assert torch.equal(rows[0][0], rows[1][0]) and torch.equal(rows[0][1], rows[1][1])
+    da = b.w_o.double().abs().sum(dim=1) * 2.0 ** -6 * float(rows[0][1].abs().max())
+    bar = da + 2.0 ** -7 * (outs[0] - h.double()).abs() + 2.0 ** -7 * outs[0].abs()
+    assert ((outs[0] - outs[1]).abs() <= bar).all()
