@@ -11,10 +11,12 @@
 // the second bounded whatever they are.
 //
 // Two kernels. Requests of up to kFewRows rows: a CTA (or a cluster) for a
-// (query, head) scores the blocks on the FMA pipe, for the means' bytes are
-// what a single query costs. More rows: 128 queries of a head a CTA, a thread
-// each, scores by tcgen05 from tensor memory; the thread keeps a list of the
-// blocks above the lowest score that can still win.
+// (query, head), bound by the latency of its steps (4 single tokens over 2048
+// blocks, 8 heads x 128: 11.6 us, 2.5 by the means' bytes). More rows: 128
+// queries of a head a CTA, a thread each, scores by tcgen05 in tensor memory
+// (4096 rows over 1024 blocks, 32/8 heads x 128: 54 us, 5.6 by the products):
+// a tile of means goes by in 2000 cycles, the copies being issued in half of
+// them, and a CTA's first and last steps are a quarter of its time.
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -40,6 +42,12 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return b ^ ((int)b < 0 ? 0xffffffffu : 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k ^ ((int)k < 0 ? 0x80000000u : 0xffffffffu)); }
+
+// The largest number that is less.
+__device__ __forceinline__ float key_below(float x) {
+  const uint32_t k = order_key(x) - 1;
+  return key_value(k - (k == 0x7fffffffu));   // -0 is not less than 0
+}
 
 // A key between lo and hi (hi > lo + 1): half way between the values, or (odd
 // steps, and where that is no key between) between the keys.
@@ -411,27 +419,58 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_select_few_kernel(const __gri
 // --------------------------------------------------------- many queries
 // Warps 0 to 3: a thread a query. Once u is in tensor memory (the A operand;
 // warps 0 to 7 work it out, a row a warp, and hand it over in the lists'
-// memory) the thread reads its row of each score tile and appends what lies
-// above its bound to its list; a list of more than kKeep is cut at a value that
-// leaves at least `need`. Warps 4 to 7 bring the means of 64 blocks a stage
-// (cp.async into 128-byte-swizzled rows); one thread of warp 8 issues the
-// products.
-constexpr int kTile = 128, kCols = 64, kStages = 2, kGroup = 32, kKeep = 64, kList = kKeep + kGroup;   // a list's places: one more
-constexpr int kManyThreads = 288, kTmem = 256;
+// memory) the thread reads its row of each score tile. Warps 4 to 7 bring the
+// means of 64 blocks a stage (cp.async into 128-byte-swizzled rows); one thread
+// of warp 8 issues the products.
+//
+// The blocks go by twice. First only the maximum of each of 32 groups (every
+// 32nd block) is kept, in registers: at least `need` blocks reach the need-th
+// largest maximum, so only blocks that do can be among the best; of 1024 blocks
+// and 13 picks about 17. The second time those go to a list. Going by once,
+// with a bound that rises as lists of more than kKeep are cut, takes 79 us
+// where this takes 54 (over 64 blocks 34 and 23). For more than kSampled picks
+// 64 groups are kept, in the lists' memory, if there are more blocks than
+// kTwiceLong (once and twice, 48 picks of 1024: 244 and 179 us, of 300 100 and
+// 91; 30 of 200 58 and 60); lists can still fill up then, and are cut at a
+// value that leaves at least `need`.
+//
+// Runs of 256 rows (one CTA an SM, four stages) are slower by a tenth, though
+// they load half as much; two threads a row with half a list each were slower
+// by half.
+constexpr int kRows = 128, kCols = 64, kStages = 2, kGroup = 32, kKeep = 64, kList = kKeep + kGroup;
+constexpr int kLists = kRows / 32, kManyThreads = kRows + 160, kTmem = 256;
 static_assert(kList % 16 == 0, "lists are read 16 entries at a time");
+// Picks for which 32 groups will do; blocks that are worth a first pass for more of them.
+constexpr int kSampled = 24, kTwiceLong = 256;
 constexpr int kMostBlocks = 65536;   // list entries name blocks in 16 bits
 
 template <int D>
 struct ManySmem {
   alignas(1024) uint8_t ring[kStages][kCols * D * 2];
-  float score[kList + 1][kTile];
-  uint16_t blk[kList + 1][kTile];
+  float score[kList + 1][kRows];   // one place more: what is written there does not stay
+  uint16_t blk[kList + 1][kRows];
   int warp_sum[kManyThreads / 32];
-  int request, tile;             // what this CTA has: request, run of kTile of its rows
+  int request, tile;             // what this CTA has: request, run of kRows of its rows
   int abort;
   uint32_t tmem;
   uint64_t full[kStages], empty[kStages], scored[2], read[2], rows_in, drained;
 };
+
+// The largest first: a bitonic network.
+__device__ __forceinline__ void sort(float (&x)[kGroup]) {
+#pragma unroll
+  for (int lk = 1; lk <= 5; ++lk)
+#pragma unroll
+    for (int ld = 4; ld >= 0; --ld)
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i)
+        if (ld < lk && !(i >> ld & 1)) {
+          const float a = x[i], b = x[i | 1 << ld];
+          const bool up = i >> lk & 1;
+          x[i] = up ? fminf(a, b) : fmaxf(a, b);
+          x[i | 1 << ld] = up ? fmaxf(a, b) : fminf(a, b);
+        }
+}
 
 // A thread's list: cnt entries in the order of their blocks; what is past them
 // is not above the bound.
@@ -469,8 +508,28 @@ struct List {
         else hi = key, above = c[0] + c[1];
       }
     }
-    const float from = key_value(lo);
-    int equals = at_least > most ? need - above : kList;   // too many of one score: the first of them
+    keep(wanted, longest, key_value(lo), at_least > most ? need - above : kList);   // too many of one score: the first of them
+  }
+
+  // Exactly `need` entries where there are more, of lists of up to kGroup: their order instead of a search.
+  __device__ __forceinline__ void cut_short(int need) {
+    const bool wanted = cnt > need && need > 0;
+    float x[kGroup];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) x[i] = sm.score[i][row];
+    sort(x);
+    float from = -INFINITY;
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i)
+      if (i < need) from = x[i];
+#pragma unroll
+    for (int i = 0; i < kGroup; ++i) above += x[i] > from;
+    keep(wanted, kGroup, from, need - above);
+  }
+
+  // What is above `from`, and the first `equals` entries equal to it.
+  __device__ __forceinline__ void keep(bool wanted, int longest, float from, int equals) {
     int w = 0;
 #pragma unroll 1
     for (int i = 0; i < longest; i += 16) {   // read ahead of what is written: w <= i
@@ -521,9 +580,9 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sm.scored[i], 1);
-      mbar_init(&sm.read[i], kTile);
+      mbar_init(&sm.read[i], kRows);
     }
-    mbar_init(&sm.rows_in, kTile);
+    mbar_init(&sm.rows_in, kRows);
     mbar_init(&sm.drained, 1);
     sm.request = -1;
     sm.abort = 0;
@@ -537,7 +596,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     if (b0 + tid < a.batch) {
       const RowOwner r = request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, cap, b0 + tid);
       if (r.bad && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-      if (r.b >= 0 && r.n > kFewRows) runs = (r.n + kTile - 1) / kTile;
+      if (r.b >= 0 && r.n > kFewRows) runs = (r.n + kRows - 1) / kRows;
     }
     int incl = runs;
 #pragma unroll
@@ -563,12 +622,14 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
   }
   if (sm.request < 0) return;
   const RowOwner own = request_of(a.cu_q, a.kv_len, a.total_q, a.max_q, cap, sm.request);
-  const int t0 = own.c0 + sm.tile * kTile, rows = min(kTile, own.c0 + own.n - t0);
+  const int t0 = own.c0 + sm.tile * kRows, rows = min(kRows, own.c0 + own.n - t0);
   const int pos0 = own.kv - own.n + t0 - own.c0;       // the first row's position
   const int32_t* const table = a.block_table + (size_t)own.b * a.max_pages;
   // The last row ranks most blocks; where it ranks none, no row does.
   const Visible last = visible(a, p.block_log, pos0 + rows - 1);
   const int end = last.need > 0 ? last.c1 : 0;
+  // whether the blocks go by twice
+  const bool twice = last.need <= kSampled || end - a.sink > kTwiceLong;
   auto ranks = [&](int r) { return r < rows && visible(a, p.block_log, pos0 + r).need > 0; };
   Visible v = {0, 0, 0, 0};
   const int t = t0 + tid;
@@ -583,17 +644,18 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     }
   }
   if (last.need == 0) return;
-  if (warp == 8) tmem_alloc(&sm.tmem, kTmem);
+  if (warp == kLists + 4) tmem_alloc(&sm.tmem, kTmem);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = sm.tmem;               // scores in columns 0..127 (two tiles), u in the D / 2 after 128
+  const uint32_t tmem = sm.tmem;   // two tiles of scores, then u
+  constexpr int kU = 2 * kCols;
   volatile int* const abort = &sm.abort;
 
   // ----------------------------------------------- the rows of u, a row a warp
   constexpr int kRowLanes = D / 8, kPasses = 32 / kRowLanes;   // lanes of a head's row, heads at once
   constexpr int kPad = D * 2 + 16;                              // bytes of a row of u on its way to tensor memory
-  static_assert(kPad * kTile <= (int)sizeof(sm.score), "u passes through the lists");
+  static_assert(kPad * kRows <= (int)sizeof(sm.score), "u passes through the lists");
   uint8_t* const rows_of_u = reinterpret_cast<uint8_t*>(sm.score);
   if (warp < 8) {
     // kHeads of a lane at most, kRowsAtOnce rows asked for together
@@ -601,7 +663,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
       constexpr int kHeads = decltype(heads_of_lane)::value, kAtOnce = decltype(rows_at_once)::value;
       const int part = lane % kRowLanes, g0 = lane / kRowLanes;
 #pragma unroll 1
-      for (int r0 = warp * (kTile / 8); r0 < (warp + 1) * (kTile / 8); r0 += kAtOnce) {
+      for (int r0 = warp * (kRows / 8); r0 < (warp + 1) * (kRows / 8); r0 += kAtOnce) {
         uint4 x[kAtOnce][kHeads];
 #pragma unroll
         for (int b = 0; b < kAtOnce; ++b)
@@ -665,7 +727,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
   }
   __syncthreads();
 
-  if (warp < 4) {
+  if (warp < kLists) {
     // ------------------------------------------------------------- queries
     const uint32_t lanes = (uint32_t)(warp * 32) << 16;
 #pragma unroll
@@ -676,33 +738,100 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
         const uint4 x = *reinterpret_cast<const uint4*>(rows_of_u + tid * kPad + d0 * 2 + i * 16);
         r[4 * i] = x.x, r[4 * i + 1] = x.y, r[4 * i + 2] = x.z, r[4 * i + 3] = x.w;
       }
-      tmem_st16(tmem + lanes + 128 + d0 / 2, r);
+      tmem_st16(tmem + lanes + kU + d0 / 2, r);
     }
     tmem_st_wait();
     tc_fence_before();
     mbar_arrive(&sm.rows_in);
     // the lists' memory is the lists' once every query has its row
-    asm volatile("bar.sync 1, 128;" ::: "memory");
+    asm volatile("bar.sync 1, %0;" ::"n"(kRows) : "memory");
     for (int i = 0; i < kList; ++i) sm.score[i][tid] = -INFINITY;
     List<Sm> list = {sm, tid, 0, -INFINITY, -INFINITY};
     int tile = 0;
     bool ok = true;
     const int c1 = v.need > 0 ? v.c1 : 0;
-    for (int j0 = a.sink; j0 < end; j0 += kCols, ++tile) {
-      const int buf = tile & 1;
-      ok = __all_sync(kFull, mbar_wait(&sm.scored[buf], tile >> 1 & 1, abort, p.wait_limit));
-      if (!ok) break;
-      tc_fence_after();
+    // take(j, n, r): this row's scores of kGroup blocks from j on, of which it ranks n.
+    auto every_score = [&](auto take) {
+      for (int j0 = a.sink; j0 < end && ok; j0 += kCols, ++tile) {
+        const int buf = tile & 1;
+        ok = __all_sync(kFull, mbar_wait(&sm.scored[buf], tile >> 1 & 1, abort, p.wait_limit));
+        if (!ok) break;
+        tc_fence_after();
 #pragma unroll 1
-      for (int g = 0; g < kCols / kGroup; ++g) {
-        uint32_t r[kGroup];
-        tmem_ld32(tmem + lanes + buf * kCols + g * kGroup, r);
-        tmem_ld_wait();
-        if (g == kCols / kGroup - 1) {
-          tc_fence_before();
-          mbar_arrive(&sm.read[buf]);
+        for (int g = 0; g < kCols / kGroup; ++g) {
+          uint32_t r[kGroup];
+          tmem_ld32(tmem + lanes + buf * kCols + g * kGroup, r);
+          tmem_ld_wait();
+          if (g == kCols / kGroup - 1) {
+            tc_fence_before();
+            mbar_arrive(&sm.read[buf]);
+          }
+          const int j = j0 + g * kGroup;
+          take(j, min(kGroup, c1 - j), r);
         }
-        const int j = j0 + g * kGroup, n = min(kGroup, c1 - j);   // this row's blocks of the group
+      }
+    };
+    if (twice && last.need <= kSampled) {
+      float best[kGroup];
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) best[i] = -INFINITY;
+      every_score([&](int, int n, uint32_t (&r)[kGroup]) {
+        if (__all_sync(kFull, n >= kGroup)) {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) best[i] = fmaxf(best[i], __uint_as_float(r[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i)
+            if (i < n) best[i] = fmaxf(best[i], __uint_as_float(r[i]));
+        }
+      });
+      sort(best);
+#pragma unroll
+      for (int i = 0; i < kGroup; ++i) sm.score[kKeep + i][tid] = best[i];
+      float least = fminf(sm.score[kKeep + max(v.need, 1) - 1][tid], FLT_MAX);
+      every_score([&](int j, int n, uint32_t (&r)[kGroup]) {
+        uint32_t reach = 0;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) {
+          sm.score[kKeep + i][tid] = __uint_as_float(r[i]);
+          if (__uint_as_float(r[i]) >= least) reach |= 1u << i;
+        }
+        if (least == -INFINITY) reach = ~0u;
+        if (n < kGroup) reach &= n <= 0 ? 0u : (1u << n) - 1u;
+        if (__any_sync(kFull, list.cnt + __popc(reach) > kKeep)) {
+          const int before = list.cnt;
+          list.cut(v.need, kKeep - kGroup);
+          if (before > kKeep - kGroup) least = key_value(order_key(list.bound) + 1);
+        }
+        for (; reach; reach &= reach - 1) {
+          const int i = __ffs((int)reach) - 1;
+          const float s = finite_score(sm.score[kKeep + i][tid]);
+          if (s >= least) {
+            sm.score[list.cnt][tid] = s;
+            sm.blk[list.cnt][tid] = (uint16_t)(j + i);
+            ++list.cnt;
+            list.top = fmaxf(list.top, s);
+          }
+        }
+        __syncwarp();
+      });
+    } else {
+      if (twice) {   // 64 groups
+        every_score([&](int j, int n, uint32_t (&r)[kGroup]) {
+          float(*const best)[kRows] = sm.score + ((j - a.sink) & kGroup);
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i)
+            if (i < n) best[i][tid] = fmaxf(best[i][tid], __uint_as_float(r[i]));
+        });
+        list.cnt = 2 * kGroup;
+        list.top = FLT_MAX;
+        list.cut(v.need, v.need);
+        list.bound = key_below(fminf(list.bound, FLT_MAX));
+        list.cnt = 0;
+        list.top = -INFINITY;
+        for (int i = 0; i < 2 * kGroup; ++i) sm.score[i][tid] = -INFINITY;
+      }
+      every_score([&](int j, int n, uint32_t (&r)[kGroup]) {
         // Every score is written behind the list, and stays if it is above: a branch for each column costs six times
         // as much.
         const bool whole = __all_sync(kFull, n >= kGroup);
@@ -720,74 +849,89 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
         }
         // One list too long: every list is cut that is much longer than it has to be.
         if (__any_sync(kFull, list.cnt > kKeep)) list.cut(v.need, min(kKeep, v.need + v.need / 2 + 8));
-      }
+      });
     }
     // ------------------------------------------------- the best, in order
-    list.cut(v.need, v.need);
+    if (__all_sync(kFull, list.cnt <= kGroup)) list.cut_short(v.need);
+    else list.cut(v.need, v.need);
     if (v.need > 0) {
       int32_t* const out = a.blocks + ((size_t)t * Hk + h) * a.top + a.sink;
       for (int i = 0; i < v.need; ++i) out[i] = ok && i < list.cnt ? sm.blk[i][tid] : -1;
     }
-  } else if (warp < 8) {
+  } else if (warp < kLists + 4) {
     // --------------------------------------------------------------- means
-    constexpr int kChunks = D / 8, kPerThread = kCols * kChunks / 128;   // 16-byte pieces of a row, of a thread
+    // A thread has one 16-byte piece of kPieces rows, kEvery rows apart; the first 16 lanes look a warp's rows up, a tile
+    // ahead.
+    constexpr int kChunks = D / 8, kEvery = 128 / kChunks, kPieces = kCols / kEvery, kBeside = 32 / kChunks;
+    const int me = tid - kRows, tiles = (end - a.sink + kCols - 1) / kCols, total = tiles << twice;
+    const int ch = lane % kChunks, row0 = me / kChunks;
+    const int looked_up = (me >> 5) * kBeside + lane % 16 % kBeside + lane % 16 / kBeside * kEvery;
+    // K halves of 64 elements one after the other, rows of 128 bytes; kEvery is a multiple of a swizzle's 8 rows
+    const uint32_t at = smem_u32(sm.ring[0]) + (uint32_t)(ch / 8 * (kCols * 128) + row0 * 128 + (((ch & 7) ^ (row0 & 7)) << 4));
+    const uint16_t* const means = a.index.means + (size_t)h * D + ch * 8;
+    const int per_page_log = max(page_log - p.block_log, 0);
     int tile = 0, done = 0;
-    bool ok = true;
-    for (int j0 = a.sink; j0 < end; j0 += kCols, ++tile) {
-      const int stage = tile % kStages;
-      // the table's entries first: they do not wait for the stage
-      int entry[kPerThread];
+    auto block_of = [&](int tile) { return a.sink + (tile < tiles ? tile : tile - tiles) * kCols + looked_up; };
+    auto page_of = [&](int tile) {
+      const int j = block_of(tile);
+      return tile < total && j < end ? __ldg(table + ((j << p.block_log) >> page_log)) : 0;
+    };
+    int page = page_of(0);
+    for (; tile < total; ++tile) {
+      const int stage = tile % kStages, j = block_of(tile);
+      const int mine = j >= end ? -2
+                       : page < 0 || page >= c.num_pages ? -1
+                                                         : (page << per_page_log) + (j & ((1 << per_page_log) - 1));
+      page = page_of(tile + 1);
+      if (!__all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, p.wait_limit))) break;
+      const uint32_t dst = at + stage * (uint32_t)sizeof(sm.ring[0]);
+      int entry[kPieces];
 #pragma unroll
-      for (int i = 0; i < kPerThread; ++i) {
-        const int j = j0 + ((tid - 128) + 128 * i) / kChunks;
-        entry[i] = j < end ? entry_of(a.index, page_log, p.block_log, table, j) : -2;
-      }
-      ok = __all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, p.wait_limit));
-      if (!ok) break;
-      const uint32_t dst = smem_u32(sm.ring[stage]);
+      for (int i = 0; i < kPieces; ++i) entry[i] = __shfl_sync(kFull, mine, i * kBeside + lane / kChunks);
+      if (!__any_sync(kFull, mine < 0)) {
 #pragma unroll
-      for (int i = 0; i < kPerThread; ++i) {
-        const int idx = tid - 128 + 128 * i, row = idx / kChunks, ch = idx % kChunks;
-        // K halves of 64 elements one after the other, rows of 128 bytes
-        const uint32_t at = (uint32_t)(ch / 8 * (kCols * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4));
-        if (entry[i] == -1) {   // a page that is not in the pool: a row of NaN, which no mean is
-          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + at), "r"(0x7e007e00u) : "memory");
-          if (a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
-        } else {
-          const uint16_t* src = a.index.means + ((size_t)max(entry[i], 0) * Hk + h) * D + ch * 8;
-          cp_async_16(dst + at, src, entry[i] >= 0 ? 16u : 0u);
+        for (int i = 0; i < kPieces; ++i) cp_async_16(dst + i * kEvery * 128, means + (size_t)entry[i] * (Hk * D), 16u);
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kPieces; ++i) {
+          const int e = __shfl_sync(kFull, mine, i * kBeside + lane / kChunks);
+          if (e == -1) {   // a page that is not in the pool: a row of NaN, which no mean is
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(dst + i * kEvery * 128), "r"(0x7e007e00u) : "memory");
+            if (a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
+          } else {
+            cp_async_16(dst + i * kEvery * 128, means + (size_t)max(e, 0) * (Hk * D), e >= 0 ? 16u : 0u);
+          }
         }
       }
       cp_async_commit();
-      if (tile > done) {     // the stage before this one is in
-        cp_async_wait<1>();
+      if (tile - done == kStages - 1) {     // the first of the stages on their way is in
+        cp_async_wait<kStages - 1>();
         fence_proxy_async_smem();
         mbar_arrive(&sm.full[done % kStages]);
         ++done;
       }
     }
     cp_async_wait_all();
-    if (done < tile) {
-      fence_proxy_async_smem();
-      mbar_arrive(&sm.full[done % kStages]);
-    }
+    fence_proxy_async_smem();
+    for (; done < tile; ++done) mbar_arrive(&sm.full[done % kStages]);
   } else if (lane == 0) {
     // ------------------------------------------------------------ products
-    constexpr uint32_t idesc = idesc_f16(kTile, kCols, 0);
-    int tile = 0;
+    constexpr uint32_t idesc = idesc_f16(128, kCols, 0);
+    const uint64_t ring = smem_desc(smem_u32(sm.ring[0]), 16, 1024, kSwizzle128B);
+    const int total = (end - a.sink + kCols - 1) / kCols << twice;
     bool ok = mbar_wait(&sm.rows_in, 0, abort, p.wait_limit);
     tc_fence_after();
-    for (int j0 = a.sink; j0 < end && ok; j0 += kCols, ++tile) {
+    for (int tile = 0; tile < total && ok; ++tile) {
       const int buf = tile & 1, stage = tile % kStages;
       ok = mbar_wait(&sm.full[stage], tile / kStages & 1, abort, p.wait_limit) &&
            mbar_wait(&sm.read[buf], (tile >> 1 & 1) ^ 1, abort, p.wait_limit);
       if (!ok) break;
       tc_fence_after();
-      const uint32_t src = smem_u32(sm.ring[stage]);
+      const uint64_t src = ring + (uint64_t)(stage * (sizeof(sm.ring[0]) >> 4));
 #pragma unroll
       for (int k = 0; k < D / 16; ++k)
-        mma_f16_tmem_a(tmem + buf * kCols, tmem + 128 + k * 8,
-                       smem_desc(src + k / 4 * (kCols * 128) + k % 4 * 32, 16, 1024, kSwizzle128B), idesc, k != 0);
+        mma_f16_tmem_a(tmem + buf * kCols, tmem + kU + k * 8, src + (uint64_t)((k / 4 * (kCols * 128) + k % 4 * 32) >> 4), idesc,
+                       k != 0);
       tc_commit(&sm.empty[stage]);
       tc_commit(&sm.scored[buf]);
     }
@@ -800,7 +944,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 8) tmem_dealloc(tmem, kTmem);
+  if (warp == kLists + 4) tmem_dealloc(tmem, kTmem);
   if (tid == 0 && sm.abort && a.device_status != nullptr) set_status(a.device_status, MOE_ERR_TIMEOUT);
 }
 
@@ -828,13 +972,15 @@ cudaError_t launch_few(const SelectArgs& p, long long items, cudaStream_t s) {
 template <int D>
 cudaError_t launch_many(const SelectArgs& p, cudaStream_t s) {
   constexpr size_t smem = sizeof(ManySmem<D>) + 1024;
+  static_assert(2 * (smem + 1024) <= 228 * 1024, "two CTAs an SM");
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = opt_in_smem(kv4_select_many_kernel<D>, smem, done);
   if (e != cudaSuccess) return e;
-  // as many runs of kTile rows as the requests can have: each but its last is full, and holds more than kFewRows
-  const long long full = p.a.total_q / kTile, part = p.a.total_q / (kFewRows + 1);
+  // as many runs of kRows rows as the requests can have: each but its last is full, and holds more than kFewRows
+  const long long full = p.a.total_q / kRows, part = p.a.total_q / (kFewRows + 1);
   const unsigned tiles = (unsigned)(full + (part < p.a.batch ? part : p.a.batch));
-  return launch_ex(true, kv4_select_many_kernel<D>, dim3(tiles * p.a.index.cache.kv_heads), dim3(kManyThreads), smem, s, p);
+  return launch_ex(true, kv4_select_many_kernel<D>, dim3(tiles * p.a.index.cache.kv_heads),
+                   dim3(kManyThreads), smem, s, p);
 }
 
 }  // namespace
@@ -849,8 +995,8 @@ moe_status launch_kv4_select(const moe_kv4_select_args& a, cudaStream_t s) {
   // kFewRows rows launches both kernels, each skipping the other's. A CTA of
   // the first then has all rows of a request, as most requests will have one.
   const bool long_lists = ((long long)a.max_pages * a.index.cache.page_tokens >> p.block_log) > kMostBlocks;
-  // A few rows go faster without it (us for 64 and 128 rows of 8 heads over 1024 blocks: 41 and 77 by the first, 57 and
-  // 60 by the second; over 128 blocks 19 and 32, 29 and 30).
+  // A few rows go faster without it (us for 64, 80 and 128 rows of 8 heads over 1024 blocks: 36, 49 and 69 by the first,
+  // 37, 37 and 38 by the second; over 128 blocks 14, 19 and 25, 16, 16 and 18).
   const bool many = a.max_q > kFewRows && (long long)a.total_q * Hk > kManyRows && !long_lists;
   p.rows = many ? 1 : a.max_q > kFewRows ? 0 : a.max_q;
   const long long items = (p.rows == 0 ? (long long)a.total_q : (long long)a.batch * p.rows) * Hk;

@@ -182,6 +182,30 @@ def test_which_kernel_takes_picks(n, heads, launches):
     assert _launches(lambda: p.check(12, 1, 2, rows=3)) == launches
 
 
+@pytest.mark.parametrize("top", [2, 14, 26, 27, 28, 45, 64])
+@pytest.mark.parametrize("kind", ["random", "rising", "falling", "equal", "few", "signs", "gone"])
+def test_many_rows_pick_whatever_the_order_of_scores(top, kind):
+    """Ranges either side of the one where a first pass finds a bound, picks either side of what it finds in registers;
+    scores in every order, mostly equal, of both signs around zero, of pages that are not there."""
+    lens = [((259 + top // 2) * 32, 420), (700 * 32, 150), (34 * 32, 30), (66 * 32 + 5, 200)]
+    p = Picker(lens, 2, 1, 64, 64, 32, seed=top)
+    if kind in ("rising", "falling", "few", "equal", "signs"):
+        p.q[:] = 0
+        p.q[:, :, 0] = 1.0
+        p.means[:] = 0.0
+        r = np.random.default_rng(top)
+        for b, (kv, _) in enumerate(lens):
+            for j in range(-(-kv // 32)):
+                x = {"rising": j / 8, "falling": 100 - j / 8, "equal": 3.0, "few": float(r.integers(0, 2)),
+                     "signs": float(r.integers(-1, 2))}[kind]
+                p.means[p.table[b, j // 2] * 2 + j % 2, 0, 0] = x
+        p.index.means.copy_(torch.tensor(p.means))
+    elif kind == "gone":
+        p.table[0, 5:100:3], p.table[1, 1:349], p.table[3, 2:30] = -1, p.cache.num_pages, -7
+    p.check(top, 0, 1, rows=6)
+    p.check(top, 1, 1, rows=4)
+
+
 def test_many_rows_of_equal_scores_and_bad_pages():
     p = Picker([(120 * 32, 400), (90 * 32, 60)], 4, 2, 64, 32, 32)
     p.means[:] = 1.0
