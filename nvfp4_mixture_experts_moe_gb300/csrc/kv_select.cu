@@ -14,9 +14,10 @@
 // (query, head), bound by the latency of its steps (4 single tokens over 2048
 // blocks, 8 heads x 128: 11.6 us, 2.5 by the means' bytes). More rows: 128
 // queries of a head a CTA, a thread each, scores by tcgen05 in tensor memory
-// (4096 rows over 1024 blocks, 32/8 heads x 128: 54 us, 5.6 by the products):
-// a tile of means goes by in 2000 cycles, the copies being issued in half of
-// them, and a CTA's first and last steps are a quarter of its time.
+// (4096 rows over 1024 blocks, 32/8 heads x 128: 54 us, 5.6 by the queries'
+// bytes): of a CTA's 80,000 cycles the queries take 11,000, a tile of 64 means
+// 1600 the first time it goes by (issue of the products, two CTAs an SM) and
+// 2500 the second (the lists, 1800), the picks 4500.
 #include <cooperative_groups.h>
 
 #include <cfloat>

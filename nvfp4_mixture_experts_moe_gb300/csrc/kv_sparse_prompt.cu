@@ -24,9 +24,11 @@
 //
 // What bounds it (2048 rows, 16 blocks of 64 each, 32/8 heads x 128: 182 us; 17
 // by the products of each row with its own blocks): a unit multiplies all its
-// rows by the union of what its tokens chose, and a step of 64 tokens takes an
-// SM's two CTAs 1400 cycles, 770 of them by the operands in shared memory. S
-// whole in registers spilled (229 us), as did two threads a row (334); one
+// rows by the union of what its tokens chose. A step of 64 tokens takes an SM
+// 950 cycles (1900 in each of its CTAs), some 650 by the products (S's operands
+// from shared memory 8 x 48, O's rate 4 x 68); a unit's entry and end take 17,000
+// of its 135,000; 512 units are four for 56 of the SMs and three for the others.
+// S whole in registers spilled (229 us), as did two threads a row (334); one
 // thread issuing all products 189.
 #include "kernels.cuh"
 #include "kv4.cuh"
