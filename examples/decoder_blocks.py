@@ -27,6 +27,15 @@ PAGE, MAX_PAGES, NUM_PAGES = 16, 20, 64
 EPS = 1e-6
 
 
+def rotate(x, positions):
+    """What ``Rope(DIM)`` computes, as torch operations: ``[tokens, heads, DIM]``, halves paired."""
+    freq = 10000.0 ** (-torch.arange(0, DIM // 2, device=x.device) / (DIM // 2))
+    angle = positions[:, None].float() * freq
+    cos, sin = angle.cos()[:, None], angle.sin()[:, None]
+    a, b = x.float().chunk(2, dim=-1)
+    return torch.cat((a * cos - b * sin, a * sin + b * cos), dim=-1).to(x.dtype)
+
+
 class Block:
     """One decoder block and its cache."""
 

@@ -412,3 +412,14 @@ def test_example_with_every_block_attends_as_without_blocks():
     da = b.w_o.double().abs().sum(dim=1) * 2.0 ** -6 * float(rows[0][1].abs().max())
     bar = da + 2.0 ** -7 * (outs[0] - h.double()).abs() + 2.0 ** -7 * outs[0].abs()
     assert ((outs[0] - outs[1]).abs() <= bar).all()
+
+
+def test_example_turns_as_its_torch_form():
+    """Two roundings to bf16, and the torch form's angles: up to 256, rounded twice, 2^-15 of a pair's magnitudes."""
+    m = _example()
+    x, pos = _bf16((256, m.Q_HEADS, m.DIM), 3).cuda(), torch.arange(256, dtype=torch.int32, device="cuda")
+    rope = m.Server(1, 256).blocks[0].rope
+    got, want = rope(x, pos).double(), m.rotate(x, pos).double()
+    a, b = x.double().abs().chunk(2, dim=-1)
+    bar = 2.0 ** -7 * want.abs() + 2.0 ** -14 * torch.cat((a + b, a + b), dim=-1)
+    assert ((got - want).abs() <= bar).all()
