@@ -22,12 +22,13 @@
 // While one CTA builds a union, enters or ends a unit, the other one's warps
 // work.
 //
-// What bounds it (2048 rows, 16 blocks of 64 each, 32/8 heads x 128: 182 us; 17
+// What bounds it (2048 rows, 16 blocks of 64 each, 32/8 heads x 128: 179 us; 17
 // by the products of each row with its own blocks): a unit multiplies all its
 // rows by the union of what its tokens chose. A step of 64 tokens takes an SM
-// 950 cycles (1900 in each of its CTAs), some 650 by the products (S's operands
-// from shared memory 8 x 48, O's rate 4 x 68); a unit's entry and end take 17,000
-// of its 135,000; 512 units are four for 56 of the SMs and three for the others.
+// 950 cycles (1900 in each of its CTAs), 770 of them by shared memory (operands
+// of S 384, of O 128, stores of the tiles 256; Q in tensor memory would save a
+// third of that, but S and O leave no columns); a unit's entry and end take
+// 17,000 of its 135,000; 512 units are four for 56 of the SMs and three for the others.
 // S whole in registers spilled (229 us), as did two threads a row (334); one
 // thread issuing all products 189.
 #include "kernels.cuh"
@@ -366,13 +367,13 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
             b.tok = tok;
             b.page = __ldg(table + (tok >> p_log));
           };
-          auto load = [&](Raw& r, const uint8_t* src, int to) {
+          auto load = [&](Raw& r, const uint8_t* src, auto there) {
             const uint8_t *codes = src + tl * L::kCodeRow + 16 * cl, *scales = src + L::kKeyScales + tl * L::kScaleRow + 2 * cl;
 #pragma unroll
             for (int y = 0; y < kLoads; ++y) {
               r.codes[y] = make_uint4(0u, 0u, 0u, 0u);   // what may not have been appended enters as zeros
               r.sf[y] = 0u;
-              if (y * kRowsPerLoad + tl < to) {
+              if (there(y * kRowsPerLoad + tl)) {
                 r.codes[y] = __ldg(reinterpret_cast<const uint4*>(codes + y * kRowsPerLoad * L::kCodeRow));
                 r.sf[y] = __ldg(reinterpret_cast<const uint16_t*>(scales + y * kRowsPerLoad * L::kScaleRow));
               }
@@ -391,8 +392,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
                 if (lane == 0 && a.device_status != nullptr) *a.device_status = MOE_ERR_DEVICE;
               }
             }
-            load(b.k, src, b.to);
-            load(b.v, src + L::kValueCodes, b.to);
+            auto both = [&](auto there) {
+              load(b.k, src, there);
+              load(b.v, src + L::kValueCodes, there);
+            };
+            if (b.to >= kKvBlock) both([](int) { return true; });   // one branch for all: 182 us with one for each load
+            else both([&](int row) { return row < b.to; });
           };
           uint32_t off[4];                             // of this lane's four 16-byte stores, in a tile
 #pragma unroll
