@@ -14,10 +14,10 @@
 // (query, head), bound by the latency of its steps (4 single tokens over 2048
 // blocks, 8 heads x 128: 11.6 us, 2.5 by the means' bytes). More rows: 128
 // queries of a head a CTA, a thread each, scores by tcgen05 in tensor memory
-// (4096 rows over 1024 blocks, 32/8 heads x 128: 54 us, 5.6 by the queries'
-// bytes): of a CTA's 80,000 cycles the queries take 11,000, a tile of 64 means
-// 1600 the first time it goes by (issue of the products, two CTAs an SM) and
-// 2500 the second (the lists, 1800), the picks 4500.
+// (4096 rows over 1024 blocks, 32/8 heads x 128: 50 us, 5.6 by the queries'
+// bytes): of a CTA's 75,000 cycles the queries take 11,000, a tile of 64 means
+// some 1500 the first time it goes by (the hand-overs between its warps) and
+// 2200 the second (the lists), the picks 4500.
 #include <cooperative_groups.h>
 
 #include <cfloat>
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_select_few_kernel(const __gri
 // largest maximum, so only blocks that do can be among the best; of 1024 blocks
 // and 13 picks about 17. The second time those go to a list. Going by once,
 // with a bound that rises as lists of more than kKeep are cut, takes 79 us
-// where this takes 54 (over 64 blocks 34 and 23). For more than kSampled picks
+// where this took 54 (over 64 blocks 34 and 23). For more than kSampled picks
 // 64 groups are kept, in the lists' memory, if there are more blocks than
 // kTwiceLong (once and twice, 48 picks of 1024: 244 and 179 us, of 300 100 and
 // 91; 30 of 200 58 and 60); lists can still fill up then, and are cut at a
@@ -791,12 +791,13 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
       for (int i = 0; i < kGroup; ++i) sm.score[kKeep + i][tid] = best[i];
       float least = fminf(sm.score[kKeep + max(v.need, 1) - 1][tid], FLT_MAX);
       every_score([&](int j, int n, uint32_t (&r)[kGroup]) {
-        uint32_t reach = 0;
+        uint32_t part[4] = {0, 0, 0, 0};
 #pragma unroll
         for (int i = 0; i < kGroup; ++i) {
           sm.score[kKeep + i][tid] = __uint_as_float(r[i]);
-          if (__uint_as_float(r[i]) >= least) reach |= 1u << i;
+          if (__uint_as_float(r[i]) >= least) part[i & 3] |= 1u << i;
         }
+        uint32_t reach = part[0] | part[1] | part[2] | part[3];
         if (least == -INFINITY) reach = ~0u;
         if (n < kGroup) reach &= n <= 0 ? 0u : (1u << n) - 1u;
         if (__any_sync(kFull, list.cnt + __popc(reach) > kKeep)) {
@@ -915,29 +916,40 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
     cp_async_wait_all();
     fence_proxy_async_smem();
     for (; done < tile; ++done) mbar_arrive(&sm.full[done % kStages]);
-  } else if (lane == 0) {
+  } else {
     // ------------------------------------------------------------ products
+    // The warp runs together, one lane issues (one lane on its own: 53 us); stages and tiles of scores by constants.
+    const bool one = elect_one();
+    static_assert(kStages == 2, "a stage a tile of scores");
     constexpr uint32_t idesc = idesc_f16(128, kCols, 0);
     const uint64_t ring = smem_desc(smem_u32(sm.ring[0]), 16, 1024, kSwizzle128B);
     const int total = (end - a.sink + kCols - 1) / kCols << twice;
-    bool ok = mbar_wait(&sm.rows_in, 0, abort, p.wait_limit);
+    bool ok = __all_sync(kFull, mbar_wait(&sm.rows_in, 0, abort, p.wait_limit));
     tc_fence_after();
-    for (int tile = 0; tile < total && ok; ++tile) {
-      const int buf = tile & 1, stage = tile % kStages;
-      ok = mbar_wait(&sm.full[stage], tile / kStages & 1, abort, p.wait_limit) &&
-           mbar_wait(&sm.read[buf], (tile >> 1 & 1) ^ 1, abort, p.wait_limit);
-      if (!ok) break;
-      tc_fence_after();
-      const uint64_t src = ring + (uint64_t)(stage * (sizeof(sm.ring[0]) >> 4));
+#pragma unroll 1
+    for (int first = 0; first < total && ok; first += 2) {
 #pragma unroll
-      for (int k = 0; k < D / 16; ++k)
-        mma_f16_tmem_a(tmem + buf * kCols, tmem + kU + k * 8, src + (uint64_t)((k / 4 * (kCols * 128) + k % 4 * 32) >> 4), idesc,
-                       k != 0);
-      tc_commit(&sm.empty[stage]);
-      tc_commit(&sm.scored[buf]);
+      for (int b = 0; b < 2; ++b) {
+        if (first + b >= total || !ok) break;
+        const uint32_t parity = first >> 1 & 1;
+        ok = __all_sync(kFull, mbar_wait(&sm.full[b], parity, abort, p.wait_limit) &&
+                                   mbar_wait(&sm.read[b], parity ^ 1, abort, p.wait_limit));
+        if (!ok) break;
+        tc_fence_after();
+        if (one) {
+          const uint64_t src = ring + (uint64_t)(b * (sizeof(sm.ring[0]) >> 4));
+#pragma unroll
+          for (int k = 0; k < D / 16; ++k)
+            mma_f16_tmem_a(tmem + b * kCols, tmem + kU + k * 8, src + (uint64_t)((k / 4 * (kCols * 128) + k % 4 * 32) >> 4),
+                           idesc, k != 0);
+          tc_commit(&sm.empty[b]);
+          tc_commit(&sm.scored[b]);
+        }
+        __syncwarp();
+      }
     }
     // What was issued is complete before tensor memory is given back (also after a wait that gave up).
-    tc_commit(&sm.drained);
+    if (one) tc_commit(&sm.drained);
     const long long c0 = clock64();
     while (!mbar_try_wait(&sm.drained, 0) && clock64() - c0 < 4000000000ll) {
     }

@@ -22,10 +22,10 @@
 // While one CTA builds a union, enters or ends a unit, the other one's warps
 // work.
 //
-// What bounds it (2048 rows, 16 blocks of 64 each, 32/8 heads x 128: 179 us; 17
+// What bounds it (2048 rows, 16 blocks of 64 each, 32/8 heads x 128: 174 us; 17
 // by the products of each row with its own blocks): a unit multiplies all its
 // rows by the union of what its tokens chose. A step of 64 tokens takes an SM
-// 950 cycles (1900 in each of its CTAs), 770 of them by shared memory (operands
+// 930 cycles (1860 in each of its CTAs), 770 of them by shared memory (operands
 // of S 384, of O 128, stores of the tiles 256; Q in tensor memory would save a
 // third of that, but S and O leave no columns); a unit's entry and end take
 // 17,000 of its 135,000; 512 units are four for 56 of the SMs and three for the others.
@@ -440,6 +440,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
         } else {
           // --------------------------------------------------------------- MMA
           bool ok = true;
+          const bool one = elect_one();   // (by lane 0 on its own 179 us)
           if (warp == kMmaWarp) {
             constexpr uint32_t id_s = idesc_f16(128, kStep, 0);
             const uint64_t qd = smem_desc(smem_u32(sm->q), 16, 1024, kSwizzle128B);
@@ -450,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               // the columns' last P has gone into O
               if (!(ok = wait(&sm->k_full[st], j >> 1) && wait(&sm->pv_done[st], (j >> 1) ^ 1))) break;
               tc_fence_after();
-              if (lane == 0) {
+              if (one) {
                 const uint64_t kb = kd + (uint64_t)((st * Sm::kTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               const int j = js + s, st = j & 1;
               if (!(ok = wait(&sm->v_full[st], j >> 1) && wait(&sm->p_full[st], j >> 1))) break;
               tc_fence_after();
-              if (lane == 0) {
+              if (one) {
                 const uint64_t vb = vd + (uint64_t)((st * Sm::kTile) >> 4);
 #pragma unroll
                 for (int kk = 0; kk < kStep / 16; ++kk)
