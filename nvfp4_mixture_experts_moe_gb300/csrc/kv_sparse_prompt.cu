@@ -488,7 +488,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
 
       // --------------------------------------------------------- the results
       if (steps_so_far > 0) {
-        if (warp == kMmaWarp + 1 && lane == 0) tc_commit(&sm->o_full);
+        // by the lane that issued (the elected one, each time the same): a commit is for its own thread's operations
+        if (warp == kMmaWarp + 1 && elect_one()) tc_commit(&sm->o_full);
         if (warp < kSoftWarps && wait(&sm->o_full, jq)) {
           tc_fence_after();
           const float2 two = unpack2(l2);
@@ -527,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
       }
     }
   }
-  if (warp >= kMmaWarp && lane == 0) {   // what was issued is complete before tensor memory is given back
+  if (warp >= kMmaWarp && elect_one()) {   // what was issued is complete before tensor memory is given back
     tc_commit(&sm->drain);
     const long long t0 = clock64();
     while (!mbar_try_wait(&sm->drain, 0) && clock64() - t0 < 4000000000ll) {
