@@ -332,20 +332,32 @@ moe_status moe_kv4_append_rope(const moe_kv4_append_rope_args* args, moe_stream_
  * The index has a row of means for each (block that starts in a page, head):
  * f16 [num_pages * max(1, page_tokens / block_tokens)][kv_heads][head_dim].
  * Block j of a request has the rows of entry
- *   block_table[b][j * block_tokens / page_tokens] * max(1, page_tokens / block_tokens)
- *     + (j * block_tokens % page_tokens) / block_tokens
- * so requests that share pages share means, and pages given back need no care.
+ *   page * max(1, page_tokens / block_tokens) + (j * block_tokens % page_tokens) / block_tokens
+ * page being the one it starts in, block_table[b][j * block_tokens / page_tokens].
+ * Where blocks are larger than pages, requests can share the page that a block
+ * starts in and not the ones after it (a common prefix that ends inside the
+ * block): owners[page] is the last page of the block that has the row of
+ * `page`, -1 while none has; the rows of any other block that starts there are
+ * those of its own last page. An update gives a row to the first block that it
+ * completes there and never takes it back, so a block's rows follow from the
+ * table and owners at any time. With that, requests that share a prefix share
+ * its means, and pages given back need no care. A page is shared at one place
+ * of its requests only; a page that is copied does not take means along (an
+ * update whose new tokens are the page's makes them).
  * A mean is that of code * scale (the key times k_gs) over the block's tokens,
  * rounded to a multiple of 2^(E - 6), E the exponent of the row's largest
  * magnitude: whole numbers of 8 bits times a power of two.
  *
  * Limits: block_tokens 32, 64 or 128; means 16-byte aligned, moe_kv4_index_size
  * bytes; it needs no initialisation (only means of complete blocks are used).
+ * owners: int32 [num_pages], -1 before the first update and kept with the means;
+ * with block_tokens <= page_tokens not used (may be NULL).
  */
 typedef struct {
   moe_kv4_cache cache;
   int block_tokens;
   uint16_t* means;
+  int32_t* owners;
 } moe_kv4_index;
 
 size_t moe_kv4_index_size(int num_pages, int page_tokens, int kv_heads, int head_dim, int block_tokens);
@@ -356,8 +368,8 @@ size_t moe_kv4_index_size(int num_pages, int page_tokens, int kv_heads, int head
  *
  * cu_q int32 [batch + 1], kv_len int32 [batch], block_table int32 [batch, max_pages], max_q as in moe_kv4_attention
  * (a request with more than max_q new tokens, or a kv_len past its table, is reported and left out).
- * Errors: NULL pointers, misaligned means, negative sizes, max_q < 1 ->
- * MOE_ERR_INVALID_ARG; another block_tokens, batch > 4096, max_pages *
+ * Errors: NULL pointers, misaligned means or owners, negative sizes, max_q < 1
+ * -> MOE_ERR_INVALID_ARG; another block_tokens, batch > 4096, max_pages *
  * page_tokens > 2^31 - 129, the cache's limits -> MOE_ERR_UNSUPPORTED. batch =
  * 0 -> MOE_OK.
  */
@@ -377,7 +389,7 @@ moe_status moe_kv4_index_update(const moe_kv4_index* index, int batch, int max_q
  *
  * blocks  int32 [total_q, kv_heads, top], ascending, -1 in the places that are left; rows no request owns are left alone
  * Others as in moe_kv4_attention (which has the contract of bad device data: a
- * page id outside the pool scores lowest, as does a mean that is NaN).
+ * page id outside the pool scores lowest, as does a mean that is NaN; of a block of several pages the first and the last count).
  * Limits: 1 <= top <= 64, sink + local <= top, local >= 1, groups of up to 16
  * query heads, a context of up to 2^28 tokens.
  * Errors: as moe_kv4_attention and moe_kv4_index_update; sink, local or top

@@ -113,7 +113,8 @@ class MoeKv4AppendRopeArgs(ctypes.Structure):
 
 
 class MoeKv4Index(ctypes.Structure):
-    _fields_ = [("cache", MoeKv4Cache), ("block_tokens", ctypes.c_int), ("means", ctypes.c_void_p)]
+    _fields_ = [("cache", MoeKv4Cache), ("block_tokens", ctypes.c_int), ("means", ctypes.c_void_p),
+                ("owners", ctypes.c_void_p)]
 
 
 class MoeKv4SelectArgs(ctypes.Structure):
@@ -187,7 +188,7 @@ PACK_KV_STEP = struct.Struct("@5i11P")
 PACK_BLOCK_NORM = struct.Struct("@iiPqPqPqiPPffffPP")
 PACK_ROPE = struct.Struct("@3ifP5iPqPqPPqPq")
 PACK_KV4_APPEND_ROPE = struct.Struct("@4i2fP3ifP2iPqPqPqPPPqP")
-PACK_KV4_SELECT = struct.Struct("@4i2fPiP5iPqPPP3iPP")
+PACK_KV4_SELECT = struct.Struct("@4i2fPiPP5iPqPPP3iPP")
 PACK_KV4_SPARSE = struct.Struct("@4i2fP7iPqPPPPfPPP")
 
 MOE_KV4_WS_ZERO = 4096  # leading workspace bytes of moe_kv4_attention that start at zero

@@ -396,21 +396,32 @@ class Kv4BlockIndex:
 
     ``means`` f16 ``[entries, kv_heads, head_dim]`` (layout in
     ``include/moe_block.h``) may be given; otherwise it is allocated,
-    uninitialised, on the current stream. Bad device data is reported in the
-    cache's ``status`` where a call has no ``device_status``.
+    uninitialised, on the current stream. Where blocks are larger than the
+    cache's pages, ``owners`` int32 ``[num_pages]`` says which blocks have the
+    rows of the pages they start in (requests may share the start of a block and
+    not its end): made as -1, nobody's, unless given. The two belong together:
+    who gives means that updates have written gives their owners too. Bad device
+    data is reported in the cache's ``status`` where a call has no ``device_status``.
     """
 
-    def __init__(self, cache, block_tokens, means=None):
+    def __init__(self, cache, block_tokens, means=None, owners=None):
         _need(block_tokens in (32, 64, 128), "block_tokens: 32, 64 or 128")
         shape = (cache.num_pages * max(1, cache.page_tokens // block_tokens), cache.kv_heads, cache.head_dim)
         if means is None:
             means = torch.empty(shape, dtype=torch.float16, device=cache.pool.device)
         _need(means.is_cuda and means.get_device() == cache._dev and means.dtype == torch.float16 and
               means.is_contiguous() and means.shape == shape, f"means: a contiguous f16 tensor {shape} on the cache's GPU")
-        self.cache, self.block_tokens, self.means = cache, block_tokens, means
+        if block_tokens <= cache.page_tokens:
+            _need(owners is None, "owners: only for blocks that are larger than a page")
+        elif owners is None:
+            owners = torch.full((cache.num_pages,), -1, dtype=_I32, device=cache.pool.device)
+        else:
+            _ints(owners, (cache.num_pages,), "owners", cache._dev)
+        self.cache, self.block_tokens, self.means, self.owners = cache, block_tokens, means, owners
         self._dev = cache._dev
-        self._fields = (*cache._fields, block_tokens, means.data_ptr())
-        self.desc = B.MoeKv4Index(cache.desc, block_tokens, means.data_ptr())
+        rows = means.data_ptr(), 0 if owners is None else owners.data_ptr()
+        self._fields = (*cache._fields, block_tokens, *rows)
+        self.desc = B.MoeKv4Index(cache.desc, block_tokens, *rows)
 
     def _here(self, stream):
         dev, handle = _where(stream)

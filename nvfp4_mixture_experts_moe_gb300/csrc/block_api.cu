@@ -112,7 +112,9 @@ moe_status check_index(const moe_kv4_index& x) {
   moe_status st = check_index_sizes(x.cache, x.block_tokens);
   if (st == MOE_OK) st = check_cache(x.cache);
   if (st != MOE_OK) return st;
-  return x.means && aligned(x.means, 16) ? MOE_OK : MOE_ERR_INVALID_ARG;
+  if (!x.means || !aligned(x.means, 16)) return MOE_ERR_INVALID_ARG;
+  // which blocks have the rows of their first pages: needed where blocks have several
+  return x.block_tokens <= x.cache.page_tokens || (x.owners && aligned(x.owners, 4)) ? MOE_OK : MOE_ERR_INVALID_ARG;
 }
 
 // The sizes of a selection and of an attention over what it selected.

@@ -59,6 +59,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_index_kernel(const __grid_con
     if (lane == 0 && p.status != nullptr) *p.status = MOE_ERR_DEVICE;
     return;
   }
+  // Whose rows: the first page's, or, where another block has those, the last one's. All heads get the same answer.
+  int row_page = __shfl_sync(kFull, my_page, 0);
+  if (B > P) {
+    const int end = __shfl_sync(kFull, my_page, subs - 1);
+    int owner = -1;
+    if (lane == 0) owner = atomicCAS(p.x.owners + row_page, -1, end);
+    owner = __shfl_sync(kFull, owner, 0);
+    if (owner >= 0 && owner != end) row_page = end;
+  }
   int sum[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) sum[i] = 0;
@@ -137,7 +146,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_index_kernel(const __grid_con
       out[i] = *reinterpret_cast<const uint32_t*>(&o);
     }
     const int per = P > B ? P / B : 1;
-    const size_t entry = (size_t)__ldg(table + tok0 / P) * per + tok0 % P / B;
+    const size_t entry = (size_t)row_page * per + tok0 % P / B;
     uint4* const dst = reinterpret_cast<uint4*>(p.x.means + (entry * c.kv_heads + h) * D + part * 32);
 #pragma unroll
     for (int i = 0; i < 4; ++i) dst[i] = make_uint4(out[4 * i], out[4 * i + 1], out[4 * i + 2], out[4 * i + 3]);

@@ -84,11 +84,23 @@ __device__ __forceinline__ Visible visible(const moe_kv4_select_args& a, int blo
   return v;
 }
 
+// The page whose rows a block of several pages has: its first one's unless another block owns those; -1: one of the two
+// is not in the pool.
+__device__ __forceinline__ int row_page(int first, int last, int owner, int num_pages) {
+  if (first < 0 || first >= num_pages || last < 0 || last >= num_pages) return -1;
+  return owner < 0 || owner == last ? first : last;
+}
+__device__ __forceinline__ int owner_of(const moe_kv4_index& x, int page) {
+  return page >= 0 && page < x.cache.num_pages ? __ldg(x.owners + page) : -1;
+}
+
 // Where the mean of block j of a request lies; -1: its page is not in the pool.
 __device__ __forceinline__ int entry_of(const moe_kv4_index& x, int page_log, int block_log, const int32_t* table, int j) {
   const int tok = j << block_log, page = __ldg(table + (tok >> page_log));
+  if (page_log < block_log)
+    return row_page(page, __ldg(table + ((tok + (1 << block_log) - 1) >> page_log)), owner_of(x, page), x.cache.num_pages);
   if (page < 0 || page >= x.cache.num_pages) return -1;
-  return page_log > block_log ? (page << (page_log - block_log)) + ((tok & ((1 << page_log) - 1)) >> block_log) : page;
+  return (page << (page_log - block_log)) + ((tok & ((1 << page_log) - 1)) >> block_log);
 }
 
 // Elements of the group's queries on their grid: 2^(5 - E), E from the largest
@@ -878,13 +890,34 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
       const int j = block_of(tile);
       return tile < total && j < end ? __ldg(table + ((j << p.block_log) >> page_log)) : 0;
     };
-    int page = page_of(0);
+    // Blocks of several pages: their last pages, and who has the rows of the first ones, which are looked up a tile earlier.
+    const bool spans = page_log < p.block_log;
+    auto last_of = [&](int tile) {
+      const int j = block_of(tile);
+      return tile < total && j < end ? __ldg(table + ((((j + 1) << p.block_log) - 1) >> page_log)) : 0;
+    };
+    int page = page_of(0), last_page = 0, owner = 0, page1 = 0, last_page1 = 0;
+    if (spans) {
+      last_page = last_of(0);
+      owner = owner_of(a.index, page);
+      page1 = page_of(1);
+      last_page1 = last_of(1);
+    }
     for (; tile < total; ++tile) {
       const int stage = tile % kStages, j = block_of(tile);
+      if (spans) page = row_page(page, last_page, owner, c.num_pages);
       const int mine = j >= end ? -2
                        : page < 0 || page >= c.num_pages ? -1
                                                          : (page << per_page_log) + (j & ((1 << per_page_log) - 1));
-      page = page_of(tile + 1);
+      if (spans) {
+        page = page1;
+        last_page = last_page1;
+        owner = owner_of(a.index, page);
+        page1 = page_of(tile + 2);
+        last_page1 = last_of(tile + 2);
+      } else {
+        page = page_of(tile + 1);
+      }
       if (!__all_sync(kFull, mbar_wait(&sm.empty[stage], (tile / kStages & 1) ^ 1, abort, p.wait_limit))) break;
       const uint32_t dst = at + stage * (uint32_t)sizeof(sm.ring[0]);
       int entry[kPieces];
