@@ -96,8 +96,8 @@ moe_status moe_kv4_read(const moe_kv4_cache* cache, const int32_t* slots, int n,
  *
  * causal = 1: j <= position; window > 0 (causal only): also j > position -
  * window. A query that sees nothing gets a zero row and lse = -inf; one with a
- * NaN gets NaN in both (an infinity does where its scores have no softmax),
- * and no other row changes. lse is the natural logarithm of sum exp(s_j).
+ * NaN or an infinity that sees something gets NaN in both (its scores have no
+ * softmax), and no other row changes. lse is the natural logarithm of sum exp(s_j).
  * Products of q with the codes are exact, sums and softmax statistics are
  * fp32; the probabilities enter the second product as f16. Results do not
  * depend on timing: the same call gives the same bits.

@@ -218,10 +218,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv4_sparse_prompt_kernel(const __
               mx = max_u16x2(max_u16x2(mx, x.x & 0x7fff7fffu), x.y & 0x7fff7fffu);
               mx = max_u16x2(max_u16x2(mx, x.z & 0x7fff7fffu), x.w & 0x7fff7fffu);
             }
-            const int ex = min(max((int)(max(mx & 0xffffu, mx >> 16) >> 7), 15), 254);
+            const uint32_t big = max(mx & 0xffffu, mx >> 16);
+            const int ex = min(max((int)(big >> 7), 15), 254);
             // never 0, so that a hidden score stays -inf
             c = fmaxf(fabsf(a.scale) * kLog2e / a.cache.k_gs * pow2(ex - 141), 1e-37f);
-            const float up = a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);   // larger scores stay larger products
+            // a larger score is a larger product; a row with a NaN or an infinity has no softmax whatever it sees: all NaN
+            const float up = big >= 0x7f80u ? __int_as_float(0x7fffffff) : a.scale < 0.0f ? -pow2(141 - ex) : pow2(141 - ex);
 #pragma unroll 4
             for (int v = 0; v < kChunks; ++v) {
               uint4* chunk = reinterpret_cast<uint4*>(sm->q + tile_chunk<>(tid, v));

@@ -146,3 +146,31 @@ def test_a_block_with_a_bad_last_page_scores_lowest():
     assert pick()[0, :, 0].tolist() == [2, 2] and int(s.cache.status) == 0
     s.table[0, 11] = -1
     assert 2 not in pick()[0].tolist()[0] and int(s.cache.status) != 0
+
+
+# ------------------------------------------------------- infinite queries
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[(40, 1), (300, 2)], [(300, 40), (90, 40)], [(700, 400), (20, 20)]])
+def test_an_infinity_whose_scores_are_all_minus_infinity_gives_nan(D, lens):
+    """exp(-inf + inf) is no number: zeros and -inf are what a row that sees nothing gives. All cached keys are negative
+    where the query is infinite."""
+    s = Scene(lens, 32, 8, D, 32, seed=D)
+    for b, (kv, _) in enumerate(lens):
+        k = _bf16((kv, 8, D), b)
+        k[:, :, 3] = -5.0
+        s.cache.append(k.cuda(), k.cuda(), _cuda(s.table[b, np.arange(kv) // 32] * 32 + np.arange(kv) % 32))
+    lists = np.tile(np.arange(24), (s.total, 8, 1))
+    row, head = int(s.cu[1]), 5                  # the second request's first token
+    lists[row + 1, 1] = -1                       # the next row sees nothing
+    q = s.q.clone()
+    q[row, head, 3] = q[row + 1, head, 3] = float("inf")
+    spoilt = torch.zeros(s.total, 32, dtype=torch.bool, device="cuda")
+    spoilt[row, head] = True
+    for name, call in (("sparse", lambda q: _attend(s, lists, 32, q=q.cuda(), want_lse=True)),
+                       ("dense", lambda q: s.run(q=q.cuda(), want_lse=True))):
+        spoilt[row + 1, head] = name == "dense"
+        (good, good_lse), (out, lse) = call(s.q), call(q)
+        assert bool(out.isnan().all(-1).eq(spoilt).all()) and bool(lse.isnan().eq(spoilt).all()), name
+        assert torch.equal(out[~spoilt], good[~spoilt]) and torch.equal(lse[~spoilt], good_lse[~spoilt]), name
+    assert bool((_attend(s, lists, 32, q=q.cuda(), want_lse=True)[1][row + 1, 4:8] == -float("inf")).all())
