@@ -17,6 +17,7 @@ raise ``ValueError``; what the C call refuses raises ``MoeError``.
 """
 from __future__ import annotations
 
+import operator
 import struct
 
 import torch
@@ -32,6 +33,16 @@ _C = torch._C
 def _need(ok, what):
     if not ok:
         raise ValueError(what)
+
+
+def _whole(x, what):
+    """A whole number that a C int holds, of whatever type (what counts as an index)."""
+    try:
+        x = operator.index(x)
+    except TypeError:
+        raise ValueError(f"{what}: a whole number is needed") from None
+    _need(-2 ** 31 <= x < 2 ** 31, f"{what}: a whole number of 32 bits is needed")
+    return x
 
 
 def _where(stream):
@@ -323,7 +334,8 @@ class Rope:
 
     def __init__(self, rotary_dim, theta=10000.0, inv_freq=None, sections=None, axes=None, pairs="half", scale=1.0,
                  device="cuda"):
-        _need(isinstance(rotary_dim, int) and rotary_dim >= 2 and rotary_dim % 2 == 0, "rotary_dim: an even number is needed")
+        rotary_dim = _whole(rotary_dim, "rotary_dim")
+        _need(rotary_dim >= 2 and rotary_dim % 2 == 0, "rotary_dim: an even number is needed")
         half = rotary_dim // 2
         _need(pairs in ("half", "adjacent"), "pairs: half or adjacent")
         _need(sections is None or axes is None, "sections or axes, not both")
@@ -405,6 +417,7 @@ class Kv4BlockIndex:
     """
 
     def __init__(self, cache, block_tokens, means=None, owners=None):
+        block_tokens = _whole(block_tokens, "block_tokens")
         _need(block_tokens in (32, 64, 128), "block_tokens: 32, 64 or 128")
         shape = (cache.num_pages * max(1, cache.page_tokens // block_tokens), cache.kv_heads, cache.head_dim)
         if means is None:
@@ -440,8 +453,7 @@ class Kv4BlockIndex:
             _, max_pages = block_table.shape
         except ValueError:
             raise ValueError("kv_len [batch] and block_table [batch, max_pages] are needed") from None
-        _need(isinstance(max_q, int) and max_q < 2 ** 31, "max_q: a whole number of 32 bits is needed")
-        B.moe_kv4_index_update(self.desc, batch, max_q, max_pages, _ints(cu_q, (batch + 1,), "cu_q", dev),
+        B.moe_kv4_index_update(self.desc, batch, _whole(max_q, "max_q"), max_pages, _ints(cu_q, (batch + 1,), "cu_q", dev),
                                _ints(kv_len, (batch,), "kv_len", dev),
                                _ints(block_table, (batch, max_pages), "block_table", dev),
                                _stamp(device_status, self.cache.status, dev), handle)
@@ -463,9 +475,10 @@ class Kv4BlockIndex:
         except ValueError:
             raise ValueError("q [rows, heads, dim], kv_len [batch] and block_table [batch, max_pages] are needed") from None
         qp, qs = _rows(q, heads, c.head_dim, "q", dev)
+        top = _whole(top, "top")
         shape = (total_q, c.kv_heads, top)
         if blocks is None:
-            _need(isinstance(top, int) and top >= 0, "top: a whole number is needed")
+            _need(top >= 0, "top: a whole number of at least 0 is needed")
             blocks = _empty(shape, _I32, q.device, stream)
             bp = blocks.data_ptr()
         else:
