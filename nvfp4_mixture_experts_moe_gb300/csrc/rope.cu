@@ -394,7 +394,7 @@ moe_status launch_rope(const moe_rope_args& args, cudaStream_t s) {
   const int heads = a.q_heads + a.k_heads;
   p.splits = head_splits((long long)a.tokens * p.units, heads);
   const long long per_token = (long long)p.splits * p.units;
-  if (a.tokens > (1ll << 31) / per_token) return MOE_ERR_UNSUPPORTED;   // threads are counted in 32 bits
+  if (a.tokens > ((1ll << 32) - kThreads) / per_token) return MOE_ERR_UNSUPPORTED;   // threads are counted in 32 bits
   const unsigned grid = (unsigned)((a.tokens * per_token + kThreads - 1) / kThreads);
   const auto k = !vectors ? rope_pair_kernel : wide_units ? rope_vector_kernel<true> : rope_vector_kernel<false>;
   const cudaError_t e = launch_ex(true, k, dim3(grid), dim3(kThreads), 0, s, p);

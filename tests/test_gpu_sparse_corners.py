@@ -174,3 +174,22 @@ def test_an_infinity_whose_scores_are_all_minus_infinity_gives_nan(D, lens):
         assert bool(out.isnan().all(-1).eq(spoilt).all()) and bool(lse.isnan().eq(spoilt).all()), name
         assert torch.equal(out[~spoilt], good[~spoilt]) and torch.equal(lse[~spoilt], good_lse[~spoilt]), name
     assert bool((_attend(s, lists, 32, q=q.cuda(), want_lse=True)[1][row + 1, 4:8] == -float("inf")).all())
+
+
+# ------------------------------------------------------- the largest rotation
+
+def test_rotation_of_as_many_elements_as_the_limit_allows():
+    """2^32 elements of heads of three: two threads a head, more of them than 2^31."""
+    from nvfp4_mixture_experts_moe_gb300 import MoeError, Rope
+    n, few = (1 << 32) // 3, 1000
+    rope = Rope(2)
+    x, pos = torch.zeros(n + 1, 1, 3, dtype=torch.bfloat16, device="cuda"), torch.zeros(n + 1, dtype=torch.int32, device="cuda")
+    spots = (0, (1 << 31) // 3 - few // 2, (1 << 31) // 2 - few // 2, n - few)
+    for i, at in enumerate(spots):
+        x[at:at + few] = _bf16((few, 1, 3), i).cuda()
+        pos[at:at + few] = torch.arange(at, at + few, dtype=torch.int32, device="cuda")
+    y = rope(x[:n], pos[:n])
+    for at in spots:
+        assert torch.equal(y[at:at + few], rope(x[at:at + few], pos[at:at + few]))
+    with pytest.raises(MoeError):
+        rope(x, pos, out=x)
