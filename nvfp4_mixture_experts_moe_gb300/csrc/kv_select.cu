@@ -35,7 +35,7 @@ using namespace tc;
 namespace cg = cooperative_groups;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kFewRows = 8, kManyRows = 640;
+constexpr int kFewRows = 8, kManyRows = 608, kManyRowsNarrow = 640;
 
 // A float's bits in the order of its value (0 is below every key of a number).
 __device__ __forceinline__ uint32_t order_key(float x) {
@@ -1041,9 +1041,12 @@ moe_status launch_kv4_select(const moe_kv4_select_args& a, cudaStream_t s) {
   // kFewRows rows launches both kernels, each skipping the other's. A CTA of
   // the first then has all rows of a request, as most requests will have one.
   const bool long_lists = ((long long)a.max_pages * a.index.cache.page_tokens >> p.block_log) > kMostBlocks;
-  // A few rows go faster without it (us for 64, 80 and 128 rows of 8 heads over 1024 blocks: 36, 49 and 69 by the first,
-  // 37, 37 and 38 by the second; over 128 blocks 14, 19 and 25, 16, 16 and 18).
-  const bool many = a.max_q > kFewRows && (long long)a.total_q * Hk > kManyRows && !long_lists;
+  // Few rows go faster without it: two CTAs of the first kernel run on an SM, 608 are two waves of 152 SMs, more a third
+  // (us of the first and the second for 76 and 80 rows of 8 heads x 128 over 151 blocks: 14.6 and 16.6, 18.2 and 16.9;
+  // over 512 blocks 23.1 and 23.3, 28.8 and 23.5; x 64 over 151 blocks 12.3 and 16.1, 15.5 and 16.2, so that a third wave
+  // begins before it does). Over tables of 2048 blocks and more the second is ahead from some 48 rows on (64 rows: 60 and
+  // 52), but a table may be far from full.
+  const bool many = a.max_q > kFewRows && (long long)a.total_q * Hk > (D == 64 ? kManyRowsNarrow : kManyRows) && !long_lists;
   p.rows = many ? 1 : a.max_q > kFewRows ? 0 : a.max_q;
   const long long items = (p.rows == 0 ? (long long)a.total_q : (long long)a.batch * p.rows) * Hk;
   cudaError_t e = D == 64 ? launch_few<64>(p, items, s) : launch_few<128>(p, items, s);

@@ -6,7 +6,8 @@ import torch
 
 from oracle import block
 from test_gpu_block import Scene, _bf16, _cuda, built  # noqa: F401
-from test_gpu_sparse import _attend, _check_sparse, _index_of
+from test_gpu_sparse import Picker, _attend, _check_sparse, _index_of
+from test_gpu_sparse_contracts import _launches
 
 pytestmark = pytest.mark.gpu
 
@@ -193,3 +194,11 @@ def test_rotation_of_as_many_elements_as_the_limit_allows():
         assert torch.equal(y[at:at + few], rope(x[at:at + few], pos[at:at + few]))
     with pytest.raises(MoeError):
         rope(x, pos, out=x)
+
+
+# ------------------------------------------------- which kernel takes picks
+
+@pytest.mark.parametrize("n,heads,launches", [(76, 8, 1), (77, 8, 2), (80, 8, 2), (608, 1, 1), (609, 1, 2)])
+def test_which_kernel_takes_picks_of_wide_heads(n, heads, launches):
+    p = Picker([(150 * 32, n)], 2 * heads, heads, 128, 32, 32, seed=n)
+    assert _launches(lambda: p.check(12, 1, 2, rows=3)) == launches
