@@ -27,6 +27,23 @@ __device__ __forceinline__ size_t kv4_block_offset(int64_t page, int head, int k
   return (((size_t)page * kv_heads + head) * blocks_per_page + block) * (size_t)block_bytes;
 }
 
+// How a row's group of 16 is stored, by its largest magnitude: the E4M3 code of
+// its scale, and what its elements are multiplied with; 0 with a scale of 0,
+// where every code is 0 (a negative element's too).
+struct KvScale {
+  uint32_t code;
+  float r;
+};
+__device__ __forceinline__ KvScale kv_scale(float amax, float gs) {
+  KvScale s;
+  s.code = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
+  const float v = e4m3_decode(s.code);
+  s.r = v > 0.0f ? __fdiv_rn(gs, v) : 0.0f;
+  return s;
+}
+// The codes of two elements of a group whose scale is not 0, in a byte.
+__device__ __forceinline__ uint32_t kv_codes2(float x, float y, float r) { return e2m1x2_rn(__fmul_rn(x, r), __fmul_rn(y, r)); }
+
 // (x * y + z) / d of non-negative numbers; a 64-bit division (some 300
 // cycles) only where 32 bits do not hold the product.
 __device__ __forceinline__ int mul_div(int x, int y, int d, int z = 0) {

@@ -154,15 +154,12 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
     amax = amax16(w);
   }
   const float gs = c.gs[p.kv].x;
-  const uint32_t scale = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
-  const float sval = e4m3_decode(scale);
+  const KvScale scale = kv_scale(amax, gs);
   uint32_t lo = 0, hi = 0;
-  if (sval > 0.0f) {
-    const float r = __fdiv_rn(gs, sval);
+  if (scale.r > 0.0f) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const uint32_t b = e2m1x2_rn(__fmul_rn(__uint_as_float(w[j] << 16), r),
-                                   __fmul_rn(__uint_as_float(w[j] & 0xffff0000u), r));
+      const uint32_t b = kv_codes2(__uint_as_float(w[j] << 16), __uint_as_float(w[j] & 0xffff0000u), scale.r);
       if (j < 4) lo |= b << (8 * j);
       else hi |= b << (8 * (j - 4));
     }
@@ -170,7 +167,7 @@ __global__ void __launch_bounds__(kMaxWarps * 32)
   int row;
   uint8_t* blk = slot_row<D>(c, slot, p.h, row) + (p.kv ? L::kValueCodes : 0);
   *reinterpret_cast<uint2*>(blk + row * L::kCodeRow + p.blk * 8) = make_uint2(lo, hi);
-  blk[L::kKeyScales + row * L::kScaleRow + p.blk] = (uint8_t)scale;
+  blk[L::kKeyScales + row * L::kScaleRow + p.blk] = (uint8_t)scale.code;
 }
 
 template <int D, bool kWide>

@@ -229,21 +229,8 @@ __device__ __forceinline__ float amax8(const float (&x)[8]) {
 __device__ __forceinline__ uint32_t codes8(const float (&x)[8], float r) {
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) w |= e2m1x2_rn(__fmul_rn(x[2 * i], r), __fmul_rn(x[2 * i + 1], r)) << (8 * i);
-  return w;
-}
-
-struct Scale {
-  uint32_t code;
-  float r;     // gs / scale; 0 with a scale of 0, whose codes are 0
-};
-
-__device__ __forceinline__ Scale scale_of(float amax, float gs) {
-  Scale s;
-  s.code = e4m3_encode_sat(__fmul_rn(__fdiv_rn(amax, 6.0f), gs));
-  const float v = e4m3_decode(s.code);
-  s.r = v > 0.0f ? __fdiv_rn(gs, v) : 0.0f;
-  return s;
+  for (int i = 0; i < 4; ++i) w |= kv_codes2(x[2 * i], x[2 * i + 1], r) << (8 * i);
+  return r > 0.0f ? w : 0u;
 }
 
 __device__ __forceinline__ void no_nan(float (&x)[8]) {
@@ -346,7 +333,7 @@ __global__ void __launch_bounds__(kThreads) kv4_append_rope_kernel(const __grid_
         mx = my = fmaxf(mx, my);
       }
       if (!keep) continue;
-      const Scale sx = scale_of(mx, gs), sy = split ? scale_of(my, gs) : sx;
+      const KvScale sx = kv_scale(mx, gs), sy = split ? kv_scale(my, gs) : sx;
       uint8_t* const blk = block_of(h) + (key ? 0 : L::kValueCodes);
       *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at0 / 2) = codes8(x, sx.r);
       *reinterpret_cast<uint32_t*>(blk + row * L::kCodeRow + at1 / 2) = codes8(y, sy.r);

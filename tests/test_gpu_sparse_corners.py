@@ -202,3 +202,33 @@ def test_rotation_of_as_many_elements_as_the_limit_allows():
 def test_which_kernel_takes_picks_of_wide_heads(n, heads, launches):
     p = Picker([(150 * 32, n)], 2 * heads, heads, 128, 32, 32, seed=n)
     assert _launches(lambda: p.check(12, 1, 2, rows=3)) == launches
+
+
+# ------------------------------------------------------------- stored bytes
+
+@pytest.mark.parametrize("D,pairs", [(64, "half"), (128, "half"), (128, "adjacent")])
+def test_groups_whose_scale_is_zero_store_zero_codes(D, pairs):
+    """Elements of either sign too small for a scale: the pool's bytes are the append's, keys (unturned ones) and values."""
+    from nvfp4_mixture_experts_moe_gb300 import Kv4Cache, Rope
+    T, heads = 40, 2
+    k, v = _bf16((T, heads, D), 1), _bf16((T, heads, D), 2)
+    for x in (k, v):
+        x[3:7, :, 16:48] *= 1e-30
+        x[9, 1] = -0.0
+        x[11, 0, 32:] = -1e-38
+    k[:, :, D // 2:] = 0.0 if pairs == "half" else k[:, :, D // 2:]
+    pools = []
+    for turned in (False, True):
+        c = Kv4Cache(3, 16, heads, D, 300.0, 300.0)
+        c.pool.fill_(0xA5)
+        at = _cuda(np.arange(T) + 5)
+        if turned:
+            c.append_rotated(None, k.cuda(), v.cuda(), at, _cuda(np.zeros(T)), Rope(D, pairs=pairs))
+        else:
+            c.append(k.cuda(), v.cuda(), at)
+        pools.append(c.pool.view(3, heads, 1, 18 * D))
+    assert torch.equal(pools[0][..., 9 * D:], pools[1][..., 9 * D:])
+    a, b = (x[..., :9 * D] for x in pools)
+    assert torch.equal(a[..., 8 * D:], b[..., 8 * D:])
+    zero = (a[..., 8 * D:] == 0).view(3, heads, 1, 16, D // 16, 1).expand(-1, -1, -1, -1, -1, 8).reshape(3, heads, 1, 8 * D)
+    assert bool(zero.any()) and torch.equal(a[..., :8 * D][zero], b[..., :8 * D][zero])
