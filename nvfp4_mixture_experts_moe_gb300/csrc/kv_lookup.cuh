@@ -51,18 +51,4 @@ __device__ __forceinline__ RowOwner row_owner(const int32_t* cu_q, const int32_t
   return request_of(cu_q, kv_len, total_q, max_q, cap, lo);
 }
 
-// The same by a thread on its own.
-__device__ __forceinline__ RowOwner row_owner_thread(const int32_t* cu_q, const int32_t* kv_len, int batch, int total_q,
-                                                     int max_q, int cap, int t) {
-  int lo = 0, hi = batch - 1;   // the last b with cu_q[b] <= t
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (__ldg(cu_q + mid) <= t) lo = mid;
-    else hi = mid - 1;
-  }
-  const RowOwner none = {-1, 0, 0, 0, false};
-  if (__ldg(cu_q + lo) > t || __ldg(cu_q + lo + 1) <= t) return none;
-  return request_of(cu_q, kv_len, total_q, max_q, cap, lo);
-}
-
 }  // namespace moe
