@@ -26,15 +26,17 @@
 #include "kernels.cuh"
 #include "kv4.cuh"
 #include "kv_lookup.cuh"
+#include "kv_math.cuh"
 #include "tc_ptx.cuh"
 
 namespace moe {
 namespace {
 
 using namespace tc;
+using kv::kFull;
+using kv::max_u16x2;
 namespace cg = cooperative_groups;
 
-constexpr unsigned kFull = 0xffffffffu;
 constexpr int kFewRows = 8, kManyRows = 608, kManyRowsNarrow = 640;
 
 // A float's bits in the order of its value (0 is below every key of a number).
@@ -117,11 +119,6 @@ __device__ __forceinline__ float on_grid(uint32_t x, float scale) {
   return finite_bits(x) == 0 ? 0.0f : rintf(__uint_as_float(x << 16) * scale);
 }
 
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
-}
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
   uint32_t r;
   asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
@@ -840,6 +837,7 @@ __global__ void __launch_bounds__(kManyThreads, 2) kv4_select_many_kernel(const 
         list.cnt = 2 * kGroup;
         list.top = FLT_MAX;
         list.cut(v.need, v.need);
+        // (NaN for a row that ranks nothing: nothing is above it)
         list.bound = key_below(fminf(list.bound, FLT_MAX));
         list.cnt = 0;
         list.top = -INFINITY;

@@ -3,25 +3,12 @@
 // kv_attention_prompt.cu).
 #pragma once
 
-#include "common.cuh"
+#include "kv_math.cuh"
 
 namespace moe {
 namespace tiles {
 
-constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kLead = 7.0f, kSlack = 15.0f;   // log2: m is set the first below the maximum, again past the second
-constexpr unsigned kFull = 0xffffffffu;
-
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
+using namespace kv;
 
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t pack2(float lo, float hi) {
@@ -59,15 +46,6 @@ __device__ __forceinline__ void ld_wait(uint32_t (&r)[32]) {
                  "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
                  "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
                  "+r"(r[30]), "+r"(r[31])::"memory");
-}
-
-// 2^k for -126 <= k <= 127.
-__device__ __forceinline__ float pow2(int k) { return __int_as_float((127 + k) << 23); }
-
-__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
-  uint32_t r;
-  asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-  return r;
 }
 
 // Byte offset of 16-byte chunk c (of D/8) of row r in an f16 tile of kRows rows:
