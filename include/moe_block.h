@@ -346,7 +346,9 @@ moe_status moe_kv4_append_rope(const moe_kv4_append_rope_args* args, moe_stream_
  * update whose new tokens are the page's makes them).
  * A mean is that of code * scale (the key times k_gs) over the block's tokens,
  * rounded to a multiple of 2^(E - 6), E the exponent of the row's largest
- * magnitude: whole numbers of 8 bits times a power of two.
+ * magnitude: whole numbers of 8 bits times a power of two. The grid is the
+ * row's, so channels whose mean is far larger than the others' cost the others
+ * bits (see moe_kv4_select).
  *
  * Limits: block_tokens 32, 64 or 128; means 16-byte aligned, moe_kv4_index_size
  * bytes; it needs no initialisation (only means of complete blocks are used).
@@ -384,14 +386,20 @@ moe_status moe_kv4_index_update(const moe_kv4_index* index, int batch, int max_q
  *   u = sum over the group's heads of round(q 2^(5 - E)), E the exponent of the largest magnitude of the group's
  *   queries (at least -100); score_j = u . mean_j
  * All of that is exact (whole numbers below 2^24 times powers of two), so
- * picks do not depend on the order of sums. Elements of q that are NaN or
- * infinite count as 0.
+ * picks do not depend on the order of sums. The two grids move picks: of 13
+ * picks among 1024 blocks (random means and queries, groups of 4 x 128) 97 % are
+ * those of scores that are not rounded; 95, 92 and 84 % where five channels of
+ * all means have a constant of 8, 20 and 40 times the others' deviation, which
+ * leaves that much less of the means' grid to the others. Elements of q that
+ * are NaN or infinite count as 0.
  *
  * blocks  int32 [total_q, kv_heads, top], ascending, -1 in the places that are left; rows no request owns are left alone
  * Others as in moe_kv4_attention (which has the contract of bad device data: a
- * page id outside the pool scores lowest, as does a mean that is NaN; of a block of several pages the first and the last count).
+ * page id outside the pool scores lowest, as does a mean that is NaN; of a block
+ * of several pages the first and the last count).
  * Limits: 1 <= top <= 64, sink + local <= top, local >= 1, groups of up to 16
- * query heads, a context of up to 2^28 tokens.
+ * query heads, tables of up to 2^28 tokens, total_q * kv_heads <= 2^30 (else
+ * MOE_ERR_UNSUPPORTED).
  * Errors: as moe_kv4_attention and moe_kv4_index_update; sink, local or top
  * outside the limits -> MOE_ERR_INVALID_ARG (top > 64: MOE_ERR_UNSUPPORTED).
  */
@@ -418,9 +426,12 @@ moe_status moe_kv4_select(const moe_kv4_select_args* args, moe_stream_t stream);
  * blocks up to the query's position. The entries of a list may come in any
  * order; one that is negative or past the query's position is skipped, one
  * listed twice counts once. A query whose list has nothing gets zeros and lse =
- * -inf. No workspace; the same call gives the same bits. The lists of
- * neighbouring queries are worked on together, so lists that share blocks cost
- * less than lists that do not.
+ * -inf. No workspace; the same call gives the same bits. The lists of 32
+ * neighbouring queries are worked on together where there are many, each with
+ * all blocks that any of them picks, so lists that share blocks cost less than
+ * lists that do not (2048 queries of 32/8 heads x 128 over 32768 tokens, 16
+ * blocks of 64 each: 164 to 247 us where neighbours agree, 640 where they do
+ * not, 916 for moe_kv4_attention).
  *
  * blocks int32 [total_q, kv_heads, top]
  * Limits: those of moe_kv4_select. Errors: as there.

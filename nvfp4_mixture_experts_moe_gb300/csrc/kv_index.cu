@@ -8,9 +8,11 @@
 //
 // What bounds it: a decode step completes few blocks, so latency (64 requests:
 // 3.3 us); prompts read the key half of their cache, 0.5625 bytes an element (4
-// of up to 8191 tokens in pages of 16, 8 heads x 128: 7.6 us, 1.6 by the bytes):
-// one wave of CTAs, whose lengths, page ids and rows are three trips to memory
-// one after the other, and then the conversion of the rows.
+// of up to 8191 tokens in pages of 16, 8 heads x 128: 7.8 us, 1.6 by the bytes):
+// a CTA's lengths, page ids and rows are three trips to memory one after the
+// other, then comes the conversion of the rows; at 138 registers three CTAs fit
+// an SM, so that case's 544 with work are two waves, among 384 more that the
+// bound on lengths launches and that leave at once.
 //
 // A warp has one block of one head: a lane holds the sums of 32 elements over
 // every 8th (head_dim 64: 16th) token.

@@ -12,7 +12,7 @@
 //
 // Two kernels. Requests of up to kFewRows rows: a CTA (or a cluster) for a
 // (query, head), bound by the latency of its steps (4 single tokens over 2048
-// blocks, 8 heads x 128: 11.6 us, 2.5 by the means' bytes). More rows: 128
+// blocks, 8 heads x 128: 11.7 us, 2.5 by the means' bytes). More rows: 128
 // queries of a head a CTA, a thread each, scores by tcgen05 in tensor memory
 // (4096 rows over 1024 blocks, 32/8 heads x 128: 50 us, 5.6 by the queries'
 // bytes): of a CTA's 75,000 cycles the queries take 11,000, a tile of 64 means

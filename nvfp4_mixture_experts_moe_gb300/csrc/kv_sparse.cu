@@ -12,11 +12,14 @@
 // share of the unit's tiles and a private ring of stages; their partial results
 // meet in shared memory (of the cluster), in the order of the shares.
 //
-// What bounds it: instruction issue for batches (64 single tokens, 32 blocks of
-// 64 each, 64/8 heads x 128: 39 us, 22.5 by the bytes; four warps a unit leave
-// 128 CTAs for the 152 SMs, and three warps a scheduler issue in 0.6 of the
-// cycles); the chain lengths, lists, page ids, rows, joins for few (one token 9.2
-// us; 16 requests of 4 drafted ones, 24 blocks of 32, 32/8 x 64, 13.7).
+// What bounds it: for batches (64 single tokens, 32 blocks of 64 each, 64/8
+// heads x 128: 39 us, 22.5 by the bytes) what a unit does before its first tile
+// (lengths, list, page ids, rows), which nothing covers where every group of
+// four warps has one unit of 16 tiles a warp, and 24 of the 152 SMs, which have
+// none: 840 tiles a us, where attention over all tokens does the same work on
+// 1220 (a scheduler's four warps issue in 0.6 of the cycles in both). The chain
+// lengths, lists, page ids, rows, joins for few (one token 9.4 us; 16 requests of
+// 4 drafted ones, 24 blocks of 32, 32/8 x 64, 13.9).
 #include <cooperative_groups.h>
 
 #include "kernels.cuh"

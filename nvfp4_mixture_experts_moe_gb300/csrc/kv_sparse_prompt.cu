@@ -22,13 +22,17 @@
 // While one CTA builds a union, enters or ends a unit, the other one's warps
 // work.
 //
-// What bounds it (2048 rows, 16 blocks of 64 each, 32/8 heads x 128: 174 us; 17
-// by the products of each row with its own blocks): a unit multiplies all its
-// rows by the union of what its tokens chose. A step of 64 tokens takes an SM
-// 930 cycles (1860 in each of its CTAs), 770 of them by shared memory (operands
-// of S 384, of O 128, stores of the tiles 256; Q in tensor memory would save a
-// third of that, but S and O leave no columns); a unit's entry and end take
-// 17,000 of its 135,000; 512 units are four for 56 of the SMs and three for the others.
+// What bounds it (2048 rows over 32768 tokens, 16 blocks of 64 each, 32/8 heads x
+// 128: 168 us; 17 by the products of each row with its own blocks): a unit
+// multiplies all its rows by the union of what its tokens chose. These lists
+// agree by runs of 32 tokens that are the units (58 blocks a union; other such
+// lists 164); the same runs 16 tokens later (88) take 221, agreement that decays
+// over 32 tokens (99) 247, nothing in common (287) 640, all tokens 916. A step of
+// 64 tokens takes an SM 930 cycles (1860 in each of its CTAs), 770 of them by
+// shared memory (operands of S 384, of O 128, stores of the tiles 256; Q in tensor
+// memory would save a third of that, but S and O leave no columns); a unit's entry
+// and end take 17,000 of its 135,000; 512 units are four for 56 of the SMs and
+// three for the others.
 // S whole in registers spilled (229 us), as did two threads a row (334); one
 // thread issuing all products 189.
 #include "kernels.cuh"

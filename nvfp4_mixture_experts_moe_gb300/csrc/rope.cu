@@ -11,8 +11,11 @@
 // sines and cosines (some 30 instructions a pair) are worked out once.
 //
 // What bounds it: bytes where there are many tokens (16384 of 32 + 8 heads x
-// 128: 52.4 us, 6.4 TB/s of the 6.7 that a copy reaches), the launch where there
-// are few (8 tokens: 2.1 us). On the way into the cache (8191 tokens of 32
+// 128: 52.7 us, 6.4 TB/s of the 6.7 that a copy reaches), the launch where there
+// are few (8 tokens: 2.3 us). Rows that vectors cannot move (rotary_dim no
+// multiple of 16, or not 16-byte aligned) go a pair a thread in 2-byte accesses,
+// at half of that rate (4096 tokens of 40 heads x 72: 15.0 us, 3.1 TB/s; x 128, 40
+// elements turned or at an odd address: 25.5, 3.3; in vectors 14.2, 5.9). On the way into the cache (8191 tokens of 32
 // query heads, 8 key/value heads x 128, adjacent pairs: 35 us, 26 by the
 // bytes) a load's latency: three kinds of rows leave 24 warps an SM.
 #include "kernels.cuh"

@@ -11,7 +11,7 @@ Test infrastructure only (see the package docstring for who may import it).
 * ``grid``, ``block_mean``, ``picks``: a block's mean key on its grid, and the
   blocks that one query picks.
 
-Each is pinned by tests/test_oracle_block.py.
+Pinned by tests/test_oracle_block.py, the last two groups by tests/test_sparse_host.py.
 """
 from __future__ import annotations
 
